@@ -19,8 +19,8 @@ from dataclasses import dataclass
 
 import torch
 
-from ._lib import (NOALLOC_SCRATCH_BYTES, SYMBOLS, USP_BF16, USP_F32, USP_OK, UspError, UspProblem,  # noqa: F401
-                   UspTraceEntry, check, load)
+from ._lib import (NOALLOC_SCRATCH_BYTES, SYMBOLS, USP_BF16, USP_F32, USP_OK, UspCache, UspError,  # noqa: F401
+                   UspProblem, UspTraceEntry, check, load)
 
 __all__ = [
     "Problem", "UspError", "SYMBOLS",
@@ -38,6 +38,8 @@ __all__ = [
     "usp_hybrid_bwd_workspace_size", "usp_hybrid_attn_fwd", "usp_hybrid_attn_bwd", "hybrid_attention_fwd",
     "hybrid_attention_bwd", "usp_diag_wait_timeout", "usp_diag_raise_status",
     "usp_attn_bwd_deterministic_workspace_size", "usp_attn_bwd_deterministic",
+    "Cache", "usp_kv_append", "usp_paged_attn_workspace_size", "usp_paged_attn", "usp_prefix_attn_workspace_size",
+    "usp_prefix_attn", "kv_append", "paged_attention", "prefix_attention",
 ]
 
 _TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
@@ -92,6 +94,46 @@ class Problem:
         return (self.P, self.B, self.Hq // Pu, self.N // (self.P // Pu))
 
 
+@dataclass(frozen=True)
+class Cache:
+    """A paged key/value cache: pool [n_pages][Hkv][page_size][d] for K and for V, page table [n_seqs][max_pages]."""
+    n_pages: int
+    page_size: int
+    n_seqs: int
+    max_pages: int
+    Hq: int
+    Hkv: int
+    d: int
+    causal: bool = True
+    scale: float = 0.0  # 0 selects 1/sqrt(d)
+    dtype: str = "bf16"
+
+    def c(self) -> UspCache:
+        if self.dtype not in _TORCH_DTYPE:
+            raise ValueError(f"dtype must be 'f32' or 'bf16', got {self.dtype!r}")
+        return UspCache(self.n_pages, self.page_size, self.n_seqs, self.max_pages, self.Hq, self.Hkv, self.d,
+                        int(bool(self.causal)), float(self.scale), USP_F32 if self.dtype == "f32" else USP_BF16)
+
+    @property
+    def torch_dtype(self) -> torch.dtype:
+        return _TORCH_DTYPE[self.dtype]
+
+    @property
+    def softmax_scale(self) -> float:
+        return self.scale if self.scale else 1.0 / math.sqrt(self.d)
+
+    def pool_shape(self):
+        """Pool of keys, or of values: [n_pages][Hkv][page_size][d]."""
+        return (self.n_pages, self.Hkv, self.page_size, self.d)
+
+    def table_shape(self):
+        return (self.n_seqs, self.max_pages)
+
+    def pages_for(self, tokens: int) -> int:
+        """Pages that hold this many tokens."""
+        return -(-tokens // self.page_size)
+
+
 def library_path() -> str:
     from .build import LIB
     return LIB
@@ -117,6 +159,29 @@ def _stream(stream) -> int:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _rows(x, heads: int, d: int):
+    """Pointer and token stride (elements) of a tensor [tokens][heads][d] whose heads are contiguous in each token, or
+    of a device pointer to contiguous rows."""
+    if x is None or isinstance(x, int):
+        return x or 0, heads * d
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"expected a torch tensor, a device pointer or None, got {type(x).__name__}")
+    if x.numel() and not x.is_cuda:
+        raise ValueError("libusp takes device tensors")
+    if x.dim() != 3 or tuple(x.shape[1:]) != (heads, d):
+        raise ValueError(f"expected [tokens][{heads}][{d}], got {list(x.shape)}")
+    if x.shape[0] > 1 or (heads > 1 and x.numel()):
+        if x.stride(2) != 1 or (heads > 1 and x.stride(1) != d):
+            raise ValueError("the heads of a token must be contiguous")
+    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else heads * d
+
+
+def _cache(c) -> ctypes.POINTER(UspCache):
+    if c is None:
+        return None
+    return ctypes.byref(c.c() if isinstance(c, Cache) else c)
 
 
 def _prob(p) -> ctypes.POINTER(UspProblem):
@@ -305,6 +370,43 @@ def usp_hybrid_attn_bwd(p, Pu: int, q, k, v, o, lse, dout, dq, dk, dv, ws, ws_by
 def usp_ring_merge(rows: int, d: int, o_a, lse_a, o_b, lse_b, o, lse, stream=None) -> None:
     check("usp_ring_merge", load().usp_ring_merge(int(rows), int(d), _ptr(o_a), _ptr(lse_a), _ptr(o_b), _ptr(lse_b),
                                                   _ptr(o), _ptr(lse), _stream(stream)))
+
+
+def usp_kv_append(c, n_tokens: int, q, k, v, seq, pos, inv_freq, q_out, k_out, k_pages, v_pages, page_table,
+                  rot: int = 0, interleaved: bool = False, rot_pos=None, stream=None) -> None:
+    """q, k, v: [n_tokens][H][d] with any token stride (q, q_out, k_out may be None); the rest contiguous."""
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, c.Hq, c.d), _rows(k, c.Hkv, c.d), _rows(v, c.Hkv, c.d)
+    check("usp_kv_append", load().usp_kv_append(_cache(c), int(n_tokens), qp, qs, kp, ks, vp, vs, _ptr(seq), _ptr(pos),
+                                                _ptr(rot_pos), _ptr(inv_freq), int(rot), int(bool(interleaved)),
+                                                _ptr(q_out), _ptr(k_out), _ptr(k_pages), _ptr(v_pages),
+                                                _ptr(page_table), _stream(stream)))
+
+
+def usp_paged_attn_workspace_size(c, n_tokens: int, max_q: int) -> int:
+    return int(load().usp_paged_attn_workspace_size(_cache(c), int(n_tokens), int(max_q)))
+
+
+def usp_paged_attn(c, n_tokens: int, max_q: int, q, k_pages, v_pages, page_table, seq_lens, q_start, o, lse, ws,
+                   ws_bytes=None, stream=None) -> None:
+    if ws_bytes is None:
+        ws_bytes = ws.numel() * ws.element_size() if isinstance(ws, torch.Tensor) else 0
+    check("usp_paged_attn", load().usp_paged_attn(_cache(c), int(n_tokens), int(max_q), _ptr(q), _ptr(k_pages),
+                                                  _ptr(v_pages), _ptr(page_table), _ptr(seq_lens), _ptr(q_start),
+                                                  _ptr(o), _ptr(lse), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def usp_prefix_attn_workspace_size(c, n_tokens: int, max_q: int, prefix_len: int) -> int:
+    return int(load().usp_prefix_attn_workspace_size(_cache(c), int(n_tokens), int(max_q), int(prefix_len)))
+
+
+def usp_prefix_attn(c, n_tokens: int, max_q: int, q, k_pages, v_pages, page_table, seq_lens, q_start, prefix_pages,
+                    prefix_len: int, o, lse, ws, ws_bytes=None, stream=None) -> None:
+    if ws_bytes is None:
+        ws_bytes = ws.numel() * ws.element_size() if isinstance(ws, torch.Tensor) else 0
+    check("usp_prefix_attn", load().usp_prefix_attn(_cache(c), int(n_tokens), int(max_q), _ptr(q), _ptr(k_pages),
+                                                    _ptr(v_pages), _ptr(page_table), _ptr(seq_lens), _ptr(q_start),
+                                                    _ptr(prefix_pages), int(prefix_len), _ptr(o), _ptr(lse), _ptr(ws),
+                                                    int(ws_bytes), _stream(stream)))
 
 
 def usp_diag_wait_timeout(stream=None) -> None:
@@ -514,3 +616,109 @@ def hybrid_attention_bwd(p: Problem, Pu: int, saved, do_seq, stream=None):
     usp_hybrid_head2seq(p, Pu, p.Hkv, dkh, dk, stream)
     usp_hybrid_head2seq(p, Pu, p.Hkv, dvh, dv, stream)
     return dq, dk, dv
+
+
+# --------------------------------------------------------- serving helpers
+def _check(c: Cache, name: str, x, shape, dtype, device, optional=False) -> None:
+    """A tensor argument of a serving helper: its type, shape and device (None entries of `shape` are free)."""
+    if x is None and optional:
+        return
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor, got {type(x).__name__}")
+    if x.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {x.dtype}")
+    if x.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, x.shape)):
+        raise ValueError(f"{name}: expected shape {['any' if w is None else w for w in shape]}, got {list(x.shape)}")
+    if x.device != device:
+        raise ValueError(f"{name}: on {x.device}, not on {device} as the queries are")
+
+
+def _serving_device(x):
+    """The device of the call's tensors: the current one, on which the library launches its kernels."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("libusp takes device tensors")
+    if x.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return x.device
+
+
+def _used_on(stream, *tensors) -> None:
+    """Tensors allocated on the current stream and used on another: the allocator must not hand them out before."""
+    if stream is None:
+        return
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    if s.cuda_stream == torch.cuda.current_stream().cuda_stream:
+        return
+    for t in tensors:
+        if t is not None:
+            t.record_stream(s)
+
+
+def kv_append(c: Cache, q, k, v, seq, pos, inv_freq, k_pages, v_pages, page_table, interleaved=False, rot_pos=None,
+              stream=None):
+    """Rotate q and k by their positions and write k and v into the cache (usp_kv_append).
+
+    q [T][Hq][d] (or None), k, v [T][Hkv][d], any token stride; seq, pos (and rot_pos) int32 [T]; inv_freq float32
+    [rot/2] or None.  Returns (rotated q or None, rotated k); rows of padding tokens hold what torch.empty left."""
+    dev, dt = _serving_device(k), c.torch_dtype
+    T = k.shape[0]
+    _check(c, "q", q, (T, c.Hq, c.d), dt, dev, optional=True)
+    _check(c, "k", k, (T, c.Hkv, c.d), dt, dev)
+    _check(c, "v", v, (T, c.Hkv, c.d), dt, dev)
+    _check(c, "seq", seq, (T,), torch.int32, dev)
+    _check(c, "pos", pos, (T,), torch.int32, dev)
+    _check(c, "rot_pos", rot_pos, (T,), torch.int32, dev, optional=True)
+    _check(c, "inv_freq", inv_freq, (None,), torch.float32, dev, optional=True)
+    _check(c, "k_pages", k_pages, c.pool_shape(), dt, dev)
+    _check(c, "v_pages", v_pages, c.pool_shape(), dt, dev)
+    _check(c, "page_table", page_table, c.table_shape(), torch.int32, dev)
+    q_out = None if q is None else _empty((T, c.Hq, c.d), dt, dev)
+    k_out = _empty((T, c.Hkv, c.d), dt, dev)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    usp_kv_append(c, T, q, k, v, seq, pos, inv_freq, q_out, k_out, k_pages, v_pages, page_table, rot, interleaved,
+                  rot_pos, stream)
+    _used_on(stream, q_out, k_out)
+    return q_out, k_out
+
+
+def _check_paged(c: Cache, q, k_pages, v_pages, page_table, seq_lens, q_start):
+    dev, dt = _serving_device(q), c.torch_dtype
+    _check(c, "q", q, (None, c.Hq, c.d), dt, dev)
+    _check(c, "k_pages", k_pages, c.pool_shape(), dt, dev)
+    _check(c, "v_pages", v_pages, c.pool_shape(), dt, dev)
+    _check(c, "page_table", page_table, c.table_shape(), torch.int32, dev)
+    _check(c, "seq_lens", seq_lens, (c.n_seqs,), torch.int32, dev)
+    _check(c, "q_start", q_start, (c.n_seqs + 1,), torch.int32, dev, optional=True)
+    return dev, dt
+
+
+def paged_attention(c: Cache, q, k_pages, v_pages, page_table, seq_lens, q_start=None, max_q=1, stream=None):
+    """Attention of each sequence's newest tokens over its cached keys (usp_paged_attn): returns (o, lse).
+
+    q [T][Hq][d]; q_start int32 [n_seqs + 1] (None: one token per sequence); max_q: the largest number of tokens a
+    sequence has in this call.  Rows of no sequence hold what torch.empty left."""
+    dev, dt = _check_paged(c, q, k_pages, v_pages, page_table, seq_lens, q_start)
+    T = q.shape[0]
+    o, lse = _empty((T, c.Hq, c.d), dt, dev), _empty((T, c.Hq), torch.float32, dev)
+    ws = torch.empty(max(usp_paged_attn_workspace_size(c, T, max_q), 256), dtype=torch.uint8, device=dev)
+    usp_paged_attn(c, T, max_q, q, k_pages, v_pages, page_table, seq_lens, q_start, o, lse, ws, None, stream)
+    _used_on(stream, o, lse, ws)
+    return o, lse
+
+
+def prefix_attention(c: Cache, q, k_pages, v_pages, page_table, seq_lens, prefix_pages, prefix_len: int, q_start=None,
+                     max_q=1, stream=None):
+    """paged_attention for sequences that share their first prefix_len tokens, held by the pages prefix_pages
+    (int32 [ceil(prefix_len/page_size)]): those are read once for the whole batch (usp_prefix_attn)."""
+    dev, dt = _check_paged(c, q, k_pages, v_pages, page_table, seq_lens, q_start)
+    _check(c, "prefix_pages", prefix_pages, (None,), torch.int32, dev)
+    if prefix_pages.numel() < c.pages_for(prefix_len):
+        raise ValueError(f"prefix_pages: {prefix_pages.numel()} pages do not hold {prefix_len} tokens")
+    T = q.shape[0]
+    o, lse = _empty((T, c.Hq, c.d), dt, dev), _empty((T, c.Hq), torch.float32, dev)
+    size = usp_prefix_attn_workspace_size(c, T, max_q, prefix_len)
+    ws = torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
+    usp_prefix_attn(c, T, max_q, q, k_pages, v_pages, page_table, seq_lens, q_start, prefix_pages, prefix_len, o, lse,
+                    ws, None, stream)
+    _used_on(stream, o, lse, ws)
+    return o, lse

@@ -35,7 +35,8 @@ SYMBOLS = (
     "usp_fused_attn_fwd", "usp_fused_attn_bwd_workspace_size", "usp_fused_attn_bwd", "usp_hybrid_seq2head",
     "usp_hybrid_head2seq", "usp_hybrid_workspace_size", "usp_hybrid_bwd_workspace_size", "usp_hybrid_attn_fwd",
     "usp_hybrid_attn_bwd", "usp_diag_wait_timeout", "usp_diag_raise_status",
-    "usp_attn_bwd_deterministic_workspace_size", "usp_attn_bwd_deterministic",
+    "usp_attn_bwd_deterministic_workspace_size", "usp_attn_bwd_deterministic", "usp_kv_append",
+    "usp_paged_attn_workspace_size", "usp_paged_attn", "usp_prefix_attn_workspace_size", "usp_prefix_attn",
 )
 
 
@@ -44,6 +45,13 @@ class UspProblem(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("N", ctypes.c_int),
                 ("d", ctypes.c_int), ("P", ctypes.c_int), ("causal", ctypes.c_int), ("scale", ctypes.c_float),
                 ("dtype", ctypes.c_int)]
+
+
+class UspCache(ctypes.Structure):
+    """Mirror of ``usp_cache``."""
+    _fields_ = [("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("n_seqs", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+                ("causal", ctypes.c_int), ("scale", ctypes.c_float), ("dtype", ctypes.c_int)]
 
 
 class UspTraceEntry(ctypes.Structure):
@@ -75,7 +83,7 @@ def load() -> ctypes.CDLL:
                 f"libusp.so not found at {LIB}; build it first "
                 "(python -m context_long_attention_ulysses_gb300.build)")
         lib = ctypes.CDLL(LIB)
-        P = ctypes.POINTER(UspProblem)
+        P, C = ctypes.POINTER(UspProblem), ctypes.POINTER(UspCache)
         vp, i64, sz, ci = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
         sig = {
             "usp_a2a_seq2head": (ci, [P, ci, vp, vp, vp]),
@@ -118,6 +126,11 @@ def load() -> ctypes.CDLL:
             "usp_diag_raise_status": (ci, [vp]),
             "usp_attn_bwd_deterministic_workspace_size": (sz, [P]),
             "usp_attn_bwd_deterministic": (ci, [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "usp_kv_append": (ci, [C, ci, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, ci, ci, vp, vp, vp, vp, vp, vp]),
+            "usp_paged_attn_workspace_size": (sz, [C, ci, ci]),
+            "usp_paged_attn": (ci, [C, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "usp_prefix_attn_workspace_size": (sz, [C, ci, ci, ci]),
+            "usp_prefix_attn": (ci, [C, ci, ci, vp, vp, vp, vp, vp, vp, vp, ci, vp, vp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)

@@ -1218,6 +1218,144 @@ usp_status usp_hybrid_attn_bwd(const usp_problem* p, int Pu, const void* q, cons
     return cuda_status(e);
 }
 
+// ---------------------------------------------------------------- serving: the paged cache
+static usp_status check_cache(const usp_cache* c) {
+    if (!c) return USP_ERR_INVALID_ARG;
+    if (c->n_pages < 0 || c->n_seqs < 0 || c->max_pages < 0 || c->Hq < 1 || c->Hkv < 1 || c->d < 1)
+        return USP_ERR_INVALID_ARG;
+    if (c->Hq % c->Hkv != 0) return USP_ERR_INVALID_ARG;
+    if (c->dtype != USP_F32 && c->dtype != USP_BF16) return USP_ERR_INVALID_ARG;
+    if (!(c->scale >= 0.f) || std::isinf(c->scale)) return USP_ERR_INVALID_ARG;
+    const int ps = c->page_size;
+    if (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256) return USP_ERR_UNSUPPORTED;
+    if (c->d != 64 && c->d != 128) return USP_ERR_UNSUPPORTED;
+    if (c->Hq > 65535 || (int64_t)c->max_pages * ps > INT32_MAX || (int64_t)c->n_pages * c->Hkv > INT32_MAX)
+        return USP_ERR_UNSUPPORTED;
+    return USP_OK;
+}
+
+static int page_log2(const usp_cache* c) {
+    int l = 4;
+    while ((1 << l) < c->page_size) ++l;
+    return l;
+}
+
+static bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// A row stride of n contiguous elements that 16-byte accesses can use.
+static bool stride_ok(int64_t stride, int64_t n, int elem) { return stride >= n && stride * elem % 16 == 0; }
+
+usp_status usp_kv_append(const usp_cache* c, int n_tokens, const void* q, int64_t q_stride, const void* k,
+                         int64_t k_stride, const void* v, int64_t v_stride, const int32_t* seq, const int32_t* pos,
+                         const int32_t* rot_pos, const float* inv_freq, int rot, int interleaved, void* q_out,
+                         void* k_out, void* k_pages, void* v_pages, const int32_t* page_table, usp_stream stream) {
+    usp_status st = check_cache(c);
+    if (st != USP_OK) return st;
+    if (n_tokens < 0 || rot < 0 || rot > c->d || rot % 16 != 0 || (q == nullptr) != (q_out == nullptr))
+        return USP_ERR_INVALID_ARG;
+    const int elem = elem_size(c->dtype);
+    if (n_tokens > 0 &&
+        ((q && !stride_ok(q_stride, (int64_t)c->Hq * c->d, elem)) ||
+         !stride_ok(k_stride, (int64_t)c->Hkv * c->d, elem) || !stride_ok(v_stride, (int64_t)c->Hkv * c->d, elem)))
+        return USP_ERR_INVALID_ARG;
+    if (n_tokens == 0 || c->n_seqs == 0 || c->n_pages == 0 || c->max_pages == 0) return USP_OK;  // no token has a slot
+    const void* ptrs[] = {k, v, k_pages, v_pages};
+    for (const void* ptr : ptrs)
+        if (!aligned16(ptr)) return USP_ERR_MISALIGNED;
+    if ((q && (!aligned16(q) || !aligned16(q_out))) || (k_out && !aligned16(k_out))) return USP_ERR_MISALIGNED;
+    if (!aligned4(seq) || !aligned4(pos) || !aligned4(page_table) || (rot_pos && !aligned4(rot_pos)) ||
+        (rot > 0 && !aligned4(inv_freq)))
+        return USP_ERR_MISALIGNED;
+    AppendParams p{};
+    p.q = q; p.k = k; p.v = v;
+    p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride;
+    p.seq = seq; p.pos = pos; p.rot_pos = rot_pos; p.inv_freq = inv_freq;
+    p.q_out = q_out; p.k_out = k_out; p.k_pages = k_pages; p.v_pages = v_pages; p.page_table = page_table;
+    p.n_tokens = n_tokens; p.n_seqs = c->n_seqs; p.max_pages = c->max_pages; p.n_pages = c->n_pages;
+    p.page_log2 = page_log2(c);
+    p.Hq = c->Hq; p.Hkv = c->Hkv; p.d = c->d; p.rot = rot; p.interleaved = interleaved != 0; p.elem = elem;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(traced("kv_append", s, [&] { return launch_kv_append(p, s); }));
+}
+
+// Shapes of a paged attention call; the pointers are filled in by the caller.
+static PagedArgs paged_args(const usp_cache* c, int n_tokens, int prefix_len) {
+    PagedArgs a{};
+    a.n_tokens = n_tokens; a.n_seqs = c->n_seqs; a.max_pages = c->max_pages; a.n_pages = c->n_pages;
+    a.page_log2 = page_log2(c);
+    a.Hq = c->Hq; a.Hkv = c->Hkv; a.g = c->Hq / c->Hkv; a.d = c->d; a.elem = elem_size(c->dtype);
+    a.causal = c->causal ? 1 : 0;
+    a.prefix_len = a.key_begin = prefix_len;
+    a.scale_log2 = (c->scale == 0.f ? 1.0f / std::sqrt((float)c->d) : c->scale) * 1.4426950408889634f;
+    return a;
+}
+
+static usp_status check_paged(const usp_cache* c, int n_tokens, int max_q, int prefix_len) {
+    usp_status st = check_cache(c);
+    if (st != USP_OK) return st;
+    if (n_tokens < 0 || max_q < 1 || prefix_len < 0 || (int64_t)prefix_len > (int64_t)c->max_pages * c->page_size)
+        return USP_ERR_INVALID_ARG;
+    if ((int64_t)n_tokens * c->Hq > INT32_MAX) return USP_ERR_UNSUPPORTED;
+    return USP_OK;
+}
+
+static size_t paged_workspace(const usp_cache* c, int n_tokens, int max_q, int prefix_len) {
+    if (check_paged(c, n_tokens, max_q, prefix_len) != USP_OK || n_tokens == 0) return 0;
+    PagedArgs a = paged_args(c, n_tokens, prefix_len);
+    return paged_plan(&a, max_q, nullptr);
+}
+
+static usp_status paged_attn(const usp_cache* c, int n_tokens, int max_q, const void* q, const void* k_pages,
+                             const void* v_pages, const int32_t* page_table, const int32_t* seq_lens,
+                             const int32_t* q_start, const int32_t* prefix_pages, int prefix_len, void* o, float* lse,
+                             void* ws, size_t ws_bytes, usp_stream stream) {
+    usp_status st = check_paged(c, n_tokens, max_q, prefix_len);
+    if (st != USP_OK) return st;
+    if (!q_start && n_tokens != c->n_seqs) return USP_ERR_INVALID_ARG;
+    if (n_tokens == 0 || c->n_seqs == 0) return USP_OK;  // no sequence has a row
+    if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return USP_ERR_MISALIGNED;
+    const bool pool = c->n_pages > 0 && c->max_pages > 0;
+    if (pool && (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(page_table))) return USP_ERR_MISALIGNED;
+    if (!aligned4(seq_lens) || (q_start && !aligned4(q_start)) || (prefix_len > 0 && !aligned4(prefix_pages)))
+        return USP_ERR_MISALIGNED;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return USP_ERR_MISALIGNED;
+    PagedArgs a = paged_args(c, n_tokens, prefix_len);
+    if (ws_bytes < paged_plan(&a, max_q, ws)) return USP_ERR_WORKSPACE;
+    a.q = q; a.k_pages = k_pages; a.v_pages = v_pages; a.page_table = page_table; a.seq_lens = seq_lens;
+    a.q_start = q_start; a.prefix_pages = prefix_pages; a.o = o; a.lse = lse;
+    a.status = status_ptr();
+    if (!a.status) return USP_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (prefix_len > 0) e = traced("paged_prefix", s, [&] { return launch_paged_prefix(a, s); });
+    if (e == cudaSuccess) e = traced("paged_own", s, [&] { return launch_paged_own(a, s); });
+    if (e == cudaSuccess) e = traced("paged_merge", s, [&] { return launch_paged_merge(a, s); });
+    return cuda_status(e);
+}
+
+size_t usp_paged_attn_workspace_size(const usp_cache* c, int n_tokens, int max_q) {
+    return paged_workspace(c, n_tokens, max_q, 0);
+}
+
+usp_status usp_paged_attn(const usp_cache* c, int n_tokens, int max_q, const void* q, const void* k_pages,
+                          const void* v_pages, const int32_t* page_table, const int32_t* seq_lens,
+                          const int32_t* q_start, void* o, float* lse, void* ws, size_t ws_bytes, usp_stream stream) {
+    return paged_attn(c, n_tokens, max_q, q, k_pages, v_pages, page_table, seq_lens, q_start, nullptr, 0, o, lse, ws,
+                      ws_bytes, stream);
+}
+
+size_t usp_prefix_attn_workspace_size(const usp_cache* c, int n_tokens, int max_q, int prefix_len) {
+    return paged_workspace(c, n_tokens, max_q, prefix_len);
+}
+
+usp_status usp_prefix_attn(const usp_cache* c, int n_tokens, int max_q, const void* q, const void* k_pages,
+                           const void* v_pages, const int32_t* page_table, const int32_t* seq_lens,
+                           const int32_t* q_start, const int32_t* prefix_pages, int prefix_len, void* o, float* lse,
+                           void* ws, size_t ws_bytes, usp_stream stream) {
+    return paged_attn(c, n_tokens, max_q, q, k_pages, v_pages, page_table, seq_lens, q_start, prefix_pages, prefix_len,
+                      o, lse, ws, ws_bytes, stream);
+}
+
 usp_status usp_trace_enable(int on) {
     std::lock_guard<std::mutex> lock(g_trace_mu);
     g_trace_on = on != 0;

@@ -139,6 +139,47 @@ cudaError_t launch_raise_status(int* status, cudaStream_t stream);
 usp_status attn_bwd_check(const usp_problem* p, const void* q, const void* k, const void* v, const void* o,
                           const float* lse, const void* dout, const void* dq, const void* dk, const void* dv);
 
+// ---- paged key/value cache (kv_append.cu)
+struct AppendParams {
+    const void *q, *k, *v;                 // q null: no queries
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    const int32_t *seq, *pos, *rot_pos;    // rot_pos null: pos
+    const float* inv_freq;
+    void *q_out, *k_out;                   // k_out may be null
+    void *k_pages, *v_pages;
+    const int32_t* page_table;
+    int n_tokens, n_seqs, max_pages, n_pages, page_log2;
+    int Hq, Hkv, d, rot, interleaved, elem;
+};
+cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
+
+// ---- attention over the paged cache (paged_attn.cu; the work's cut is explained in paged.cuh)
+struct PagedArgs {
+    const void *q, *k_pages, *v_pages;
+    const int32_t *page_table, *seq_lens, *q_start, *prefix_pages;
+    void* o;
+    float* lse;
+    int n_tokens, n_seqs, max_pages, n_pages, page_log2;
+    int Hq, Hkv, g, d, elem, causal;
+    int prefix_len;   // > 0: keys below it come from prefix_pages, once for the batch
+    int key_begin;    // first own key (= prefix_len)
+    float scale_log2; // softmax scale * log2(e)
+    // the plan: row-tile sizes and CTAs of the own and the prefix part, and the workspace
+    int rows, p_rows;
+    int ctas, p_ctas;
+    uint2* row_info;               // per row of o
+    float *own_o, *own_lse;        // prefix only: own part of whole units, [n_tokens][Hq][d], [n_tokens][Hq]
+    float *slot_o, *slot_l;        // [ctas][2][rows][d], [ctas][2][rows]
+    float *pslot_o, *pslot_l;      // [p_ctas][2][p_rows][d], [p_ctas][2][p_rows]
+    int* status;
+};
+// Fills the plan's sizes (rows, p_rows, ctas, p_ctas) from the shapes and returns the workspace's bytes; with ws, also
+// the workspace pointers.
+size_t paged_plan(PagedArgs* a, int max_q, void* ws);
+cudaError_t launch_paged_own(const PagedArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_prefix(const PagedArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream);
+
 // ---- tensor maps (api.cu)
 // 4-D bf16 tensor map over Tensor4 with box {64, 1, 128, 1} and 128-byte swizzle.
 bool make_tmap_bf16(CUtensorMap* map, const Tensor4& t, int d, int box_rows);

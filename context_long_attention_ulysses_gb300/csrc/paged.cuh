@@ -1,0 +1,355 @@
+// Attention over a paged cache: what its kernels share -- how the work is cut
+// into equal shares, and where a row's result goes.
+//
+// A unit is (sequence, KV head, tile of M consecutive rows), a row being one
+// (token, query head of the group): K and V of the head are read once for all
+// M rows.  A unit's keys are cut into tiles of kKeyTile.  All tiles of all
+// units, in the order sequence, head, row tile, key tile, form one line of W
+// tiles; CTA c of G takes the tiles [c*W/G, (c+1)*W/G).  So every CTA has the
+// same work whatever the lengths are, one sequence of 128K tokens spreads over
+// all SMs, and the lengths are read on the device (a captured graph replays
+// with new ones).  A unit that lies in one share is finished by its CTA; the
+// rows of a unit cut by a border leave partial results (normalised output and
+// log-sum-exp) in the workspace, which paged_merge_kernel joins in the order
+// of the keys.  A share holds at most two cut units: its first (slot 0, begun
+// by an earlier CTA) and its last (slot 1).
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+
+namespace usp {
+
+constexpr int kKeyTile = 64;  // keys per tile
+
+// What paged_merge_kernel does with a row: word x = kind | row in the tile << 2, y = first CTA | last CTA << 16.
+enum RowKind : uint32_t {
+    kRowDone = 0,   // nothing (finished, or a row of no sequence)
+    kRowNone = 1,   // no own keys (prefix only)
+    kRowWhole = 2,  // own part in own_o, own_lse (prefix only)
+    kRowSplit = 3   // own part in the slots of the CTAs named in y
+};
+
+// Rows of one sequence in this call.
+struct SeqRows {
+    int t0, n, len;  // first token (row of q), tokens, cached tokens
+};
+
+__device__ __forceinline__ SeqRows seq_rows(const PagedArgs& a, int b) {
+    SeqRows s;
+    if (a.q_start) {
+        s.t0 = min(max(__ldg(a.q_start + b), 0), a.n_tokens);
+        s.n = min(max(__ldg(a.q_start + b + 1), s.t0), a.n_tokens) - s.t0;
+    } else {
+        s.t0 = b;
+        s.n = 1;
+    }
+    s.len = min(max(__ldg(a.seq_lens + b), 0), a.max_pages << a.page_log2);
+    return s;
+}
+
+// Keys [0, vis) are seen by token i of the sequence.
+__device__ __forceinline__ int visible(const PagedArgs& a, const SeqRows& s, int i) {
+    return a.causal ? max(s.len - s.n + i + 1, 0) : s.len;
+}
+
+// Key tiles of row tile rt of a sequence: those that hold a key in [key_begin, vis of the tile's last row).
+template <int M>
+__device__ __forceinline__ int unit_tiles(const PagedArgs& a, const SeqRows& s, int rt) {
+    const int last = min(((rt + 1) * M - 1) / a.g, s.n - 1);
+    const int end = visible(a, s, last);
+    return end > a.key_begin ? (end + kKeyTile - 1) / kKeyTile - a.key_begin / kKeyTile : 0;
+}
+
+template <int M>
+__device__ __forceinline__ int row_tiles(const PagedArgs& a, const SeqRows& s) {
+    return (s.n * a.g + M - 1) / M;
+}
+
+// Key tiles of all row tiles of one head of a sequence.
+template <int M>
+__device__ __forceinline__ int64_t head_tiles(const PagedArgs& a, int b) {
+    const SeqRows s = seq_rows(a, b);
+    const int nrt = row_tiles<M>(a, s);
+    if (nrt == 0) return 0;
+    if (!a.causal || s.n == 1) return (int64_t)nrt * unit_tiles<M>(a, s, 0);
+    int64_t sum = 0;
+    for (int rt = 0; rt < nrt; ++rt) sum += unit_tiles<M>(a, s, rt);
+    return sum;
+}
+
+// A CTA's share of the line: [pos, end), beginning `off` tiles into sequence b; W (total) tiles over n_cta CTAs, no
+// share empty (so that every CTA between a unit's first and last holds a part of it).
+struct Share {
+    int64_t pos, end, off, total;
+    int b, n_cta;
+};
+
+// Computed by all threads of the CTA (a scan over the sequences; NT threads), result in *out (shared memory).
+template <int M, int NT>
+__device__ void find_share(const PagedArgs& a, int cta, int n_cta, Share* out) {
+    constexpr int kWarps = NT / 32;
+    __shared__ int64_t part[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t mine = 0;
+    for (int b = threadIdx.x; b < a.n_seqs; b += NT) mine += head_tiles<M>(a, b);
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
+    if (lane == 0) part[warp] = mine;
+    if (threadIdx.x == 0) *out = Share{0, 0, 0, 0, a.n_seqs, 1};
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < kWarps; ++w) total += part[w];
+    total *= a.Hkv;
+    if (n_cta > total) n_cta = (int)total;
+    if (cta >= n_cta) return;
+    const int64_t pos = total * cta / n_cta, end = total * (cta + 1) / n_cta;
+    int64_t base = 0;
+    for (int b0 = 0; b0 < a.n_seqs; b0 += NT) {  // chunk by chunk: inclusive scan of the sequences' tiles
+        __syncthreads();
+        const int b = b0 + threadIdx.x;
+        const int64_t cost = b < a.n_seqs ? head_tiles<M>(a, b) * a.Hkv : 0;
+        int64_t inc = cost;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(~0u, inc, o);
+            if (lane >= o) inc += up;
+        }
+        if (lane == 31) part[warp] = inc;
+        __syncthreads();
+        int64_t before = base;
+        for (int w = 0; w < warp; ++w) before += part[w];
+        const int64_t lo = before + inc - cost;
+        if (lo <= pos && pos < lo + cost) *out = Share{pos, end, pos - lo, total, b, n_cta};
+        for (int w = 0; w < kWarps; ++w) base += part[w];
+        if (base > pos) break;
+    }
+    __syncthreads();
+}
+
+// The CTA that owns tile x of W, shares as above.
+__device__ __forceinline__ int share_owner(int64_t x, int64_t total, int n_cta) {
+    return (int)(((x + 1) * n_cta - 1) / total);
+}
+
+// A piece of one unit: the rows row0 .. row0 + n_rows of a sequence's n*g rows (prefix: of the batch's n_tokens*g
+// rows) against key tiles tile0 .. tile0 + n_tiles.
+struct Seg {
+    int b, h, row0, n_rows;
+    int t0, n, len;        // the sequence (prefix: the whole batch, t0 = 0)
+    int tile0, n_tiles;    // tile numbers from key 0
+    bool begins, ends;     // the piece holds the unit's first / last tile
+    int ordinal;           // pieces of this CTA before it
+    int first_cta, last_cta;
+};
+
+// Walks a CTA's share piece by piece (own keys).  Uniform over the threads that call it.
+template <int M>
+struct OwnWalk {
+    const PagedArgs& a;
+    int64_t pos, end, base;  // base: line position of the unit's first tile
+    int64_t total;
+    int n_cta;
+    SeqRows s;
+    int b, h, rt, nrt, ut, ordinal;
+
+    __device__ OwnWalk(const PagedArgs& args, const Share& sh)
+        : a(args), pos(sh.pos), end(sh.end), total(sh.total), n_cta(sh.n_cta), b(sh.b), ordinal(0) {
+        if (pos >= end) return;
+        s = seq_rows(a, b);
+        nrt = row_tiles<M>(a, s);
+        const int64_t per_head = head_tiles<M>(a, b);
+        h = (int)(sh.off / per_head);
+        int64_t off = sh.off - h * per_head;
+        rt = 0;
+        ut = unit_tiles<M>(a, s, 0);
+        while (off >= ut) {
+            off -= ut;
+            ++rt;
+            ut = unit_tiles<M>(a, s, rt);
+        }
+        base = pos - off;
+    }
+
+    __device__ bool next(Seg& g) {
+        if (pos >= end) return false;
+        while (ut == 0 || pos >= base + ut) {  // on to the next unit that has keys
+            base += ut;
+            if (++rt >= nrt) {
+                rt = 0;
+                if (++h >= a.Hkv) {
+                    h = 0;
+                    do {
+                        if (++b >= a.n_seqs) return false;
+                        s = seq_rows(a, b);
+                        nrt = row_tiles<M>(a, s);
+                    } while (nrt == 0);
+                }
+            }
+            ut = unit_tiles<M>(a, s, rt);
+        }
+        const int64_t to = min(end, base + ut);
+        g.b = b;
+        g.h = h;
+        g.row0 = rt * M;
+        g.n_rows = min(M, s.n * a.g - g.row0);
+        g.t0 = s.t0;
+        g.n = s.n;
+        g.len = s.len;
+        g.tile0 = a.key_begin / kKeyTile + (int)(pos - base);
+        g.n_tiles = (int)(to - pos);
+        g.begins = pos == base;
+        g.ends = to == base + ut;
+        g.ordinal = ordinal++;
+        g.first_cta = g.begins ? -1 : share_owner(base, total, n_cta);  // -1: this CTA
+        g.last_cta = g.ends ? -1 : share_owner(base + ut - 1, total, n_cta);
+        pos = to;
+        return true;
+    }
+};
+
+// The same over the keys of a shared prefix: units (row tile of the whole batch, head), all of prefix_tiles tiles, in
+// the order head, row tile.
+template <int M>
+struct PrefixWalk {
+    const PagedArgs& a;
+    int64_t pos, end;
+    int tiles, nrt, ordinal;
+
+    __device__ PrefixWalk(const PagedArgs& args, int cta) : a(args), ordinal(0) {
+        tiles = (a.prefix_len + kKeyTile - 1) / kKeyTile;
+        nrt = (a.n_tokens * a.g + M - 1) / M;
+        const int64_t total = (int64_t)a.Hkv * nrt * tiles;
+        pos = total * cta / a.p_ctas;
+        end = total * (cta + 1) / a.p_ctas;
+    }
+
+    __device__ bool next(Seg& g) {
+        if (pos >= end) return false;
+        const int64_t unit = pos / tiles, base = unit * tiles, to = min(end, base + tiles);
+        g.b = -1;
+        g.h = (int)(unit / nrt);
+        g.row0 = (int)(unit % nrt) * M;
+        g.n_rows = min(M, a.n_tokens * a.g - g.row0);
+        g.t0 = 0;
+        g.n = a.n_tokens;
+        g.len = 0;
+        g.tile0 = (int)(pos - base);
+        g.n_tiles = (int)(to - pos);
+        g.begins = pos == base;
+        g.ends = to == base + tiles;
+        g.ordinal = ordinal++;
+        pos = to;
+        return true;
+    }
+};
+
+// Keys that row r of a piece sees: below this limit (0 for a row of no sequence).
+template <bool PREFIX>
+__device__ __forceinline__ int row_limit(const PagedArgs& a, const Seg& g, int r) {
+    const int i = (g.row0 + r) / a.g;
+    if constexpr (!PREFIX) {
+        return visible(a, SeqRows{g.t0, g.n, g.len}, i);
+    } else {
+        int lo = i;  // the sequence of token i
+        if (a.q_start) {
+            int hi = a.n_seqs;
+            lo = 0;
+            while (lo < hi) {  // first b with q_start[b + 1] > i
+                const int mid = (lo + hi) >> 1;
+                if (__ldg(a.q_start + mid + 1) > i) hi = mid; else lo = mid + 1;
+            }
+        }
+        if (lo >= a.n_seqs) return 0;
+        const SeqRows s = seq_rows(a, lo);
+        if (i < s.t0 || i >= s.t0 + s.n) return 0;
+        return min(visible(a, s, i - s.t0), a.prefix_len);
+    }
+}
+
+// First and last key (exclusive) that some row of a piece may see.
+template <bool PREFIX>
+__device__ __forceinline__ int seg_key_end(const PagedArgs& a, const Seg& g) {
+    if constexpr (PREFIX) return a.prefix_len;
+    return visible(a, SeqRows{g.t0, g.n, g.len}, (g.row0 + g.n_rows - 1) / a.g);
+}
+
+// Pages of a piece's keys; an entry outside the pool reads as -1.
+template <bool PREFIX>
+__device__ __forceinline__ int seg_page(const PagedArgs& a, const Seg& g, int j) {
+    const int id = __ldg((PREFIX ? a.prefix_pages : a.page_table + (int64_t)g.b * a.max_pages) + j);
+    return (unsigned)id < (unsigned)a.n_pages ? id : -1;
+}
+
+// Where the result of row r of a piece goes: `out` (final, dtype of q) or `part` (float32), and its log-sum-exp
+// (natural log in lse, log2 units elsewhere).
+struct RowDst {
+    void* out;
+    float* part;
+    float* lse;
+};
+
+template <int M, bool PREFIX>
+__device__ __forceinline__ RowDst row_dst(const PagedArgs& a, const Seg& g, int r, int cta) {
+    const int R = g.row0 + r, i = R / a.g;
+    const int64_t row = (int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g);
+    if (!PREFIX && g.begins && g.ends) {
+        if (a.prefix_len == 0)
+            return {static_cast<char*>(a.o) + row * a.d * a.elem, nullptr, a.lse + row};
+        return {nullptr, a.own_o + row * a.d, a.own_lse + row};
+    }
+    const int slot = PREFIX ? g.ordinal : (g.begins ? 1 : 0);
+    const int64_t at = ((int64_t)cta * 2 + slot) * M + r;
+    return PREFIX ? RowDst{nullptr, a.pslot_o + at * a.d, a.pslot_l + at}
+                  : RowDst{nullptr, a.slot_o + at * a.d, a.slot_l + at};
+}
+
+// Tells paged_merge_kernel about row r of a piece; called by the CTA that holds the unit's last tile.
+template <int M>
+__device__ __forceinline__ void note_row(const PagedArgs& a, const Seg& g, int r, int cta) {
+    const int R = g.row0 + r, i = R / a.g;
+    const int64_t row = (int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g);
+    uint2 w;
+    if (g.begins) {
+        w = make_uint2(a.prefix_len ? kRowWhole : kRowDone, 0);
+    } else {
+        w = make_uint2(kRowSplit | (uint32_t)r << 2, (uint32_t)g.first_cta | (uint32_t)cta << 16);
+    }
+    a.row_info[row] = w;
+}
+
+// Rows that no unit covers: those of sequences whose row tiles have no keys (o = 0, lse = -inf, or left to the prefix),
+// and rows of no sequence (not touched).  Spread over the CTAs; all threads of the CTA (NT) call it.
+template <typename T, int M, int NT>
+__device__ void finish_empty_rows(const PagedArgs& a, int cta, int n_cta) {
+    const int lo = a.q_start ? min(max(__ldg(a.q_start), 0), a.n_tokens) : 0;
+    const int hi = a.q_start ? min(max(__ldg(a.q_start + a.n_seqs), lo), a.n_tokens) : a.n_tokens;
+    for (int64_t x = (int64_t)cta * NT + threadIdx.x; x < (int64_t)(a.n_tokens - (hi - lo)) * a.Hq;
+         x += (int64_t)n_cta * NT) {
+        const int64_t row = x < (int64_t)lo * a.Hq ? x : x + (int64_t)(hi - lo) * a.Hq;
+        a.row_info[row] = make_uint2(kRowDone, 0);
+    }
+    for (int b = cta; b < a.n_seqs; b += n_cta) {
+        const SeqRows s = seq_rows(a, b);
+        const int nrt = row_tiles<M>(a, s);
+        for (int rt = 0; rt < nrt; ++rt) {
+            if (unit_tiles<M>(a, s, rt) > 0) break;  // limits grow with the row: the later tiles have keys, too
+            const int rows = min(M, s.n * a.g - rt * M);
+            for (int x = threadIdx.x; x < rows * a.Hkv; x += NT) {
+                const int h = x / rows, R = rt * M + x % rows, i = R / a.g;
+                const int64_t row = (int64_t)(s.t0 + i) * a.Hq + h * a.g + (R - i * a.g);
+                a.row_info[row] = make_uint2(a.prefix_len ? kRowNone : kRowDone, 0);
+                if (a.prefix_len == 0) {
+                    a.lse[row] = -INFINITY;
+                    uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + row * a.d);
+                    for (int c = 0; c < a.d * (int)sizeof(T) / 16; ++c) o[c] = make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
+    }
+}
+
+}  // namespace usp

@@ -1,0 +1,279 @@
+// Attention over a paged cache (decoding, verification, chunks of prompts) and behind a shared prefix.
+//
+// Per row (token, query head): S_j = scale q.k_j over the keys the row sees, o = softmax(S) V, lse = ln sum exp(S), in one
+// pass over the keys with a running maximum and sum.  How the work is cut is explained in paged.cuh.
+#include <cmath>
+
+#include <cuda_bf16.h>
+
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace usp {
+
+namespace {
+
+constexpr int kSms = 152;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// ---------------------------------------------------------------- CUDA cores
+// Four warps, each every fourth key; a lane holds D/32 columns of the row's key, value and output.
+constexpr int kSimpleThreads = 128;
+constexpr int kSimpleRows = 8;
+
+template <typename T, int D, bool PREFIX>
+__global__ void __launch_bounds__(kSimpleThreads) paged_simple_kernel(const PagedArgs a) {
+    constexpr int M = kSimpleRows, V = D / 32, kWarps = kSimpleThreads / 32;
+    __shared__ Share share;
+    __shared__ float s_acc[kWarps][M][D];
+    __shared__ float s_m[kWarps][M], s_l[kWarps][M];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
+    if constexpr (!PREFIX) {
+        find_share<M, kSimpleThreads>(a, cta, a.ctas, &share);
+        finish_empty_rows<T, M, kSimpleThreads>(a, cta, a.ctas);
+    }
+    auto run = [&](const Seg& g) {
+        float q[M][V], acc[M][V], m[M], l[M];
+        int lim[M];
+#pragma unroll
+        for (int r = 0; r < M; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+            lim[r] = 0;
+            const int R = g.row0 + r, i = R / a.g;
+#pragma unroll
+            for (int c = 0; c < V; ++c) acc[r][c] = q[r][c] = 0.f;
+            if (r < g.n_rows) {
+                lim[r] = row_limit<PREFIX>(a, g, r);
+                const T* src = static_cast<const T*>(a.q) +
+                               ((int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g)) * D + lane * V;
+#pragma unroll
+                for (int c = 0; c < V; ++c) q[r][c] = to_f32(src[c]) * a.scale_log2;
+            }
+        }
+        const int first = PREFIX ? 0 : a.key_begin;
+        const int k0 = max(g.tile0 * kKeyTile, first);
+        const int k1 = min((g.tile0 + g.n_tiles) * kKeyTile, seg_key_end<PREFIX>(a, g));
+        for (int j = k0 + warp; j < k1; j += kWarps) {
+            const int page = seg_page<PREFIX>(a, g, j >> a.page_log2);
+            if (page < 0) continue;
+            const int64_t at = ((((int64_t)page * a.Hkv + g.h) << a.page_log2) + (j & ((1 << a.page_log2) - 1))) * D +
+                               lane * V;
+            const T* kj = static_cast<const T*>(a.k_pages) + at;
+            const T* vj = static_cast<const T*>(a.v_pages) + at;
+            float kv[V], vv[V];
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+                kv[c] = to_f32(kj[c]);
+                vv[c] = to_f32(vj[c]);
+            }
+#pragma unroll
+            for (int r = 0; r < M; ++r) {
+                float x = 0.f;
+#pragma unroll
+                for (int c = 0; c < V; ++c) x = fmaf(q[r][c], kv[c], x);
+                for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+                if (j < lim[r]) {
+                    const float mn = fmaxf(m[r], x);
+                    const float ms = mn == -INFINITY ? 0.f : mn;
+                    const float al = exp2f(m[r] - ms), p = exp2f(x - ms);
+                    m[r] = mn;
+                    l[r] = l[r] * al + p;
+#pragma unroll
+                    for (int c = 0; c < V; ++c) acc[r][c] = acc[r][c] * al + p * vv[c];
+                }
+            }
+        }
+        // join the four warps
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < M; ++r) {
+#pragma unroll
+            for (int c = 0; c < V; ++c) s_acc[warp][r][lane * V + c] = acc[r][c];
+            if (lane == 0) {
+                s_m[warp][r] = m[r];
+                s_l[warp][r] = l[r];
+            }
+        }
+        __syncthreads();
+        for (int x = threadIdx.x; x < g.n_rows * D; x += kSimpleThreads) {
+            const int r = x / D, c = x % D;
+            float mx = -INFINITY;
+            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][r]);
+            float sum = 0.f, o = 0.f;
+            const float ms = mx == -INFINITY ? 0.f : mx;
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = exp2f(s_m[w][r] - ms);
+                sum += f * s_l[w][r];
+                o += f * s_acc[w][r][c];
+            }
+            const bool has = sum > 0.f;
+            o = has ? o / sum : 0.f;
+            const float lse2 = has ? ms + log2f(sum) : -INFINITY;
+            const RowDst dst = row_dst<M, PREFIX>(a, g, r, cta);
+            if (dst.out) {
+                put(static_cast<T*>(dst.out) + c, o);
+                if (c == 0) *dst.lse = lse2 * kLn2;
+            } else {
+                dst.part[c] = o;
+                if (c == 0) *dst.lse = lse2;
+            }
+            if (!PREFIX && g.ends && c == 0) note_row<M>(a, g, r, cta);
+        }
+        __syncthreads();
+    };
+    Seg g;
+    if constexpr (PREFIX) {
+        PrefixWalk<M> walk(a, cta);
+        while (walk.next(g)) run(g);
+    } else {
+        OwnWalk<M> walk(a, share);
+        while (walk.next(g)) run(g);
+    }
+}
+
+// ---------------------------------------------------------------- joining partial results
+// One warp per row: o = sum_c 2^(lse_c - lse) o_c over the row's partial results, prefix first, keys in order.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= (int64_t)a.n_tokens * a.Hq) return;
+    const uint2 info = a.row_info[row];
+    const uint32_t kind = info.x & 3u;
+    if (kind == kRowDone) return;
+    // the row's own parts: n_own of them, part c at own_o + c * step
+    const float *oo = nullptr, *ol = nullptr;
+    int n_own = 0;
+    int64_t o0 = 0, step = 0;
+    if (kind == kRowWhole) {
+        oo = a.own_o + row * D;
+        ol = a.own_lse + row;
+        n_own = 1;
+    } else if (kind == kRowSplit) {
+        const int c0 = info.y & 0xffffu, c1 = info.y >> 16, r = info.x >> 2;
+        n_own = c1 - c0 + 1;
+        o0 = ((int64_t)c0 * 2 + 1) * a.rows + r;  // slot 1 of c0, then slot 0 of the CTAs after it
+        step = 2 * a.rows;
+        oo = a.slot_o;
+        ol = a.slot_l;
+    }
+    auto own_at = [&](int c) { return kind == kRowWhole ? (int64_t)0 : c == 0 ? o0 : o0 - a.rows + c * step; };
+    int n_pre = 0, pc0 = 0;
+    int64_t p_total = 0, p_base = 0;
+    int p_r = 0;
+    if (a.prefix_len > 0) {
+        const int t = (int)(row / a.Hq), hq = (int)(row % a.Hq), h = hq / a.g;
+        const int64_t R = (int64_t)t * a.g + (hq - h * a.g);
+        const int tiles = (a.prefix_len + kKeyTile - 1) / kKeyTile;
+        const int nrt = (int)(((int64_t)a.n_tokens * a.g + a.p_rows - 1) / a.p_rows);
+        p_total = (int64_t)a.Hkv * nrt * tiles;
+        p_base = ((int64_t)h * nrt + R / a.p_rows) * tiles;
+        p_r = (int)(R % a.p_rows);
+        pc0 = share_owner(p_base, p_total, a.p_ctas);
+        n_pre = share_owner(p_base + tiles - 1, p_total, a.p_ctas) - pc0 + 1;
+    }
+    // a CTA's pieces are numbered: the unit's piece is number 1 where the CTA's share begins before the unit
+    auto pre_at = [&](int c) {
+        const int cta = pc0 + c;
+        const int slot = p_total * cta / a.p_ctas < p_base ? 1 : 0;
+        return ((int64_t)cta * 2 + slot) * a.p_rows + p_r;
+    };
+    float mx = -INFINITY;
+    for (int c = lane; c < n_pre; c += 32) mx = fmaxf(mx, a.pslot_l[pre_at(c)]);
+    for (int c = lane; c < n_own; c += 32) mx = fmaxf(mx, ol[own_at(c)]);
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+    const float ms = mx == -INFINITY ? 0.f : mx;
+    float acc[V], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    auto add = [&](const float* o, float l) {
+        const float w = exp2f(l - ms);
+        sum += w;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(w, o[lane * V + e], acc[e]);
+    };
+    for (int c = 0; c < n_pre; ++c) add(a.pslot_o + pre_at(c) * D, a.pslot_l[pre_at(c)]);
+    for (int c = 0; c < n_own; ++c) add(oo + own_at(c) * D, ol[own_at(c)]);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    T* out = static_cast<T*>(a.o) + row * D + lane * V;
+#pragma unroll
+    for (int e = 0; e < V; ++e) put(out + e, acc[e] * inv);
+    if (lane == 0) a.lse[row] = sum > 0.f ? (ms + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+template <typename T, int D>
+cudaError_t simple_t(const PagedArgs& a, bool prefix, cudaStream_t s) {
+    if (prefix)
+        paged_simple_kernel<T, D, true><<<a.p_ctas, kSimpleThreads, 0, s>>>(a);
+    else
+        paged_simple_kernel<T, D, false><<<a.ctas, kSimpleThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <bool PREFIX>
+cudaError_t simple(const PagedArgs& a, cudaStream_t s) {
+    if (a.elem == 4) return a.d == 64 ? simple_t<float, 64>(a, PREFIX, s) : simple_t<float, 128>(a, PREFIX, s);
+    return a.d == 64 ? simple_t<__nv_bfloat16, 64>(a, PREFIX, s) : simple_t<__nv_bfloat16, 128>(a, PREFIX, s);
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+}  // namespace
+
+size_t paged_plan(PagedArgs* a, int max_q, void* ws) {
+    (void)max_q;
+    const int64_t rows = (int64_t)a->n_tokens * a->Hq;
+    a->rows = a->p_rows = kSimpleRows;
+    a->ctas = kSms * 4;
+    a->p_ctas = 0;
+    if (a->prefix_len > 0) {
+        // a share no longer than a unit touches at most two units: one slot each
+        const int64_t units = ((int64_t)a->n_tokens * a->g + a->p_rows - 1) / a->p_rows * a->Hkv;
+        const int64_t tiles = units * ((a->prefix_len + kKeyTile - 1) / kKeyTile);
+        a->p_ctas = (int)(units > kSms * 4 ? units : tiles < kSms * 4 ? tiles : kSms * 4);
+    }
+    size_t at = 0;
+    char* w = static_cast<char*>(ws);
+    auto take = [&](size_t bytes) {
+        char* p = w ? w + at : nullptr;
+        at += align256(bytes);
+        return p;
+    };
+    a->row_info = reinterpret_cast<uint2*>(take(rows * sizeof(uint2)));
+    a->slot_o = reinterpret_cast<float*>(take((size_t)a->ctas * 2 * a->rows * a->d * 4));
+    a->slot_l = reinterpret_cast<float*>(take((size_t)a->ctas * 2 * a->rows * 4));
+    a->own_o = a->own_lse = a->pslot_o = a->pslot_l = nullptr;
+    if (a->prefix_len > 0) {
+        a->own_o = reinterpret_cast<float*>(take((size_t)rows * a->d * 4));
+        a->own_lse = reinterpret_cast<float*>(take((size_t)rows * 4));
+        a->pslot_o = reinterpret_cast<float*>(take((size_t)a->p_ctas * 2 * a->p_rows * a->d * 4));
+        a->pslot_l = reinterpret_cast<float*>(take((size_t)a->p_ctas * 2 * a->p_rows * 4));
+    }
+    return at;
+}
+
+cudaError_t launch_paged_own(const PagedArgs& a, cudaStream_t stream) { return simple<false>(a, stream); }
+
+cudaError_t launch_paged_prefix(const PagedArgs& a, cudaStream_t stream) { return simple<true>(a, stream); }
+
+cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream) {
+    const int64_t rows = (int64_t)a.n_tokens * a.Hq;
+    const unsigned blocks = (unsigned)((rows + 7) / 8);
+    if (a.elem == 4) {
+        if (a.d == 64) paged_merge_kernel<float, 64><<<blocks, 256, 0, stream>>>(a);
+        else paged_merge_kernel<float, 128><<<blocks, 256, 0, stream>>>(a);
+    } else {
+        if (a.d == 64) paged_merge_kernel<__nv_bfloat16, 64><<<blocks, 256, 0, stream>>>(a);
+        else paged_merge_kernel<__nv_bfloat16, 128><<<blocks, 256, 0, stream>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace usp

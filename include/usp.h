@@ -396,6 +396,116 @@ usp_status usp_hybrid_attn_bwd(const usp_problem* p, int Pu, const void* q, cons
 usp_status usp_ring_merge(int64_t rows, int d, const float* o_a, const float* lse_a, const float* o_b,
                           const float* lse_b, float* o, float* lse, usp_stream stream);
 
+/* ---- serving: a paged key/value cache, what fills it and what reads it.
+ * The paths above attend a whole sequence at once; answering token by token
+ * needs the keys and values of the tokens so far.  They are kept in a pool of
+ * pages that sequences of any length share, each page page_size tokens of
+ * every KV head, head-major:
+ *   k_pages, v_pages  [n_pages][Hkv][page_size][d]   (dtype)
+ *   page_table        int32 [n_seqs][max_pages]: page j of a sequence holds
+ *                     its tokens [j*page_size, (j+1)*page_size)
+ * Tokens of a call are rows of ragged batches: q and o are [n_tokens][Hq][d],
+ * lse is float32 [n_tokens][Hq] (natural log).  A sequence-sharded tensor
+ * [P][B][N/P][H][d] is such a batch of P*B*N/P rows.  Index arrays are int32
+ * device arrays, 4-byte aligned; their values are read on the device, so a
+ * captured graph replays with new values.  No index value makes a kernel
+ * access memory outside the buffers: what an index out of range means is said
+ * at each call.
+ * Requirements: n_pages, n_seqs, max_pages >= 0; page_size in {16, 32, 64,
+ * 128, 256}; Hq, Hkv >= 1 and Hq % Hkv == 0; Hq <= 65535; d in {64, 128};
+ * max_pages * page_size and n_pages * Hkv below 2^31. */
+typedef struct {
+    int n_pages;
+    int page_size;
+    int n_seqs;
+    int max_pages;
+    int Hq;
+    int Hkv;
+    int d;
+    int causal;  /* attention: see usp_paged_attn */
+    float scale; /* softmax scale, 0: 1/sqrt(d) */
+    int dtype;   /* usp_dtype of the pool, q and o */
+} usp_cache;
+
+/* Rotary position embedding of q and k, and k and v written into the cache,
+ * in one pass.  Token t of sequence s = seq[t], slot p = pos[t], rotation
+ * position r = rot_pos[t] (rot_pos NULL: r = p), per head and i < rot/2, with
+ * the pair (a, b) = elements (i, i + rot/2), or (2i, 2i+1) if interleaved:
+ *   a' = a cos(r f_i) - b sin(r f_i) ;  b' = b cos(r f_i) + a sin(r f_i)
+ * with f_i = inv_freq[i] (float32 [rot/2]); elements rot.. pass unchanged.
+ * The angle is formed in float64 (a float32 product of position 10^6 and f_0
+ * would be off by up to 0.06 rad), the rotation in float32, rounded once.
+ *   q_out [n_tokens][Hq][d] = rotated q ;  k_out [n_tokens][Hkv][d] = rotated k
+ *   k_pages[page_table[s][p / page_size]][h][p % page_size] = rotated k,
+ *   v_pages likewise = v
+ * q, k, v: rows of H*d contiguous elements q_stride, k_stride, v_stride
+ * elements apart (slices of one projection's output are fine); 16-byte
+ * aligned, strides at least the row and a multiple of 16 bytes.
+ * q with q_out may both be NULL (no queries), and k_out may be NULL.  q_out
+ * may be q and k_out may be k where the stride is the row length; otherwise
+ * no overlap.  rot: a multiple of 16 with 0 <= rot <= d; 0 rotates nothing
+ * (inv_freq may be NULL).
+ * A token without a slot -- seq outside [0, n_seqs), pos outside [0,
+ * max_pages*page_size), or a page table entry outside [0, n_pages) -- is
+ * padding: nothing is written for it, its rows of q_out and k_out stay as
+ * they were.  Two tokens of a call must not share a slot (the slot would hold
+ * pieces of both). */
+usp_status usp_kv_append(const usp_cache* c, int n_tokens, const void* q, int64_t q_stride, const void* k,
+                         int64_t k_stride, const void* v, int64_t v_stride, const int32_t* seq, const int32_t* pos,
+                         const int32_t* rot_pos, const float* inv_freq, int rot, int interleaved, void* q_out,
+                         void* k_out, void* k_pages, void* v_pages, const int32_t* page_table, usp_stream stream);
+
+/* Bytes of workspace usp_paged_attn needs; 0 for an invalid problem. */
+size_t usp_paged_attn_workspace_size(const usp_cache* c, int n_tokens, int max_q);
+
+/* Attention of each sequence's newest tokens over its cached keys: decoding
+ * (one token each), verification of drafted tokens, further chunks of prompts.
+ * Sequence s has n_q = q_start[s+1] - q_start[s] tokens in this call, rows
+ * q_start[s] .. of q, and len = seq_lens[s] cached tokens (those of this call
+ * included).  Row i of it sees the keys j < vis,
+ *   vis = len - n_q + i + 1 (causal)  or  len (not causal: the states of an
+ *   encoder, say),
+ *   S_j = scale * q . K_j ;  o = softmax_j(S) V ;  lse = ln sum_j exp(S_j)
+ * A row that sees no key (len 0, or vis <= 0) gets o = 0 and lse = -inf.
+ * q_start: int32 [n_seqs + 1], not decreasing; NULL: one token per sequence
+ * (n_tokens == n_seqs).  Rows of no sequence (before q_start[0], from
+ * q_start[n_seqs] on) stay as they were.  max_q: the largest n_q (>= 1); it
+ * picks the kernel for that many rows, and a wrong value costs speed only.
+ * Values out of range: q_start is clamped to [0, n_tokens], seq_lens to [0,
+ * max_pages*page_size]; keys of a page table entry outside [0, n_pages) are
+ * left out.  What pages hold beyond a sequence's length (NaN, too) never
+ * reaches a result.  A value that is not finite in a key or value below len
+ * may reach every row of its sequence, masked or not (0 * inf in the product).
+ * BF16: float32 scores, sums and accumulation, probabilities rounded to bf16
+ * for the product with V (o divides by the sum of the rounded ones); F32:
+ * float32 throughout.  Results do not depend on the run (fixed order of sums).
+ * ws: at least usp_paged_attn_workspace_size(c, n_tokens, max_q) bytes,
+ * 256-byte aligned, contents on entry irrelevant; calls that can overlap on
+ * the GPU need one each. */
+usp_status usp_paged_attn(const usp_cache* c, int n_tokens, int max_q, const void* q, const void* k_pages,
+                          const void* v_pages, const int32_t* page_table, const int32_t* seq_lens,
+                          const int32_t* q_start, void* o, float* lse, void* ws, size_t ws_bytes, usp_stream stream);
+
+/* Bytes of workspace usp_prefix_attn needs; 0 for an invalid problem. */
+size_t usp_prefix_attn_workspace_size(const usp_cache* c, int n_tokens, int max_q, int prefix_len);
+
+/* usp_paged_attn for a batch whose sequences share their first prefix_len
+ * tokens: those keys and values are read from prefix_pages (int32
+ * [ceil(prefix_len/page_size)], pages of the same pool) once for the whole
+ * batch -- one matrix product over all rows per KV head -- and joined by
+ * log-sum-exp with each sequence's own keys prefix_len .. len-1, which its page
+ * table gives as always (entries of whole prefix pages are not read; where the
+ * prefix ends inside a page, the sequence's own page holds its tokens from
+ * there on).  Masks, lengths (seq_lens counts the prefix), rows and checks as
+ * usp_paged_attn, whose results it gives up to rounding; a sequence no longer
+ * than the prefix sees that part of it.  0 <= prefix_len <=
+ * max_pages*page_size.  ws: at least usp_prefix_attn_workspace_size(c,
+ * n_tokens, max_q, prefix_len) bytes, 256-byte aligned. */
+usp_status usp_prefix_attn(const usp_cache* c, int n_tokens, int max_q, const void* q, const void* k_pages,
+                           const void* v_pages, const int32_t* page_table, const int32_t* seq_lens,
+                           const int32_t* q_start, const int32_t* prefix_pages, int prefix_len, void* o, float* lse,
+                           void* ws, size_t ws_bytes, usp_stream stream);
+
 /* ---- kernel tracing ----
  * When enabled, every kernel the library launches is bracketed by two CUDA
  * events recorded on the launch's stream (a few microseconds per launch).
