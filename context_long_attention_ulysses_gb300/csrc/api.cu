@@ -1321,6 +1321,13 @@ static usp_status paged_attn(const usp_cache* c, int n_tokens, int max_q, const 
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return USP_ERR_MISALIGNED;
     PagedArgs a = paged_args(c, n_tokens, prefix_len);
     if (ws_bytes < paged_plan(&a, max_q, ws)) return USP_ERR_WORKSPACE;
+    if (!pool) {  // no page: no sequence has a key, and nothing is read through these pointers
+        a = paged_args(c, n_tokens, 0);
+        paged_plan(&a, max_q, ws);
+        a.max_pages = 0;
+        a.n_pages = 1;
+        k_pages = v_pages = q;
+    }
     a.q = q; a.k_pages = k_pages; a.v_pages = v_pages; a.page_table = page_table; a.seq_lens = seq_lens;
     a.q_start = q_start; a.prefix_pages = prefix_pages; a.o = o; a.lse = lse;
     a.status = status_ptr();

@@ -178,6 +178,7 @@ struct PagedArgs {
 size_t paged_plan(PagedArgs* a, int max_q, void* ws);
 cudaError_t launch_paged_own(const PagedArgs& a, cudaStream_t stream);
 cudaError_t launch_paged_prefix(const PagedArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_mma(const PagedArgs& a, bool prefix, cudaStream_t stream);  // paged_mma.cu
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream);
 
 // ---- tensor maps (api.cu)

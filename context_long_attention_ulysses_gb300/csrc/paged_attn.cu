@@ -2,6 +2,7 @@
 //
 // Per row (token, query head): S_j = scale q.k_j over the keys the row sees, o = softmax(S) V, lse = ln sum exp(S), in one
 // pass over the keys with a running maximum and sum.  How the work is cut is explained in paged.cuh.
+#include <algorithm>
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -219,25 +220,34 @@ cudaError_t simple_t(const PagedArgs& a, bool prefix, cudaStream_t s) {
 
 template <bool PREFIX>
 cudaError_t simple(const PagedArgs& a, cudaStream_t s) {
-    if (a.elem == 4) return a.d == 64 ? simple_t<float, 64>(a, PREFIX, s) : simple_t<float, 128>(a, PREFIX, s);
-    return a.d == 64 ? simple_t<__nv_bfloat16, 64>(a, PREFIX, s) : simple_t<__nv_bfloat16, 128>(a, PREFIX, s);
+    return a.d == 64 ? simple_t<float, 64>(a, PREFIX, s) : simple_t<float, 128>(a, PREFIX, s);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
+// Rows of a unit for `rows` rows per KV head.
+static int pick_rows(const PagedArgs& a, int64_t rows) {
+    if (a.elem == 4) return kSimpleRows;
+    return rows <= 16 ? 16 : 32;
+}
+
+static int resident_ctas(const PagedArgs& a) { return a.elem == 4 ? kSms * 4 : kSms * 2; }
+
 size_t paged_plan(PagedArgs* a, int max_q, void* ws) {
-    (void)max_q;
     const int64_t rows = (int64_t)a->n_tokens * a->Hq;
-    a->rows = a->p_rows = kSimpleRows;
-    a->ctas = kSms * 4;
-    a->p_ctas = 0;
+    a->rows = pick_rows(*a, (int64_t)max_q * a->g);
+    a->ctas = resident_ctas(*a);
+    a->p_rows = a->p_ctas = 0;
     if (a->prefix_len > 0) {
-        // a share no longer than a unit touches at most two units: one slot each
-        const int64_t units = ((int64_t)a->n_tokens * a->g + a->p_rows - 1) / a->p_rows * a->Hkv;
+        const int64_t batch = (int64_t)a->n_tokens * a->g;
+        a->p_rows = pick_rows(*a, batch);
+        // no share longer than a unit, so that it touches two units at most: one slot each; and none empty
+        const int64_t units = (batch + a->p_rows - 1) / a->p_rows * a->Hkv;
         const int64_t tiles = units * ((a->prefix_len + kKeyTile - 1) / kKeyTile);
-        a->p_ctas = (int)(units > kSms * 4 ? units : tiles < kSms * 4 ? tiles : kSms * 4);
+        const int64_t want = std::min<int64_t>(resident_ctas(*a), tiles);
+        a->p_ctas = (int)std::max(units, want);
     }
     size_t at = 0;
     char* w = static_cast<char*>(ws);
@@ -259,9 +269,13 @@ size_t paged_plan(PagedArgs* a, int max_q, void* ws) {
     return at;
 }
 
-cudaError_t launch_paged_own(const PagedArgs& a, cudaStream_t stream) { return simple<false>(a, stream); }
+cudaError_t launch_paged_own(const PagedArgs& a, cudaStream_t stream) {
+    return a.elem == 4 ? simple<false>(a, stream) : launch_paged_mma(a, false, stream);
+}
 
-cudaError_t launch_paged_prefix(const PagedArgs& a, cudaStream_t stream) { return simple<true>(a, stream); }
+cudaError_t launch_paged_prefix(const PagedArgs& a, cudaStream_t stream) {
+    return a.elem == 4 ? simple<true>(a, stream) : launch_paged_mma(a, true, stream);
+}
 
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream) {
     const int64_t rows = (int64_t)a.n_tokens * a.Hq;
