@@ -167,6 +167,7 @@ struct PagedArgs {
     // the plan: row-tile sizes and CTAs of the own and the prefix part, and the workspace
     int rows, p_rows;
     int ctas, p_ctas;
+    int p_keys;  // keys per tile of the prefix part
     uint2* row_info;               // per row of o
     float *own_o, *own_lse;        // prefix only: own part of whole units, [n_tokens][Hq][d], [n_tokens][Hq]
     float *slot_o, *slot_l;        // [ctas][2][rows][d], [ctas][2][rows]
@@ -178,7 +179,8 @@ struct PagedArgs {
 size_t paged_plan(PagedArgs* a, int max_q, void* ws);
 cudaError_t launch_paged_own(const PagedArgs& a, cudaStream_t stream);
 cudaError_t launch_paged_prefix(const PagedArgs& a, cudaStream_t stream);
-cudaError_t launch_paged_mma(const PagedArgs& a, bool prefix, cudaStream_t stream);  // paged_mma.cu
+cudaError_t launch_paged_mma(const PagedArgs& a, bool prefix, cudaStream_t stream);  // paged_mma.cu: up to 32 rows
+cudaError_t launch_paged_tc(const PagedArgs& a, bool prefix, cudaStream_t stream);   // paged_tc.cu: 128 or 256 rows
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream);
 
 // ---- tensor maps (api.cu)

@@ -3,7 +3,7 @@
 //
 // A unit is (sequence, KV head, tile of M consecutive rows), a row being one
 // (token, query head of the group): K and V of the head are read once for all
-// M rows.  A unit's keys are cut into tiles of kKeyTile.  All tiles of all
+// M rows.  A unit's keys are cut into tiles of KT.  All tiles of all
 // units, in the order sequence, head, row tile, key tile, form one line of W
 // tiles; CTA c of G takes the tiles [c*W/G, (c+1)*W/G).  So every CTA has the
 // same work whatever the lengths are, one sequence of 128K tokens spreads over
@@ -24,8 +24,6 @@
 #include "kernels.h"
 
 namespace usp {
-
-constexpr int kKeyTile = 64;  // keys per tile
 
 // What paged_merge_kernel does with a row: word x = kind | row in the tile << 2, y = first CTA | last CTA << 16.
 enum RowKind : uint32_t {
@@ -59,11 +57,11 @@ __device__ __forceinline__ int visible(const PagedArgs& a, const SeqRows& s, int
 }
 
 // Key tiles of row tile rt of a sequence: those that hold a key in [key_begin, vis of the tile's last row).
-template <int M>
+template <int M, int KT>
 __device__ __forceinline__ int unit_tiles(const PagedArgs& a, const SeqRows& s, int rt) {
     const int last = min(((rt + 1) * M - 1) / a.g, s.n - 1);
     const int end = visible(a, s, last);
-    return end > a.key_begin ? (end + kKeyTile - 1) / kKeyTile - a.key_begin / kKeyTile : 0;
+    return end > a.key_begin ? (end + KT - 1) / KT - a.key_begin / KT : 0;
 }
 
 template <int M>
@@ -72,14 +70,14 @@ __device__ __forceinline__ int row_tiles(const PagedArgs& a, const SeqRows& s) {
 }
 
 // Key tiles of all row tiles of one head of a sequence.
-template <int M>
+template <int M, int KT>
 __device__ __forceinline__ int64_t head_tiles(const PagedArgs& a, int b) {
     const SeqRows s = seq_rows(a, b);
     const int nrt = row_tiles<M>(a, s);
     if (nrt == 0) return 0;
-    if (!a.causal || s.n == 1) return (int64_t)nrt * unit_tiles<M>(a, s, 0);
+    if (!a.causal || s.n == 1) return (int64_t)nrt * unit_tiles<M, KT>(a, s, 0);
     int64_t sum = 0;
-    for (int rt = 0; rt < nrt; ++rt) sum += unit_tiles<M>(a, s, rt);
+    for (int rt = 0; rt < nrt; ++rt) sum += unit_tiles<M, KT>(a, s, rt);
     return sum;
 }
 
@@ -91,13 +89,13 @@ struct Share {
 };
 
 // Computed by all threads of the CTA (a scan over the sequences; NT threads), result in *out (shared memory).
-template <int M, int NT>
+template <int M, int KT, int NT>
 __device__ void find_share(const PagedArgs& a, int cta, int n_cta, Share* out) {
     constexpr int kWarps = NT / 32;
     __shared__ int64_t part[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t mine = 0;
-    for (int b = threadIdx.x; b < a.n_seqs; b += NT) mine += head_tiles<M>(a, b);
+    for (int b = threadIdx.x; b < a.n_seqs; b += NT) mine += head_tiles<M, KT>(a, b);
     for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
     if (lane == 0) part[warp] = mine;
     if (threadIdx.x == 0) *out = Share{0, 0, 0, 0, a.n_seqs, 1};
@@ -112,7 +110,7 @@ __device__ void find_share(const PagedArgs& a, int cta, int n_cta, Share* out) {
     for (int b0 = 0; b0 < a.n_seqs; b0 += NT) {  // chunk by chunk: inclusive scan of the sequences' tiles
         __syncthreads();
         const int b = b0 + threadIdx.x;
-        const int64_t cost = b < a.n_seqs ? head_tiles<M>(a, b) * a.Hkv : 0;
+        const int64_t cost = b < a.n_seqs ? head_tiles<M, KT>(a, b) * a.Hkv : 0;
         int64_t inc = cost;
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t up = __shfl_up_sync(~0u, inc, o);
@@ -147,7 +145,7 @@ struct Seg {
 };
 
 // Walks a CTA's share piece by piece (own keys).  Uniform over the threads that call it.
-template <int M>
+template <int M, int KT>
 struct OwnWalk {
     const PagedArgs& a;
     int64_t pos, end, base;  // base: line position of the unit's first tile
@@ -161,15 +159,15 @@ struct OwnWalk {
         if (pos >= end) return;
         s = seq_rows(a, b);
         nrt = row_tiles<M>(a, s);
-        const int64_t per_head = head_tiles<M>(a, b);
+        const int64_t per_head = head_tiles<M, KT>(a, b);
         h = (int)(sh.off / per_head);
         int64_t off = sh.off - h * per_head;
         rt = 0;
-        ut = unit_tiles<M>(a, s, 0);
+        ut = unit_tiles<M, KT>(a, s, 0);
         while (off >= ut) {
             off -= ut;
             ++rt;
-            ut = unit_tiles<M>(a, s, rt);
+            ut = unit_tiles<M, KT>(a, s, rt);
         }
         base = pos - off;
     }
@@ -189,7 +187,7 @@ struct OwnWalk {
                     } while (nrt == 0);
                 }
             }
-            ut = unit_tiles<M>(a, s, rt);
+            ut = unit_tiles<M, KT>(a, s, rt);
         }
         const int64_t to = min(end, base + ut);
         g.b = b;
@@ -199,7 +197,7 @@ struct OwnWalk {
         g.t0 = s.t0;
         g.n = s.n;
         g.len = s.len;
-        g.tile0 = a.key_begin / kKeyTile + (int)(pos - base);
+        g.tile0 = a.key_begin / KT + (int)(pos - base);
         g.n_tiles = (int)(to - pos);
         g.begins = pos == base;
         g.ends = to == base + ut;
@@ -213,14 +211,14 @@ struct OwnWalk {
 
 // The same over the keys of a shared prefix: units (row tile of the whole batch, head), all of prefix_tiles tiles, in
 // the order head, row tile.
-template <int M>
+template <int M, int KT>
 struct PrefixWalk {
     const PagedArgs& a;
     int64_t pos, end;
     int tiles, nrt, ordinal;
 
     __device__ PrefixWalk(const PagedArgs& args, int cta) : a(args), ordinal(0) {
-        tiles = (a.prefix_len + kKeyTile - 1) / kKeyTile;
+        tiles = (a.prefix_len + KT - 1) / KT;
         nrt = (a.n_tokens * a.g + M - 1) / M;
         const int64_t total = (int64_t)a.Hkv * nrt * tiles;
         pos = total * cta / a.p_ctas;
@@ -323,7 +321,7 @@ __device__ __forceinline__ void note_row(const PagedArgs& a, const Seg& g, int r
 
 // Rows that no unit covers: those of sequences whose row tiles have no keys (o = 0, lse = -inf, or left to the prefix),
 // and rows of no sequence (not touched).  Spread over the CTAs; all threads of the CTA (NT) call it.
-template <typename T, int M, int NT>
+template <typename T, int M, int KT, int NT>
 __device__ void finish_empty_rows(const PagedArgs& a, int cta, int n_cta) {
     const int lo = a.q_start ? min(max(__ldg(a.q_start), 0), a.n_tokens) : 0;
     const int hi = a.q_start ? min(max(__ldg(a.q_start + a.n_seqs), lo), a.n_tokens) : a.n_tokens;
@@ -336,7 +334,7 @@ __device__ void finish_empty_rows(const PagedArgs& a, int cta, int n_cta) {
         const SeqRows s = seq_rows(a, b);
         const int nrt = row_tiles<M>(a, s);
         for (int rt = 0; rt < nrt; ++rt) {
-            if (unit_tiles<M>(a, s, rt) > 0) break;  // limits grow with the row: the later tiles have keys, too
+            if (unit_tiles<M, KT>(a, s, rt) > 0) break;  // limits grow with the row: the later tiles have keys, too
             const int rows = min(M, s.n * a.g - rt * M);
             for (int x = threadIdx.x; x < rows * a.Hkv; x += NT) {
                 const int h = x / rows, R = rt * M + x % rows, i = R / a.g;

@@ -24,6 +24,7 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bf
 
 // ---------------------------------------------------------------- CUDA cores
 // Four warps, each every fourth key; a lane holds D/32 columns of the row's key, value and output.
+constexpr int kSimpleKeys = 64;
 constexpr int kSimpleThreads = 128;
 constexpr int kSimpleRows = 8;
 
@@ -35,8 +36,8 @@ __global__ void __launch_bounds__(kSimpleThreads) paged_simple_kernel(const Page
     __shared__ float s_m[kWarps][M], s_l[kWarps][M];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
     if constexpr (!PREFIX) {
-        find_share<M, kSimpleThreads>(a, cta, a.ctas, &share);
-        finish_empty_rows<T, M, kSimpleThreads>(a, cta, a.ctas);
+        find_share<M, kSimpleKeys, kSimpleThreads>(a, cta, a.ctas, &share);
+        finish_empty_rows<T, M, kSimpleKeys, kSimpleThreads>(a, cta, a.ctas);
     }
     auto run = [&](const Seg& g) {
         float q[M][V], acc[M][V], m[M], l[M];
@@ -58,8 +59,8 @@ __global__ void __launch_bounds__(kSimpleThreads) paged_simple_kernel(const Page
             }
         }
         const int first = PREFIX ? 0 : a.key_begin;
-        const int k0 = max(g.tile0 * kKeyTile, first);
-        const int k1 = min((g.tile0 + g.n_tiles) * kKeyTile, seg_key_end<PREFIX>(a, g));
+        const int k0 = max(g.tile0 * kSimpleKeys, first);
+        const int k1 = min((g.tile0 + g.n_tiles) * kSimpleKeys, seg_key_end<PREFIX>(a, g));
         for (int j = k0 + warp; j < k1; j += kWarps) {
             const int page = seg_page<PREFIX>(a, g, j >> a.page_log2);
             if (page < 0) continue;
@@ -130,10 +131,10 @@ __global__ void __launch_bounds__(kSimpleThreads) paged_simple_kernel(const Page
     };
     Seg g;
     if constexpr (PREFIX) {
-        PrefixWalk<M> walk(a, cta);
+        PrefixWalk<M, kSimpleKeys> walk(a, cta);
         while (walk.next(g)) run(g);
     } else {
-        OwnWalk<M> walk(a, share);
+        OwnWalk<M, kSimpleKeys> walk(a, share);
         while (walk.next(g)) run(g);
     }
 }
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
     if (a.prefix_len > 0) {
         const int t = (int)(row / a.Hq), hq = (int)(row % a.Hq), h = hq / a.g;
         const int64_t R = (int64_t)t * a.g + (hq - h * a.g);
-        const int tiles = (a.prefix_len + kKeyTile - 1) / kKeyTile;
+        const int tiles = (a.prefix_len + a.p_keys - 1) / a.p_keys;
         const int nrt = (int)(((int64_t)a.n_tokens * a.g + a.p_rows - 1) / a.p_rows);
         p_total = (int64_t)a.Hkv * nrt * tiles;
         p_base = ((int64_t)h * nrt + R / a.p_rows) * tiles;
@@ -227,27 +228,32 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
-// Rows of a unit for `rows` rows per KV head.
-static int pick_rows(const PagedArgs& a, int64_t rows) {
-    if (a.elem == 4) return kSimpleRows;
-    return rows <= 16 ? 16 : 32;
+// The kernel for `rows` rows per KV head: rows of a unit, keys of a tile, CTAs that run at a time.
+struct Pick {
+    int rows, keys, ctas;
+};
+static Pick pick(const PagedArgs& a, int64_t rows) {
+    if (a.elem == 4) return {kSimpleRows, kSimpleKeys, kSms * 4};
+    if (rows <= 32) return {rows <= 16 ? 16 : 32, 64, kSms * 2};
+    return {rows <= 128 ? 128 : 256, 128, kSms};
 }
-
-static int resident_ctas(const PagedArgs& a) { return a.elem == 4 ? kSms * 4 : kSms * 2; }
 
 size_t paged_plan(PagedArgs* a, int max_q, void* ws) {
     const int64_t rows = (int64_t)a->n_tokens * a->Hq;
-    a->rows = pick_rows(*a, (int64_t)max_q * a->g);
-    a->ctas = resident_ctas(*a);
-    a->p_rows = a->p_ctas = 0;
+    const Pick own = pick(*a, (int64_t)max_q * a->g);
+    a->rows = own.rows;
+    a->ctas = own.ctas;
+    a->p_rows = a->p_ctas = a->p_keys = 0;
     if (a->prefix_len > 0) {
         const int64_t batch = (int64_t)a->n_tokens * a->g;
-        a->p_rows = pick_rows(*a, batch);
-        // no share longer than a unit, so that it touches two units at most: one slot each; and none empty
-        const int64_t units = (batch + a->p_rows - 1) / a->p_rows * a->Hkv;
-        const int64_t tiles = units * ((a->prefix_len + kKeyTile - 1) / kKeyTile);
-        const int64_t want = std::min<int64_t>(resident_ctas(*a), tiles);
-        a->p_ctas = (int)std::max(units, want);
+        const Pick pre = pick(*a, batch);
+        a->p_rows = pre.rows;
+        a->p_keys = pre.keys;
+        // no share longer than a unit, so that it touches two units at most: one slot each; none empty; whole waves
+        const int64_t units = (batch + pre.rows - 1) / pre.rows * a->Hkv;
+        const int64_t tiles = units * ((a->prefix_len + pre.keys - 1) / pre.keys);
+        const int64_t waves = (units + pre.ctas - 1) / pre.ctas;
+        a->p_ctas = (int)std::min(tiles, waves * pre.ctas);
     }
     size_t at = 0;
     char* w = static_cast<char*>(ws);
@@ -270,11 +276,13 @@ size_t paged_plan(PagedArgs* a, int max_q, void* ws) {
 }
 
 cudaError_t launch_paged_own(const PagedArgs& a, cudaStream_t stream) {
-    return a.elem == 4 ? simple<false>(a, stream) : launch_paged_mma(a, false, stream);
+    if (a.elem == 4) return simple<false>(a, stream);
+    return a.rows <= 32 ? launch_paged_mma(a, false, stream) : launch_paged_tc(a, false, stream);
 }
 
 cudaError_t launch_paged_prefix(const PagedArgs& a, cudaStream_t stream) {
-    return a.elem == 4 ? simple<true>(a, stream) : launch_paged_mma(a, true, stream);
+    if (a.elem == 4) return simple<true>(a, stream);
+    return a.p_rows <= 32 ? launch_paged_mma(a, true, stream) : launch_paged_tc(a, true, stream);
 }
 
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream) {

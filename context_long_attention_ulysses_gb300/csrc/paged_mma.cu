@@ -22,6 +22,7 @@ namespace usp {
 
 namespace {
 
+constexpr int kKeyTile = 64;  // keys per tile
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr float kLn2 = 0.6931471805599453f;
@@ -83,8 +84,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     if constexpr (PREFIX) {
         __syncthreads();
     } else {
-        find_share<M, kThreads>(a, cta, a.ctas, &share);  // holds the barrier that publishes the set-up, too
-        finish_empty_rows<__nv_bfloat16, M, kThreads>(a, cta, a.ctas);
+        find_share<M, kKeyTile, kThreads>(a, cta, a.ctas, &share);  // holds the barrier that publishes the set-up, too
+        finish_empty_rows<__nv_bfloat16, M, kKeyTile, kThreads>(a, cta, a.ctas);
         __syncthreads();
     }
     volatile int* abort_p = &abort_flag;
@@ -92,10 +93,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     auto walk_all = [&](auto&& piece) {
         Seg g;
         if constexpr (PREFIX) {
-            PrefixWalk<M> walk(a, cta);
+            PrefixWalk<M, kKeyTile> walk(a, cta);
             while (walk.next(g)) piece(g);
         } else {
-            OwnWalk<M> walk(a, share);
+            OwnWalk<M, kKeyTile> walk(a, share);
             while (walk.next(g)) piece(g);
         }
     };

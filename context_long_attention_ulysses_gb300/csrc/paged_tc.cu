@@ -1,0 +1,457 @@
+// Attention over a paged cache for many rows per KV head (bf16): chunks of prompts, and the prefix that a batch shares.
+//
+// 33 rows per KV head and more are a matrix product: with M rows a key costs 4 d M flops per 4 d bytes, and from about 260
+// rows on the tensor cores bound it (1735 TFLOP/s against 6.7 TB/s).  One CTA per SM owns a unit of 128 rows (one stream) or
+// 256 (two streams A and B that share every K/V tile); rows are (token, query head of the group) pairs, of one sequence or,
+// over a prefix, of the whole batch:
+//   warp 4 NS      TMA producer: K and V of each tile of 128 keys, page by page, into two rings
+//   warp 4 NS + 1  TMEM owner and single-thread tcgen05.mma issuer, per tile j: PV_A(j), QK_A(j+1), PV_B(j), QK_B(j+1)
+//   warps 0-3 (A), 4-7 (B)  Q rows into shared memory, softmax (thread = row = TMEM lane; log2 domain, O rescaled only when
+//                  the maximum grows by more than 2^8), normalisation, stores
+// With two streams the tensor core runs one stream's products while the other's softmax works.  A CTA walks its share
+// piece by piece (paged.cuh); the rings run on across pieces, so the next piece's keys arrive during the epilogue.
+// TMEM columns: S_A [0,128), S_B [128,256), O_A [256,256+D), O_B [384,384+D); P (bf16) lies over its own S.
+#include <cmath>
+
+#include <cuda_bf16.h>
+
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace usp {
+
+namespace {
+
+constexpr int kKeyTile = 128;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.0f;  // log2 units
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;  // of 168 at launch (NS = 2): 2 * 208 + 88 <= 3 * 168
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "register split exceeds the launch allocation");
+constexpr int kFlags = 8;  // ring of loaded-box masks; longer than the K ring by what the softmax may lag behind
+
+template <int D, int NS>
+struct Cfg {
+    static constexpr int M = 128 * NS;
+    static constexpr int kThreads = (4 * NS + 4) * 32;
+    static constexpr int kChunks = D / 64;
+    static constexpr int kTileBytes = kChunks * 128 * 128;  // 128 rows of bf16
+    static constexpr int kKStages = D == 64 ? 4 : 3;
+    static constexpr int kVStages = D == 64 ? 4 : (NS == 2 ? 2 : 3);
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = NS * kTileBytes;
+    static constexpr int kOffV = kOffK + kKStages * kTileBytes;
+    static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
+    static constexpr int kBars = 2 * kKStages + 2 * kVStages + 4 * NS + 1;
+    static constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
+};
+
+// Bits lo .. hi-1 of word w (32 bits each) of a mask.
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int w) {
+    lo = min(max(lo - 32 * w, 0), 32);
+    hi = min(max(hi - 32 * w, 0), 32);
+    if (lo >= hi) return 0u;
+    return (0xffffffffu >> (32 - (hi - lo))) << lo;
+}
+
+template <int D, int NS, bool PREFIX>
+__global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const PagedArgs a) {
+    using C = Cfg<D, NS>;
+    constexpr int M = C::M, KS = C::kKStages, VS = C::kVStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + C::kBars * 8);
+    __shared__ Share share;
+    __shared__ int abort_flag;
+    __shared__ uint32_t s_boxes[kFlags];  // boxes of a tile that were loaded
+    auto BAR = [&](int i) { return sbase + C::kOffBar + 8u * (uint32_t)i; };
+    const int kKFull = 0, kKEmpty = KS, kVFull = 2 * KS, kVEmpty = kVFull + VS;
+    const int kQFull = kVEmpty + VS, kSFull = kQFull + NS, kPReady = kSFull + NS, kOReady = kPReady + NS;  // per stream
+    const int kDrain = kOReady + NS;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+    constexpr int kProducer = 4 * NS, kIssuer = 4 * NS + 1;
+
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int s = 0; s < KS; ++s) { mbar_init(BAR(kKFull + s), 1); mbar_init(BAR(kKEmpty + s), 1); }
+        for (int s = 0; s < VS; ++s) { mbar_init(BAR(kVFull + s), 1); mbar_init(BAR(kVEmpty + s), 1); }
+        for (int st = 0; st < NS; ++st) {
+            mbar_init(BAR(kQFull + st), 128);
+            mbar_init(BAR(kSFull + st), 1);
+            mbar_init(BAR(kPReady + st), 128);
+            mbar_init(BAR(kOReady + st), 1);
+        }
+        mbar_init(BAR(kDrain), 1);
+        fence_mbar_init();
+    }
+    if (warp == kIssuer) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    if constexpr (!PREFIX) {
+        find_share<M, kKeyTile, C::kThreads>(a, cta, a.ctas, &share);
+        finish_empty_rows<__nv_bfloat16, M, kKeyTile, C::kThreads>(a, cta, a.ctas);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    volatile int* abort_p = &abort_flag;
+
+    // piece(g) returns false to stop (a wait gave up)
+    auto walk_all = [&](auto&& piece) {
+        Seg g;
+        if constexpr (PREFIX) {
+            PrefixWalk<M, kKeyTile> walk(a, cta);
+            while (walk.next(g))
+                if (!piece(g)) break;
+        } else {
+            OwnWalk<M, kKeyTile> walk(a, share);
+            while (walk.next(g))
+                if (!piece(g)) break;
+        }
+    };
+    // tiles of a piece that hold a key which some row of stream st sees
+    auto stream_tiles = [&](const Seg& g, int st) {
+        if (st * 128 >= g.n_rows) return 0;
+        if (PREFIX) return g.n_tiles;
+        const int last = min(g.n_rows, st * 128 + 128) - 1;
+        const int end = visible(a, SeqRows{g.t0, g.n, g.len}, (g.row0 + last) / a.g);
+        return min(max((end + kKeyTile - 1) / kKeyTile - g.tile0, 0), g.n_tiles);
+    };
+
+    if (warp >= 4 * NS) {
+        if constexpr (NS == 2) setmaxnreg_dec<kOtherRegs>();
+        if (warp == kProducer) {
+            // ---------------------------------------------------------------- TMA producer
+            const int psize = 1 << a.page_log2, box = min(psize, kKeyTile), nb = kKeyTile / box;
+            const int my_box = lane % nb, my_chunk = lane / nb;
+            int it = 0, nv = 0;
+            walk_all([&](const Seg& g) {
+                const int first = PREFIX ? 0 : a.key_begin, end = seg_key_end<PREFIX>(a, g);
+                auto page_of = [&](int tile) {  // of this lane's box, -1: not loaded
+                    const int j = tile * kKeyTile + my_box * box;
+                    return my_chunk < C::kChunks && j < end && j + box > first
+                               ? seg_page<PREFIX>(a, g, j >> a.page_log2) : -1;
+                };
+                int page = page_of(g.tile0);
+                for (int x = 0; x < g.n_tiles; ++x, ++it) {
+                    const int next = x + 1 < g.n_tiles ? page_of(g.tile0 + x + 1) : -1;  // on its way during the waits
+                    const uint32_t live = __ballot_sync(~0u, page >= 0);
+                    const uint32_t bytes = __popc(live) * box * 128;
+                    const int j = (g.tile0 + x) * kKeyTile + my_box * box;
+                    const uint32_t off = my_chunk * 16384 + my_box * box * 128;
+                    const int ks = it % KS, vs = it % VS;
+                    if (it >= KS &&
+                        !__all_sync(~0u, mbar_wait(BAR(kKEmpty + ks), (it / KS - 1) & 1, abort_p, 31, a.status)))
+                        return false;
+                    if (lane == 0) {
+                        s_boxes[it % kFlags] = live;
+                        mbar_arrive_expect_tx(BAR(kKFull + ks), bytes);
+                    }
+                    __syncwarp();
+                    if (page >= 0)
+                        tma_load_4d(sbase + C::kOffK + ks * C::kTileBytes + off, &tm_k, my_chunk * 64, g.h,
+                                    j & (psize - 1), page, BAR(kKFull + ks));
+                    if (it >= VS &&
+                        !__all_sync(~0u, mbar_wait(BAR(kVEmpty + vs), (it / VS - 1) & 1, abort_p, 32, a.status))) {
+                        ++it;  // this K tile was issued, its V tile was not
+                        return false;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(BAR(kVFull + vs), bytes);
+                    __syncwarp();
+                    if (page >= 0)
+                        tma_load_4d(sbase + C::kOffV + vs * C::kTileBytes + off, &tm_v, my_chunk * 64, g.h,
+                                    j & (psize - 1), page, BAR(kVFull + vs));
+                    nv = it + 1;
+                    page = next;
+                }
+                return true;
+            });
+            __syncwarp();
+            if (lane == 0) {  // every issued load lands before the CTA can exit
+                drain_ring(BAR(kKFull), KS, it, 33, a.status);
+                drain_ring(BAR(kVFull), VS, nv, 34, a.status);
+            }
+        } else if (warp == kIssuer && lane == 0) {
+            // ---------------------------------------------------------------- MMA issuer
+            constexpr uint32_t kIdS = idesc_bf16(128, kKeyTile, 0, 0);  // S = Q K^T, both K-major
+            constexpr uint32_t kIdO = idesc_bf16(128, D, 0, 1);         // O += P V, V MN-major
+            int base = 0, cnt[NS] = {}, pieces[NS] = {};  // tiles so far; tiles and pieces of each stream
+            auto issue_qk = [&](int st, int it) {
+                const uint64_t dq = sdesc_sw128(sbase + C::kOffQ + st * C::kTileBytes, 16, 1024);
+                const uint64_t dk = sdesc_sw128(sbase + C::kOffK + (it % KS) * C::kTileBytes, 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
+                    mma_ss(tmem + st * 128, dq + off, dk + off, kIdS, kk > 0);
+                }
+                mma_commit(BAR(kSFull + st));
+            };
+            walk_all([&](const Seg& g) {
+                int nt[NS];
+                for (int st = 0; st < NS; ++st) {
+                    nt[st] = stream_tiles(g, st);
+                    if (nt[st] == 0) continue;
+                    if (!mbar_wait(BAR(kQFull + st), pieces[st] & 1, abort_p, 35, a.status)) return false;
+                    ++pieces[st];
+                }
+                if (!mbar_wait(BAR(kKFull + base % KS), (base / KS) & 1, abort_p, 36, a.status)) return false;
+                tc_fence_after();
+                for (int st = 0; st < NS; ++st)
+                    if (nt[st] > 0) issue_qk(st, base);
+                mma_commit(BAR(kKEmpty + base % KS));
+                for (int j = 0; j < g.n_tiles; ++j) {
+                    const int it = base + j, vs = it % VS, k1 = (it + 1) % KS;
+                    if (!mbar_wait(BAR(kVFull + vs), (it / VS) & 1, abort_p, 37, a.status)) return false;
+                    const uint64_t dv = sdesc_sw128(sbase + C::kOffV + vs * C::kTileBytes, 16384, 1024);
+                    bool k_waited = false;
+                    for (int st = 0; st < NS; ++st) {
+                        if (j >= nt[st]) continue;
+                        if (!mbar_wait(BAR(kPReady + st), (cnt[st] + j) & 1, abort_p, 38, a.status)) return false;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < kKeyTile / 16; ++kk)
+                            mma_ts(tmem + 256 + st * 128, tmem + st * 128 + kk * 8, dv + (kk * 2048 >> 4), kIdO,
+                                   (j > 0 || kk > 0) ? 1u : 0u);
+                        if (j + 1 < nt[st]) {
+                            if (!k_waited) {
+                                if (!mbar_wait(BAR(kKFull + k1), ((it + 1) / KS) & 1, abort_p, 36, a.status))
+                                    return false;
+                                tc_fence_after();
+                                k_waited = true;
+                            }
+                            issue_qk(st, it + 1);  // in issue order after the product that read P from these columns
+                        } else {
+                            mma_commit(BAR(kOReady + st));
+                        }
+                    }
+                    mma_commit(BAR(kVEmpty + vs));
+                    if (k_waited) mma_commit(BAR(kKEmpty + k1));
+                }
+                base += g.n_tiles;
+                for (int st = 0; st < NS; ++st) cnt[st] += nt[st];
+                return true;
+            });
+            // every issued MMA completes before TMEM is freed (after an abort, too)
+            mma_commit(BAR(kDrain));
+            mbar_drain(BAR(kDrain), 0, 39, a.status);
+        }
+    } else {
+        if constexpr (NS == 2) setmaxnreg_inc<kSoftmaxRegs>();
+        // ---------------------------------------------------------------- softmax warps
+        const int st = warp >> 2;                    // stream
+        const int row = (warp & 3) * 32 + lane;      // row of the stream = TMEM lane
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t scol = lane_base + st * 128, ocol = lane_base + 256 + st * 128;
+        const int box_log2 = min(a.page_log2, 7);
+        const uint32_t all_boxes = (1u << (kKeyTile >> box_log2)) - 1u;
+        auto warp_wait = [&](uint32_t bar, uint32_t parity, int site) {  // one answer for the warp: TMEM access is collective
+            return __all_sync(~0u, mbar_wait(bar, parity, abort_p, site, a.status)) != 0;
+        };
+        int base = 0, cnt = 0, pieces = 0;
+        walk_all([&](const Seg& g) {
+            const int r = st * 128 + row;
+            const bool valid = r < g.n_rows;
+            const int n_tiles = stream_tiles(g, st);
+            const int first = PREFIX ? 0 : a.key_begin, end = seg_key_end<PREFIX>(a, g);
+            const int lim = valid ? row_limit<PREFIX>(a, g, r) : INT_MAX;
+            // (a warp without a valid row has its rows of V to clear, too)
+            const int lim_min = min(__reduce_min_sync(~0u, lim), end);
+            if (n_tiles > 0) {  // this row of Q, swizzled as a TMA load would place it; rows beyond the unit are zero
+                const int R = g.row0 + r, i = R / a.g;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    static_cast<const __nv_bfloat16*>(a.q) +
+                    ((int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g)) * D);
+                uint8_t* dst = smem + C::kOffQ + st * C::kTileBytes + row * 128;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 w = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(dst + (c / 8) * 16384 + (((c & 7) ^ (row & 7)) << 4)) = w;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(BAR(kQFull + st));
+            }
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int j = 0; j < n_tiles; ++j) {
+                if (!warp_wait(BAR(kSFull + st), (cnt + j) & 1, 40)) return false;
+                tc_fence_after();
+                uint32_t r0r[32], r1r[32], r2r[32], r3r[32];
+                tmem_ld32(scol, r0r);
+                tmem_ld32(scol + 32, r1r);
+                tmem_ld32(scol + 64, r2r);
+                tmem_ld32(scol + 96, r3r);
+                tmem_wait_ld();
+                float s[kKeyTile];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    s[c] = __uint_as_float(r0r[c]);
+                    s[32 + c] = __uint_as_float(r1r[c]);
+                    s[64 + c] = __uint_as_float(r2r[c]);
+                    s[96 + c] = __uint_as_float(r3r[c]);
+                }
+                const int key0 = (g.tile0 + j) * kKeyTile;
+                const uint32_t live = s_boxes[(base + j) % kFlags] & all_boxes;
+                if (key0 + kKeyTile > lim_min || key0 < first || live != all_boxes) {
+                    uint32_t boxes[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        boxes[w] = 0u;
+                        for (int b = 0; b < kKeyTile >> box_log2; ++b)
+                            if (live >> b & 1u) boxes[w] |= range_bits(b << box_log2, (b + 1) << box_log2, w);
+                    }
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t see = boxes[w] & range_bits(first - key0, min(lim, end) - key0, w);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!(see >> c & 1u)) s[32 * w + c] = -INFINITY;
+                    }
+                    // V rows that are no key of this piece may hold anything, NaN too, and 0 * NaN must not reach O:
+                    // thread = row of the V tile (both streams write the same zeros)
+                    const int vs = (base + j) % VS;
+                    if (!warp_wait(BAR(kVFull + vs), ((base + j) / VS) & 1, 41)) return false;
+                    const bool real = key0 + row >= first && key0 + row < end && (live >> (row >> box_log2) & 1u);
+                    if (!real) {
+                        uint8_t* v = smem + C::kOffV + vs * C::kTileBytes + row * 128;
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c)
+                            *reinterpret_cast<uint4*>(v + (c / 8) * 16384 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                // row max as eight independent chains of three-input maxima
+                float m8[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) m8[c] = s[c];
+#pragma unroll
+                for (int c = 8; c < kKeyTile; c += 2) m8[(c / 2) & 7] = max3f(m8[(c / 2) & 7], s[c], s[c + 1]);
+                float mx = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+                mx *= a.scale_log2;
+                const bool up = mx > m_run + kRescale;
+                const float alpha = up ? ex2_approx(m_run - mx) : 1.f;
+                if (up) m_run = mx;
+                const float msub = m_run == -INFINITY ? 0.f : m_run;
+                const float2 c2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(-msub, -msub);
+                float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float2 x = fma2(make_float2(s[h * 32 + 2 * c], s[h * 32 + 2 * c + 1]), c2, nm2);
+                        const float2 pv = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                        sum2[c & 1] = add2(sum2[c & 1], pv);
+                        pk[c] = pack_bf16(pv.x, pv.y);
+                    }
+                    tmem_st16(scol + h * 16, pk);  // P over S: this row's S is in registers
+                }
+                l_run = l_run * alpha + ((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y));
+                if (j > 0 && __any_sync(~0u, up)) {
+                    // the products of earlier tiles completed before S_j was signalled: scale O in place
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(ocol + c * 32, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st32(ocol + c * 32, o);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(BAR(kPReady + st));
+            }
+            // ---------------------------------------------------------------- the piece's result
+            if (n_tiles > 0) {
+                if (!warp_wait(BAR(kOReady + st), pieces & 1, 42)) return false;
+                ++pieces;
+                tc_fence_after();
+            }
+            const bool has = n_tiles > 0 && l_run > 0.f;
+            const float inv = has ? 1.f / l_run : 0.f;
+            const float lse2 = has ? m_run + log2f(l_run) : -INFINITY;
+            const RowDst dst = row_dst<M, PREFIX>(a, g, valid ? r : 0, cta);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (n_tiles > 0) {
+                    tmem_ld32(ocol + c * 32, o);
+                    tmem_wait_ld();
+                }
+                if (!has) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                }
+                if (valid && dst.out) {
+                    uint4* y = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dst.out) + c * 32);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint4 v;
+                        v.x = pack_bf16(__uint_as_float(o[8 * e + 0]) * inv, __uint_as_float(o[8 * e + 1]) * inv);
+                        v.y = pack_bf16(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv);
+                        v.z = pack_bf16(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv);
+                        v.w = pack_bf16(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv);
+                        y[e] = v;
+                    }
+                } else if (valid) {
+                    float4* y = reinterpret_cast<float4*>(dst.part + c * 32);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                           __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+                }
+            }
+            tc_fence_before();  // O is read: the next piece's first product may overwrite it once P is ready
+            if (valid) {
+                *dst.lse = dst.out ? lse2 * kLn2 : lse2;
+                if (!PREFIX && g.ends) note_row<M>(a, g, r, cta);
+            }
+            base += g.n_tiles;
+            cnt += n_tiles;
+            return true;
+        });
+    }
+    // ---------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kIssuer) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, int NS, bool PREFIX>
+cudaError_t launch_t(const PagedArgs& a, cudaStream_t s) {
+    using C = Cfg<D, NS>;
+    const int psize = 1 << a.page_log2, box = psize < kKeyTile ? psize : kKeyTile;
+    const int64_t page = (int64_t)psize * D;
+    CUtensorMap tk, tv;
+    const Tensor4 k{const_cast<void*>(a.k_pages), page, D, page * a.Hkv, a.Hkv, psize, a.n_pages};
+    Tensor4 v = k;
+    v.ptr = const_cast<void*>(a.v_pages);
+    if (!make_tmap_bf16(&tk, k, D, box) || !make_tmap_bf16(&tv, v, D, box)) return cudaErrorInvalidValue;
+    auto kern = paged_tc_kernel<D, NS, PREFIX>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    kern<<<PREFIX ? a.p_ctas : a.ctas, C::kThreads, C::kSmem, s>>>(tk, tv, a);
+    return cudaGetLastError();
+}
+
+template <int D, bool PREFIX>
+cudaError_t launch_d(const PagedArgs& a, cudaStream_t s) {
+    return (PREFIX ? a.p_rows : a.rows) == 128 ? launch_t<D, 1, PREFIX>(a, s) : launch_t<D, 2, PREFIX>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tc(const PagedArgs& a, bool prefix, cudaStream_t s) {
+    if (a.d == 64) return prefix ? launch_d<64, true>(a, s) : launch_d<64, false>(a, s);
+    return prefix ? launch_d<128, true>(a, s) : launch_d<128, false>(a, s);
+}
+
+}  // namespace usp
