@@ -4,11 +4,14 @@
 // A unit is (sequence, KV head, tile of M consecutive rows), a row being one
 // (token, query head of the group): K and V of the head are read once for all
 // M rows.  A unit's keys are cut into tiles of KT.  All tiles of all
-// units, in the order sequence, head, row tile, key tile, form one line of W
-// tiles; CTA c of G takes the tiles [c*W/G, (c+1)*W/G).  So every CTA has the
-// same work whatever the lengths are, one sequence of 128K tokens spreads over
-// all SMs, and the lengths are read on the device (a captured graph replays
-// with new ones).  A unit that lies in one share is finished by its CTA; the
+// units, in the order sequence, head, row tile, key tile, form one line, in
+// which a unit takes PC places before its first tile: beginning and ending a
+// unit costs about as much as that many tiles (without them, 16 sequences of
+// one tile each fell to one CTA and decided the time of the whole launch).  Of
+// the W places CTA c of G takes [c*W/G, (c+1)*W/G).  So every CTA has the same
+// work whatever the lengths are, one sequence of 128K tokens spreads over all
+// SMs, and the lengths are read on the device (a captured graph replays with
+// new ones).  A unit that lies in one share is finished by its CTA; the
 // rows of a unit cut by a border leave partial results (normalised output and
 // log-sum-exp) in the workspace, which paged_merge_kernel joins in the order
 // of the keys.  A share holds at most two cut units: its first (slot 0, begun
@@ -24,6 +27,37 @@
 #include "kernels.h"
 
 namespace usp {
+
+// The kernels of a call follow each other by programmatic dependent launch: a kernel lets its successor's CTAs start as
+// soon as its own have all begun (the successor's set-up then overlaps with it), and the successor waits for its
+// predecessor's end, and everything it wrote, before it reads or overwrites any of that.
+__device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+                             const A&... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Own keys: behind the prefix kernel this one may begin while that one ends (neither reads what the other writes).
+template <typename... P, typename... A>
+cudaError_t launch_own(void (*kernel)(P...), const PagedArgs& a, unsigned threads, size_t smem, cudaStream_t stream,
+                       const A&... args) {
+    if (a.prefix_len > 0) return launch_dependent(kernel, a.ctas, threads, smem, stream, args...);
+    kernel<<<a.ctas, threads, smem, stream>>>(args...);
+    return cudaGetLastError();
+}
 
 // What paged_merge_kernel does with a row: word x = kind | row in the tile << 2, y = first CTA | last CTA << 16.
 enum RowKind : uint32_t {
@@ -69,33 +103,39 @@ __device__ __forceinline__ int row_tiles(const PagedArgs& a, const SeqRows& s) {
     return (s.n * a.g + M - 1) / M;
 }
 
-// Key tiles of all row tiles of one head of a sequence.
-template <int M, int KT>
-__device__ __forceinline__ int64_t head_tiles(const PagedArgs& a, int b) {
+// Places of a unit of ut tiles on the line.
+template <int PC>
+__device__ __forceinline__ int unit_places(int ut) {
+    return ut > 0 ? ut + PC : 0;
+}
+
+// Places of all row tiles of one head of a sequence.
+template <int M, int KT, int PC>
+__device__ __forceinline__ int64_t head_places(const PagedArgs& a, int b) {
     const SeqRows s = seq_rows(a, b);
     const int nrt = row_tiles<M>(a, s);
     if (nrt == 0) return 0;
-    if (!a.causal || s.n == 1) return (int64_t)nrt * unit_tiles<M, KT>(a, s, 0);
+    if (!a.causal || s.n == 1) return (int64_t)nrt * unit_places<PC>(unit_tiles<M, KT>(a, s, 0));
     int64_t sum = 0;
-    for (int rt = 0; rt < nrt; ++rt) sum += unit_tiles<M, KT>(a, s, rt);
+    for (int rt = 0; rt < nrt; ++rt) sum += unit_places<PC>(unit_tiles<M, KT>(a, s, rt));
     return sum;
 }
 
-// A CTA's share of the line: [pos, end), beginning `off` tiles into sequence b; W (total) tiles over n_cta CTAs, no
-// share empty (so that every CTA between a unit's first and last holds a part of it).
+// A CTA's share of the line: [pos, end), beginning `off` places into sequence b; W (total) places over n_cta CTAs, no
+// share empty (so that every CTA between those of a unit's first and last tile holds a part of it).
 struct Share {
     int64_t pos, end, off, total;
     int b, n_cta;
 };
 
 // Computed by all threads of the CTA (a scan over the sequences; NT threads), result in *out (shared memory).
-template <int M, int KT, int NT>
+template <int M, int KT, int PC, int NT>
 __device__ void find_share(const PagedArgs& a, int cta, int n_cta, Share* out) {
     constexpr int kWarps = NT / 32;
     __shared__ int64_t part[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t mine = 0;
-    for (int b = threadIdx.x; b < a.n_seqs; b += NT) mine += head_tiles<M, KT>(a, b);
+    for (int b = threadIdx.x; b < a.n_seqs; b += NT) mine += head_places<M, KT, PC>(a, b);
     for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
     if (lane == 0) part[warp] = mine;
     if (threadIdx.x == 0) *out = Share{0, 0, 0, 0, a.n_seqs, 1};
@@ -107,10 +147,10 @@ __device__ void find_share(const PagedArgs& a, int cta, int n_cta, Share* out) {
     if (cta >= n_cta) return;
     const int64_t pos = total * cta / n_cta, end = total * (cta + 1) / n_cta;
     int64_t base = 0;
-    for (int b0 = 0; b0 < a.n_seqs; b0 += NT) {  // chunk by chunk: inclusive scan of the sequences' tiles
+    for (int b0 = 0; b0 < a.n_seqs; b0 += NT) {  // chunk by chunk: inclusive scan of the sequences' places
         __syncthreads();
         const int b = b0 + threadIdx.x;
-        const int64_t cost = b < a.n_seqs ? head_tiles<M, KT>(a, b) * a.Hkv : 0;
+        const int64_t cost = b < a.n_seqs ? head_places<M, KT, PC>(a, b) * a.Hkv : 0;
         int64_t inc = cost;
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t up = __shfl_up_sync(~0u, inc, o);
@@ -128,7 +168,7 @@ __device__ void find_share(const PagedArgs& a, int cta, int n_cta, Share* out) {
     __syncthreads();
 }
 
-// The CTA that owns tile x of W, shares as above.
+// The CTA that owns place x of W, shares as above.
 __device__ __forceinline__ int share_owner(int64_t x, int64_t total, int n_cta) {
     return (int)(((x + 1) * n_cta - 1) / total);
 }
@@ -141,14 +181,14 @@ struct Seg {
     int tile0, n_tiles;    // tile numbers from key 0
     bool begins, ends;     // the piece holds the unit's first / last tile
     int ordinal;           // pieces of this CTA before it
-    int first_cta, last_cta;
+    int first_cta;         // of a cut unit, known where it ends
 };
 
 // Walks a CTA's share piece by piece (own keys).  Uniform over the threads that call it.
-template <int M, int KT>
+template <int M, int KT, int PC>
 struct OwnWalk {
     const PagedArgs& a;
-    int64_t pos, end, base;  // base: line position of the unit's first tile
+    int64_t pos, end, base;  // base: the place of the unit's first tile
     int64_t total;
     int n_cta;
     SeqRows s;
@@ -159,35 +199,40 @@ struct OwnWalk {
         if (pos >= end) return;
         s = seq_rows(a, b);
         nrt = row_tiles<M>(a, s);
-        const int64_t per_head = head_tiles<M, KT>(a, b);
+        const int64_t per_head = head_places<M, KT, PC>(a, b);
         h = (int)(sh.off / per_head);
         int64_t off = sh.off - h * per_head;
         rt = 0;
         ut = unit_tiles<M, KT>(a, s, 0);
-        while (off >= ut) {
-            off -= ut;
+        while (off >= unit_places<PC>(ut)) {
+            off -= unit_places<PC>(ut);
             ++rt;
             ut = unit_tiles<M, KT>(a, s, rt);
         }
-        base = pos - off;
+        base = pos - off + PC;
     }
 
     __device__ bool next(Seg& g) {
-        if (pos >= end) return false;
-        while (ut == 0 || pos >= base + ut) {  // on to the next unit that has keys
-            base += ut;
-            if (++rt >= nrt) {
-                rt = 0;
-                if (++h >= a.Hkv) {
-                    h = 0;
-                    do {
-                        if (++b >= a.n_seqs) return false;
-                        s = seq_rows(a, b);
-                        nrt = row_tiles<M>(a, s);
-                    } while (nrt == 0);
+        for (;;) {
+            pos = max(pos, base);  // past the unit's places without a tile
+            if (pos >= end) return false;
+            if (ut > 0 && pos < base + ut) break;
+            base += ut;  // on to the next unit that has keys
+            do {
+                if (++rt >= nrt) {
+                    rt = 0;
+                    if (++h >= a.Hkv) {
+                        h = 0;
+                        do {
+                            if (++b >= a.n_seqs) return false;
+                            s = seq_rows(a, b);
+                            nrt = row_tiles<M>(a, s);
+                        } while (nrt == 0);
+                    }
                 }
-            }
-            ut = unit_tiles<M, KT>(a, s, rt);
+                ut = unit_tiles<M, KT>(a, s, rt);
+            } while (ut == 0);
+            base += PC;
         }
         const int64_t to = min(end, base + ut);
         g.b = b;
@@ -202,8 +247,7 @@ struct OwnWalk {
         g.begins = pos == base;
         g.ends = to == base + ut;
         g.ordinal = ordinal++;
-        g.first_cta = g.begins ? -1 : share_owner(base, total, n_cta);  // -1: this CTA
-        g.last_cta = g.ends ? -1 : share_owner(base + ut - 1, total, n_cta);
+        g.first_cta = g.begins || !g.ends ? -1 : share_owner(base, total, n_cta);  // noted where the unit ends
         pos = to;
         return true;
     }
@@ -244,6 +288,10 @@ struct PrefixWalk {
         return true;
     }
 };
+
+// The producer warp walks the share and hands each piece to the other warps through a ring of kSegs entries, so that the
+// walk's divisions and registers are paid once; a piece without tiles ends it.
+constexpr int kSegs = 4;
 
 // Keys that row r of a piece sees: below this limit (0 for a row of no sequence).
 template <bool PREFIX>

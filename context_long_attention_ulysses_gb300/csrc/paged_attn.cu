@@ -25,6 +25,7 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bf
 // ---------------------------------------------------------------- CUDA cores
 // Four warps, each every fourth key; a lane holds D/32 columns of the row's key, value and output.
 constexpr int kSimpleKeys = 64;
+constexpr int kSimplePiece = 1;
 constexpr int kSimpleThreads = 128;
 constexpr int kSimpleRows = 8;
 
@@ -35,8 +36,9 @@ __global__ void __launch_bounds__(kSimpleThreads) paged_simple_kernel(const Page
     __shared__ float s_acc[kWarps][M][D];
     __shared__ float s_m[kWarps][M], s_l[kWarps][M];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
+    let_dependents_start();
     if constexpr (!PREFIX) {
-        find_share<M, kSimpleKeys, kSimpleThreads>(a, cta, a.ctas, &share);
+        find_share<M, kSimpleKeys, kSimplePiece, kSimpleThreads>(a, cta, a.ctas, &share);
         finish_empty_rows<T, M, kSimpleKeys, kSimpleThreads>(a, cta, a.ctas);
     }
     auto run = [&](const Seg& g) {
@@ -134,75 +136,106 @@ __global__ void __launch_bounds__(kSimpleThreads) paged_simple_kernel(const Page
         PrefixWalk<M, kSimpleKeys> walk(a, cta);
         while (walk.next(g)) run(g);
     } else {
-        OwnWalk<M, kSimpleKeys> walk(a, share);
+        OwnWalk<M, kSimpleKeys, kSimplePiece> walk(a, share);
         while (walk.next(g)) run(g);
+        grid_dependency_wait();  // ends after the prefix kernel, so that the merge after this one sees both
     }
 }
 
 // ---------------------------------------------------------------- joining partial results
-// One warp per row: o = sum_c 2^(lse_c - lse) o_c over the row's partial results, prefix first, keys in order.
-template <typename T, int D>
+// WPR warps per row: o = sum_c 2^(lse_c - lse) o_c over the row's partial results, the prefix's first, keys in order.
+// Bound by latency: the log-sum-exps are read by all lanes at once, the outputs kAhead at a time (one after the other they
+// took 15 us for the 38 parts of a row, which is what few rows have; so those have more warps, too).
+template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
-    constexpr int V = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.n_tokens * a.Hq) return;
-    const uint2 info = a.row_info[row];
-    const uint32_t kind = info.x & 3u;
-    if (kind == kRowDone) return;
-    // the row's own parts: n_own of them, part c at own_o + c * step
-    const float *oo = nullptr, *ol = nullptr;
-    int n_own = 0;
-    int64_t o0 = 0, step = 0;
-    if (kind == kRowWhole) {
-        oo = a.own_o + row * D;
-        ol = a.own_lse + row;
-        n_own = 1;
-    } else if (kind == kRowSplit) {
-        const int c0 = info.y & 0xffffu, c1 = info.y >> 16, r = info.x >> 2;
-        n_own = c1 - c0 + 1;
-        o0 = ((int64_t)c0 * 2 + 1) * a.rows + r;  // slot 1 of c0, then slot 0 of the CTAs after it
-        step = 2 * a.rows;
-        oo = a.slot_o;
-        ol = a.slot_l;
-    }
-    auto own_at = [&](int c) { return kind == kRowWhole ? (int64_t)0 : c == 0 ? o0 : o0 - a.rows + c * step; };
-    int n_pre = 0, pc0 = 0;
-    int64_t p_total = 0, p_base = 0;
-    int p_r = 0;
-    if (a.prefix_len > 0) {
+    constexpr int V = D / 32, kRows = 8 / WPR, kAhead = 4;
+    __shared__ float s_sum[8], s_acc[WPR > 1 ? 8 : 1][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % WPR;
+    const int64_t row = (int64_t)blockIdx.x * kRows + warp / WPR;
+    const bool in = row < (int64_t)a.n_tokens * a.Hq;
+    // the prefix's parts: one per CTA from pc0 on, each the first piece (slot 0) of its CTA, but for the unit's first part
+    // where that CTA's share begins in the unit before
+    int n_pre = 0;
+    int64_t p0 = 0, p1 = 0;
+    if (in && a.prefix_len > 0) {
         const int t = (int)(row / a.Hq), hq = (int)(row % a.Hq), h = hq / a.g;
         const int64_t R = (int64_t)t * a.g + (hq - h * a.g);
         const int tiles = (a.prefix_len + a.p_keys - 1) / a.p_keys;
         const int nrt = (int)(((int64_t)a.n_tokens * a.g + a.p_rows - 1) / a.p_rows);
-        p_total = (int64_t)a.Hkv * nrt * tiles;
-        p_base = ((int64_t)h * nrt + R / a.p_rows) * tiles;
-        p_r = (int)(R % a.p_rows);
-        pc0 = share_owner(p_base, p_total, a.p_ctas);
-        n_pre = share_owner(p_base + tiles - 1, p_total, a.p_ctas) - pc0 + 1;
+        const int64_t total = (int64_t)a.Hkv * nrt * tiles, base = ((int64_t)h * nrt + R / a.p_rows) * tiles;
+        const int r = (int)(R % a.p_rows), c0 = share_owner(base, total, a.p_ctas);
+        n_pre = share_owner(base + tiles - 1, total, a.p_ctas) - c0 + 1;
+        p0 = ((int64_t)c0 * 2 + (total * c0 / a.p_ctas < base ? 1 : 0)) * a.p_rows + r;
+        p1 = ((int64_t)c0 * 2) * a.p_rows + r;
     }
-    // a CTA's pieces are numbered: the unit's piece is number 1 where the CTA's share begins before the unit
-    auto pre_at = [&](int c) {
-        const int cta = pc0 + c;
-        const int slot = p_total * cta / a.p_ctas < p_base ? 1 : 0;
-        return ((int64_t)cta * 2 + slot) * a.p_rows + p_r;
+    grid_dependency_wait();  // all above needs nothing that a kernel before this one writes
+    const uint2 info = in ? a.row_info[row] : make_uint2(kRowDone, 0);
+    const uint32_t kind = info.x & 3u;
+    if (WPR == 1 && kind == kRowDone) return;
+    if (kind == kRowDone) n_pre = 0;
+    const float *oo = a.slot_o, *ol = a.slot_l;
+    int n_own = 0;
+    int64_t o0 = 0, o1 = 0;  // slot 1 of the unit's first CTA, then slot 0 of those after it
+    if (kind == kRowWhole) {
+        oo = a.own_o;
+        ol = a.own_lse;
+        n_own = 1;
+        o0 = row;
+    } else if (kind == kRowSplit) {
+        const int c0 = info.y & 0xffffu, c1 = info.y >> 16, r = info.x >> 2;
+        n_own = c1 - c0 + 1;
+        o0 = ((int64_t)c0 * 2 + 1) * a.rows + r;
+        o1 = ((int64_t)c0 * 2) * a.rows + r;
+    }
+    const int n = n_pre + n_own;
+    auto lse_of = [&](int c) -> float {
+        if (c < n_pre) return a.pslot_l[c ? p1 + (int64_t)c * 2 * a.p_rows : p0];
+        c -= n_pre;
+        return ol[c ? o1 + (int64_t)c * 2 * a.rows : o0];
+    };
+    auto out_of = [&](int c) -> const float* {
+        if (c < n_pre) return a.pslot_o + (c ? p1 + (int64_t)c * 2 * a.p_rows : p0) * D;
+        c -= n_pre;
+        return oo + (c ? o1 + (int64_t)c * 2 * a.rows : o0) * D;
     };
     float mx = -INFINITY;
-    for (int c = lane; c < n_pre; c += 32) mx = fmaxf(mx, a.pslot_l[pre_at(c)]);
-    for (int c = lane; c < n_own; c += 32) mx = fmaxf(mx, ol[own_at(c)]);
+    for (int c = lane; c < n; c += 32) mx = fmaxf(mx, lse_of(c));
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
     const float ms = mx == -INFINITY ? 0.f : mx;
     float acc[V], sum = 0.f;
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    auto add = [&](const float* o, float l) {
-        const float w = exp2f(l - ms);
-        sum += w;
+    for (int c0 = w; c0 < n; c0 += WPR * kAhead) {
+        float x[kAhead][V], f[kAhead];
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(w, o[lane * V + e], acc[e]);
-    };
-    for (int c = 0; c < n_pre; ++c) add(a.pslot_o + pre_at(c) * D, a.pslot_l[pre_at(c)]);
-    for (int c = 0; c < n_own; ++c) add(oo + own_at(c) * D, ol[own_at(c)]);
+        for (int u = 0; u < kAhead; ++u) {
+            const int c = c0 + u * WPR;
+            f[u] = c < n ? lse_of(c) : -INFINITY;
+            const float* src = out_of(c < n ? c : c0) + lane * V;
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[u][e] = src[e];
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const float g = exp2f(f[u] - ms);
+            sum += g;
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] = fmaf(g, x[u][e], acc[e]);
+        }
+    }
+    if constexpr (WPR > 1) {
+        if (lane == 0) s_sum[warp] = sum;
+#pragma unroll
+        for (int e = 0; e < V; ++e) s_acc[warp][lane * V + e] = acc[e];
+        __syncthreads();
+        if (w != 0 || kind == kRowDone) return;
+#pragma unroll
+        for (int x = 1; x < WPR; ++x) {
+            sum += s_sum[warp + x];
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] += s_acc[warp + x][lane * V + e];
+        }
+    }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     T* out = static_cast<T*>(a.o) + row * D + lane * V;
 #pragma unroll
@@ -215,7 +248,7 @@ cudaError_t simple_t(const PagedArgs& a, bool prefix, cudaStream_t s) {
     if (prefix)
         paged_simple_kernel<T, D, true><<<a.p_ctas, kSimpleThreads, 0, s>>>(a);
     else
-        paged_simple_kernel<T, D, false><<<a.ctas, kSimpleThreads, 0, s>>>(a);
+        return launch_own(paged_simple_kernel<T, D, false>, a, kSimpleThreads, 0, s, a);
     return cudaGetLastError();
 }
 
@@ -285,17 +318,17 @@ cudaError_t launch_paged_prefix(const PagedArgs& a, cudaStream_t stream) {
     return a.p_rows <= 32 ? launch_paged_mma(a, true, stream) : launch_paged_tc(a, true, stream);
 }
 
-cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream) {
+template <typename T, int D>
+static cudaError_t merge_t(const PagedArgs& a, cudaStream_t stream) {
+    // few rows have many parts each (a batch of any size is cut into as many shares as there are CTAs)
     const int64_t rows = (int64_t)a.n_tokens * a.Hq;
-    const unsigned blocks = (unsigned)((rows + 7) / 8);
-    if (a.elem == 4) {
-        if (a.d == 64) paged_merge_kernel<float, 64><<<blocks, 256, 0, stream>>>(a);
-        else paged_merge_kernel<float, 128><<<blocks, 256, 0, stream>>>(a);
-    } else {
-        if (a.d == 64) paged_merge_kernel<__nv_bfloat16, 64><<<blocks, 256, 0, stream>>>(a);
-        else paged_merge_kernel<__nv_bfloat16, 128><<<blocks, 256, 0, stream>>>(a);
-    }
-    return cudaGetLastError();
+    if (rows <= 8 * kSms) return launch_dependent(paged_merge_kernel<T, D, 8>, (unsigned)rows, 256, 0, stream, a);
+    return launch_dependent(paged_merge_kernel<T, D, 1>, (unsigned)((rows + 7) / 8), 256, 0, stream, a);
+}
+
+cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream) {
+    if (a.elem == 4) return a.d == 64 ? merge_t<float, 64>(a, stream) : merge_t<float, 128>(a, stream);
+    return a.d == 64 ? merge_t<__nv_bfloat16, 64>(a, stream) : merge_t<__nv_bfloat16, 128>(a, stream);
 }
 
 }  // namespace usp

@@ -23,6 +23,8 @@ namespace usp {
 namespace {
 
 constexpr int kKeyTile = 64;  // keys per tile
+// A piece's beginning and end (rows of Q, the join, the stores) cost about 3 to 4 us, a tile 1.5 us at the memory's rate.
+constexpr int kPieceCost = 2;
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr float kLn2 = 0.6931471805599453f;
@@ -41,7 +43,7 @@ struct Cfg {
     static constexpr int kOffJoin = kStages * 2 * kTileBytes;
     static constexpr int kOffStat = kOffJoin + kJoinBytes;    // m, sum, sum of rounded: 3 x [4][M]
     static constexpr int kOffBar = kOffStat + 3 * kConsumers * M * 4;
-    static constexpr int kSmem = kOffBar + 2 * kStages * 8 + 1024;
+    static constexpr int kSmem = kOffBar + 2 * (kStages + kSegs) * 8 + 1024;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -58,6 +60,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void bar_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory"); }
+// The same barrier, and whether all of them say yes.
+__device__ __forceinline__ bool bar_all_consumers(bool yes) {
+    uint32_t all;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all) : "r"((uint32_t)yes), "n"(32 * kConsumers) : "memory");
+    return all != 0;
+}
 
 template <int D, int MT, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -71,43 +80,51 @@ __global__ void __launch_bounds__(kThreads, 2)
     __shared__ Share share;
     __shared__ int abort_flag;
     __shared__ uint32_t s_boxes[C::kStages];  // boxes of the stage that were loaded
+    __shared__ Seg s_seg[kSegs];
     const uint32_t full0 = sbase + C::kOffBar, empty0 = full0 + 8 * C::kStages;
+    const uint32_t seg_full0 = empty0 + 8 * C::kStages, seg_empty0 = seg_full0 + 8 * kSegs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+    let_dependents_start();
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, kConsumers);
         }
+        for (int s = 0; s < kSegs; ++s) {
+            mbar_init(seg_full0 + 8 * s, 1);
+            mbar_init(seg_empty0 + 8 * s, kConsumers);
+        }
         fence_mbar_init();
     }
     if constexpr (PREFIX) {
         __syncthreads();
     } else {
-        find_share<M, kKeyTile, kThreads>(a, cta, a.ctas, &share);  // holds the barrier that publishes the set-up, too
+        find_share<M, kKeyTile, kPieceCost, kThreads>(a, cta, a.ctas, &share);  // holds the barrier that publishes the set-up, too
         finish_empty_rows<__nv_bfloat16, M, kKeyTile, kThreads>(a, cta, a.ctas);
         __syncthreads();
     }
     volatile int* abort_p = &abort_flag;
 
-    auto walk_all = [&](auto&& piece) {
-        Seg g;
-        if constexpr (PREFIX) {
-            PrefixWalk<M, kKeyTile> walk(a, cta);
-            while (walk.next(g)) piece(g);
-        } else {
-            OwnWalk<M, kKeyTile> walk(a, share);
-            while (walk.next(g)) piece(g);
-        }
-    };
-
     if (warp == kConsumers) {
         // ---------------------------------------------------------------- producer
         const int psize = 1 << a.page_log2, box = min(psize, kKeyTile), nb = kKeyTile / box;
         const int my_box = lane % nb, my_chunk = lane / nb % C::kChunks, my_kv = lane / nb / C::kChunks;
-        int it = 0;
+        int it = 0, n_seg = 0;
         bool ok = true;
-        walk_all([&](const Seg& g) {
+        auto publish = [&](const Seg& g) {
+            const int i = n_seg % kSegs;
+            if (n_seg >= kSegs)
+                ok = __all_sync(~0u, mbar_wait(seg_empty0 + 8 * i, (n_seg / kSegs - 1) & 1, abort_p, 24, a.status));
+            if (ok && lane == 0) {
+                s_seg[i] = g;
+                mbar_arrive(seg_full0 + 8 * i);
+            }
+            ++n_seg;
+            __syncwarp();
+        };
+        auto piece = [&](const Seg& g) {
+            publish(g);
             const int first = PREFIX ? 0 : a.key_begin, end = seg_key_end<PREFIX>(a, g);
             auto page_of = [&](int tile) {  // of this lane's box, -1: not loaded
                 const int j = tile * kKeyTile + my_box * box;
@@ -136,7 +153,18 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 page = next;
             }
-        });
+            return ok;
+        };
+        Seg g;
+        if constexpr (PREFIX) {
+            PrefixWalk<M, kKeyTile> walk(a, cta);
+            while (walk.next(g) && piece(g)) {}
+        } else {
+            OwnWalk<M, kKeyTile, kPieceCost> walk(a, share);
+            while (walk.next(g) && piece(g)) {}
+        }
+        g.n_tiles = 0;
+        if (ok) publish(g);
         if (lane == 0) drain_ring(full0, C::kStages, it, 22, a.status);  // every load has landed before the CTA exits
     } else {
         // ---------------------------------------------------------------- consumers
@@ -151,7 +179,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int v_key = warp * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), v_c = lane >> 4;
         int it = 0;
         bool ok = true;
-        walk_all([&](const Seg& g) {
+        for (int n_seg = 0;; ++n_seg) {
+            const int si = n_seg % kSegs;
+            ok = ok && mbar_wait(seg_full0 + 8 * si, (n_seg / kSegs) & 1, abort_p, 25, a.status);
+            // (one answer for the four warps, which meet at barriers below; a wait that gives up within a piece lets its
+            // warp run on to the next one without waiting)
+            if (!bar_all_consumers(ok)) break;
+            const Seg& g = s_seg[si];
+            if (g.n_tiles == 0) break;
             const int first = PREFIX ? 0 : a.key_begin, end = seg_key_end<PREFIX>(a, g);
             // ---- rows: Q, limits
             uint32_t q[MT == 1 ? D / 16 : 1][4];
@@ -202,11 +237,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                 l[t][0] = l[t][1] = lr[t][0] = lr[t][1] = 0.f;
             }
             // ---- keys
-            for (int x = 0; x < g.n_tiles; ++x, ++it) {
+            const int tile0 = g.tile0, n_tiles = g.n_tiles;
+            for (int x = 0; x < n_tiles; ++x, ++it) {
                 const int st = it % C::kStages;
                 ok = ok && mbar_wait(full0 + 8 * st, (it / C::kStages) & 1, abort_p, 23, a.status);
                 ok = __all_sync(~0u, ok);
-                const int key0 = (g.tile0 + x) * kKeyTile + warp * 16;  // this warp's keys key0 .. key0 + 15
+                const int key0 = (tile0 + x) * kKeyTile + warp * 16;  // this warp's keys key0 .. key0 + 15
                 if (ok && key0 < end && key0 + 16 > first && (s_boxes[st] >> box_of_warp & 1u)) {
                     const uint32_t kb = sbase + st * 2 * C::kTileBytes, vb = kb + C::kTileBytes;
                     float s[MT][2][4];
@@ -405,8 +441,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 bar_consumers();  // the join buffer is free again
             }
-        });
+            if (lane == 0) mbar_arrive(seg_empty0 + 8 * si);
+        }
     }
+    if constexpr (!PREFIX) grid_dependency_wait();  // ends after the prefix kernel: the merge after this one sees both
 }
 
 template <int D, int MT, bool PREFIX>
@@ -422,7 +460,8 @@ cudaError_t launch_t(const PagedArgs& a, cudaStream_t s) {
     auto kern = paged_mma_kernel<D, MT, PREFIX>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<PREFIX ? a.p_ctas : a.ctas, kThreads, C::kSmem, s>>>(tk, tv, a);
+    if (!PREFIX) return launch_own(kern, a, kThreads, C::kSmem, s, tk, tv, a);
+    kern<<<a.p_ctas, kThreads, C::kSmem, s>>>(tk, tv, a);
     return cudaGetLastError();
 }
 

@@ -23,6 +23,8 @@ namespace usp {
 namespace {
 
 constexpr int kKeyTile = 128;
+// A piece's beginning and end (Q, the first products, the stores) against a tile's 1.5 to 2 us.
+constexpr int kPieceCost = 3;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;  // log2 units
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;  // of 168 at launch (NS = 2): 2 * 208 + 88 <= 3 * 168
@@ -41,7 +43,7 @@ struct Cfg {
     static constexpr int kOffK = NS * kTileBytes;
     static constexpr int kOffV = kOffK + kKStages * kTileBytes;
     static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
-    static constexpr int kBars = 2 * kKStages + 2 * kVStages + 4 * NS + 1;
+    static constexpr int kBars = 2 * kKStages + 2 * kVStages + 4 * NS + 1 + 2 * kSegs;
     static constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
 };
 
@@ -66,12 +68,14 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
     __shared__ Share share;
     __shared__ int abort_flag;
     __shared__ uint32_t s_boxes[kFlags];  // boxes of a tile that were loaded
+    __shared__ Seg s_seg[kSegs];
     auto BAR = [&](int i) { return sbase + C::kOffBar + 8u * (uint32_t)i; };
     const int kKFull = 0, kKEmpty = KS, kVFull = 2 * KS, kVEmpty = kVFull + VS;
     const int kQFull = kVEmpty + VS, kSFull = kQFull + NS, kPReady = kSFull + NS, kOReady = kPReady + NS;  // per stream
-    const int kDrain = kOReady + NS;
+    const int kDrain = kOReady + NS, kSegFull = kDrain + 1, kSegEmpty = kSegFull + kSegs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
     constexpr int kProducer = 4 * NS, kIssuer = 4 * NS + 1;
+    let_dependents_start();
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
@@ -84,6 +88,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
             mbar_init(BAR(kOReady + st), 1);
         }
         mbar_init(BAR(kDrain), 1);
+        for (int s = 0; s < kSegs; ++s) { mbar_init(BAR(kSegFull + s), 1); mbar_init(BAR(kSegEmpty + s), 4 * NS + 1); }
         fence_mbar_init();
     }
     if (warp == kIssuer) {
@@ -91,7 +96,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
         tmem_relinquish();
     }
     if constexpr (!PREFIX) {
-        find_share<M, kKeyTile, C::kThreads>(a, cta, a.ctas, &share);
+        find_share<M, kKeyTile, kPieceCost, C::kThreads>(a, cta, a.ctas, &share);
         finish_empty_rows<__nv_bfloat16, M, kKeyTile, C::kThreads>(a, cta, a.ctas);
     }
     tc_fence_before();
@@ -100,19 +105,6 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     volatile int* abort_p = &abort_flag;
 
-    // piece(g) returns false to stop (a wait gave up)
-    auto walk_all = [&](auto&& piece) {
-        Seg g;
-        if constexpr (PREFIX) {
-            PrefixWalk<M, kKeyTile> walk(a, cta);
-            while (walk.next(g))
-                if (!piece(g)) break;
-        } else {
-            OwnWalk<M, kKeyTile> walk(a, share);
-            while (walk.next(g))
-                if (!piece(g)) break;
-        }
-    };
     // tiles of a piece that hold a key which some row of stream st sees
     auto stream_tiles = [&](const Seg& g, int st) {
         if (st * 128 >= g.n_rows) return 0;
@@ -128,8 +120,22 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
             // ---------------------------------------------------------------- TMA producer
             const int psize = 1 << a.page_log2, box = min(psize, kKeyTile), nb = kKeyTile / box;
             const int my_box = lane % nb, my_chunk = lane / nb;
-            int it = 0, nv = 0;
-            walk_all([&](const Seg& g) {
+            int it = 0, nv = 0, n_seg = 0;
+            auto publish = [&](const Seg& g) {
+                const int i = n_seg % kSegs;
+                if (n_seg >= kSegs &&
+                    !__all_sync(~0u, mbar_wait(BAR(kSegEmpty + i), (n_seg / kSegs - 1) & 1, abort_p, 43, a.status)))
+                    return false;
+                if (lane == 0) {
+                    s_seg[i] = g;
+                    mbar_arrive(BAR(kSegFull + i));
+                }
+                ++n_seg;
+                __syncwarp();
+                return true;
+            };
+            auto piece = [&](const Seg& g) {  // false: a wait gave up
+                if (!publish(g)) return false;
                 const int first = PREFIX ? 0 : a.key_begin, end = seg_key_end<PREFIX>(a, g);
                 auto page_of = [&](int tile) {  // of this lane's box, -1: not loaded
                     const int j = tile * kKeyTile + my_box * box;
@@ -169,7 +175,30 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                     page = next;
                 }
                 return true;
-            });
+            };
+            Seg g;
+            bool ok = true;
+            if constexpr (PREFIX) {
+                PrefixWalk<M, kKeyTile> walk(a, cta);
+                while (ok && walk.next(g)) ok = piece(g);
+            } else {
+                OwnWalk<M, kKeyTile, kPieceCost> walk(a, share);
+                // The end of a unit that an earlier CTA began comes last.  All shares being equally long, the CTAs of a
+                // head are then at the same key tile, or at one of two, at any time, and read it from L2 together.
+                Seg tail;
+                bool has_tail = false;
+                while (ok && walk.next(g)) {
+                    if (g.ordinal == 0 && !g.begins) {
+                        tail = g;
+                        has_tail = true;
+                    } else {
+                        ok = piece(g);
+                    }
+                }
+                if (ok && has_tail) ok = piece(tail);
+            }
+            g.n_tiles = 0;
+            if (ok) publish(g);
             __syncwarp();
             if (lane == 0) {  // every issued load lands before the CTA can exit
                 drain_ring(BAR(kKFull), KS, it, 33, a.status);
@@ -190,10 +219,16 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                 }
                 mma_commit(BAR(kSFull + st));
             };
-            walk_all([&](const Seg& g) {
+            for (int n_seg = 0;; ++n_seg) {
+                const int si = n_seg % kSegs;
+                if (!mbar_wait(BAR(kSegFull + si), (n_seg / kSegs) & 1, abort_p, 44, a.status)) break;
+                const int n_tiles = s_seg[si].n_tiles;
+                if (n_tiles == 0) break;
                 int nt[NS];
+                for (int st = 0; st < NS; ++st) nt[st] = stream_tiles(s_seg[si], st);
+                mbar_arrive(BAR(kSegEmpty + si));
+                bool ok = [&] {
                 for (int st = 0; st < NS; ++st) {
-                    nt[st] = stream_tiles(g, st);
                     if (nt[st] == 0) continue;
                     if (!mbar_wait(BAR(kQFull + st), pieces[st] & 1, abort_p, 35, a.status)) return false;
                     ++pieces[st];
@@ -203,7 +238,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                 for (int st = 0; st < NS; ++st)
                     if (nt[st] > 0) issue_qk(st, base);
                 mma_commit(BAR(kKEmpty + base % KS));
-                for (int j = 0; j < g.n_tiles; ++j) {
+                for (int j = 0; j < n_tiles; ++j) {
                     const int it = base + j, vs = it % VS, k1 = (it + 1) % KS;
                     if (!mbar_wait(BAR(kVFull + vs), (it / VS) & 1, abort_p, 37, a.status)) return false;
                     const uint64_t dv = sdesc_sw128(sbase + C::kOffV + vs * C::kTileBytes, 16384, 1024);
@@ -231,10 +266,12 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                     mma_commit(BAR(kVEmpty + vs));
                     if (k_waited) mma_commit(BAR(kKEmpty + k1));
                 }
-                base += g.n_tiles;
-                for (int st = 0; st < NS; ++st) cnt[st] += nt[st];
                 return true;
-            });
+                }();
+                if (!ok) break;
+                base += n_tiles;
+                for (int st = 0; st < NS; ++st) cnt[st] += nt[st];
+            }
             // every issued MMA completes before TMEM is freed (after an abort, too)
             mma_commit(BAR(kDrain));
             mbar_drain(BAR(kDrain), 0, 39, a.status);
@@ -252,10 +289,10 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
             return __all_sync(~0u, mbar_wait(bar, parity, abort_p, site, a.status)) != 0;
         };
         int base = 0, cnt = 0, pieces = 0;
-        walk_all([&](const Seg& g) {
+        auto piece = [&](const Seg& g) {  // false: a wait gave up
             const int r = st * 128 + row;
             const bool valid = r < g.n_rows;
-            const int n_tiles = stream_tiles(g, st);
+            const int n_tiles = stream_tiles(g, st), tile0 = g.tile0;
             const int first = PREFIX ? 0 : a.key_begin, end = seg_key_end<PREFIX>(a, g);
             const int lim = valid ? row_limit<PREFIX>(a, g, r) : INT_MAX;
             // (a warp without a valid row has its rows of V to clear, too)
@@ -292,7 +329,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                     s[64 + c] = __uint_as_float(r2r[c]);
                     s[96 + c] = __uint_as_float(r3r[c]);
                 }
-                const int key0 = (g.tile0 + j) * kKeyTile;
+                const int key0 = (tile0 + j) * kKeyTile;
                 const uint32_t live = s_boxes[(base + j) % kFlags] & all_boxes;
                 if (key0 + kKeyTile > lim_min || key0 < first || live != all_boxes) {
                     uint32_t boxes[4];
@@ -413,7 +450,14 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
             base += g.n_tiles;
             cnt += n_tiles;
             return true;
-        });
+        };
+        for (int n_seg = 0;; ++n_seg) {
+            const int si = n_seg % kSegs;
+            if (!warp_wait(BAR(kSegFull + si), (n_seg / kSegs) & 1, 45)) break;
+            if (s_seg[si].n_tiles == 0 || !piece(s_seg[si])) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(kSegEmpty + si));
+        }
     }
     // ---------------------------------------------------------------- teardown
     tc_fence_before();
@@ -423,6 +467,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if constexpr (!PREFIX) grid_dependency_wait();  // ends after the prefix kernel: the merge after this one sees both
 }
 
 template <int D, int NS, bool PREFIX>
@@ -438,7 +483,8 @@ cudaError_t launch_t(const PagedArgs& a, cudaStream_t s) {
     auto kern = paged_tc_kernel<D, NS, PREFIX>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<PREFIX ? a.p_ctas : a.ctas, C::kThreads, C::kSmem, s>>>(tk, tv, a);
+    if (!PREFIX) return launch_own(kern, a, C::kThreads, C::kSmem, s, tk, tv, a);
+    kern<<<a.p_ctas, C::kThreads, C::kSmem, s>>>(tk, tv, a);
     return cudaGetLastError();
 }
 
