@@ -109,6 +109,14 @@ class Cache:
     dtype: str = "bf16"
 
     def c(self) -> UspCache:
+        """The struct of the C ABI (kept: a decoding step is short enough for its making to show)."""
+        made = self.__dict__.get("_c")
+        if made is None:
+            made = self._make()
+            object.__setattr__(self, "_c", made)
+        return made
+
+    def _make(self) -> UspCache:
         if self.dtype not in _TORCH_DTYPE:
             raise ValueError(f"dtype must be 'f32' or 'bf16', got {self.dtype!r}")
         return UspCache(self.n_pages, self.page_size, self.n_seqs, self.max_pages, self.Hq, self.Hkv, self.d,
@@ -145,7 +153,7 @@ def _ptr(x) -> int:
     if isinstance(x, int):
         return x
     if isinstance(x, torch.Tensor):
-        if x.numel() and not x.is_cuda:
+        if not x.is_cuda and x.numel():
             raise ValueError("libusp takes device tensors")
         if not x.is_contiguous():
             raise ValueError("libusp takes contiguous tensors")
@@ -155,7 +163,8 @@ def _ptr(x) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else 0
+        # (is_initialized reads a flag; is_available asks the driver, a microsecond of every call)
+        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_initialized() or torch.cuda.is_available() else 0
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -168,14 +177,14 @@ def _rows(x, heads: int, d: int):
         return x or 0, heads * d
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"expected a torch tensor, a device pointer or None, got {type(x).__name__}")
-    if x.numel() and not x.is_cuda:
+    if not x.is_cuda and x.numel():
         raise ValueError("libusp takes device tensors")
-    if x.dim() != 3 or tuple(x.shape[1:]) != (heads, d):
-        raise ValueError(f"expected [tokens][{heads}][{d}], got {list(x.shape)}")
-    if x.shape[0] > 1 or (heads > 1 and x.numel()):
-        if x.stride(2) != 1 or (heads > 1 and x.stride(1) != d):
-            raise ValueError("the heads of a token must be contiguous")
-    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else heads * d
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        raise ValueError(f"expected [tokens][{heads}][{d}], got {list(shape)}")
+    if shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
+        raise ValueError("the heads of a token must be contiguous")
+    return x.data_ptr(), stride[0] if shape[0] > 1 else heads * d
 
 
 def _cache(c) -> ctypes.POINTER(UspCache):

@@ -181,6 +181,7 @@ cudaError_t launch_paged_own(const PagedArgs& a, cudaStream_t stream);
 cudaError_t launch_paged_prefix(const PagedArgs& a, cudaStream_t stream);
 cudaError_t launch_paged_mma(const PagedArgs& a, bool prefix, cudaStream_t stream);  // paged_mma.cu: up to 32 rows
 cudaError_t launch_paged_tc(const PagedArgs& a, bool prefix, cudaStream_t stream);   // paged_tc.cu: 128 or 256 rows
+cudaError_t launch_paged_f32(const PagedArgs& a, bool prefix, cudaStream_t stream);  // paged_f32.cu: float32
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream);
 
 // ---- tensor maps (api.cu)

@@ -4,6 +4,13 @@
 //   a' = a cos(r f_i) - b sin(r f_i),  b' = b cos(r f_i) + a sin(r f_i).
 // The angle is the float64 product of the position and the float32 frequency, reduced by 2 pi in float64 (in float32
 // the angle of position 10^6 is off by up to 0.06 rad); sine, cosine and the rotation are float32.
+//
+// Bound by HBM: every value is read once and written once (k twice with k_out).  A head is d / (2 V) items of two 16-byte
+// vectors (V values): the two that a rotation pairs up, or two neighbours where pairs are neighbours or pass unchanged.  A
+// CTA takes as many tokens as make about kItems items; its threads first issue their loads, then find the tokens' slots
+// (two dependent loads) and the tokens' cosines and sines (one per pair, shared by all heads; float64 is scarce here), and
+// only then wait for the data.
+#include <algorithm>
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -15,6 +22,9 @@ namespace usp {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kAhead = 3;                     // items of a thread in flight
+constexpr int kItems = kThreads * kAhead;     // items of a CTA per round
+constexpr int kMaxTokens = 16;
 
 // cos and sin of r * f
 __device__ __forceinline__ float2 turn(int r, float f) {
@@ -24,76 +34,185 @@ __device__ __forceinline__ float2 turn(int r, float f) {
     return make_float2(c, s);
 }
 
-__device__ __forceinline__ float ld(const float* p) { return *p; }
-__device__ __forceinline__ float ld(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void st(float* p, float x) { *p = x; }
-__device__ __forceinline__ void st(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-
+// The values of a 16-byte vector, and back (one rounding).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams p) {
-    const int t = blockIdx.x;
-    const int s = p.seq[t], pos = p.pos[t];
-    if (s < 0 || s >= p.n_seqs || pos < 0 || pos >> p.page_log2 >= p.max_pages) return;
-    const int page = p.page_table[(int64_t)s * p.max_pages + (pos >> p.page_log2)];
-    if (page < 0 || page >= p.n_pages) return;
-    const int r = p.rot_pos ? p.rot_pos[t] : pos;
-    __shared__ float2 cs[64];
-    for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) cs[i] = turn(r, p.inv_freq[i]);
+struct Vec;
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void open(const uint4& w, float (&x)[4]) {
+        x[0] = __uint_as_float(w.x);
+        x[1] = __uint_as_float(w.y);
+        x[2] = __uint_as_float(w.z);
+        x[3] = __uint_as_float(w.w);
+    }
+    static __device__ __forceinline__ uint4 close(const float (&x)[4]) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void open(const uint4& w, float (&x)[8]) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = __uint_as_float(u[e] << 16);
+            x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 close(const float (&x)[8]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[e]) : "f"(x[2 * e + 1]), "f"(x[2 * e]));
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+};
+
+template <typename T, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams p, int tokens_per_cta, int item_log2) {
+    constexpr int V = Vec<T>::N;
+    __shared__ float2 cs[kMaxTokens][64];
+    __shared__ int64_t s_row[kMaxTokens];  // row of head 0 in the pool, -1: padding
+    __shared__ int s_rot[kMaxTokens];
+    const int t0 = blockIdx.x * tokens_per_cta, n_tok = min(tokens_per_cta, p.n_tokens - t0);
+    const int d = p.d, half = p.rot / 2, psize = 1 << p.page_log2;
+    const int hq = p.q ? p.Hq : 0, heads = hq + 2 * p.Hkv, per_token = heads << item_log2;
+    const int total = n_tok * per_token;
+
+    // an item: token, head (q heads, then k, then v), place of its two vectors within the head
+    struct Item {
+        int tok, head, e0, e1;
+        bool rotates;
+    };
+    auto item = [&](int x) {
+        Item it;
+        it.tok = x / per_token;
+        const int y = x - it.tok * per_token;
+        it.head = y >> item_log2;
+        const int i = (y & ((1 << item_log2) - 1)) * V;  // values of the first vectors before this one
+        it.rotates = it.head < hq + p.Hkv && i < half;
+        if (INTERLEAVED || !it.rotates) {
+            it.e0 = 2 * i;
+            it.e1 = 2 * i + V;
+        } else {
+            it.e0 = i;
+            it.e1 = i + half;
+        }
+        return it;
+    };
+    auto source = [&](const Item& it) {
+        const int64_t t = t0 + it.tok;
+        return it.head < hq ? static_cast<const T*>(p.q) + t * p.q_stride + it.head * d
+               : it.head < hq + p.Hkv ? static_cast<const T*>(p.k) + t * p.k_stride + (it.head - hq) * d
+                                      : static_cast<const T*>(p.v) + t * p.v_stride + (it.head - hq - p.Hkv) * d;
+    };
+    uint4 w[kAhead][2];
+    auto fetch = [&](int x0) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int x = x0 + u * kThreads;
+            if (x < total) {
+                const Item it = item(x);
+                const T* src = source(it);
+                w[u][0] = __ldcs(reinterpret_cast<const uint4*>(src + it.e0));
+                w[u][1] = __ldcs(reinterpret_cast<const uint4*>(src + it.e1));
+            }
+        }
+    };
+    fetch(threadIdx.x);
+    if (threadIdx.x < n_tok) {
+        const int t = t0 + threadIdx.x, s = p.seq[t], pos = p.pos[t];
+        int64_t row = -1;
+        if (s >= 0 && s < p.n_seqs && pos >= 0 && pos >> p.page_log2 < p.max_pages) {
+            const int page = p.page_table[(int64_t)s * p.max_pages + (pos >> p.page_log2)];
+            if (page >= 0 && page < p.n_pages) row = (((int64_t)page * p.Hkv) << p.page_log2) + (pos & (psize - 1));
+        }
+        s_row[threadIdx.x] = row;
+    }
+    // (not through shared memory: the angles need not wait for the slots)
+    for (int x = threadIdx.x; x < n_tok * half; x += kThreads) {
+        const int tok = x / half, i = x - tok * half;
+        cs[tok][i] = turn(p.rot_pos ? p.rot_pos[t0 + tok] : p.pos[t0 + tok], p.inv_freq[i]);
+    }
     __syncthreads();
-    const int psize = 1 << p.page_log2, slot = pos & (psize - 1), d = p.d, half = p.rot / 2;
-    const T* q = p.q ? static_cast<const T*>(p.q) + t * p.q_stride : nullptr;
-    const T* k = static_cast<const T*>(p.k) + t * p.k_stride;
-    const T* v = static_cast<const T*>(p.v) + t * p.v_stride;
-    T* q_out = static_cast<T*>(p.q_out) + (int64_t)t * p.Hq * d;
-    T* k_out = p.k_out ? static_cast<T*>(p.k_out) + (int64_t)t * p.Hkv * d : nullptr;
-    T* kp = static_cast<T*>(p.k_pages) + (((int64_t)page * p.Hkv) * psize + slot) * d;
-    T* vp = static_cast<T*>(p.v_pages) + (((int64_t)page * p.Hkv) * psize + slot) * d;
-    const int64_t hs = (int64_t)psize * d;
-    // pairs, then the elements that pass, of each q and k head; a thread handles both of a pair
-    const int per = half + (d - p.rot);
-    for (int x = threadIdx.x; x < (p.Hq + p.Hkv) * per; x += kThreads) {
-        const int h = x / per, i = x % per;
-        const bool is_q = h < p.Hq;
-        if (is_q && !q) continue;
-        const T* src = is_q ? q + h * d : k + (h - p.Hq) * d;
-        int e0, e1;
-        if (i < half) {
-            e0 = p.interleaved ? 2 * i : i;
-            e1 = p.interleaved ? 2 * i + 1 : i + half;
-        } else {
-            e0 = e1 = p.rot + (i - half);
-        }
-        float a = ld(src + e0), b = ld(src + e1);
-        if (i < half) {
-            const float2 w = cs[i];
-            const float a2 = a * w.x - b * w.y, b2 = b * w.x + a * w.y;
-            a = a2;
-            b = b2;
-        }
-        if (is_q) {
-            st(q_out + h * d + e0, a);
-            st(q_out + h * d + e1, b);
-        } else {
-            const int hk = h - p.Hq;
-            st(kp + hk * hs + e0, a);
-            st(kp + hk * hs + e1, b);
-            if (k_out) {
-                st(k_out + hk * d + e0, a);
-                st(k_out + hk * d + e1, b);
+    for (int x0 = threadIdx.x; x0 < total; x0 += kItems) {
+        if (x0 != threadIdx.x) fetch(x0);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int x = x0 + u * kThreads;
+            if (x >= total) break;
+            const Item it = item(x);
+            const int64_t row = s_row[it.tok];
+            if (row < 0) continue;
+            if (it.rotates) {
+                float a[V], b[V];
+                Vec<T>::open(w[u][0], a);
+                Vec<T>::open(w[u][1], b);
+                if constexpr (INTERLEAVED) {
+                    const float2* c = cs[it.tok] + it.e0 / 2;
+#pragma unroll
+                    for (int e = 0; e < V; e += 2) {
+                        const float2 f = c[e / 2], g = c[(V + e) / 2];
+                        const float a0 = a[e], a1 = a[e + 1], b0 = b[e], b1 = b[e + 1];
+                        a[e] = a0 * f.x - a1 * f.y;
+                        a[e + 1] = a1 * f.x + a0 * f.y;
+                        b[e] = b0 * g.x - b1 * g.y;
+                        b[e + 1] = b1 * g.x + b0 * g.y;
+                    }
+                } else {
+                    const float2* c = cs[it.tok] + it.e0;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float2 f = c[e];
+                        const float a0 = a[e], b0 = b[e];
+                        a[e] = a0 * f.x - b0 * f.y;
+                        b[e] = b0 * f.x + a0 * f.y;
+                    }
+                }
+                w[u][0] = Vec<T>::close(a);
+                w[u][1] = Vec<T>::close(b);
+            }
+            auto store = [&](T* dst) {
+                *reinterpret_cast<uint4*>(dst + it.e0) = w[u][0];
+                *reinterpret_cast<uint4*>(dst + it.e1) = w[u][1];
+            };
+            const int64_t t = t0 + it.tok;
+            if (it.head < hq) {
+                store(static_cast<T*>(p.q_out) + (t * p.Hq + it.head) * d);
+            } else if (it.head < hq + p.Hkv) {
+                const int h = it.head - hq;
+                store(static_cast<T*>(p.k_pages) + (row + ((int64_t)h << p.page_log2)) * d);
+                if (p.k_out) store(static_cast<T*>(p.k_out) + (t * p.Hkv + h) * d);
+            } else {
+                const int h = it.head - hq - p.Hkv;
+                store(static_cast<T*>(p.v_pages) + (row + ((int64_t)h << p.page_log2)) * d);
             }
         }
     }
-    for (int x = threadIdx.x; x < p.Hkv * d; x += kThreads) vp[(x / d) * hs + x % d] = v[x];
+}
+
+template <typename T>
+cudaError_t launch_t(const AppendParams& p, cudaStream_t s) {
+    int item_log2 = 0;  // items per head
+    while ((2 * Vec<T>::N << item_log2) < p.d) ++item_log2;
+    const int per_token = ((p.q ? p.Hq : 0) + 2 * p.Hkv) << item_log2;
+    // few heads: several tokens per CTA, as long as there are CTAs enough for every SM
+    int n = std::min(kMaxTokens, std::max(1, kItems / per_token));
+    while (n > 1 && (p.n_tokens + n - 1) / n < 4 * 152) --n;
+    const unsigned grid = (unsigned)((p.n_tokens + n - 1) / n);
+    if (p.interleaved)
+        kv_append_kernel<T, true><<<grid, kThreads, 0, s>>>(p, n, item_log2);
+    else
+        kv_append_kernel<T, false><<<grid, kThreads, 0, s>>>(p, n, item_log2);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream) {
-    if (p.elem == 4)
-        kv_append_kernel<float><<<p.n_tokens, kThreads, 0, stream>>>(p);
-    else
-        kv_append_kernel<__nv_bfloat16><<<p.n_tokens, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return p.elem == 4 ? launch_t<float>(p, stream) : launch_t<__nv_bfloat16>(p, stream);
 }
 
 }  // namespace usp

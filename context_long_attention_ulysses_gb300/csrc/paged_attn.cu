@@ -1,4 +1,5 @@
-// Attention over a paged cache (decoding, verification, chunks of prompts) and behind a shared prefix.
+// Attention over a paged cache (decoding, verification, chunks of prompts) and behind a shared prefix: the choice of
+// kernels, the workspace, and the join of partial results.
 //
 // Per row (token, query head): S_j = scale q.k_j over the keys the row sees, o = softmax(S) V, lse = ln sum exp(S), in one
 // pass over the keys with a running maximum and sum.  How the work is cut is explained in paged.cuh.
@@ -8,7 +9,6 @@
 #include <cuda_bf16.h>
 
 #include "paged.cuh"
-#include "ptx.cuh"
 
 namespace usp {
 
@@ -17,130 +17,8 @@ namespace {
 constexpr int kSms = 152;
 constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-
-// ---------------------------------------------------------------- CUDA cores
-// Four warps, each every fourth key; a lane holds D/32 columns of the row's key, value and output.
-constexpr int kSimpleKeys = 64;
-constexpr int kSimplePiece = 1;
-constexpr int kSimpleThreads = 128;
-constexpr int kSimpleRows = 8;
-
-template <typename T, int D, bool PREFIX>
-__global__ void __launch_bounds__(kSimpleThreads) paged_simple_kernel(const PagedArgs a) {
-    constexpr int M = kSimpleRows, V = D / 32, kWarps = kSimpleThreads / 32;
-    __shared__ Share share;
-    __shared__ float s_acc[kWarps][M][D];
-    __shared__ float s_m[kWarps][M], s_l[kWarps][M];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
-    let_dependents_start();
-    if constexpr (!PREFIX) {
-        find_share<M, kSimpleKeys, kSimplePiece, kSimpleThreads>(a, cta, a.ctas, &share);
-        finish_empty_rows<T, M, kSimpleKeys, kSimpleThreads>(a, cta, a.ctas);
-    }
-    auto run = [&](const Seg& g) {
-        float q[M][V], acc[M][V], m[M], l[M];
-        int lim[M];
-#pragma unroll
-        for (int r = 0; r < M; ++r) {
-            m[r] = -INFINITY;
-            l[r] = 0.f;
-            lim[r] = 0;
-            const int R = g.row0 + r, i = R / a.g;
-#pragma unroll
-            for (int c = 0; c < V; ++c) acc[r][c] = q[r][c] = 0.f;
-            if (r < g.n_rows) {
-                lim[r] = row_limit<PREFIX>(a, g, r);
-                const T* src = static_cast<const T*>(a.q) +
-                               ((int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g)) * D + lane * V;
-#pragma unroll
-                for (int c = 0; c < V; ++c) q[r][c] = to_f32(src[c]) * a.scale_log2;
-            }
-        }
-        const int first = PREFIX ? 0 : a.key_begin;
-        const int k0 = max(g.tile0 * kSimpleKeys, first);
-        const int k1 = min((g.tile0 + g.n_tiles) * kSimpleKeys, seg_key_end<PREFIX>(a, g));
-        for (int j = k0 + warp; j < k1; j += kWarps) {
-            const int page = seg_page<PREFIX>(a, g, j >> a.page_log2);
-            if (page < 0) continue;
-            const int64_t at = ((((int64_t)page * a.Hkv + g.h) << a.page_log2) + (j & ((1 << a.page_log2) - 1))) * D +
-                               lane * V;
-            const T* kj = static_cast<const T*>(a.k_pages) + at;
-            const T* vj = static_cast<const T*>(a.v_pages) + at;
-            float kv[V], vv[V];
-#pragma unroll
-            for (int c = 0; c < V; ++c) {
-                kv[c] = to_f32(kj[c]);
-                vv[c] = to_f32(vj[c]);
-            }
-#pragma unroll
-            for (int r = 0; r < M; ++r) {
-                float x = 0.f;
-#pragma unroll
-                for (int c = 0; c < V; ++c) x = fmaf(q[r][c], kv[c], x);
-                for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-                if (j < lim[r]) {
-                    const float mn = fmaxf(m[r], x);
-                    const float ms = mn == -INFINITY ? 0.f : mn;
-                    const float al = exp2f(m[r] - ms), p = exp2f(x - ms);
-                    m[r] = mn;
-                    l[r] = l[r] * al + p;
-#pragma unroll
-                    for (int c = 0; c < V; ++c) acc[r][c] = acc[r][c] * al + p * vv[c];
-                }
-            }
-        }
-        // join the four warps
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < M; ++r) {
-#pragma unroll
-            for (int c = 0; c < V; ++c) s_acc[warp][r][lane * V + c] = acc[r][c];
-            if (lane == 0) {
-                s_m[warp][r] = m[r];
-                s_l[warp][r] = l[r];
-            }
-        }
-        __syncthreads();
-        for (int x = threadIdx.x; x < g.n_rows * D; x += kSimpleThreads) {
-            const int r = x / D, c = x % D;
-            float mx = -INFINITY;
-            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][r]);
-            float sum = 0.f, o = 0.f;
-            const float ms = mx == -INFINITY ? 0.f : mx;
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2f(s_m[w][r] - ms);
-                sum += f * s_l[w][r];
-                o += f * s_acc[w][r][c];
-            }
-            const bool has = sum > 0.f;
-            o = has ? o / sum : 0.f;
-            const float lse2 = has ? ms + log2f(sum) : -INFINITY;
-            const RowDst dst = row_dst<M, PREFIX>(a, g, r, cta);
-            if (dst.out) {
-                put(static_cast<T*>(dst.out) + c, o);
-                if (c == 0) *dst.lse = lse2 * kLn2;
-            } else {
-                dst.part[c] = o;
-                if (c == 0) *dst.lse = lse2;
-            }
-            if (!PREFIX && g.ends && c == 0) note_row<M>(a, g, r, cta);
-        }
-        __syncthreads();
-    };
-    Seg g;
-    if constexpr (PREFIX) {
-        PrefixWalk<M, kSimpleKeys> walk(a, cta);
-        while (walk.next(g)) run(g);
-    } else {
-        OwnWalk<M, kSimpleKeys, kSimplePiece> walk(a, share);
-        while (walk.next(g)) run(g);
-        grid_dependency_wait();  // ends after the prefix kernel, so that the merge after this one sees both
-    }
-}
 
 // ---------------------------------------------------------------- joining partial results
 // WPR warps per row: o = sum_c 2^(lse_c - lse) o_c over the row's partial results, the prefix's first, keys in order.
@@ -243,20 +121,6 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
     if (lane == 0) a.lse[row] = sum > 0.f ? (ms + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-template <typename T, int D>
-cudaError_t simple_t(const PagedArgs& a, bool prefix, cudaStream_t s) {
-    if (prefix)
-        paged_simple_kernel<T, D, true><<<a.p_ctas, kSimpleThreads, 0, s>>>(a);
-    else
-        return launch_own(paged_simple_kernel<T, D, false>, a, kSimpleThreads, 0, s, a);
-    return cudaGetLastError();
-}
-
-template <bool PREFIX>
-cudaError_t simple(const PagedArgs& a, cudaStream_t s) {
-    return a.d == 64 ? simple_t<float, 64>(a, PREFIX, s) : simple_t<float, 128>(a, PREFIX, s);
-}
-
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
@@ -266,7 +130,7 @@ struct Pick {
     int rows, keys, ctas;
 };
 static Pick pick(const PagedArgs& a, int64_t rows) {
-    if (a.elem == 4) return {kSimpleRows, kSimpleKeys, kSms * 4};
+    if (a.elem == 4) return {8, 64, kSms};
     if (rows <= 32) return {rows <= 16 ? 16 : 32, 64, kSms * 2};
     return {rows <= 128 ? 128 : 256, 128, kSms};
 }
@@ -309,12 +173,12 @@ size_t paged_plan(PagedArgs* a, int max_q, void* ws) {
 }
 
 cudaError_t launch_paged_own(const PagedArgs& a, cudaStream_t stream) {
-    if (a.elem == 4) return simple<false>(a, stream);
+    if (a.elem == 4) return launch_paged_f32(a, false, stream);
     return a.rows <= 32 ? launch_paged_mma(a, false, stream) : launch_paged_tc(a, false, stream);
 }
 
 cudaError_t launch_paged_prefix(const PagedArgs& a, cudaStream_t stream) {
-    if (a.elem == 4) return simple<true>(a, stream);
+    if (a.elem == 4) return launch_paged_f32(a, true, stream);
     return a.p_rows <= 32 ? launch_paged_mma(a, true, stream) : launch_paged_tc(a, true, stream);
 }
 
