@@ -42,6 +42,7 @@ __all__ = [
     "usp_prefix_attn", "kv_append", "paged_attention", "prefix_attention",
 ]
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
@@ -163,8 +164,11 @@ def _ptr(x) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
-        # (is_initialized reads a flag; is_available asks the driver, a microsecond of every call)
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_initialized() or torch.cuda.is_available() else 0
+        # (a decoding step is short enough for this to show: the stream object costs 3 us, asking the driver whether there is
+        # a device another; the handle alone a few tenths)
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else 0
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

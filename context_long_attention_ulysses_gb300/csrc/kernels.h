@@ -167,11 +167,12 @@ struct PagedArgs {
     // the plan: row-tile sizes and CTAs of the own and the prefix part, and the workspace
     int rows, p_rows;
     int ctas, p_ctas;
-    int p_keys;  // keys per tile of the prefix part
+    int p_split;                   // parts of a unit of the prefix
     uint2* row_info;               // per row of o
     float *own_o, *own_lse;        // prefix only: own part of whole units, [n_tokens][Hq][d], [n_tokens][Hq]
     float *slot_o, *slot_l;        // [ctas][2][rows][d], [ctas][2][rows]
-    float *pslot_o, *pslot_l;      // [p_ctas][2][p_rows][d], [p_ctas][2][p_rows]
+    float *pslot_o, *pslot_l;      // [p_ctas][p_rows][d], [p_ctas][p_rows]
+                                   // (slots of 128 and more rows are [d/4][rows][4] each)
     int* status;
 };
 // Fills the plan's sizes (rows, p_rows, ctas, p_ctas) from the shapes and returns the workspace's bytes; with ws, also

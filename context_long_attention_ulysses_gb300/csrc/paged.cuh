@@ -35,13 +35,13 @@ __device__ __forceinline__ void let_dependents_start() { asm volatile("griddepco
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
                              const A&... args) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -54,7 +54,7 @@ cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threa
 template <typename... P, typename... A>
 cudaError_t launch_own(void (*kernel)(P...), const PagedArgs& a, unsigned threads, size_t smem, cudaStream_t stream,
                        const A&... args) {
-    if (a.prefix_len > 0) return launch_dependent(kernel, a.ctas, threads, smem, stream, args...);
+    if (a.prefix_len > 0) return launch_dependent(kernel, dim3(a.ctas), threads, smem, stream, args...);
     kernel<<<a.ctas, threads, smem, stream>>>(args...);
     return cudaGetLastError();
 }
@@ -121,12 +121,26 @@ __device__ __forceinline__ int64_t head_places(const PagedArgs& a, int b) {
     return sum;
 }
 
-// A CTA's share of the line: [pos, end), beginning `off` places into sequence b; W (total) places over n_cta CTAs, no
-// share empty (so that every CTA between those of a unit's first and last tile holds a part of it).
-struct Share {
-    int64_t pos, end, off, total;
-    int b, n_cta;
+// A CTA's share of the line: [pos, end), beginning `off` places into sequence b, whose heads take per_head places each.
+// Of W (total) places over n CTAs the first W % n CTAs take one more than the others; no share is empty (so that every CTA
+// between those of a unit's first and last tile holds a part of it).
+struct Cut {
+    int64_t each;  // places of a share, rounded down
+    int more;      // CTAs that take one more
 };
+struct Share {
+    int64_t pos, end, off, per_head;
+    Cut cut;
+    int b;
+};
+
+__device__ __forceinline__ int64_t share_begin(const Cut& c, int cta) { return c.each * cta + min(cta, c.more); }
+
+// The CTA that owns place x.
+__device__ __forceinline__ int share_owner(const Cut& c, int64_t x) {
+    const int64_t big = (c.each + 1) * c.more;
+    return x < big ? (int)(x / (c.each + 1)) : c.more + (int)((x - big) / c.each);
+}
 
 // Computed by all threads of the CTA (a scan over the sequences; NT threads), result in *out (shared memory).
 template <int M, int KT, int PC, int NT>
@@ -134,43 +148,49 @@ __device__ void find_share(const PagedArgs& a, int cta, int n_cta, Share* out) {
     constexpr int kWarps = NT / 32;
     __shared__ int64_t part[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t mine = 0;
-    for (int b = threadIdx.x; b < a.n_seqs; b += NT) mine += head_places<M, KT, PC>(a, b);
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
-    if (lane == 0) part[warp] = mine;
-    if (threadIdx.x == 0) *out = Share{0, 0, 0, 0, a.n_seqs, 1};
-    __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < kWarps; ++w) total += part[w];
-    total *= a.Hkv;
-    if (n_cta > total) n_cta = (int)total;
-    if (cta >= n_cta) return;
-    const int64_t pos = total * cta / n_cta, end = total * (cta + 1) / n_cta;
-    int64_t base = 0;
-    for (int b0 = 0; b0 < a.n_seqs; b0 += NT) {  // chunk by chunk: inclusive scan of the sequences' places
-        __syncthreads();
+    if (threadIdx.x == 0) *out = Share{0, 0, 0, 0, Cut{0, 0}, a.n_seqs};
+    // sequence b0 + threadIdx.x: its places of a head, and the inclusive sum of all heads' places from b0 on
+    int64_t per_head, inc, sum;
+    auto scan = [&](int b0) {
         const int b = b0 + threadIdx.x;
-        const int64_t cost = b < a.n_seqs ? head_places<M, KT, PC>(a, b) * a.Hkv : 0;
-        int64_t inc = cost;
+        per_head = b < a.n_seqs ? head_places<M, KT, PC>(a, b) : 0;
+        inc = per_head * a.Hkv;
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t up = __shfl_up_sync(~0u, inc, o);
             if (lane >= o) inc += up;
         }
+        __syncthreads();  // (the warp sums of the scan before are read)
         if (lane == 31) part[warp] = inc;
         __syncthreads();
-        int64_t before = base;
-        for (int w = 0; w < warp; ++w) before += part[w];
-        const int64_t lo = before + inc - cost;
-        if (lo <= pos && pos < lo + cost) *out = Share{pos, end, pos - lo, total, b, n_cta};
-        for (int w = 0; w < kWarps; ++w) base += part[w];
-        if (base > pos) break;
+        sum = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) inc += part[w];
+            sum += part[w];
+        }
+    };
+    int64_t total = 0;
+    int b0 = 0;
+    for (;; b0 += NT) {
+        scan(b0);
+        total += sum;
+        if (b0 + NT >= a.n_seqs) break;
     }
+    if (n_cta > total) n_cta = (int)total;
+    if (cta >= n_cta) return;
+    const Cut cut = total <= INT_MAX ? Cut{(int)total / n_cta, (int)total % n_cta}
+                                     : Cut{total / n_cta, (int)(total % n_cta)};
+    const int64_t pos = share_begin(cut, cta), end = share_begin(cut, cta + 1);
+    int64_t before = 0;
+    if (b0 > 0) {  // more than one chunk of sequences: find the one
+        for (b0 = 0;; b0 += NT) {
+            scan(b0);
+            if (before + sum > pos) break;
+            before += sum;
+        }
+    }
+    const int64_t lo = before + inc - per_head * a.Hkv;
+    if (lo <= pos && pos < before + inc) *out = Share{pos, end, pos - lo, per_head, cut, b0 + (int)threadIdx.x};
     __syncthreads();
-}
-
-// The CTA that owns place x of W, shares as above.
-__device__ __forceinline__ int share_owner(int64_t x, int64_t total, int n_cta) {
-    return (int)(((x + 1) * n_cta - 1) / total);
 }
 
 // A piece of one unit: the rows row0 .. row0 + n_rows of a sequence's n*g rows (prefix: of the batch's n_tokens*g
@@ -180,7 +200,7 @@ struct Seg {
     int t0, n, len;        // the sequence (prefix: the whole batch, t0 = 0)
     int tile0, n_tiles;    // tile numbers from key 0
     bool begins, ends;     // the piece holds the unit's first / last tile
-    int ordinal;           // pieces of this CTA before it
+    int ordinal;           // own keys: pieces of this CTA before it
     int first_cta;         // of a cut unit, known where it ends
 };
 
@@ -189,19 +209,17 @@ template <int M, int KT, int PC>
 struct OwnWalk {
     const PagedArgs& a;
     int64_t pos, end, base;  // base: the place of the unit's first tile
-    int64_t total;
-    int n_cta;
+    Cut cut;
     SeqRows s;
     int b, h, rt, nrt, ut, ordinal;
 
     __device__ OwnWalk(const PagedArgs& args, const Share& sh)
-        : a(args), pos(sh.pos), end(sh.end), total(sh.total), n_cta(sh.n_cta), b(sh.b), ordinal(0) {
+        : a(args), pos(sh.pos), end(sh.end), cut(sh.cut), b(sh.b), ordinal(0) {
         if (pos >= end) return;
         s = seq_rows(a, b);
         nrt = row_tiles<M>(a, s);
-        const int64_t per_head = head_places<M, KT, PC>(a, b);
-        h = (int)(sh.off / per_head);
-        int64_t off = sh.off - h * per_head;
+        h = (int)(sh.off / sh.per_head);
+        int64_t off = sh.off - h * sh.per_head;
         rt = 0;
         ut = unit_tiles<M, KT>(a, s, 0);
         while (off >= unit_places<PC>(ut)) {
@@ -247,47 +265,34 @@ struct OwnWalk {
         g.begins = pos == base;
         g.ends = to == base + ut;
         g.ordinal = ordinal++;
-        g.first_cta = g.begins || !g.ends ? -1 : share_owner(base, total, n_cta);  // noted where the unit ends
+        g.first_cta = g.begins || !g.ends ? -1 : share_owner(cut, base);  // noted where the unit ends
         pos = to;
         return true;
     }
 };
 
-// The same over the keys of a shared prefix: units (row tile of the whole batch, head), all of prefix_tiles tiles, in
-// the order head, row tile.
+// The keys of a shared prefix: units are (row tile of the whole batch, head), all alike, so the host cuts each into
+// p_split parts (what it weighs is said in paged_plan), one per CTA: CTA (head * row tiles + row tile) * p_split + part.
 template <int M, int KT>
-struct PrefixWalk {
-    const PagedArgs& a;
-    int64_t pos, end;
-    int tiles, nrt, ordinal;
-
-    __device__ PrefixWalk(const PagedArgs& args, int cta) : a(args), ordinal(0) {
-        tiles = (a.prefix_len + KT - 1) / KT;
-        nrt = (a.n_tokens * a.g + M - 1) / M;
-        const int64_t total = (int64_t)a.Hkv * nrt * tiles;
-        pos = total * cta / a.p_ctas;
-        end = total * (cta + 1) / a.p_ctas;
-    }
-
-    __device__ bool next(Seg& g) {
-        if (pos >= end) return false;
-        const int64_t unit = pos / tiles, base = unit * tiles, to = min(end, base + tiles);
-        g.b = -1;
-        g.h = (int)(unit / nrt);
-        g.row0 = (int)(unit % nrt) * M;
-        g.n_rows = min(M, a.n_tokens * a.g - g.row0);
-        g.t0 = 0;
-        g.n = a.n_tokens;
-        g.len = 0;
-        g.tile0 = (int)(pos - base);
-        g.n_tiles = (int)(to - pos);
-        g.begins = pos == base;
-        g.ends = to == base + tiles;
-        g.ordinal = ordinal++;
-        pos = to;
-        return true;
-    }
-};
+__device__ __forceinline__ Seg prefix_piece(const PagedArgs& a, int cta) {
+    const int tiles = (a.prefix_len + KT - 1) / KT, nrt = (a.n_tokens * a.g + M - 1) / M;
+    const int unit = cta / a.p_split, part = cta - unit * a.p_split;
+    Seg g;
+    g.b = -1;
+    g.h = unit / nrt;
+    g.row0 = (unit - g.h * nrt) * M;
+    g.n_rows = min(M, a.n_tokens * a.g - g.row0);
+    g.t0 = 0;
+    g.n = a.n_tokens;
+    g.len = 0;
+    g.tile0 = (int)((int64_t)tiles * part / a.p_split);
+    g.n_tiles = (int)((int64_t)tiles * (part + 1) / a.p_split) - g.tile0;
+    g.begins = part == 0;
+    g.ends = part == a.p_split - 1;
+    g.ordinal = 0;
+    g.first_cta = 0;
+    return g;
+}
 
 // The producer warp walks the share and hands each piece to the other warps through a ring of kSegs entries, so that the
 // walk's divisions and registers are paid once; a piece without tiles ends it.
@@ -331,26 +336,29 @@ __device__ __forceinline__ int seg_page(const PagedArgs& a, const Seg& g, int j)
 }
 
 // Where the result of row r of a piece goes: `out` (final, dtype of q) or `part` (float32), and its log-sum-exp
-// (natural log in lse, log2 units elsewhere).
+// (natural log in lse, log2 units elsewhere).  The four values from column c (a multiple of 4) on lie at part + c * step: a
+// row of d values has step 1; slots written with a thread per row (GROUPS) are [d/4][M][4], so that a warp's stores of one
+// group of columns are 512 contiguous bytes, and have step M.
 struct RowDst {
     void* out;
     float* part;
     float* lse;
+    int step;
 };
 
-template <int M, bool PREFIX>
+template <int M, bool PREFIX, bool GROUPS = false>
 __device__ __forceinline__ RowDst row_dst(const PagedArgs& a, const Seg& g, int r, int cta) {
-    const int R = g.row0 + r, i = R / a.g;
-    const int64_t row = (int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g);
     if (!PREFIX && g.begins && g.ends) {
+        const int R = g.row0 + r, i = R / a.g;
+        const int64_t row = (int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g);
         if (a.prefix_len == 0)
-            return {static_cast<char*>(a.o) + row * a.d * a.elem, nullptr, a.lse + row};
-        return {nullptr, a.own_o + row * a.d, a.own_lse + row};
+            return {static_cast<char*>(a.o) + row * a.d * a.elem, nullptr, a.lse + row, 1};
+        return {nullptr, a.own_o + row * a.d, a.own_lse + row, 1};
     }
-    const int slot = PREFIX ? g.ordinal : (g.begins ? 1 : 0);
-    const int64_t at = ((int64_t)cta * 2 + slot) * M + r;
-    return PREFIX ? RowDst{nullptr, a.pslot_o + at * a.d, a.pslot_l + at}
-                  : RowDst{nullptr, a.slot_o + at * a.d, a.slot_l + at};
+    const int64_t slot = PREFIX ? (int64_t)cta : (int64_t)cta * 2 + (g.begins ? 1 : 0);
+    float* o = (PREFIX ? a.pslot_o : a.slot_o) + slot * M * a.d;
+    float* l = (PREFIX ? a.pslot_l : a.slot_l) + slot * M + r;
+    return GROUPS ? RowDst{nullptr, o + r * 4, l, M} : RowDst{nullptr, o + (int64_t)r * a.d, l, 1};
 }
 
 // Tells paged_merge_kernel about row r of a piece; called by the CTA that holds the unit's last tile.

@@ -17,122 +17,160 @@ namespace {
 constexpr int kSms = 152;
 constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-
 // ---------------------------------------------------------------- joining partial results
-// WPR warps per row: o = sum_c 2^(lse_c - lse) o_c over the row's partial results, the prefix's first, keys in order.
-// Bound by latency: the log-sum-exps are read by all lanes at once, the outputs kAhead at a time (one after the other they
-// took 15 us for the 38 parts of a row, which is what few rows have; so those have more warps, too).
-template <typename T, int D, int WPR>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const PagedArgs a) {
-    constexpr int V = D / 32, kRows = 8 / WPR, kAhead = 4;
-    __shared__ float s_sum[8], s_acc[WPR > 1 ? 8 : 1][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % WPR;
-    const int64_t row = (int64_t)blockIdx.x * kRows + warp / WPR;
-    const bool in = row < (int64_t)a.n_tokens * a.Hq;
-    // the prefix's parts: one per CTA from pc0 on, each the first piece (slot 0) of its CTA, but for the unit's first part
-    // where that CTA's share begins in the unit before
-    int n_pre = 0;
-    int64_t p0 = 0, p1 = 0;
-    if (in && a.prefix_len > 0) {
-        const int t = (int)(row / a.Hq), hq = (int)(row % a.Hq), h = hq / a.g;
-        const int64_t R = (int64_t)t * a.g + (hq - h * a.g);
-        const int tiles = (a.prefix_len + a.p_keys - 1) / a.p_keys;
-        const int nrt = (int)(((int64_t)a.n_tokens * a.g + a.p_rows - 1) / a.p_rows);
-        const int64_t total = (int64_t)a.Hkv * nrt * tiles, base = ((int64_t)h * nrt + R / a.p_rows) * tiles;
-        const int r = (int)(R % a.p_rows), c0 = share_owner(base, total, a.p_ctas);
-        n_pre = share_owner(base + tiles - 1, total, a.p_ctas) - c0 + 1;
-        p0 = ((int64_t)c0 * 2 + (total * c0 / a.p_ctas < base ? 1 : 0)) * a.p_rows + r;
-        p1 = ((int64_t)c0 * 2) * a.p_rows + r;
+// o = sum_c 2^(lse_c - lse) o_c over a row's partial results, the prefix's first, keys in order.  A row's parts:
+struct Parts {
+    const float *po, *pl;  // prefix part c: log-sum-exp at pl[c * p_step_l], values at po + c * p_step_o
+    const float *oo, *ol;  // own part c, likewise (the first part of a cut unit is in slot 1, the others in slot 0)
+    int64_t p_step_l, p_step_o, o_step_l, o_step_o, o_fix_l, o_fix_o;
+    int n_pre, n;          // prefix parts, all parts
+    int p_col, o_col;      // floats between groups of four columns
+};
+
+// Row (token t, KV head h, place j in the group); `info` as note_row wrote it.
+__device__ __forceinline__ Parts row_parts(const PagedArgs& a, int t, int h, int j, uint2 info) {
+    Parts p{};
+    const int64_t row = (int64_t)t * a.Hq + h * a.g + j;
+    if (a.prefix_len > 0) {
+        const int R = t * a.g + j, nrt = (a.n_tokens * a.g + a.p_rows - 1) / a.p_rows, rt = R / a.p_rows;
+        const int r = R - rt * a.p_rows;
+        const int64_t slot = ((int64_t)h * nrt + rt) * a.p_split;
+        const bool groups = a.p_rows >= 128;
+        p.n_pre = a.p_split;
+        p.pl = a.pslot_l + slot * a.p_rows + r;
+        p.po = a.pslot_o + slot * a.p_rows * a.d + (groups ? r * 4 : r * a.d);
+        p.p_step_l = a.p_rows;
+        p.p_step_o = (int64_t)a.p_rows * a.d;
+        p.p_col = groups ? a.p_rows * 4 : 4;
     }
-    grid_dependency_wait();  // all above needs nothing that a kernel before this one writes
-    const uint2 info = in ? a.row_info[row] : make_uint2(kRowDone, 0);
+    p.n = p.n_pre;
+    p.o_col = 4;
     const uint32_t kind = info.x & 3u;
-    if (WPR == 1 && kind == kRowDone) return;
-    if (kind == kRowDone) n_pre = 0;
-    const float *oo = a.slot_o, *ol = a.slot_l;
-    int n_own = 0;
-    int64_t o0 = 0, o1 = 0;  // slot 1 of the unit's first CTA, then slot 0 of those after it
     if (kind == kRowWhole) {
-        oo = a.own_o;
-        ol = a.own_lse;
-        n_own = 1;
-        o0 = row;
+        p.n += 1;
+        p.oo = a.own_o + row * a.d;
+        p.ol = a.own_lse + row;
     } else if (kind == kRowSplit) {
         const int c0 = info.y & 0xffffu, c1 = info.y >> 16, r = info.x >> 2;
-        n_own = c1 - c0 + 1;
-        o0 = ((int64_t)c0 * 2 + 1) * a.rows + r;
-        o1 = ((int64_t)c0 * 2) * a.rows + r;
+        const bool groups = a.rows >= 128;
+        p.n += c1 - c0 + 1;
+        p.ol = a.slot_l + ((int64_t)c0 * 2 + 1) * a.rows + r;
+        p.oo = a.slot_o + ((int64_t)c0 * 2 + 1) * a.rows * a.d + (groups ? r * 4 : r * a.d);
+        p.o_step_l = 2 * a.rows;
+        p.o_step_o = (int64_t)2 * a.rows * a.d;
+        p.o_fix_l = -a.rows;
+        p.o_fix_o = -(int64_t)a.rows * a.d;
+        p.o_col = groups ? a.rows * 4 : 4;
     }
-    const int n = n_pre + n_own;
-    auto lse_of = [&](int c) -> float {
-        if (c < n_pre) return a.pslot_l[c ? p1 + (int64_t)c * 2 * a.p_rows : p0];
-        c -= n_pre;
-        return ol[c ? o1 + (int64_t)c * 2 * a.rows : o0];
-    };
-    auto out_of = [&](int c) -> const float* {
-        if (c < n_pre) return a.pslot_o + (c ? p1 + (int64_t)c * 2 * a.p_rows : p0) * D;
-        c -= n_pre;
-        return oo + (c ? o1 + (int64_t)c * 2 * a.rows : o0) * D;
-    };
-    float mx = -INFINITY;
-    for (int c = lane; c < n; c += 32) mx = fmaxf(mx, lse_of(c));
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-    const float ms = mx == -INFINITY ? 0.f : mx;
-    float acc[V], sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    for (int c0 = w; c0 < n; c0 += WPR * kAhead) {
-        float x[kAhead][V], f[kAhead];
+    return p;
+}
+__device__ __forceinline__ float part_lse(const Parts& p, int c) {
+    if (c < p.n_pre) return __ldcg(p.pl + c * p.p_step_l);
+    c -= p.n_pre;
+    return __ldcg(p.ol + c * p.o_step_l + (c ? p.o_fix_l : 0));
+}
+// columns 4 * c4 .. of part c
+__device__ __forceinline__ float4 part_cols(const Parts& p, int c, int c4) {
+    if (c < p.n_pre) return __ldcg(reinterpret_cast<const float4*>(p.po + c * p.p_step_o + c4 * p.p_col));
+    c -= p.n_pre;
+    return __ldcg(reinterpret_cast<const float4*>(p.oo + c * p.o_step_o + (c ? p.o_fix_o : 0) + c4 * p.o_col));
+}
+
+__device__ __forceinline__ void put4(float* p, const float4& x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void put4(__nv_bfloat16* p, const float4& x) {
+    uint2 w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(x.y), "f"(x.x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x.w), "f"(x.z));
+    *reinterpret_cast<uint2*>(p) = w;
+}
+
+// A CTA joins ROWS = 8 or 1 neighbouring rows of a KV head: thread = (row, four columns, every WAYS-th part), with a
+// running maximum, four parts' reads in flight.  With eight rows the reads of slots kept in column groups are 128 contiguous
+// bytes (a row at a time they would be 16).  A call of few rows has many parts per row, 38 for one sequence of 128K tokens,
+// and is bound by the latency of the reads, so it takes more ways: one after the other these took 15 us.  With few parts
+// per row more ways only cost: 21.9 us against 13.7 for five parts of 6400 rows.
+template <typename T, int D, int ROWS, int NT>
+__global__ void __launch_bounds__(NT) paged_merge_kernel(const PagedArgs a) {
+    constexpr int kCols = D / 4, kWays = NT / (kCols * ROWS), kAhead = 4;
+    __shared__ float4 s_acc[kWays > 1 ? NT : 1];
+    __shared__ float2 s_stat[kWays > 1 ? NT : 1];
+    const int r = threadIdx.x % ROWS, c4 = threadIdx.x / ROWS % kCols, way = threadIdx.x / (ROWS * kCols);
+    const int h = blockIdx.y, R = blockIdx.x * ROWS + r, t = R / a.g, j = R - t * a.g;
+    const bool in = R < a.n_tokens * a.g;
+    const int64_t row = (int64_t)t * a.Hq + h * a.g + j;
+    grid_dependency_wait();
+    const uint2 info = in ? __ldcg(a.row_info + row) : make_uint2(kRowDone, 0);
+    const bool done = (info.x & 3u) == kRowDone;
+    Parts p{};
+    if (!done) p = row_parts(a, t, h, j, info);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f, mx = -INFINITY;
+    for (int c0 = way; c0 < p.n; c0 += kWays * kAhead) {
+        float4 x[kAhead];
+        float f[kAhead], m = mx;
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int c = c0 + u * WPR;
-            f[u] = c < n ? lse_of(c) : -INFINITY;
-            const float* src = out_of(c < n ? c : c0) + lane * V;
-#pragma unroll
-            for (int e = 0; e < V; ++e) x[u][e] = src[e];
+            const int c = c0 + u * kWays;
+            f[u] = c < p.n ? part_lse(p, c) : -INFINITY;
+            x[u] = part_cols(p, c < p.n ? c : c0, c4);
         }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) m = fmaxf(m, f[u]);
+        const float ms = m == -INFINITY ? 0.f : m, al = exp2f(mx - ms);
+        mx = m;
+        sum *= al;
+        acc = make_float4(acc.x * al, acc.y * al, acc.z * al, acc.w * al);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const float g = exp2f(f[u] - ms);
-            sum += g;
-#pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] = fmaf(g, x[u][e], acc[e]);
+            const float w = exp2f(f[u] - ms);
+            sum += w;
+            acc.x = fmaf(w, x[u].x, acc.x);
+            acc.y = fmaf(w, x[u].y, acc.y);
+            acc.z = fmaf(w, x[u].z, acc.z);
+            acc.w = fmaf(w, x[u].w, acc.w);
         }
     }
-    if constexpr (WPR > 1) {
-        if (lane == 0) s_sum[warp] = sum;
-#pragma unroll
-        for (int e = 0; e < V; ++e) s_acc[warp][lane * V + e] = acc[e];
+    if constexpr (kWays > 1) {
+        s_acc[threadIdx.x] = acc;
+        s_stat[threadIdx.x] = make_float2(mx, sum);
         __syncthreads();
-        if (w != 0 || kind == kRowDone) return;
+        if (way != 0) return;
 #pragma unroll
-        for (int x = 1; x < WPR; ++x) {
-            sum += s_sum[warp + x];
+        for (int w = 1; w < kWays; ++w) mx = fmaxf(mx, s_stat[threadIdx.x + w * ROWS * kCols].x);
+        const float ms = mx == -INFINITY ? 0.f : mx;
+        sum = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] += s_acc[warp + x][lane * V + e];
+        for (int w = 0; w < kWays; ++w) {
+            const float4 y = s_acc[threadIdx.x + w * ROWS * kCols];
+            const float2 z = s_stat[threadIdx.x + w * ROWS * kCols];
+            const float f = exp2f(z.x - ms);
+            sum = fmaf(f, z.y, sum);
+            acc.x = fmaf(f, y.x, acc.x);
+            acc.y = fmaf(f, y.y, acc.y);
+            acc.z = fmaf(f, y.z, acc.z);
+            acc.w = fmaf(f, y.w, acc.w);
         }
     }
+    if (done) return;
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    T* out = static_cast<T*>(a.o) + row * D + lane * V;
-#pragma unroll
-    for (int e = 0; e < V; ++e) put(out + e, acc[e] * inv);
-    if (lane == 0) a.lse[row] = sum > 0.f ? (ms + log2f(sum)) * kLn2 : -INFINITY;
+    put4(static_cast<T*>(a.o) + row * D + c4 * 4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    if (c4 == 0) a.lse[row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
-// The kernel for `rows` rows per KV head: rows of a unit, keys of a tile, CTAs that run at a time.
+// The kernel for `rows` rows per KV head: rows of a unit, keys of a tile, CTAs that run at a time, and what beginning and
+// ending a unit costs in tiles.
 struct Pick {
-    int rows, keys, ctas;
+    int rows, keys, ctas, piece;
 };
 static Pick pick(const PagedArgs& a, int64_t rows) {
-    if (a.elem == 4) return {8, 64, kSms};
-    if (rows <= 32) return {rows <= 16 ? 16 : 32, 64, kSms * 2};
-    return {rows <= 128 ? 128 : 256, 128, kSms};
+    if (a.elem == 4) return {8, 64, kSms, 2};
+    if (rows <= 32) return {rows <= 16 ? 16 : 32, 64, kSms * 2, 2};
+    return {rows <= 128 ? 128 : 256, 128, kSms, 3};
 }
 
 size_t paged_plan(PagedArgs* a, int max_q, void* ws) {
@@ -140,17 +178,22 @@ size_t paged_plan(PagedArgs* a, int max_q, void* ws) {
     const Pick own = pick(*a, (int64_t)max_q * a->g);
     a->rows = own.rows;
     a->ctas = own.ctas;
-    a->p_rows = a->p_ctas = a->p_keys = 0;
+    a->p_rows = a->p_ctas = a->p_split = 0;
     if (a->prefix_len > 0) {
         const int64_t batch = (int64_t)a->n_tokens * a->g;
         const Pick pre = pick(*a, batch);
         a->p_rows = pre.rows;
-        a->p_keys = pre.keys;
-        // no share longer than a unit, so that it touches two units at most: one slot each; none empty; whole waves
-        const int64_t units = (batch + pre.rows - 1) / pre.rows * a->Hkv;
-        const int64_t tiles = units * ((a->prefix_len + pre.keys - 1) / pre.keys);
-        const int64_t waves = (units + pre.ctas - 1) / pre.ctas;
-        a->p_ctas = (int)std::min(tiles, waves * pre.ctas);
+        // Parts of a unit: few waves of CTAs, each of few tiles and the cost of a piece.
+        const int64_t units = (batch + pre.rows - 1) / pre.rows * a->Hkv, tiles = (a->prefix_len + pre.keys - 1) / pre.keys;
+        int64_t best = INT64_MAX;
+        for (int64_t k = 1; k <= tiles && k <= 4 * pre.ctas && (k == 1 || units * k <= 16 * pre.ctas); ++k) {
+            const int64_t cost = (units * k + pre.ctas - 1) / pre.ctas * ((tiles + k - 1) / k + pre.piece);
+            if (cost < best) {
+                best = cost;
+                a->p_split = (int)k;
+            }
+        }
+        a->p_ctas = (int)(units * a->p_split);
     }
     size_t at = 0;
     char* w = static_cast<char*>(ws);
@@ -166,8 +209,8 @@ size_t paged_plan(PagedArgs* a, int max_q, void* ws) {
     if (a->prefix_len > 0) {
         a->own_o = reinterpret_cast<float*>(take((size_t)rows * a->d * 4));
         a->own_lse = reinterpret_cast<float*>(take((size_t)rows * 4));
-        a->pslot_o = reinterpret_cast<float*>(take((size_t)a->p_ctas * 2 * a->p_rows * a->d * 4));
-        a->pslot_l = reinterpret_cast<float*>(take((size_t)a->p_ctas * 2 * a->p_rows * 4));
+        a->pslot_o = reinterpret_cast<float*>(take((size_t)a->p_ctas * a->p_rows * a->d * 4));
+        a->pslot_l = reinterpret_cast<float*>(take((size_t)a->p_ctas * a->p_rows * 4));
     }
     return at;
 }
@@ -184,10 +227,15 @@ cudaError_t launch_paged_prefix(const PagedArgs& a, cudaStream_t stream) {
 
 template <typename T, int D>
 static cudaError_t merge_t(const PagedArgs& a, cudaStream_t stream) {
-    // few rows have many parts each (a batch of any size is cut into as many shares as there are CTAs)
-    const int64_t rows = (int64_t)a.n_tokens * a.Hq;
-    if (rows <= 8 * kSms) return launch_dependent(paged_merge_kernel<T, D, 8>, (unsigned)rows, 256, 0, stream, a);
-    return launch_dependent(paged_merge_kernel<T, D, 1>, (unsigned)((rows + 7) / 8), 256, 0, stream, a);
+    const int batch = a.n_tokens * a.g;
+    if ((int64_t)batch * a.Hkv <= 8 * kSms)
+        return launch_dependent(paged_merge_kernel<T, D, 1, 512>, dim3(batch, a.Hkv), 512, 0, stream, a);
+    // parts of a row: those of the prefix, and own ones as equal shares give them
+    const int units = a.Hkv * std::max(a.n_seqs, (batch + a.rows - 1) / a.rows);
+    const dim3 grid((batch + 7) / 8, a.Hkv);
+    if (a.p_split + a.ctas / units > 8)
+        return launch_dependent(paged_merge_kernel<T, D, 8, 1024>, grid, 1024, 0, stream, a);
+    return launch_dependent(paged_merge_kernel<T, D, 8, 256>, grid, 256, 0, stream, a);
 }
 
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream) {

@@ -242,11 +242,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
         }
         __syncthreads();
     };
-    Seg g;
     if constexpr (PREFIX) {
-        PrefixWalk<M, kKeyTile> walk(a, cta);
-        while (walk.next(g)) piece(g);
+        piece(prefix_piece<M, kKeyTile>(a, cta));
     } else {
+        Seg g;
         OwnWalk<M, kKeyTile, kPieceCost> walk(a, share);
         while (walk.next(g)) piece(g);
         grid_dependency_wait();  // ends after the prefix kernel: the merge after this one sees both

@@ -157,8 +157,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
         Seg g;
         if constexpr (PREFIX) {
-            PrefixWalk<M, kKeyTile> walk(a, cta);
-            while (walk.next(g) && piece(g)) {}
+            g = prefix_piece<M, kKeyTile>(a, cta);
+            piece(g);
         } else {
             OwnWalk<M, kKeyTile, kPieceCost> walk(a, share);
             while (walk.next(g) && piece(g)) {}

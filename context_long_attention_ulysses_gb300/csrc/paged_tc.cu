@@ -5,10 +5,15 @@
 // 256 (two streams A and B that share every K/V tile); rows are (token, query head of the group) pairs, of one sequence or,
 // over a prefix, of the whole batch:
 //   warp 4 NS      TMA producer: K and V of each tile of 128 keys, page by page, into two rings
-//   warp 4 NS + 1  TMEM owner and single-thread tcgen05.mma issuer, per tile j: PV_A(j), QK_A(j+1), PV_B(j), QK_B(j+1)
+//   warps 4 NS + 1 (and + 2)  one thread each issues its stream's tcgen05.mma: QK(0), then PV(j), QK(j+1) per tile (the
+//                  first of these warps owns the TMEM)
 //   warps 0-3 (A), 4-7 (B)  Q rows into shared memory, softmax (thread = row = TMEM lane; log2 domain, O rescaled only when
 //                  the maximum grows by more than 2^8), normalisation, stores
-// With two streams the tensor core runs one stream's products while the other's softmax works.  A CTA walks its share
+// With two streams the tensor core runs one stream's products while the other's softmax works.  Each stream has an issuer of
+// its own, and they take turns, QK(0) and then [PV(j), QK(j+1)] being a turn: while one's products run, the other does its
+// waits and the commits of its last turn.  (One issuer for both streams spent 1470 of the 3517 clocks of a tile in those,
+// with nothing queued; two issuers without turns mix the streams' products, both softmaxes then work at the same time and
+// the tensor core waits for both: 1991 us against 1570 for 2048 rows at 64K.)  A CTA walks its share
 // piece by piece (paged.cuh); the rings run on across pieces, so the next piece's keys arrive during the epilogue.
 // TMEM columns: S_A [0,128), S_B [128,256), O_A [256,256+D), O_B [384,384+D); P (bf16) lies over its own S.
 #include <cmath>
@@ -43,7 +48,7 @@ struct Cfg {
     static constexpr int kOffK = NS * kTileBytes;
     static constexpr int kOffV = kOffK + kKStages * kTileBytes;
     static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
-    static constexpr int kBars = 2 * kKStages + 2 * kVStages + 4 * NS + 1 + 2 * kSegs;
+    static constexpr int kBars = 2 * kKStages + 2 * kVStages + 5 * NS + 1 + 2 * kSegs;
     static constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
 };
 
@@ -72,23 +77,25 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
     auto BAR = [&](int i) { return sbase + C::kOffBar + 8u * (uint32_t)i; };
     const int kKFull = 0, kKEmpty = KS, kVFull = 2 * KS, kVEmpty = kVFull + VS;
     const int kQFull = kVEmpty + VS, kSFull = kQFull + NS, kPReady = kSFull + NS, kOReady = kPReady + NS;  // per stream
-    const int kDrain = kOReady + NS, kSegFull = kDrain + 1, kSegEmpty = kSegFull + kSegs;
+    const int kTurn = kOReady + NS;  // per stream: its issuer may issue
+    const int kDrain = kTurn + NS, kSegFull = kDrain + 1, kSegEmpty = kSegFull + kSegs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
     constexpr int kProducer = 4 * NS, kIssuer = 4 * NS + 1;
     let_dependents_start();
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
-        for (int s = 0; s < KS; ++s) { mbar_init(BAR(kKFull + s), 1); mbar_init(BAR(kKEmpty + s), 1); }
-        for (int s = 0; s < VS; ++s) { mbar_init(BAR(kVFull + s), 1); mbar_init(BAR(kVEmpty + s), 1); }
+        for (int s = 0; s < KS; ++s) { mbar_init(BAR(kKFull + s), 1); mbar_init(BAR(kKEmpty + s), NS); }
+        for (int s = 0; s < VS; ++s) { mbar_init(BAR(kVFull + s), 1); mbar_init(BAR(kVEmpty + s), NS); }
         for (int st = 0; st < NS; ++st) {
             mbar_init(BAR(kQFull + st), 128);
             mbar_init(BAR(kSFull + st), 1);
             mbar_init(BAR(kPReady + st), 128);
             mbar_init(BAR(kOReady + st), 1);
+            mbar_init(BAR(kTurn + st), 1);
         }
-        mbar_init(BAR(kDrain), 1);
-        for (int s = 0; s < kSegs; ++s) { mbar_init(BAR(kSegFull + s), 1); mbar_init(BAR(kSegEmpty + s), 4 * NS + 1); }
+        mbar_init(BAR(kDrain), NS);
+        for (int s = 0; s < kSegs; ++s) { mbar_init(BAR(kSegFull + s), 1); mbar_init(BAR(kSegEmpty + s), 5 * NS); }
         fence_mbar_init();
     }
     if (warp == kIssuer) {
@@ -179,8 +186,8 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
             Seg g;
             bool ok = true;
             if constexpr (PREFIX) {
-                PrefixWalk<M, kKeyTile> walk(a, cta);
-                while (ok && walk.next(g)) ok = piece(g);
+                g = prefix_piece<M, kKeyTile>(a, cta);
+                ok = piece(g);
             } else {
                 OwnWalk<M, kKeyTile, kPieceCost> walk(a, share);
                 // The end of a unit that an earlier CTA began comes last.  All shares being equally long, the CTAs of a
@@ -204,73 +211,64 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                 drain_ring(BAR(kKFull), KS, it, 33, a.status);
                 drain_ring(BAR(kVFull), VS, nv, 34, a.status);
             }
-        } else if (warp == kIssuer && lane == 0) {
+        } else if (warp < kIssuer + NS && lane == 0) {
             // ---------------------------------------------------------------- MMA issuer
             constexpr uint32_t kIdS = idesc_bf16(128, kKeyTile, 0, 0);  // S = Q K^T, both K-major
             constexpr uint32_t kIdO = idesc_bf16(128, D, 0, 1);         // O += P V, V MN-major
-            int base = 0, cnt[NS] = {}, pieces[NS] = {};  // tiles so far; tiles and pieces of each stream
-            auto issue_qk = [&](int st, int it) {
-                const uint64_t dq = sdesc_sw128(sbase + C::kOffQ + st * C::kTileBytes, 16, 1024);
-                const uint64_t dk = sdesc_sw128(sbase + C::kOffK + (it % KS) * C::kTileBytes, 16, 1024);
+            const int st = warp - kIssuer;
+            const uint64_t dq = sdesc_sw128(sbase + C::kOffQ + st * C::kTileBytes, 16, 1024),
+                           dk0 = sdesc_sw128(sbase + C::kOffK, 16, 1024), dv0 = sdesc_sw128(sbase + C::kOffV, 16384, 1024);
+            const uint32_t s_col = tmem + st * 128, o_col = tmem + 256 + st * 128;
+            int base = 0;                           // tiles so far
+            uint32_t cnt = 0, pieces = 0, turn = 0; // tiles, pieces and turns of this stream so far
+            // A turn: the product PV of tile j and QK of tile j + 1, for a piece of n_tiles tiles of which this stream sees the
+            // first nt (j = -1: the first QK only); false: a wait gave up.  A tile that the stream does not see is released,
+            // once it is there, without a product.
+            auto do_turn = [&](int j, int n_tiles, int nt) {
+                const bool has_v = j >= 0, has_k = j + 1 < n_tiles, pv = has_v && j < nt, qk = has_k && j + 1 < nt;
+                const int iv = base + j, ik = iv + 1, vs = iv % VS, ks = ik % KS;
+                if (has_v && !mbar_wait(BAR(kVFull + vs), (iv / VS) & 1, abort_p, 37, a.status)) return false;
+                if (has_k && !mbar_wait(BAR(kKFull + ks), (ik / KS) & 1, abort_p, 36, a.status)) return false;
+                if (pv && !mbar_wait(BAR(kPReady + st), (cnt + j) & 1, abort_p, 38, a.status)) return false;
+                if (NS == 2 && (st == 1 || turn > 0) &&
+                    !mbar_wait(BAR(kTurn + st), (turn - 1 + st) & 1, abort_p, 46, a.status))
+                    return false;
+                ++turn;
+                tc_fence_after();
+                if (pv) {
+                    const uint64_t dv = dv0 + (uint32_t)(vs * C::kTileBytes >> 4);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
-                    mma_ss(tmem + st * 128, dq + off, dk + off, kIdS, kk > 0);
+                    for (int kk = 0; kk < kKeyTile / 16; ++kk)
+                        mma_ts(o_col, s_col + kk * 8, dv + (kk * 2048 >> 4), kIdO, (j > 0 || kk > 0) ? 1u : 0u);
                 }
-                mma_commit(BAR(kSFull + st));
+                if (qk) {  // in issue order after the product that read P from the columns of S
+                    const uint64_t dk = dk0 + (uint32_t)(ks * C::kTileBytes >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
+                        mma_ss(s_col, dq + off, dk + off, kIdS, kk > 0);
+                    }
+                }
+                if (NS == 2) mbar_arrive(BAR(kTurn + 1 - st));
+                if (qk) mma_commit(BAR(kSFull + st));
+                if (pv && j == nt - 1) mma_commit(BAR(kOReady + st));
+                if (has_v) { if (pv) mma_commit(BAR(kVEmpty + vs)); else mbar_arrive(BAR(kVEmpty + vs)); }
+                if (has_k) { if (qk) mma_commit(BAR(kKEmpty + ks)); else mbar_arrive(BAR(kKEmpty + ks)); }
+                return true;
             };
             for (int n_seg = 0;; ++n_seg) {
                 const int si = n_seg % kSegs;
                 if (!mbar_wait(BAR(kSegFull + si), (n_seg / kSegs) & 1, abort_p, 44, a.status)) break;
                 const int n_tiles = s_seg[si].n_tiles;
                 if (n_tiles == 0) break;
-                int nt[NS];
-                for (int st = 0; st < NS; ++st) nt[st] = stream_tiles(s_seg[si], st);
+                const int nt = stream_tiles(s_seg[si], st);
                 mbar_arrive(BAR(kSegEmpty + si));
-                bool ok = [&] {
-                for (int st = 0; st < NS; ++st) {
-                    if (nt[st] == 0) continue;
-                    if (!mbar_wait(BAR(kQFull + st), pieces[st] & 1, abort_p, 35, a.status)) return false;
-                    ++pieces[st];
-                }
-                if (!mbar_wait(BAR(kKFull + base % KS), (base / KS) & 1, abort_p, 36, a.status)) return false;
-                tc_fence_after();
-                for (int st = 0; st < NS; ++st)
-                    if (nt[st] > 0) issue_qk(st, base);
-                mma_commit(BAR(kKEmpty + base % KS));
-                for (int j = 0; j < n_tiles; ++j) {
-                    const int it = base + j, vs = it % VS, k1 = (it + 1) % KS;
-                    if (!mbar_wait(BAR(kVFull + vs), (it / VS) & 1, abort_p, 37, a.status)) return false;
-                    const uint64_t dv = sdesc_sw128(sbase + C::kOffV + vs * C::kTileBytes, 16384, 1024);
-                    bool k_waited = false;
-                    for (int st = 0; st < NS; ++st) {
-                        if (j >= nt[st]) continue;
-                        if (!mbar_wait(BAR(kPReady + st), (cnt[st] + j) & 1, abort_p, 38, a.status)) return false;
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < kKeyTile / 16; ++kk)
-                            mma_ts(tmem + 256 + st * 128, tmem + st * 128 + kk * 8, dv + (kk * 2048 >> 4), kIdO,
-                                   (j > 0 || kk > 0) ? 1u : 0u);
-                        if (j + 1 < nt[st]) {
-                            if (!k_waited) {
-                                if (!mbar_wait(BAR(kKFull + k1), ((it + 1) / KS) & 1, abort_p, 36, a.status))
-                                    return false;
-                                tc_fence_after();
-                                k_waited = true;
-                            }
-                            issue_qk(st, it + 1);  // in issue order after the product that read P from these columns
-                        } else {
-                            mma_commit(BAR(kOReady + st));
-                        }
-                    }
-                    mma_commit(BAR(kVEmpty + vs));
-                    if (k_waited) mma_commit(BAR(kKEmpty + k1));
-                }
-                return true;
-                }();
+                if (nt > 0 && !mbar_wait(BAR(kQFull + st), pieces++ & 1, abort_p, 35, a.status)) break;
+                bool ok = true;
+                for (int j = -1; ok && j < n_tiles; ++j) ok = do_turn(j, n_tiles, nt);
                 if (!ok) break;
                 base += n_tiles;
-                for (int st = 0; st < NS; ++st) cnt[st] += nt[st];
+                cnt += nt;
             }
             // every issued MMA completes before TMEM is freed (after an abort, too)
             mma_commit(BAR(kDrain));
@@ -293,24 +291,24 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
             const int r = st * 128 + row;
             const bool valid = r < g.n_rows;
             const int n_tiles = stream_tiles(g, st), tile0 = g.tile0;
-            const int first = PREFIX ? 0 : a.key_begin, end = seg_key_end<PREFIX>(a, g);
-            const int lim = valid ? row_limit<PREFIX>(a, g, r) : INT_MAX;
-            // (a warp without a valid row has its rows of V to clear, too)
-            const int lim_min = min(__reduce_min_sync(~0u, lim), end);
             if (n_tiles > 0) {  // this row of Q, swizzled as a TMA load would place it; rows beyond the unit are zero
                 const int R = g.row0 + r, i = R / a.g;
                 const uint4* src = reinterpret_cast<const uint4*>(
                     static_cast<const __nv_bfloat16*>(a.q) +
                     ((int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g)) * D);
                 uint8_t* dst = smem + C::kOffQ + st * C::kTileBytes + row * 128;
+                uint4 w[D / 8];
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 w = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(dst + (c / 8) * 16384 + (((c & 7) ^ (row & 7)) << 4)) = w;
-                }
+                for (int c = 0; c < D / 8; ++c) w[c] = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                    *reinterpret_cast<uint4*>(dst + (c / 8) * 16384 + (((c & 7) ^ (row & 7)) << 4)) = w[c];
                 fence_proxy_async_smem();
                 mbar_arrive(BAR(kQFull + st));
             }
+            const int lim = valid ? row_limit<PREFIX>(a, g, r) : INT_MAX;
+            // (a warp without a valid row has its rows of V to clear, too)
+            const int lim_min = min(__reduce_min_sync(~0u, lim), seg_key_end<PREFIX>(a, g));
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = 0; j < n_tiles; ++j) {
                 if (!warp_wait(BAR(kSFull + st), (cnt + j) & 1, 40)) return false;
@@ -320,6 +318,8 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                 tmem_ld32(scol + 32, r1r);
                 tmem_ld32(scol + 64, r2r);
                 tmem_ld32(scol + 96, r3r);
+                const int key0 = (tile0 + j) * kKeyTile;
+                const uint32_t live = s_boxes[(base + j) % kFlags] & all_boxes;
                 tmem_wait_ld();
                 float s[kKeyTile];
 #pragma unroll
@@ -329,19 +329,15 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                     s[64 + c] = __uint_as_float(r2r[c]);
                     s[96 + c] = __uint_as_float(r3r[c]);
                 }
-                const int key0 = (tile0 + j) * kKeyTile;
-                const uint32_t live = s_boxes[(base + j) % kFlags] & all_boxes;
-                if (key0 + kKeyTile > lim_min || key0 < first || live != all_boxes) {
-                    uint32_t boxes[4];
+                if (key0 + kKeyTile > lim_min || (!PREFIX && key0 < a.key_begin) || live != all_boxes) {
+                    const int first = PREFIX ? 0 : a.key_begin, end = seg_key_end<PREFIX>(a, g);
+                    const int lo = first - key0, hi = min(lim, end) - key0;
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
-                        boxes[w] = 0u;
+                        uint32_t see = 0u;
                         for (int b = 0; b < kKeyTile >> box_log2; ++b)
-                            if (live >> b & 1u) boxes[w] |= range_bits(b << box_log2, (b + 1) << box_log2, w);
-                    }
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t see = boxes[w] & range_bits(first - key0, min(lim, end) - key0, w);
+                            if (live >> b & 1u) see |= range_bits(b << box_log2, (b + 1) << box_log2, w);
+                        see &= range_bits(lo, hi, w);
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
                             if (!(see >> c & 1u)) s[32 * w + c] = -INFINITY;
@@ -411,7 +407,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
             const bool has = n_tiles > 0 && l_run > 0.f;
             const float inv = has ? 1.f / l_run : 0.f;
             const float lse2 = has ? m_run + log2f(l_run) : -INFINITY;
-            const RowDst dst = row_dst<M, PREFIX>(a, g, valid ? r : 0, cta);
+            const RowDst dst = row_dst<M, PREFIX, true>(a, g, valid ? r : 0, cta);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -435,10 +431,11 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                         y[e] = v;
                     }
                 } else if (valid) {
-                    float4* y = reinterpret_cast<float4*>(dst.part + c * 32);
+                    float* y = dst.part + c * 32 * dst.step;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        y[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                        *reinterpret_cast<float4*>(y + 4 * e * dst.step) =
+                            make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
                                            __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
                 }
             }
