@@ -168,8 +168,9 @@ struct Pick {
     int rows, keys, ctas, piece;
 };
 static Pick pick(const PagedArgs& a, int64_t rows) {
-    if (a.elem == 4) return {8, 64, kSms, 2};
-    if (rows <= 32) return {rows <= 16 ? 16 : 32, 64, kSms * 2, 2};
+    if (a.elem == 4) return {8, a.d == 64 ? 128 : 64, kSms, 2};
+    if (rows <= 16) return {16, 64, kSms * 2, 2};
+    if (rows <= 32) return {32, 64, kSms, 4};
     return {rows <= 128 ? 128 : 256, 128, kSms, 3};
 }
 

@@ -1,11 +1,12 @@
 // Attention over a paged cache in float32, on CUDA cores (the tensor cores' tf32 would not keep float32's digits).
 //
 // With 8 rows per KV head a key costs 4 d 8 flops per 8 d bytes, within what the CUDA cores do at the memory's rate, so
-// the kernel is built around the loads as its bf16 sibling is: each of four warps owns 16 keys of a tile of 64 and streams
+// the kernel is built around the loads as its bf16 sibling is: each of eight warps owns 1024 / d keys of a tile and streams
 // them by itself through a ring of shared memory (cp.async, 16 bytes a lane; missing keys are filled with zeros), with a
-// running maximum, sum and output of its own; the four meet only where a piece ends.
-//   scores: two lanes per key, half of d each; a key's row is padded by 16 bytes, so that 8 lanes' 16-byte reads fall into
-//           different banks, and the rows of Q are read by all lanes at once
+// running maximum, sum and output of its own; the eight meet only where a piece ends.  (Four warps with twice the keys, one
+// per scheduler, left it waiting for its own instructions: 34 us for 16 sequences of up to 16000 tokens.)
+//   scores: d/32 lanes per key, 32 values each; a key's row is padded by 16 bytes, so that 8 lanes' 16-byte reads fall into
+//           different banks, and the rows of Q are read by all lanes of a part at once
 //   output: a lane holds d/32 columns; the probabilities go through shared memory to be read by all lanes
 // More rows are more units, each reading K and V again (through L2).
 #include <cmath>
@@ -16,20 +17,21 @@ namespace usp {
 
 namespace {
 
-constexpr int kKeyTile = 64;
-constexpr int kSub = 16;      // keys of a warp in a tile
-constexpr int kPieceCost = 2; // see paged.cuh
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kPieceCost = 2;  // see paged.cuh
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kRows = 8;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
 struct Cfg {
+    static constexpr int kParts = D / 32;                         // lanes per key in the scores
+    static constexpr int kSub = 32 / kParts;                      // keys of a warp in a tile
+    static constexpr int kKeyTile = kWarps * kSub;
     static constexpr int kKStride = D + 4;                        // floats per key of K in shared memory
     static constexpr int kStageFloats = kSub * (kKStride + D);    // K, V
-    static constexpr int kStages = D == 128 ? 3 : 6;              // about 130 KB in flight per SM
+    static constexpr int kStages = 3;                             // about 130 KB in flight per SM
     static constexpr int kOffJoin = kWarps * kStages * kStageFloats;
-    static constexpr int kOffQ = kOffJoin + kWarps * kRows * D;
+    static constexpr int kOffQ = kOffJoin + kWarps / 2 * kRows * D;
     static constexpr int kOffP = kOffQ + kRows * D;
     static constexpr int kOffStat = kOffP + kWarps * kSub * kRows;
     static constexpr int kFloats = kOffStat + 2 * kWarps * kRows;
@@ -47,14 +49,15 @@ template <int D, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs a) {
     using C = Cfg<D>;
     constexpr int M = kRows, V = D / 32, S = C::kStages, kVecs = D / 4;  // kVecs: 16-byte vectors of a row
+    constexpr int kSub = C::kSub, kKeyTile = C::kKeyTile;
     extern __shared__ __align__(16) float smem[];
     __shared__ Share share;
     __shared__ uint32_t s_live[kWarps][S];  // keys of the stage that exist
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
     let_dependents_start();
     if constexpr (!PREFIX) {
-        find_share<M, kKeyTile, kPieceCost, kThreads>(a, cta, a.ctas, &share);
-        finish_empty_rows<float, M, kKeyTile, kThreads>(a, cta, a.ctas);
+        find_share<M, C::kKeyTile, kPieceCost, kThreads>(a, cta, a.ctas, &share);
+        finish_empty_rows<float, M, C::kKeyTile, kThreads>(a, cta, a.ctas);
         __syncthreads();
     }
     float* ring = smem + warp * S * C::kStageFloats;
@@ -65,7 +68,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
     float* s_l = s_m + kWarps * M;
     const float* kp = static_cast<const float*>(a.k_pages);
     const float* vp = static_cast<const float*>(a.v_pages);
-    const int key = lane & (kSub - 1), part = lane >> 4;  // scores: this lane's key and half of d
+    constexpr uint32_t kAll = 0xffffffffu >> (32 - kSub);
+    const int key = lane % kSub, part = lane / kSub;  // scores: this lane's key and 32 of its values
 
     auto piece = [&](const Seg& g) {
         const int first = PREFIX ? 0 : a.key_begin, end = seg_key_end<PREFIX>(a, g);
@@ -103,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
             if (x < g.n_tiles) {
                 const int st = x % S;
                 const uint32_t k_dst = ring_addr + st * C::kStageFloats * 4, v_dst = k_dst + kSub * C::kKStride * 4;
-                const uint32_t live = __ballot_sync(~0u, row >= 0) & 0xffffu;
+                const uint32_t live = __ballot_sync(~0u, row >= 0) & kAll;
                 if (lane == 0) s_live[warp][st] = live;
                 if (live) {
 #pragma unroll
@@ -138,10 +142,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
                 float s[M];
 #pragma unroll
                 for (int r = 0; r < M; ++r) s[r] = 0.f;
-                const float* kr = ks + key * C::kKStride + part * (D / 2);
-                const float* qr = s_q + part * (D / 2);
+                const float* kr = ks + key * C::kKStride + part * 32;
+                const float* qr = s_q + part * 32;
 #pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
+                for (int c = 0; c < 8; ++c) {
                     const float4 k4 = *reinterpret_cast<const float4*>(kr + c * 4);
 #pragma unroll
                     for (int r = 0; r < M; ++r) {
@@ -153,16 +157,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
                     }
                 }
                 const int j = (g.tile0 + x) * kKeyTile + warp * kSub + key;
-                const bool masked = (live != 0xffffu) || (g.tile0 + x) * kKeyTile + (warp + 1) * kSub > lim_min;
+                const bool masked = (live != kAll) || (g.tile0 + x) * kKeyTile + (warp + 1) * kSub > lim_min;
                 float al[M];
                 bool grew = false;
 #pragma unroll
                 for (int r = 0; r < M; ++r) {
-                    s[r] += __shfl_xor_sync(~0u, s[r], 16);
+#pragma unroll
+                    for (int o = 16; o >= kSub; o >>= 1) s[r] += __shfl_xor_sync(~0u, s[r], o);
                     if (masked && (j >= lim[r] || !(live >> key & 1u))) s[r] = -INFINITY;
                     float mx = s[r];
 #pragma unroll
-                    for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+                    for (int o = kSub / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
                     const bool up = mx > m[r];
                     al[r] = up ? exp2f(m[r] - mx) : 1.f;
                     if (up) m[r] = mx;
@@ -198,30 +203,49 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
             __syncwarp();
         }
         copies_wait<0>();
-        // ---- join the four warps, normalise, store
+        // ---- join the warps (four and four through the same buffer), normalise, store
         float* s_join = smem + C::kOffJoin;
 #pragma unroll
         for (int r = 0; r < M; ++r) {
-            // both halves of the warp hold the same sums: add up 16 lanes
-            for (int o = 8; o; o >>= 1) l[r] += __shfl_xor_sync(~0u, l[r], o);
+            // the parts of a key hold the same sums: add up one lane per key
+            for (int o = kSub / 2; o; o >>= 1) l[r] += __shfl_xor_sync(~0u, l[r], o);
             if (lane == 0) {
                 s_m[warp * M + r] = m[r];
                 s_l[warp * M + r] = l[r];
             }
+            if (warp >= 4)
 #pragma unroll
-            for (int c = 0; c < V; ++c) s_join[(warp * M + r) * D + lane * V + c] = acc[r][c];
+                for (int c = 0; c < V; ++c) s_join[((warp - 4) * M + r) * D + lane * V + c] = acc[r][c];
+        }
+        __syncthreads();
+        if (warp < 4) {
+#pragma unroll
+            for (int r = 0; r < M; ++r) {
+                const float m2 = s_m[(warp + 4) * M + r], mx = fmaxf(m[r], m2), ms = mx == -INFINITY ? 0.f : mx;
+                const float f1 = exp2f(m[r] - ms), f2 = exp2f(m2 - ms);
+#pragma unroll
+                for (int c = 0; c < V; ++c) {
+                    float* y = s_join + (warp * M + r) * D + lane * V + c;
+                    *y = f1 * acc[r][c] + f2 * *y;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    s_m[warp * M + r] = mx;
+                    s_l[warp * M + r] = f1 * l[r] + f2 * s_l[(warp + 4) * M + r];
+                }
+            }
         }
         __syncthreads();
         for (int x = threadIdx.x; x < g.n_rows * kVecs; x += kThreads) {
             const int r = x / kVecs, c = x % kVecs * 4;
             float mx = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w * M + r]);
+            for (int w = 0; w < 4; ++w) mx = fmaxf(mx, s_m[w * M + r]);
             const float ms = mx == -INFINITY ? 0.f : mx;
             float sum = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < 4; ++w) {
                 const float f = exp2f(s_m[w * M + r] - ms);
                 const float4 y = *reinterpret_cast<const float4*>(s_join + (w * M + r) * D + c);
                 sum += f * s_l[w * M + r];

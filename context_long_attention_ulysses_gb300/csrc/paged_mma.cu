@@ -2,11 +2,12 @@
 //
 // With up to 32 rows per KV head the work is reading K and V once: 2 d bf16 values per key against 4 d M flops, 16 to 32
 // flops a byte, far below what the tensor cores could do with it.  So the kernel is built around the loads:
-//   warp 4       producer: every tile of 64 keys, K and V, comes by TMA from its pages into a ring of stages
-//   warps 0-3    16 keys of each tile each, for all M rows: S = Q K^T (m16n8k16, Q in registers or shared memory), the
-//                running maximum and sum of the softmax, O += P V -- no warp waits for another while keys go by; the four
-//                partial results are joined through shared memory where a piece ends.
-// Two CTAs per SM, so that one loads while the other joins, stores or begins a piece.
+//   last warp    producer: every tile of 64 keys, K and V, comes by TMA from its pages into a ring of stages
+//   4 MT warps   a group of four per 16 rows, each warp with 16 keys of each tile: S = Q K^T (m16n8k16, Q in registers), the
+//                running maximum and sum of the softmax, O += P V -- no warp waits for another while keys go by; a group's
+//                four partial results are joined through shared memory where a piece ends.
+// Up to 16 rows: two CTAs per SM, so that one loads while the other joins, stores or begins a piece.  Up to 32: one CTA with
+// twice the stages (four warps with 32 rows each, two CTAs, spilled: 123 us for five tokens of 16 sequences).
 //
 // The pool is one tensor map (column, KV head, token of the page, page); a box holds min(page_size, 64) tokens, so that a
 // tile is 1, 2 or 4 boxes per 64 columns, issued by as many lanes.  Boxes without a visible key, or of a page that the pool
@@ -23,26 +24,28 @@ namespace usp {
 namespace {
 
 constexpr int kKeyTile = 64;  // keys per tile
-// A piece's beginning and end (rows of Q, the join, the stores) cost about 3 to 4 us, a tile 1.5 us at the memory's rate.
-constexpr int kPieceCost = 2;
-constexpr int kConsumers = 4;
-constexpr int kThreads = 32 * (kConsumers + 1);
+// A piece's beginning and end (rows of Q, the join, the stores) cost about 3 us; a tile takes a CTA 1.5 us at the memory's
+// rate where two share the SM, 0.75 us where it has the SM to itself.
+template <int MT>
+constexpr int kPieceCost = MT == 1 ? 2 : 4;
+constexpr int kGroup = 4;  // warps that share 16 rows
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;  // log2 units: O is rescaled only when the maximum grows by more than 2^8
 
 template <int D, int MT>
 struct Cfg {
     static constexpr int M = 16 * MT;
-    static constexpr int kChunks = D / 64;
-    static constexpr int kTileBytes = kKeyTile * D * 2;       // K or V of a tile
-    static constexpr int kStages = D == 128 ? 3 : 6;          // 96 KB in flight per CTA, two CTAs per SM
-    static constexpr int kJoinStride = D + 8;                 // float32 per row: no bank conflicts between rows
-    static constexpr int kQStride = D * 2 + 16;               // bytes per row of Q in shared memory (MT = 2)
-    static constexpr int kJoinBytes = 16 * kJoinStride * 4;
-    static_assert(MT == 1 || 32 * kQStride <= kJoinBytes, "Q shares the join buffer");
+    static constexpr int kConsumers = kGroup * MT;
+    static constexpr int kThreads = 32 * (kConsumers + 1);
+    static constexpr int kCtasPerSm = MT == 1 ? 2 : 1;
+    static constexpr int kChunks = D / 64;                                    // 64-column boxes per row
+    static constexpr int kTileBytes = kKeyTile * D * 2;                       // K or V of a tile
+    static constexpr int kStages = (D == 128 ? 3 : 6) * (MT == 1 ? 1 : 2);    // 192 KB in flight per SM
+    static constexpr int kJoinStride = D + 8;                                 // float32 per row: rows in different banks
+    static constexpr int kJoinBytes = 16 * kJoinStride * 4;                   // per group
     static constexpr int kOffJoin = kStages * 2 * kTileBytes;
-    static constexpr int kOffStat = kOffJoin + kJoinBytes;    // m, sum, sum of rounded: 3 x [4][M]
-    static constexpr int kOffBar = kOffStat + 3 * kConsumers * M * 4;
+    static constexpr int kOffStat = kOffJoin + MT * kJoinBytes;               // per group m, sum, sum of rounded: 3 x [4][16]
+    static constexpr int kOffBar = kOffStat + MT * 3 * kGroup * 16 * 4;
     static constexpr int kSmem = kOffBar + 2 * (kStages + kSegs) * 8 + 1024;
 };
 
@@ -59,21 +62,23 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void bar_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory"); }
-// The same barrier, and whether all of them say yes.
-__device__ __forceinline__ bool bar_all_consumers(bool yes) {
+// Barrier of a group's warps, and the same with whether all of them say yes.
+__device__ __forceinline__ void bar_group(int group) {
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * kGroup) : "memory");
+}
+__device__ __forceinline__ bool bar_group_all(int group, bool yes) {
     uint32_t all;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(all) : "r"((uint32_t)yes), "n"(32 * kConsumers) : "memory");
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all) : "r"((uint32_t)yes), "r"(group + 1), "n"(32 * kGroup) : "memory");
     return all != 0;
 }
 
 template <int D, int MT, bool PREFIX>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
     paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const PagedArgs a) {
     using C = Cfg<D, MT>;
-    constexpr int M = C::M;
+    constexpr int M = C::M, kThreads = C::kThreads, kConsumers = C::kConsumers;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -100,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if constexpr (PREFIX) {
         __syncthreads();
     } else {
-        find_share<M, kKeyTile, kPieceCost, kThreads>(a, cta, a.ctas, &share);  // holds the barrier that publishes the set-up, too
+        find_share<M, kKeyTile, kPieceCost<MT>, kThreads>(a, cta, a.ctas, &share);  // holds the barrier that publishes the set-up, too
         finish_empty_rows<__nv_bfloat16, M, kKeyTile, kThreads>(a, cta, a.ctas);
         __syncthreads();
     }
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             g = prefix_piece<M, kKeyTile>(a, cta);
             piece(g);
         } else {
-            OwnWalk<M, kKeyTile, kPieceCost> walk(a, share);
+            OwnWalk<M, kKeyTile, kPieceCost<MT>> walk(a, share);
             while (walk.next(g) && piece(g)) {}
         }
         g.n_tiles = 0;
@@ -168,169 +173,122 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) drain_ring(full0, C::kStages, it, 22, a.status);  // every load has landed before the CTA exits
     } else {
         // ---------------------------------------------------------------- consumers
-        const int r0 = lane >> 2, c0 = (lane & 3) * 2;  // this lane's first row and column of a fragment
-        const int box_of_warp = warp * 16 / min(1 << a.page_log2, kKeyTile);
-        float* s_m = reinterpret_cast<float*>(smem + C::kOffStat);
-        float* s_l = s_m + kConsumers * M;
-        float* s_lr = s_l + kConsumers * M;
-        float* s_join = reinterpret_cast<float*>(smem + C::kOffJoin);
+        const int group = warp / kGroup, kw = warp % kGroup;  // rows 16 * group .., keys 16 * kw .. of each tile
+        const int r0 = lane >> 2, c0 = (lane & 3) * 2;        // this lane's first row and column of a fragment
+        const int box_of_warp = kw * 16 / min(1 << a.page_log2, kKeyTile);
+        float* s_m = reinterpret_cast<float*>(smem + C::kOffStat) + group * 3 * kGroup * 16;
+        float* s_l = s_m + kGroup * 16;
+        float* s_lr = s_l + kGroup * 16;
+        float* s_join = reinterpret_cast<float*>(smem + C::kOffJoin + group * C::kJoinBytes);
         // ldmatrix rows of this lane: K (key, 16-byte column) and V transposed
-        const int k_key = warp * 16 + ((lane >> 4) << 3) + (lane & 7), k_c = (lane >> 3) & 1;
-        const int v_key = warp * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), v_c = lane >> 4;
+        const int k_key = kw * 16 + ((lane >> 4) << 3) + (lane & 7), k_c = (lane >> 3) & 1;
+        const int v_key = kw * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), v_c = lane >> 4;
         int it = 0;
         bool ok = true;
         for (int n_seg = 0;; ++n_seg) {
             const int si = n_seg % kSegs;
             ok = ok && mbar_wait(seg_full0 + 8 * si, (n_seg / kSegs) & 1, abort_p, 25, a.status);
-            // (one answer for the four warps, which meet at barriers below; a wait that gives up within a piece lets its
+            // (one answer for the group's warps, which meet at barriers below; a wait that gives up within a piece lets its
             // warp run on to the next one without waiting)
-            if (!bar_all_consumers(ok)) break;
+            if (!bar_group_all(group, ok)) break;
             const Seg& g = s_seg[si];
             if (g.n_tiles == 0) break;
             const int first = PREFIX ? 0 : a.key_begin, end = seg_key_end<PREFIX>(a, g);
-            // ---- rows: Q, limits
-            uint32_t q[MT == 1 ? D / 16 : 1][4];
-            int lim[MT][2];
-            int lim_min = INT_MAX;
-            auto q_row = [&](int r) {
-                const int R = g.row0 + r, i = R / a.g;
-                return static_cast<const __nv_bfloat16*>(a.q) +
-                       ((int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g)) * D;
-            };
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const int r = t * 16 + hh * 8 + r0;
-                    lim[t][hh] = r < g.n_rows ? row_limit<PREFIX>(a, g, r) : INT_MAX;
-                    lim_min = min(lim_min, lim[t][hh]);
-                }
-            lim_min = __reduce_min_sync(~0u, lim_min);
-            if constexpr (MT == 1) {
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const bool live = hh * 8 + r0 < g.n_rows;
-                    const uint32_t* src = reinterpret_cast<const uint32_t*>(q_row(live ? hh * 8 + r0 : 0) + c0);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        q[kk][hh] = live ? __ldg(src + kk * 8) : 0u;
-                        q[kk][hh + 2] = live ? __ldg(src + kk * 8 + 4) : 0u;
-                    }
-                }
-            } else {
-                for (int x = threadIdx.x; x < M * (D / 8); x += 32 * kConsumers) {
-                    const int r = x / (D / 8), c = x % (D / 8);
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (r < g.n_rows) w = __ldg(reinterpret_cast<const uint4*>(q_row(r)) + c);
-                    *reinterpret_cast<uint4*>(smem + C::kOffJoin + r * C::kQStride + c * 16) = w;
-                }
-                bar_consumers();
-            }
-            float o[MT][D / 8][4], m[MT][2], l[MT][2], lr[MT][2];
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[t][n][e] = 0.f;
-                m[t][0] = m[t][1] = -INFINITY;
-                l[t][0] = l[t][1] = lr[t][0] = lr[t][1] = 0.f;
-            }
-            // ---- keys
             const int tile0 = g.tile0, n_tiles = g.n_tiles;
+            const bool rows_here = MT == 1 || group * 16 < g.n_rows;
+            // ---- rows: Q, limits
+            uint32_t q[D / 16][4];
+            int lim[2];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                const int r = group * 16 + hh * 8 + r0;
+                const bool live = r < g.n_rows;
+                const int R = g.row0 + (live ? r : 0), i = R / a.g;
+                const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                    static_cast<const __nv_bfloat16*>(a.q) +
+                    ((int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g)) * D + c0);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    q[kk][hh] = live ? __ldg(src + kk * 8) : 0u;
+                    q[kk][hh + 2] = live ? __ldg(src + kk * 8 + 4) : 0u;
+                }
+                lim[hh] = live ? row_limit<PREFIX>(a, g, r) : INT_MAX;
+            }
+            const int lim_min = __reduce_min_sync(~0u, min(lim[0], lim[1]));
+            float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+            // ---- keys
             for (int x = 0; x < n_tiles; ++x, ++it) {
                 const int st = it % C::kStages;
                 ok = ok && mbar_wait(full0 + 8 * st, (it / C::kStages) & 1, abort_p, 23, a.status);
                 ok = __all_sync(~0u, ok);
-                const int key0 = (tile0 + x) * kKeyTile + warp * 16;  // this warp's keys key0 .. key0 + 15
-                if (ok && key0 < end && key0 + 16 > first && (s_boxes[st] >> box_of_warp & 1u)) {
+                const int key0 = (tile0 + x) * kKeyTile + kw * 16;  // this warp's keys key0 .. key0 + 15
+                if (ok && rows_here && key0 < end && key0 + 16 > first && (s_boxes[st] >> box_of_warp & 1u)) {
                     const uint32_t kb = sbase + st * 2 * C::kTileBytes, vb = kb + C::kTileBytes;
-                    float s[MT][2][4];
+                    float s[2][4];
 #pragma unroll
-                    for (int t = 0; t < MT; ++t)
+                    for (int n = 0; n < 2; ++n)
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) s[t][n][e] = 0.f;
+                        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         uint32_t b[4];
                         ldsm4(kb + (kk / 4) * (kKeyTile * 128) + k_key * 128 +
                                   ((((kk & 3) * 2 + k_c) ^ (k_key & 7)) << 4), b);
-#pragma unroll
-                        for (int t = 0; t < MT; ++t) {
-                            if constexpr (MT == 1) {
-                                mma16816(s[t][0], q[kk], b[0], b[1]);
-                                mma16816(s[t][1], q[kk], b[2], b[3]);
-                            } else {
-                                uint32_t qa[4];
-                                ldsm4(sbase + C::kOffJoin + (t * 16 + (lane & 15)) * C::kQStride +
-                                          (kk * 2 + (lane >> 4)) * 16, qa);
-                                mma16816(s[t][0], qa, b[0], b[1]);
-                                mma16816(s[t][1], qa, b[2], b[3]);
-                            }
-                        }
+                        mma16816(s[0], q[kk], b[0], b[1]);
+                        mma16816(s[1], q[kk], b[2], b[3]);
                     }
                     // ---- masks: only where a key of these 16 is hidden from some row
                     uint32_t vm[2] = {~0u, ~0u};
-                    if (key0 + 16 > lim_min || key0 < first) {
-#pragma unroll
-                        for (int t = 0; t < MT; ++t)
-#pragma unroll
-                            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const int key = key0 + n * 8 + c0 + (e & 1);
-                                    if (key >= lim[t][e >> 1] || key < first) s[t][n][e] = -INFINITY;
-                                }
-                        // what lies beyond the sequence in its last page may be NaN: 0 * NaN must not reach O
+                    if (key0 + 16 > lim_min || key0 + 16 > end || key0 < first) {
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
                             const int key = key0 + n * 8 + c0;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (key + (e & 1) >= lim[e >> 1] || key + (e & 1) < first) s[n][e] = -INFINITY;
+                            // what lies beyond the sequence in its last page may be NaN: 0 * NaN must not reach O
                             if (key >= end || key < first) vm[n] &= 0xffff0000u;
                             if (key + 1 >= end || key + 1 < first) vm[n] &= 0x0000ffffu;
                         }
                     }
                     // ---- softmax
-                    uint32_t p[MT][4];
+                    uint32_t p[4];
+                    bool grew = false;
+                    float al[2];
 #pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        bool grew = false;
-                        float al[2];
+                    for (int hh = 0; hh < 2; ++hh) {
+                        float mx = fmaxf(fmaxf(s[0][2 * hh], s[0][2 * hh + 1]), fmaxf(s[1][2 * hh], s[1][2 * hh + 1]));
+                        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+                        mx *= a.scale_log2;
+                        const bool up = mx > m[hh] + kRescale;
+                        al[hh] = up ? ex2_approx(m[hh] - mx) : 1.f;
+                        if (up) m[hh] = mx;
+                        grew |= up;
+                        const float ms = m[hh] == -INFINITY ? 0.f : m[hh];
+                        const float e0 = ex2_approx(fmaf(s[0][2 * hh], a.scale_log2, -ms));
+                        const float e1 = ex2_approx(fmaf(s[0][2 * hh + 1], a.scale_log2, -ms));
+                        const float e2 = ex2_approx(fmaf(s[1][2 * hh], a.scale_log2, -ms));
+                        const float e3 = ex2_approx(fmaf(s[1][2 * hh + 1], a.scale_log2, -ms));
+                        p[hh] = pack_bf16(e0, e1);
+                        p[hh + 2] = pack_bf16(e2, e3);
+                        l[hh] = l[hh] * al[hh] + ((e0 + e1) + (e2 + e3));
+                        // O is divided by the sum of what the product below uses: the rounded probabilities
+                        const float f0 = __uint_as_float(p[hh] << 16), f1 = __uint_as_float(p[hh] & 0xffff0000u),
+                                    f2 = __uint_as_float(p[hh + 2] << 16), f3 = __uint_as_float(p[hh + 2] & 0xffff0000u);
+                        lr[hh] = lr[hh] * al[hh] + ((f0 + f1) + (f2 + f3));
+                    }
+                    if (__any_sync(~0u, grew)) {
 #pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) {
-                            float mx = fmaxf(fmaxf(s[t][0][2 * hh], s[t][0][2 * hh + 1]),
-                                             fmaxf(s[t][1][2 * hh], s[t][1][2 * hh + 1]));
-                            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-                            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-                            mx *= a.scale_log2;
-                            const bool up = mx > m[t][hh] + kRescale;
-                            al[hh] = up ? ex2_approx(m[t][hh] - mx) : 1.f;
-                            if (up) m[t][hh] = mx;
-                            grew |= up;
-                            const float ms = m[t][hh] == -INFINITY ? 0.f : m[t][hh];
-                            float e0 = ex2_approx(fmaf(s[t][0][2 * hh], a.scale_log2, -ms));
-                            float e1 = ex2_approx(fmaf(s[t][0][2 * hh + 1], a.scale_log2, -ms));
-                            float e2 = ex2_approx(fmaf(s[t][1][2 * hh], a.scale_log2, -ms));
-                            float e3 = ex2_approx(fmaf(s[t][1][2 * hh + 1], a.scale_log2, -ms));
-                            p[t][hh] = pack_bf16(e0, e1);
-                            p[t][hh + 2] = pack_bf16(e2, e3);
-                            l[t][hh] = l[t][hh] * al[hh] + ((e0 + e1) + (e2 + e3));
-                            // O is divided by the sum of what the product below uses: the rounded probabilities
-                            const float f0 = __uint_as_float(p[t][hh] << 16),
-                                        f1 = __uint_as_float(p[t][hh] & 0xffff0000u),
-                                        f2 = __uint_as_float(p[t][hh + 2] << 16),
-                                        f3 = __uint_as_float(p[t][hh + 2] & 0xffff0000u);
-                            lr[t][hh] = lr[t][hh] * al[hh] + ((f0 + f1) + (f2 + f3));
-                        }
-                        if (__any_sync(~0u, grew)) {
-#pragma unroll
-                            for (int n = 0; n < D / 8; ++n) {
-                                o[t][n][0] *= al[0];
-                                o[t][n][1] *= al[0];
-                                o[t][n][2] *= al[1];
-                                o[t][n][3] *= al[1];
-                            }
+                        for (int n = 0; n < D / 8; ++n) {
+                            o[n][0] *= al[0];
+                            o[n][1] *= al[0];
+                            o[n][2] *= al[1];
+                            o[n][3] *= al[1];
                         }
                     }
                     // ---- O += P V
@@ -339,108 +297,96 @@ __global__ void __launch_bounds__(kThreads, 2)
                         uint32_t b[4];
                         ldsm4t(vb + (nn / 4) * (kKeyTile * 128) + v_key * 128 +
                                    ((((nn & 3) * 2 + v_c) ^ (v_key & 7)) << 4), b);
-                        b[0] &= vm[0];
-                        b[1] &= vm[1];
-                        b[2] &= vm[0];
-                        b[3] &= vm[1];
-#pragma unroll
-                        for (int t = 0; t < MT; ++t) {
-                            mma16816(o[t][2 * nn], p[t], b[0], b[1]);
-                            mma16816(o[t][2 * nn + 1], p[t], b[2], b[3]);
-                        }
+                        mma16816(o[2 * nn], p, b[0] & vm[0], b[1] & vm[1]);
+                        mma16816(o[2 * nn + 1], p, b[2] & vm[0], b[3] & vm[1]);
                     }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty0 + 8 * st);
             }
-            // ---- join the four warps (in an order fixed per column quarter), normalise, store
+            // ---- join the group's four warps (in an order fixed per column quarter), normalise, store
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    float s1 = l[t][hh], s2 = lr[t][hh];
-                    s1 += __shfl_xor_sync(~0u, s1, 1);
-                    s2 += __shfl_xor_sync(~0u, s2, 1);
-                    s1 += __shfl_xor_sync(~0u, s1, 2);
-                    s2 += __shfl_xor_sync(~0u, s2, 2);
-                    if ((lane & 3) == 0) {
-                        const int r = warp * M + t * 16 + hh * 8 + r0;
-                        s_m[r] = m[t][hh];
-                        s_l[r] = s1;
-                        s_lr[r] = s2;
-                    }
+            for (int hh = 0; hh < 2; ++hh) {
+                float s1 = l[hh], s2 = lr[hh];
+                s1 += __shfl_xor_sync(~0u, s1, 1);
+                s2 += __shfl_xor_sync(~0u, s2, 1);
+                s1 += __shfl_xor_sync(~0u, s1, 2);
+                s2 += __shfl_xor_sync(~0u, s2, 2);
+                if ((lane & 3) == 0) {
+                    const int r = kw * 16 + hh * 8 + r0;
+                    s_m[r] = m[hh];
+                    s_l[r] = s1;
+                    s_lr[r] = s2;
                 }
-            bar_consumers();  // also: every warp is done with Q in the join buffer
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                float f[2];
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const int r = t * 16 + hh * 8 + r0;
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < kConsumers; ++w) mx = fmaxf(mx, s_m[w * M + r]);
-                    f[hh] = mx == -INFINITY ? 0.f : ex2_approx(m[t][hh] - mx);
-                }
-#pragma unroll
-                for (int round = 0; round < kConsumers; ++round) {
-                    const int part = (warp + round) % kConsumers;
-#pragma unroll
-                    for (int n = 0; n < D / 8; ++n)
-                        if (n / (D / 32) == part) {
-#pragma unroll
-                            for (int hh = 0; hh < 2; ++hh) {
-                                float2* dst = reinterpret_cast<float2*>(s_join + (hh * 8 + r0) * C::kJoinStride + n * 8 + c0);
-                                float2 w = round ? *dst : make_float2(0.f, 0.f);
-                                w.x += o[t][n][2 * hh] * f[hh];
-                                w.y += o[t][n][2 * hh + 1] * f[hh];
-                                *dst = w;
-                            }
-                        }
-                    bar_consumers();
-                }
-                // eight threads per row, D/8 columns each
-                const int rr = threadIdx.x >> 3, cc = (threadIdx.x & 7) * (D / 8), r = t * 16 + rr;
-                if (r < g.n_rows) {
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < kConsumers; ++w) mx = fmaxf(mx, s_m[w * M + r]);
-                    float sum = 0.f, sum_r = 0.f;
-#pragma unroll
-                    for (int w = 0; w < kConsumers; ++w) {
-                        const float e = mx == -INFINITY ? 0.f : ex2_approx(s_m[w * M + r] - mx);
-                        sum += e * s_l[w * M + r];
-                        sum_r += e * s_lr[w * M + r];
-                    }
-                    const bool has = sum_r > 0.f;
-                    const float inv = has ? 1.f / sum_r : 0.f;
-                    const float lse2 = has ? mx + log2f(sum) : -INFINITY;
-                    const float* src = s_join + rr * C::kJoinStride + cc;
-                    const RowDst dst = row_dst<M, PREFIX>(a, g, r, cta);
-                    if (dst.out) {
-                        uint4* w = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dst.out) + cc);
-#pragma unroll
-                        for (int e = 0; e < D / 64; ++e) {
-                            const float* y = src + e * 8;
-                            w[e] = has ? make_uint4(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv),
-                                                    pack_bf16(y[4] * inv, y[5] * inv), pack_bf16(y[6] * inv, y[7] * inv))
-                                       : make_uint4(0, 0, 0, 0);
-                        }
-                        if ((threadIdx.x & 7) == 0) *dst.lse = lse2 * kLn2;
-                    } else {
-                        float4* w = reinterpret_cast<float4*>(dst.part + cc);
-#pragma unroll
-                        for (int e = 0; e < D / 32; ++e) {
-                            const float* y = src + e * 4;
-                            w[e] = has ? make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv)
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-                        }
-                        if ((threadIdx.x & 7) == 0) *dst.lse = lse2;
-                    }
-                    if (!PREFIX && g.ends && (threadIdx.x & 7) == 0) note_row<M>(a, g, r, cta);
-                }
-                bar_consumers();  // the join buffer is free again
             }
+            bar_group(group);
+            float f[2];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kGroup; ++w) mx = fmaxf(mx, s_m[w * 16 + hh * 8 + r0]);
+                f[hh] = mx == -INFINITY ? 0.f : ex2_approx(m[hh] - mx);
+            }
+#pragma unroll
+            for (int round = 0; round < kGroup; ++round) {
+                const int part = (kw + round) % kGroup;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+                    if (n / (D / 32) == part) {
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            float2* dst = reinterpret_cast<float2*>(s_join + (hh * 8 + r0) * C::kJoinStride + n * 8 + c0);
+                            float2 w = round ? *dst : make_float2(0.f, 0.f);
+                            w.x += o[n][2 * hh] * f[hh];
+                            w.y += o[n][2 * hh + 1] * f[hh];
+                            *dst = w;
+                        }
+                    }
+                bar_group(group);
+            }
+            // eight threads per row, D/8 columns each
+            const int rr = (threadIdx.x % (32 * kGroup)) >> 3, cc = (threadIdx.x & 7) * (D / 8), r = group * 16 + rr;
+            if (r < g.n_rows) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kGroup; ++w) mx = fmaxf(mx, s_m[w * 16 + rr]);
+                float sum = 0.f, sum_r = 0.f;
+#pragma unroll
+                for (int w = 0; w < kGroup; ++w) {
+                    const float e = mx == -INFINITY ? 0.f : ex2_approx(s_m[w * 16 + rr] - mx);
+                    sum += e * s_l[w * 16 + rr];
+                    sum_r += e * s_lr[w * 16 + rr];
+                }
+                const bool has = sum_r > 0.f;
+                const float inv = has ? 1.f / sum_r : 0.f;
+                const float lse2 = has ? mx + log2f(sum) : -INFINITY;
+                const float* src = s_join + rr * C::kJoinStride + cc;
+                const RowDst dst = row_dst<M, PREFIX>(a, g, r, cta);
+                if (dst.out) {
+                    uint4* w = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dst.out) + cc);
+#pragma unroll
+                    for (int e = 0; e < D / 64; ++e) {
+                        const float* y = src + e * 8;
+                        w[e] = has ? make_uint4(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv),
+                                                pack_bf16(y[4] * inv, y[5] * inv), pack_bf16(y[6] * inv, y[7] * inv))
+                                   : make_uint4(0, 0, 0, 0);
+                    }
+                    if ((threadIdx.x & 7) == 0) *dst.lse = lse2 * kLn2;
+                } else {
+                    float4* w = reinterpret_cast<float4*>(dst.part + cc);
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) {
+                        const float* y = src + e * 4;
+                        w[e] = has ? make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                    if ((threadIdx.x & 7) == 0) *dst.lse = lse2;
+                }
+                if (!PREFIX && g.ends && (threadIdx.x & 7) == 0) note_row<M>(a, g, r, cta);
+            }
+            // (the next piece's first barrier comes before anyone writes the join buffer or the statistics again)
+            __syncwarp();
             if (lane == 0) mbar_arrive(seg_empty0 + 8 * si);
         }
     }
@@ -460,8 +406,8 @@ cudaError_t launch_t(const PagedArgs& a, cudaStream_t s) {
     auto kern = paged_mma_kernel<D, MT, PREFIX>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    if (!PREFIX) return launch_own(kern, a, kThreads, C::kSmem, s, tk, tv, a);
-    kern<<<a.p_ctas, kThreads, C::kSmem, s>>>(tk, tv, a);
+    if (!PREFIX) return launch_own(kern, a, C::kThreads, C::kSmem, s, tk, tv, a);
+    kern<<<a.p_ctas, C::kThreads, C::kSmem, s>>>(tk, tv, a);
     return cudaGetLastError();
 }
 
