@@ -6,12 +6,14 @@
 // running maximum, sum and output of its own; the eight meet only where a piece ends.  (Four warps with twice the keys, one
 // per scheduler, left it waiting for its own instructions: 34 us for 16 sequences of up to 16000 tokens.)
 //   scores: d/32 lanes per key, 32 values each; a key's row is padded by 16 bytes, so that 8 lanes' 16-byte reads fall into
-//           different banks, and the rows of Q are read by all lanes of a part at once
+//           different banks, and the rows of Q are read by all lanes of a part at once; the parts' sums are added such that
+//           each lane ends with the whole scores of 8 / parts rows, and does the softmax of those only
 //   output: a lane holds d/32 columns; the probabilities go through shared memory to be read by all lanes
 // More rows are more units, each reading K and V again (through L2).
 #include <cmath>
 
 #include "paged.cuh"
+#include "ptx.cuh"
 
 namespace usp {
 
@@ -33,7 +35,8 @@ struct Cfg {
     static constexpr int kOffJoin = kWarps * kStages * kStageFloats;
     static constexpr int kOffQ = kOffJoin + kWarps / 2 * kRows * D;
     static constexpr int kOffP = kOffQ + kRows * D;
-    static constexpr int kOffStat = kOffP + kWarps * kSub * kRows;
+    static constexpr int kOffScale = kOffP + kWarps * kSub * kRows;
+    static constexpr int kOffStat = kOffScale + kWarps * kRows;
     static constexpr int kFloats = kOffStat + 2 * kWarps * kRows;
 };
 
@@ -64,84 +67,104 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
     const uint32_t ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
     float* s_q = smem + C::kOffQ;
     float* s_p = smem + C::kOffP + warp * kSub * M;  // [key][row]
+    float* s_al = smem + C::kOffScale + warp * M;
     float* s_m = smem + C::kOffStat;
     float* s_l = s_m + kWarps * M;
     const float* kp = static_cast<const float*>(a.k_pages);
     const float* vp = static_cast<const float*>(a.v_pages);
     constexpr uint32_t kAll = 0xffffffffu >> (32 - kSub);
     const int key = lane % kSub, part = lane / kSub;  // scores: this lane's key and 32 of its values
+    constexpr int RL = M / C::kParts;                 // rows of the softmax per lane: row0 ..
+    const int row0 = C::kParts == 2 ? part * 4 : (part >> 1) * 4 + (part & 1) * 2;
 
-    auto piece = [&](const Seg& g) {
-        const int first = PREFIX ? 0 : a.key_begin, end = seg_key_end<PREFIX>(a, g);
-        // ---- rows
-        for (int x = threadIdx.x; x < M * D; x += kThreads) {
-            const int r = x / D, R = g.row0 + r, i = R / a.g;
-            s_q[x] = r < g.n_rows ? static_cast<const float*>(a.q)[((int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g)) * D +
-                                                                   x % D] * a.scale_log2
-                                  : 0.f;
-        }
-        int lim[M], lim_min = INT_MAX;
+    // Where this warp's keys of tile x of a piece lie (row of the pool, -1: no key).
+    auto locate = [&](const Seg& g, int x) -> int64_t {
+        const int j = (g.tile0 + x) * kKeyTile + warp * kSub + key;
+        if (j < (PREFIX ? 0 : a.key_begin) || j >= seg_key_end<PREFIX>(a, g)) return -1;
+        const int page = seg_page<PREFIX>(a, g, j >> a.page_log2);
+        if (page < 0) return -1;
+        return (((int64_t)page * a.Hkv + g.h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
+    };
+    // The copies run on across pieces, up to the end of the next one: `next_row` is where the tile to be issued next lies.
+    Seg cur, nxt;
+    bool has_nxt = false;
+    int it = 0, issued = 0;           // tiles worked on and tiles issued by this CTA so far
+    int ahead = 0;                    // tiles of the current piece (and then the next) that were issued
+    int64_t next_row = -1;
+    auto find_next = [&] {            // `ahead` is the tile to be issued next
+        const int y = ahead - cur.n_tiles;
+        next_row = y < 0 ? locate(cur, ahead) : has_nxt && y < nxt.n_tiles ? locate(nxt, y) : -1;
+    };
+    auto issue = [&] {                // one group of copies, if there is a tile
+        if (ahead >= cur.n_tiles + (has_nxt ? nxt.n_tiles : 0)) return;
+        const int st = issued % S;
+        const uint32_t k_dst = ring_addr + st * C::kStageFloats * 4, v_dst = k_dst + kSub * C::kKStride * 4;
+        const uint32_t live = __ballot_sync(~0u, next_row >= 0) & kAll;
+        if (lane == 0) s_live[warp][st] = live;
+        if (live) {
 #pragma unroll
-        for (int r = 0; r < M; ++r) {
-            lim[r] = r < g.n_rows ? row_limit<PREFIX>(a, g, r) : INT_MAX;
+            for (int i = 0; i < kSub * kVecs / 32; ++i) {
+                const int r = (i * 32 + lane) / kVecs, c = (i * 32 + lane) % kVecs;
+                const int64_t at = __shfl_sync(~0u, next_row, r);
+                const int64_t off = (at < 0 ? 0 : at) * D + c * 4;
+                copy16(k_dst + (r * C::kKStride + c * 4) * 4, kp + off, at >= 0);
+                copy16(v_dst + (r * D + c * 4) * 4, vp + off, at >= 0);
+            }
+        }
+        copies_commit();
+        ++issued;
+        ++ahead;
+        find_next();  // its page is on its way while the tile before is worked on
+    };
+
+    // Works through `cur`; then `nxt` becomes the current piece.
+    auto piece = [&] {
+        const Seg& g = cur;
+        while (issued < it + S - 1 && ahead < cur.n_tiles + (has_nxt ? nxt.n_tiles : 0)) issue();
+        // ---- rows
+        for (int x = threadIdx.x; x < M * kVecs; x += kThreads) {
+            const int r = x / kVecs, R = g.row0 + r, i = R / a.g;
+            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < g.n_rows) {
+                w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
+                                                          ((int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g)) * D) +
+                          x % kVecs);
+                w = make_float4(w.x * a.scale_log2, w.y * a.scale_log2, w.z * a.scale_log2, w.w * a.scale_log2);
+            }
+            reinterpret_cast<float4*>(s_q)[x] = w;
+        }
+        int lim[RL], lim_min = INT_MAX;
+#pragma unroll
+        for (int r = 0; r < RL; ++r) {
+            lim[r] = row0 + r < g.n_rows ? row_limit<PREFIX>(a, g, row0 + r) : INT_MAX;
             lim_min = min(lim_min, lim[r]);
         }
+        lim_min = __reduce_min_sync(~0u, lim_min);
         __syncthreads();
-        float acc[M][V], m[M], l[M];
+        // (packed float32: the scores sum two products, the output takes two rows at a time)
+        float2 acc[V][M / 2];
+        float m[RL], l[RL];
 #pragma unroll
-        for (int r = 0; r < M; ++r) {
+        for (int r = 0; r < RL; ++r) {
             m[r] = -INFINITY;
             l[r] = 0.f;
-#pragma unroll
-            for (int c = 0; c < V; ++c) acc[r][c] = 0.f;
         }
-        // ---- this warp's keys of tile x: where they lie (row of the pool, -1: no key)
-        auto locate = [&](int x) -> int64_t {
-            const int j = (g.tile0 + x) * kKeyTile + warp * kSub + key;
-            if (x >= g.n_tiles || j < first || j >= end) return -1;
-            const int page = seg_page<PREFIX>(a, g, j >> a.page_log2);
-            if (page < 0) return -1;
-            return (((int64_t)page * a.Hkv + g.h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
-        };
-        auto issue = [&](int x, int64_t row) {
-            if (x < g.n_tiles) {
-                const int st = x % S;
-                const uint32_t k_dst = ring_addr + st * C::kStageFloats * 4, v_dst = k_dst + kSub * C::kKStride * 4;
-                const uint32_t live = __ballot_sync(~0u, row >= 0) & kAll;
-                if (lane == 0) s_live[warp][st] = live;
-                if (live) {
 #pragma unroll
-                    for (int i = 0; i < kSub * kVecs / 32; ++i) {
-                        const int r = (i * 32 + lane) / kVecs, c = (i * 32 + lane) % kVecs;
-                        const int64_t at = __shfl_sync(~0u, row, r);
-                        const int64_t off = (at < 0 ? 0 : at) * D + c * 4;
-                        copy16(k_dst + (r * C::kKStride + c * 4) * 4, kp + off, at >= 0);
-                        copy16(v_dst + (r * D + c * 4) * 4, vp + off, at >= 0);
-                    }
-                }
-            }
-            copies_commit();
-        };
-        int64_t ahead = locate(0);
-        for (int x = 0; x < S - 1; ++x) {
-            const int64_t now = ahead;
-            ahead = locate(x + 1);
-            issue(x, now);
-        }
-        for (int x = 0; x < g.n_tiles; ++x) {
-            const int64_t now = ahead;
-            ahead = locate(x + S);  // its page is on its way while this tile is worked on
-            copies_wait<S - 2>();
+        for (int c = 0; c < V; ++c)
+#pragma unroll
+            for (int r = 0; r < M / 2; ++r) acc[c][r] = make_float2(0.f, 0.f);
+        for (int x = 0; x < g.n_tiles; ++x, ++it) {
+            if (issued - it >= S - 1) copies_wait<S - 2>(); else copies_wait<0>();
             __syncwarp();
-            issue(x + S - 1, now);  // into the stage that was read in the iteration before
-            const int st = x % S;
+            if (issued < it + S) issue();  // into the stage that was read in the iteration before
+            const int st = it % S;
             const uint32_t live = s_live[warp][st];
             if (live) {
                 const float* ks = ring + st * C::kStageFloats;
                 const float* vs = ks + kSub * C::kKStride;
-                float s[M];
+                float2 s2[M];
 #pragma unroll
-                for (int r = 0; r < M; ++r) s[r] = 0.f;
+                for (int r = 0; r < M; ++r) s2[r] = make_float2(0.f, 0.f);
                 const float* kr = ks + key * C::kKStride + part * 32;
                 const float* qr = s_q + part * 32;
 #pragma unroll 4
@@ -150,88 +173,118 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
 #pragma unroll
                     for (int r = 0; r < M; ++r) {
                         const float4 q4 = *reinterpret_cast<const float4*>(qr + r * D + c * 4);
-                        s[r] = fmaf(q4.x, k4.x, s[r]);
-                        s[r] = fmaf(q4.y, k4.y, s[r]);
-                        s[r] = fmaf(q4.z, k4.z, s[r]);
-                        s[r] = fmaf(q4.w, k4.w, s[r]);
+                        s2[r] = fma2(make_float2(q4.x, q4.y), make_float2(k4.x, k4.y), s2[r]);
+                        s2[r] = fma2(make_float2(q4.z, q4.w), make_float2(k4.z, k4.w), s2[r]);
                     }
                 }
-                const int j = (g.tile0 + x) * kKeyTile + warp * kSub + key;
-                const bool masked = (live != kAll) || (g.tile0 + x) * kKeyTile + (warp + 1) * kSub > lim_min;
-                float al[M];
+                // add the parts up, each step keeping half of the rows
+                float s4[M / 2], s[RL];
+                const bool hi = lane & 16;
+#pragma unroll
+                for (int r = 0; r < M / 2; ++r) {
+                    const float lo_sum = s2[r].x + s2[r].y, hi_sum = s2[r + M / 2].x + s2[r + M / 2].y;
+                    s4[r] = (hi ? hi_sum : lo_sum) + __shfl_xor_sync(~0u, hi ? lo_sum : hi_sum, 16);
+                }
+                if constexpr (C::kParts == 4) {
+                    const bool odd = lane & 8;
+#pragma unroll
+                    for (int r = 0; r < RL; ++r)
+                        s[r] = (odd ? s4[r + RL] : s4[r]) + __shfl_xor_sync(~0u, odd ? s4[r] : s4[r + RL], 8);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < RL; ++r) s[r] = s4[r];
+                }
+                const int key0 = (g.tile0 + x) * kKeyTile + warp * kSub;
+                if (live != kAll || key0 + kSub > lim_min) {
+#pragma unroll
+                    for (int r = 0; r < RL; ++r)
+                        if (key0 + key >= lim[r] || !(live >> key & 1u)) s[r] = -INFINITY;
+                }
+                float mx[RL];
                 bool grew = false;
 #pragma unroll
-                for (int r = 0; r < M; ++r) {
+                for (int r = 0; r < RL; ++r) {
+                    mx[r] = s[r];
 #pragma unroll
-                    for (int o = 16; o >= kSub; o >>= 1) s[r] += __shfl_xor_sync(~0u, s[r], o);
-                    if (masked && (j >= lim[r] || !(live >> key & 1u))) s[r] = -INFINITY;
-                    float mx = s[r];
+                    for (int o = kSub / 2; o; o >>= 1) mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], o));
+                    grew |= mx[r] > m[r];
+                }
+                if (__any_sync(~0u, grew)) {
 #pragma unroll
-                    for (int o = kSub / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-                    const bool up = mx > m[r];
-                    al[r] = up ? exp2f(m[r] - mx) : 1.f;
-                    if (up) m[r] = mx;
-                    grew |= up;
+                    for (int r = 0; r < RL; ++r) {
+                        const bool up = mx[r] > m[r];
+                        const float al = up ? exp2f(m[r] - mx[r]) : 1.f;
+                        if (up) m[r] = mx[r];
+                        l[r] *= al;
+                        if (key == 0) s_al[row0 + r] = al;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int r = 0; r < M / 2; ++r) {
+                        const float2 al = *reinterpret_cast<const float2*>(s_al + 2 * r);
+#pragma unroll
+                        for (int c = 0; c < V; ++c) acc[c][r] = mul2(acc[c][r], al);
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < RL; ++r) {
                     s[r] = exp2f(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
-                    l[r] = l[r] * al[r] + s[r];
-                }
-                if (part == 0) {
-#pragma unroll
-                    for (int r = 0; r < M; r += 4)
-                        *reinterpret_cast<float4*>(s_p + key * M + r) = make_float4(s[r], s[r + 1], s[r + 2], s[r + 3]);
-                }
-                if (grew) {  // the same for all lanes
-#pragma unroll
-                    for (int r = 0; r < M; ++r)
-#pragma unroll
-                        for (int c = 0; c < V; ++c) acc[r][c] *= al[r];
+                    l[r] += s[r];
+                    s_p[key * M + row0 + r] = s[r];
                 }
                 __syncwarp();
 #pragma unroll 4
                 for (int k = 0; k < kSub; ++k) {
-                    float v[V], p[M];
+                    float v[V];
+                    float4 p[M / 4];
 #pragma unroll
-                    for (int c = 0; c < V; ++c) v[c] = vs[k * D + lane * V + c];
+                    for (int c = 0; c < V; c += 2) *reinterpret_cast<float2*>(v + c) = *reinterpret_cast<const float2*>(vs + k * D + lane * V + c);
 #pragma unroll
-                    for (int r = 0; r < M; r += 4) *reinterpret_cast<float4*>(p + r) = *reinterpret_cast<const float4*>(s_p + k * M + r);
+                    for (int r = 0; r < M / 4; ++r) p[r] = *reinterpret_cast<const float4*>(s_p + k * M + 4 * r);
 #pragma unroll
-                    for (int r = 0; r < M; ++r)
+                    for (int c = 0; c < V; ++c) {
+                        const float2 vv = make_float2(v[c], v[c]);
 #pragma unroll
-                        for (int c = 0; c < V; ++c) acc[r][c] = fmaf(p[r], v[c], acc[r][c]);
+                        for (int r = 0; r < M / 4; ++r) {
+                            acc[c][2 * r] = fma2(make_float2(p[r].x, p[r].y), vv, acc[c][2 * r]);
+                            acc[c][2 * r + 1] = fma2(make_float2(p[r].z, p[r].w), vv, acc[c][2 * r + 1]);
+                        }
+                    }
                 }
             }
             __syncwarp();
         }
-        copies_wait<0>();
         // ---- join the warps (four and four through the same buffer), normalise, store
         float* s_join = smem + C::kOffJoin;
 #pragma unroll
-        for (int r = 0; r < M; ++r) {
-            // the parts of a key hold the same sums: add up one lane per key
+        for (int r = 0; r < RL; ++r) {
             for (int o = kSub / 2; o; o >>= 1) l[r] += __shfl_xor_sync(~0u, l[r], o);
-            if (lane == 0) {
-                s_m[warp * M + r] = m[r];
-                s_l[warp * M + r] = l[r];
+            if (key == 0) {
+                s_m[warp * M + row0 + r] = m[r];
+                s_l[warp * M + row0 + r] = l[r];
             }
-            if (warp >= 4)
-#pragma unroll
-                for (int c = 0; c < V; ++c) s_join[((warp - 4) * M + r) * D + lane * V + c] = acc[r][c];
         }
+        if (warp >= 4)
+#pragma unroll
+            for (int r = 0; r < M; ++r)
+#pragma unroll
+                for (int c = 0; c < V; ++c)
+                    s_join[((warp - 4) * M + r) * D + lane * V + c] = r & 1 ? acc[c][r / 2].y : acc[c][r / 2].x;
         __syncthreads();
         if (warp < 4) {
 #pragma unroll
             for (int r = 0; r < M; ++r) {
-                const float m2 = s_m[(warp + 4) * M + r], mx = fmaxf(m[r], m2), ms = mx == -INFINITY ? 0.f : mx;
-                const float f1 = exp2f(m[r] - ms), f2 = exp2f(m2 - ms);
+                const float m1 = s_m[warp * M + r], m2 = s_m[(warp + 4) * M + r], mx = fmaxf(m1, m2);
+                const float ms = mx == -INFINITY ? 0.f : mx, f1 = exp2f(m1 - ms), f2 = exp2f(m2 - ms);
 #pragma unroll
                 for (int c = 0; c < V; ++c) {
                     float* y = s_join + (warp * M + r) * D + lane * V + c;
-                    *y = f1 * acc[r][c] + f2 * *y;
+                    *y = f1 * (r & 1 ? acc[c][r / 2].y : acc[c][r / 2].x) + f2 * *y;
                 }
                 __syncwarp();
                 if (lane == 0) {
                     s_m[warp * M + r] = mx;
-                    s_l[warp * M + r] = f1 * l[r] + f2 * s_l[(warp + 4) * M + r];
+                    s_l[warp * M + r] = f1 * s_l[warp * M + r] + f2 * s_l[(warp + 4) * M + r];
                 }
             }
         }
@@ -267,11 +320,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
         __syncthreads();
     };
     if constexpr (PREFIX) {
-        piece(prefix_piece<M, kKeyTile>(a, cta));
+        cur = prefix_piece<M, kKeyTile>(a, cta);
+        find_next();
+        piece();
     } else {
-        Seg g;
         OwnWalk<M, kKeyTile, kPieceCost> walk(a, share);
-        while (walk.next(g)) piece(g);
+        if (walk.next(cur)) {
+            find_next();
+            for (;;) {
+                has_nxt = walk.next(nxt);
+                if (has_nxt && ahead == cur.n_tiles) find_next();
+                piece();
+                if (!has_nxt) break;
+                ahead -= cur.n_tiles;
+                cur = nxt;
+            }
+        }
         grid_dependency_wait();  // ends after the prefix kernel: the merge after this one sees both
     }
 }

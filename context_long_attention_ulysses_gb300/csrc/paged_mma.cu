@@ -9,8 +9,8 @@
 // Up to 16 rows: two CTAs per SM, so that one loads while the other joins, stores or begins a piece.  Up to 32: one CTA with
 // twice the stages (four warps with 32 rows each, two CTAs, spilled: 123 us for five tokens of 16 sequences).
 //
-// The pool is one tensor map (column, KV head, token of the page, page); a box holds min(page_size, 64) tokens, so that a
-// tile is 1, 2 or 4 boxes per 64 columns, issued by as many lanes.  Boxes without a visible key, or of a page that the pool
+// The pool is one tensor map (column, KV head, token of the page, page); a box holds min(page_size, 32) tokens, so that a
+// tile is 2 or 4 boxes per 64 columns, issued by as many lanes.  Boxes without a visible key, or of a page that the pool
 // does not have, are not loaded: their keys are left out by the warps that own them.
 #include <cmath>
 
@@ -29,6 +29,10 @@ constexpr int kKeyTile = 64;  // keys per tile
 template <int MT>
 constexpr int kPieceCost = MT == 1 ? 2 : 4;
 constexpr int kGroup = 4;  // warps that share 16 rows
+// Keys of a box at most.  Smaller boxes read less beyond a sequence's ends (200 sequences of about 750 own keys behind a prefix:
+// 128 us against 133 with boxes of 64), but boxes of 16 keep the producer too busy where one CTA has the SM (107 us against 91
+// for five tokens of 16 sequences).
+constexpr int kBox = 32;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;  // log2 units: O is rescaled only when the maximum grows by more than 2^8
 
@@ -113,7 +117,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
 
     if (warp == kConsumers) {
         // ---------------------------------------------------------------- producer
-        const int psize = 1 << a.page_log2, box = min(psize, kKeyTile), nb = kKeyTile / box;
+        const int psize = 1 << a.page_log2, box = min(psize, kBox), nb = kKeyTile / box;
         const int my_box = lane % nb, my_chunk = lane / nb % C::kChunks, my_kv = lane / nb / C::kChunks;
         int it = 0, n_seg = 0;
         bool ok = true;
@@ -175,7 +179,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
         // ---------------------------------------------------------------- consumers
         const int group = warp / kGroup, kw = warp % kGroup;  // rows 16 * group .., keys 16 * kw .. of each tile
         const int r0 = lane >> 2, c0 = (lane & 3) * 2;        // this lane's first row and column of a fragment
-        const int box_of_warp = kw * 16 / min(1 << a.page_log2, kKeyTile);
+        const int box_of_warp = kw * 16 / min(1 << a.page_log2, kBox);
         float* s_m = reinterpret_cast<float*>(smem + C::kOffStat) + group * 3 * kGroup * 16;
         float* s_l = s_m + kGroup * 16;
         float* s_lr = s_l + kGroup * 16;
@@ -396,7 +400,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
 template <int D, int MT, bool PREFIX>
 cudaError_t launch_t(const PagedArgs& a, cudaStream_t s) {
     using C = Cfg<D, MT>;
-    const int psize = 1 << a.page_log2, box = psize < kKeyTile ? psize : kKeyTile;
+    const int psize = 1 << a.page_log2, box = psize < kBox ? psize : kBox;
     const int64_t page = (int64_t)psize * D;
     CUtensorMap tk, tv;
     const Tensor4 k{const_cast<void*>(a.k_pages), page, D, page * a.Hkv, a.Hkv, psize, a.n_pages};
