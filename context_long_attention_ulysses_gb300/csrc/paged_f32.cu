@@ -5,9 +5,9 @@
 // them by itself through a ring of shared memory (cp.async, 16 bytes a lane; missing keys are filled with zeros), with a
 // running maximum, sum and output of its own; the eight meet only where a piece ends.  (Four warps with twice the keys, one
 // per scheduler, left it waiting for its own instructions: 34 us for 16 sequences of up to 16000 tokens.)
-//   scores: d/32 lanes per key, 32 values each; a key's row is padded by 16 bytes, so that 8 lanes' 16-byte reads fall into
-//           different banks, and the rows of Q are read by all lanes of a part at once; the parts' sums are added such that
-//           each lane ends with the whole scores of 8 / parts rows, and does the softmax of those only
+//   scores: eight lanes per key, d/8 values each, whose part of all 8 rows of Q stays in registers (read from shared memory
+//           for every key it was most of that memory's traffic, half of its peak, and the kernel took 28 us); the eight
+//           lanes' sums are added such that each ends with the whole score of one row, and does the softmax of that row
 //   output: a lane holds d/32 columns; the probabilities go through shared memory to be read by all lanes
 // More rows are more units, each reading K and V again (through L2).
 #include <cmath>
@@ -26,15 +26,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
 struct Cfg {
-    static constexpr int kParts = D / 32;                         // lanes per key in the scores
-    static constexpr int kSub = 32 / kParts;                      // keys of a warp in a tile
+    static constexpr int kSub = 1024 / D;                         // keys of a warp in a tile
     static constexpr int kKeyTile = kWarps * kSub;
-    static constexpr int kKStride = D + 4;                        // floats per key of K in shared memory
-    static constexpr int kStageFloats = kSub * (kKStride + D);    // K, V
+    static constexpr int kStageFloats = kSub * 2 * D;             // K, V
     static constexpr int kStages = 3;                             // about 130 KB in flight per SM
     static constexpr int kOffJoin = kWarps * kStages * kStageFloats;
-    static constexpr int kOffQ = kOffJoin + kWarps / 2 * kRows * D;
-    static constexpr int kOffP = kOffQ + kRows * D;
+    static constexpr int kOffP = kOffJoin + kWarps / 2 * kRows * D;
     static constexpr int kOffScale = kOffP + kWarps * kSub * kRows;
     static constexpr int kOffStat = kOffScale + kWarps * kRows;
     static constexpr int kFloats = kOffStat + 2 * kWarps * kRows;
@@ -65,7 +62,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
     }
     float* ring = smem + warp * S * C::kStageFloats;
     const uint32_t ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-    float* s_q = smem + C::kOffQ;
     float* s_p = smem + C::kOffP + warp * kSub * M;  // [key][row]
     float* s_al = smem + C::kOffScale + warp * M;
     float* s_m = smem + C::kOffStat;
@@ -73,13 +69,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
     const float* kp = static_cast<const float*>(a.k_pages);
     const float* vp = static_cast<const float*>(a.v_pages);
     constexpr uint32_t kAll = 0xffffffffu >> (32 - kSub);
-    const int key = lane % kSub, part = lane / kSub;  // scores: this lane's key and 32 of its values
-    constexpr int RL = M / C::kParts;                 // rows of the softmax per lane: row0 ..
-    const int row0 = C::kParts == 2 ? part * 4 : (part >> 1) * 4 + (part & 1) * 2;
+    const int ckey = lane % kSub;                     // copies: the key this lane looks up
+    const int part = lane & 7, kk = lane >> 3;        // scores: values 4 part .. of every 32, of keys kk, kk + 4, ..
+    constexpr int NP = kSub / 4, NV = D / 32;         // keys per lane, 16-byte vectors per lane and key
+                                                      // softmax: row `part` of the unit, those keys
 
     // Where this warp's keys of tile x of a piece lie (row of the pool, -1: no key).
     auto locate = [&](const Seg& g, int x) -> int64_t {
-        const int j = (g.tile0 + x) * kKeyTile + warp * kSub + key;
+        const int j = (g.tile0 + x) * kKeyTile + warp * kSub + ckey;
         if (j < (PREFIX ? 0 : a.key_begin) || j >= seg_key_end<PREFIX>(a, g)) return -1;
         const int page = seg_page<PREFIX>(a, g, j >> a.page_log2);
         if (page < 0) return -1;
@@ -98,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
     auto issue = [&] {                // one group of copies, if there is a tile
         if (ahead >= cur.n_tiles + (has_nxt ? nxt.n_tiles : 0)) return;
         const int st = issued % S;
-        const uint32_t k_dst = ring_addr + st * C::kStageFloats * 4, v_dst = k_dst + kSub * C::kKStride * 4;
+        const uint32_t k_dst = ring_addr + st * C::kStageFloats * 4, v_dst = k_dst + kSub * D * 4;
         const uint32_t live = __ballot_sync(~0u, next_row >= 0) & kAll;
         if (lane == 0) s_live[warp][st] = live;
         if (live) {
@@ -107,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
                 const int r = (i * 32 + lane) / kVecs, c = (i * 32 + lane) % kVecs;
                 const int64_t at = __shfl_sync(~0u, next_row, r);
                 const int64_t off = (at < 0 ? 0 : at) * D + c * 4;
-                copy16(k_dst + (r * C::kKStride + c * 4) * 4, kp + off, at >= 0);
+                copy16(k_dst + (r * D + c * 4) * 4, kp + off, at >= 0);
                 copy16(v_dst + (r * D + c * 4) * 4, vp + off, at >= 0);
             }
         }
@@ -122,33 +119,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
         const Seg& g = cur;
         while (issued < it + S - 1 && ahead < cur.n_tiles + (has_nxt ? nxt.n_tiles : 0)) issue();
         // ---- rows
-        for (int x = threadIdx.x; x < M * kVecs; x += kThreads) {
-            const int r = x / kVecs, R = g.row0 + r, i = R / a.g;
-            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < g.n_rows) {
-                w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
-                                                          ((int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g)) * D) +
-                          x % kVecs);
-                w = make_float4(w.x * a.scale_log2, w.y * a.scale_log2, w.z * a.scale_log2, w.w * a.scale_log2);
-            }
-            reinterpret_cast<float4*>(s_q)[x] = w;
-        }
-        int lim[RL], lim_min = INT_MAX;
+        float4 q[M][NV];
 #pragma unroll
-        for (int r = 0; r < RL; ++r) {
-            lim[r] = row0 + r < g.n_rows ? row_limit<PREFIX>(a, g, row0 + r) : INT_MAX;
-            lim_min = min(lim_min, lim[r]);
+        for (int r = 0; r < M; ++r) {
+            const bool live = r < g.n_rows;
+            const int R = g.row0 + (live ? r : 0), i = R / a.g;
+            const float4* src = reinterpret_cast<const float4*>(
+                static_cast<const float*>(a.q) + ((int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g)) * D) + part;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const float4 w = live ? __ldg(src + 8 * v) : make_float4(0.f, 0.f, 0.f, 0.f);
+                q[r][v] = make_float4(w.x * a.scale_log2, w.y * a.scale_log2, w.z * a.scale_log2, w.w * a.scale_log2);
+            }
         }
-        lim_min = __reduce_min_sync(~0u, lim_min);
-        __syncthreads();
+        const int lim = part < g.n_rows ? row_limit<PREFIX>(a, g, part) : INT_MAX;
+        const int lim_min = __reduce_min_sync(~0u, lim);
         // (packed float32: the scores sum two products, the output takes two rows at a time)
         float2 acc[V][M / 2];
-        float m[RL], l[RL];
-#pragma unroll
-        for (int r = 0; r < RL; ++r) {
-            m[r] = -INFINITY;
-            l[r] = 0.f;
-        }
+        float m = -INFINITY, l = 0.f;
 #pragma unroll
         for (int c = 0; c < V; ++c)
 #pragma unroll
@@ -161,76 +149,67 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
             const uint32_t live = s_live[warp][st];
             if (live) {
                 const float* ks = ring + st * C::kStageFloats;
-                const float* vs = ks + kSub * C::kKStride;
-                float2 s2[M];
+                const float* vs = ks + kSub * D;
+                float s[NP];
 #pragma unroll
-                for (int r = 0; r < M; ++r) s2[r] = make_float2(0.f, 0.f);
-                const float* kr = ks + key * C::kKStride + part * 32;
-                const float* qr = s_q + part * 32;
-#pragma unroll 4
-                for (int c = 0; c < 8; ++c) {
-                    const float4 k4 = *reinterpret_cast<const float4*>(kr + c * 4);
+                for (int j = 0; j < NP; ++j) {
+                    float2 s2[M];
 #pragma unroll
-                    for (int r = 0; r < M; ++r) {
-                        const float4 q4 = *reinterpret_cast<const float4*>(qr + r * D + c * 4);
-                        s2[r] = fma2(make_float2(q4.x, q4.y), make_float2(k4.x, k4.y), s2[r]);
-                        s2[r] = fma2(make_float2(q4.z, q4.w), make_float2(k4.z, k4.w), s2[r]);
+                    for (int r = 0; r < M; ++r) s2[r] = make_float2(0.f, 0.f);
+                    const float4* kr = reinterpret_cast<const float4*>(ks + (j * 4 + kk) * D) + part;
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        const float4 k4 = kr[8 * v];
+#pragma unroll
+                        for (int r = 0; r < M; ++r) {
+                            s2[r] = fma2(make_float2(q[r][v].x, q[r][v].y), make_float2(k4.x, k4.y), s2[r]);
+                            s2[r] = fma2(make_float2(q[r][v].z, q[r][v].w), make_float2(k4.z, k4.w), s2[r]);
+                        }
                     }
-                }
-                // add the parts up, each step keeping half of the rows
-                float s4[M / 2], s[RL];
-                const bool hi = lane & 16;
+                    // add the eight lanes up, each step keeping half of the rows
+                    float t[M];
 #pragma unroll
-                for (int r = 0; r < M / 2; ++r) {
-                    const float lo_sum = s2[r].x + s2[r].y, hi_sum = s2[r + M / 2].x + s2[r + M / 2].y;
-                    s4[r] = (hi ? hi_sum : lo_sum) + __shfl_xor_sync(~0u, hi ? lo_sum : hi_sum, 16);
-                }
-                if constexpr (C::kParts == 4) {
-                    const bool odd = lane & 8;
+                    for (int r = 0; r < M; ++r) t[r] = s2[r].x + s2[r].y;
 #pragma unroll
-                    for (int r = 0; r < RL; ++r)
-                        s[r] = (odd ? s4[r + RL] : s4[r]) + __shfl_xor_sync(~0u, odd ? s4[r] : s4[r + RL], 8);
-                } else {
+                    for (int o = 4; o; o >>= 1) {
+                        const bool hi = lane & o;
 #pragma unroll
-                    for (int r = 0; r < RL; ++r) s[r] = s4[r];
-                }
-                const int key0 = (g.tile0 + x) * kKeyTile + warp * kSub;
-                if (live != kAll || key0 + kSub > lim_min) {
-#pragma unroll
-                    for (int r = 0; r < RL; ++r)
-                        if (key0 + key >= lim[r] || !(live >> key & 1u)) s[r] = -INFINITY;
-                }
-                float mx[RL];
-                bool grew = false;
-#pragma unroll
-                for (int r = 0; r < RL; ++r) {
-                    mx[r] = s[r];
-#pragma unroll
-                    for (int o = kSub / 2; o; o >>= 1) mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], o));
-                    grew |= mx[r] > m[r];
-                }
-                if (__any_sync(~0u, grew)) {
-#pragma unroll
-                    for (int r = 0; r < RL; ++r) {
-                        const bool up = mx[r] > m[r];
-                        const float al = up ? exp2f(m[r] - mx[r]) : 1.f;
-                        if (up) m[r] = mx[r];
-                        l[r] *= al;
-                        if (key == 0) s_al[row0 + r] = al;
+                        for (int r = 0; r < o; ++r)
+                            t[r] = (hi ? t[r + o] : t[r]) + __shfl_xor_sync(~0u, hi ? t[r] : t[r + o], o);
                     }
+                    s[j] = t[0];
+                }
+                const int key0 = (g.tile0 + x) * kKeyTile + warp * kSub + kk;
+                if (live != kAll || key0 - kk + kSub > lim_min) {
+#pragma unroll
+                    for (int j = 0; j < NP; ++j)
+                        if (key0 + 4 * j >= lim || !(live >> (4 * j + kk) & 1u)) s[j] = -INFINITY;
+                }
+                float mx = s[0];
+#pragma unroll
+                for (int j = 1; j < NP; ++j) mx = fmaxf(mx, s[j]);
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
+                const bool up = mx > m;
+                if (__any_sync(~0u, up)) {
+                    const float al = up ? exp2f(m - mx) : 1.f;
+                    if (up) m = mx;
+                    l *= al;
+                    if (kk == 0) s_al[part] = al;
                     __syncwarp();
 #pragma unroll
                     for (int r = 0; r < M / 2; ++r) {
-                        const float2 al = *reinterpret_cast<const float2*>(s_al + 2 * r);
+                        const float2 al2 = *reinterpret_cast<const float2*>(s_al + 2 * r);
 #pragma unroll
-                        for (int c = 0; c < V; ++c) acc[c][r] = mul2(acc[c][r], al);
+                        for (int c = 0; c < V; ++c) acc[c][r] = mul2(acc[c][r], al2);
                     }
                 }
+                const float ms = m == -INFINITY ? 0.f : m;
 #pragma unroll
-                for (int r = 0; r < RL; ++r) {
-                    s[r] = exp2f(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
-                    l[r] += s[r];
-                    s_p[key * M + row0 + r] = s[r];
+                for (int j = 0; j < NP; ++j) {
+                    s[j] = exp2f(s[j] - ms);
+                    l += s[j];
+                    s_p[(4 * j + kk) * M + part] = s[j];
                 }
                 __syncwarp();
 #pragma unroll 4
@@ -256,13 +235,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
         }
         // ---- join the warps (four and four through the same buffer), normalise, store
         float* s_join = smem + C::kOffJoin;
-#pragma unroll
-        for (int r = 0; r < RL; ++r) {
-            for (int o = kSub / 2; o; o >>= 1) l[r] += __shfl_xor_sync(~0u, l[r], o);
-            if (key == 0) {
-                s_m[warp * M + row0 + r] = m[r];
-                s_l[warp * M + row0 + r] = l[r];
-            }
+        l += __shfl_xor_sync(~0u, l, 8);
+        l += __shfl_xor_sync(~0u, l, 16);
+        if (kk == 0) {
+            s_m[warp * M + part] = m;
+            s_l[warp * M + part] = l;
         }
         if (warp >= 4)
 #pragma unroll
