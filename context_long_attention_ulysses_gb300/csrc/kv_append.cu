@@ -2,8 +2,8 @@
 //
 // Per token, head and i < rot/2 the pair (a, b) of frequency f_i turns by the angle r f_i (r: the token's position):
 //   a' = a cos(r f_i) - b sin(r f_i),  b' = b cos(r f_i) + a sin(r f_i).
-// The angle is the float64 product of the position and the float32 frequency, reduced by 2 pi in float64 (in float32
-// the angle of position 10^6 is off by up to 0.06 rad); sine, cosine and the rotation are float32.
+// The angle is formed to 64 bits (in float32 the angle of position 10^6 is off by up to 0.06 rad); sine, cosine and the
+// rotation are float32.
 //
 // Bound by HBM: every value is read once and written once (k twice with k_out).  A head is d / (2 V) items of two 16-byte
 // vectors (V values): the two that a rotation pairs up, or two neighbours where pairs are neighbours or pass unchanged.  A
@@ -21,16 +21,34 @@ namespace usp {
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kAhead = 3;                     // items of a thread in flight
+// (96 threads with four items in flight, measured against 128 x 3, 64 x 3, 64 x 6 and 256 x 3 for a prompt of 32768 tokens:
+// 135.6 us against 137.3, 136.7, 147.4 and 154)
+constexpr int kThreads = 96;
+constexpr int kAhead = 4;                     // items of a thread in flight
 constexpr int kItems = kThreads * kAhead;     // items of a CTA per round
 constexpr int kMaxTokens = 16;
 
-// cos and sin of r * f
+// cos and sin of r * f.  Only the fraction of the turns r f / 2 pi counts, so it is formed in 64-bit fixed point, where whole
+// turns fall off the top: f = m 2^-shift with an integer m of 24 bits, the fraction of f / 2 pi is m * (2^64 / 2 pi) >> shift
+// to 64 bits, and times r, up to 2^31, it is off by less than 2^-30 turns for f up to 8.
+// (The scarce float64 units took 3.5 of 144 us for a prompt of
+// 32768 tokens; they remain for f of 2^24 and more, infinities and NaN.)
 __device__ __forceinline__ float2 turn(int r, float f) {
-    const double turns = (double)r * (double)f * 0.15915494309189535;  // / 2 pi
+    const uint32_t bits = __float_as_uint(f) & 0x7fffffffu;
+    const int exponent = (int)(bits >> 23), shift = 150 - exponent;
     float s, c;
-    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+    if (shift >= 0) {
+        const uint32_t m = exponent > 0 ? (bits & 0x7fffffu) | 0x800000u : 0u;  // (a subnormal f turns by nothing: 2^-95 turns)
+        constexpr uint64_t kPerTurn = 0x28be60db9391054aull;                    // 2^64 / 2 pi
+        const uint64_t lo = m * kPerTurn, hi = __umul64hi((uint64_t)m, kPerTurn);
+        const uint64_t frac = shift == 0 ? lo : shift < 64 ? (lo >> shift) | (hi << (64 - shift)) : shift < 128 ? hi >> (shift - 64) : 0;
+        int64_t turns = (int64_t)((uint64_t)(int64_t)r * frac);
+        if (f < 0.f) turns = -turns;
+        sincospif((float)(int)(turns >> 32) * 0x1p-31f, &s, &c);
+    } else {
+        const double turns = (double)r * (double)f * 0.15915494309189535;  // / 2 pi
+        sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+    }
     return make_float2(c, s);
 }
 
@@ -174,9 +192,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
                 w[u][0] = Vec<T>::close(a);
                 w[u][1] = Vec<T>::close(b);
             }
-            auto store = [&](T* dst) {
-                *reinterpret_cast<uint4*>(dst + it.e0) = w[u][0];
-                *reinterpret_cast<uint4*>(dst + it.e1) = w[u][1];
+            auto store = [&](T* dst) {  // (streaming: 141 us against 148)
+                __stcs(reinterpret_cast<uint4*>(dst + it.e0), w[u][0]);
+                __stcs(reinterpret_cast<uint4*>(dst + it.e1), w[u][1]);
             };
             const int64_t t = t0 + it.tok;
             if (it.head < hq) {

@@ -18,6 +18,7 @@
 // by an earlier CTA) and its last (slot 1).
 #pragma once
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -57,6 +58,20 @@ cudaError_t launch_own(void (*kernel)(P...), const PagedArgs& a, unsigned thread
     if (a.prefix_len > 0) return launch_dependent(kernel, dim3(a.ctas), threads, smem, stream, args...);
     kernel<<<a.ctas, threads, smem, stream>>>(args...);
     return cudaGetLastError();
+}
+
+// Allows a kernel its dynamic shared memory, once per device (asked for on every call it shows in the smallest ones).
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 // What paged_merge_kernel does with a row: word x = kind | row in the tile << 2, y = first CTA | last CTA << 16.

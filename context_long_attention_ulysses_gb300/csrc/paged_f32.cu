@@ -320,16 +320,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
 template <int D>
 cudaError_t launch_d(const PagedArgs& a, bool prefix, cudaStream_t s) {
     constexpr size_t smem = Cfg<D>::kFloats * 4;
-    auto set = [](auto kern) {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    };
     if (prefix) {
-        const cudaError_t e = set(paged_f32_kernel<D, true>);
+        const cudaError_t e = allow_smem<paged_f32_kernel<D, true>>((int)smem);
         if (e != cudaSuccess) return e;
         paged_f32_kernel<D, true><<<a.p_ctas, kThreads, smem, s>>>(a);
         return cudaGetLastError();
     }
-    const cudaError_t e = set(paged_f32_kernel<D, false>);
+    const cudaError_t e = allow_smem<paged_f32_kernel<D, false>>((int)smem);
     return e != cudaSuccess ? e : launch_own(paged_f32_kernel<D, false>, a, kThreads, smem, s, a);
 }
 

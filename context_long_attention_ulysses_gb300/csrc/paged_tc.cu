@@ -478,7 +478,7 @@ cudaError_t launch_t(const PagedArgs& a, cudaStream_t s) {
     v.ptr = const_cast<void*>(a.v_pages);
     if (!make_tmap_bf16(&tk, k, D, box) || !make_tmap_bf16(&tv, v, D, box)) return cudaErrorInvalidValue;
     auto kern = paged_tc_kernel<D, NS, PREFIX>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    const cudaError_t e = allow_smem<paged_tc_kernel<D, NS, PREFIX>>(C::kSmem);
     if (e != cudaSuccess) return e;
     if (!PREFIX) return launch_own(kern, a, C::kThreads, C::kSmem, s, tk, tv, a);
     kern<<<a.p_ctas, C::kThreads, C::kSmem, s>>>(tk, tv, a);
