@@ -187,7 +187,8 @@ size_t paged_plan(PagedArgs* a, int max_q, void* ws) {
         // Parts of a unit: few waves of CTAs, each of few tiles and the cost of a piece.
         const int64_t units = (batch + pre.rows - 1) / pre.rows * a->Hkv, tiles = (a->prefix_len + pre.keys - 1) / pre.keys;
         int64_t best = INT64_MAX;
-        for (int64_t k = 1; k <= tiles && k <= 4 * pre.ctas && (k == 1 || units * k <= 16 * pre.ctas); ++k) {
+        for (int64_t waves = 1; waves <= 16; ++waves) {
+            const int64_t k = std::max<int64_t>(1, std::min(tiles, waves * pre.ctas / units));
             const int64_t cost = (units * k + pre.ctas - 1) / pre.ctas * ((tiles + k - 1) / k + pre.piece);
             if (cost < best) {
                 best = cost;
@@ -232,7 +233,7 @@ static cudaError_t merge_t(const PagedArgs& a, cudaStream_t stream) {
     if ((int64_t)batch * a.Hkv <= 8 * kSms)
         return launch_dependent(paged_merge_kernel<T, D, 1, 512>, dim3(batch, a.Hkv), 512, 0, stream, a);
     // parts of a row: those of the prefix, and own ones as equal shares give them
-    const int units = a.Hkv * std::max(a.n_seqs, (batch + a.rows - 1) / a.rows);
+    const int64_t units = (int64_t)a.Hkv * std::max(a.n_seqs, (batch + a.rows - 1) / a.rows);
     const dim3 grid((batch + 7) / 8, a.Hkv);
     if (a.p_split + a.ctas / units > 8)
         return launch_dependent(paged_merge_kernel<T, D, 8, 1024>, grid, 1024, 0, stream, a);

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
         return (((int64_t)page * a.Hkv + g.h) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
     };
     // The copies run on across pieces, up to the end of the next one: `next_row` is where the tile to be issued next lies.
-    Seg cur, nxt;
+    Seg cur{}, nxt{};
     bool has_nxt = false;
     int it = 0, issued = 0;           // tiles worked on and tiles issued by this CTA so far
     int ahead = 0;                    // tiles of the current piece (and then the next) that were issued
