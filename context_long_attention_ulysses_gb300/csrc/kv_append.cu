@@ -15,7 +15,7 @@
 
 #include <cuda_bf16.h>
 
-#include "kernels.h"
+#include "paged.cuh"
 
 namespace usp {
 
@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
             }
         }
     };
+    begin_kernel(false);
     fetch(threadIdx.x);
     if (threadIdx.x < n_tok) {
         const int t = t0 + threadIdx.x, s = p.seq[t], pos = p.pos[t];
@@ -220,11 +221,8 @@ cudaError_t launch_t(const AppendParams& p, cudaStream_t s) {
     int n = std::min(kMaxTokens, std::max(1, kItems / per_token));
     while (n > 1 && (p.n_tokens + n - 1) / n < 4 * 152) --n;
     const unsigned grid = (unsigned)((p.n_tokens + n - 1) / n);
-    if (p.interleaved)
-        kv_append_kernel<T, true><<<grid, kThreads, 0, s>>>(p, n, item_log2);
-    else
-        kv_append_kernel<T, false><<<grid, kThreads, 0, s>>>(p, n, item_log2);
-    return cudaGetLastError();
+    return p.interleaved ? launch_dependent(kv_append_kernel<T, true>, dim3(grid), kThreads, 0, s, p, n, item_log2)
+                         : launch_dependent(kv_append_kernel<T, false>, dim3(grid), kThreads, 0, s, p, n, item_log2);
 }
 
 }  // namespace

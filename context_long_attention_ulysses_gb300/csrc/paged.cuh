@@ -29,9 +29,11 @@
 
 namespace usp {
 
-// The kernels of a call follow each other by programmatic dependent launch: a kernel lets its successor's CTAs start as
-// soon as its own have all begun (the successor's set-up then overlaps with it), and the successor waits for its
-// predecessor's end, and everything it wrote, before it reads or overwrites any of that.
+// The kernels follow each other by programmatic dependent launch: a kernel lets its successor's CTAs start as soon as its own
+// have all begun, so that the successor's set-up overlaps with it, and every kernel waits for its predecessor's end, and
+// everything it wrote, before it reads or overwrites any of that.  The own kernel behind a prefix kernel needs nothing of it:
+// it waits at its end only, so that the merge after it sees what both wrote (and the prefix kernel lets it start only after
+// its own wait, so that it has what came before the call).
 __device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -51,13 +53,10 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Own keys: behind the prefix kernel this one may begin while that one ends (neither reads what the other writes).
-template <typename... P, typename... A>
-cudaError_t launch_own(void (*kernel)(P...), const PagedArgs& a, unsigned threads, size_t smem, cudaStream_t stream,
-                       const A&... args) {
-    if (a.prefix_len > 0) return launch_dependent(kernel, dim3(a.ctas), threads, smem, stream, args...);
-    kernel<<<a.ctas, threads, smem, stream>>>(args...);
-    return cudaGetLastError();
+// To be called by all threads, before anything is read: `behind_prefix` for the own kernel behind a prefix kernel.
+__device__ __forceinline__ void begin_kernel(bool behind_prefix) {
+    if (!behind_prefix) grid_dependency_wait();
+    let_dependents_start();
 }
 
 // Allows a kernel its dynamic shared memory, once per device (asked for on every call it shows in the smallest ones).

@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(NT) paged_merge_kernel(const PagedArgs a) {
     const int h = blockIdx.y, R = blockIdx.x * ROWS + r, t = R / a.g, j = R - t * a.g;
     const bool in = R < a.n_tokens * a.g;
     const int64_t row = (int64_t)t * a.Hq + h * a.g + j;
-    grid_dependency_wait();
+    begin_kernel(false);
     const uint2 info = in ? __ldcg(a.row_info + row) : make_uint2(kRowDone, 0);
     const bool done = (info.x & 3u) == kRowDone;
     Parts p{};

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
     __shared__ Share share;
     __shared__ uint32_t s_live[kWarps][S];  // keys of the stage that exist
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
-    let_dependents_start();
+    begin_kernel(!PREFIX && a.prefix_len > 0);
     if constexpr (!PREFIX) {
         find_share<M, C::kKeyTile, kPieceCost, kThreads>(a, cta, a.ctas, &share);
         finish_empty_rows<float, M, C::kKeyTile, kThreads>(a, cta, a.ctas);
@@ -313,21 +313,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
                 cur = nxt;
             }
         }
-        grid_dependency_wait();  // ends after the prefix kernel: the merge after this one sees both
+        grid_dependency_wait();  // behind a prefix kernel: end after it
     }
 }
 
 template <int D>
 cudaError_t launch_d(const PagedArgs& a, bool prefix, cudaStream_t s) {
     constexpr size_t smem = Cfg<D>::kFloats * 4;
-    if (prefix) {
-        const cudaError_t e = allow_smem<paged_f32_kernel<D, true>>((int)smem);
-        if (e != cudaSuccess) return e;
-        paged_f32_kernel<D, true><<<a.p_ctas, kThreads, smem, s>>>(a);
-        return cudaGetLastError();
-    }
-    const cudaError_t e = allow_smem<paged_f32_kernel<D, false>>((int)smem);
-    return e != cudaSuccess ? e : launch_own(paged_f32_kernel<D, false>, a, kThreads, smem, s, a);
+    const cudaError_t e = prefix ? allow_smem<paged_f32_kernel<D, true>>((int)smem) : allow_smem<paged_f32_kernel<D, false>>((int)smem);
+    if (e != cudaSuccess) return e;
+    return prefix ? launch_dependent(paged_f32_kernel<D, true>, dim3(a.p_ctas), kThreads, smem, s, a)
+                  : launch_dependent(paged_f32_kernel<D, false>, dim3(a.ctas), kThreads, smem, s, a);
 }
 
 }  // namespace

@@ -93,7 +93,6 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
     const uint32_t full0 = sbase + C::kOffBar, empty0 = full0 + 8 * C::kStages;
     const uint32_t seg_full0 = empty0 + 8 * C::kStages, seg_empty0 = seg_full0 + 8 * kSegs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
-    let_dependents_start();
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int s = 0; s < C::kStages; ++s) {
@@ -106,6 +105,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
         }
         fence_mbar_init();
     }
+    begin_kernel(!PREFIX && a.prefix_len > 0);
     if constexpr (PREFIX) {
         __syncthreads();
     } else {
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
             if (lane == 0) mbar_arrive(seg_empty0 + 8 * si);
         }
     }
-    if constexpr (!PREFIX) grid_dependency_wait();  // ends after the prefix kernel: the merge after this one sees both
+    if constexpr (!PREFIX) grid_dependency_wait();  // behind a prefix kernel: end after it
 }
 
 template <int D, int MT, bool PREFIX>
@@ -410,9 +410,7 @@ cudaError_t launch_t(const PagedArgs& a, cudaStream_t s) {
     auto kern = paged_mma_kernel<D, MT, PREFIX>;
     const cudaError_t e = allow_smem<paged_mma_kernel<D, MT, PREFIX>>(C::kSmem);
     if (e != cudaSuccess) return e;
-    if (!PREFIX) return launch_own(kern, a, C::kThreads, C::kSmem, s, tk, tv, a);
-    kern<<<a.p_ctas, C::kThreads, C::kSmem, s>>>(tk, tv, a);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3(PREFIX ? a.p_ctas : a.ctas), C::kThreads, C::kSmem, s, tk, tv, a);
 }
 
 template <int D, bool PREFIX>

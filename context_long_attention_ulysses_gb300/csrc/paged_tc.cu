@@ -81,7 +81,6 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
     const int kDrain = kTurn + NS, kSegFull = kDrain + 1, kSegEmpty = kSegFull + kSegs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
     constexpr int kProducer = 4 * NS, kIssuer = 4 * NS + 1;
-    let_dependents_start();
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
@@ -102,6 +101,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
+    begin_kernel(!PREFIX && a.prefix_len > 0);
     if constexpr (!PREFIX) {
         find_share<M, kKeyTile, kPieceCost, C::kThreads>(a, cta, a.ctas, &share);
         finish_empty_rows<__nv_bfloat16, M, kKeyTile, C::kThreads>(a, cta, a.ctas);
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if constexpr (!PREFIX) grid_dependency_wait();  // ends after the prefix kernel: the merge after this one sees both
+    if constexpr (!PREFIX) grid_dependency_wait();  // behind a prefix kernel: end after it
 }
 
 template <int D, int NS, bool PREFIX>
@@ -480,9 +480,7 @@ cudaError_t launch_t(const PagedArgs& a, cudaStream_t s) {
     auto kern = paged_tc_kernel<D, NS, PREFIX>;
     const cudaError_t e = allow_smem<paged_tc_kernel<D, NS, PREFIX>>(C::kSmem);
     if (e != cudaSuccess) return e;
-    if (!PREFIX) return launch_own(kern, a, C::kThreads, C::kSmem, s, tk, tv, a);
-    kern<<<a.p_ctas, C::kThreads, C::kSmem, s>>>(tk, tv, a);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3(PREFIX ? a.p_ctas : a.ctas), C::kThreads, C::kSmem, s, tk, tv, a);
 }
 
 template <int D, bool PREFIX>
