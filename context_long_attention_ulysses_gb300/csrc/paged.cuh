@@ -291,6 +291,7 @@ template <int M, int KT>
 __device__ __forceinline__ Seg prefix_piece(const PagedArgs& a, int cta) {
     const int tiles = (a.prefix_len + KT - 1) / KT, nrt = (a.n_tokens * a.g + M - 1) / M;
     const int unit = cta / a.p_split, part = cta - unit * a.p_split;
+    const int each = tiles / a.p_split, more = tiles - each * a.p_split;  // the first `more` parts have one tile more
     Seg g;
     g.b = -1;
     g.h = unit / nrt;
@@ -299,8 +300,8 @@ __device__ __forceinline__ Seg prefix_piece(const PagedArgs& a, int cta) {
     g.t0 = 0;
     g.n = a.n_tokens;
     g.len = 0;
-    g.tile0 = (int)((int64_t)tiles * part / a.p_split);
-    g.n_tiles = (int)((int64_t)tiles * (part + 1) / a.p_split) - g.tile0;
+    g.tile0 = part * each + min(part, more);
+    g.n_tiles = each + (part < more ? 1 : 0);
     g.begins = part == 0;
     g.ends = part == a.p_split - 1;
     g.ordinal = 0;
@@ -309,7 +310,8 @@ __device__ __forceinline__ Seg prefix_piece(const PagedArgs& a, int cta) {
 }
 
 // The producer warp walks the share and hands each piece to the other warps through a ring of kSegs entries, so that the
-// walk's divisions and registers are paid once; a piece without tiles ends it.
+// walk's divisions and registers are paid once; a piece without tiles ends it.  (The one piece of a prefix CTA follows from
+// its number: every warp finds it for itself, and Q and the first pages are on their way before anything else is set up.)
 constexpr int kSegs = 4;
 
 // Keys that row r of a piece sees: below this limit (0 for a row of no sequence).

@@ -93,6 +93,13 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
     const uint32_t full0 = sbase + C::kOffBar, empty0 = full0 + 8 * C::kStages;
     const uint32_t seg_full0 = empty0 + 8 * C::kStages, seg_empty0 = seg_full0 + 8 * kSegs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+    begin_kernel(!PREFIX && a.prefix_len > 0);
+    Seg pre{};
+    if constexpr (PREFIX) pre = prefix_piece<M, kKeyTile>(a, cta);
+    if (threadIdx.x == 32 * kConsumers) {
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int s = 0; s < C::kStages; ++s) {
@@ -105,7 +112,6 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
         }
         fence_mbar_init();
     }
-    begin_kernel(!PREFIX && a.prefix_len > 0);
     if constexpr (PREFIX) {
         __syncthreads();
     } else {
@@ -122,6 +128,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
         int it = 0, n_seg = 0;
         bool ok = true;
         auto publish = [&](const Seg& g) {
+            if (PREFIX) return;
             const int i = n_seg % kSegs;
             if (n_seg >= kSegs)
                 ok = __all_sync(~0u, mbar_wait(seg_empty0 + 8 * i, (n_seg / kSegs - 1) & 1, abort_p, 24, a.status));
@@ -164,9 +171,8 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
             }
             return ok;
         };
-        Seg g;
+        Seg g = pre;
         if constexpr (PREFIX) {
-            g = prefix_piece<M, kKeyTile>(a, cta);
             piece(g);
         } else {
             OwnWalk<M, kKeyTile, kPieceCost<MT>> walk(a, share);
@@ -189,13 +195,13 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
         const int v_key = kw * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), v_c = lane >> 4;
         int it = 0;
         bool ok = true;
-        for (int n_seg = 0;; ++n_seg) {
+        for (int n_seg = 0; !PREFIX || n_seg == 0; ++n_seg) {
             const int si = n_seg % kSegs;
-            ok = ok && mbar_wait(seg_full0 + 8 * si, (n_seg / kSegs) & 1, abort_p, 25, a.status);
+            ok = PREFIX || ok && mbar_wait(seg_full0 + 8 * si, (n_seg / kSegs) & 1, abort_p, 25, a.status);
             // (one answer for the group's warps, which meet at barriers below; a wait that gives up within a piece lets its
             // warp run on to the next one without waiting)
-            if (!bar_group_all(group, ok)) break;
-            const Seg& g = s_seg[si];
+            if (!PREFIX && !bar_group_all(group, ok)) break;
+            const Seg& g = PREFIX ? pre : s_seg[si];
             if (g.n_tiles == 0) break;
             const int first = PREFIX ? 0 : a.key_begin, end = seg_key_end<PREFIX>(a, g);
             const int tile0 = g.tile0, n_tiles = g.n_tiles;
@@ -391,7 +397,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
             }
             // (the next piece's first barrier comes before anyone writes the join buffer or the statistics again)
             __syncwarp();
-            if (lane == 0) mbar_arrive(seg_empty0 + 8 * si);
+            if (!PREFIX && lane == 0) mbar_arrive(seg_empty0 + 8 * si);
         }
     }
     if constexpr (!PREFIX) grid_dependency_wait();  // behind a prefix kernel: end after it

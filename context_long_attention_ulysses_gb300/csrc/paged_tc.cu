@@ -60,6 +60,17 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int w) {
     return (0xffffffffu >> (32 - (hi - lo))) << lo;
 }
 
+// Row r of a piece's queries, zero beyond its last row.
+template <int N>
+__device__ __forceinline__ void load_q_row(const PagedArgs& a, const Seg& g, int r, uint4 (&w)[N]) {
+    const bool live = r < g.n_rows;
+    const int R = g.row0 + r, i = R / a.g;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                      ((int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g)) * (N * 8));
+#pragma unroll
+    for (int c = 0; c < N; ++c) w[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+}
+
 template <int D, int NS, bool PREFIX>
 __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -73,7 +84,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
     __shared__ Share share;
     __shared__ int abort_flag;
     __shared__ uint32_t s_boxes[kFlags];  // boxes of a tile that were loaded
-    __shared__ Seg s_seg[kSegs];
+    __shared__ Seg s_seg[kSegs], s_tail;
     auto BAR = [&](int i) { return sbase + C::kOffBar + 8u * (uint32_t)i; };
     const int kKFull = 0, kKEmpty = KS, kVFull = 2 * KS, kVEmpty = kVFull + VS;
     const int kQFull = kVEmpty + VS, kSFull = kQFull + NS, kPReady = kSFull + NS, kOReady = kPReady + NS;  // per stream
@@ -82,6 +93,17 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
     constexpr int kProducer = 4 * NS, kIssuer = 4 * NS + 1;
 
+    begin_kernel(!PREFIX && a.prefix_len > 0);
+    Seg pre{};
+    uint4 first_q[PREFIX ? D / 8 : 1];  // prefix: a softmax thread's row of Q
+    if constexpr (PREFIX) {
+        pre = prefix_piece<M, kKeyTile>(a, cta);
+        if (warp < 4 * NS) load_q_row(a, pre, threadIdx.x, first_q);
+    }
+    if (threadIdx.x == 32 * kProducer) {
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int s = 0; s < KS; ++s) { mbar_init(BAR(kKFull + s), 1); mbar_init(BAR(kKEmpty + s), NS); }
@@ -101,7 +123,6 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
-    begin_kernel(!PREFIX && a.prefix_len > 0);
     if constexpr (!PREFIX) {
         find_share<M, kKeyTile, kPieceCost, C::kThreads>(a, cta, a.ctas, &share);
         finish_empty_rows<__nv_bfloat16, M, kKeyTile, C::kThreads>(a, cta, a.ctas);
@@ -129,6 +150,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
             const int my_box = lane % nb, my_chunk = lane / nb;
             int it = 0, nv = 0, n_seg = 0;
             auto publish = [&](const Seg& g) {
+                if (PREFIX) return true;
                 const int i = n_seg % kSegs;
                 if (n_seg >= kSegs &&
                     !__all_sync(~0u, mbar_wait(BAR(kSegEmpty + i), (n_seg / kSegs - 1) & 1, abort_p, 43, a.status)))
@@ -183,26 +205,25 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                 }
                 return true;
             };
-            Seg g;
+            Seg g = pre;
             bool ok = true;
             if constexpr (PREFIX) {
-                g = prefix_piece<M, kKeyTile>(a, cta);
                 ok = piece(g);
             } else {
                 OwnWalk<M, kKeyTile, kPieceCost> walk(a, share);
                 // The end of a unit that an earlier CTA began comes last.  All shares being equally long, the CTAs of a
                 // head are then at the same key tile, or at one of two, at any time, and read it from L2 together.
-                Seg tail;
                 bool has_tail = false;
                 while (ok && walk.next(g)) {
                     if (g.ordinal == 0 && !g.begins) {
-                        tail = g;
+                        if (lane == 0) s_tail = g;
                         has_tail = true;
                     } else {
                         ok = piece(g);
                     }
                 }
-                if (ok && has_tail) ok = piece(tail);
+                __syncwarp();
+                if (ok && has_tail) ok = piece(s_tail);
             }
             g.n_tiles = 0;
             if (ok) publish(g);
@@ -256,13 +277,13 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                 if (has_k) { if (qk) mma_commit(BAR(kKEmpty + ks)); else mbar_arrive(BAR(kKEmpty + ks)); }
                 return true;
             };
-            for (int n_seg = 0;; ++n_seg) {
+            for (int n_seg = 0; !PREFIX || n_seg == 0; ++n_seg) {
                 const int si = n_seg % kSegs;
-                if (!mbar_wait(BAR(kSegFull + si), (n_seg / kSegs) & 1, abort_p, 44, a.status)) break;
-                const int n_tiles = s_seg[si].n_tiles;
+                if (!PREFIX && !mbar_wait(BAR(kSegFull + si), (n_seg / kSegs) & 1, abort_p, 44, a.status)) break;
+                const int n_tiles = PREFIX ? pre.n_tiles : s_seg[si].n_tiles;
                 if (n_tiles == 0) break;
-                const int nt = stream_tiles(s_seg[si], st);
-                mbar_arrive(BAR(kSegEmpty + si));
+                const int nt = PREFIX ? stream_tiles(pre, st) : stream_tiles(s_seg[si], st);
+                if (!PREFIX) mbar_arrive(BAR(kSegEmpty + si));
                 if (nt > 0 && !mbar_wait(BAR(kQFull + st), pieces++ & 1, abort_p, 35, a.status)) break;
                 bool ok = true;
                 for (int j = -1; ok && j < n_tiles; ++j) ok = do_turn(j, n_tiles, nt);
@@ -286,23 +307,18 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
         auto warp_wait = [&](uint32_t bar, uint32_t parity, int site) {  // one answer for the warp: TMEM access is collective
             return __all_sync(~0u, mbar_wait(bar, parity, abort_p, site, a.status)) != 0;
         };
-        int base = 0, cnt = 0, pieces = 0;
+        uint32_t base = 0, cnt = 0, pieces = 0;
         auto piece = [&](const Seg& g) {  // false: a wait gave up
             const int r = st * 128 + row;
             const bool valid = r < g.n_rows;
             const int n_tiles = stream_tiles(g, st), tile0 = g.tile0;
             if (n_tiles > 0) {  // this row of Q, swizzled as a TMA load would place it; rows beyond the unit are zero
-                const int R = g.row0 + r, i = R / a.g;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    static_cast<const __nv_bfloat16*>(a.q) +
-                    ((int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g)) * D);
                 uint8_t* dst = smem + C::kOffQ + st * C::kTileBytes + row * 128;
                 uint4 w[D / 8];
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) w[c] = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                if constexpr (!PREFIX) load_q_row(a, g, r, w);
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c)
-                    *reinterpret_cast<uint4*>(dst + (c / 8) * 16384 + (((c & 7) ^ (row & 7)) << 4)) = w[c];
+                    *reinterpret_cast<uint4*>(dst + (c / 8) * 16384 + (((c & 7) ^ (row & 7)) << 4)) = PREFIX ? first_q[PREFIX ? c : 0] : w[c];
                 fence_proxy_async_smem();
                 mbar_arrive(BAR(kQFull + st));
             }
@@ -331,7 +347,9 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                 }
                 if (key0 + kKeyTile > lim_min || (!PREFIX && key0 < a.key_begin) || live != all_boxes) {
                     const int first = PREFIX ? 0 : a.key_begin, end = seg_key_end<PREFIX>(a, g);
-                    const int lo = first - key0, hi = min(lim, end) - key0;
+                    // (own keys: the limit again, as the registers are short in the loop)
+                    const int mine = PREFIX ? lim : st * 128 + row < g.n_rows ? row_limit<PREFIX>(a, g, st * 128 + row) : INT_MAX;
+                    const int lo = first - key0, hi = min(mine, end) - key0;
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         uint32_t see = 0u;
@@ -344,7 +362,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                     }
                     // V rows that are no key of this piece may hold anything, NaN too, and 0 * NaN must not reach O:
                     // thread = row of the V tile (both streams write the same zeros)
-                    const int vs = (base + j) % VS;
+                    const uint32_t vs = (base + j) % VS;
                     if (!warp_wait(BAR(kVFull + vs), ((base + j) / VS) & 1, 41)) return false;
                     const bool real = key0 + row >= first && key0 + row < end && (live >> (row >> box_log2) & 1u);
                     if (!real) {
@@ -448,12 +466,16 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
             cnt += n_tiles;
             return true;
         };
-        for (int n_seg = 0;; ++n_seg) {
-            const int si = n_seg % kSegs;
-            if (!warp_wait(BAR(kSegFull + si), (n_seg / kSegs) & 1, 45)) break;
-            if (s_seg[si].n_tiles == 0 || !piece(s_seg[si])) break;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(kSegEmpty + si));
+        if constexpr (PREFIX) {
+            piece(pre);
+        } else {
+            for (int n_seg = 0;; ++n_seg) {
+                const int si = n_seg % kSegs;
+                if (!warp_wait(BAR(kSegFull + si), (n_seg / kSegs) & 1, 45)) break;
+                if (s_seg[si].n_tiles == 0 || !piece(s_seg[si])) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(kSegEmpty + si));
+            }
         }
     }
     // ---------------------------------------------------------------- teardown
