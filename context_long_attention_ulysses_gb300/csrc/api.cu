@@ -1229,7 +1229,8 @@ static usp_status check_cache(const usp_cache* c) {
     const int ps = c->page_size;
     if (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256) return USP_ERR_UNSUPPORTED;
     if (c->d != 64 && c->d != 128) return USP_ERR_UNSUPPORTED;
-    if (c->Hq > 65535 || (int64_t)c->max_pages * ps > INT32_MAX || (int64_t)c->n_pages * c->Hkv > INT32_MAX)
+    // (positions rounded up to whole tiles, and rows of the pool's outer dimension, are ints)
+    if (c->Hq > 65535 || (int64_t)c->max_pages * ps > INT32_MAX - 1023 || (int64_t)c->n_pages * c->Hkv > INT32_MAX)
         return USP_ERR_UNSUPPORTED;
     return USP_OK;
 }
@@ -1334,7 +1335,7 @@ static usp_status paged_attn(const usp_cache* c, int n_tokens, int max_q, const 
     if (!a.status) return USP_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    if (prefix_len > 0) e = traced("paged_prefix", s, [&] { return launch_paged_prefix(a, s); });
+    if (a.prefix_len > 0) e = traced("paged_prefix", s, [&] { return launch_paged_prefix(a, s); });
     if (e == cudaSuccess) e = traced("paged_own", s, [&] { return launch_paged_own(a, s); });
     if (e == cudaSuccess) e = traced("paged_merge", s, [&] { return launch_paged_merge(a, s); });
     return cuda_status(e);

@@ -413,7 +413,8 @@ usp_status usp_ring_merge(int64_t rows, int d, const float* o_a, const float* ls
  * at each call.
  * Requirements: n_pages, n_seqs, max_pages >= 0; page_size in {16, 32, 64,
  * 128, 256}; Hq, Hkv >= 1 and Hq % Hkv == 0; Hq <= 65535; d in {64, 128};
- * max_pages * page_size and n_pages * Hkv below 2^31. */
+ * max_pages * page_size <= 2^31 - 1024, n_pages * Hkv < 2^31, and for the
+ * attention calls n_tokens * Hq <= 2^31 - 513. */
 typedef struct {
     int n_pages;
     int page_size;
@@ -477,8 +478,8 @@ size_t usp_paged_attn_workspace_size(const usp_cache* c, int n_tokens, int max_q
  * reaches a result.  A value that is not finite in a key or value below len
  * may reach every row of its sequence, masked or not (0 * inf in the product).
  * BF16: float32 scores, sums and accumulation, probabilities rounded to bf16
- * for the product with V (o divides by the sum of the rounded ones); F32:
- * float32 throughout.  Results do not depend on the run (fixed order of sums).
+ * for the product with V; F32: float32 throughout, on CUDA cores.  Results do
+ * not depend on the run (fixed order of sums).
  * ws: at least usp_paged_attn_workspace_size(c, n_tokens, max_q) bytes,
  * 256-byte aligned, contents on entry irrelevant; calls that can overlap on
  * the GPU need one each. */

@@ -271,7 +271,8 @@ def _status(call, /, *a, **kw):
     (dict(n_pages=-1), 1), (dict(n_seqs=-1), 1), (dict(max_pages=-1), 1), (dict(Hq=0), 1), (dict(Hkv=0), 1),
     (dict(Hq=5), 1), (dict(scale=-1.0), 1), (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1),
     (dict(page_size=24), 2), (dict(page_size=8), 2), (dict(page_size=512), 2), (dict(d=96), 2),
-    (dict(Hq=65536, Hkv=1), 2), (dict(max_pages=1 << 27), 2), (dict(n_pages=1 << 30, Hkv=4), 2)])
+    (dict(Hq=65536, Hkv=1), 2), (dict(max_pages=1 << 27), 2), (dict(max_pages=(1 << 27) - 63), 2),
+    (dict(n_pages=1 << 30, Hkv=4), 2)])
 def test_cache_shapes_are_refused(lib, kw, code):
     for f in (_append, _paged):
         assert _status(f, _c(**kw)) == code
@@ -581,6 +582,92 @@ def test_two_streams_at_once(usp):
     _done(usp, guard)
     for b in bs:
         b.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("prefix", [0, 16])
+def test_without_pages_no_row_sees_a_key(usp, dtype, prefix):
+    """A pool, or a page table, of size zero: every row is empty, and no pool pointer is needed."""
+    import torch
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for kw in (dict(n_pages=0, max_pages=4), dict(n_pages=3, max_pages=0)):
+        if prefix > kw["max_pages"] * 16:
+            continue
+        c = usp.Cache(page_size=16, n_seqs=2, Hq=4, Hkv=2, d=64, dtype=dtype, **kw)
+        q = torch.ones((2, 4, 64), dtype=c.torch_dtype, device="cuda")
+        o, lse = torch.full_like(q, 7.0), torch.full((2, 4), 7.0, device="cuda")
+        table = torch.zeros((2, max(kw["max_pages"], 1)), **i32)
+        ws = torch.empty(usp.usp_prefix_attn_workspace_size(c, 2, 1, prefix), dtype=torch.uint8, device="cuda")
+        usp.usp_prefix_attn(c, 2, 1, q, None, None, table, torch.tensor([30, 1], **i32), None, table, prefix, o, lse, ws)
+        torch.cuda.synchronize()
+        assert usp.usp_device_status() == 0
+        assert (o == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.gpu
+def test_many_sequences_and_many_short_ones(usp):
+    """More sequences than a CTA has threads, most of a tile or less, some empty, one long."""
+    guard = Guarded()
+    rng = np.random.default_rng(5)
+    seqs = [(1, int(n)) for n in rng.integers(0, 40, 1000)]
+    seqs[617] = (1, 3000)
+    for dtype, Hq, Hkv in (("bf16", 4, 4), ("f32", 2, 1)):
+        b = Batch(seqs, Hq, Hkv, 64, 16, dtype).to_gpu(usp, guard)
+        b.run(usp)
+        _done(usp, guard)
+        b.check()
+    b = Batch([(int(n % 3), int(n)) for n in rng.integers(0, 40, 700)] + [(90, 500)], 4, 2, 64, 16).to_gpu(usp, guard)
+    b.run(usp)
+    _done(usp, guard)
+    b.check()
+
+
+@pytest.mark.gpu
+def test_wide_tables_and_idle_slots(usp):
+    """A serving batch keeps rows for sequences that are not there: their table rows may hold anything."""
+    import torch
+    guard = Guarded()
+    b = Batch([(1, 200), (1, 0), (1, 77), (1, 0)], 8, 2, 128, 64)
+    wide = np.full((4, 500), 1 << 30, np.int64)
+    wide[:, :b.table.shape[1]] = np.where(b.table < 0, 12345678, b.table)
+    b.table = wide.astype(np.int32)
+    import dataclasses
+    b.c = dataclasses.replace(b.c, max_pages=500)
+    b.to_gpu(usp, guard)
+    b.run(usp)
+    _done(usp, guard)
+    b.check()
+
+
+@pytest.mark.gpu
+def test_abort_path_gives_up_fast_and_recovers(usp):
+    """With a timeout on record every kernel gives up at its first wait that is not satisfied, drains its loads and
+    products and returns; the host reads the timeout once, and the next run is the clean one, bit for bit."""
+    import time
+
+    import torch
+    guard = Guarded()
+    cases = [([(1, 3000), (1, 500)], 8, 2, 128, 0), ([(6, 900)], 8, 2, 128, 0), ([(70, 900), (3, 10)], 8, 2, 128, 0),
+             ([(300, 2000)], 4, 1, 64, 0), ([(1, 1000 + i) for i in range(40)], 8, 2, 128, 900),
+             ([(1, 1000 + i) for i in range(3)], 8, 2, 64, 900)]
+    bs = [Batch(seqs, Hq, Hkv, d, 64, prefix=p).to_gpu(usp, guard) for seqs, Hq, Hkv, d, p in cases]
+    clean = []
+    for b in bs:
+        b.run(usp)
+        _done(usp, guard)
+        clean.append((b.g["o"].clone(), b.g["lse"].clone()))
+    t0 = time.perf_counter()
+    usp.usp_diag_raise_status()
+    for b in bs:
+        b.run(usp)
+    assert usp.usp_device_status() == _lib.USP_ERR_TIMEOUT
+    assert time.perf_counter() - t0 < 1.5
+    assert usp.usp_device_status() == _lib.USP_OK
+    for b, (o, lse) in zip(bs, clean):
+        b.run(usp)
+        _done(usp, guard)
+        assert torch.equal(b.g["o"], o) and torch.equal(b.g["lse"], lse)
 
 
 @pytest.mark.gpu
