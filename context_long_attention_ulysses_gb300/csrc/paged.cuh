@@ -33,7 +33,8 @@ namespace usp {
 // have all begun, so that the successor's set-up overlaps with it, and every kernel waits for its predecessor's end, and
 // everything it wrote, before it reads or overwrites any of that.  The own kernel behind a prefix kernel needs nothing of it:
 // it waits at its end only, so that the merge after it sees what both wrote (and the prefix kernel lets it start only after
-// its own wait, so that it has what came before the call).
+// its own wait, so that it has what came before the call).  What a predecessor may have written is read by plain loads, not
+// through the read-only path, which holds what it likes from before the wait.
 __device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -89,13 +90,13 @@ struct SeqRows {
 __device__ __forceinline__ SeqRows seq_rows(const PagedArgs& a, int b) {
     SeqRows s;
     if (a.q_start) {
-        s.t0 = min(max(__ldg(a.q_start + b), 0), a.n_tokens);
-        s.n = min(max(__ldg(a.q_start + b + 1), s.t0), a.n_tokens) - s.t0;
+        s.t0 = min(max(*(a.q_start + b), 0), a.n_tokens);
+        s.n = min(max(*(a.q_start + b + 1), s.t0), a.n_tokens) - s.t0;
     } else {
         s.t0 = b;
         s.n = 1;
     }
-    s.len = min(max(__ldg(a.seq_lens + b), 0), a.max_pages << a.page_log2);
+    s.len = min(max(*(a.seq_lens + b), 0), a.max_pages << a.page_log2);
     return s;
 }
 
@@ -198,7 +199,7 @@ __device__ void find_share(const PagedArgs& a, int cta, int n_cta, Share* out) {
     if (b0 > 0) {  // more than one chunk of sequences: find the one
         for (b0 = 0;; b0 += NT) {
             scan(b0);
-            if (before + sum > pos) break;
+            if (before + sum > pos || b0 + NT >= a.n_seqs) break;  // (the second only if the lengths changed meanwhile)
             before += sum;
         }
     }
@@ -236,7 +237,7 @@ struct OwnWalk {
         int64_t off = sh.off - h * sh.per_head;
         rt = 0;
         ut = unit_tiles<M, KT>(a, s, 0);
-        while (off >= unit_places<PC>(ut)) {
+        while (off >= unit_places<PC>(ut) && rt + 1 < nrt) {
             off -= unit_places<PC>(ut);
             ++rt;
             ut = unit_tiles<M, KT>(a, s, rt);
@@ -327,7 +328,7 @@ __device__ __forceinline__ int row_limit(const PagedArgs& a, const Seg& g, int r
             lo = 0;
             while (lo < hi) {  // first b with q_start[b + 1] > i
                 const int mid = (lo + hi) >> 1;
-                if (__ldg(a.q_start + mid + 1) > i) hi = mid; else lo = mid + 1;
+                if (*(a.q_start + mid + 1) > i) hi = mid; else lo = mid + 1;
             }
         }
         if (lo >= a.n_seqs) return 0;
@@ -347,7 +348,7 @@ __device__ __forceinline__ int seg_key_end(const PagedArgs& a, const Seg& g) {
 // Pages of a piece's keys; an entry outside the pool reads as -1.
 template <bool PREFIX>
 __device__ __forceinline__ int seg_page(const PagedArgs& a, const Seg& g, int j) {
-    const int id = __ldg((PREFIX ? a.prefix_pages : a.page_table + (int64_t)g.b * a.max_pages) + j);
+    const int id = *((PREFIX ? a.prefix_pages : a.page_table + (int64_t)g.b * a.max_pages) + j);
     return (unsigned)id < (unsigned)a.n_pages ? id : -1;
 }
 
@@ -395,8 +396,8 @@ __device__ __forceinline__ void note_row(const PagedArgs& a, const Seg& g, int r
 // and rows of no sequence (not touched).  Spread over the CTAs; all threads of the CTA (NT) call it.
 template <typename T, int M, int KT, int NT>
 __device__ void finish_empty_rows(const PagedArgs& a, int cta, int n_cta) {
-    const int lo = a.q_start ? min(max(__ldg(a.q_start), 0), a.n_tokens) : 0;
-    const int hi = a.q_start ? min(max(__ldg(a.q_start + a.n_seqs), lo), a.n_tokens) : a.n_tokens;
+    const int lo = a.q_start ? min(max(*a.q_start, 0), a.n_tokens) : 0;
+    const int hi = a.q_start ? min(max(*(a.q_start + a.n_seqs), lo), a.n_tokens) : a.n_tokens;
     for (int64_t x = (int64_t)cta * NT + threadIdx.x; x < (int64_t)(a.n_tokens - (hi - lo)) * a.Hq;
          x += (int64_t)n_cta * NT) {
         const int64_t row = x < (int64_t)lo * a.Hq ? x : x + (int64_t)(hi - lo) * a.Hq;

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
                 static_cast<const float*>(a.q) + ((int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g)) * D) + part;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const float4 w = live ? __ldg(src + 8 * v) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 w = live ? *(src + 8 * v) : make_float4(0.f, 0.f, 0.f, 0.f);
                 q[r][v] = make_float4(w.x * a.scale_log2, w.y * a.scale_log2, w.z * a.scale_log2, w.w * a.scale_log2);
             }
         }

@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
                     ((int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g)) * D + c0);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    q[kk][hh] = live ? __ldg(src + kk * 8) : 0u;
-                    q[kk][hh + 2] = live ? __ldg(src + kk * 8 + 4) : 0u;
+                    q[kk][hh] = live ? *(src + kk * 8) : 0u;
+                    q[kk][hh + 2] = live ? *(src + kk * 8 + 4) : 0u;
                 }
                 lim[hh] = live ? row_limit<PREFIX>(a, g, r) : INT_MAX;
             }

@@ -68,7 +68,7 @@ __device__ __forceinline__ void load_q_row(const PagedArgs& a, const Seg& g, int
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
                                                       ((int64_t)(g.t0 + i) * a.Hq + g.h * a.g + (R - i * a.g)) * (N * 8));
 #pragma unroll
-    for (int c = 0; c < N; ++c) w[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < N; ++c) w[c] = live ? *(src + c) : make_uint4(0, 0, 0, 0);
 }
 
 template <int D, int NS, bool PREFIX>
