@@ -1334,9 +1334,9 @@ static usp_status paged_attn(const usp_cache* c, int n_tokens, int max_q, const 
     a.status = status_ptr();
     if (!a.status) return USP_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaSuccess;
-    if (a.prefix_len > 0) e = traced("paged_prefix", s, [&] { return launch_paged_prefix(a, s); });
-    if (e == cudaSuccess) e = traced("paged_own", s, [&] { return launch_paged_own(a, s); });
+    // (the prefix second: its partial results, the larger ones, are still in L2 when they are joined)
+    cudaError_t e = traced("paged_own", s, [&] { return launch_paged_own(a, s); });
+    if (e == cudaSuccess && a.prefix_len > 0) e = traced("paged_prefix", s, [&] { return launch_paged_prefix(a, s); });
     if (e == cudaSuccess) e = traced("paged_merge", s, [&] { return launch_paged_merge(a, s); });
     return cuda_status(e);
 }

@@ -31,9 +31,9 @@ namespace usp {
 
 // The kernels follow each other by programmatic dependent launch: a kernel lets its successor's CTAs start as soon as its own
 // have all begun, so that the successor's set-up overlaps with it, and every kernel waits for its predecessor's end, and
-// everything it wrote, before it reads or overwrites any of that.  The own kernel behind a prefix kernel needs nothing of it:
-// it waits at its end only, so that the merge after it sees what both wrote (and the prefix kernel lets it start only after
-// its own wait, so that it has what came before the call).  What a predecessor may have written is read by plain loads, not
+// everything it wrote, before it reads or overwrites any of that.  The prefix kernel, which comes second, needs nothing of the
+// own kernel: it waits at its end only, so that the merge after it sees what both wrote (and the own kernel lets it start only
+// after its own wait, so that it has what came before the call).  What a predecessor may have written is read by plain loads, not
 // through the read-only path, which holds what it likes from before the wait.
 __device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -54,9 +54,9 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// To be called by all threads, before anything is read: `behind_prefix` for the own kernel behind a prefix kernel.
-__device__ __forceinline__ void begin_kernel(bool behind_prefix) {
-    if (!behind_prefix) grid_dependency_wait();
+// To be called by all threads, before anything is read; the prefix kernel waits at its end instead.
+__device__ __forceinline__ void begin_kernel(bool prefix) {
+    if (!prefix) grid_dependency_wait();
     let_dependents_start();
 }
 

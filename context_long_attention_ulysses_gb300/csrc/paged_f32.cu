@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
     __shared__ Share share;
     __shared__ uint32_t s_live[kWarps][S];  // keys of the stage that exist
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
-    begin_kernel(!PREFIX && a.prefix_len > 0);
+    begin_kernel(PREFIX);
     if constexpr (!PREFIX) {
         find_share<M, C::kKeyTile, kPieceCost, kThreads>(a, cta, a.ctas, &share);
         finish_empty_rows<float, M, C::kKeyTile, kThreads>(a, cta, a.ctas);
@@ -300,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
         cur = prefix_piece<M, kKeyTile>(a, cta);
         find_next();
         piece();
+        grid_dependency_wait();  // end after the own kernel
     } else {
         OwnWalk<M, kKeyTile, kPieceCost> walk(a, share);
         if (walk.next(cur)) {
@@ -313,7 +314,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
                 cur = nxt;
             }
         }
-        grid_dependency_wait();  // behind a prefix kernel: end after it
     }
 }
 

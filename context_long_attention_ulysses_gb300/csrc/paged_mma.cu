@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
     const uint32_t full0 = sbase + C::kOffBar, empty0 = full0 + 8 * C::kStages;
     const uint32_t seg_full0 = empty0 + 8 * C::kStages, seg_empty0 = seg_full0 + 8 * kSegs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
-    begin_kernel(!PREFIX && a.prefix_len > 0);
+    begin_kernel(PREFIX);
     Seg pre{};
     if constexpr (PREFIX) pre = prefix_piece<M, kKeyTile>(a, cta);
     if (threadIdx.x == 32 * kConsumers) {
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
             if (!PREFIX && lane == 0) mbar_arrive(seg_empty0 + 8 * si);
         }
     }
-    if constexpr (!PREFIX) grid_dependency_wait();  // behind a prefix kernel: end after it
+    if constexpr (PREFIX) grid_dependency_wait();  // end after the own kernel
 }
 
 template <int D, int MT, bool PREFIX>

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
     constexpr int kProducer = 4 * NS, kIssuer = 4 * NS + 1;
 
-    begin_kernel(!PREFIX && a.prefix_len > 0);
+    begin_kernel(PREFIX);
     Seg pre{};
     uint4 first_q[PREFIX ? D / 8 : 1];  // prefix: a softmax thread's row of Q
     if constexpr (PREFIX) {
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if constexpr (!PREFIX) grid_dependency_wait();  // behind a prefix kernel: end after it
+    if constexpr (PREFIX) grid_dependency_wait();  // end after the own kernel
 }
 
 template <int D, int NS, bool PREFIX>
