@@ -84,11 +84,12 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, const float4& x) {
     *reinterpret_cast<uint2*>(p) = w;
 }
 
-// A CTA joins ROWS = 8 or 1 neighbouring rows of a KV head: thread = (row, four columns, every WAYS-th part), with a
-// running maximum, four parts' reads in flight.  With eight rows the reads of slots kept in column groups are 128 contiguous
-// bytes (a row at a time they would be 16).  A call of few rows has many parts per row, 38 for one sequence of 128K tokens,
-// and is bound by the latency of the reads, so it takes more ways: one after the other these took 15 us.  With few parts
-// per row more ways only cost: 21.9 us against 13.7 for five parts of 6400 rows.
+// A CTA joins ROWS = 4 or 1 neighbouring rows of a KV head: thread = (row, four columns, every WAYS-th part), with a
+// running maximum, four parts' reads in flight.  With four rows the reads of slots kept in column groups are 64 contiguous
+// bytes (a row at a time they would be 16; eight rows were 1 us slower for 64 samples behind a prefix).  A call of few rows has
+// many parts per row, 38 for one sequence of 128K tokens, and is bound by the latency of the reads, so it takes more ways: one
+// after the other these took 15 us.  With few parts per row more ways only cost: 21.9 us against 13.7 for five parts of 6400
+// rows.
 template <typename T, int D, int ROWS, int NT>
 __global__ void __launch_bounds__(NT) paged_merge_kernel(const PagedArgs a) {
     constexpr int kCols = D / 4, kWays = NT / (kCols * ROWS), kAhead = 4;
@@ -234,10 +235,10 @@ static cudaError_t merge_t(const PagedArgs& a, cudaStream_t stream) {
         return launch_dependent(paged_merge_kernel<T, D, 1, 512>, dim3(batch, a.Hkv), 512, 0, stream, a);
     // parts of a row: those of the prefix, and own ones as equal shares give them
     const int64_t units = (int64_t)a.Hkv * std::max(a.n_seqs, (batch + a.rows - 1) / a.rows);
-    const dim3 grid((batch + 7) / 8, a.Hkv);
+    const dim3 grid((batch + 3) / 4, a.Hkv);
     if (a.p_split + a.ctas / units > 8)
-        return launch_dependent(paged_merge_kernel<T, D, 8, 1024>, grid, 1024, 0, stream, a);
-    return launch_dependent(paged_merge_kernel<T, D, 8, 256>, grid, 256, 0, stream, a);
+        return launch_dependent(paged_merge_kernel<T, D, 4, 512>, grid, 512, 0, stream, a);
+    return launch_dependent(paged_merge_kernel<T, D, 4, 256>, grid, 256, 0, stream, a);
 }
 
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream) {
