@@ -87,8 +87,8 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, const float4& x) {
 // A CTA joins ROWS = 4 or 1 neighbouring rows of a KV head: thread = (row, four columns, every WAYS-th part), with a
 // running maximum, four parts' reads in flight.  With four rows the reads of slots kept in column groups are 64 contiguous
 // bytes (a row at a time they would be 16; eight rows were 1 us slower for 64 samples behind a prefix).  A call of few rows has
-// many parts per row, 38 for one sequence of 128K tokens, and is bound by the latency of the reads, so it takes more ways: one
-// after the other these took 15 us.  With few parts per row more ways only cost: 21.9 us against 13.7 for five parts of 6400
+// many parts per row, 38 for one sequence of 128K tokens, and is bound by the latency of the reads, so it takes more ways,
+// unless its slots are in column groups: one after the other these took 15 us.  With few parts per row more ways only cost: 21.9 us against 13.7 for five parts of 6400
 // rows.
 template <typename T, int D, int ROWS, int NT>
 __global__ void __launch_bounds__(NT) paged_merge_kernel(const PagedArgs a) {
@@ -168,6 +168,11 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 struct Pick {
     int rows, keys, ctas, piece;
 };
+// bf16 by the rows per KV head, 32 query and 8 KV heads of 128 values, 16 sequences of 1000 to 20000 tokens:
+//   20 rows: 88.0 us in a unit of 32 (m16n8k16 products), 91.7 in one of 128 (tcgen05); 32 rows: 92.1 and 96.9
+//   48 rows: 98.6 in a unit of 128, 162 in two of 32
+//   64 rows: 101 in one of 128, 110 in one of 256, whose second stream is idle; 96 rows: 107 and 117
+// and 160 rows of 8 sequences: 64 in one of 256, 76 in two of 128.
 static Pick pick(const PagedArgs& a, int64_t rows) {
     if (a.elem == 4) return {8, a.d == 64 ? 128 : 64, kSms, 2};
     if (rows <= 16) return {16, 64, kSms * 2, 2};
@@ -231,7 +236,7 @@ cudaError_t launch_paged_prefix(const PagedArgs& a, cudaStream_t stream) {
 template <typename T, int D>
 static cudaError_t merge_t(const PagedArgs& a, cudaStream_t stream) {
     const int batch = a.n_tokens * a.g;
-    if ((int64_t)batch * a.Hkv <= 8 * kSms)
+    if ((int64_t)batch * a.Hkv <= 8 * kSms && a.rows < 128 && a.p_rows < 128)
         return launch_dependent(paged_merge_kernel<T, D, 1, 512>, dim3(batch, a.Hkv), 512, 0, stream, a);
     // parts of a row: those of the prefix, and own ones as equal shares give them
     const int64_t units = (int64_t)a.Hkv * std::max(a.n_seqs, (batch + a.rows - 1) / a.rows);
