@@ -9,7 +9,8 @@ device memory and streams.
 The helpers ``ulysses_attention_fwd``/``ulysses_attention_bwd`` and
 ``ring_attention_fwd`` chain those calls the way one sequence-parallel
 attention layer does (all-to-all, attention, all-to-all back) and allocate
-their outputs with torch.
+their outputs with torch.  ``kv_append``, ``paged_attention`` and
+``prefix_attention`` serve from a paged key/value cache (:class:`Cache`).
 """
 from __future__ import annotations
 

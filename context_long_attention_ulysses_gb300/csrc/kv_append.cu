@@ -8,8 +8,9 @@
 // Bound by HBM: every value is read once and written once (k twice with k_out).  A head is d / (2 V) items of two 16-byte
 // vectors (V values): the two that a rotation pairs up, or two neighbours where pairs are neighbours or pass unchanged.  A
 // CTA takes as many tokens as make about kItems items; its threads first issue their loads, then find the tokens' slots
-// (two dependent loads) and the tokens' cosines and sines (one per pair, shared by all heads; float64 is scarce here), and
-// only then wait for the data.
+// (two dependent loads) and the tokens' cosines and sines (one per pair, shared by all heads), and only then wait for the
+// data.  Measured: 32768 tokens of 32 query and 8 KV heads of 128 bf16 values, k_out too, 134 us, 6.5 TB/s (0.98 of a copy);
+// one token each of eight sequences 3.5 us in a graph.
 #include <algorithm>
 #include <cmath>
 
@@ -30,9 +31,8 @@ constexpr int kMaxTokens = 16;
 
 // cos and sin of r * f.  Only the fraction of the turns r f / 2 pi counts, so it is formed in 64-bit fixed point, where whole
 // turns fall off the top: f = m 2^-shift with an integer m of 24 bits, the fraction of f / 2 pi is m * (2^64 / 2 pi) >> shift
-// to 64 bits, and times r, up to 2^31, it is off by less than 2^-30 turns for f up to 8.
-// (The scarce float64 units took 3.5 of 144 us for a prompt of
-// 32768 tokens; they remain for f of 2^24 and more, infinities and NaN.)
+// to 64 bits, and times r, up to 2^31, it is off by less than 2^-30 turns for f up to 8.  (The scarce float64 units took 3.5 of
+// 144 us for a prompt of 32768 tokens; they remain for f of 2^24 and more, infinities and NaN.)
 __device__ __forceinline__ float2 turn(int r, float f) {
     const uint32_t bits = __float_as_uint(f) & 0x7fffffffu;
     const int exponent = (int)(bits >> 23), shift = 150 - exponent;
