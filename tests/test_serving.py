@@ -545,6 +545,74 @@ def test_lengths_and_starts_out_of_range_stay_inside(usp, prefix):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decoding_steps_between_other_work(usp, dtype):
+    """A whole decoding step, with tensor operations before, between and after the calls (each call reads what the one
+    before it wrote, and the step after overwrites it): eager steps, and one captured step replayed, give the same bits as
+    steps that are waited for one by one."""
+    import torch
+    B, Hq, Hkv, d, page, steps = 5, 8, 2, 64, 16, 12
+    c = usp.Cache(B * 8, page, B, 8, Hq, Hkv, d, dtype=dtype)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    gen = torch.Generator().manual_seed(1)
+    table = torch.randperm(c.n_pages, generator=gen).int().view(B, 8).cuda()
+    x = torch.randn((steps, B, (Hq + 2 * Hkv) * d), generator=gen).to(c.torch_dtype).cuda()
+    inv = (10000.0 ** (-torch.arange(d // 2, dtype=torch.float64) / (d // 2))).float().cuda()
+    pre = table[0, :1].contiguous()
+    ws = torch.empty(usp.usp_prefix_attn_workspace_size(c, B, 1, page), dtype=torch.uint8, device="cuda")
+
+    class Run:
+        def __init__(self):
+            self.kp, self.vp = (torch.zeros(c.pool_shape(), dtype=c.torch_dtype, device="cuda") for _ in range(2))
+            self.pos, self.seq = torch.full((B,), page + 3, **i32), torch.arange(B, **i32)
+            self.x, self.o = torch.zeros_like(x[0]), torch.zeros((B, Hq, d), dtype=c.torch_dtype, device="cuda")
+            self.q, self.lse = torch.zeros_like(self.o), torch.zeros((B, Hq), device="cuda")
+            self.total = torch.zeros((B, Hq, d), device="cuda")
+
+        def step(self, wait=False):
+            sync = torch.cuda.synchronize if wait else lambda: None
+            y = self.x + self.o.view(B, -1).repeat(1, 2)[:, :self.x.shape[1]]        # the answer before goes into this token
+            sync()
+            q, k, v = (t.view(B, -1, d) for t in y.split([Hq * d, Hkv * d, Hkv * d], 1))
+            usp.usp_kv_append(c, B, q, k, v, self.seq, self.pos, inv, self.q, None, self.kp, self.vp, table, rot=d)
+            sync()
+            self.pos += 1
+            sync()
+            usp.usp_paged_attn(c, B, 1, self.q, self.kp, self.vp, table, self.pos, None, self.o, self.lse, ws)
+            sync()
+            self.total += self.o.float()
+            sync()
+            usp.usp_prefix_attn(c, B, 1, self.o, self.kp, self.vp, table, self.pos, None, pre, page, self.q, self.lse, ws)
+            usp.usp_paged_attn(c, B, 1, self.q, self.kp, self.vp, table, self.pos, None, self.o, self.lse, ws)
+            sync()
+            self.total += self.o.float()
+
+    runs = []
+    for kind in ("waited", "eager", "graph"):
+        r = Run()
+        if kind == "graph":
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            warm = Run()
+            with torch.cuda.stream(s):
+                warm.step()
+            s.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                r.step()
+        for i in range(steps):
+            r.x.copy_(x[i])
+            g.replay() if kind == "graph" else r.step(kind == "waited")
+        torch.cuda.synchronize()
+        assert usp.usp_device_status() == 0
+        runs.append((r.total, r.kp, r.vp, r.lse))
+    assert torch.isfinite(runs[0][0]).all() and runs[0][0].abs().max() > 0
+    for other in runs[1:]:
+        for a, b in zip(runs[0], other):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("prefix", [0, 500])
 def test_captured_graph_replays_with_new_lengths(usp, prefix):
     """One capture serves every later step: tables, lengths and starts are read on the device."""
