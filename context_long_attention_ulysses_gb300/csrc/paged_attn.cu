@@ -86,10 +86,10 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, const float4& x) {
 
 // A CTA joins ROWS = 4 or 1 neighbouring rows of a KV head: thread = (row, four columns, every WAYS-th part), with a
 // running maximum, four parts' reads in flight.  With four rows the reads of slots kept in column groups are 64 contiguous
-// bytes (a row at a time they would be 16; eight rows were 1 us slower for 64 samples behind a prefix).  A call of few rows has
-// many parts per row, 38 for one sequence of 128K tokens, and is bound by the latency of the reads, so it takes more ways,
-// unless its slots are in column groups: one after the other these took 15 us.  With few parts per row more ways only cost: 21.9 us against 13.7 for five parts of 6400
-// rows.
+// bytes (a row at a time they would be 16; eight rows were 1 us slower for 64 samples behind a prefix).  A call of few rows
+// has many parts per row, 38 for one sequence of 128K tokens, and is bound by the latency of the reads, so it takes more
+// ways, unless its slots are in column groups: one after the other these took 15 us.  With few parts per row more ways only
+// cost: two instead of one, 40 us against 21 for the two parts of 65536 rows, 10 against 9 for five parts of 6400.
 template <typename T, int D, int ROWS, int NT>
 __global__ void __launch_bounds__(NT) paged_merge_kernel(const PagedArgs a) {
     constexpr int kCols = D / 4, kWays = NT / (kCols * ROWS), kAhead = 4;
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(NT) paged_merge_kernel(const PagedArgs a) {
         for (int u = 0; u < kAhead; ++u) {
             const int c = c0 + u * kWays;
             f[u] = c < p.n ? part_lse(p, c) : -INFINITY;
-            x[u] = part_cols(p, c < p.n ? c : c0, c4);
+            x[u] = c < p.n ? part_cols(p, c, c4) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) m = fmaxf(m, f[u]);
@@ -243,7 +243,7 @@ static cudaError_t merge_t(const PagedArgs& a, cudaStream_t stream) {
     const dim3 grid((batch + 3) / 4, a.Hkv);
     if (a.p_split + a.ctas / units > 8)
         return launch_dependent(paged_merge_kernel<T, D, 4, 512>, grid, 512, 0, stream, a);
-    return launch_dependent(paged_merge_kernel<T, D, 4, 256>, grid, 256, 0, stream, a);
+    return launch_dependent(paged_merge_kernel<T, D, 4, 128>, grid, 128, 0, stream, a);
 }
 
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream) {
