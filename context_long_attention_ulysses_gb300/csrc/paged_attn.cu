@@ -154,9 +154,9 @@ __global__ void __launch_bounds__(NT) paged_merge_kernel(const PagedArgs a) {
         }
     }
     if (done) return;
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;  // (NaN has to show)
     put4(static_cast<T*>(a.o) + row * D + c4 * 4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-    if (c4 == 0) a.lse[row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+    if (c4 == 0) a.lse[row] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }

@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_f32_kernel(const PagedArgs 
                 o.z = fmaf(f, y.z, o.z);
                 o.w = fmaf(f, y.w, o.w);
             }
-            const bool has = sum > 0.f;
+            const bool has = sum != 0.f;  // (NaN, too, which has to show)
             o = has ? make_float4(o.x / sum, o.y / sum, o.z / sum, o.w / sum) : make_float4(0.f, 0.f, 0.f, 0.f);
             const float lse2 = has ? ms + log2f(sum) : -INFINITY;
             const RowDst dst = row_dst<M, PREFIX>(a, g, r, cta);

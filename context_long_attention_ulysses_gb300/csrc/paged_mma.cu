@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
                     sum += e * s_l[w * 16 + rr];
                     sum_r += e * s_lr[w * 16 + rr];
                 }
-                const bool has = sum_r > 0.f;
+                const bool has = sum_r != 0.f;  // (NaN, too, which has to show)
                 const float inv = has ? 1.f / sum_r : 0.f;
                 const float lse2 = has ? mx + log2f(sum) : -INFINITY;
                 const float* src = s_join + rr * C::kJoinStride + cc;

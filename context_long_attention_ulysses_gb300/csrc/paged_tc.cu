@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                 ++pieces;
                 tc_fence_after();
             }
-            const bool has = n_tiles > 0 && l_run > 0.f;
+            const bool has = n_tiles > 0 && l_run != 0.f;  // (NaN, too, which has to show)
             const float inv = has ? 1.f / l_run : 0.f;
             const float lse2 = has ? m_run + log2f(l_run) : -INFINITY;
             const RowDst dst = row_dst<M, PREFIX, true>(a, g, valid ? r : 0, cta);

@@ -476,7 +476,8 @@ size_t usp_paged_attn_workspace_size(const usp_cache* c, int n_tokens, int max_q
  * max_pages*page_size]; keys of a page table entry outside [0, n_pages) are
  * left out.  What pages hold beyond a sequence's length (NaN, too) never
  * reaches a result.  A value that is not finite in a key or value below len
- * may reach every row of its sequence, masked or not (0 * inf in the product).
+ * may reach every row of its sequence, masked or not (0 * inf in the product);
+ * a NaN in a query makes that row's o and lse NaN.
  * BF16: float32 scores, sums and accumulation, probabilities rounded to bf16
  * for the product with V; F32: float32 throughout, on CUDA cores.  Results do
  * not depend on the run (fixed order of sums).

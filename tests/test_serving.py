@@ -637,6 +637,39 @@ def test_captured_graph_replays_with_new_lengths(usp, prefix):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("prefix", [0, 300])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 6, 20, 70])
+def test_nan_of_a_query_or_key_shows(usp, n, dtype, prefix):
+    """A NaN in a row of q makes that row's output and log-sum-exp NaN, a NaN in a key those of the rows that see it
+    (and no other sequence's, nor another KV head's); nothing turns it into zeros.  Other rows keep their bits."""
+    import torch
+    guard = Guarded()
+    b = Batch([(n, 3000), (n, 400), (n, prefix + n)], 8, 2, 128, 64, dtype, prefix=prefix).to_gpu(usp, guard)
+    o, lse = (x.clone() for x in b.run(usp))
+    _done(usp, guard)
+    b.check()
+    last = torch.zeros((b.T, 8), dtype=torch.bool, device="cuda")
+    last[n - 1, 1] = last[2 * n - 1, 6] = last[3 * n - 1, 0] = True
+    b.g["q"][last] = float("nan")
+    for y, was in zip(b.run(usp), (o, lse)):
+        _done(usp, guard)
+        assert torch.isnan(y[last]).all()
+        assert torch.equal(y[~last], was[~last])
+    b.g["q"].copy_(b.q)
+    page, at = b.table[1, 399 // 64], 399 % 64  # the last key of the second sequence, seen by its last token only
+    b.g["kp"][int(page), 1, at, 5] = float("nan")
+    hit = torch.zeros_like(last)
+    hit[2 * n - 1, 4:] = True
+    for y, was in zip(b.run(usp), (o, lse)):
+        _done(usp, guard)
+        assert torch.isnan(y[hit]).all()
+        others = torch.ones_like(last)
+        others[n:2 * n, 4:] = False
+        assert torch.equal(y[others], was[others])
+
+
+@pytest.mark.gpu
 def test_two_streams_at_once(usp):
     import torch
     guard = Guarded()
