@@ -52,6 +52,8 @@ __device__ __forceinline__ Parts row_parts(const PagedArgs& a, int t, int h, int
         p.ol = a.own_lse + row;
     } else if (kind == kRowSplit) {
         const int c0 = info.y & 0xffffu, c1 = info.y >> 16, r = info.x >> 2;
+        // A kernel whose wait gave up has not noted its rows: what the workspace held instead leads nowhere outside it.
+        if (c0 > c1 || c1 >= a.ctas || r >= a.rows) return p;
         const bool groups = a.rows >= 128;
         p.n += c1 - c0 + 1;
         p.ol = a.slot_l + ((int64_t)c0 * 2 + 1) * a.rows + r;

@@ -772,6 +772,24 @@ def test_abort_path_gives_up_fast_and_recovers(usp):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fill", [0xFF, 0x03, 0x7F])
+def test_abort_with_a_workspace_that_holds_anything(usp, fill):
+    """After a kernel that gave up, the merge finds whatever the workspace held where rows should be noted; it stays
+    inside the workspace, and the next run is right."""
+    guard = Guarded()
+    for seqs, Hq, Hkv, d, p in [([(70, 900), (3, 10)], 8, 2, 128, 0), ([(300, 2000)], 4, 1, 64, 300),
+                                ([(40, 5000)], 8, 2, 128, 100), ([(1, 3000)], 8, 2, 64, 0)]:
+        b = Batch(seqs, Hq, Hkv, d, 64, prefix=p).to_gpu(usp, guard)
+        b.g["ws"].fill_(fill)
+        usp.usp_diag_raise_status()
+        b.run(usp)
+        assert usp.usp_device_status() == _lib.USP_ERR_TIMEOUT
+        b.run(usp)
+        _done(usp, guard)
+        b.check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,d,page", [("bf16", 128, 64), ("f32", 64, 16)])
 def test_pool_beyond_32_bit_offsets(usp, dtype, d, page):
     """Pages whose elements lie beyond 2^31 of the pool."""
