@@ -14,6 +14,7 @@ their outputs with torch.  ``kv_append``, ``paged_attention`` and
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from dataclasses import dataclass
@@ -656,23 +657,31 @@ def _serving_device(x):
     return x.device
 
 
-def _used_on(stream, *tensors) -> None:
-    """Tensors allocated on the current stream and used on another: the allocator must not hand them out before."""
+def _made_on(stream):
+    """Context in which a helper makes its outputs and its workspace: the stream that writes them.  (Memory freed on the
+    current stream may still be in use there, and must not be handed to a kernel on another.)"""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
+def _returned(stream, *tensors) -> None:
+    """Outputs made on `stream` go to a caller on the current one: the allocator must not hand them out before it is done."""
     if stream is None:
         return
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    if s.cuda_stream == torch.cuda.current_stream().cuda_stream:
+    current = torch.cuda.current_stream()
+    if current.cuda_stream == (stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)):
         return
     for t in tensors:
         if t is not None:
-            t.record_stream(s)
+            t.record_stream(current)
 
 
 def kv_append(c: Cache, q, k, v, seq, pos, inv_freq, k_pages, v_pages, page_table, interleaved=False, rot_pos=None,
               stream=None):
     """Rotate q and k by their positions and write k and v into the cache (usp_kv_append).
 
-    q [T][Hq][d] (or None), k, v [T][Hkv][d], any token stride; seq, pos (and rot_pos) int32 [T]; inv_freq float32
+    q [T][Hq][d] (or None), k, v [T][Hkv][d], any token stride (they and the rest must be ready on `stream`); seq, pos (and rot_pos) int32 [T]; inv_freq float32
     [rot/2] or None.  Returns (rotated q or None, rotated k); rows of padding tokens hold what torch.empty left."""
     dev, dt = _serving_device(k), c.torch_dtype
     T = k.shape[0]
@@ -686,12 +695,13 @@ def kv_append(c: Cache, q, k, v, seq, pos, inv_freq, k_pages, v_pages, page_tabl
     _check(c, "k_pages", k_pages, c.pool_shape(), dt, dev)
     _check(c, "v_pages", v_pages, c.pool_shape(), dt, dev)
     _check(c, "page_table", page_table, c.table_shape(), torch.int32, dev)
-    q_out = None if q is None else _empty((T, c.Hq, c.d), dt, dev)
-    k_out = _empty((T, c.Hkv, c.d), dt, dev)
+    with _made_on(stream):
+        q_out = None if q is None else _empty((T, c.Hq, c.d), dt, dev)
+        k_out = _empty((T, c.Hkv, c.d), dt, dev)
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
     usp_kv_append(c, T, q, k, v, seq, pos, inv_freq, q_out, k_out, k_pages, v_pages, page_table, rot, interleaved,
                   rot_pos, stream)
-    _used_on(stream, q_out, k_out)
+    _returned(stream, q_out, k_out)
     return q_out, k_out
 
 
@@ -713,10 +723,12 @@ def paged_attention(c: Cache, q, k_pages, v_pages, page_table, seq_lens, q_start
     sequence has in this call.  Rows of no sequence hold what torch.empty left."""
     dev, dt = _check_paged(c, q, k_pages, v_pages, page_table, seq_lens, q_start)
     T = q.shape[0]
-    o, lse = _empty((T, c.Hq, c.d), dt, dev), _empty((T, c.Hq), torch.float32, dev)
-    ws = torch.empty(max(usp_paged_attn_workspace_size(c, T, max_q), 256), dtype=torch.uint8, device=dev)
+    size = usp_paged_attn_workspace_size(c, T, max_q)
+    with _made_on(stream):
+        o, lse = _empty((T, c.Hq, c.d), dt, dev), _empty((T, c.Hq), torch.float32, dev)
+        ws = _empty((max(size, 256),), torch.uint8, dev)
     usp_paged_attn(c, T, max_q, q, k_pages, v_pages, page_table, seq_lens, q_start, o, lse, ws, None, stream)
-    _used_on(stream, o, lse, ws)
+    _returned(stream, o, lse)
     return o, lse
 
 
@@ -729,10 +741,11 @@ def prefix_attention(c: Cache, q, k_pages, v_pages, page_table, seq_lens, prefix
     if prefix_pages.numel() < c.pages_for(prefix_len):
         raise ValueError(f"prefix_pages: {prefix_pages.numel()} pages do not hold {prefix_len} tokens")
     T = q.shape[0]
-    o, lse = _empty((T, c.Hq, c.d), dt, dev), _empty((T, c.Hq), torch.float32, dev)
     size = usp_prefix_attn_workspace_size(c, T, max_q, prefix_len)
-    ws = torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
+    with _made_on(stream):
+        o, lse = _empty((T, c.Hq, c.d), dt, dev), _empty((T, c.Hq), torch.float32, dev)
+        ws = _empty((max(size, 256),), torch.uint8, dev)
     usp_prefix_attn(c, T, max_q, q, k_pages, v_pages, page_table, seq_lens, q_start, prefix_pages, prefix_len, o, lse,
                     ws, None, stream)
-    _used_on(stream, o, lse, ws)
+    _returned(stream, o, lse)
     return o, lse

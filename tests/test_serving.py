@@ -670,6 +670,44 @@ def test_nan_of_a_query_or_key_shows(usp, n, dtype, prefix):
 
 
 @pytest.mark.gpu
+def test_captured_fork_and_join(usp):
+    """A captured step whose appending runs on a stream of its own beside other work, and whose attention waits for both."""
+    import torch
+    guard = Guarded()
+    b = Batch([(1, 600), (1, 650), (1, 520)], 8, 2, 128, 64, seed=3).to_gpu(usp, guard)
+    g, c = b.g, b.c
+    k, v = (torch.empty((3, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pos, seq = g["lens"] - 1, torch.arange(3, dtype=torch.int32, device="cuda")
+    for s in range(3):  # the newest key and value of each sequence arrive through the graph
+        page, at = int(b.table[s, (b.lens[s] - 1) // 64]), int(b.lens[s] - 1) % 64
+        k[s], v[s] = g["kp"][page, :, at], g["vp"][page, :, at]
+        g["kp"][page, :, at] = g["vp"][page, :, at] = float("nan")
+    q_in = g["q"].clone()
+    b.run(usp)  # (before any capture: the library makes its status word with the first call)
+    g["q"].zero_()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def step():
+        side.wait_stream(main)
+        usp.usp_kv_append(c, 3, None, k, v, seq, pos, None, None, None, g["kp"], g["vp"], g["table"], stream=side)
+        g["q"].copy_(q_in)
+        main.wait_stream(side)
+        b.run(usp)
+        side.wait_stream(main)
+        main.wait_stream(side)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        step()
+    for _ in range(3):
+        g["o"].fill_(7.0)
+        graph.replay()
+        _done(usp, guard)
+        b.check()
+
+
+@pytest.mark.gpu
 def test_two_streams_at_once(usp):
     import torch
     guard = Guarded()
@@ -837,6 +875,35 @@ def test_helpers(usp):
         usp.prefix_attention(b.c, g["q"], g["kp"], g["vp"], g["table"], g["lens"], g["prefix"], 129)
     with pytest.raises(ValueError):
         usp.paged_attention(b.c, g["q"].float(), g["kp"], g["vp"], g["table"], g["lens"])
+
+
+@pytest.mark.gpu
+def test_helpers_on_a_side_stream_leave_freed_memory_alone(usp):
+    """Memory that was freed on the current stream is still being written there when a helper makes its outputs for
+    another stream; and outputs freed here are not handed out there while this stream reads them."""
+    import torch
+    guard = Guarded()
+    b = Batch([(1, 200), (1, 190), (1, 129)], 8, 2, 128, 64).to_gpu(usp, guard)
+    g, c = b.g, b.c
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    sizes = [b.T * c.Hq * c.d * 2, b.T * c.Hq * 4, usp.usp_paged_attn_workspace_size(c, b.T, 1)]
+    for handle in (side, side.cuda_stream):
+        xs = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+        torch.cuda._sleep(40_000_000)  # some 20 ms
+        for x in xs:
+            x.fill_(0x7F)
+        del x, xs
+        o, lse = usp.paged_attention(c, g["q"], g["kp"], g["vp"], g["table"], g["lens"], stream=handle)
+        side.synchronize()
+        torch.cuda.synchronize()
+        b.check(o, lse)
+        torch.cuda._sleep(40_000_000)
+        late_o, late_l = o + 0, lse + 0
+        del o, lse
+        usp.paged_attention(c, torch.zeros_like(g["q"]), g["kp"], g["vp"], g["table"], g["lens"], stream=handle)
+        torch.cuda.synchronize()
+        b.check(late_o, late_l)
 
 
 @pytest.mark.gpu
