@@ -1229,8 +1229,8 @@ static usp_status check_cache(const usp_cache* c) {
     const int ps = c->page_size;
     if (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256) return USP_ERR_UNSUPPORTED;
     if (c->d != 64 && c->d != 128) return USP_ERR_UNSUPPORTED;
-    // (positions rounded up to whole tiles, and rows of the pool's outer dimension, are ints)
-    if (c->Hq > 65535 || (int64_t)c->max_pages * ps > INT32_MAX - 1023 || (int64_t)c->n_pages * c->Hkv > INT32_MAX)
+    // (positions and sequences rounded up to whole tiles and scans, and rows of the pool's outer dimension, are ints)
+    if (c->Hq > 65535 || c->n_seqs > INT32_MAX - 1023 || (int64_t)c->max_pages * ps > INT32_MAX - 1023 || (int64_t)c->n_pages * c->Hkv > INT32_MAX)
         return USP_ERR_UNSUPPORTED;
     return USP_OK;
 }

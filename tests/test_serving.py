@@ -272,7 +272,7 @@ def _status(call, /, *a, **kw):
     (dict(Hq=5), 1), (dict(scale=-1.0), 1), (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1),
     (dict(page_size=24), 2), (dict(page_size=8), 2), (dict(page_size=512), 2), (dict(d=96), 2),
     (dict(Hq=65536, Hkv=1), 2), (dict(max_pages=1 << 27), 2), (dict(max_pages=(1 << 27) - 63), 2),
-    (dict(n_pages=1 << 30, Hkv=4), 2)])
+    (dict(n_pages=1 << 30, Hkv=4), 2), (dict(n_seqs=(1 << 31) - 1), 2)])
 def test_cache_shapes_are_refused(lib, kw, code):
     for f in (_append, _paged):
         assert _status(f, _c(**kw)) == code
