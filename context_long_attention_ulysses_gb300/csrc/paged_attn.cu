@@ -171,14 +171,14 @@ struct Pick {
     int rows, keys, ctas, piece;
 };
 // bf16 by the rows per KV head, 32 query and 8 KV heads of 128 values, 16 sequences of 1000 to 20000 tokens:
-//   20 rows: 88.0 us in a unit of 32 (m16n8k16 products), 91.7 in one of 128 (tcgen05); 32 rows: 92.1 and 96.9
+//   20 rows: 84.0 us in a unit of 32 (m16n8k16 products), 91.7 in one of 128 (tcgen05); 32 rows: 85.1 and 96.9
 //   48 rows: 98.6 in a unit of 128, 162 in two of 32
 //   64 rows: 101 in one of 128, 110 in one of 256, whose second stream is idle; 96 rows: 107 and 117
 // and 160 rows of 8 sequences: 64 in one of 256, 76 in two of 128.
 static Pick pick(const PagedArgs& a, int64_t rows) {
     if (a.elem == 4) return {8, a.d == 64 ? 128 : 64, kSms, 2};
-    if (rows <= 16) return {16, 64, kSms * 2, 2};
-    if (rows <= 32) return {32, 64, kSms, 4};
+    if (rows <= 16) return a.d == 64 ? Pick{16, 128, kSms * 2, 3} : Pick{16, 64, kSms * 2, 2};
+    if (rows <= 32) return {32, 128, kSms, 3};
     return {rows <= 128 ? 128 : 256, 128, kSms, 3};
 }
 

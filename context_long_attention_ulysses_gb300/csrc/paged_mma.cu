@@ -2,15 +2,15 @@
 //
 // With up to 32 rows per KV head the work is reading K and V once: 2 d bf16 values per key against 4 d M flops, 16 to 32
 // flops a byte, far below what the tensor cores could do with it.  So the kernel is built around the loads:
-//   last warp    producer: every tile of 64 keys, K and V, comes by TMA from its pages into a ring of stages
-//   4 MT warps   a group of four per 16 rows, each warp with 16 keys of each tile: S = Q K^T (m16n8k16, Q in registers), the
-//                running maximum and sum of the softmax, O += P V -- no warp waits for another while keys go by; a group's
-//                four partial results are joined through shared memory where a piece ends.
+//   last warp    producer: every tile of 64 or 128 keys, K and V, comes by TMA from its pages into a ring of stages
+//   4 MT warps   a group of four per 16 rows, each warp with 16 or 32 keys of each tile: S = Q K^T (m16n8k16, Q in
+//                registers), the running maximum and sum of the softmax, O += P V -- no warp waits for another while keys go
+//                by; a group's four partial results are joined through shared memory where a piece ends.
 // Up to 16 rows: two CTAs per SM, so that one loads while the other joins, stores or begins a piece.  Up to 32: one CTA with
 // twice the stages (four warps with 32 rows each, two CTAs, spilled: 123 us for five tokens of 16 sequences).
 //
 // The pool is one tensor map (column, KV head, token of the page, page); a box holds min(page_size, 32) tokens, so that a
-// tile is 2 or 4 boxes per 64 columns, issued by as many lanes.  Boxes without a visible key, or of a page that the pool
+// tile is 2 to 8 boxes per 64 columns, issued by as many lanes.  Boxes without a visible key, or of a page that the pool
 // does not have, are not loaded: their keys are left out by the warps that own them.
 //
 // Measured, 32 query and 8 KV heads of 128 values: one token of one sequence of 131072 in 83 us, 6.5 TB/s; of 64 sequences of 17
@@ -26,11 +26,6 @@ namespace usp {
 
 namespace {
 
-constexpr int kKeyTile = 64;  // keys per tile
-// A piece's beginning and end (rows of Q, the join, the stores) cost about 3 us; a tile takes a CTA 1.5 us at the memory's
-// rate where two share the SM, 0.75 us where it has the SM to itself.
-template <int MT>
-constexpr int kPieceCost = MT == 1 ? 2 : 4;
 constexpr int kGroup = 4;  // warps that share 16 rows
 // Keys of a box at most.  Smaller boxes read less beyond a sequence's ends (200 sequences of about 750 own keys behind a prefix:
 // 128 us against 133 with boxes of 64), but boxes of 16 keep the producer too busy where one CTA has the SM (107 us against 91
@@ -42,12 +37,21 @@ constexpr float kRescale = 8.0f;  // log2 units: O is rescaled only when the max
 template <int D, int MT>
 struct Cfg {
     static constexpr int M = 16 * MT;
+    // Steps of 16 keys of a warp per tile.  Two hide each other's latency and share the maximum's exchange, where the ring
+    // allows for larger tiles: five tokens of 16 sequences 84.0 us against 88.0, one of 64 sequences with heads of 64 values 85.7
+    // against 100.  (16 rows of 128 values would have stages of 64 KB, one and a half per CTA.)
+    static constexpr int KS = D == 64 ? 2 : MT;
+    static constexpr int kKeyTile = 16 * KS * kGroup;
+    // Places that a piece's beginning and end (rows of Q, the join, the stores) count, in tiles.  It takes about 3 us, a tile of
+    // 64 keys 1.5 us at the memory's rate where two CTAs share the SM.  With two steps: 88.4, 84.5, 84.0, 83.8, 84.3 us for
+    // five tokens of 16 sequences at 1 to 5, and 37.8 at 2, 38.0 at 3, 39.6 at 4 for those of 64 short ones.
+    static constexpr int kPieceCost = KS == 1 ? 2 : 3;
     static constexpr int kConsumers = kGroup * MT;
     static constexpr int kThreads = 32 * (kConsumers + 1);
     static constexpr int kCtasPerSm = MT == 1 ? 2 : 1;
     static constexpr int kChunks = D / 64;                                    // 64-column boxes per row
     static constexpr int kTileBytes = kKeyTile * D * 2;                       // K or V of a tile
-    static constexpr int kStages = (D == 128 ? 3 : 6) * (MT == 1 ? 1 : 2);    // 192 KB in flight per SM
+    static constexpr int kStages = D == 64 ? 3 * MT : 3;                      // 192 KB in flight per SM
     static constexpr int kJoinStride = D + 8;                                 // float32 per row: rows in different banks
     static constexpr int kJoinBytes = 16 * kJoinStride * 4;                   // per group
     static constexpr int kOffJoin = kStages * 2 * kTileBytes;
@@ -85,7 +89,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
     paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const PagedArgs a) {
     using C = Cfg<D, MT>;
-    constexpr int M = C::M, kThreads = C::kThreads, kConsumers = C::kConsumers;
+    constexpr int M = C::M, kThreads = C::kThreads, kConsumers = C::kConsumers, kKeyTile = C::kKeyTile, KS = C::KS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -118,7 +122,8 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
     if constexpr (PREFIX) {
         __syncthreads();
     } else {
-        find_share<M, kKeyTile, kPieceCost<MT>, kThreads>(a, cta, a.ctas, &share);  // holds the barrier that publishes the set-up, too
+        // (holds the barrier that publishes the set-up, too)
+        find_share<M, kKeyTile, C::kPieceCost, kThreads>(a, cta, a.ctas, &share);
         finish_empty_rows<__nv_bfloat16, M, kKeyTile, kThreads>(a, cta, a.ctas);
         __syncthreads();
     }
@@ -178,7 +183,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
         if constexpr (PREFIX) {
             piece(g);
         } else {
-            OwnWalk<M, kKeyTile, kPieceCost<MT>> walk(a, share);
+            OwnWalk<M, kKeyTile, C::kPieceCost> walk(a, share);
             while (walk.next(g) && piece(g)) {}
         }
         g.n_tiles = 0;
@@ -186,16 +191,16 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
         if (lane == 0) drain_ring(full0, C::kStages, it, 22, a.status);  // every load has landed before the CTA exits
     } else {
         // ---------------------------------------------------------------- consumers
-        const int group = warp / kGroup, kw = warp % kGroup;  // rows 16 * group .., keys 16 * kw .. of each tile
+        const int group = warp / kGroup, kw = warp % kGroup;  // rows 16 * group .., keys 16 KS * kw .. of each tile
         const int r0 = lane >> 2, c0 = (lane & 3) * 2;        // this lane's first row and column of a fragment
-        const int box_of_warp = kw * 16 / min(1 << a.page_log2, kBox);
+        const int box_log2 = min(a.page_log2, 5);  // of kBox
         float* s_m = reinterpret_cast<float*>(smem + C::kOffStat) + group * 3 * kGroup * 16;
         float* s_l = s_m + kGroup * 16;
         float* s_lr = s_l + kGroup * 16;
         float* s_join = reinterpret_cast<float*>(smem + C::kOffJoin + group * C::kJoinBytes);
         // ldmatrix rows of this lane: K (key, 16-byte column) and V transposed
-        const int k_key = kw * 16 + ((lane >> 4) << 3) + (lane & 7), k_c = (lane >> 3) & 1;
-        const int v_key = kw * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), v_c = lane >> 4;
+        const int k_key = kw * 16 * KS + ((lane >> 4) << 3) + (lane & 7), k_c = (lane >> 3) & 1;
+        const int v_key = kw * 16 * KS + (((lane >> 3) & 1) << 3) + (lane & 7), v_c = lane >> 4;
         int it = 0;
         bool ok = true;
         for (int n_seg = 0; !PREFIX || n_seg == 0; ++n_seg) {
@@ -238,43 +243,56 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
                 const int st = it % C::kStages;
                 ok = ok && mbar_wait(full0 + 8 * st, (it / C::kStages) & 1, abort_p, 23, a.status);
                 ok = __all_sync(~0u, ok);
-                const int key0 = (tile0 + x) * kKeyTile + kw * 16;  // this warp's keys key0 .. key0 + 15
-                if (ok && rows_here && key0 < end && key0 + 16 > first && (s_boxes[st] >> box_of_warp & 1u)) {
-                    const uint32_t kb = sbase + st * 2 * C::kTileBytes, vb = kb + C::kTileBytes;
-                    float s[2][4];
+                const int key0 = (tile0 + x) * kKeyTile + kw * 16 * KS;  // this warp's keys key0 .. key0 + 16 KS - 1
+                uint32_t live = 0;  // steps whose box was loaded
+                if (ok && rows_here && key0 < end && key0 + 16 * KS > first) {
+                    const uint32_t boxes = s_boxes[st];
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int u = 0; u < KS; ++u) live |= (boxes >> ((kw * KS + u) * 16 >> box_log2) & 1u) << u;
+                }
+                if (live) {
+                    const uint32_t kb = sbase + st * 2 * C::kTileBytes, vb = kb + C::kTileBytes;
+                    float s[2 * KS][4];
+#pragma unroll
+                    for (int n = 0; n < 2 * KS; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        uint32_t b[4];
-                        ldsm4(kb + (kk / 4) * (kKeyTile * 128) + k_key * 128 +
-                                  ((((kk & 3) * 2 + k_c) ^ (k_key & 7)) << 4), b);
-                        mma16816(s[0], q[kk], b[0], b[1]);
-                        mma16816(s[1], q[kk], b[2], b[3]);
-                    }
-                    // ---- masks: only where a key of these 16 is hidden from some row
-                    uint32_t vm[2] = {~0u, ~0u};
-                    if (key0 + 16 > lim_min || key0 + 16 > end || key0 < first) {
+                    for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) {
+                        for (int u = 0; u < KS; ++u) {
+                            uint32_t b[4];
+                            ldsm4(kb + (kk / 4) * (kKeyTile * 128) + (k_key + u * 16) * 128 +
+                                      ((((kk & 3) * 2 + k_c) ^ (k_key & 7)) << 4), b);
+                            mma16816(s[2 * u], q[kk], b[0], b[1]);
+                            mma16816(s[2 * u + 1], q[kk], b[2], b[3]);
+                        }
+                    // ---- masks: only where one of these keys is hidden from some row
+                    uint32_t vm[KS][2];
+#pragma unroll
+                    for (int u = 0; u < KS; ++u) vm[u][0] = vm[u][1] = ~0u;
+                    if (key0 + 16 * KS > lim_min || key0 + 16 * KS > end || key0 < first || live != (1u << KS) - 1u) {
+#pragma unroll
+                        for (int n = 0; n < 2 * KS; ++n) {
+                            const bool there = live >> (n / 2) & 1u;
                             const int key = key0 + n * 8 + c0;
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                if (key + (e & 1) >= lim[e >> 1] || key + (e & 1) < first) s[n][e] = -INFINITY;
+                                if (!there || key + (e & 1) >= lim[e >> 1] || key + (e & 1) < first) s[n][e] = -INFINITY;
                             // what lies beyond the sequence in its last page may be NaN: 0 * NaN must not reach O
-                            if (key >= end || key < first) vm[n] &= 0xffff0000u;
-                            if (key + 1 >= end || key + 1 < first) vm[n] &= 0x0000ffffu;
+                            if (!there || key >= end || key < first) vm[n / 2][n & 1] &= 0xffff0000u;
+                            if (!there || key + 1 >= end || key + 1 < first) vm[n / 2][n & 1] &= 0x0000ffffu;
                         }
                     }
                     // ---- softmax
-                    uint32_t p[4];
+                    uint32_t p[KS][4];
                     bool grew = false;
                     float al[2];
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
-                        float mx = fmaxf(fmaxf(s[0][2 * hh], s[0][2 * hh + 1]), fmaxf(s[1][2 * hh], s[1][2 * hh + 1]));
+                        float mx = fmaxf(s[0][2 * hh], s[0][2 * hh + 1]);
+#pragma unroll
+                        for (int n = 1; n < 2 * KS; ++n) mx = fmaxf(mx, fmaxf(s[n][2 * hh], s[n][2 * hh + 1]));
                         mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
                         mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
                         mx *= a.scale_log2;
@@ -283,17 +301,24 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
                         if (up) m[hh] = mx;
                         grew |= up;
                         const float ms = m[hh] == -INFINITY ? 0.f : m[hh];
-                        const float e0 = ex2_approx(fmaf(s[0][2 * hh], a.scale_log2, -ms));
-                        const float e1 = ex2_approx(fmaf(s[0][2 * hh + 1], a.scale_log2, -ms));
-                        const float e2 = ex2_approx(fmaf(s[1][2 * hh], a.scale_log2, -ms));
-                        const float e3 = ex2_approx(fmaf(s[1][2 * hh + 1], a.scale_log2, -ms));
-                        p[hh] = pack_bf16(e0, e1);
-                        p[hh + 2] = pack_bf16(e2, e3);
-                        l[hh] = l[hh] * al[hh] + ((e0 + e1) + (e2 + e3));
-                        // O is divided by the sum of what the product below uses: the rounded probabilities
-                        const float f0 = __uint_as_float(p[hh] << 16), f1 = __uint_as_float(p[hh] & 0xffff0000u),
-                                    f2 = __uint_as_float(p[hh + 2] << 16), f3 = __uint_as_float(p[hh + 2] & 0xffff0000u);
-                        lr[hh] = lr[hh] * al[hh] + ((f0 + f1) + (f2 + f3));
+                        float sum = 0.f, sum_r = 0.f;
+#pragma unroll
+                        for (int u = 0; u < KS; ++u) {
+                            const float e0 = ex2_approx(fmaf(s[2 * u][2 * hh], a.scale_log2, -ms));
+                            const float e1 = ex2_approx(fmaf(s[2 * u][2 * hh + 1], a.scale_log2, -ms));
+                            const float e2 = ex2_approx(fmaf(s[2 * u + 1][2 * hh], a.scale_log2, -ms));
+                            const float e3 = ex2_approx(fmaf(s[2 * u + 1][2 * hh + 1], a.scale_log2, -ms));
+                            p[u][hh] = pack_bf16(e0, e1);
+                            p[u][hh + 2] = pack_bf16(e2, e3);
+                            sum += (e0 + e1) + (e2 + e3);
+                            // O is divided by the sum of what the product below uses: the rounded probabilities
+                            const float f0 = __uint_as_float(p[u][hh] << 16), f1 = __uint_as_float(p[u][hh] & 0xffff0000u),
+                                        f2 = __uint_as_float(p[u][hh + 2] << 16),
+                                        f3 = __uint_as_float(p[u][hh + 2] & 0xffff0000u);
+                            sum_r += (f0 + f1) + (f2 + f3);
+                        }
+                        l[hh] = l[hh] * al[hh] + sum;
+                        lr[hh] = lr[hh] * al[hh] + sum_r;
                     }
                     if (__any_sync(~0u, grew)) {
 #pragma unroll
@@ -306,13 +331,15 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
                     }
                     // ---- O += P V
 #pragma unroll
-                    for (int nn = 0; nn < D / 16; ++nn) {
-                        uint32_t b[4];
-                        ldsm4t(vb + (nn / 4) * (kKeyTile * 128) + v_key * 128 +
-                                   ((((nn & 3) * 2 + v_c) ^ (v_key & 7)) << 4), b);
-                        mma16816(o[2 * nn], p, b[0] & vm[0], b[1] & vm[1]);
-                        mma16816(o[2 * nn + 1], p, b[2] & vm[0], b[3] & vm[1]);
-                    }
+                    for (int nn = 0; nn < D / 16; ++nn)
+#pragma unroll
+                        for (int u = 0; u < KS; ++u) {
+                            uint32_t b[4];
+                            ldsm4t(vb + (nn / 4) * (kKeyTile * 128) + (v_key + u * 16) * 128 +
+                                       ((((nn & 3) * 2 + v_c) ^ (v_key & 7)) << 4), b);
+                            mma16816(o[2 * nn], p[u], b[0] & vm[u][0], b[1] & vm[u][1]);
+                            mma16816(o[2 * nn + 1], p[u], b[2] & vm[u][0], b[3] & vm[u][1]);
+                        }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty0 + 8 * st);
