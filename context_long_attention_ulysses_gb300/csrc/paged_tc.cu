@@ -5,21 +5,24 @@
 // 256 (two streams A and B that share every K/V tile); rows are (token, query head of the group) pairs, of one sequence or,
 // over a prefix, of the whole batch:
 //   warp 4 NS      TMA producer: K and V of each tile of 128 keys, page by page, into two rings
-//   warps 4 NS + 1 (and + 2)  one thread each issues its stream's tcgen05.mma: QK(0), then PV(j), QK(j+1) per tile (the
-//                  first of these warps owns the TMEM)
+//   warps 4 NS + 1 (and + 2)  one thread each issues tcgen05.mma (the first of these warps owns the TMEM)
 //   warps 0-3 (A), 4-7 (B)  Q rows into shared memory, softmax (thread = row = TMEM lane; log2 domain, O rescaled only when
 //                  the maximum grows by more than 2^8), normalisation, stores
 // With two streams the tensor core runs one stream's products while the other's softmax works.  Each stream has an issuer of
 // its own, and they take turns, QK(0) and then [PV(j), QK(j+1)] being a turn: while one's products run, the other does its
 // waits and the commits of its last turn.  (One issuer for both streams spent 1470 of the 3517 clocks of a tile in those,
 // with nothing queued; two issuers without turns mix the streams' products, both softmaxes then work at the same time and
-// the tensor core waits for both: 1991 us against 1570 for 2048 tokens at 64K.)  A CTA walks its share
-// piece by piece (paged.cuh); the rings run on across pieces, so the next piece's keys arrive during the epilogue.
-// Measured, 32 query and 8 KV heads of 128 values: 2048 tokens over 67584 keys in 1.42 ms, 1570 TFLOP/s (1.51 ms and more when
-// run on end, under the power cap), the tensor pipe active 67 % of the time: a stream's own chain, S to P (1360 clocks) and two
-// products, is what a tile takes.  A prefix of 32768 under 64 tokens (256 rows per KV head): 35 us for 134 MB, of which 6 pass before
-// the first scores.
-// TMEM columns: S_A [0,128), S_B [128,256), O_A [256,256+D), O_B [384,384+D); P (bf16) lies over its own S.
+// the tensor core waits for both: 1991 us against 1570 for 2048 tokens at 64K.)  With d = 64 there is room in TMEM for a third
+// buffer of scores: a turn is PV(n), QK(n + 3) over n = 2 j + stream, a softmax finds its next scores made, and the two are
+// no longer a chain with the products (1305 -> 1130 us).  A CTA walks its share piece by piece (paged.cuh); the rings run on
+// across pieces, so the next piece's keys arrive during the epilogue.
+// Measured, 32 query and 8 KV heads of 128 values: 2048 tokens over 67584 keys in 1.42 ms, 1570 TFLOP/s (1.51 ms when run on
+// end, under the power cap), the tensor pipe active 67 % of the time: a stream's own chain, S to P (1360 clocks) and two
+// products, is what a tile takes.  With heads of 64 values 1.12 ms, the tensor pipe active 42 %, issue slots 51 %: the two
+// softmax warps per scheduler wait for their own instructions.  A prefix of 32768 under 64 tokens (256 rows per KV head):
+// 35 us for 134 MB, of which 6 pass before the first scores.
+// TMEM columns: S_A [0,128), S_B [128,256), O_A [256,256+D), O_B [384,384+D), or three S of 128, O_A [384,448), O_B [448,512);
+// P (bf16) lies over its own S.
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -48,11 +51,15 @@ struct Cfg {
     static constexpr int kTileBytes = kChunks * 128 * 128;  // 128 rows of bf16
     static constexpr int kKStages = D == 64 ? 4 : 3;
     static constexpr int kVStages = D == 64 ? 4 : (NS == 2 ? 2 : 3);
+    // Three buffers of scores where O leaves the columns for them (d = 64): a stream's next scores are made while it works on
+    // these.
+    static constexpr bool kAhead = NS == 2 && D == 64;
+    static constexpr int kDbl = kAhead ? 2 : 1;  // barriers of a stream's scores, of its P and of its O, used in turn
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = NS * kTileBytes;
     static constexpr int kOffV = kOffK + kKStages * kTileBytes;
     static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
-    static constexpr int kBars = 2 * kKStages + 2 * kVStages + 5 * NS + 1 + 2 * kSegs;
+    static constexpr int kBars = 2 * kKStages + 2 * kVStages + (2 + 3 * kDbl) * NS + 1 + 2 * kSegs;
     static constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
 };
 
@@ -91,8 +98,9 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
     __shared__ Seg s_seg[kSegs], s_tail;
     auto BAR = [&](int i) { return sbase + C::kOffBar + 8u * (uint32_t)i; };
     const int kKFull = 0, kKEmpty = KS, kVFull = 2 * KS, kVEmpty = kVFull + VS;
-    const int kQFull = kVEmpty + VS, kSFull = kQFull + NS, kPReady = kSFull + NS, kOReady = kPReady + NS;  // per stream
-    const int kTurn = kOReady + NS;  // per stream: its issuer may issue
+    constexpr int DB = C::kDbl;
+    const int kQFull = kVEmpty + VS, kSFull = kQFull + NS, kPReady = kSFull + NS * DB, kOReady = kPReady + NS * DB;  // per stream
+    const int kTurn = kOReady + NS * DB;  // per stream: its issuer may issue
     const int kDrain = kTurn + NS, kSegFull = kDrain + 1, kSegEmpty = kSegFull + kSegs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
     constexpr int kProducer = 4 * NS, kIssuer = 4 * NS + 1;
@@ -114,9 +122,11 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
         for (int s = 0; s < VS; ++s) { mbar_init(BAR(kVFull + s), 1); mbar_init(BAR(kVEmpty + s), NS); }
         for (int st = 0; st < NS; ++st) {
             mbar_init(BAR(kQFull + st), 128);
-            mbar_init(BAR(kSFull + st), 1);
-            mbar_init(BAR(kPReady + st), 128);
-            mbar_init(BAR(kOReady + st), 1);
+            for (int b = 0; b < DB; ++b) {
+                mbar_init(BAR(kSFull + st * DB + b), 1);
+                mbar_init(BAR(kPReady + st * DB + b), 128);
+                mbar_init(BAR(kOReady + st * DB + b), 1);
+            }
             mbar_init(BAR(kTurn + st), 1);
         }
         mbar_init(BAR(kDrain), NS);
@@ -136,6 +146,10 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     volatile int* abort_p = &abort_flag;
+
+    // the barrier of a stream's n-th scores (or P, or product with V), and its phase
+    auto DBAR = [&](int first, int st, uint32_t n) { return BAR(first + st * DB + (int)(n % DB)); };
+    auto phase = [](uint32_t n) { return (n / DB) & 1u; };
 
     // tiles of a piece that hold a key which some row of stream st sees
     auto stream_tiles = [&](const Seg& g, int st) {
@@ -241,44 +255,77 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
             constexpr uint32_t kIdS = idesc_bf16(128, kKeyTile, 0, 0);  // S = Q K^T, both K-major
             constexpr uint32_t kIdO = idesc_bf16(128, D, 0, 1);         // O += P V, V MN-major
             const int st = warp - kIssuer;
-            const uint64_t dq = sdesc_sw128(sbase + C::kOffQ + st * C::kTileBytes, 16, 1024),
-                           dk0 = sdesc_sw128(sbase + C::kOffK, 16, 1024), dv0 = sdesc_sw128(sbase + C::kOffV, 16384, 1024);
-            const uint32_t s_col = tmem + st * 128, o_col = tmem + 256 + st * 128;
+            const uint64_t dq0 = sdesc_sw128(sbase + C::kOffQ, 16, 1024), dk0 = sdesc_sw128(sbase + C::kOffK, 16, 1024),
+                           dv0 = sdesc_sw128(sbase + C::kOffV, 16384, 1024);
             int base = 0;                           // tiles so far
-            uint32_t cnt = 0, pieces = 0, turn = 0; // tiles, pieces and turns of this stream so far
-            // A turn: the product PV of tile j and QK of tile j + 1, for a piece of n_tiles tiles of which this stream sees the
-            // first nt (j = -1: the first QK only); false: a wait gave up.  A tile that the stream does not see is released,
-            // once it is there, without a product.
-            auto do_turn = [&](int j, int n_tiles, int nt) {
+            uint32_t cnt = 0, turn = 0;             // tiles of this stream, and turns waited for, so far
+            auto products_pv = [&](uint32_t o_col, uint32_t p_col, int vs, bool first) {
+                const uint64_t dv = dv0 + (uint32_t)(vs * C::kTileBytes >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kKeyTile / 16; ++kk)
+                    mma_ts(o_col, p_col + kk * 8, dv + (kk * 2048 >> 4), kIdO, (!first || kk > 0) ? 1u : 0u);
+            };
+            auto products_qk = [&](uint32_t s_col, int stream, int ks) {
+                const uint64_t dq = dq0 + (uint32_t)(stream * C::kTileBytes >> 4), dk = dk0 + (uint32_t)(ks * C::kTileBytes >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
+                    mma_ss(s_col, dq + off, dk + off, kIdS, kk > 0);
+                }
+            };
+            // (a tile that a stream does not see is released, once it is there, without a product)
+            auto release = [&](uint32_t bar, bool used) { if (used) mma_commit(bar); else mbar_arrive(bar); };
+            uint32_t q_pieces = 0;                  // pieces with Q of the stream whose scores this issuer makes
+            uint32_t cnt_q = 0;                     // and their tiles
+            const int sq = C::kAhead ? 1 - st : st;
+            // Turn j of stream st: PV(j), QK(j + 1), for a piece of n_tiles tiles of which the stream sees the first nt
+            // (j = -1: the first QK only); false: a wait gave up.
+            auto turn_of_two = [&](int j, int n_tiles, int nt) {
                 const bool has_v = j >= 0, has_k = j + 1 < n_tiles, pv = has_v && j < nt, qk = has_k && j + 1 < nt;
                 const int iv = base + j, ik = iv + 1, vs = iv % VS, ks = ik % KS;
                 if (has_v && !mbar_wait(BAR(kVFull + vs), (iv / VS) & 1, abort_p, 37, a.status)) return false;
                 if (has_k && !mbar_wait(BAR(kKFull + ks), (ik / KS) & 1, abort_p, 36, a.status)) return false;
-                if (pv && !mbar_wait(BAR(kPReady + st), (cnt + j) & 1, abort_p, 38, a.status)) return false;
+                if (pv && !mbar_wait(DBAR(kPReady, st, cnt + j), phase(cnt + j), abort_p, 38, a.status)) return false;
                 if (NS == 2 && (st == 1 || turn > 0) &&
                     !mbar_wait(BAR(kTurn + st), (turn - 1 + st) & 1, abort_p, 46, a.status))
                     return false;
                 ++turn;
                 tc_fence_after();
-                if (pv) {
-                    const uint64_t dv = dv0 + (uint32_t)(vs * C::kTileBytes >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < kKeyTile / 16; ++kk)
-                        mma_ts(o_col, s_col + kk * 8, dv + (kk * 2048 >> 4), kIdO, (j > 0 || kk > 0) ? 1u : 0u);
-                }
-                if (qk) {  // in issue order after the product that read P from the columns of S
-                    const uint64_t dk = dk0 + (uint32_t)(ks * C::kTileBytes >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
-                        mma_ss(s_col, dq + off, dk + off, kIdS, kk > 0);
-                    }
-                }
+                const uint32_t s_col = tmem + st * 128;
+                if (pv) products_pv(tmem + 256 + st * 128, s_col, vs, j == 0);
+                if (qk) products_qk(s_col, st, ks);  // in issue order after the product that read P from the columns of S
                 if (NS == 2) mbar_arrive(BAR(kTurn + 1 - st));
-                if (qk) mma_commit(BAR(kSFull + st));
+                if (qk) mma_commit(DBAR(kSFull, st, cnt + j + 1));
                 if (pv && j == nt - 1) mma_commit(BAR(kOReady + st));
-                if (has_v) { if (pv) mma_commit(BAR(kVEmpty + vs)); else mbar_arrive(BAR(kVEmpty + vs)); }
-                if (has_k) { if (qk) mma_commit(BAR(kKEmpty + ks)); else mbar_arrive(BAR(kKEmpty + ks)); }
+                if (has_v) release(BAR(kVEmpty + vs), pv);
+                if (has_k) release(BAR(kKEmpty + ks), qk);
+                return true;
+            };
+            // Turn n = 2 j + st with three score buffers: PV(n), and into the columns that it leaves QK(n + 3), which is the
+            // other stream's.  From n = -3 on, the turns of a piece begin and end with stream 1, and buffers rotate on across
+            // pieces, so that a buffer is always refilled by the thread that issued the product before.
+            auto turn_of_three = [&](int n, int n_tiles, int nt, int nt_q) {
+                const int j = n >> 1, jk = (n + 3) >> 1;
+                const bool has_v = n >= 0, has_k = jk < n_tiles, pv = has_v && j < nt, qk = has_k && jk < nt_q;
+                const int iv = base + j, ik = base + jk, vs = iv % VS, ks = ik % KS;
+                if (has_v && !mbar_wait(BAR(kVFull + vs), (iv / VS) & 1, abort_p, 37, a.status)) return false;
+                if (has_k && !mbar_wait(BAR(kKFull + ks), (ik / KS) & 1, abort_p, 36, a.status)) return false;
+                if (pv && !mbar_wait(DBAR(kPReady, st, cnt + j), phase(cnt + j), abort_p, 38, a.status)) return false;
+                if (n != -3 && !mbar_wait(BAR(kTurn + st), turn++ & 1, abort_p, 46, a.status)) return false;
+                // (where this stream sees no tile the columns are those of the other's product three tiles before, and another
+                // thread's: it has to be complete.  In a piece's first turns that follows from Q being there.)
+                if (qk && !pv && jk >= 3 &&
+                    !mbar_wait(DBAR(kOReady, sq, cnt_q + jk - 3), phase(cnt_q + jk - 3), abort_p, 47, a.status))
+                    return false;
+                tc_fence_after();
+                const uint32_t col = tmem + (uint32_t)((2 * base + n + 3) % 3) * 128;
+                if (pv) products_pv(tmem + 384 + st * 64, col, vs, j == 0);
+                if (qk) products_qk(col, sq, ks);
+                if (n != 2 * n_tiles - 1) mbar_arrive(BAR(kTurn + 1 - st));
+                if (qk) mma_commit(DBAR(kSFull, sq, cnt_q + jk));
+                if (pv) mma_commit(DBAR(kOReady, st, cnt + j));
+                if (has_v) release(BAR(kVEmpty + vs), pv);
+                if (has_k) release(BAR(kKEmpty + ks), qk);
                 return true;
             };
             for (int n_seg = 0; !PREFIX || n_seg == 0; ++n_seg) {
@@ -287,13 +334,19 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                 const int n_tiles = PREFIX ? pre.n_tiles : s_seg[si].n_tiles;
                 if (n_tiles == 0) break;
                 const int nt = PREFIX ? stream_tiles(pre, st) : stream_tiles(s_seg[si], st);
+                const int nt_q = !C::kAhead ? nt : PREFIX ? stream_tiles(pre, sq) : stream_tiles(s_seg[si], sq);
                 if (!PREFIX) mbar_arrive(BAR(kSegEmpty + si));
-                if (nt > 0 && !mbar_wait(BAR(kQFull + st), pieces++ & 1, abort_p, 35, a.status)) break;
+                if (nt_q > 0 && !mbar_wait(BAR(kQFull + sq), q_pieces++ & 1, abort_p, 35, a.status)) break;
                 bool ok = true;
-                for (int j = -1; ok && j < n_tiles; ++j) ok = do_turn(j, n_tiles, nt);
+                if constexpr (C::kAhead) {
+                    for (int n = -2 - st; ok && n < 2 * n_tiles; n += 2) ok = turn_of_three(n, n_tiles, nt, nt_q);
+                } else {
+                    for (int j = -1; ok && j < n_tiles; ++j) ok = turn_of_two(j, n_tiles, nt);
+                }
                 if (!ok) break;
                 base += n_tiles;
                 cnt += nt;
+                cnt_q += nt_q;
             }
             // every issued MMA completes before TMEM is freed (after an abort, too)
             mma_commit(BAR(kDrain));
@@ -305,11 +358,16 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
         const int st = warp >> 2;                    // stream
         const int row = (warp & 3) * 32 + lane;      // row of the stream = TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t scol = lane_base + st * 128, ocol = lane_base + 256 + st * 128;
+        const uint32_t ocol = lane_base + (C::kAhead ? 384 + st * 64 : 256 + st * 128);
         const int box_log2 = min(a.page_log2, 7);
         const uint32_t all_boxes = (1u << (kKeyTile >> box_log2)) - 1u;
         auto warp_wait = [&](uint32_t bar, uint32_t parity, int site) {  // one answer for the warp: TMEM access is collective
             return __all_sync(~0u, mbar_wait(bar, parity, abort_p, site, a.status)) != 0;
+        };
+        auto o_wait = [&](uint32_t n) {  // three buffers: for the stream's n-th product with V; two: for its n-th piece
+            if (!warp_wait(DBAR(kOReady, st, n), phase(n), 42)) return false;
+            tc_fence_after();
+            return true;
         };
         uint32_t base = 0, cnt = 0, pieces = 0;
         auto piece = [&](const Seg& g) {  // false: a wait gave up
@@ -322,7 +380,8 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                 if constexpr (!PREFIX) load_q_row(a, g, r, w);
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c)
-                    *reinterpret_cast<uint4*>(dst + (c / 8) * 16384 + (((c & 7) ^ (row & 7)) << 4)) = PREFIX ? first_q[PREFIX ? c : 0] : w[c];
+                    *reinterpret_cast<uint4*>(dst + (c / 8) * 16384 + (((c & 7) ^ (row & 7)) << 4)) =
+                        PREFIX ? first_q[PREFIX ? c : 0] : w[c];
                 fence_proxy_async_smem();
                 mbar_arrive(BAR(kQFull + st));
             }
@@ -330,9 +389,11 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
             // (a warp without a valid row has its rows of V to clear, too)
             const int lim_min = min(__reduce_min_sync(~0u, lim), seg_key_end<PREFIX>(a, g));
             float m_run = -INFINITY, l_run = 0.f;
+            uint32_t buf = C::kAhead ? (2 * base + st) % 3 : st;  // of the scores
             for (int j = 0; j < n_tiles; ++j) {
-                if (!warp_wait(BAR(kSFull + st), (cnt + j) & 1, 40)) return false;
+                if (!warp_wait(DBAR(kSFull, st, cnt + j), phase(cnt + j), 40)) return false;
                 tc_fence_after();
+                const uint32_t scol = lane_base + buf * 128;
                 uint32_t r0r[32], r1r[32], r2r[32], r3r[32];
                 tmem_ld32(scol, r0r);
                 tmem_ld32(scol + 32, r1r);
@@ -404,8 +465,12 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                     tmem_st16(scol + h * 16, pk);  // P over S: this row's S is in registers
                 }
                 l_run = l_run * alpha + ((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y));
+                // Three buffers: S_j was signalled before the product of tile j - 1, even j - 2, had to be complete.  Each is
+                // waited for, in order (a phase that is skipped could be taken for the one after next), the last but one always.
+                if (C::kAhead && j > 1 && !o_wait(cnt + j - 2)) return false;
                 if (j > 0 && __any_sync(~0u, up)) {
-                    // the products of earlier tiles completed before S_j was signalled: scale O in place
+                    // (two: the products of earlier tiles completed before S_j was signalled) scale O in place
+                    if (C::kAhead && !o_wait(cnt + j - 1)) return false;
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
@@ -418,13 +483,14 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(BAR(kPReady + st));
+                mbar_arrive(DBAR(kPReady, st, cnt + j));
+                if constexpr (C::kAhead) buf = buf == 0 ? 2 : buf - 1;
             }
             // ---------------------------------------------------------------- the piece's result
             if (n_tiles > 0) {
-                if (!warp_wait(BAR(kOReady + st), pieces & 1, 42)) return false;
+                if (C::kAhead && n_tiles > 1 && !o_wait(cnt + n_tiles - 2)) return false;
+                if (!o_wait(C::kAhead ? cnt + n_tiles - 1 : pieces)) return false;
                 ++pieces;
-                tc_fence_after();
             }
             const bool has = n_tiles > 0 && l_run != 0.f;  // (NaN, too, which has to show)
             const float inv = has ? 1.f / l_run : 0.f;

@@ -516,6 +516,49 @@ def test_prefix_attention(usp, case, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 6, 30, 70])
+def test_scores_that_grow_along_the_keys(usp, n, d, dtype):
+    """Keys that grow with their position: the running maximum keeps rising, and what is summed so far is scaled down
+    again and again, tile after tile."""
+    import torch
+    guard = Guarded()
+    b = Batch([(n, 1900), (n, 700), (n, n)], 8, 2, d, 64, dtype, seed=n)
+    for s, ln in enumerate(b.lens):
+        for j in range(-(-int(ln) // 64)):
+            b.kp[int(b.table[s, j])] *= (1 + (torch.arange(64) + 64 * j) / 48).to(b.kp.dtype)[None, :, None]
+    b.to_gpu(usp, guard).run(usp)
+    _done(usp, guard)
+    b.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_short_pieces_of_many_rows(usp, d):
+    """Pieces of a tile or two, whose values arrive late: nothing may be taken for the product before it.  The memory is
+    cold and busy in every second run; all runs have the same bits."""
+    import torch
+    guard = Guarded()
+    b = Batch([(10, 1206), (6, 878), (9, 300), (20, 140)], 128, 8, d, 16, pad=(2, 1)).to_gpu(usp, guard)
+    b.run(usp)
+    _done(usp, guard)
+    b.check()
+    o, lse = b.g["o"].clone(), b.g["lse"].clone()
+    noise, side = torch.empty(1 << 28, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+    for i in range(60):
+        b.g["o"].fill_(7.0)
+        if i % 2:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                noise.add_(1)
+        b.run(usp)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(b.g["o"], o) and torch.equal(b.g["lse"], lse), i
+    _done(usp, guard)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("max_q", [1, 4, 1000])
 def test_max_q_is_a_hint(usp, max_q):
     """A wrong max_q costs speed, never results."""
