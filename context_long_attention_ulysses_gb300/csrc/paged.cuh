@@ -403,21 +403,22 @@ __device__ void finish_empty_rows(const PagedArgs& a, int cta, int n_cta) {
         const int64_t row = x < (int64_t)lo * a.Hq ? x : x + (int64_t)(hi - lo) * a.Hq;
         a.row_info[row] = make_uint2(kRowDone, 0);
     }
-    for (int b = cta; b < a.n_seqs; b += n_cta) {
+    // (as many CTAs per sequence as there are: three whose 290 tokens mostly see nothing: 51 us with one each, 27 so)
+    const int per_seq = max(n_cta / a.n_seqs, 1), part = cta % per_seq;
+    for (int b = cta / per_seq; b < a.n_seqs; b += n_cta / per_seq) {
         const SeqRows s = seq_rows(a, b);
         const int nrt = row_tiles<M>(a, s);
-        for (int rt = 0; rt < nrt; ++rt) {
-            if (unit_tiles<M, KT>(a, s, rt) > 0) break;  // limits grow with the row: the later tiles have keys, too
-            const int rows = min(M, s.n * a.g - rt * M);
-            for (int x = threadIdx.x; x < rows * a.Hkv; x += NT) {
-                const int h = x / rows, R = rt * M + x % rows, i = R / a.g;
-                const int64_t row = (int64_t)(s.t0 + i) * a.Hq + h * a.g + (R - i * a.g);
-                a.row_info[row] = make_uint2(a.prefix_len ? kRowNone : kRowDone, 0);
-                if (a.prefix_len == 0) {
-                    a.lse[row] = -INFINITY;
-                    uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + row * a.d);
-                    for (int c = 0; c < a.d * (int)sizeof(T) / 16; ++c) o[c] = make_uint4(0, 0, 0, 0);
-                }
+        int rt = 0;
+        while (rt < nrt && unit_tiles<M, KT>(a, s, rt) == 0) ++rt;  // limits grow with the row: the later tiles have keys, too
+        const uint32_t rows = rt < nrt ? rt * M : s.n * a.g;
+        for (uint32_t x = part * NT + threadIdx.x; x < rows * a.Hkv; x += per_seq * NT) {
+            const int h = x / rows, R = x % rows, i = R / a.g;
+            const int64_t row = (int64_t)(s.t0 + i) * a.Hq + h * a.g + (R - i * a.g);
+            a.row_info[row] = make_uint2(a.prefix_len ? kRowNone : kRowDone, 0);
+            if (a.prefix_len == 0) {
+                a.lse[row] = -INFINITY;
+                uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + row * a.d);
+                for (int c = 0; c < a.d * (int)sizeof(T) / 16; ++c) o[c] = make_uint4(0, 0, 0, 0);
             }
         }
     }
