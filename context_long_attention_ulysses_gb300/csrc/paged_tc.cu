@@ -12,16 +12,17 @@
 // its own, and they take turns, QK(0) and then [PV(j), QK(j+1)] being a turn: while one's products run, the other does its
 // waits and the commits of its last turn.  (One issuer for both streams spent 1470 of the 3517 clocks of a tile in those,
 // with nothing queued; two issuers without turns mix the streams' products, both softmaxes then work at the same time and
-// the tensor core waits for both: 1991 us against 1570 for 2048 tokens at 64K.)  With d = 64 there is room in TMEM for a third
-// buffer of scores: a turn is PV(n), QK(n + 3) over n = 2 j + stream, a softmax finds its next scores made, and the two are
-// no longer a chain with the products (1305 -> 1130 us).  A CTA walks its share piece by piece (paged.cuh); the rings run on
+// the tensor core waits for both: 1991 us against 1570 for 2048 tokens at 64K.)  Where TMEM has room for one more
+// buffer of scores (one stream, or d = 64), a turn is PV(n), QK(n + NS + 1) over n = NS j + stream: a softmax finds its next
+// scores made, and is no longer a chain with the products (2048 tokens over 67584 keys, d = 64: 1305 -> 1130 us; 64 and 96
+// rows of 16 sequences of 1000 to 20000 tokens 97 -> 93 and 101 -> 97).  A CTA walks its share piece by piece (paged.cuh); the rings run on
 // across pieces, so the next piece's keys arrive during the epilogue.
 // Measured, 32 query and 8 KV heads of 128 values: 2048 tokens over 67584 keys in 1.42 ms, 1570 TFLOP/s (1.51 ms when run on
 // end, under the power cap), the tensor pipe active 67 % of the time: a stream's own chain, S to P (1360 clocks) and two
 // products, is what a tile takes.  With heads of 64 values 1.12 ms, the tensor pipe active 42 %, issue slots 51 %: the two
 // softmax warps per scheduler wait for their own instructions.  A prefix of 32768 under 64 tokens (256 rows per KV head):
 // 35 us for 134 MB, of which 6 pass before the first scores.
-// TMEM columns: S_A [0,128), S_B [128,256), O_A [256,256+D), O_B [384,384+D), or three S of 128, O_A [384,448), O_B [448,512);
+// TMEM columns: S_A [0,128), S_B [128,256), O_A [256,256+D), O_B [384,384+D); with three S O_A [384,448), O_B [448,512);
 // P (bf16) lies over its own S.
 #include <cmath>
 
@@ -51,9 +52,10 @@ struct Cfg {
     static constexpr int kTileBytes = kChunks * 128 * 128;  // 128 rows of bf16
     static constexpr int kKStages = D == 64 ? 4 : 3;
     static constexpr int kVStages = D == 64 ? 4 : (NS == 2 ? 2 : 3);
-    // Three buffers of scores where O leaves the columns for them (d = 64): a stream's next scores are made while it works on
-    // these.
-    static constexpr bool kAhead = NS == 2 && D == 64;
+    // One buffer of scores more than streams where O leaves the columns for it: a stream's next scores are made while it works
+    // on these.
+    static constexpr bool kAhead = NS == 1 || D == 64;
+    static constexpr int kBufs = kAhead ? NS + 1 : NS;
     static constexpr int kDbl = kAhead ? 2 : 1;  // barriers of a stream's scores, of its P and of its O, used in turn
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = NS * kTileBytes;
@@ -277,10 +279,10 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
             auto release = [&](uint32_t bar, bool used) { if (used) mma_commit(bar); else mbar_arrive(bar); };
             uint32_t q_pieces = 0;                  // pieces with Q of the stream whose scores this issuer makes
             uint32_t cnt_q = 0;                     // and their tiles
-            const int sq = C::kAhead ? 1 - st : st;
+            const int sq = C::kAhead ? NS - 1 - st : st;
             // Turn j of stream st: PV(j), QK(j + 1), for a piece of n_tiles tiles of which the stream sees the first nt
             // (j = -1: the first QK only); false: a wait gave up.
-            auto turn_of_two = [&](int j, int n_tiles, int nt) {
+            auto turn_in_chain = [&](int j, int n_tiles, int nt) {
                 const bool has_v = j >= 0, has_k = j + 1 < n_tiles, pv = has_v && j < nt, qk = has_k && j + 1 < nt;
                 const int iv = base + j, ik = iv + 1, vs = iv % VS, ks = ik % KS;
                 if (has_v && !mbar_wait(BAR(kVFull + vs), (iv / VS) & 1, abort_p, 37, a.status)) return false;
@@ -301,27 +303,29 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                 if (has_k) release(BAR(kKEmpty + ks), qk);
                 return true;
             };
-            // Turn n = 2 j + st with three score buffers: PV(n), and into the columns that it leaves QK(n + 3), which is the
-            // other stream's.  From n = -3 on, the turns of a piece begin and end with stream 1, and buffers rotate on across
-            // pieces, so that a buffer is always refilled by the thread that issued the product before.
-            auto turn_of_three = [&](int n, int n_tiles, int nt, int nt_q) {
-                const int j = n >> 1, jk = (n + 3) >> 1;
+            // Turn n = NS j + st with a buffer more than streams: PV(n), and into the columns that it leaves QK(n + NS + 1), with
+            // two streams the other's.  From n = -NS - 1 on, the turns of a piece end with the last stream, as they began with two,
+            // and buffers rotate on across pieces, so that a buffer is always refilled by the thread that issued the product
+            // before.
+            auto turn_ahead = [&](int n, int n_tiles, int nt, int nt_q) {
+                constexpr int NB = C::kBufs;
+                const int j = NS == 2 ? n >> 1 : n, jk = NS == 2 ? (n + NB) >> 1 : n + NB;
                 const bool has_v = n >= 0, has_k = jk < n_tiles, pv = has_v && j < nt, qk = has_k && jk < nt_q;
                 const int iv = base + j, ik = base + jk, vs = iv % VS, ks = ik % KS;
                 if (has_v && !mbar_wait(BAR(kVFull + vs), (iv / VS) & 1, abort_p, 37, a.status)) return false;
                 if (has_k && !mbar_wait(BAR(kKFull + ks), (ik / KS) & 1, abort_p, 36, a.status)) return false;
                 if (pv && !mbar_wait(DBAR(kPReady, st, cnt + j), phase(cnt + j), abort_p, 38, a.status)) return false;
-                if (n != -3 && !mbar_wait(BAR(kTurn + st), turn++ & 1, abort_p, 46, a.status)) return false;
+                if (NS == 2 && n != -NB && !mbar_wait(BAR(kTurn + st), turn++ & 1, abort_p, 46, a.status)) return false;
                 // (where this stream sees no tile the columns are those of the other's product three tiles before, and another
                 // thread's: it has to be complete.  In a piece's first turns that follows from Q being there.)
-                if (qk && !pv && jk >= 3 &&
+                if (NS == 2 && qk && !pv && jk >= 3 &&
                     !mbar_wait(DBAR(kOReady, sq, cnt_q + jk - 3), phase(cnt_q + jk - 3), abort_p, 47, a.status))
                     return false;
                 tc_fence_after();
-                const uint32_t col = tmem + (uint32_t)((2 * base + n + 3) % 3) * 128;
-                if (pv) products_pv(tmem + 384 + st * 64, col, vs, j == 0);
+                const uint32_t col = tmem + (uint32_t)((NS * base + n + NB) % NB) * 128;
+                if (pv) products_pv(tmem + NB * 128 + st * 64, col, vs, j == 0);
                 if (qk) products_qk(col, sq, ks);
-                if (n != 2 * n_tiles - 1) mbar_arrive(BAR(kTurn + 1 - st));
+                if (NS == 2 && n != 2 * n_tiles - 1) mbar_arrive(BAR(kTurn + 1 - st));
                 if (qk) mma_commit(DBAR(kSFull, sq, cnt_q + jk));
                 if (pv) mma_commit(DBAR(kOReady, st, cnt + j));
                 if (has_v) release(BAR(kVEmpty + vs), pv);
@@ -339,9 +343,9 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                 if (nt_q > 0 && !mbar_wait(BAR(kQFull + sq), q_pieces++ & 1, abort_p, 35, a.status)) break;
                 bool ok = true;
                 if constexpr (C::kAhead) {
-                    for (int n = -2 - st; ok && n < 2 * n_tiles; n += 2) ok = turn_of_three(n, n_tiles, nt, nt_q);
+                    for (int n = -2 - st; ok && n < NS * n_tiles; n += NS) ok = turn_ahead(n, n_tiles, nt, nt_q);
                 } else {
-                    for (int j = -1; ok && j < n_tiles; ++j) ok = turn_of_two(j, n_tiles, nt);
+                    for (int j = -1; ok && j < n_tiles; ++j) ok = turn_in_chain(j, n_tiles, nt);
                 }
                 if (!ok) break;
                 base += n_tiles;
@@ -358,13 +362,13 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
         const int st = warp >> 2;                    // stream
         const int row = (warp & 3) * 32 + lane;      // row of the stream = TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t ocol = lane_base + (C::kAhead ? 384 + st * 64 : 256 + st * 128);
+        const uint32_t ocol = lane_base + (C::kAhead ? C::kBufs * 128 + st * 64 : 256 + st * 128);
         const int box_log2 = min(a.page_log2, 7);
         const uint32_t all_boxes = (1u << (kKeyTile >> box_log2)) - 1u;
         auto warp_wait = [&](uint32_t bar, uint32_t parity, int site) {  // one answer for the warp: TMEM access is collective
             return __all_sync(~0u, mbar_wait(bar, parity, abort_p, site, a.status)) != 0;
         };
-        auto o_wait = [&](uint32_t n) {  // three buffers: for the stream's n-th product with V; two: for its n-th piece
+        auto o_wait = [&](uint32_t n) {  // ahead: for the stream's n-th product with V; in a chain: for its n-th piece
             if (!warp_wait(DBAR(kOReady, st, n), phase(n), 42)) return false;
             tc_fence_after();
             return true;
@@ -389,7 +393,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
             // (a warp without a valid row has its rows of V to clear, too)
             const int lim_min = min(__reduce_min_sync(~0u, lim), seg_key_end<PREFIX>(a, g));
             float m_run = -INFINITY, l_run = 0.f;
-            uint32_t buf = C::kAhead ? (2 * base + st) % 3 : st;  // of the scores
+            uint32_t buf = C::kAhead ? (NS * base + st) % C::kBufs : st;  // of the scores
             for (int j = 0; j < n_tiles; ++j) {
                 if (!warp_wait(DBAR(kSFull, st, cnt + j), phase(cnt + j), 40)) return false;
                 tc_fence_after();
@@ -465,11 +469,11 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                     tmem_st16(scol + h * 16, pk);  // P over S: this row's S is in registers
                 }
                 l_run = l_run * alpha + ((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y));
-                // Three buffers: S_j was signalled before the product of tile j - 1, even j - 2, had to be complete.  Each is
+                // Made ahead, S_j was signalled before the product of tile j - 1, even j - 2, had to be complete.  Each is
                 // waited for, in order (a phase that is skipped could be taken for the one after next), the last but one always.
                 if (C::kAhead && j > 1 && !o_wait(cnt + j - 2)) return false;
                 if (j > 0 && __any_sync(~0u, up)) {
-                    // (two: the products of earlier tiles completed before S_j was signalled) scale O in place
+                    // (in a chain the products of earlier tiles completed before S_j was signalled) scale O in place
                     if (C::kAhead && !o_wait(cnt + j - 1)) return false;
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(DBAR(kPReady, st, cnt + j));
-                if constexpr (C::kAhead) buf = buf == 0 ? 2 : buf - 1;
+                if constexpr (C::kAhead) buf = buf == 0 ? C::kBufs - 1 : buf - 1;  // NS buffers on
             }
             // ---------------------------------------------------------------- the piece's result
             if (n_tiles > 0) {
