@@ -169,17 +169,18 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 // ending a unit costs in tiles.
 struct Pick {
     int rows, keys, ctas, piece;
+    float us;  // time of a tile
 };
 // bf16 by the rows per KV head, 32 query and 8 KV heads of 128 values, 16 sequences of 1000 to 20000 tokens:
-//   20 rows: 84.0 us in a unit of 32 (m16n8k16 products), 91.7 in one of 128 (tcgen05); 32 rows: 85.1 and 96.9
-//   48 rows: 98.6 in a unit of 128, 162 in two of 32
-//   64 rows: 101 in one of 128, 110 in one of 256, whose second stream is idle; 96 rows: 107 and 117
-// and 160 rows of 8 sequences: 64 in one of 256, 76 in two of 128.
+//   20 rows: 84.1 us in a unit of 32 (m16n8k16 products), 93.2 in one of 128 (tcgen05); 32 rows: 85.2 and 90.9
+//   48 rows: 91.6 in a unit of 128, 162 in two of 32
+//   64 rows: 93.1 in one of 128, 108 in one of 256, whose second stream is idle; 96 rows: 97.8 and 112
+// and 160 rows of 8 sequences: 59.6 in one of 256, 67.8 in two of 128.
 static Pick pick(const PagedArgs& a, int64_t rows) {
-    if (a.elem == 4) return {8, a.d == 64 ? 128 : 64, kSms, 2};
-    if (rows <= 16) return a.d == 64 ? Pick{16, 128, kSms * 2, 3} : Pick{16, 64, kSms * 2, 2};
-    if (rows <= 32) return {32, 128, kSms, 3};
-    return {rows <= 128 ? 128 : 256, 128, kSms, 3};
+    if (a.elem == 4) return {8, a.d == 64 ? 128 : 64, kSms, 2, 1.5f};
+    if (rows <= 16) return a.d == 64 ? Pick{16, 128, kSms * 2, 3, 1.5f} : Pick{16, 64, kSms * 2, 2, 1.5f};
+    if (rows <= 32) return {32, 128, kSms, 3, a.d == 64 ? 0.8f : 1.5f};
+    return rows <= 128 ? Pick{128, 128, kSms, 3, 1.1f} : Pick{256, 128, kSms, 3, 1.6f};
 }
 
 size_t paged_plan(PagedArgs* a, int max_q, void* ws) {
@@ -190,20 +191,26 @@ size_t paged_plan(PagedArgs* a, int max_q, void* ws) {
     a->p_rows = a->p_ctas = a->p_split = 0;
     if (a->prefix_len > 0) {
         const int64_t batch = (int64_t)a->n_tokens * a->g;
-        const Pick pre = pick(*a, batch);
-        a->p_rows = pre.rows;
-        // Parts of a unit: few waves of CTAs, each of few tiles and the cost of a piece.
-        const int64_t units = (batch + pre.rows - 1) / pre.rows * a->Hkv, tiles = (a->prefix_len + pre.keys - 1) / pre.keys;
-        int64_t best = INT64_MAX;
-        for (int64_t waves = 1; waves <= 16; ++waves) {
-            const int64_t k = std::max<int64_t>(1, std::min(tiles, waves * pre.ctas / units));
-            const int64_t cost = (units * k + pre.ctas - 1) / pre.ctas * ((tiles + k - 1) / k + pre.piece);
-            if (cost < best) {
-                best = cost;
-                a->p_split = (int)k;
+        // Rows of a unit and its parts: few waves of CTAs, each of few tiles and the cost of a piece, and few partial results,
+        // which the merge reads back at about 2 TB/s.  (Units of 256 rows always, and as many parts as CTAs, the partial results
+        // left out of the account: 37.6 us for 106 samples behind 1271 tokens against 29.5, 29 requests with one KV head
+        // behind 53364 41.6 against 34.4, 200 requests behind 4001 122.9 against 120.5.)
+        float best = INFINITY;
+        for (const Pick& pre : {pick(*a, batch), pick(*a, std::min<int64_t>(batch, 128))}) {
+            const int64_t units = (batch + pre.rows - 1) / pre.rows * a->Hkv, tiles = (a->prefix_len + pre.keys - 1) / pre.keys;
+            const float slot = (float)pre.rows * a->d * 4 / 2e6f;
+            for (int64_t quarter = 1; quarter <= 16; ++quarter) {  // of a wave
+                const int64_t k = std::max<int64_t>(1, std::min(tiles, quarter * pre.ctas / (4 * units)));
+                const int64_t waves = (units * k + pre.ctas - 1) / pre.ctas;
+                const float cost = (float)(waves * ((tiles + k - 1) / k + pre.piece)) * pre.us + (float)(units * k) * slot;
+                if (cost < best) {
+                    best = cost;
+                    a->p_rows = pre.rows;
+                    a->p_split = (int)k;
+                    a->p_ctas = (int)(units * k);
+                }
             }
         }
-        a->p_ctas = (int)(units * a->p_split);
     }
     size_t at = 0;
     char* w = static_cast<char*>(ws);
@@ -243,6 +250,9 @@ static cudaError_t merge_t(const PagedArgs& a, cudaStream_t stream) {
     // parts of a row: those of the prefix, and own ones as equal shares give them
     const int64_t units = (int64_t)a.Hkv * std::max(a.n_seqs, (batch + a.rows - 1) / a.rows);
     const dim3 grid((batch + 3) / 4, a.Hkv);
+    // (few CTAs with very many parts each: 31.4 us against 34.4 for 29 requests with one KV head behind 53364 tokens)
+    if (a.p_split + a.ctas / units > 32 && (int64_t)grid.x * grid.y <= kSms)
+        return launch_dependent(paged_merge_kernel<T, D, 4, 1024>, grid, 1024, 0, stream, a);
     if (a.p_split + a.ctas / units > 8)
         return launch_dependent(paged_merge_kernel<T, D, 4, 512>, grid, 512, 0, stream, a);
     return launch_dependent(paged_merge_kernel<T, D, 4, 128>, grid, 128, 0, stream, a);
