@@ -13,8 +13,8 @@
 // tile is 2 to 8 boxes per 64 columns, issued by as many lanes.  Boxes without a visible key, or of a page that the pool
 // does not have, are not loaded: their keys are left out by the warps that own them.
 //
-// Measured, 32 query and 8 KV heads of 128 values: one token of one sequence of 131072 in 83 us, 6.5 TB/s; of 64 sequences of 17
-// to 32768 in 153 us, 6.6 TB/s; five tokens of 16 sequences in 84 us, 5.8 TB/s (bound by the two groups' instructions).
+// Measured, 32 query and 8 KV heads of 128 values: one token of one sequence of 131072 in 83 us, 6.5 TB/s; of 64 sequences of
+// 17 to 32768 in 153 us, 6.6 TB/s; five tokens of 16 sequences in 80 us, 6.1 TB/s.
 #include <cmath>
 
 #include <cuda_bf16.h>
