@@ -657,12 +657,16 @@ def _serving_device(x):
     return x.device
 
 
+def _as_stream(stream):
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+
+
 def _made_on(stream):
     """Context in which a helper makes its outputs and its workspace: the stream that writes them.  (Memory freed on the
     current stream may still be in use there, and must not be handed to a kernel on another.)"""
-    if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(_as_stream(stream))
 
 
 def _returned(stream, *tensors) -> None:
@@ -670,7 +674,7 @@ def _returned(stream, *tensors) -> None:
     if stream is None:
         return
     current = torch.cuda.current_stream()
-    if current.cuda_stream == (stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)):
+    if current.cuda_stream == _as_stream(stream).cuda_stream:
         return
     for t in tensors:
         if t is not None:

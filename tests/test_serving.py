@@ -950,6 +950,24 @@ def test_helpers_on_a_side_stream_leave_freed_memory_alone(usp):
 
 
 @pytest.mark.gpu
+def test_helpers_on_the_default_stream_from_another(usp):
+    """Stream handle 0 is the default stream: outputs and workspace are made there, whatever the current stream is."""
+    import torch
+    guard = Guarded()
+    b = Batch([(1, 200), (1, 190), (1, 129)], 8, 2, 128, 64).to_gpu(usp, guard)
+    g = b.g
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        o, lse = usp.paged_attention(b.c, g["q"], g["kp"], g["vp"], g["table"], g["lens"], stream=0)
+        x, _ = usp.kv_append(b.c, g["q"], *(torch.zeros(3, 2, 128, dtype=torch.bfloat16, device="cuda"),) * 2,
+                             torch.full((3,), -1, dtype=torch.int32, device="cuda"), g["lens"], None, g["kp"], g["vp"],
+                             g["table"], stream=torch.cuda.default_stream())
+        assert x.shape == g["q"].shape
+    torch.cuda.synchronize()
+    b.check(o, lse)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("P,path", [(2, "ulysses"), (4, "ring")])
 def test_prompt_then_answer(usp, orc, P, path):
     """A prompt through the sequence-parallel attention, its keys and values into the cache, then tokens one by one, and
