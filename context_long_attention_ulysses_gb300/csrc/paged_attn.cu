@@ -46,13 +46,15 @@ __device__ __forceinline__ Parts row_parts(const PagedArgs& a, int t, int h, int
     p.n = p.n_pre;
     p.o_col = 4;
     const uint32_t kind = info.x & 3u;
+    // A kernel whose wait gave up has not noted its rows: what the workspace held instead (an earlier call's words, say) leads
+    // nowhere outside it.  Without a prefix there is no own_o.
+    if (kind == kRowWhole && a.prefix_len == 0) return p;
     if (kind == kRowWhole) {
         p.n += 1;
         p.oo = a.own_o + row * a.d;
         p.ol = a.own_lse + row;
     } else if (kind == kRowSplit) {
         const int c0 = info.y & 0xffffu, c1 = info.y >> 16, r = info.x >> 2;
-        // A kernel whose wait gave up has not noted its rows: what the workspace held instead leads nowhere outside it.
         if (c0 > c1 || c1 >= a.ctas || r >= a.rows) return p;
         const bool groups = a.rows >= 128;
         p.n += c1 - c0 + 1;

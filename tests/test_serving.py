@@ -871,6 +871,53 @@ def test_abort_with_a_workspace_that_holds_anything(usp, fill):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fill", [0x01, 0x02, 0xFE, 0x00])
+def test_abort_with_every_kind_of_stale_row_word(usp, fill):
+    """The same with words of every kind that the merge tells apart, a split whose CTAs and row are in range among them."""
+    guard = Guarded()
+    for seqs, Hq, Hkv, d, p in [([(70, 900), (3, 10)], 8, 2, 128, 0), ([(300, 2000)], 4, 1, 64, 300),
+                                ([(40, 5000)], 8, 2, 128, 100), ([(1, 3000)], 8, 2, 64, 0), ([(6, 900)], 8, 2, 128, 0)]:
+        b = Batch(seqs, Hq, Hkv, d, 64, prefix=p).to_gpu(usp, guard)
+        words = b.g["ws"][:8 * b.T * Hq]
+        fills = [fill]
+        if fill == 0:
+            fills = [(3, 0, 0, 0, 0, 0, 1, 0), (3 | 5 << 2, 0, 0, 0, 1, 0, 3, 0)]  # row 0 of CTAs 0 and 1, row 5 of 1 to 3
+        for f in fills:
+            if fill == 0:
+                words.view(-1, 8).copy_(b.torch.tensor(f, dtype=b.torch.uint8))
+            else:
+                b.g["ws"].fill_(f)
+            usp.usp_diag_raise_status()
+            b.run(usp)
+            assert usp.usp_device_status() == _lib.USP_ERR_TIMEOUT
+            b.run(usp)
+            _done(usp, guard)
+            b.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 6, 70])
+def test_abort_after_a_prefix_call_in_the_same_workspace(usp, n):
+    """One workspace for both calls: what a call behind a prefix noted of its rows is there when a call without one gives
+    up before it notes its own."""
+    guard = Guarded()
+    pre = Batch([(n, 700), (n, 500), (n, 900)], 8, 2, 128, 64, prefix=300).to_gpu(usp, guard)
+    own = Batch([(n, 700), (n, 500), (n, 900)], 8, 2, 128, 64, seed=1).to_gpu(usp, guard)
+    assert own.g["ws"].numel() <= pre.g["ws"].numel()
+    own.g["ws"] = pre.g["ws"]
+    for _ in range(2):
+        pre.run(usp)
+        _done(usp, guard)
+        pre.check()
+        usp.usp_diag_raise_status()
+        own.run(usp)
+        assert usp.usp_device_status() == _lib.USP_ERR_TIMEOUT
+        own.run(usp)
+        _done(usp, guard)
+        own.check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,d,page", [("bf16", 128, 64), ("f32", 64, 16)])
 def test_pool_beyond_32_bit_offsets(usp, dtype, d, page):
     """Pages whose elements lie beyond 2^31 of the pool."""
