@@ -1297,6 +1297,7 @@ static usp_status check_paged(const usp_cache* c, int n_tokens, int max_q, int p
     if (n_tokens < 0 || max_q < 1 || prefix_len < 0 || (int64_t)prefix_len > (int64_t)c->max_pages * c->page_size)
         return USP_ERR_INVALID_ARG;
     if ((int64_t)n_tokens * c->Hq > INT32_MAX - 512) return USP_ERR_UNSUPPORTED;  // rows, rounded up to whole tiles, are ints
+    if (c->n_seqs > 1 << 24) return USP_ERR_UNSUPPORTED;  // one warp passes over idle ones, 0.2 s for these; others wait 2 s
     return USP_OK;
 }
 

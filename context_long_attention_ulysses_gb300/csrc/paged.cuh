@@ -118,6 +118,15 @@ __device__ __forceinline__ int row_tiles(const PagedArgs& a, const SeqRows& s) {
     return (s.n * a.g + M - 1) / M;
 }
 
+// The first row tile with a key, row_tiles if none has one (limits grow with the row, so all from it on have keys): that of the
+// first token that sees a key from key_begin on.
+template <int M>
+__device__ __forceinline__ int first_row_tile(const PagedArgs& a, const SeqRows& s) {
+    const int keys = s.len - a.key_begin;
+    if (keys <= 0 || s.n == 0) return row_tiles<M>(a, s);
+    return a.causal ? max(s.n - keys, 0) * a.g / M : 0;
+}
+
 // Places of a unit of ut tiles on the line.
 template <int PC>
 __device__ __forceinline__ int unit_places(int ut) {
@@ -132,7 +141,7 @@ __device__ __forceinline__ int64_t head_places(const PagedArgs& a, int b) {
     if (nrt == 0) return 0;
     if (!a.causal || s.n == 1) return (int64_t)nrt * unit_places<PC>(unit_tiles<M, KT>(a, s, 0));
     int64_t sum = 0;
-    for (int rt = 0; rt < nrt; ++rt) sum += unit_places<PC>(unit_tiles<M, KT>(a, s, rt));
+    for (int rt = first_row_tile<M>(a, s); rt < nrt; ++rt) sum += unit_places<PC>(unit_tiles<M, KT>(a, s, rt));
     return sum;
 }
 
@@ -219,7 +228,24 @@ struct Seg {
     int first_cta;         // of a cut unit, known where it ends
 };
 
-// Walks a CTA's share piece by piece (own keys).  Uniform over the threads that call it.
+// The first sequence from b on that has a row with a key, n_seqs if there is none.  Called by whole warps, which look at 32
+// sequences at a time.  (One by one, and each of their eight heads: 60 us against 23 for eight sequences in 256 slots, 770 against
+// 92 in 4096, and a million idle slots on end took longer than the other warps wait for a piece.)
+__device__ __forceinline__ int next_sequence(const PagedArgs& a, int b) {
+    for (; b < a.n_seqs; b += 32) {
+        const int mine = b + (int)(threadIdx.x & 31);
+        bool has = false;
+        if (mine < a.n_seqs) {
+            const SeqRows s = seq_rows(a, mine);
+            has = s.n > 0 && s.len > a.key_begin;
+        }
+        const uint32_t some = __ballot_sync(~0u, has);
+        if (some) return b + __ffs(some) - 1;
+    }
+    return a.n_seqs;
+}
+
+// Walks a CTA's share piece by piece (own keys).  Uniform over the threads that call it, whole warps.
 template <int M, int KT, int PC>
 struct OwnWalk {
     const PagedArgs& a;
@@ -235,8 +261,8 @@ struct OwnWalk {
         nrt = row_tiles<M>(a, s);
         h = (int)(sh.off / sh.per_head);
         int64_t off = sh.off - h * sh.per_head;
-        rt = 0;
-        ut = unit_tiles<M, KT>(a, s, 0);
+        rt = first_row_tile<M>(a, s);
+        ut = unit_tiles<M, KT>(a, s, rt);
         while (off >= unit_places<PC>(ut) && rt + 1 < nrt) {
             off -= unit_places<PC>(ut);
             ++rt;
@@ -251,20 +277,17 @@ struct OwnWalk {
             if (pos >= end) return false;
             if (ut > 0 && pos < base + ut) break;
             base += ut;  // on to the next unit that has keys
-            do {
-                if (++rt >= nrt) {
-                    rt = 0;
-                    if (++h >= a.Hkv) {
-                        h = 0;
-                        do {
-                            if (++b >= a.n_seqs) return false;
-                            s = seq_rows(a, b);
-                            nrt = row_tiles<M>(a, s);
-                        } while (nrt == 0);
-                    }
+            if (++rt >= nrt) {
+                if (++h >= a.Hkv) {
+                    h = 0;
+                    b = next_sequence(a, b + 1);
+                    if (b >= a.n_seqs) return false;
+                    s = seq_rows(a, b);
+                    nrt = row_tiles<M>(a, s);
                 }
-                ut = unit_tiles<M, KT>(a, s, rt);
-            } while (ut == 0);
+                rt = first_row_tile<M>(a, s);
+            }
+            ut = unit_tiles<M, KT>(a, s, rt);
             base += PC;
         }
         const int64_t to = min(end, base + ut);
@@ -407,10 +430,8 @@ __device__ void finish_empty_rows(const PagedArgs& a, int cta, int n_cta) {
     const int per_seq = max(n_cta / a.n_seqs, 1), part = cta % per_seq;
     for (int b = cta / per_seq; b < a.n_seqs; b += n_cta / per_seq) {
         const SeqRows s = seq_rows(a, b);
-        const int nrt = row_tiles<M>(a, s);
-        int rt = 0;
-        while (rt < nrt && unit_tiles<M, KT>(a, s, rt) == 0) ++rt;  // limits grow with the row: the later tiles have keys, too
-        const uint32_t rows = rt < nrt ? rt * M : s.n * a.g;
+        const int rt = first_row_tile<M>(a, s);
+        const uint32_t rows = rt < row_tiles<M>(a, s) ? rt * M : s.n * a.g;
         for (uint32_t x = part * NT + threadIdx.x; x < rows * a.Hkv; x += per_seq * NT) {
             const int h = x / rows, R = x % rows, i = R / a.g;
             const int64_t row = (int64_t)(s.t0 + i) * a.Hq + h * a.g + (R - i * a.g);

@@ -822,6 +822,77 @@ def test_wide_tables_and_idle_slots(usp):
     b.check()
 
 
+def test_attention_refuses_more_sequences_than_a_warp_passes_over_in_time(lib):
+    c = _c(n_seqs=(1 << 24) + 1)
+    assert _status(_paged, c, q_start=FAKE) == 2
+    assert usp_mod.usp_paged_attn_workspace_size(c, 2, 1) == 0
+    assert usp_mod.usp_prefix_attn_workspace_size(c, 2, 1, 16) == 0
+    assert usp_mod.usp_paged_attn_workspace_size(_c(n_seqs=1 << 24), 2, 1) > 0
+
+
+def _few_live(usp, B, Hq, Hkv, d, dtype, live, ragged, prefix=0):
+    """B sequences of which those of `live` (index -> cached tokens) hold something, one token each; the others are idle
+    slots (or, ragged, sequences without a token in this call): o and lse of the live ones against the formula."""
+    import torch
+    page, mp = 16, max(-(-n // 16) for n in live.values())
+    n_pages = mp * len(live)
+    c = usp.Cache(n_pages, page, B, mp, Hq, Hkv, d, dtype=dtype)
+    gen = torch.Generator().manual_seed(B)
+    kp, vp = (torch.randn(c.pool_shape(), generator=gen).to(c.torch_dtype).cuda() for _ in range(2))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, lens = torch.full((B, mp), -1, **i32), torch.zeros(B, **i32)
+    at = torch.tensor(sorted(live), device="cuda")
+    table[at] = torch.randperm(n_pages, generator=gen).int().view(len(live), mp).cuda()
+    lens[at] = torch.tensor([live[b] for b in sorted(live)], **i32)
+    T, start, rows = B, None, at
+    if ragged:
+        T, rows = len(live), torch.arange(len(live), device="cuda")
+        n = torch.zeros(B, dtype=torch.int64, device="cuda")
+        n[at] = 1
+        start = torch.cat([torch.zeros(1, **i32), n.cumsum(0).int()])
+    qn = torch.randn((len(live), Hq, d), generator=gen).to(c.torch_dtype)
+    q = torch.zeros((T, Hq, d), dtype=c.torch_dtype, device="cuda")
+    q[rows] = qn.cuda()
+    o, lse = torch.full_like(q, 7.0), torch.full((T, Hq), 7.0, device="cuda")
+    pre = table[at[0]].contiguous() if prefix else None
+    ws = torch.empty(usp.usp_prefix_attn_workspace_size(c, T, 1, prefix), dtype=torch.uint8, device="cuda")
+    usp.usp_prefix_attn(c, T, 1, q, kp, vp, table, lens, start, pre, prefix, o, lse, ws)
+    torch.cuda.synchronize()
+    assert usp.usp_device_status() == 0
+    ro, rl, bo, bl = ref_attention(_np(qn), _np(kp), _np(vp), table[at].cpu().numpy(), lens[at].cpu().numpy(), None, True,
+                                   c.softmax_scale, dtype, None if pre is None else pre.cpu().numpy(), prefix)
+    assert (np.abs(_np(o[rows]) - ro) <= bo).all() and (np.abs(_np(lse[rows]) - rl) <= bl).all()
+    if not ragged:
+        idle = torch.ones(B, dtype=torch.bool, device="cuda")
+        idle[at] = False
+        assert not o[idle].any() and (lse[idle] == -math.inf).all()
+
+
+@pytest.mark.gpu
+def test_a_quarter_million_idle_slots(usp):
+    """Idle slots between two sequences are passed over in no time: at 0.18 us a slot and KV head, as it was, the gap takes
+    3 s, and the warps that wait for a piece give up after 2."""
+    _few_live(usp, 1 << 18, 64, 64, 64, "bf16", {0: 700, (1 << 18) - 1: 900}, False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_as_many_sequences_as_allowed(usp, dtype):
+    B = 1 << 24
+    _few_live(usp, B, 8, 2, 64, dtype, {1: 60, 1 << 23: 500, (1 << 23) + 31: 40, B - 1: 300}, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,Hq,Hkv", [("bf16", 8, 2), ("bf16", 40, 1), ("bf16", 4, 4), ("f32", 8, 2)])
+@pytest.mark.parametrize("B", [31, 33, 64, 500])
+def test_idle_slots_between_sequences(usp, B, dtype, Hq, Hkv):
+    for live in ({0: 100, B - 1: 40}, {B // 2: 300}, {B - 1: 1000}, {0: 33, 1: 5, B - 2: 17},
+                 {b: 20 + 7 * b for b in range(0, min(B, 100), 3)}):
+        _few_live(usp, B, Hq, Hkv, 64, dtype, live, False)
+        _few_live(usp, B, Hq, Hkv, 64, dtype, live, True)
+    _few_live(usp, B, Hq, Hkv, 64, dtype, {0: 100, B // 2: 44, B - 1: 70}, False, prefix=48)
+
+
 @pytest.mark.gpu
 def test_abort_path_gives_up_fast_and_recovers(usp):
     """With a timeout on record every kernel gives up at its first wait that is not satisfied, drains its loads and
