@@ -414,7 +414,8 @@ usp_status usp_ring_merge(int64_t rows, int d, const float* o_a, const float* ls
  * Requirements: n_pages, n_seqs, max_pages >= 0; page_size in {16, 32, 64,
  * 128, 256}; Hq, Hkv >= 1 and Hq % Hkv == 0; Hq <= 65535; d in {64, 128};
  * n_seqs and max_pages * page_size <= 2^31 - 1024, n_pages * Hkv < 2^31, and
- * for the attention calls n_seqs <= 2^24 and n_tokens * Hq <= 2^31 - 513. */
+ * for the attention calls n_seqs <= 2^24 and n_tokens * Hq <= 2^31 - 513, for
+ * usp_kv_append n_tokens <= 2^31 - 16. */
 typedef struct {
     int n_pages;
     int page_size;

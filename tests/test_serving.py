@@ -822,6 +822,12 @@ def test_wide_tables_and_idle_slots(usp):
     b.check()
 
 
+def test_append_refuses_more_tokens_than_its_grid_can_count(lib):
+    for T in ((1 << 31) - 1, (1 << 31) - 15):
+        assert _status(_append, T=T) == 2
+        assert _status(_append, _c(Hq=64, Hkv=64), T=T) == 2
+
+
 def test_attention_refuses_more_sequences_than_a_warp_passes_over_in_time(lib):
     c = _c(n_seqs=(1 << 24) + 1)
     assert _status(_paged, c, q_start=FAKE) == 2
