@@ -669,24 +669,27 @@ def _made_on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(_as_stream(stream))
 
 
-def _returned(stream, *tensors) -> None:
-    """Outputs made on `stream` go to a caller on the current one: the allocator must not hand them out before it is done."""
+def _share(stream, inputs, outputs) -> None:
+    """Where `stream` is not the current one, the allocator must not hand out the caller's inputs before `stream` has read
+    them, nor outputs, made on `stream`, before the caller's stream is done with them."""
     if stream is None:
         return
-    current = torch.cuda.current_stream()
-    if current.cuda_stream == _as_stream(stream).cuda_stream:
+    current, other = torch.cuda.current_stream(), _as_stream(stream)
+    if current.cuda_stream == other.cuda_stream:
         return
-    for t in tensors:
-        if t is not None:
-            t.record_stream(current)
+    for tensors, user in ((inputs, other), (outputs, current)):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(user)
 
 
 def kv_append(c: Cache, q, k, v, seq, pos, inv_freq, k_pages, v_pages, page_table, interleaved=False, rot_pos=None,
               stream=None):
     """Rotate q and k by their positions and write k and v into the cache (usp_kv_append).
 
-    q [T][Hq][d] (or None), k, v [T][Hkv][d], any token stride (they and the rest must be ready on `stream`); seq, pos (and rot_pos) int32 [T]; inv_freq float32
-    [rot/2] or None.  Returns (rotated q or None, rotated k); rows of padding tokens hold what torch.empty left."""
+    q [T][Hq][d] (or None), k, v [T][Hkv][d], any token stride; seq, pos (and rot_pos) int32 [T]; inv_freq float32 [rot/2]
+    or None.  With `stream`, what is passed must be ready there (it may be freed once the call returns).  Returns (rotated q
+    or None, rotated k); rows of padding tokens hold what torch.empty left."""
     dev, dt = _serving_device(k), c.torch_dtype
     T = k.shape[0]
     _check(c, "q", q, (T, c.Hq, c.d), dt, dev, optional=True)
@@ -705,7 +708,7 @@ def kv_append(c: Cache, q, k, v, seq, pos, inv_freq, k_pages, v_pages, page_tabl
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
     usp_kv_append(c, T, q, k, v, seq, pos, inv_freq, q_out, k_out, k_pages, v_pages, page_table, rot, interleaved,
                   rot_pos, stream)
-    _returned(stream, q_out, k_out)
+    _share(stream, (q, k, v, seq, pos, rot_pos, inv_freq, k_pages, v_pages, page_table), (q_out, k_out))
     return q_out, k_out
 
 
@@ -732,7 +735,7 @@ def paged_attention(c: Cache, q, k_pages, v_pages, page_table, seq_lens, q_start
         o, lse = _empty((T, c.Hq, c.d), dt, dev), _empty((T, c.Hq), torch.float32, dev)
         ws = _empty((max(size, 256),), torch.uint8, dev)
     usp_paged_attn(c, T, max_q, q, k_pages, v_pages, page_table, seq_lens, q_start, o, lse, ws, None, stream)
-    _returned(stream, o, lse)
+    _share(stream, (q, k_pages, v_pages, page_table, seq_lens, q_start), (o, lse))
     return o, lse
 
 
@@ -751,5 +754,5 @@ def prefix_attention(c: Cache, q, k_pages, v_pages, page_table, seq_lens, prefix
         ws = _empty((max(size, 256),), torch.uint8, dev)
     usp_prefix_attn(c, T, max_q, q, k_pages, v_pages, page_table, seq_lens, q_start, prefix_pages, prefix_len, o, lse,
                     ws, None, stream)
-    _returned(stream, o, lse)
+    _share(stream, (q, k_pages, v_pages, page_table, seq_lens, q_start, prefix_pages), (o, lse))
     return o, lse

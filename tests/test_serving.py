@@ -1074,6 +1074,92 @@ def test_helpers_on_a_side_stream_leave_freed_memory_alone(usp):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("handle", [False, True])
+def test_inputs_freed_while_a_side_stream_reads_them(usp, handle):
+    """A helper called for another stream may be given tensors that nothing else holds: their memory must not be handed
+    out here before that stream has read it."""
+    import torch
+    guard = Guarded()
+    b = Batch([(1, 200), (1, 190), (1, 129)], 8, 2, 128, 64, prefix=128).to_gpu(usp, guard)
+    g, c = b.g, b.c
+    whole = b.table.copy()
+    whole[:, :2] = b.prefix_pages
+    whole = torch.from_numpy(whole).cuda()
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = [torch.randn((3, H, 128), generator=gen, device="cuda").bfloat16() for H in (8, 2, 2)]
+    inv = (10000.0 ** (-torch.arange(64, device="cuda", dtype=torch.float64) / 64)).float()
+    kp, vp = torch.zeros_like(g["kp"]), torch.zeros_like(g["vp"])
+    seq = torch.arange(3, dtype=torch.int32, device="cuda")
+
+    def temporary(*ts):
+        return [t.clone() for t in ts]
+
+    def reused():  # whatever the allocator has free on this stream is written over
+        free = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in (512, 1024, 1536, 2048, 4096, 6144) for _ in range(24)]
+        for t in free:
+            t.fill_(0x3F)
+        torch.cuda.current_stream().synchronize()
+
+    def paged(q, lens):
+        return usp.paged_attention(c, q, g["kp"], g["vp"], whole, lens, stream=stream)
+
+    def prefix(q, lens, pages):
+        return usp.prefix_attention(c, q, g["kp"], g["vp"], g["table"], lens, pages, 128, stream=stream)
+
+    def append(q, k, v, seq, pos, inv):
+        return usp.kv_append(c, q, k, v, seq, pos, inv, kp, vp, whole, stream=stream)
+
+    for call, args in ((paged, (g["q"], g["lens"])), (prefix, (g["q"], g["lens"], g["prefix"])),
+                       (append, (*x, seq, g["lens"] - 1, inv))):
+        torch.cuda.synchronize()
+        want = [t.clone() for t in call(*args)]
+        torch.cuda.synchronize()
+        ts = temporary(*args)
+        torch.cuda.current_stream().synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)  # some 50 ms
+        got = call(*ts)
+        del ts
+        reused()
+        side.synchronize()
+        assert usp.usp_device_status() == 0
+        for a, w in zip(got, want):
+            assert torch.equal(a, w), call.__name__
+
+
+@pytest.mark.gpu
+def test_helpers_captured_on_a_forked_stream(usp):
+    """The same inside a capture: temporaries and outputs of a forked stream live as long as the graph needs them."""
+    import torch
+    guard = Guarded()
+    b = Batch([(1, 200), (1, 190), (1, 129)], 8, 2, 128, 64, prefix=128).to_gpu(usp, guard)
+    g = b.g
+    b.run(usp)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    outs = []
+    with torch.cuda.graph(graph, stream=main):
+        for scale in (1.0, 2.0):
+            q = g["q"] * scale
+            side.wait_stream(main)
+            o, lse = usp.prefix_attention(b.c, q, g["kp"], g["vp"], g["table"], g["lens"], g["prefix"], 128, stream=side)
+            del q
+            junk = torch.full_like(g["q"], float("nan"))
+            main.wait_stream(side)
+            outs.append((o + 0, lse + 0))
+            del o, lse, junk
+    for _ in range(2):
+        graph.replay()
+        _done(usp, guard)
+        b.check(*outs[0])
+    b.q = b.q * 2
+    b.check(*outs[1])
+
+
+@pytest.mark.gpu
 def test_helpers_on_the_default_stream_from_another(usp):
     """Stream handle 0 is the default stream: outputs and workspace are made there, whatever the current stream is."""
     import torch
