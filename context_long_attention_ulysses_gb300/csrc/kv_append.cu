@@ -2,8 +2,8 @@
 //
 // Per token, head and i < rot/2 the pair (a, b) of frequency f_i turns by the angle r f_i (r: the token's position):
 //   a' = a cos(r f_i) - b sin(r f_i),  b' = b cos(r f_i) + a sin(r f_i).
-// The angle is formed to 64 bits (in float32 the angle of position 10^6 is off by up to 0.06 rad); sine, cosine and the
-// rotation are float32.
+// The angle is formed to 64 bits for |f_i| < 2^24, in float64 beyond (in float32 the angle of position 10^6 is off by up to 0.06
+// rad); sine, cosine and the rotation are float32.
 //
 // Bound by HBM: every value is read once and written once (k twice with k_out).  A head is d / (2 V) items of two 16-byte
 // vectors (V values): the two that a rotation pairs up, or two neighbours where pairs are neighbours or pass unchanged.  A
@@ -31,8 +31,9 @@ constexpr int kMaxTokens = 16;
 
 // cos and sin of r * f.  Only the fraction of the turns r f / 2 pi counts, so it is formed in 64-bit fixed point, where whole
 // turns fall off the top: f = m 2^-shift with an integer m of 24 bits, the fraction of f / 2 pi is m * (2^64 / 2 pi) >> shift
-// to 64 bits, and times r, up to 2^31, it is off by less than 2^-30 turns for f up to 8.  (The scarce float64 units took 3.5 of
-// 144 us for a prompt of 32768 tokens; they remain for f of 2^24 and more, infinities and NaN.)
+// to 64 bits: off by f / 2 units of the last bit, as the constant is by a half, and by one of the shift.  Times r, up to 2^31, that
+// is less than 2^-30 turns for f up to 8.  (The scarce float64 units took 3.5 of 144 us for a prompt of 32768 tokens; they
+// remain for f of 2^24 and more, where r f and its turns are three roundings, 3 2^-53 of themselves; infinities and NaN give NaN.)
 __device__ __forceinline__ float2 turn(int r, float f) {
     const uint32_t bits = __float_as_uint(f) & 0x7fffffffu;
     const int exponent = (int)(bits >> 23), shift = 150 - exponent;

@@ -435,8 +435,11 @@ typedef struct {
  * the pair (a, b) = elements (i, i + rot/2), or (2i, 2i+1) if interleaved:
  *   a' = a cos(r f_i) - b sin(r f_i) ;  b' = b cos(r f_i) + a sin(r f_i)
  * with f_i = inv_freq[i] (float32 [rot/2]); elements rot.. pass unchanged.
- * The angle is formed to 64 bits (a float32 product of position 10^6 and f_0
- * would be off by up to 0.06 rad), the rotation in float32, rounded once.
+ * f_i is finite, of either sign.  For |f_i| < 2^24 the angle is off by less
+ * than (|f_i| / 2 + 1) |r| 2^-64 turns, then rounded to float32 (a float32
+ * product of position 10^6 and f_0 = 1 would be off by up to 0.06 rad); from
+ * 2^24 on, which no model uses, r f_i is a float64 product, off by 3 2^-53 of
+ * itself.  The rotation is float32, rounded once.
  *   q_out [n_tokens][Hq][d] = rotated q ;  k_out [n_tokens][Hkv][d] = rotated k
  *   k_pages[page_table[s][p / page_size]][h][p % page_size] = rotated k,
  *   v_pages likewise = v

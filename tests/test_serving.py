@@ -438,6 +438,63 @@ def test_append(usp, dtype, Hq, Hkv, d, rot, inter, T, page, far):
     assert torch.equal(q2[~m], q[~m]) and torch.equal(k2[~m], k[~m])
 
 
+def _turns(r, f):
+    """r f / 2 pi less whole turns, to the nearest float64: whole-number arithmetic on 400 bits of 1 / 2 pi."""
+    bits = 400
+    atan_inv = lambda n: sum((-1) ** k * (1 << bits + 64) // ((2 * k + 1) * n ** (2 * k + 1)) for k in range(120))  # noqa: E731
+    pi = 16 * atan_inv(5) - 4 * atan_inv(239)                   # Machin's formula, scaled by 2^464
+    per_turn = (1 << 2 * bits + 64) // (2 * pi)                 # 1 / 2 pi, scaled by 2^400
+    num, den = np.float32(f).item().as_integer_ratio()          # den is a power of two
+    x = r * num * per_turn % (den << bits)                      # (Python's %: 0 <= x)
+    x = x - (den << bits) if 2 * x >= den << bits else x
+    return x / (den << bits)
+
+
+def test_oracle_turns():
+    assert _turns(0, 1.0) == 0.0
+    for r, f in ((1, 1.0), (1000, 0.25), (-7, 0.5), (123456, 1e-3), (3, -2.0)):
+        t = r * float(np.float32(f)) / (2 * math.pi)
+        assert abs(_turns(r, f) - (t - round(t))) < 1e-11
+    # the continued fraction of pi: 710 / 113 of 2 pi is 60 times 10^-6 short of whole
+    assert abs(_turns(710, 1.0) * 2 * math.pi - (710 - 226 * math.pi)) < 1e-12
+
+
+FREQ = [1.0, -1.0, 0.0, -0.0, 0.73, 7.9, -7.9, 3.1e-3, 2.0 ** -40, 1.7 * 2.0 ** -41, 1.9 * 2.0 ** -42, 1.1 * 2.0 ** -60,
+        -1.3 * 2.0 ** -104, 1.5 * 2.0 ** -106, 2.0 ** -126, 2.0 ** -140, 8.1, 1000.5, -2.0 ** 22 * 1.3, 2.0 ** 23 * 1.9,
+        2.0 ** 24, 1.7 * 2.0 ** 24, -1.1 * 2.0 ** 25, 1.3 * 2.0 ** 31]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_angles_of_every_size(usp, inter):
+    """Frequencies of either sign, zero, subnormal, from far below one to 2^31, at the nearest and the farthest positions:
+    cosine and sine themselves, of pairs (1, 0), against angles in whole-number arithmetic."""
+    import torch
+    r = [0, 1, 2, 3, 710, 1000, 131071, 1 << 20, (1 << 24) + 1, (1 << 30) - 1, (1 << 31) - 1, -1, -710, -(1 << 31)]
+    T, half, d = len(r), len(FREQ), 64
+    c = usp.Cache(T, 16, T, 1, 1, 1, d, dtype="f32")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    a = torch.zeros((T, 1, d), device="cuda")
+    first = torch.arange(0, 2 * half, 2) if inter else torch.arange(half)
+    other = first + 1 if inter else first + half
+    a[..., first] = 1.0
+    kp, vp = (torch.zeros(c.pool_shape(), device="cuda") for _ in range(2))
+    f = np.array(FREQ, np.float32)
+    _, k = usp.kv_append(c, None, a, a, torch.arange(T, **i32), torch.zeros(T, **i32), torch.from_numpy(f).cuda(), kp, vp,
+                         torch.arange(T, **i32)[:, None].contiguous(), inter, torch.tensor(r, **i32))
+    torch.cuda.synchronize()
+    k = _np(k)[:, 0]
+    turns = np.array([[_turns(ri, fi) for fi in FREQ] for ri in r])
+    size, far = np.abs(f.astype(np.float64))[None], np.abs(np.array(r, np.float64))[:, None]
+    # the angle, in radians: the fixed-point product or the three roundings in float64; whole 2^-31 half-turns and the rounding of
+    # up to one half-turn to float32.  Then sine and cosine, two steps of a value up to 1.
+    angle = np.where(size < 2.0 ** 24, 2 * math.pi * (size / 2 + 1) * far * 2.0 ** -64, 3 * 2.0 ** -53 * size * far)
+    bound = angle * (1 + 2.0 ** -20) + math.pi * (2.0 ** -31 + 2.0 ** -24) + 2 * 2.0 ** -23
+    assert (np.abs(k[:, first] - np.cos(2 * math.pi * turns)) <= bound).all()
+    assert (np.abs(k[:, other] - np.sin(2 * math.pi * turns)) <= bound).all()
+    assert (k[:, 2 * half:] == 0).all()
+
+
 PAGED = [  # seqs, Hq, Hkv, d, page, dtype, more
     (SMALL, 4, 4, 64, 16, {}),
     (SMALL, 32, 8, 128, 64, {}),
