@@ -479,9 +479,10 @@ size_t usp_paged_attn_workspace_size(const usp_cache* c, int n_tokens, int max_q
  * Values out of range: q_start is clamped to [0, n_tokens], seq_lens to [0,
  * max_pages*page_size]; keys of a page table entry outside [0, n_pages) are
  * left out.  What pages hold beyond a sequence's length (NaN, too) never
- * reaches a result.  A value that is not finite in a key or value below len
- * may reach every row of its sequence, masked or not (0 * inf in the product);
- * a NaN in a query makes that row's o and lse NaN.
+ * reaches a result (usp_prefix_attn: beyond its length and the prefix).  A
+ * value that is not finite in a key or value below len may reach every row of
+ * its sequence, masked or not (0 * inf in the product); a NaN in a query makes
+ * that row's o and lse NaN.
  * BF16: float32 scores, sums and accumulation, probabilities rounded to bf16
  * for the product with V; F32: float32 throughout, on CUDA cores.  Results do
  * not depend on the run (fixed order of sums).
@@ -504,9 +505,11 @@ size_t usp_prefix_attn_workspace_size(const usp_cache* c, int n_tokens, int max_
  * prefix ends inside a page, the sequence's own page holds its tokens from
  * there on).  Masks, lengths (seq_lens counts the prefix), rows and checks as
  * usp_paged_attn, whose results it gives up to rounding; a sequence no longer
- * than the prefix sees that part of it.  0 <= prefix_len <=
- * max_pages*page_size.  ws: at least usp_prefix_attn_workspace_size(c,
- * n_tokens, max_q, prefix_len) bytes, 256-byte aligned. */
+ * than the prefix sees that part of it.  The prefix is one piece to all rows of
+ * the batch: a value of it that is not finite may reach every row, those of
+ * sequences that end before it, too.  0 <= prefix_len <= max_pages*page_size.
+ * ws: at least usp_prefix_attn_workspace_size(c, n_tokens, max_q, prefix_len)
+ * bytes, 256-byte aligned. */
 usp_status usp_prefix_attn(const usp_cache* c, int n_tokens, int max_q, const void* q, const void* k_pages,
                            const void* v_pages, const int32_t* page_table, const int32_t* seq_lens,
                            const int32_t* q_start, const int32_t* prefix_pages, int prefix_len, void* o, float* lse,

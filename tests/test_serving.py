@@ -770,6 +770,34 @@ def test_nan_of_a_query_or_key_shows(usp, n, dtype, prefix):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 6, 70])
+def test_infinite_value_of_a_prefix(usp, n, dtype):
+    """An infinity among the prefix's values reaches that column of that KV head only: there the rows that see it, and
+    perhaps those of a sequence that ends before it.  Everything else keeps its bits, and what the pages hold beyond
+    lengths and prefix (NaN in every test) still reaches nothing."""
+    import torch
+    guard = Guarded()
+    b = Batch([(n, 700), (n, 290), (n, 350), (n, 60 + n)], 8, 2, 128, 64, dtype, prefix=300).to_gpu(usp, guard)
+    o, lse = (x.clone() for x in b.run(usp))
+    _done(usp, guard)
+    b.check()
+    key = 295                                                       # the second and the fourth sequence end before it
+    b.g["vp"][int(b.prefix_pages[key // 64]), 1, key % 64, 9] = float("inf")
+    b.run(usp)
+    _done(usp, guard)
+    assert torch.equal(b.g["lse"], lse)
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[:, 4:, 9] = True
+    assert torch.equal(b.g["o"][~hit], o[~hit])
+    last = b.g["o"][[n - 1, 3 * n - 1], 4:, 9]                      # the newest token of the others sees it
+    assert not torch.isfinite(last).any()
+    short = b.g["o"][[*range(n, 2 * n), *range(3 * n, 4 * n)], 4:, 9]
+    was = o[[*range(n, 2 * n), *range(3 * n, 4 * n)], 4:, 9]
+    assert (torch.isnan(short) | (short == was)).all()
+
+
+@pytest.mark.gpu
 def test_captured_fork_and_join(usp):
     """A captured step whose appending runs on a stream of its own beside other work, and whose attention waits for both."""
     import torch
