@@ -742,7 +742,7 @@ def paged_attention(c: Cache, q, k_pages, v_pages, page_table, seq_lens, q_start
 def prefix_attention(c: Cache, q, k_pages, v_pages, page_table, seq_lens, prefix_pages, prefix_len: int, q_start=None,
                      max_q=1, stream=None):
     """paged_attention for sequences that share their first prefix_len tokens, held by the pages prefix_pages
-    (int32 [ceil(prefix_len/page_size)]): those are read once for the whole batch (usp_prefix_attn)."""
+    (int32 [ceil(prefix_len/page_size)]): those are read for many sequences at a time (usp_prefix_attn)."""
     dev, dt = _check_paged(c, q, k_pages, v_pages, page_table, seq_lens, q_start)
     _check(c, "prefix_pages", prefix_pages, (None,), torch.int32, dev)
     if prefix_pages.numel() < c.pages_for(prefix_len):

@@ -161,7 +161,7 @@ struct PagedArgs {
     float* lse;
     int n_tokens, n_seqs, max_pages, n_pages, page_log2;
     int Hq, Hkv, g, d, elem, causal;
-    int prefix_len;   // > 0: keys below it come from prefix_pages, once for the batch
+    int prefix_len;   // > 0: keys below it come from prefix_pages, for all sequences
     int key_begin;    // first own key (= prefix_len)
     float scale_log2; // softmax scale * log2(e)
     // the plan: row-tile sizes and CTAs of the own and the prefix part, and the workspace

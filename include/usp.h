@@ -498,9 +498,10 @@ size_t usp_prefix_attn_workspace_size(const usp_cache* c, int n_tokens, int max_
 
 /* usp_paged_attn for a batch whose sequences share their first prefix_len
  * tokens: those keys and values are read from prefix_pages (int32
- * [ceil(prefix_len/page_size)], pages of the same pool) once for the whole
- * batch -- one matrix product over all rows per KV head -- and joined by
- * log-sum-exp with each sequence's own keys prefix_len .. len-1, which its page
+ * [ceil(prefix_len/page_size)], pages of the same pool) not once per sequence
+ * but once per tile of the batch's rows of a KV head, the tiles side by side,
+ * mostly from L2 -- BF16: up to 256 rows, a matrix product on the tensor
+ * cores; F32: 8 rows, on CUDA cores -- and joined by log-sum-exp with each sequence's own keys prefix_len .. len-1, which its page
  * table gives as always (entries of whole prefix pages are not read; where the
  * prefix ends inside a page, the sequence's own page holds its tokens from
  * there on).  Masks, lengths (seq_lens counts the prefix), rows and checks as
