@@ -689,7 +689,8 @@ def kv_append(c: Cache, q, k, v, seq, pos, inv_freq, k_pages, v_pages, page_tabl
 
     q [T][Hq][d] (or None), k, v [T][Hkv][d], any token stride; seq, pos (and rot_pos) int32 [T]; inv_freq float32 [rot/2]
     or None.  With `stream`, what is passed must be ready there (it may be freed once the call returns).  Returns (rotated q
-    or None, rotated k); rows of padding tokens hold what torch.empty left."""
+    or None, rotated k); rows of padding tokens hold what torch.empty left.  (usp_kv_append with k_out None leaves the rotated
+    k, which decoding does not need, out.)"""
     dev, dt = _serving_device(k), c.torch_dtype
     T = k.shape[0]
     _check(c, "q", q, (T, c.Hq, c.d), dt, dev, optional=True)
@@ -727,7 +728,8 @@ def paged_attention(c: Cache, q, k_pages, v_pages, page_table, seq_lens, q_start
     """Attention of each sequence's newest tokens over its cached keys (usp_paged_attn): returns (o, lse).
 
     q [T][Hq][d]; q_start int32 [n_seqs + 1] (None: one token per sequence); max_q: the largest number of tokens a
-    sequence has in this call.  Rows of no sequence hold what torch.empty left."""
+    sequence has in this call.  Rows of no sequence hold what torch.empty left.  Checks, outputs and workspace take the host
+    20 us more than usp_paged_attn with buffers that are kept."""
     dev, dt = _check_paged(c, q, k_pages, v_pages, page_table, seq_lens, q_start)
     T = q.shape[0]
     size = usp_paged_attn_workspace_size(c, T, max_q)

@@ -476,6 +476,10 @@ size_t usp_paged_attn_workspace_size(const usp_cache* c, int n_tokens, int max_q
  * (n_tokens == n_seqs).  Rows of no sequence (before q_start[0], from
  * q_start[n_seqs] on) stay as they were.  max_q: the largest n_q (>= 1); it
  * picks the kernel for that many rows, and a wrong value costs speed only.
+ * That kernel serves the whole call: sequences with a token each next to one
+ * with a long piece of a prompt are faster in a call of their own (32 query
+ * and 8 KV heads of 128, 63 sequences of 500 to 8000 tokens and one piece of
+ * 512 at 8192: 298 us in one call, 187 and 73 in two).
  * Values out of range: q_start is clamped to [0, n_tokens], seq_lens to [0,
  * max_pages*page_size]; keys of a page table entry outside [0, n_pages) are
  * left out.  What pages hold beyond a sequence's length (NaN, too) never
