@@ -497,7 +497,11 @@ usp_status usp_paged_attn(const usp_cache* c, int n_tokens, int max_q, const voi
                           const void* v_pages, const int32_t* page_table, const int32_t* seq_lens,
                           const int32_t* q_start, void* o, float* lse, void* ws, size_t ws_bytes, usp_stream stream);
 
-/* Bytes of workspace usp_prefix_attn needs; 0 for an invalid problem. */
+/* Bytes of workspace usp_prefix_attn needs; 0 for an invalid problem.  They
+ * follow how the prefix is cut and do not grow with n_tokens and prefix_len
+ * throughout (bf16, 32 query and 8 KV heads of 128, 32768 shared tokens: 25 MB
+ * for 64 tokens, 15 MB for 65): a workspace that is kept for several shapes
+ * has the largest of their sizes. */
 size_t usp_prefix_attn_workspace_size(const usp_cache* c, int n_tokens, int max_q, int prefix_len);
 
 /* usp_paged_attn for a batch whose sequences share their first prefix_len
@@ -505,12 +509,13 @@ size_t usp_prefix_attn_workspace_size(const usp_cache* c, int n_tokens, int max_
  * [ceil(prefix_len/page_size)], pages of the same pool) not once per sequence
  * but once per tile of the batch's rows of a KV head, the tiles side by side,
  * mostly from L2 -- BF16: up to 256 rows, a matrix product on the tensor
- * cores; F32: 8 rows, on CUDA cores -- and joined by log-sum-exp with each sequence's own keys prefix_len .. len-1, which its page
- * table gives as always (entries of whole prefix pages are not read; where the
- * prefix ends inside a page, the sequence's own page holds its tokens from
- * there on).  Masks, lengths (seq_lens counts the prefix), rows and checks as
- * usp_paged_attn, whose results it gives up to rounding; a sequence no longer
- * than the prefix sees that part of it.  The prefix is one piece to all rows of
+ * cores; F32: 8 rows, on CUDA cores -- and joined by log-sum-exp with each
+ * sequence's own keys prefix_len .. len-1, which its page table gives as always
+ * (entries of whole prefix pages are not read; where the prefix ends inside a
+ * page, the sequence's own page holds its tokens from there on).  Masks,
+ * lengths (seq_lens counts the prefix), rows and checks as usp_paged_attn,
+ * whose results it gives up to rounding; a sequence no longer than the prefix
+ * sees that part of it.  The prefix is one piece to all rows of
  * the batch: a value of it that is not finite may reach every row, those of
  * sequences that end before it, too.  0 <= prefix_len <= max_pages*page_size.
  * ws: at least usp_prefix_attn_workspace_size(c, n_tokens, max_q, prefix_len)
