@@ -74,6 +74,18 @@ cudaError_t allow_smem(int bytes) {
     return e;
 }
 
+// A kernel's unit: rows, keys of a tile, CTAs that an SM holds, and the places on the line that its beginning and end count
+// (below).  The kernels are built with these, and paged_plan cuts the prefix and lays out the workspace by them.
+struct UnitShape {
+    int rows, keys, ctas_per_sm, piece;
+};
+constexpr int mma_steps(int d, int mt) { return d == 64 ? 2 : mt; }  // steps of 16 keys of a warp per tile
+constexpr UnitShape mma_unit(int d, int mt) {                        // paged_mma.cu, 16 mt rows
+    return {16 * mt, 64 * mma_steps(d, mt), mt == 1 ? 2 : 1, mma_steps(d, mt) == 1 ? 2 : 3};
+}
+constexpr UnitShape tc_unit(int ns) { return {128 * ns, 128, 1, 3}; }        // paged_tc.cu, ns streams
+constexpr UnitShape f32_unit(int d) { return {8, 8 * (1024 / d), 1, 2}; }    // paged_f32.cu
+
 // What paged_merge_kernel does with a row: word x = kind | row in the tile << 2, y = first CTA | last CTA << 16.
 enum RowKind : uint32_t {
     kRowDone = 0,   // nothing (finished, or a row of no sequence)

@@ -167,11 +167,11 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
-// The kernel for `rows` rows per KV head: rows of a unit, keys of a tile, CTAs that run at a time, and what beginning and
-// ending a unit costs in tiles.
+// The kernel for `rows` rows per KV head: its unit, and the CTAs that run at a time.
 struct Pick {
     int rows, keys, ctas, piece;
     float us;  // time of a tile
+    Pick(const UnitShape& u, float tile_us) : rows(u.rows), keys(u.keys), ctas(kSms * u.ctas_per_sm), piece(u.piece), us(tile_us) {}
 };
 // bf16 by the rows per KV head, 32 query and 8 KV heads of 128 values, 16 sequences of 1000 to 20000 tokens:
 //   20 rows: 84.1 us in a unit of 32 (m16n8k16 products), 93.2 in one of 128 (tcgen05); 32 rows: 85.2 and 90.9
@@ -179,10 +179,10 @@ struct Pick {
 //   64 rows: 93.1 in one of 128, 108 in one of 256, whose second stream is idle; 96 rows: 97.8 and 112
 // and 160 rows of 8 sequences: 59.6 in one of 256, 67.8 in two of 128.
 static Pick pick(const PagedArgs& a, int64_t rows) {
-    if (a.elem == 4) return {8, a.d == 64 ? 128 : 64, kSms, 2, 1.5f};
-    if (rows <= 16) return a.d == 64 ? Pick{16, 128, kSms * 2, 3, 1.5f} : Pick{16, 64, kSms * 2, 2, 1.5f};
-    if (rows <= 32) return {32, 128, kSms, 3, a.d == 64 ? 0.8f : 1.5f};
-    return rows <= 128 ? Pick{128, 128, kSms, 3, 1.1f} : Pick{256, 128, kSms, 3, 1.6f};
+    if (a.elem == 4) return {f32_unit(a.d), 1.5f};
+    if (rows <= 16) return {mma_unit(a.d, 1), 1.5f};
+    if (rows <= 32) return {mma_unit(a.d, 2), a.d == 64 ? 0.8f : 1.5f};
+    return rows <= 128 ? Pick{tc_unit(1), 1.1f} : Pick{tc_unit(2), 1.6f};
 }
 
 size_t paged_plan(PagedArgs* a, int max_q, void* ws) {

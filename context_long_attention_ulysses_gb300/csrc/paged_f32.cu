@@ -21,7 +21,7 @@ namespace usp {
 
 namespace {
 
-constexpr int kPieceCost = 2;  // see paged.cuh
+constexpr int kPieceCost = f32_unit(64).piece;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kRows = 8;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -30,6 +30,8 @@ template <int D>
 struct Cfg {
     static constexpr int kSub = 1024 / D;                         // keys of a warp in a tile
     static constexpr int kKeyTile = kWarps * kSub;
+    static_assert(f32_unit(D).rows == kRows && f32_unit(D).keys == kKeyTile && f32_unit(D).ctas_per_sm == 1 &&
+                  f32_unit(D).piece == kPieceCost, "the unit's shape");
     static constexpr int kStageFloats = kSub * 2 * D;             // K, V
     static constexpr int kStages = 3;                             // about 130 KB in flight per SM
     static constexpr int kOffJoin = kWarps * kStages * kStageFloats;

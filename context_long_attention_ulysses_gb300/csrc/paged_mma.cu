@@ -36,19 +36,21 @@ constexpr float kRescale = 8.0f;  // log2 units: O is rescaled only when the max
 
 template <int D, int MT>
 struct Cfg {
-    static constexpr int M = 16 * MT;
+    static constexpr UnitShape kUnit = mma_unit(D, MT);
+    static constexpr int M = kUnit.rows;
     // Steps of 16 keys of a warp per tile.  Two hide each other's latency and share the maximum's exchange, where the ring
     // allows for larger tiles: five tokens of 16 sequences 84.0 us against 88.0, one of 64 sequences with heads of 64 values 85.7
     // against 100.  (16 rows of 128 values would have stages of 64 KB, one and a half per CTA.)
-    static constexpr int KS = D == 64 ? 2 : MT;
-    static constexpr int kKeyTile = 16 * KS * kGroup;
+    static constexpr int KS = mma_steps(D, MT);
+    static constexpr int kKeyTile = kUnit.keys;
+    static_assert(M == 16 * MT && kKeyTile == 16 * KS * kGroup, "the unit's shape");
     // Places that a piece's beginning and end (rows of Q, the join, the stores) count, in tiles.  It takes about 3 us, a tile of
     // 64 keys 1.5 us at the memory's rate where two CTAs share the SM.  With two steps: 88.4, 84.5, 84.0, 83.8, 84.3 us for
     // five tokens of 16 sequences at 1 to 5, and 37.8 at 2, 38.0 at 3, 39.6 at 4 for those of 64 short ones.
-    static constexpr int kPieceCost = KS == 1 ? 2 : 3;
+    static constexpr int kPieceCost = kUnit.piece;
     static constexpr int kConsumers = kGroup * MT;
     static constexpr int kThreads = 32 * (kConsumers + 1);
-    static constexpr int kCtasPerSm = MT == 1 ? 2 : 1;
+    static constexpr int kCtasPerSm = kUnit.ctas_per_sm;
     static constexpr int kChunks = D / 64;                                    // 64-column boxes per row
     static constexpr int kTileBytes = kKeyTile * D * 2;                       // K or V of a tile
     static constexpr int kStages = D == 64 ? 3 * MT : 3;                      // 192 KB in flight per SM

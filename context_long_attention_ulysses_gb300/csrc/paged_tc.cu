@@ -37,7 +37,8 @@ namespace {
 
 constexpr int kKeyTile = 128;
 // A piece's beginning and end (Q, the first products, the stores) against a tile's 1.5 to 2 us.
-constexpr int kPieceCost = 3;
+constexpr int kPieceCost = tc_unit(1).piece;
+static_assert(tc_unit(1).keys == kKeyTile && tc_unit(2).keys == kKeyTile && tc_unit(2).piece == kPieceCost, "the unit's shape");
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;  // log2 units
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;  // of 168 at launch (NS = 2): 2 * 208 + 88 <= 3 * 168
@@ -46,7 +47,8 @@ constexpr int kFlags = 8;  // ring of loaded-box masks; longer than the K ring b
 
 template <int D, int NS>
 struct Cfg {
-    static constexpr int M = 128 * NS;
+    static constexpr int M = tc_unit(NS).rows;
+    static_assert(M == 128 * NS && tc_unit(NS).ctas_per_sm == 1, "the unit's shape");
     static constexpr int kThreads = (4 * NS + 4) * 32;
     static constexpr int kChunks = D / 64;
     static constexpr int kTileBytes = kChunks * 128 * 128;  // 128 rows of bf16
