@@ -1259,6 +1259,10 @@ usp_status usp_kv_append(const usp_cache* c, int n_tokens, const void* q, int64_
         ((q && !stride_ok(q_stride, (int64_t)c->Hq * c->d, elem)) ||
          !stride_ok(k_stride, (int64_t)c->Hkv * c->d, elem) || !stride_ok(v_stride, (int64_t)c->Hkv * c->d, elem)))
         return USP_ERR_INVALID_ARG;
+    // (in place, rows that move would overwrite others that are still to be read)
+    if (n_tokens > 1 && ((q && q_out == q && q_stride != (int64_t)c->Hq * c->d) ||
+                         (k_out && k_out == k && k_stride != (int64_t)c->Hkv * c->d)))
+        return USP_ERR_INVALID_ARG;
     if (n_tokens > INT32_MAX - 15) return USP_ERR_UNSUPPORTED;  // tokens, rounded up to a CTA's sixteen, are an int
     if (n_tokens == 0 || c->n_seqs == 0 || c->n_pages == 0 || c->max_pages == 0) return USP_OK;  // no token has a slot
     const void* ptrs[] = {k, v, k_pages, v_pages};

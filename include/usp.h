@@ -447,8 +447,8 @@ typedef struct {
  * elements apart (slices of one projection's output are fine); 16-byte
  * aligned, strides at least the row and a multiple of 16 bytes.
  * q with q_out may both be NULL (no queries), and k_out may be NULL.  q_out
- * may be q and k_out may be k where the stride is the row length; otherwise
- * no overlap.  rot: a multiple of 16 with 0 <= rot <= d; 0 rotates nothing
+ * may be q and k_out may be k where the stride is the row length (otherwise
+ * USP_ERR_INVALID_ARG); no other overlap.  rot: a multiple of 16 with 0 <= rot <= d; 0 rotates nothing
  * (inv_freq may be NULL).
  * A token without a slot -- seq outside [0, n_seqs), pos outside [0,
  * max_pages*page_size), or a page table entry outside [0, n_pages) -- is

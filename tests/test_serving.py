@@ -907,6 +907,19 @@ def test_wide_tables_and_idle_slots(usp):
     b.check()
 
 
+def test_append_in_place_needs_rows_without_gaps(lib):
+    cc, far = _c().c(), FAKE + (1 << 16)
+    tail = [FAKE, FAKE, None, FAKE, 64, 0]
+
+    def status(T, q, sq, k, sk, qo, ko):
+        return lib.usp_kv_append(cc, T, q, sq, k, sk, far, 512, *tail, qo, ko, far, far, FAKE + 2, None)  # (bad table: 3)
+
+    for T in (2, 7):
+        assert status(T, FAKE, 512, FAKE, 128, FAKE, far) == 1 and status(T, FAKE, 256, FAKE, 512, far, FAKE) == 1
+        assert status(T, FAKE, 256, FAKE, 128, FAKE, FAKE) == 3 and status(T, FAKE, 512, FAKE, 512, far, far) == 3
+    assert status(1, FAKE, 512, FAKE, 512, FAKE, FAKE) == 3       # one token: no stride
+
+
 def test_append_refuses_more_tokens_than_its_grid_can_count(lib):
     for T in ((1 << 31) - 1, (1 << 31) - 15):
         assert _status(_append, T=T) == 2
