@@ -13,8 +13,9 @@
 // tile is 2 to 8 boxes per 64 columns, issued by as many lanes.  Boxes without a visible key, or of a page that the pool
 // does not have, are not loaded: their keys are left out by the warps that own them.
 //
-// Measured, 32 query and 8 KV heads of 128 values: one token of one sequence of 131072 in 83 us, 6.5 TB/s; of 64 sequences of
-// 17 to 32768 in 153 us, 6.6 TB/s; five tokens of 16 sequences in 80 us, 6.1 TB/s.
+// Measured, 32 query and 8 KV heads of 128 values, whole calls with their merge (in brackets this kernel alone, caches cold): one
+// token of one sequence of 131072 in 87 us, 6.2 TB/s (85); of 64 sequences of 17 to 32768 in 155 us, 6.5 TB/s (157); five
+// tokens of 16 sequences in 84 us, 5.8 TB/s (80, 6.1 TB/s).
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -313,7 +314,9 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtasPerSm)
                             p[u][hh] = pack_bf16(e0, e1);
                             p[u][hh + 2] = pack_bf16(e2, e3);
                             sum += (e0 + e1) + (e2 + e3);
-                            // O is divided by the sum of what the product below uses: the rounded probabilities
+                            // P is rounded to bf16, V's type: each p is off by up to 2^-8 of itself.  O is divided by the sum of
+                            // what the product uses, the rounded p, so that o is off by up to 2^-8 sum p|v - o| / sum p (measured
+                            // 2.0e-3 to 2.3e-3 of the output, with the output's own rounding, 1.7e-3 by itself)
                             const float f0 = __uint_as_float(p[u][hh] << 16), f1 = __uint_as_float(p[u][hh] & 0xffff0000u),
                                         f2 = __uint_as_float(p[u][hh + 2] << 16),
                                         f3 = __uint_as_float(p[u][hh + 2] & 0xffff0000u);

@@ -470,6 +470,11 @@ __global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
                     }
                     tmem_st16(scol + h * 16, pk);  // P over S: this row's S is in registers
                 }
+                // P is rounded to bf16: both operands of the product have V's type.  Each p is off by up to 2^-8 of itself, o by up to
+                // 2^-8 sum p|v| / sum p (measured 2.3e-3 of the output, with the output's own rounding, 1.7e-3 by itself; a second
+                // product with what the rounding leaves would be half as much tensor work again).  O is divided by the sum of
+                // the unrounded p: the sum of the rounded ones, as in paged_mma.cu, is two more operations per pair in the warps
+                // that this kernel waits for.
                 l_run = l_run * alpha + ((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y));
                 // Made ahead, S_j was signalled before the product of tile j - 1, even j - 2, had to be complete.  Each is
                 // waited for, in order (a phase that is skipped could be taken for the one after next), the last but one always.
