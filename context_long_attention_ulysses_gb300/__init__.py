@@ -112,18 +112,19 @@ class Cache:
     dtype: str = "bf16"
 
     def c(self) -> UspCache:
-        """The struct of the C ABI (kept: a decoding step is short enough for its making to show)."""
-        made = self.__dict__.get("_c")
-        if made is None:
-            made = self._make()
-            object.__setattr__(self, "_c", made)
-        return made
-
-    def _make(self) -> UspCache:
+        """A struct of the C ABI, the caller's own."""
         if self.dtype not in _TORCH_DTYPE:
             raise ValueError(f"dtype must be 'f32' or 'bf16', got {self.dtype!r}")
         return UspCache(self.n_pages, self.page_size, self.n_seqs, self.max_pages, self.Hq, self.Hkv, self.d,
                         int(bool(self.causal)), float(self.scale), USP_F32 if self.dtype == "f32" else USP_BF16)
+
+    def _kept(self) -> UspCache:
+        """The struct that calls pass on (kept: a decoding step is short enough for its making to show)."""
+        made = self.__dict__.get("_c")
+        if made is None:
+            made = self.c()
+            object.__setattr__(self, "_c", made)
+        return made
 
     @property
     def torch_dtype(self) -> torch.dtype:
@@ -196,7 +197,7 @@ def _rows(x, heads: int, d: int):
 def _cache(c) -> ctypes.POINTER(UspCache):
     if c is None:
         return None
-    return ctypes.byref(c.c() if isinstance(c, Cache) else c)
+    return ctypes.byref(c._kept() if isinstance(c, Cache) else c)
 
 
 def _prob(p) -> ctypes.POINTER(UspProblem):

@@ -345,6 +345,21 @@ def test_helpers_check_tensors():
         usp_mod.Cache(1, 16, 1, 1, 1, 1, 64, dtype="fp8").c()
 
 
+def test_struct_of_a_cache_is_the_callers_own(lib):
+    """A changed struct is another cache's: it does not reach the calls of the one it was made from."""
+    import copy
+    import pickle
+    c = _c()
+    size = usp_mod.usp_paged_attn_workspace_size(c, 2, 1)
+    assert size > 0
+    s = c.c()
+    s.d, s.causal = 96, 0
+    assert usp_mod.usp_paged_attn_workspace_size(s, 2, 1) == 0
+    assert usp_mod.usp_paged_attn_workspace_size(c, 2, 1) == size and c.c().d == 64 and c.c().causal == 1
+    for other in (copy.copy(c), copy.deepcopy(c), pickle.loads(pickle.dumps(c))):
+        assert other == c and usp_mod.usp_paged_attn_workspace_size(other, 2, 1) == size
+
+
 def test_row_strides_of_a_fused_projection():
     import torch
     x = torch.zeros(5, 8 * 64)
