@@ -438,8 +438,8 @@ typedef struct {
  * f_i is finite, of either sign.  For |f_i| < 2^24 the angle is off by less
  * than (|f_i| / 2 + 1) |r| 2^-64 turns, then rounded to float32 (a float32
  * product of position 10^6 and f_0 = 1 would be off by up to 0.06 rad); from
- * 2^24 on, which no model uses, r f_i is a float64 product, off by 3 2^-53 of
- * itself.  The rotation is float32, rounded once.
+ * 2^24 on r f_i and its turns are formed in float64, off by 3 2^-53 of r f_i.
+ * The rotation is float32, rounded once.
  *   q_out [n_tokens][Hq][d] = rotated q ;  k_out [n_tokens][Hkv][d] = rotated k
  *   k_pages[page_table[s][p / page_size]][h][p % page_size] = rotated k,
  *   v_pages likewise = v
@@ -448,8 +448,8 @@ typedef struct {
  * aligned, strides at least the row and a multiple of 16 bytes.
  * q with q_out may both be NULL (no queries), and k_out may be NULL.  q_out
  * may be q and k_out may be k where the stride is the row length (otherwise
- * USP_ERR_INVALID_ARG); no other overlap.  rot: a multiple of 16 with 0 <= rot <= d; 0 rotates nothing
- * (inv_freq may be NULL).
+ * USP_ERR_INVALID_ARG); no other overlap.  rot: a multiple of 16 with
+ * 0 <= rot <= d; 0 rotates nothing (inv_freq may be NULL).
  * A token without a slot -- seq outside [0, n_seqs), pos outside [0,
  * max_pages*page_size), or a page table entry outside [0, n_pages) -- is
  * padding: nothing is written for it, its rows of q_out and k_out stay as

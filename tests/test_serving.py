@@ -851,6 +851,30 @@ def test_captured_fork_and_join(usp):
 
 
 @pytest.mark.gpu
+def test_traced_calls_give_the_same_bits(usp):
+    """Events between the launches, which then no longer overlap: the same results, and each launch on record."""
+    import torch
+    guard = Guarded()
+    bs = [Batch([(n, 900 + 100 * i) for i in range(5)], 8, 2, 128, 64, seed=n, prefix=p).to_gpu(usp, guard)
+          for n, p in ((1, 0), (1, 640), (70, 0))]
+    plain = [tuple(x.clone() for x in b.run(usp)) for b in bs]
+    _done(usp, guard)
+    usp.usp_trace_reset()
+    usp.usp_trace_enable(True)
+    try:
+        for b, (o, lse) in zip(bs, plain):
+            b.g["o"].fill_(7.0)
+            b.run(usp)
+            _done(usp, guard)
+            assert torch.equal(b.g["o"], o) and torch.equal(b.g["lse"], lse)
+        seen = {name: launches for name, (launches, _) in usp.usp_trace_report().items()}
+    finally:
+        usp.usp_trace_enable(False)
+        usp.usp_trace_reset()
+    assert seen == {"paged_own": 3, "paged_prefix": 1, "paged_merge": 3}
+
+
+@pytest.mark.gpu
 def test_two_streams_at_once(usp):
     import torch
     guard = Guarded()
