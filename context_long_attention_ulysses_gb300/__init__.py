@@ -21,8 +21,8 @@ from dataclasses import dataclass
 
 import torch
 
-from ._lib import (NOALLOC_SCRATCH_BYTES, SYMBOLS, USP_BF16, USP_F32, USP_OK, UspCache, UspError,  # noqa: F401
-                   UspProblem, UspTraceEntry, check, load)
+from ._lib import (NOALLOC_SCRATCH_BYTES, SYMBOLS, USP_BF16, USP_F32, USP_MAX_AXES, USP_OK, UspCache,  # noqa: F401
+                   UspError, UspProblem, UspRotary, UspTraceEntry, check, load)
 
 __all__ = [
     "Problem", "UspError", "SYMBOLS",
@@ -42,6 +42,9 @@ __all__ = [
     "usp_attn_bwd_deterministic_workspace_size", "usp_attn_bwd_deterministic",
     "Cache", "usp_kv_append", "usp_paged_attn_workspace_size", "usp_paged_attn", "usp_prefix_attn_workspace_size",
     "usp_prefix_attn", "kv_append", "paged_attention", "prefix_attention",
+    "Rotary", "usp_rotary_embed", "usp_kv_append_axes", "rotary_embed", "kv_append_axes",
+    "usp_pages_update_workspace_size", "usp_pages_update", "usp_pages_compact", "usp_pages_copy", "pages_empty",
+    "pages_update", "pages_compact", "pages_copy", "usp_verify_drafts", "verify_drafts",
 ]
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -146,6 +149,52 @@ class Cache:
         return -(-tokens // self.page_size)
 
 
+@dataclass(frozen=True)
+class Rotary:
+    """Rotary positions with several axes: axis[i] is the axis of pair i of a head's elements."""
+    axis: tuple
+    interleaved: bool = False  # pairs are elements (2i, 2i+1), otherwise (i, i + rot/2)
+    n_axes: int = 0            # 0: as many as axis names
+
+    @staticmethod
+    def sections(sizes, cycled=False, interleaved=False) -> "Rotary":
+        """sizes[a] pairs of axis a: one axis after the other, or (cycled) the axes in turn, with the pairs for which the
+        axis in turn has no more left going to axis 0."""
+        sizes = tuple(int(n) for n in sizes)
+        n = len(sizes)
+        if cycled:
+            axis = tuple(i % n if i // n < sizes[i % n] else 0 for i in range(sum(sizes)))
+            if any(axis.count(a) != sizes[a] for a in range(n)):
+                raise ValueError(f"axes in turn do not come out as {sizes}")
+        else:
+            axis = tuple(a for a, k in enumerate(sizes) for _ in range(k))
+        return Rotary(axis, interleaved, n)
+
+    @property
+    def axes(self) -> int:
+        return self.n_axes or max(self.axis, default=0) + 1
+
+    @property
+    def rot(self) -> int:
+        return 2 * len(self.axis)
+
+    def c(self) -> UspRotary:
+        """A struct of the C ABI, the caller's own."""
+        if len(self.axis) > 64:
+            raise ValueError(f"at most 64 pairs, got {len(self.axis)}")
+        if any(not 0 <= int(a) < self.axes for a in self.axis) or self.axes > USP_MAX_AXES:
+            raise ValueError(f"axes are 0 .. {min(self.axes, USP_MAX_AXES) - 1}")
+        return UspRotary(self.axes, self.rot, int(bool(self.interleaved)), (ctypes.c_uint8 * 64)(*self.axis))
+
+    def _kept(self) -> UspRotary:
+        """The struct that calls pass on."""
+        made = self.__dict__.get("_c")
+        if made is None:
+            made = self.c()
+            object.__setattr__(self, "_c", made)
+        return made
+
+
 def library_path() -> str:
     from .build import LIB
     return LIB
@@ -192,6 +241,19 @@ def _rows(x, heads: int, d: int):
     if shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
         raise ValueError("the heads of a token must be contiguous")
     return x.data_ptr(), stride[0] if shape[0] > 1 else heads * d
+
+
+def _token_rows(x, heads: int, d: int):
+    """`_rows` of a sequence-sharded tensor [P][B][N/P][heads][d], or of one that is [tokens][heads][d] already."""
+    if isinstance(x, torch.Tensor) and x.dim() == 5:
+        x = x.view(-1, *x.shape[3:])   # (raises where the tokens are not evenly apart)
+    return _rows(x, heads, d)
+
+
+def _rotary(r) -> ctypes.POINTER(UspRotary):
+    if r is None:
+        return None
+    return ctypes.byref(r._kept() if isinstance(r, Rotary) else r)
 
 
 def _cache(c) -> ctypes.POINTER(UspCache):
@@ -423,6 +485,78 @@ def usp_prefix_attn(c, n_tokens: int, max_q: int, q, k_pages, v_pages, page_tabl
                                                     _ptr(v_pages), _ptr(page_table), _ptr(seq_lens), _ptr(q_start),
                                                     _ptr(prefix_pages), int(prefix_len), _ptr(o), _ptr(lse), _ptr(ws),
                                                     int(ws_bytes), _stream(stream)))
+
+
+def usp_rotary_embed(p, r, q, k, pos, inv_freq, q_out, k_out, inverse: bool = False, stream=None) -> None:
+    """q, q_out, k, k_out: sequence-sharded [P][B][N/P][H][d], or [tokens][H][d], with any token stride (q, q_out or k,
+    k_out may be None)."""
+    (qp, qs), (kp, ks) = _token_rows(q, p.Hq, p.d), _token_rows(k, p.Hkv, p.d)
+    (qo, qos), (ko, kos) = _token_rows(q_out, p.Hq, p.d), _token_rows(k_out, p.Hkv, p.d)
+    check("usp_rotary_embed", load().usp_rotary_embed(_prob(p), _rotary(r), int(bool(inverse)), qp, qs, kp, ks, _ptr(pos),
+                                                      _ptr(inv_freq), qo, qos, ko, kos, _stream(stream)))
+
+
+def usp_kv_append_axes(c, n_tokens: int, q, k, v, seq, pos, rot_pos, inv_freq, r, q_out, k_out, k_pages, v_pages,
+                       page_table, stream=None) -> None:
+    """q, k, v: [n_tokens][H][d] with any token stride (q, q_out and k_out may be None); the rest contiguous."""
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, c.Hq, c.d), _rows(k, c.Hkv, c.d), _rows(v, c.Hkv, c.d)
+    check("usp_kv_append_axes", load().usp_kv_append_axes(_cache(c), int(n_tokens), qp, qs, kp, ks, vp, vs, _ptr(seq),
+                                                          _ptr(pos), _ptr(rot_pos), _ptr(inv_freq), _rotary(r),
+                                                          _ptr(q_out), _ptr(k_out), _ptr(k_pages), _ptr(v_pages),
+                                                          _ptr(page_table), _stream(stream)))
+
+
+def usp_pages_update_workspace_size(c) -> int:
+    return int(load().usp_pages_update_workspace_size(_cache(c)))
+
+
+def usp_pages_update(c, parent, keep, grow, seq_lens, page_table, ref, copies, ws, ws_bytes=None, stream=None) -> None:
+    """seq_lens, page_table and ref are updated in place; copies int32 [1 + n_seqs][4]."""
+    if ws_bytes is None:
+        ws_bytes = ws.numel() * ws.element_size() if isinstance(ws, torch.Tensor) else 0
+    check("usp_pages_update", load().usp_pages_update(_cache(c), _ptr(parent), _ptr(keep), _ptr(grow), _ptr(seq_lens),
+                                                      _ptr(page_table), _ptr(ref), _ptr(copies), _ptr(ws),
+                                                      int(ws_bytes), _stream(stream)))
+
+
+def usp_pages_compact(c, page_table, ref, page_table_out, ref_out, new_id, copies, stream=None) -> None:
+    """copies int32 [1 + n_pages // 2][4]; page_table_out and ref_out may be page_table and ref."""
+    check("usp_pages_compact", load().usp_pages_compact(_cache(c), _ptr(page_table), _ptr(ref), _ptr(page_table_out),
+                                                        _ptr(ref_out), _ptr(new_id), _ptr(copies), _stream(stream)))
+
+
+def usp_pages_copy(c, max_copies: int, copies, k_pages, v_pages, n_layers: int = 1, layer_stride: int = 0,
+                   stream=None) -> None:
+    check("usp_pages_copy", load().usp_pages_copy(_cache(c), int(max_copies), _ptr(copies), int(n_layers),
+                                                  int(layer_stride), _ptr(k_pages), _ptr(v_pages), _stream(stream)))
+
+
+def _prob_rows(x, vocab: int):
+    """Pointer and row stride (elements) of probabilities [rows][vocab], or of a device pointer to contiguous rows."""
+    if x is None or isinstance(x, int):
+        return x or 0, vocab
+    if not x.is_cuda and x.numel():
+        raise ValueError("libusp takes device tensors")
+    if x.dim() != 2 or x.shape[1] != vocab or (x.shape[0] and vocab > 1 and x.stride(1) != 1):
+        raise ValueError(f"expected rows of {vocab} contiguous elements, got {list(x.shape)}")
+    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else vocab
+
+
+def usp_verify_drafts(n_seqs: int, n_tokens: int, vocab: int, target, draft, tokens, u, q_start, seq_lens, n_accepted,
+                      next_tokens, keep_lens, dtype=None, stream=None) -> None:
+    """target, draft (or None): [n_tokens][vocab] with any row stride; dtype: theirs, "f32" or "bf16" (needed for device
+    pointers)."""
+    if dtype is None:
+        dtype = "bf16" if isinstance(target, torch.Tensor) and target.dtype == torch.bfloat16 else "f32"
+    for x in (target, draft):
+        if isinstance(x, torch.Tensor) and x.dtype != _TORCH_DTYPE[dtype]:
+            raise ValueError(f"expected {_TORCH_DTYPE[dtype]}, got {x.dtype}")
+    (tp, ts), (dp, ds) = _prob_rows(target, vocab), _prob_rows(draft, vocab)
+    check("usp_verify_drafts", load().usp_verify_drafts(int(n_seqs), int(n_tokens), int(vocab),
+                                                        USP_F32 if dtype == "f32" else USP_BF16, tp, ts, dp, ds,
+                                                        _ptr(tokens), _ptr(u), _ptr(q_start), _ptr(seq_lens),
+                                                        _ptr(n_accepted), _ptr(next_tokens), _ptr(keep_lens),
+                                                        _stream(stream)))
 
 
 def usp_diag_wait_timeout(stream=None) -> None:
@@ -759,3 +893,129 @@ def prefix_attention(c: Cache, q, k_pages, v_pages, page_table, seq_lens, prefix
                     ws, None, stream)
     _share(stream, (q, k_pages, v_pages, page_table, seq_lens, q_start, prefix_pages), (o, lse))
     return o, lse
+
+
+def rotary_embed(p: Problem, r: Rotary, q_seq, k_seq, pos, inv_freq, inverse=False, stream=None):
+    """Rotate sequence-sharded queries and keys (or None) by their positions on several axes (usp_rotary_embed), in front
+    of any of the attention helpers; with `inverse`, the backward: gradients of the rotated ones in, of q and k out.
+
+    q_seq [P][B][N/P][Hq][d], k_seq likewise, any token stride; pos int32 [axes][P][B][N/P]; inv_freq float32 [rot/2].
+    Returns new (q, k)."""
+    some = q_seq if q_seq is not None else k_seq
+    dev, dt = _serving_device(some), p.torch_dtype
+    _check(p, "q", q_seq, p.seq_shape(p.Hq), dt, dev, optional=True)
+    _check(p, "k", k_seq, p.seq_shape(p.Hkv), dt, dev, optional=True)
+    _check(p, "pos", pos, (r.axes, p.P, p.B, p.N // p.P), torch.int32, dev)
+    _check(p, "inv_freq", inv_freq, (r.rot // 2,), torch.float32, dev)
+    with _made_on(stream):
+        q_out = None if q_seq is None else _empty(p.seq_shape(p.Hq), dt, dev)
+        k_out = None if k_seq is None else _empty(p.seq_shape(p.Hkv), dt, dev)
+    usp_rotary_embed(p, r, q_seq, k_seq, pos, inv_freq, q_out, k_out, inverse, stream)
+    _share(stream, (q_seq, k_seq, pos, inv_freq), (q_out, k_out))
+    return q_out, k_out
+
+
+def kv_append_axes(c: Cache, r: Rotary, q, k, v, seq, pos, rot_pos, inv_freq, k_pages, v_pages, page_table, stream=None):
+    """kv_append with several axes (usp_kv_append_axes): pos int32 [T] are the tokens' slots, rot_pos int32 [axes][T] their
+    positions.  Returns (rotated q or None, rotated k)."""
+    dev, dt = _serving_device(k), c.torch_dtype
+    T = k.shape[0]
+    _check(c, "q", q, (T, c.Hq, c.d), dt, dev, optional=True)
+    _check(c, "k", k, (T, c.Hkv, c.d), dt, dev)
+    _check(c, "v", v, (T, c.Hkv, c.d), dt, dev)
+    _check(c, "seq", seq, (T,), torch.int32, dev)
+    _check(c, "pos", pos, (T,), torch.int32, dev)
+    _check(c, "rot_pos", rot_pos, (r.axes, T), torch.int32, dev)
+    _check(c, "inv_freq", inv_freq, (r.rot // 2,), torch.float32, dev)
+    _check(c, "k_pages", k_pages, c.pool_shape(), dt, dev)
+    _check(c, "v_pages", v_pages, c.pool_shape(), dt, dev)
+    _check(c, "page_table", page_table, c.table_shape(), torch.int32, dev)
+    with _made_on(stream):
+        q_out = None if q is None else _empty((T, c.Hq, c.d), dt, dev)
+        k_out = _empty((T, c.Hkv, c.d), dt, dev)
+    usp_kv_append_axes(c, T, q, k, v, seq, pos, rot_pos, inv_freq, r, q_out, k_out, k_pages, v_pages, page_table, stream)
+    _share(stream, (q, k, v, seq, pos, rot_pos, inv_freq, k_pages, v_pages, page_table), (q_out, k_out))
+    return q_out, k_out
+
+
+def pages_empty(c: Cache, device="cuda"):
+    """The state of a cache that holds nothing: (seq_lens, page_table, ref), as usp_pages_update keeps it."""
+    i32 = dict(dtype=torch.int32, device=device)
+    return torch.zeros(c.n_seqs, **i32), torch.full(c.table_shape(), -1, **i32), torch.zeros(c.n_pages, **i32)
+
+
+def _check_state(c: Cache, page_table, ref):
+    dev = _serving_device(ref)
+    _check(c, "page_table", page_table, c.table_shape(), torch.int32, dev)
+    _check(c, "ref", ref, (c.n_pages,), torch.int32, dev)
+    return dev
+
+
+def pages_update(c: Cache, seq_lens, page_table, ref, parent=None, keep=None, grow=None, stream=None):
+    """Fork, truncate, free and grow sequences (usp_pages_update), in place: slot s goes on with the first keep[s] tokens of
+    slot parent[s] and gets room for grow[s] more.  int32 [n_seqs] each, or None: itself, all, none.  Returns the list of
+    copies that pages_copy is to make; its row 0 is {copies, pages lacking (then nothing was changed), free pages, 0}."""
+    dev = _check_state(c, page_table, ref)
+    for name, x in (("seq_lens", seq_lens), ("parent", parent), ("keep", keep), ("grow", grow)):
+        _check(c, name, x, (c.n_seqs,), torch.int32, dev, optional=name != "seq_lens")
+    size = usp_pages_update_workspace_size(c)
+    with _made_on(stream):
+        copies = _empty((1 + c.n_seqs, 4), torch.int32, dev)
+        ws = _empty((max(size, 256),), torch.uint8, dev)
+    usp_pages_update(c, parent, keep, grow, seq_lens, page_table, ref, copies, ws, None, stream)
+    _share(stream, (seq_lens, page_table, ref, parent, keep, grow), (copies,))
+    return copies
+
+
+def pages_compact(c: Cache, page_table, ref, stream=None):
+    """Bring the pages in use to the front of the pool (usp_pages_compact); page_table and ref are updated in place.  Returns
+    (copies, new_id): the list that pages_copy is to make, and each page's number afterwards."""
+    dev = _check_state(c, page_table, ref)
+    with _made_on(stream):
+        copies = _empty((1 + c.n_pages // 2, 4), torch.int32, dev)
+        new_id = _empty((c.n_pages,), torch.int32, dev)
+    usp_pages_compact(c, page_table, ref, page_table, ref, new_id, copies, stream)
+    _share(stream, (page_table, ref), (copies, new_id))
+    return copies, new_id
+
+
+def pages_copy(c: Cache, copies, k_pages, v_pages, stream=None) -> None:
+    """Make the copies of a list of pages_update or pages_compact (usp_pages_copy), in one layer's pools or, given as
+    [layers][n_pages][Hkv][page_size][d], in those of all layers."""
+    dev, dt = _serving_device(k_pages), c.torch_dtype
+    shape = c.pool_shape() if k_pages.dim() == 4 else (k_pages.shape[0], *c.pool_shape())
+    _check(c, "k_pages", k_pages, shape, dt, dev)
+    _check(c, "v_pages", v_pages, shape, dt, dev)
+    _check(c, "copies", copies, (None, 4), torch.int32, dev)
+    layers = 1 if len(shape) == 4 else shape[0]
+    usp_pages_copy(c, copies.shape[0] - 1, copies, k_pages, v_pages, layers, math.prod(c.pool_shape()), stream)
+    _share(stream, (copies, k_pages, v_pages), ())
+
+
+def verify_drafts(target, draft, tokens, u, q_start, seq_lens=None, stream=None):
+    """Accept or refuse drafted tokens and draw the next one (usp_verify_drafts).
+
+    target [T][vocab] probabilities (float32 or bf16, any row stride): row t is for the token after tokens[t]; draft likewise:
+    row t is what tokens[t] was drawn from, or None; tokens int32 [T], u float32 [T] in [0, 1); q_start int32 [n_seqs + 1].
+    Returns (n_accepted, next token, keep_lens), int32 [n_seqs] each; keep_lens: the cached tokens that stay, None without
+    seq_lens."""
+    dev = _serving_device(target)
+    if target.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"target: expected float32 or bfloat16, got {target.dtype}")
+    _check(None, "target", target, (None, None), target.dtype, dev)
+    T, vocab = target.shape
+    _check(None, "draft", draft, (T, vocab), target.dtype, dev, optional=True)
+    _check(None, "tokens", tokens, (T,), torch.int32, dev)
+    _check(None, "u", u, (T,), torch.float32, dev)
+    _check(None, "q_start", q_start, (None,), torch.int32, dev)
+    n = q_start.numel() - 1
+    if n < 0:
+        raise ValueError("q_start: expected [n_seqs + 1]")
+    _check(None, "seq_lens", seq_lens, (n,), torch.int32, dev, optional=True)
+    with _made_on(stream):
+        n_accepted, nxt = _empty((n,), torch.int32, dev), _empty((n,), torch.int32, dev)
+        keep_lens = None if seq_lens is None else _empty((n,), torch.int32, dev)
+    usp_verify_drafts(n, T, vocab, target, draft, tokens, u, q_start, seq_lens, n_accepted, nxt, keep_lens,
+                      "bf16" if target.dtype == torch.bfloat16 else "f32", stream)
+    _share(stream, (target, draft, tokens, u, q_start, seq_lens), (n_accepted, nxt, keep_lens))
+    return n_accepted, nxt, keep_lens

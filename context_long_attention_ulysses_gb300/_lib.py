@@ -37,6 +37,8 @@ SYMBOLS = (
     "usp_hybrid_attn_bwd", "usp_diag_wait_timeout", "usp_diag_raise_status",
     "usp_attn_bwd_deterministic_workspace_size", "usp_attn_bwd_deterministic", "usp_kv_append",
     "usp_paged_attn_workspace_size", "usp_paged_attn", "usp_prefix_attn_workspace_size", "usp_prefix_attn",
+    "usp_rotary_embed", "usp_kv_append_axes", "usp_pages_update_workspace_size", "usp_pages_update", "usp_pages_compact",
+    "usp_pages_copy", "usp_verify_drafts",
 )
 
 
@@ -52,6 +54,15 @@ class UspCache(ctypes.Structure):
     _fields_ = [("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("n_seqs", ctypes.c_int),
                 ("max_pages", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
                 ("causal", ctypes.c_int), ("scale", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
+USP_MAX_AXES = 4
+
+
+class UspRotary(ctypes.Structure):
+    """Mirror of ``usp_rotary``."""
+    _fields_ = [("n_axes", ctypes.c_int), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("axis", ctypes.c_uint8 * 64)]
 
 
 class UspTraceEntry(ctypes.Structure):
@@ -83,7 +94,7 @@ def load() -> ctypes.CDLL:
                 f"libusp.so not found at {LIB}; build it first "
                 "(python -m context_long_attention_ulysses_gb300.build)")
         lib = ctypes.CDLL(LIB)
-        P, C = ctypes.POINTER(UspProblem), ctypes.POINTER(UspCache)
+        P, C, R = ctypes.POINTER(UspProblem), ctypes.POINTER(UspCache), ctypes.POINTER(UspRotary)
         vp, i64, sz, ci = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
         sig = {
             "usp_a2a_seq2head": (ci, [P, ci, vp, vp, vp]),
@@ -131,6 +142,13 @@ def load() -> ctypes.CDLL:
             "usp_paged_attn": (ci, [C, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
             "usp_prefix_attn_workspace_size": (sz, [C, ci, ci, ci]),
             "usp_prefix_attn": (ci, [C, ci, ci, vp, vp, vp, vp, vp, vp, vp, ci, vp, vp, vp, sz, vp]),
+            "usp_rotary_embed": (ci, [P, R, ci, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp]),
+            "usp_kv_append_axes": (ci, [C, ci, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, R, vp, vp, vp, vp, vp, vp]),
+            "usp_pages_update_workspace_size": (sz, [C]),
+            "usp_pages_update": (ci, [C, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "usp_pages_compact": (ci, [C, vp, vp, vp, vp, vp, vp, vp]),
+            "usp_pages_copy": (ci, [C, ci, vp, ci, i64, vp, vp, vp]),
+            "usp_verify_drafts": (ci, [ci, ci, ci, ci, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)

@@ -16,8 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libusp.so")
 SOURCES = ["api.cu", "remap.cu", "attn_f32.cu", "attn_fwd.cu", "attn_bwd.cu", "ring.cu", "noalloc.cu", "diag.cu",
-           "kv_append.cu", "paged_attn.cu", "paged_mma.cu", "paged_tc.cu", "paged_f32.cu"]
-HEADERS = ["kernels.h", "ptx.cuh", "paged.cuh"]
+           "kv_append.cu", "rotary.cu", "pages.cu", "verify.cu", "paged_attn.cu", "paged_mma.cu", "paged_tc.cu", "paged_f32.cu"]
+HEADERS = ["kernels.h", "ptx.cuh", "paged.cuh", "rotary.cuh", "cluster.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-diag-suppress", "177"]

@@ -1246,10 +1246,11 @@ static bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<u
 // A row stride of n contiguous elements that 16-byte accesses can use.
 static bool stride_ok(int64_t stride, int64_t n, int elem) { return stride >= n && stride * elem % 16 == 0; }
 
-usp_status usp_kv_append(const usp_cache* c, int n_tokens, const void* q, int64_t q_stride, const void* k,
-                         int64_t k_stride, const void* v, int64_t v_stride, const int32_t* seq, const int32_t* pos,
-                         const int32_t* rot_pos, const float* inv_freq, int rot, int interleaved, void* q_out,
-                         void* k_out, void* k_pages, void* v_pages, const int32_t* page_table, usp_stream stream) {
+static usp_status kv_append(const usp_cache* c, int n_tokens, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride, const int32_t* seq, const int32_t* pos,
+                            const int32_t* rot_pos, const float* inv_freq, int rot, int interleaved, const PairAxes& axes,
+                            void* q_out, void* k_out, void* k_pages, void* v_pages, const int32_t* page_table,
+                            usp_stream stream) {
     usp_status st = check_cache(c);
     if (st != USP_OK) return st;
     if (n_tokens < 0 || rot < 0 || rot > c->d || rot % 16 != 0 || (q == nullptr) != (q_out == nullptr))
@@ -1280,8 +1281,17 @@ usp_status usp_kv_append(const usp_cache* c, int n_tokens, const void* q, int64_
     p.n_tokens = n_tokens; p.n_seqs = c->n_seqs; p.max_pages = c->max_pages; p.n_pages = c->n_pages;
     p.page_log2 = page_log2(c);
     p.Hq = c->Hq; p.Hkv = c->Hkv; p.d = c->d; p.rot = rot; p.interleaved = interleaved != 0; p.elem = elem;
+    p.axes = axes;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return cuda_status(traced("kv_append", s, [&] { return launch_kv_append(p, s); }));
+}
+
+usp_status usp_kv_append(const usp_cache* c, int n_tokens, const void* q, int64_t q_stride, const void* k,
+                         int64_t k_stride, const void* v, int64_t v_stride, const int32_t* seq, const int32_t* pos,
+                         const int32_t* rot_pos, const float* inv_freq, int rot, int interleaved, void* q_out,
+                         void* k_out, void* k_pages, void* v_pages, const int32_t* page_table, usp_stream stream) {
+    return kv_append(c, n_tokens, q, q_stride, k, k_stride, v, v_stride, seq, pos, rot_pos, inv_freq, rot, interleaved,
+                     PairAxes{}, q_out, k_out, k_pages, v_pages, page_table, stream);
 }
 
 // Shapes of a paged attention call; the pointers are filled in by the caller.
@@ -1368,6 +1378,151 @@ usp_status usp_prefix_attn(const usp_cache* c, int n_tokens, int max_q, const vo
                            void* ws, size_t ws_bytes, usp_stream stream) {
     return paged_attn(c, n_tokens, max_q, q, k_pages, v_pages, page_table, seq_lens, q_start, prefix_pages, prefix_len,
                       o, lse, ws, ws_bytes, stream);
+}
+
+// ---------------------------------------------------------------- rotary positions with several axes
+// The axes of the pairs, packed; false if r is no rotation of heads of d values.
+static bool pack_axes(const usp_rotary* r, int d, PairAxes* out) {
+    if (!r || r->n_axes < 1 || r->n_axes > USP_MAX_AXES || r->rot < 0 || r->rot > d || r->rot > 128 || r->rot % 16 != 0) return false;
+    *out = PairAxes{};
+    for (int i = 0; i < r->rot / 2; ++i) {
+        if (r->axis[i] >= r->n_axes) return false;
+        out->w[i / 16] |= (uint32_t)r->axis[i] << (2 * (i % 16));
+    }
+    return true;
+}
+
+usp_status usp_rotary_embed(const usp_problem* p, const usp_rotary* r, int inverse, const void* q, int64_t q_stride,
+                            const void* k, int64_t k_stride, const int32_t* pos, const float* inv_freq, void* q_out,
+                            int64_t q_out_stride, void* k_out, int64_t k_out_stride, usp_stream stream) {
+    usp_status st = check_problem(p, false);
+    if (st != USP_OK) return st;
+    RotaryParams a{};
+    if (!pack_axes(r, p->d, &a.axes) || (q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr))
+        return USP_ERR_INVALID_ARG;
+    if (p->d != 64 && p->d != 128) return USP_ERR_UNSUPPORTED;
+    const int64_t T = (int64_t)p->B * p->N;
+    if (T > INT32_MAX - 15) return USP_ERR_UNSUPPORTED;  // tokens, rounded up to a CTA's sixteen, are an int
+    const int elem = elem_size(p->dtype);
+    const int64_t qn = (int64_t)p->Hq * p->d, kn = (int64_t)p->Hkv * p->d;
+    if (T > 0 && ((q && (!stride_ok(q_stride, qn, elem) || !stride_ok(q_out_stride, qn, elem))) ||
+                  (k && (!stride_ok(k_stride, kn, elem) || !stride_ok(k_out_stride, kn, elem)))))
+        return USP_ERR_INVALID_ARG;
+    // (in place, rows that move would overwrite others that are still to be read)
+    if (T > 1 && ((q && q == q_out && q_stride != q_out_stride) || (k && k == k_out && k_stride != k_out_stride)))
+        return USP_ERR_INVALID_ARG;
+    if (T == 0 || (!q && !k)) return USP_OK;
+    if ((q && (!aligned16(q) || !aligned16(q_out))) || (k && (!aligned16(k) || !aligned16(k_out)))) return USP_ERR_MISALIGNED;
+    if (r->rot > 0 && (!aligned4(pos) || !aligned4(inv_freq))) return USP_ERR_MISALIGNED;
+    a.q = q; a.k = k; a.q_out = q_out; a.k_out = k_out;
+    a.q_stride = q_stride; a.k_stride = k_stride; a.q_out_stride = q_out_stride; a.k_out_stride = k_out_stride;
+    a.pos = pos; a.inv_freq = inv_freq;
+    a.n_tokens = (int)T; a.Hq = p->Hq; a.Hkv = p->Hkv; a.d = p->d; a.rot = r->rot;
+    a.interleaved = r->interleaved != 0; a.inverse = inverse != 0; a.elem = elem;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(traced("rotary_embed", s, [&] { return launch_rotary(a, s); }));
+}
+
+usp_status usp_kv_append_axes(const usp_cache* c, int n_tokens, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, const int32_t* seq, const int32_t* pos,
+                              const int32_t* rot_pos, const float* inv_freq, const usp_rotary* r, void* q_out, void* k_out,
+                              void* k_pages, void* v_pages, const int32_t* page_table, usp_stream stream) {
+    usp_status st = check_cache(c);
+    if (st != USP_OK) return st;
+    PairAxes axes;
+    if (!pack_axes(r, c->d, &axes)) return USP_ERR_INVALID_ARG;
+    if (r->rot > 0 && !rot_pos && n_tokens > 0) return USP_ERR_MISALIGNED;
+    return kv_append(c, n_tokens, q, q_stride, k, k_stride, v, v_stride, seq, pos, rot_pos, inv_freq, r->rot, r->interleaved,
+                     axes, q_out, k_out, k_pages, v_pages, page_table, stream);
+}
+
+// ---------------------------------------------------------------- pages of the cache
+static usp_status check_pages(const usp_cache* c) {
+    usp_status st = check_cache(c);
+    if (st == USP_OK && c->n_pages > 1 << 30) return USP_ERR_UNSUPPORTED;  // (loops over pages count in ints)
+    return st;
+}
+
+size_t usp_pages_update_workspace_size(const usp_cache* c) {
+    if (check_pages(c) != USP_OK) return 0;
+    return pages_update_workspace(c->n_seqs, c->max_pages, c->n_pages);
+}
+
+usp_status usp_pages_update(const usp_cache* c, const int32_t* parent, const int32_t* keep, const int32_t* grow,
+                            int32_t* seq_lens, int32_t* page_table, int32_t* ref, int32_t* copies, void* ws, size_t ws_bytes,
+                            usp_stream stream) {
+    usp_status st = check_pages(c);
+    if (st != USP_OK) return st;
+    if (!aligned16(copies)) return USP_ERR_MISALIGNED;
+    if ((parent && !aligned4(parent)) || (keep && !aligned4(keep)) || (grow && !aligned4(grow))) return USP_ERR_MISALIGNED;
+    if (c->n_seqs > 0 && (!aligned4(seq_lens) || (c->max_pages > 0 && !aligned4(page_table)))) return USP_ERR_MISALIGNED;
+    if (c->n_pages > 0 && !aligned4(ref)) return USP_ERR_MISALIGNED;
+    const size_t need = pages_update_workspace(c->n_seqs, c->max_pages, c->n_pages);
+    if (need > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u))) return USP_ERR_MISALIGNED;
+    if (ws_bytes < need) return USP_ERR_WORKSPACE;
+    PagesUpdateParams p{};
+    p.parent = parent; p.keep = keep; p.grow = grow;
+    p.seq_lens = seq_lens; p.page_table = page_table; p.ref = ref; p.copies = copies; p.ws = ws;
+    p.n_seqs = c->n_seqs; p.max_pages = c->max_pages; p.n_pages = c->n_pages; p.page_log2 = page_log2(c);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(traced("pages_update", s, [&] { return launch_pages_update(p, s); }));
+}
+
+usp_status usp_pages_compact(const usp_cache* c, const int32_t* page_table, const int32_t* ref, int32_t* page_table_out,
+                             int32_t* ref_out, int32_t* new_id, int32_t* copies, usp_stream stream) {
+    usp_status st = check_pages(c);
+    if (st != USP_OK) return st;
+    if (!aligned16(copies)) return USP_ERR_MISALIGNED;
+    if (c->n_pages > 0 && (!aligned4(ref) || !aligned4(ref_out) || !aligned4(new_id))) return USP_ERR_MISALIGNED;
+    if (c->n_seqs > 0 && c->max_pages > 0 && (!aligned4(page_table) || !aligned4(page_table_out))) return USP_ERR_MISALIGNED;
+    PagesCompactParams p{};
+    p.page_table = page_table; p.ref = ref; p.page_table_out = page_table_out; p.ref_out = ref_out;
+    p.new_id = new_id; p.copies = copies;
+    p.n_seqs = c->n_seqs; p.max_pages = c->max_pages; p.n_pages = c->n_pages; p.page_log2 = page_log2(c);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(traced("pages_compact", s, [&] { return launch_pages_compact(p, s); }));
+}
+
+usp_status usp_pages_copy(const usp_cache* c, int max_copies, const int32_t* copies, int n_layers, int64_t layer_stride,
+                          void* k_pages, void* v_pages, usp_stream stream) {
+    usp_status st = check_cache(c);
+    if (st != USP_OK) return st;
+    const int elem = elem_size(c->dtype);
+    const int64_t pool = (int64_t)c->n_pages * c->Hkv * c->page_size * c->d;
+    if (max_copies < 0 || n_layers < 0) return USP_ERR_INVALID_ARG;
+    if (n_layers > 1 && (layer_stride < pool || layer_stride * elem % 16 != 0)) return USP_ERR_INVALID_ARG;
+    if (max_copies == 0 || n_layers == 0 || c->n_pages == 0) return USP_OK;
+    if (!aligned16(copies) || !aligned16(k_pages) || !aligned16(v_pages)) return USP_ERR_MISALIGNED;
+    PagesCopyParams p{};
+    p.copies = copies; p.k_pages = k_pages; p.v_pages = v_pages; p.layer_bytes = layer_stride * elem;
+    p.max_copies = max_copies; p.n_layers = n_layers; p.n_pages = c->n_pages; p.page_log2 = page_log2(c);
+    p.Hkv = c->Hkv; p.row_bytes = c->d * elem;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(traced("pages_copy", s, [&] { return launch_pages_copy(p, s); }));
+}
+
+// ---------------------------------------------------------------- verification of drafted tokens
+usp_status usp_verify_drafts(int n_seqs, int n_tokens, int vocab, int dtype, const void* target, int64_t target_stride,
+                             const void* draft, int64_t draft_stride, const int32_t* tokens, const float* u,
+                             const int32_t* q_start, const int32_t* seq_lens, int32_t* n_accepted, int32_t* next,
+                             int32_t* keep_lens, usp_stream stream) {
+    const int elem = elem_size(dtype);
+    if (n_seqs < 0 || n_tokens < 0 || vocab < 1 || elem == 0 || (seq_lens == nullptr) != (keep_lens == nullptr))
+        return USP_ERR_INVALID_ARG;
+    if (n_tokens > 0 && (target_stride < vocab || (draft && draft_stride < vocab))) return USP_ERR_INVALID_ARG;
+    if (vocab > 1 << 19 || n_seqs > INT32_MAX / 8) return USP_ERR_UNSUPPORTED;  // sums of whole numbers; CTAs of the grid
+    if (n_seqs == 0) return USP_OK;
+    if (!aligned4(q_start) || !aligned4(n_accepted) || !aligned4(next) || (seq_lens && (!aligned4(seq_lens) || !aligned4(keep_lens))))
+        return USP_ERR_MISALIGNED;
+    if (n_tokens > 0 && (!aligned16(target) || (draft && !aligned16(draft)) || !aligned4(tokens) || !aligned4(u)))
+        return USP_ERR_MISALIGNED;
+    VerifyParams p{};
+    p.target = target; p.draft = draft; p.target_stride = target_stride; p.draft_stride = draft_stride;
+    p.tokens = tokens; p.u = u; p.q_start = q_start; p.seq_lens = seq_lens;
+    p.n_accepted = n_accepted; p.next = next; p.keep_lens = keep_lens;
+    p.n_seqs = n_seqs; p.n_tokens = n_tokens; p.vocab = vocab; p.elem = elem;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(traced("verify_drafts", s, [&] { return launch_verify(p, s); }));
 }
 
 usp_status usp_trace_enable(int on) {

@@ -139,17 +139,34 @@ cudaError_t launch_raise_status(int* status, cudaStream_t stream);
 usp_status attn_bwd_check(const usp_problem* p, const void* q, const void* k, const void* v, const void* o,
                           const float* lse, const void* dout, const void* dq, const void* dk, const void* dv);
 
+// ---- rotary positions (rotary.cuh): the axis of pair i in bits 2 (i % 16) .. of word i / 16
+struct PairAxes {
+    uint32_t w[4];
+};
+// Rotation of q and k (rotary.cu); x_stride: elements between tokens
+struct RotaryParams {
+    const void *q, *k;  // either may be null
+    void *q_out, *k_out;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+    const int32_t* pos;  // [axes][n_tokens]
+    const float* inv_freq;
+    PairAxes axes;
+    int n_tokens, Hq, Hkv, d, rot, interleaved, inverse, elem;
+};
+cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t stream);
+
 // ---- paged key/value cache (kv_append.cu)
 struct AppendParams {
     const void *q, *k, *v;                 // q null: no queries
     int64_t q_stride, k_stride, v_stride;  // elements between tokens
-    const int32_t *seq, *pos, *rot_pos;    // rot_pos null: pos
+    const int32_t *seq, *pos, *rot_pos;    // rot_pos [axes][n_tokens], null: pos
     const float* inv_freq;
     void *q_out, *k_out;                   // k_out may be null
     void *k_pages, *v_pages;
     const int32_t* page_table;
     int n_tokens, n_seqs, max_pages, n_pages, page_log2;
     int Hq, Hkv, d, rot, interleaved, elem;
+    PairAxes axes;  // all 0: one axis
 };
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
 
@@ -184,6 +201,40 @@ cudaError_t launch_paged_mma(const PagedArgs& a, bool prefix, cudaStream_t strea
 cudaError_t launch_paged_tc(const PagedArgs& a, bool prefix, cudaStream_t stream);   // paged_tc.cu: 128 or 256 rows
 cudaError_t launch_paged_f32(const PagedArgs& a, bool prefix, cudaStream_t stream);  // paged_f32.cu: float32
 cudaError_t launch_paged_merge(const PagedArgs& a, cudaStream_t stream);
+
+// ---- pages of the cache (pages.cu)
+struct PagesUpdateParams {
+    const int32_t *parent, *keep, *grow;  // each may be null
+    int32_t *seq_lens, *page_table, *ref, *copies;
+    void* ws;
+    int n_seqs, max_pages, n_pages, page_log2;
+};
+size_t pages_update_workspace(int n_seqs, int max_pages, int n_pages);
+cudaError_t launch_pages_update(const PagesUpdateParams& p, cudaStream_t stream);
+struct PagesCompactParams {
+    const int32_t *page_table, *ref;
+    int32_t *page_table_out, *ref_out, *new_id, *copies;
+    int n_seqs, max_pages, n_pages, page_log2;
+};
+cudaError_t launch_pages_compact(const PagesCompactParams& p, cudaStream_t stream);
+struct PagesCopyParams {
+    const int32_t* copies;
+    void *k_pages, *v_pages;
+    int64_t layer_bytes;       // between the pools of two layers
+    int max_copies, n_layers, n_pages, page_log2, Hkv, row_bytes;
+};
+cudaError_t launch_pages_copy(const PagesCopyParams& p, cudaStream_t stream);
+
+// ---- verification of drafted tokens (verify.cu)
+struct VerifyParams {
+    const void *target, *draft;  // draft null: drafts without probabilities
+    int64_t target_stride, draft_stride;
+    const int32_t *tokens, *q_start, *seq_lens;  // seq_lens null with keep_lens
+    const float* u;
+    int32_t *n_accepted, *next, *keep_lens;
+    int n_seqs, n_tokens, vocab, elem;
+};
+cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream);
 
 // ---- tensor maps (api.cu)
 // 4-D bf16 tensor map over Tensor4 with box {64, 1, 128, 1} and 128-byte swizzle.

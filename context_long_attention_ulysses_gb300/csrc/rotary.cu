@@ -1,0 +1,115 @@
+// Rotary position embedding with several axes, of the queries and keys of a sequence-sharded batch, and its backward.
+//
+// Per token, head and i < rot/2 the pair (a, b) of frequency f_i turns by the angle r f_i, r being the token's position on
+// the pair's axis (time, height, width ...):
+//   a' = a cos(r f_i) - b sin(r f_i),  b' = b cos(r f_i) + a sin(r f_i).
+// The backward is the transposed rotation, by -r f_i.  Angles as in kv_append.cu (rotary.cuh).
+//
+// Bound by HBM: every value is read once and written once.  Work is cut as in kv_append.cu: items of two 16-byte vectors, a CTA
+// takes as many tokens as make about kItems of them, and the loads are under way while the tokens' cosines and sines (one per
+// pair, shared by all heads) are formed.
+#include <algorithm>
+
+#include "paged.cuh"
+#include "rotary.cuh"
+
+namespace usp {
+
+namespace {
+
+constexpr int kThreads = 96;
+constexpr int kAhead = 4;                  // items of a thread in flight
+constexpr int kItems = kThreads * kAhead;  // items of a CTA per round
+constexpr int kMaxTokens = 16;
+
+template <typename T, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p, int tokens_per_cta, int item_log2) {
+    constexpr int V = Vec<T>::N;
+    __shared__ float2 cs[kMaxTokens][64];
+    const int64_t t0 = (int64_t)blockIdx.x * tokens_per_cta;
+    const int n_tok = (int)min((int64_t)tokens_per_cta, p.n_tokens - t0);
+    const int d = p.d, half = p.rot / 2;
+    const int hq = p.q ? p.Hq : 0, heads = hq + (p.k ? p.Hkv : 0), per_token = heads << item_log2;
+    const int total = n_tok * per_token;
+
+    struct Item {
+        int tok, head, e0, e1;
+        bool rotates;
+    };
+    auto item = [&](int x) {
+        Item it;
+        it.tok = x / per_token;
+        const int y = x - it.tok * per_token;
+        it.head = y >> item_log2;
+        const int i = (y & ((1 << item_log2) - 1)) * V;  // values of the first vectors before this one
+        it.rotates = i < half;
+        if (INTERLEAVED || !it.rotates) {
+            it.e0 = 2 * i;
+            it.e1 = 2 * i + V;
+        } else {
+            it.e0 = i;
+            it.e1 = i + half;
+        }
+        return it;
+    };
+    uint4 w[kAhead][2];
+    auto fetch = [&](int x0) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int x = x0 + u * kThreads;
+            if (x < total) {
+                const Item it = item(x);
+                const int64_t t = t0 + it.tok;
+                const T* src = it.head < hq ? static_cast<const T*>(p.q) + t * p.q_stride + it.head * d
+                                            : static_cast<const T*>(p.k) + t * p.k_stride + (it.head - hq) * d;
+                w[u][0] = __ldcs(reinterpret_cast<const uint4*>(src + it.e0));
+                w[u][1] = __ldcs(reinterpret_cast<const uint4*>(src + it.e1));
+            }
+        }
+    };
+    begin_kernel(false);
+    fetch(threadIdx.x);
+    for (int x = threadIdx.x; x < n_tok * half; x += kThreads) {
+        const int tok = x / half, i = x - tok * half;
+        cs[tok][i] = turn(p.pos[pair_axis(p.axes, i) * (int64_t)p.n_tokens + t0 + tok], p.inv_freq[i]);
+    }
+    __syncthreads();
+    const float sign = p.inverse ? -1.f : 1.f;
+    for (int x0 = threadIdx.x; x0 < total; x0 += kItems) {
+        if (x0 != threadIdx.x) fetch(x0);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int x = x0 + u * kThreads;
+            if (x >= total) break;
+            const Item it = item(x);
+            if (it.rotates)
+                rotate_vectors<T, INTERLEAVED>(w[u][0], w[u][1], cs[it.tok] + (INTERLEAVED ? it.e0 / 2 : it.e0), sign);
+            const int64_t t = t0 + it.tok;
+            T* dst = it.head < hq ? static_cast<T*>(p.q_out) + t * p.q_out_stride + it.head * d
+                                  : static_cast<T*>(p.k_out) + t * p.k_out_stride + (it.head - hq) * d;
+            __stcs(reinterpret_cast<uint4*>(dst + it.e0), w[u][0]);
+            __stcs(reinterpret_cast<uint4*>(dst + it.e1), w[u][1]);
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_t(const RotaryParams& p, cudaStream_t s) {
+    int item_log2 = 0;  // items per head
+    while ((2 * Vec<T>::N << item_log2) < p.d) ++item_log2;
+    const int per_token = ((p.q ? p.Hq : 0) + (p.k ? p.Hkv : 0)) << item_log2;
+    // few heads: several tokens per CTA, as long as there are CTAs enough for every SM
+    int n = std::min(kMaxTokens, std::max(1, kItems / per_token));
+    while (n > 1 && (p.n_tokens + n - 1) / n < 4 * 152) --n;
+    const unsigned grid = (unsigned)((p.n_tokens + n - 1) / n);
+    return p.interleaved ? launch_dependent(rotary_kernel<T, true>, dim3(grid), kThreads, 0, s, p, n, item_log2)
+                         : launch_dependent(rotary_kernel<T, false>, dim3(grid), kThreads, 0, s, p, n, item_log2);
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t stream) {
+    return p.elem == 4 ? launch_t<float>(p, stream) : launch_t<__nv_bfloat16>(p, stream);
+}
+
+}  // namespace usp

@@ -525,6 +525,147 @@ usp_status usp_prefix_attn(const usp_cache* c, int n_tokens, int max_q, const vo
                            const int32_t* q_start, const int32_t* prefix_pages, int prefix_len, void* o, float* lse,
                            void* ws, size_t ws_bytes, usp_stream stream);
 
+/* ---- rotary positions with several axes: tokens of an image or a video have a
+ * position on each axis (time, height, width), and each pair of a head's
+ * elements turns by the position on the pair's own axis. */
+#define USP_MAX_AXES 4
+typedef struct {
+    int n_axes;       /* 1 .. USP_MAX_AXES */
+    int rot;          /* rotated elements of a head: a multiple of 16, 0 <= rot <= d */
+    int interleaved;  /* pairs are elements (2i, 2i+1), otherwise (i, i + rot/2) */
+    uint8_t axis[64]; /* axis of pair i < rot/2, below n_axes (sections one after the other, in turn, any order) */
+} usp_rotary;
+
+/* Rotation of the queries and keys of a sequence-sharded batch, in front of any
+ * of the attention paths above: token t of the T = B*N of the layout
+ * [P][B][N/P], per head and pair i < rot/2 with elements (a, b),
+ *   w = pos[axis[i]][t] f_i ;  a' = a cos w - b sin w ;  b' = b cos w + a sin w
+ * inverse != 0 turns by -w: the transposed rotation, which is the backward
+ * (gradients of the rotated q and k in, those of q and k out).  Angles,
+ * frequencies (inv_freq, float32 [rot/2]) and rounding as usp_kv_append;
+ * elements rot.. pass unchanged.
+ * pos: int32 [n_axes][P][B][N/P].  q, q_out: rows of Hq*d contiguous elements,
+ * one per token, q_stride and q_out_stride elements apart; k, k_out likewise
+ * of Hkv*d (slices of one projection's output, and of its gradient, are
+ * fine); 16-byte aligned, strides at least the row and a multiple of 16
+ * bytes.  q with q_out, or k with k_out, may be NULL.  In place (q_out is q,
+ * the strides are equal) is fine, no other overlap.  dtype F32 or BF16, d in
+ * {64, 128}; B*N <= 2^31 - 16; p->causal, scale and the head split play no part. */
+usp_status usp_rotary_embed(const usp_problem* p, const usp_rotary* r, int inverse, const void* q, int64_t q_stride,
+                            const void* k, int64_t k_stride, const int32_t* pos, const float* inv_freq, void* q_out,
+                            int64_t q_out_stride, void* k_out, int64_t k_out_stride, usp_stream stream);
+
+/* usp_kv_append with several axes: the pairs of token t turn by
+ * rot_pos[axis[i]][t] f_i (rot_pos: int32 [n_axes][n_tokens], needed if
+ * rot > 0); pos[t] is the token's slot only.  Everything else as there. */
+usp_status usp_kv_append_axes(const usp_cache* c, int n_tokens, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, const int32_t* seq, const int32_t* pos,
+                              const int32_t* rot_pos, const float* inv_freq, const usp_rotary* r, void* q_out, void* k_out,
+                              void* k_pages, void* v_pages, const int32_t* page_table, usp_stream stream);
+
+/* ---- who holds the pages of a paged cache, and copies of them.
+ * The state of a cache is, on the device, the page table, the lengths and
+ *   ref  int32 [n_pages]: how many entries of the page table name the page
+ *        (entries of a sequence's length), and holds of the caller's own
+ * A page whose count is 0 (or below) is free.  Empty: every length and count 0,
+ * whatever the table holds.  A caller who adds 1 to a page's count keeps it,
+ * unwritten, until that 1 is taken off (pages of a shared prefix, pages that
+ * some other cache uses).  Entries outside [0, n_pages) within a length are
+ * no pages: they are handed on as they are and not counted.
+ * One table serves the pools of all layers: the calls that change it
+ * (usp_pages_update, usp_pages_compact) write a list of the copies that are
+ * to be made, and usp_pages_copy makes them, in one layer's pools or in many.
+ *   copies  int32 [1 + rows][4], 16-byte aligned: row 0 is
+ *           {copies, pages lacking, free pages left, 0}, row 1 + i is copy i,
+ *           {from, to, tokens, 0}: the first `tokens` tokens of page `from`
+ *           to page `to`.  Rows behind the last copy stay as they were.
+ * No page of a list is both copied from and copied to.  All index arrays are
+ * read on the device (a captured graph replays with new values), results do
+ * not depend on the run. */
+
+/* Bytes of workspace usp_pages_update needs (20 per page, 24 per slot and 4 per
+ * entry of the table); 0 for an invalid cache. */
+size_t usp_pages_update_workspace_size(const usp_cache* c);
+
+/* One step of all slots: forking, reordering, truncating, freeing and growing
+ * sequences.  Slot s goes on with the first
+ *   kept = min(keep[s], length of a)  tokens of a = parent[s], and has
+ *   now  = min(kept + grow[s], max_pages*page_size)  tokens afterwards
+ * (parent NULL: a = s; a outside [0, n_seqs): kept = 0; keep NULL: all; grow
+ * NULL: 0; negative numbers are 0; lengths are clamped to the table).  All
+ * slots begin from the state before the call, so that slots may change places.
+ * Whole pages of the kept tokens are shared with every other slot that goes on
+ * with them.  A page that ends inside the kept tokens and is about to be
+ * written (now > kept) belongs to the slot alone afterwards: if only such slots hold
+ * it, the one that held it before (parent[s] == s), otherwise the lowest, keeps
+ * it, and every other one gets a page of its own and a copy in the list; if
+ * anyone else holds it, all of them do.  New pages -- a slot's copy before its
+ * further pages, lower slots first -- are the free ones with the lowest
+ * numbers, those that this call frees among them.
+ * seq_lens [n_seqs], page_table [n_seqs][max_pages] and ref are updated in
+ * place; entries of a slot that are no longer used become -1.  If there are not
+ * enough free pages, nothing is changed, no copy is listed, and row 0 of
+ * copies tells how many are lacking.  copies has n_seqs rows after row 0.
+ * (Tokens that are appended next have the slots kept .. now - 1; drafts that
+ * were refused are dropped by keep, say by usp_verify_drafts' keep_lens.)
+ * ws: at least usp_pages_update_workspace_size(c) bytes, 256-byte aligned,
+ * contents on entry irrelevant; calls that can overlap on the GPU need one
+ * each.  n_pages <= 2^30. */
+usp_status usp_pages_update(const usp_cache* c, const int32_t* parent, const int32_t* keep, const int32_t* grow,
+                            int32_t* seq_lens, int32_t* page_table, int32_t* ref, int32_t* copies, void* ws, size_t ws_bytes,
+                            usp_stream stream);
+
+/* Brings a pool's n pages in use to its front: pages with numbers from n on, lowest
+ * first, are listed to be copied to the free ones below n, lowest first.
+ * new_id int32 [n_pages]: a page's number afterwards, -1 if it is free (for
+ * numbers that the caller holds elsewhere, as prefix_pages); ref_out the
+ * counts afterwards; page_table_out the table with new numbers (entries that
+ * name no page in use stay as they are).  page_table_out may be page_table
+ * and ref_out may be ref.  copies has n_pages/2 rows after row 0.
+ * n_pages <= 2^30. */
+usp_status usp_pages_compact(const usp_cache* c, const int32_t* page_table, const int32_t* ref, int32_t* page_table_out,
+                             int32_t* ref_out, int32_t* new_id, int32_t* copies, usp_stream stream);
+
+/* Makes the copies of a list of at most max_copies, in k_pages and v_pages of
+ * n_layers layers: layer l's pools begin l*layer_stride elements after the
+ * pointers (n_layers 1: layer_stride plays no part; more: it is at least a
+ * pool's elements and a multiple of 16 bytes).  Rows with a page outside
+ * [0, n_pages) are passed over.  What a page holds behind the copied tokens stays as
+ * it was. */
+usp_status usp_pages_copy(const usp_cache* c, int max_copies, const int32_t* copies, int n_layers, int64_t layer_stride,
+                          void* k_pages, void* v_pages, usp_stream stream);
+
+/* Verification of drafted tokens against the target's probabilities, from given
+ * random numbers, so that the tokens are distributed as the target's own
+ * (speculative sampling).  Sequence s has n = q_start[s+1] - q_start[s] rows t0
+ * = q_start[s] .. of the call, the tokens that usp_paged_attn was just given: one that
+ * counts already and n - 1 drafts.  Row t of target holds the probabilities of
+ * the token after tokens[t]; row t of draft those from which tokens[t] was drawn
+ * (rows t0 are not read); draft NULL: drafts that were not drawn (found in the
+ * text, say), as if of probability 1.  For t = t0+1, t0+2, ..., x = tokens[t]:
+ *   accepted if u[t] * draft[t][x] < target[t-1][x]  (computed exactly; an x
+ *   outside [0, vocab) is refused)
+ * up to the first draft that is refused, at t = r.  next[s] is drawn from the weights
+ *   w_x = max(target[r-1][x] - draft[r][x], 0)  (draft NULL: target[r-1]
+ *         without tokens[r]), or target's last row if no draft is refused
+ * as the lowest token whose running sum w_0 + .. + w_x exceeds u[t0] sum w.
+ * If all w are 0, target's row itself is drawn from; if that is 0 too, next is -1.
+ * n_accepted[s]: drafts accepted; keep_lens[s] = seq_lens[s] - (drafts not
+ * accepted), the cached tokens that stay (both NULL: not asked for; keep_lens
+ * may be seq_lens).  A sequence without rows has n_accepted 0, next -1 and
+ * keep_lens seq_lens.
+ * Weights are cut to whole numbers of 2^-53 and summed exactly: a token is off
+ * only where u[t0] falls within vocab 2^-53 of a border.  Probabilities are
+ * taken to be in [0, 1] (what lies outside is taken as the nearer end, NaN as 0;
+ * NaN refuses a draft), u in [0, 1); rows need not add up to 1.
+ * target, draft: [n_tokens] rows of vocab contiguous elements of dtype F32 or
+ * BF16, strides in elements, at least vocab.  q_start is clamped to [0,
+ * n_tokens].  1 <= vocab <= 2^19; n_seqs <= 2^28 - 1. */
+usp_status usp_verify_drafts(int n_seqs, int n_tokens, int vocab, int dtype, const void* target, int64_t target_stride,
+                             const void* draft, int64_t draft_stride, const int32_t* tokens, const float* u,
+                             const int32_t* q_start, const int32_t* seq_lens, int32_t* n_accepted, int32_t* next,
+                             int32_t* keep_lens, usp_stream stream);
+
 /* ---- kernel tracing ----
  * When enabled, every kernel the library launches is bracketed by two CUDA
  * events recorded on the launch's stream (a few microseconds per launch).
