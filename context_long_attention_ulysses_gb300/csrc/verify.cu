@@ -6,13 +6,14 @@
 // drawn from max(p_i - q_{i + 1}, 0), after none from the last row's p: the tokens are distributed as the target's own.
 //
 // The draw: the weights' running sum in the order of the tokens, the first token at which it exceeds u_0 times the total.
-// A float32 sum of 10^5 weights is off by more than most weights are, so the sums are whole numbers of 2^-53 (weights are
-// cut to that; float64 would do as well, but its units are scarce), which do not depend on the order either.
+// A float32 sum of 10^5 weights is off by more than most weights are, so the sums are whole numbers of 2^-46, to which the
+// probabilities are rounded (float64 would do as well, but its units are scarce); they do not depend on the order either.
 //
 // Bound by HBM for many sequences (one row of p, and of q where a draft is refused, are read once) and by latency for few: a
-// cluster of CTAs takes a sequence, each a slice of the vocabulary in registers' sums only; the CTA, then the warp that holds
-// the threshold goes over its part again, out of L2.
+// cluster of CTAs takes a sequence, each CTA a slice of the vocabulary in tiles, whose sums stay in shared
+// memory; the CTA that holds the threshold finds the tile by them and goes over that tile alone again.
 #include <algorithm>
+#include <type_traits>
 
 #include "cluster.cuh"
 #include "paged.cuh"
@@ -21,21 +22,91 @@ namespace usp {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxVocab = 1 << 19;
+// A lane's values of a tile: twice as many in vectors of bf16 (200 sequences of 50001 tokens 12.7 us against 13.6), not in
+// general (126 sequences of 5239 8.0 against 7.0).
+template <typename T, bool VEC>
+constexpr int kEach = VEC && sizeof(T) == 2 ? 16 : 8;
+template <typename T, bool VEC>
+constexpr int kTile = 32 * kEach<T, VEC>;  // tokens
 
-__device__ __forceinline__ float value(const float* p, int64_t i) { return p[i]; }
-__device__ __forceinline__ float value(const __nv_bfloat16* p, int64_t i) {
-    return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << 16);
+__device__ __forceinline__ float value(const float* p) { return *p; }
+__device__ __forceinline__ float value(const __nv_bfloat16* p) {
+    return __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(p) << 16);
 }
 
-// x in [0, 1] in whole numbers of 2^-53 (53 > 0: cut off), what is not in it (NaN: 0) taken as the nearer end.
-__device__ __forceinline__ uint64_t fixed53(float x) {
-    const uint32_t bits = __float_as_uint(fminf(fmaxf(x, 0.f), 1.f));
-    const uint32_t m = (bits & 0x7fffffu) | 0x800000u;
-    const int shift = (int)(bits >> 23) - 97;                    // x = m 2^(exponent - 150)
-    return shift >= 0 ? (uint64_t)m << shift : (uint64_t)(m >> min(-shift, 31));
+// A lane's values of a tile, as loaded: whole vectors, or one by one where the tile is not 16-byte aligned and where the row begins
+// or ends inside it (EDGE: places [from, to) of it are the row's).  Which lane has which does not matter to a sum.
+template <typename T, bool VEC, int E>
+struct Loaded {
+    float x[E];
+    template <bool EDGE>
+    __device__ __forceinline__ void load(const T* p, int from, int to, int lane) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int i = lane + 32 * e;
+            x[e] = !EDGE || (i >= from && i < to) ? value(p + i) : 0.f;
+        }
+    }
+    __device__ __forceinline__ float at(int e) const { return x[e]; }
+};
+template <typename T, int E>
+struct Loaded<T, true, E> {
+    static constexpr int V = E * sizeof(T) / 16;  // vectors
+    uint32_t w[4 * V];
+    template <bool EDGE>
+    __device__ __forceinline__ void load(const T* p, int, int, int lane) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint4 x = reinterpret_cast<const uint4*>(p)[lane + 32 * v];
+            w[4 * v] = x.x;
+            w[4 * v + 1] = x.y;
+            w[4 * v + 2] = x.z;
+            w[4 * v + 3] = x.w;
+        }
+    }
+    __device__ __forceinline__ float at(int e) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+        return __uint_as_float(e % 2 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    }
+};
+
+// Sums of x in [0, 1], each rounded to whole numbers of 2^-46, kept as two digits: added to a power of two a number's last bits
+// are the digit, what that leaves is exact and, added to a smaller one, gives the next.  (The powers' own bits, which come with
+// every digit, cancel where numbers are subtracted.)  A weight takes 13 instructions, of three digits to 2^-53 cut off it took
+// 20 and by shifting mantissas 30: 64 x 131072 of them 5 us of all schedulers' time against 7 and 11.
+struct Digits {
+    static constexpr float kOne = 1.f, kTwo = 0x1.8p-23f;  // steps of 2^-23 and 2^-46 (x = 1 is the next power: a step on)
+    uint32_t d0 = 0, d1 = 0;
+    static __device__ __forceinline__ void of(float x, uint32_t& a, uint32_t& b) {
+        const float t = x + kOne;
+        a = __float_as_uint(t);
+        b = __float_as_uint((x - (t - kOne)) + kTwo);
+    }
+    __device__ __forceinline__ void add(float x) {
+        uint32_t a, b;
+        of(x, a, b);
+        d0 += a - __float_as_uint(kOne);
+        d1 += b - __float_as_uint(kTwo);
+    }
+    __device__ __forceinline__ void add(float x, float y) {  // x - y, x >= y (a digit of the difference may be negative)
+        uint32_t a, b, c, d;
+        of(x, a, b);
+        of(y, c, d);
+        d0 += a - c;
+        d1 += b - d;
+    }
+    __device__ __forceinline__ uint64_t whole() const { return (uint64_t)(((int64_t)(int32_t)d0 << 23) + (int32_t)d1); }
+};
+// (what is not in [0, 1] is taken as the nearer end, NaN as 0)
+__device__ __forceinline__ uint64_t fixed46(float x) {
+    Digits d;
+    d.add(__saturatef(x));
+    return d.whole();
 }
+
 // u in [0, 1) in whole numbers of 2^-64; what is not in it (NaN: 0) taken as the nearer end.
 __device__ __forceinline__ uint64_t fixed64(float u) {
     const uint32_t bits = __float_as_uint(fminf(fmaxf(u, 0.f), 0x1.fffffep-1f));
@@ -44,80 +115,123 @@ __device__ __forceinline__ uint64_t fixed64(float u) {
     return shift >= 0 ? m << shift : m >> min(-shift, 63);
 }
 
-// Sums stop at the largest number, so that rows which are no probabilities (a thousand ones) still lead to a token.
+// Sums of tiles stop at the largest number, so that rows which are no probabilities (thousands of ones) still lead to a token.
 __device__ __forceinline__ uint64_t add(uint64_t x, uint64_t y) { return x + y < x ? ~0ull : x + y; }
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x = add(x, __shfl_xor_sync(~0u, x, o));
     return x;
 }
-
-// A sequence's weights: max(p - q, 0) with q a row of the draft, one token (`except`), or nothing.
-template <typename T>
-struct Weights {
-    const T *p, *q;  // q null: none
-    int except;      // -1: none
-    __device__ __forceinline__ uint64_t at(int i) const {
-        const uint64_t a = fixed53(value(p, i));
-        if (q) {
-            const uint64_t b = fixed53(value(q, i));
-            return a > b ? a - b : 0;
-        }
-        return i == except ? 0 : a;
+__device__ __forceinline__ uint64_t warp_scan(uint64_t x, int lane) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(~0u, x, o);
+        if (lane >= o) x = add(x, y);
     }
-    // this thread's share of the weights of [i0, i1), which a warp takes in turn (at most 1024 of them: no overflow)
-    __device__ __forceinline__ uint64_t sum(int i0, int i1, int lane) const {
-        uint64_t s = 0;
-        int i = i0 + lane;
-        if (q) {
-            for (; i + 7 * 32 < i1; i += 8 * 32) {
-                float a[8], b[8];
+    return x;
+}
+// The sum over the lanes of numbers below 2^50, to all.
+__device__ __forceinline__ uint64_t lanes_total(uint64_t x) {
+    const uint32_t a = __reduce_add_sync(~0u, (uint32_t)x & 0x3ffffffu), b = __reduce_add_sync(~0u, (uint32_t)(x >> 26));
+    return a + ((uint64_t)b << 26);
+}
+
+template <int N>
+using Const = std::integral_constant<int, N>;
+
+// A sequence's weights: max(p - q, 0) with q a row of the draft, p without one token (`except`), or p.  Places are counted from
+// the 16-byte boundary before the row, so that its vectors are aligned: the row has places [from, to).
+template <typename T, bool VEC>
+struct Weights {
+    static constexpr int E = kEach<T, VEC>, kLength = kTile<T, VEC>;
+    const T *p, *q;  // q null: none
+    int from, to;
+    int except;      // its place, -1: none
+
+    __device__ __forceinline__ uint64_t at(int i) const {
+        if (i < from || i >= to || i == except) return 0;
+        const uint64_t a = fixed46(value(p + i)), b = q ? fixed46(value(q + i)) : 0;
+        return a > b ? a - b : 0;
+    }
+    // The sum of a lane's places in a row, from i on.
+    __device__ __forceinline__ uint64_t few(int i) const {
+        Digits d;
+        float x[E], y[E];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) a[e] = value(p, i + 32 * e);
+        for (int e = 0; e < E; ++e) {
+            const bool some = i + e >= from && i + e < to && i + e != except;
+            x[e] = some ? value(p + i + e) : 0.f;
+            y[e] = some && q ? value(q + i + e) : 0.f;
+        }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) b[e] = value(q, i + 32 * e);
+        for (int e = 0; e < E; ++e) {
+            const float z = __saturatef(y[e]);
+            d.add(fmaxf(__saturatef(x[e]), z), z);
+        }
+        return d.whole();
+    }
+    // Sums of N tiles from place i on, `step` places apart (loads first), each to all lanes; Q: q is not null; EDGE: the row's
+    // first tile or last.
+    template <bool Q, bool EDGE, int N>
+    __device__ __forceinline__ void tiles(int i, int step, int lane, uint64_t (&sum)[N]) const {
+        Loaded<T, VEC && !EDGE, E> a[N], b[Q ? N : 1];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint64_t x = fixed53(a[e]), y = fixed53(b[e]);
-                    s += x > y ? x - y : 0;
+        for (int k = 0; k < N; ++k) a[k].template load<EDGE>(p + i + k * step, from - i, to - i, lane);
+        if constexpr (Q)
+#pragma unroll
+            for (int k = 0; k < N; ++k) b[k].template load<EDGE>(q + i + k * step, from - i, to - i, lane);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            Digits d;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float x = __saturatef(a[k].at(e));
+                if constexpr (Q) {
+                    const float y = __saturatef(b[k].at(e));
+                    d.add(fmaxf(x, y), y);
+                } else {
+                    d.add(x);
                 }
             }
-        } else {
-            for (; i + 7 * 32 < i1; i += 8 * 32) {
-                float a[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) a[e] = value(p, i + 32 * e);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s += i + 32 * e == except ? 0 : fixed53(a[e]);
-            }
+            sum[k] = lanes_total(d.whole());
+            const int j = except - (i + k * step);
+            if (!Q && j >= 0 && j < kLength) sum[k] -= fixed46(value(p + except));
         }
-        for (; i < i1; i += 32) s += at(i);
-        return s;
+    }
+    // Sums of the tiles [first, end), taken by the CTA's warps in turn, to `out`; returns the sum of this warp's.
+    template <bool Q>
+    __device__ __forceinline__ uint64_t slice(int first, int end, int warp, int lane, uint64_t* out) const {
+        constexpr int N = VEC && !Q ? 4 : 2;  // tiles at a time (of vectors: 128 bytes of a lane in flight)
+        const int whole = min(end, to / kLength);
+        uint64_t sum = 0;
+        int t = first + warp;
+        auto some = [&](auto edge, auto count) {
+            uint64_t s[count.value];
+            tiles<Q, edge.value>(t * kLength, kWarps * kLength, lane, s);
+#pragma unroll
+            for (int k = 0; k < count.value; ++k) {
+                sum = add(sum, s[k]);
+                if (lane == 0) out[t - first + k * kWarps] = s[k];
+            }
+            t += count.value * kWarps;
+        };
+        if (t == 0 && from > 0) some(Const<1>(), Const<1>());
+        while (t + (N - 1) * kWarps < whole) some(Const<0>(), Const<N>());
+        if constexpr (N > 2)
+            while (t + kWarps < whole) some(Const<0>(), Const<2>());
+        if constexpr (N > 1)
+            if (t < whole) some(Const<0>(), Const<1>());
+        if (t < end) some(Const<1>(), Const<1>());
+        return sum;
     }
 };
 
-// Piece k of [i0, i1) cut into n equal ones.
-__device__ __forceinline__ int cut(int i0, int i1, int k, int n) { return i0 + (int)((int64_t)(i1 - i0) * k / n); }
-
-// Of n <= 32 sums in order (lane k has the k-th): the one that holds `rest`, which becomes what is left within it.
-__device__ __forceinline__ int holder(uint64_t sum, int lane, int n, uint64_t& rest) {
-    uint64_t to = lane < n ? sum : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t x = __shfl_up_sync(~0u, to, o);
-        if (lane >= o) to = add(to, x);
-    }
-    const uint32_t over = __ballot_sync(~0u, lane < n && to > rest);
-    const int k = over ? __ffs(over) - 1 : n - 1;
-    const uint64_t before = __shfl_sync(~0u, to, max(k - 1, 0));
-    if (k > 0) rest -= min(rest, before);
-    return k;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, int size) {
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams p, int size) {
+    __shared__ uint64_t tile_sum[kMaxVocab / kTile<T, VEC> + 1];  // (rows begin inside a vector)
     __shared__ uint64_t warp_total[kWarps];
     __shared__ uint64_t cta_total[2];   // (a place for each of two goes)
+    constexpr int E = kEach<T, VEC>, kLength = kTile<T, VEC>;
     const int rank = (int)cluster_rank(), b = blockIdx.x / size;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     begin_kernel(false);
@@ -134,6 +248,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
     }
     const T* target = static_cast<const T*>(p.target) + t0 * p.target_stride;
     const T* draft = p.draft ? static_cast<const T*>(p.draft) + t0 * p.draft_stride : nullptr;
+    const float u0 = p.u[t0];
 
     // drafts accepted, found by every warp for itself
     int a = n - 1;
@@ -144,8 +259,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
             const int x = p.tokens[t0 + i + 1];
             refused = true;
             if (x >= 0 && x < p.vocab) {
-                const double q = draft ? (double)value(draft + (i + 1) * p.draft_stride, x) : 1.0;
-                refused = !((double)p.u[t0 + i + 1] * q < (double)value(target + i * p.target_stride, x));  // (exact)
+                const double q = draft ? (double)value(draft + (i + 1) * p.draft_stride + x) : 1.0;
+                refused = !((double)p.u[t0 + i + 1] * q < (double)value(target + i * p.target_stride + x));  // (exact)
             }
         }
         const uint32_t r = __ballot_sync(~0u, refused);
@@ -154,22 +269,26 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
             break;
         }
     }
-    Weights<T> w{target + a * p.target_stride, nullptr, -1};
+    const T* row = target + a * p.target_stride;
+    const int skip = VEC ? (int)(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T)) : 0;
+    Weights<T, VEC> w{row - skip, nullptr, skip, skip + p.vocab, -1};
     if (a < n - 1) {
+        const int x = p.tokens[t0 + a + 1];
         if (draft)
-            w.q = draft + (a + 1) * p.draft_stride;
-        else
-            w.except = p.tokens[t0 + a + 1];
+            w.q = draft + (a + 1) * p.draft_stride - skip;
+        else if (x >= 0 && x < p.vocab)
+            w.except = skip + x;
     }
-    const int i0 = cut(0, p.vocab, rank, size), i1 = cut(0, p.vocab, rank + 1, size);
+    const int all = (w.to + kLength - 1) / kLength;
+    const int first = all * rank / size, end = all * (rank + 1) / size;  // this CTA's tiles
 
-    uint64_t total = 0, mine = 0, before = 0, sum = 0;
+    uint64_t total = 0, mine = 0, before = 0;
     for (int go = 0; go < 2; ++go) {
-        sum = warp_sum(w.sum(cut(i0, i1, warp, kWarps), cut(i0, i1, warp + 1, kWarps), lane));
+        const uint64_t sum = w.q ? w.template slice<true>(first, end, warp, lane, tile_sum)
+                                 : w.template slice<false>(first, end, warp, lane, tile_sum);
         if (lane == 0) warp_total[warp] = sum;
         __syncthreads();
-        sum = lane < kWarps ? warp_total[lane] : 0;
-        mine = warp_sum(sum);
+        mine = warp_sum(lane < kWarps ? warp_total[lane] : 0);
         if (threadIdx.x == 0) cta_total[go] = mine;
         cluster_sync();
         const uint64_t x = lane < size ? cluster_read(&cta_total[go], lane) : 0;
@@ -180,50 +299,53 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
         w.q = nullptr;
         w.except = -1;
     }
+    cluster_arrive();  // (waited for at the end: others may still read this CTA's total)
     if (rank == 0 && threadIdx.x == 0) {
         p.n_accepted[b] = a;
         if (p.keep_lens) p.keep_lens[b] = len - (n - 1 - a);
         if (total == 0) p.next[b] = -1;
     }
-    uint64_t rest = __umul64hi(total, fixed64(p.u[t0]));  // the first token whose running sum exceeds this
-    if (rest >= before && rest - before < mine) {         // (one CTA of the cluster)
+    uint64_t rest = __umul64hi(total, fixed64(u0));                     // the first token whose running sum exceeds this
+    if (warp == 0 && rest >= before && rest - before < mine) {          // (in one CTA of the cluster)
         rest -= before;
-        const int k = holder(sum, lane, kWarps, rest);    // the warp whose part holds it: gone over by all
-        const int j0 = cut(i0, i1, k, kWarps), j1 = cut(i0, i1, k + 1, kWarps);
-        sum = warp_sum(w.sum(cut(j0, j1, warp, kWarps), cut(j0, j1, warp + 1, kWarps), lane));
-        if (lane == 0) warp_total[warp] = sum;
-        __syncthreads();
-        sum = lane < kWarps ? warp_total[lane] : 0;
-        const int l = holder(sum, lane, kWarps, rest);
-        if (warp == 0) {
-            const int c0 = cut(j0, j1, l, kWarps), c1 = cut(j0, j1, l + 1, kWarps);
-            for (int i = c0; i < c1; i += 32) {
-                const uint64_t x = i + lane < c1 ? w.at(i + lane) : 0;
-                uint64_t to = x;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint64_t y = __shfl_up_sync(~0u, to, o);
-                    if (lane >= o) to += y;
-                }
-                const uint32_t over = __ballot_sync(~0u, to > rest);
-                if (over) {
-                    if (lane == 0) p.next[b] = i + __ffs(over) - 1;
-                    break;
-                }
+        for (int t = first; t < end; t += 32) {
+            const uint64_t to = warp_scan(t + lane < end ? tile_sum[t + lane - first] : 0, lane);
+            const uint32_t over = __ballot_sync(~0u, to > rest);
+            if (!over) {
                 rest -= __shfl_sync(~0u, to, 31);
+                continue;
             }
+            const int k = __ffs(over) - 1;
+            const uint64_t less = __shfl_sync(~0u, to, max(k - 1, 0));  // (not to - sum: `to` may have stopped)
+            if (k > 0) rest -= less;
+            // the tile again: the lane that holds it, then each of its values to a lane
+            const int i0 = (t + k) * kLength;
+            const uint64_t upto = warp_scan(w.few(i0 + lane * E), lane);
+            const int l = __ffs(__ballot_sync(~0u, upto > rest)) - 1;
+            const uint64_t less_l = __shfl_sync(~0u, upto, max(l - 1, 0));
+            if (l > 0) rest -= less_l;
+            const int i1 = i0 + l * E;
+            const uint64_t run = warp_scan(lane < E ? w.at(i1 + lane) : 0, lane);
+            const int e = __ffs(__ballot_sync(~0u, run > rest)) - 1;
+            if (lane == 0) p.next[b] = i1 + e - skip;
+            break;
         }
     }
-    cluster_sync();  // (others may still read this CTA's total)
+    cluster_wait();
 }
 
 }  // namespace
 
 cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream) {
-    // A cluster's CTAs: as many as the SMs hold at once, but no fewer than 2048 tokens each.
-    int size = 1;
-    while (size < 8 && (int64_t)p.n_seqs * size * 2 <= 4 * 152 && p.vocab >= 2048 * size * 2) size *= 2;
-    auto kernel = p.elem == 4 ? verify_kernel<float> : verify_kernel<__nv_bfloat16>;
+    // A cluster's CTAs: as many as the SMs hold at once (four each; of a cluster's size less one may be left over in each of the
+    // eight groups that clusters do not cross), but no fewer than 256 tokens for each warp.
+    const int most = std::min(8, std::max(1, p.vocab / (256 * kWarps)));
+    const int size = std::min(most, std::max(1, (4 * 152 + 8) / (p.n_seqs + 8)));
+    // Vectors need a row's and, where a draft's is subtracted, both rows' places aligned alike: any single row is (from its first
+    // 16-byte boundary on), two where the strides are.
+    const bool vec = !p.draft || (p.target_stride * p.elem % 16 == 0 && p.draft_stride * p.elem % 16 == 0);
+    auto kernel = p.elem == 4 ? vec ? verify_kernel<float, true> : verify_kernel<float, false>
+                              : vec ? verify_kernel<__nv_bfloat16, true> : verify_kernel<__nv_bfloat16, false>;
     return launch_clusters(kernel, (unsigned)p.n_seqs, (unsigned)size, kThreads, 0, stream, p, size);
 }
 

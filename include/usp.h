@@ -654,10 +654,10 @@ usp_status usp_pages_copy(const usp_cache* c, int max_copies, const int32_t* cop
  * accepted), the cached tokens that stay (both NULL: not asked for; keep_lens
  * may be seq_lens).  A sequence without rows has n_accepted 0, next -1 and
  * keep_lens seq_lens.
- * Weights are cut to whole numbers of 2^-53 and summed exactly: a token is off
- * only where u[t0] falls within vocab 2^-53 of a border.  Probabilities are
- * taken to be in [0, 1] (what lies outside is taken as the nearer end, NaN as 0;
- * NaN refuses a draft), u in [0, 1); rows need not add up to 1.
+ * For the draw probabilities are rounded to whole numbers of 2^-46 (half a step
+ * of u is 2^-25) and summed exactly, in whatever order.  They are to be in
+ * [0, 1] (what lies outside is taken as the nearer end, NaN as 0; NaN refuses a
+ * draft), u in [0, 1); rows need not add up to 1.
  * target, draft: [n_tokens] rows of vocab contiguous elements of dtype F32 or
  * BF16, strides in elements, at least vocab.  q_start is clamped to [0,
  * n_tokens].  1 <= vocab <= 2^19; n_seqs <= 2^28 - 1. */
