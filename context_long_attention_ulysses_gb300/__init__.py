@@ -48,6 +48,8 @@ __all__ = [
 ]
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_Tensor = torch.Tensor
 _TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
@@ -69,6 +71,14 @@ class Problem:
             raise ValueError(f"dtype must be 'f32' or 'bf16', got {self.dtype!r}")
         return UspProblem(self.B, self.Hq, self.Hkv, self.N, self.d, self.P, int(bool(self.causal)),
                           float(self.scale), USP_F32 if self.dtype == "f32" else USP_BF16)
+
+    def _kept(self) -> UspProblem:
+        """The struct that calls pass on."""
+        made = self.__dict__.get("_c")
+        if made is None:
+            made = self.c()
+            object.__setattr__(self, "_c", made)
+        return made
 
     @property
     def torch_dtype(self) -> torch.dtype:
@@ -201,16 +211,18 @@ def library_path() -> str:
 
 
 def _ptr(x) -> int:
-    if x is None:
-        return 0
-    if isinstance(x, int):
-        return x
-    if isinstance(x, torch.Tensor):
+    if isinstance(x, _Tensor):
+        if x.is_cuda and x.is_contiguous():
+            return x.data_ptr()
         if not x.is_cuda and x.numel():
             raise ValueError("libusp takes device tensors")
         if not x.is_contiguous():
             raise ValueError("libusp takes contiguous tensors")
         return x.data_ptr()
+    if x is None:
+        return 0
+    if isinstance(x, int):
+        return x
     raise TypeError(f"expected a torch tensor, a device pointer or None, got {type(x).__name__}")
 
 
@@ -219,7 +231,7 @@ def _stream(stream) -> int:
         # (a decoding step is short enough for this to show: the stream object costs 3 us, asking the driver whether there is
         # a device another; the handle alone a few tenths)
         if _raw_stream is not None and torch.cuda.is_initialized():
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else 0
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -245,9 +257,23 @@ def _rows(x, heads: int, d: int):
 
 def _token_rows(x, heads: int, d: int):
     """`_rows` of a sequence-sharded tensor [P][B][N/P][heads][d], or of one that is [tokens][heads][d] already."""
-    if isinstance(x, torch.Tensor) and x.dim() == 5:
-        x = x.view(-1, *x.shape[3:])   # (raises where the tokens are not evenly apart)
-    return _rows(x, heads, d)
+    if not isinstance(x, _Tensor) or x.dim() != 5:
+        return _rows(x, heads, d)
+    P, B, n, H, w = x.shape
+    sP, sB, sn, sh, sd = x.stride()
+    if H != heads or w != d:
+        raise ValueError(f"expected [P][B][N/P][{heads}][{d}], got {list(x.shape)}")
+    if not P * B * n:
+        return x.data_ptr(), heads * d
+    if not x.is_cuda:
+        raise ValueError("libusp takes device tensors")
+    if sd != 1 or (heads > 1 and sh != d):
+        raise ValueError("the heads of a token must be contiguous")
+    # the one distance between tokens: of the innermost dimension that has more than one of them
+    step = sn if n > 1 else sB if B > 1 else sP if P > 1 else heads * d
+    if (B > 1 and sB != n * step) or (P > 1 and sP != B * n * step):
+        raise ValueError("tokens must be evenly apart")
+    return x.data_ptr(), step
 
 
 def _rotary(r) -> ctypes.POINTER(UspRotary):
@@ -265,7 +291,7 @@ def _cache(c) -> ctypes.POINTER(UspCache):
 def _prob(p) -> ctypes.POINTER(UspProblem):
     if p is None:
         return None
-    return ctypes.byref(p.c() if isinstance(p, Problem) else p)
+    return ctypes.byref(p._kept() if isinstance(p, Problem) else p)
 
 
 # --------------------------------------------------------------- C ABI mirror
@@ -531,15 +557,22 @@ def usp_pages_copy(c, max_copies: int, copies, k_pages, v_pages, n_layers: int =
                                                   int(layer_stride), _ptr(k_pages), _ptr(v_pages), _stream(stream)))
 
 
-def _prob_rows(x, vocab: int):
+def _prob_rows(x, vocab: int, dtype):
     """Pointer and row stride (elements) of probabilities [rows][vocab], or of a device pointer to contiguous rows."""
-    if x is None or isinstance(x, int):
-        return x or 0, vocab
-    if not x.is_cuda and x.numel():
+    if not isinstance(x, _Tensor):
+        return _ptr(x), vocab
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != vocab:
+        raise ValueError(f"expected rows of {vocab} elements, got {list(shape)}")
+    if x.dtype != dtype:
+        raise ValueError(f"expected {dtype}, got {x.dtype}")
+    rows = shape[0]
+    if not x.is_cuda and rows:
         raise ValueError("libusp takes device tensors")
-    if x.dim() != 2 or x.shape[1] != vocab or (x.shape[0] and vocab > 1 and x.stride(1) != 1):
-        raise ValueError(f"expected rows of {vocab} contiguous elements, got {list(x.shape)}")
-    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else vocab
+    step, one = x.stride()
+    if rows and vocab > 1 and one != 1:
+        raise ValueError("the probabilities of a row must be contiguous")
+    return x.data_ptr(), step if rows > 1 else vocab
 
 
 def usp_verify_drafts(n_seqs: int, n_tokens: int, vocab: int, target, draft, tokens, u, q_start, seq_lens, n_accepted,
@@ -547,16 +580,13 @@ def usp_verify_drafts(n_seqs: int, n_tokens: int, vocab: int, target, draft, tok
     """target, draft (or None): [n_tokens][vocab] with any row stride; dtype: theirs, "f32" or "bf16" (needed for device
     pointers)."""
     if dtype is None:
-        dtype = "bf16" if isinstance(target, torch.Tensor) and target.dtype == torch.bfloat16 else "f32"
-    for x in (target, draft):
-        if isinstance(x, torch.Tensor) and x.dtype != _TORCH_DTYPE[dtype]:
-            raise ValueError(f"expected {_TORCH_DTYPE[dtype]}, got {x.dtype}")
-    (tp, ts), (dp, ds) = _prob_rows(target, vocab), _prob_rows(draft, vocab)
-    check("usp_verify_drafts", load().usp_verify_drafts(int(n_seqs), int(n_tokens), int(vocab),
-                                                        USP_F32 if dtype == "f32" else USP_BF16, tp, ts, dp, ds,
-                                                        _ptr(tokens), _ptr(u), _ptr(q_start), _ptr(seq_lens),
-                                                        _ptr(n_accepted), _ptr(next_tokens), _ptr(keep_lens),
-                                                        _stream(stream)))
+        dtype = "bf16" if isinstance(target, _Tensor) and target.dtype == torch.bfloat16 else "f32"
+    kind = _TORCH_DTYPE[dtype]
+    (tp, ts), (dp, ds) = _prob_rows(target, vocab, kind), _prob_rows(draft, vocab, kind)
+    check("usp_verify_drafts", load().usp_verify_drafts(n_seqs, n_tokens, vocab, USP_F32 if dtype == "f32" else USP_BF16,
+                                                        tp, ts, dp, ds, _ptr(tokens), _ptr(u), _ptr(q_start),
+                                                        _ptr(seq_lens), _ptr(n_accepted), _ptr(next_tokens),
+                                                        _ptr(keep_lens), _stream(stream)))
 
 
 def usp_diag_wait_timeout(stream=None) -> None:

@@ -86,6 +86,8 @@ _lib = None
 def load() -> ctypes.CDLL:
     """Load libusp.so (built by ``build.build()``); raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

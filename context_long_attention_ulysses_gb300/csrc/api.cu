@@ -1439,7 +1439,7 @@ usp_status usp_kv_append_axes(const usp_cache* c, int n_tokens, const void* q, i
 // ---------------------------------------------------------------- pages of the cache
 static usp_status check_pages(const usp_cache* c) {
     usp_status st = check_cache(c);
-    if (st == USP_OK && c->n_pages > 1 << 30) return USP_ERR_UNSUPPORTED;  // (loops over pages count in ints)
+    if (st == USP_OK && c->n_pages > 1 << 23) return USP_ERR_UNSUPPORTED;  // (who is live fits a cluster's shared memory)
     return st;
 }
 

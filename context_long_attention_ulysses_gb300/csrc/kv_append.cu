@@ -8,10 +8,12 @@
 //
 // Bound by HBM: every value is read once and written once (k twice with k_out).  A head is d / (2 V) items of two 16-byte
 // vectors (V values): the two that a rotation pairs up, or two neighbours where pairs are neighbours or pass unchanged.  A
-// CTA takes as many tokens as make about kItems items; its threads first issue their loads, then find the tokens' slots
-// (two dependent loads) and the tokens' cosines and sines (one per pair, shared by all heads), and only then wait for the
-// data.  Measured: 32768 tokens of 32 query and 8 KV heads of 128 bf16 values, k_out too, 134 us, 6.5 TB/s (0.98 of a copy);
-// one token each of eight sequences 3.5 us in a graph.
+// CTA takes as many tokens as make about kItems items; its threads first load their angles' positions and frequencies, then
+// issue the data's loads, find the tokens' slots (two dependent loads) and the tokens' cosines and sines (one per pair, shared by
+// all heads), and only then wait for the data.  (Positions on three axes are three lines of memory: asked for behind the
+// data, 32768 tokens took 140.5 us, before it 132.4; on one axis 131.5 and 130.5.)  Measured: 32768 tokens of 32 query and 8 KV
+// heads of 128 bf16 values, k_out too, 130.5 us (three axes 132.4, 6.6 TB/s, 0.97 of a copy); one token each of eight
+// sequences 3.5 us in a graph.
 #include <algorithm>
 #include <cmath>
 
@@ -81,6 +83,16 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
         }
     };
     begin_kernel(false);
+    const int angles = n_tok * half;
+    int r0 = 0;
+    float f0 = 0.f;
+    auto angle_of = [&](int x, int& r, float& f) {
+        const int tok = x / half, i = x - tok * half;
+        const int64_t t = t0 + tok;
+        r = p.rot_pos ? p.rot_pos[pair_axis(p.axes, i) * (int64_t)p.n_tokens + t] : p.pos[t];
+        f = p.inv_freq[i];
+    };
+    if (threadIdx.x < angles) angle_of(threadIdx.x, r0, f0);
     fetch(threadIdx.x);
     if (threadIdx.x < n_tok) {
         const int t = t0 + threadIdx.x, s = p.seq[t], pos = p.pos[t];
@@ -92,10 +104,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
         s_row[threadIdx.x] = row;
     }
     // (not through shared memory: the angles need not wait for the slots)
-    for (int x = threadIdx.x; x < n_tok * half; x += kThreads) {
+    for (int x = threadIdx.x; x < angles; x += kThreads) {
+        if (x != threadIdx.x) angle_of(x, r0, f0);
         const int tok = x / half, i = x - tok * half;
-        const int64_t t = t0 + tok;
-        cs[tok][i] = turn(p.rot_pos ? p.rot_pos[pair_axis(p.axes, i) * (int64_t)p.n_tokens + t] : p.pos[t], p.inv_freq[i]);
+        cs[tok][i] = turn(r0, f0);
     }
     __syncthreads();
     for (int x0 = threadIdx.x; x0 < total; x0 += kItems) {

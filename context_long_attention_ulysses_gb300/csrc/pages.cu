@@ -5,13 +5,16 @@
 // a page whose count is 0 is free.  There is no list of free pages: pages are handed out lowest first, found by going over
 // the counts, so that the same state gives the same pages and a pool fills from its beginning.
 //
-// usp_pages_update is bound by latency (64 conversations in a pool of 4568 pages need 20 KB): one launch of one cluster, whose CTAs
-// each take a share of the slots and of the pages, with a barrier of the cluster where all have to have counted:
-//   1 the counts are copied to the workspace and what the slots do is worked out: what they hold is counted off, what they go
-//     on with is counted on (what stays is left alone), rows that come from another slot are put aside, and a page that
-//     ends inside and is about to be written counts its writers and remembers the first;
-//   2 a writer that must not keep such a page takes a copy; new pages and copies are numbered slot by slot, free pages page by page;
-//   3 if there are enough: rows, counts and lengths are written, and the list of copies.
+// usp_pages_update is bound by latency (64 conversations in a pool of 4568 pages need 20 KB), its steps are
+//   init    the pages' counts;
+//   enter, move   what the slots hold is counted off, what they go on with is counted on (what stays is left alone).  A page that
+//           ends inside and is about to be written is not counted but remembers the first of its writers: if its count is 0
+//           then, the writers alone hold it, and the first keeps it;
+//   number  new pages and copies slot by slot, free pages page by page;
+//   write   rows, lengths, the list of copies, counts, if there are pages enough.
+// Small caches take one CTA with all counts in its shared memory (64 conversations 11.4 us as one cluster of eight CTAs with the
+// counts in L2, where a step's few dependent accesses and a barrier cost 1 to 4 us), others a launch for each step, which
+// follow each other by dependent launch.
 #include <algorithm>
 
 #include "cluster.cuh"
@@ -23,7 +26,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtas = 8;          // of a cluster
+constexpr int kCtas = 8;           // of a cluster
 
 // Exclusive running sum over the CTA's threads, and the total to all.
 __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* total, uint64_t (&part)[kWarps]) {
@@ -47,9 +50,8 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* total, uint
     return before + to - x;
 }
 
-// Share `rank` of n things among kCtas, and of a CTA's share among its warps.
-__device__ __forceinline__ int share(int n, int rank) { return (int)((int64_t)n * rank / kCtas); }
-__device__ __forceinline__ int warp_share(int i0, int i1, int warp) { return i0 + (int)((int64_t)(i1 - i0) * warp / kWarps); }
+// Share `k` of `n` in [i0, i1).
+__device__ __forceinline__ int share(int i0, int i1, int k, int n) { return i0 + (int)((int64_t)(i1 - i0) * k / n); }
 
 // The places of [i0, i1) (a warp's) for which `is` holds, in order: f(place, number of those before it).  Returns how many.
 template <typename Is, typename F>
@@ -66,265 +68,444 @@ __device__ __forceinline__ int each_of(int i0, int i1, Is&& is, F&& f) {
     return n;
 }
 
-struct UpdateSpace {
-    int32_t *count, *writers, *free_ids;  // [n_pages]
-    uint32_t* first;                      // [n_pages]
-    int4* slot;                                    // [n_seqs]: kept, new, pages held, place of what it needs
-    int32_t* copy;                                 // [n_seqs]: its copy's place in the list, -1: none
-    int32_t* stage;                                // [n_seqs][max_pages]: rows that come from another slot
-};
+constexpr uint32_t kNobody = ~0u;
 
-__host__ __device__ inline size_t layout(int n_seqs, int max_pages, int n_pages, char* ws, UpdateSpace* u) {
+// What the update's steps keep between them: in the shared memory of the one CTA, or in the workspace.
+struct Books {
+    int32_t* count;     // [n_pages]: holders, without those that are about to write the page
+    uint32_t* first;    // [n_pages]: the first of those, kNobody
+    int32_t* free_ids;  // [n_pages]: free pages, lowest first
+    int4* slot;         // [n_seqs]: tokens kept, tokens afterwards, pages held before, the page that ends inside (-1: none)
+    int4* place;        // [n_seqs]: what it needs begins here; place of its copy in the list, -1; kSlot...; parent
+    int32_t* stage;     // [n_seqs][max_pages]: rows of slots that change places (workspace in any case)
+    int64_t* totals;    // pages needed, free pages, copies, pages free before
+};
+enum : int { kSlotOther = 1, kSlotStaged = 2, kSlotWrites = 4 };
+
+__host__ __device__ inline size_t books_bytes(int n_seqs, int n_pages) { return 12 * (size_t)n_pages + 32 * (size_t)n_seqs; }
+
+// (n_pages and n_seqs of the caches that one CTA takes; of one with forks, also the entries that it may have to copy: 3400 of them
+// took one CTA 13 us and the launches 16, 132000 38 and 16)
+constexpr int kOnePages = 16384, kOneSeqs = 1024;
+constexpr int64_t kOneEntries = 1 << 16;
+__host__ __device__ inline bool one_cta(const PagesUpdateParams& p) {
+    return p.n_pages <= kOnePages && p.n_seqs <= kOneSeqs && (!p.parent || (int64_t)p.n_seqs * p.max_pages <= kOneEntries);
+}
+
+__host__ __device__ inline size_t layout(int n_seqs, int max_pages, int n_pages, char* ws, Books* u) {
     size_t at = 0;
     auto take = [&](size_t bytes) {
         char* p = ws + at;
         at += (bytes + 255) / 256 * 256;
         return p;
     };
+    u->totals = reinterpret_cast<int64_t*>(take(4 * sizeof(int64_t)));
     u->count = reinterpret_cast<int32_t*>(take(4 * (size_t)n_pages));
-    u->writers = reinterpret_cast<int32_t*>(take(4 * (size_t)n_pages));
     u->first = reinterpret_cast<uint32_t*>(take(4 * (size_t)n_pages));
     u->free_ids = reinterpret_cast<int32_t*>(take(4 * (size_t)n_pages));
     u->slot = reinterpret_cast<int4*>(take(16 * (size_t)n_seqs));
-    u->copy = reinterpret_cast<int32_t*>(take(4 * (size_t)n_seqs));
+    u->place = reinterpret_cast<int4*>(take(16 * (size_t)n_seqs));
     u->stage = reinterpret_cast<int32_t*>(take(4 * (size_t)n_seqs * max_pages));
     return at;
 }
 
-__global__ void __launch_bounds__(kThreads) pages_update_kernel(const PagesUpdateParams p, const UpdateSpace u) {
+// The steps, for PagesUpdateParams p and Books u that more than one CTA uses (ONE: one CTA, the books in its shared memory).
+template <bool ONE>
+struct Update {
+    static constexpr int kRowLanes = ONE ? 8 : 32;  // lanes to a row (one CTA has few warps, and rows that are short or few)
+    const PagesUpdateParams& p;
+    const Books u;
+
+    template <typename T>
+    __device__ __forceinline__ static T get(const T* x) {
+        if constexpr (ONE) return *x;
+        return __ldcg(x);
+    }
+    __device__ __forceinline__ int pages(int tokens) const { return (tokens + (1 << p.page_log2) - 1) >> p.page_log2; }
+    __device__ __forceinline__ bool inside(int id) const { return id >= 0 && id < p.n_pages; }
+    __device__ __forceinline__ bool slot_exists(int b) const { return b >= 0 && b < p.n_seqs; }
+    __device__ __forceinline__ int length(int b) const { return min(max(__ldcg(p.seq_lens + b), 0), p.max_pages << p.page_log2); }
+    __device__ __forceinline__ int parent(int b) const { return p.parent ? __ldcg(p.parent + b) : b; }
+    __device__ __forceinline__ int kept(int b, int most) const { return p.keep ? min(max(__ldcg(p.keep + b), 0), most) : most; }
+    __device__ __forceinline__ int32_t* row(int b) const { return p.page_table + (int64_t)b * p.max_pages; }
+    __device__ __forceinline__ int32_t* stage(int b) const { return u.stage + (int64_t)b * p.max_pages; }
+    // of the writers of a page the one that holds it already is the first, then the lowest slot
+    __device__ __forceinline__ static uint32_t order(int a, int b) { return a == b ? (uint32_t)b : (uint32_t)b | 0x80000000u; }
+    __device__ __forceinline__ bool is_free(int i) const { return get(u.count + i) <= 0 && get(u.first + i) == kNobody; }
+
+    // Pages [i0, i1), in steps of n from i0 + k on.  Returns how many of this thread's are free as they are.
+    __device__ __forceinline__ int init(int k, int n) const {
+        int held = 0;
+#pragma unroll 4
+        for (int i = k; i < p.n_pages; i += n) {
+            const int c = __ldcg(p.ref + i);
+            u.count[i] = c;
+            u.first[i] = kNobody;
+            held += c <= 0;
+        }
+        return held;
+    }
+
+    __device__ __forceinline__ void add(int id, int n) const {
+        if (inside(id)) atomicAdd(u.count + id, n);
+    }
+
+    // f(j, x[j], y[j]) for the places [from, max(nx, ny)) of two rows, -1 behind the first nx and ny, by kRowLanes lanes.
+    template <typename F>
+    __device__ __forceinline__ static void entries(const int32_t* x, int nx, const int32_t* y, int ny, int from, int lane, F&& f) {
+        const int end = max(nx, ny);
+        for (int j = from + lane; j < end; j += 8 * kRowLanes) {
+            int a[8], b[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int i = j + e * kRowLanes;
+                a[e] = i < nx ? __ldcg(x + i) : -1;
+                b[e] = i < ny ? __ldcg(y + i) : -1;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (j + e * kRowLanes < end) f(j + e * kRowLanes, a[e], b[e]);
+        }
+    }
+
+    // What slot b is to do, by a thread; a slot that goes on by itself also gives up the first two pages that it drops.
+    __device__ __forceinline__ void enter(int b) const {
+        const int a = parent(b), cap = p.max_pages << p.page_log2;
+        const bool known = slot_exists(a), other = a != b;
+        const int old = length(b), most = known ? other ? length(a) : old : 0;
+        const int keeps = kept(b, most), grow = p.grow ? max(__ldcg(p.grow + b), 0) : 0;
+        const int now = keeps + min(grow, cap - keeps), old_n = pages(old), kept_n = pages(keeps);
+        // (what a slot that goes on by itself keeps is not written in this call, and can be read from its row at the end)
+        const bool staged = other && keeps > 0 && (parent(a) != a || kept(a, most) < keeps);
+        const bool ends_inside = keeps & ((1 << p.page_log2) - 1);
+        const int last = ends_inside ? __ldcg(row(a) + kept_n - 1) : -1;
+        const bool writes = ends_inside && now > keeps && inside(last);
+        u.slot[b] = make_int4(keeps, now, old_n, last);
+        u.place[b] = make_int4(0, -1, (other ? kSlotOther : 0) | (staged ? kSlotStaged : 0) | (writes ? kSlotWrites : 0), a);
+        if (writes) {
+            atomicMin(u.first + last, order(a, b));
+            atomicAdd(u.count + last, -1);  // (counted on by move(), or already)
+        }
+        if (!other) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (kept_n + j < old_n) add(__ldcg(row(b) + kept_n + j), -1);
+        }
+    }
+    // The rest of what slot b gives up, and what it takes over, by kRowLanes lanes.  (Pages that it holds in the same place
+    // before and after, as when the same prompt is forked again, are left alone.)
+    __device__ __forceinline__ void move(int b, int lane) const {
+        const int4 s = get(u.slot + b), at = get(u.place + b);
+        const int kept_n = pages(s.x);
+        if (!(at.z & kSlotOther)) {
+            entries(row(b), s.z, nullptr, 0, kept_n + 2, lane, [&](int, int id, int) { add(id, -1); });
+            return;
+        }
+        int32_t* const to = at.z & kSlotStaged ? stage(b) : nullptr;
+        entries(row(b), s.z, kept_n > 0 ? row(at.w) : nullptr, kept_n, 0, lane, [&](int j, int old, int id) {
+            if (old != id) {
+                add(old, -1);
+                add(id, 1);
+            }
+            if (to && j < kept_n) to[j] = id;
+        });
+    }
+
+    // What slot b needs: pages (2^27 at most), and 2^40 if one of them is a copy.
+    __device__ __forceinline__ uint64_t needs(int b) const {
+        const int4 s = get(u.slot + b), at = get(u.place + b);
+        const bool copies = (at.z & kSlotWrites) && (get(u.count + s.w) > 0 || get(u.first + s.w) != order(at.w, b));
+        return (uint64_t)(pages(s.y) - pages(s.x) + copies) | (uint64_t)copies << 40;
+    }
+
+    // Slot b, by kRowLanes lanes.
+    __device__ __forceinline__ void write(int b, int lane) const {
+        const int4 s = get(u.slot + b), at = get(u.place + b);
+        const int kept_n = pages(s.x), new_n = pages(s.y);
+        int32_t* to = row(b);
+        int k = at.x;
+        int last = s.w;
+        if (at.y >= 0) {
+            last = get(u.free_ids + k++);
+            if (lane == 0)
+                *reinterpret_cast<int4*>(p.copies + 4 * (1 + (int64_t)at.y)) = make_int4(s.w, last, s.x & ((1 << p.page_log2) - 1), 0);
+        }
+        const bool ends_inside = s.x & ((1 << p.page_log2) - 1);
+        if (at.z & kSlotOther) {
+            const int32_t* from = at.z & kSlotStaged ? stage(b) : slot_exists(at.w) ? row(at.w) : to;
+            entries(from, kept_n - ends_inside, nullptr, 0, 0, lane, [&](int j, int id, int) { to[j] = id; });
+        }
+        if (lane == 0 && ends_inside && (at.y >= 0 || (at.z & kSlotOther))) to[kept_n - 1] = last;
+        for (int j = kept_n + lane; j < new_n; j += kRowLanes) to[j] = get(u.free_ids + k + (j - kept_n));
+        for (int j = new_n + lane; j < s.z; j += kRowLanes) to[j] = -1;
+        if (lane == 0) p.seq_lens[b] = s.y;
+    }
+
+    // The count of page i; the free pages up to `taken` are taken.
+    __device__ __forceinline__ void commit(int i, int taken) const {
+        const int c = get(u.count + i);
+        p.ref[i] = c > 0 ? c : get(u.first + i) != kNobody || i <= taken;
+    }
+
+    __device__ __forceinline__ void head(int64_t need, int64_t free_n, int64_t copies, int64_t held) const {
+        *reinterpret_cast<int4*>(p.copies) = need <= free_n
+                                                 ? make_int4((int)copies, 0, (int)(free_n - need), 0)
+                                                 : make_int4(0, (int)min(need - free_n, (int64_t)INT32_MAX), (int)held, 0);
+    }
+};
+
+__global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_constant__ PagesUpdateParams p, int32_t* stage) {
+    extern __shared__ int4 smem[];
+    __shared__ uint64_t part[kWarps];
+    Books u;
+    u.slot = smem;
+    u.place = u.slot + p.n_seqs;
+    u.count = reinterpret_cast<int32_t*>(u.place + p.n_seqs);
+    u.first = reinterpret_cast<uint32_t*>(u.count + p.n_pages);
+    u.free_ids = reinterpret_cast<int32_t*>(u.first + p.n_pages);
+    u.stage = stage;
+    const Update<true> x{p, u};
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    begin_kernel(false);
+    const int held = x.init(threadIdx.x, kThreads);
+    __syncthreads();
+    // (one slot to a thread: kOneSeqs of them at most)
+    const int b = threadIdx.x;
+    if (b < p.n_seqs) x.enter(b);
+    __syncthreads();
+    constexpr int kLanes = Update<true>::kRowLanes;
+    const int group = threadIdx.x / kLanes, row_lane = threadIdx.x % kLanes;
+    for (int s = group; s < p.n_seqs; s += kThreads / kLanes) x.move(s, row_lane);
+    __syncthreads();
+    const uint64_t mine = b < p.n_seqs ? x.needs(b) : 0;
+    const int w0 = share(0, p.n_pages, warp, kWarps), w1 = share(0, p.n_pages, warp + 1, kWarps);
+    auto is_free = [&](int i) { return x.is_free(i); };
+    const int free_here = each_of(w0, w1, is_free, [](int, int) {});
+    uint64_t sum, all;
+    const uint64_t at = block_scan(mine, &sum, part);
+    uint64_t before = block_scan((lane == 0 ? free_here : 0) | (uint64_t)held << 32, &all, part);
+    const int64_t need = sum & ((1ull << 40) - 1), copies = sum >> 40, free_n = (uint32_t)all;
+    if (threadIdx.x == 0) x.head(need, free_n, copies, all >> 32);
+    if (need > free_n) return;
+    if (b < p.n_seqs) {
+        u.place[b].x = (int)(at & ((1ull << 40) - 1));
+        if (mine >> 40) u.place[b].y = (int)(at >> 40);
+    }
+    const int first = (int)(uint32_t)__shfl_sync(~0u, before, 0);
+    if (first < need) each_of(w0, w1, is_free, [&](int i, int k) { u.free_ids[first + k] = i; });
+    __syncthreads();
+    for (int s = group; s < p.n_seqs; s += kThreads / kLanes) x.write(s, row_lane);
+    const int taken = need > 0 ? u.free_ids[need - 1] : -1;
+    for (int i = threadIdx.x; i < p.n_pages; i += kThreads) x.commit(i, taken);
+}
+
+// The same, a launch for each step, with the books in the workspace.
+constexpr int kStepThreads = 256;
+constexpr int kStepLanes = Update<false>::kRowLanes;
+
+__global__ void __launch_bounds__(kStepThreads) pages_init_kernel(const __grid_constant__ PagesUpdateParams p, const Books u) {
+    const Update<false> x{p, u};
+    begin_kernel(false);
+    if (blockIdx.x == 0 && threadIdx.x < 4) u.totals[threadIdx.x] = 0;
+    x.init(blockIdx.x * kStepThreads + threadIdx.x, gridDim.x * kStepThreads);
+}
+
+__global__ void __launch_bounds__(kStepThreads) pages_count_kernel(const __grid_constant__ PagesUpdateParams p, const Books u) {
+    const Update<false> x{p, u};
+    begin_kernel(false);
+    const int groups = gridDim.x * (kStepThreads / kStepLanes), group = blockIdx.x * (kStepThreads / kStepLanes) + threadIdx.x / kStepLanes;
+    const int lane = threadIdx.x % kStepLanes;
+    for (int64_t b = group; b < p.n_seqs; b += groups) {
+        if (lane == 0) x.enter((int)b);
+        __syncwarp();
+        x.move((int)b, lane);
+    }
+}
+
+// One cluster; CTA `rank` has a share of the slots and of the pages.
+__global__ void __launch_bounds__(kThreads, 1) pages_number_kernel(const __grid_constant__ PagesUpdateParams p, const Books u) {
     __shared__ uint64_t part[kWarps];
     __shared__ uint64_t said[3];  // to the cluster: what its slots need, their copies, its free pages | those before << 32
+    const Update<false> x{p, u};
     const int rank = (int)cluster_rank(), warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int page = 1 << p.page_log2, cap = p.max_pages << p.page_log2;
-    const int p0 = share(p.n_pages, rank), p1 = share(p.n_pages, rank + 1);
-    const int s0 = share(p.n_seqs, rank), s1 = share(p.n_seqs, rank + 1);
-    auto pages = [&](int tokens) { return (tokens + page - 1) >> p.page_log2; };
-    auto inside = [&](int id) { return id >= 0 && id < p.n_pages; };
-    auto length = [&](int b) { return min(max(__ldcg(p.seq_lens + b), 0), cap); };
-    auto parent = [&](int b) { return p.parent ? __ldcg(p.parent + b) : b; };
-    // of the writers of a page the one that holds it already is the first, then the lowest slot
-    auto order = [](int a, int b) { return a == b ? (uint32_t)b : (uint32_t)b | 0x80000000u; };
+    const int s0 = share(0, p.n_seqs, rank, kCtas), s1 = share(0, p.n_seqs, rank + 1, kCtas);
+    const int p0 = share(0, p.n_pages, rank, kCtas), p1 = share(0, p.n_pages, rank + 1, kCtas);
+    const int w0 = share(p0, p1, warp, kWarps), w1 = share(p0, p1, warp + 1, kWarps);
     begin_kernel(false);
-    int held = 0;  // pages that are free before
-    for (int i = p0 + threadIdx.x; i < p1; i += kThreads) {
-        const int c = __ldcg(p.ref + i);
-        u.count[i] = c;
-        u.writers[i] = 0;
-        u.first[i] = ~0u;
-        held += c <= 0;
-    }
-    cluster_sync();
-
-    // (warps of all CTAs in turn: rows are of any length)
-    for (int64_t b0 = warp * kCtas + rank; b0 < p.n_seqs; b0 += kWarps * kCtas) {
-        const int b = (int)b0, a = parent(b);
-        const bool known = a >= 0 && a < p.n_seqs;
-        const int old = length(b), most = known ? length(a) : 0;
-        const int kept = p.keep ? min(max(__ldcg(p.keep + b), 0), most) : most;
-        const int grow = p.grow ? max(__ldcg(p.grow + b), 0) : 0;
-        const int now = kept + min(grow, cap - kept);
-        const int kept_n = pages(kept);
-        if (lane == 0) u.slot[b] = make_int4(kept, now, pages(old), 0);
-        const int32_t* mine = p.page_table + (int64_t)b * p.max_pages;
-        const int32_t* from = known ? p.page_table + (int64_t)a * p.max_pages : mine;
-#pragma unroll 4
-        for (int j = (a == b ? kept_n : 0) + lane; j < pages(old); j += 32) {
-            const int id = __ldcg(mine + j);
-            if (inside(id)) atomicAdd(u.count + id, -1);
-        }
-        if (a != b) {
-            int32_t* stage = u.stage + (int64_t)b * p.max_pages;
-#pragma unroll 4
-            for (int j = lane; j < kept_n; j += 32) {
-                const int id = __ldcg(from + j);
-                stage[j] = id;
-                if (inside(id)) atomicAdd(u.count + id, 1);
-            }
-        }
-        if (lane == 0 && now > kept && (kept & (page - 1))) {
-            const int id = __ldcg(from + kept_n - 1);
-            if (inside(id)) {
-                atomicAdd(u.writers + id, 1);
-                atomicMin(u.first + id, order(a, b));
-            }
-        }
-    }
-    cluster_sync();
-
     uint64_t needs = 0, copying = 0;  // of this CTA's slots
     for (int64_t b0 = s0; b0 < s1; b0 += kThreads) {
-        const int b = (int)b0 + threadIdx.x;
         const bool some = b0 + threadIdx.x < s1;
-        uint64_t x = 0;  // pages that the slot needs (2^27 at most), and 2^40 if one of them is a copy
-        bool copies = false;
-        if (some) {
-            const int4 s = __ldcg(u.slot + b);
-            if (s.y > s.x && (s.x & (page - 1))) {
-                const int a = parent(b);
-                const int id = __ldcg(p.page_table + (int64_t)a * p.max_pages + (s.x >> p.page_log2));
-                if (inside(id))
-                    copies = __ldcg(u.count + id) != __ldcg(u.writers + id) || __ldcg(u.first + id) != order(a, b);
-            }
-            x = (uint64_t)(pages(s.y) - pages(s.x) + copies) | (uint64_t)copies << 40;
-        }
         uint64_t sum;
-        const uint64_t at = block_scan(x, &sum, part);
-        if (some) {
-            u.slot[b].w = (int)(needs + (at & ((1ull << 40) - 1)));
-            u.copy[b] = copies ? (int)(copying + (at >> 40)) : -1;
-        }
+        block_scan(some ? x.needs((int)b0 + threadIdx.x) : 0, &sum, part);
         needs += sum & ((1ull << 40) - 1);
         copying += sum >> 40;
     }
-    const int w0 = warp_share(p0, p1, warp), w1 = warp_share(p0, p1, warp + 1);
-    auto is_free = [&](int i) { return __ldcg(u.count + i) <= 0; };
+    auto is_free = [&](int i) { return x.is_free(i); };
+    int held = 0;
+    for (int i = p0 + threadIdx.x; i < p1; i += kThreads) held += __ldcg(p.ref + i) <= 0;
     const int mine = each_of(w0, w1, is_free, [](int, int) {});
     uint64_t sum;
-    const int before = (int)(block_scan((lane == 0 ? mine : 0) | (uint64_t)held << 32, &sum, part) & 0xffffffffu);
-    const int at = p0 + __shfl_sync(~0u, before, 0);
-    each_of(w0, w1, is_free, [&](int i, int k) { u.free_ids[at + k] = i; });
+    const int before = (int)(uint32_t)block_scan((lane == 0 ? mine : 0) | (uint64_t)held << 32, &sum, part);
     if (threadIdx.x == 0) {
         said[0] = needs;
         said[1] = copying;
         said[2] = sum;
     }
     cluster_sync();
-
-    uint64_t told[3];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) told[k] = lane < kCtas ? cluster_read(&said[k], lane) : 0;
-    cluster_arrive();  // (waited for at the end: others may still read what this CTA says)
-    int64_t need = 0, copies = 0, free_n = 0, left = 0, need_before = 0, copies_before = 0, free_before[kCtas];
-#pragma unroll
+    int64_t need = 0, copies = 0, free_n = 0, left = 0, need_at = 0, copies_at = 0, free_at = 0;
     for (int c = 0; c < kCtas; ++c) {
-        const uint64_t x = __shfl_sync(~0u, told[0], c), y = __shfl_sync(~0u, told[1], c), z = __shfl_sync(~0u, told[2], c);
+        const uint64_t a = cluster_read(&said[0], c), b = cluster_read(&said[1], c), f = cluster_read(&said[2], c);
         if (c < rank) {
-            need_before += x;
-            copies_before += y;
+            need_at += a;
+            copies_at += b;
+            free_at += (uint32_t)f;
         }
-        free_before[c] = free_n;
-        need += x;
-        copies += y;
-        free_n += (uint32_t)z;
-        left += z >> 32;
+        need += a;
+        copies += b;
+        free_n += (uint32_t)f;
+        left += f >> 32;
     }
-    const bool enough = need <= free_n;
-    if (rank == 0 && threadIdx.x == 0)
-        *reinterpret_cast<int4*>(p.copies) = enough ? make_int4((int)copies, 0, (int)(free_n - need), 0)
-                                                    : make_int4(0, (int)min(need - free_n, (int64_t)INT32_MAX), (int)left, 0);
-    if (enough) {
-        auto free_page = [&](int64_t k) {  // the k-th free page
-            int c = 0;
-            int64_t first = 0;
-#pragma unroll
-            for (int i = 1; i < kCtas; ++i)
-                if (free_before[i] <= k) {
-                    c = i;
-                    first = free_before[i];
-                }
-            return __ldcg(u.free_ids + share(p.n_pages, c) + (k - first));
-        };
-        for (int64_t b0 = s0 + warp; b0 < s1; b0 += kWarps) {
-            const int b = (int)b0;
-            const int4 s = __ldcg(u.slot + b);
-            const int copy = __ldcg(u.copy + b), kept_n = pages(s.x), new_n = pages(s.y);
-            const bool other = parent(b) != b;
-            int32_t* row = p.page_table + (int64_t)b * p.max_pages;
-            const int32_t* had = other ? u.stage + (int64_t)b * p.max_pages : row;
-            int64_t k = need_before + s.w;
-            if (copy >= 0) {
-                const int from = __ldcg(had + kept_n - 1), to = free_page(k);
-                __syncwarp();  // (the row's entry is read before it is written)
-                if (lane == 0) {
-                    row[kept_n - 1] = to;
-                    *reinterpret_cast<int4*>(p.copies + 4 * (1 + copies_before + copy)) = make_int4(from, to, s.x & (page - 1), 0);
-                }
-                ++k;
+    cluster_arrive();  // (waited for at the end: others may still read what this CTA says)
+    if (rank == 0 && threadIdx.x == 0) {
+        x.head(need, free_n, copies, left);
+        u.totals[0] = need;
+        u.totals[1] = free_n;
+    }
+    if (need <= free_n) {
+        for (int64_t b0 = s0; b0 < s1; b0 += kThreads) {
+            const int b = (int)b0 + threadIdx.x;
+            const uint64_t n = b0 + threadIdx.x < s1 ? x.needs(b) : 0;
+            uint64_t all;
+            const uint64_t at = block_scan(n, &all, part);
+            if (b0 + threadIdx.x < s1) {
+                u.place[b].x = (int)(need_at + (at & ((1ull << 40) - 1)));
+                if (n >> 40) u.place[b].y = (int)(copies_at + (at >> 40));
             }
-            if (other) {
-#pragma unroll 4
-                for (int j = lane; j < kept_n - (copy >= 0); j += 32) row[j] = __ldcg(had + j);
-            }
-            for (int j = kept_n + lane; j < new_n; j += 32) row[j] = free_page(k + (j - kept_n));
-            for (int j = new_n + lane; j < s.z; j += 32) row[j] = -1;
-            if (lane == 0) p.seq_lens[b] = s.y;
+            need_at += all & ((1ull << 40) - 1);
+            copies_at += all >> 40;
         }
-        // the free pages up to `last` of this CTA's are taken
-        int64_t taken = need, here = 0;
-#pragma unroll
-        for (int c = 0; c < kCtas; ++c)
-            if (c == rank) {
-                taken -= free_before[c];
-                here = (c + 1 < kCtas ? free_before[c + 1 < kCtas ? c + 1 : c] : free_n) - free_before[c];
-            }
-        taken = min(taken, here);
-        const int last = taken > 0 ? __ldcg(u.free_ids + p0 + (taken - 1)) : -1;
-        for (int i = p0 + threadIdx.x; i < p1; i += kThreads) {
-            const int c = __ldcg(u.count + i), w = __ldcg(u.writers + i);
-            p.ref[i] = c <= 0 ? i <= last : c - w + (w > 0 && c == w);  // (where all write, one stays)
-        }
+        const int64_t at = free_at + __shfl_sync(~0u, before, 0);
+        if (at < need) each_of(w0, w1, is_free, [&](int i, int k) { u.free_ids[at + k] = i; });
     }
     cluster_wait();
 }
 
-// Live pages with ids from their number on go, lowest first, to the free ids below it, lowest first.
-__global__ void __launch_bounds__(kThreads) pages_compact_kernel(const PagesCompactParams p) {
+__global__ void __launch_bounds__(kStepThreads, 4) pages_write_kernel(const __grid_constant__ PagesUpdateParams p, const Books u) {
+    const Update<false> x{p, u};
+    begin_kernel(false);
+    const int64_t need = __ldcg(u.totals);
+    if (need > __ldcg(u.totals + 1)) return;
+    const int groups = gridDim.x * (kStepThreads / kStepLanes), group = blockIdx.x * (kStepThreads / kStepLanes) + threadIdx.x / kStepLanes;
+    for (int64_t b = group; b < p.n_seqs; b += groups) x.write((int)b, threadIdx.x % kStepLanes);
+    const int taken = need > 0 ? __ldcg(u.free_ids + need - 1) : -1;
+    for (int i = blockIdx.x * kStepThreads + threadIdx.x; i < p.n_pages; i += gridDim.x * kStepThreads) x.commit(i, taken);
+}
+
+// Live pages with ids from their number on go, lowest first, to the free ids below it, lowest first.  C CTAs each take a share of
+// the pages; who is live stays in shared memory, a bit for each page.
+template <int C>
+__global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_constant__ PagesCompactParams p) {
+    extern __shared__ uint32_t bits[];
     __shared__ uint64_t part[kWarps];
     __shared__ uint64_t said[2];  // to the cluster: its live pages; those that move | free ids that are filled << 32
-    const int rank = (int)cluster_rank(), warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int p0 = share(p.n_pages, rank), p1 = share(p.n_pages, rank + 1);
-    const int w0 = warp_share(p0, p1, warp), w1 = warp_share(p0, p1, warp + 1);
-    begin_kernel(false);
-    auto live = [&](int i) { return __ldcg(p.ref + i) > 0; };
-    const int mine = each_of(w0, w1, live, [](int, int) {});
-    uint64_t sum;
-    block_scan(lane == 0 ? mine : 0, &sum, part);
-    if (threadIdx.x == 0) said[0] = sum;
-    cluster_sync();
-    uint64_t x = lane < kCtas ? cluster_read(&said[0], lane) : 0;
+    const int rank = C > 1 ? (int)cluster_rank() : 0, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // (shares in whole words of bits)
+    const int words = (p.n_pages + 31) / 32;
+    const int c0 = share(0, words, rank, C), c1 = share(0, words, rank + 1, C);
+    const int v0 = share(c0, c1, warp, kWarps), v1 = share(c0, c1, warp + 1, kWarps);
+    const int w0 = 32 * v0, w1 = min(32 * v1, p.n_pages);
+    auto sync = [] {
+        if constexpr (C > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+    };
+    auto tell = [&](int k, uint64_t mine, uint64_t* before) {  // the sum over the CTAs, and over those before this one
+        if constexpr (C == 1) {
+            *before = 0;
+            return mine;
+        } else {
+            if (threadIdx.x == 0) said[k] = mine;
+            cluster_sync();
+            uint64_t all = lane < C ? cluster_read(&said[k], lane) : 0, less = lane < rank ? all : 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-    const int n_live = (int)x;
+            for (int o = 16; o > 0; o >>= 1) {
+                all += __shfl_xor_sync(~0u, all, o);
+                less += __shfl_xor_sync(~0u, less, o);
+            }
+            *before = less;
+            return all;
+        }
+    };
+    begin_kernel(false);
+    int mine = 0;
+#pragma unroll 8
+    for (int v = v0; v < v1; ++v) {
+        const int i = 32 * v + lane;
+        const uint32_t m = __ballot_sync(~0u, i < p.n_pages && __ldcg(p.ref + i) > 0);
+        if (lane == 0) bits[v - c0] = m;
+        mine += __popc(m);
+    }
+    __syncwarp();
+    uint64_t sum, less;
+    block_scan(lane == 0 ? mine : 0, &sum, part);
+    const int n_live = (int)tell(0, sum, &less);
+    auto live = [&](int i) { return bits[i / 32 - c0] >> (i % 32) & 1; };
     auto moves = [&](int i) { return i >= n_live && live(i); };
     auto filled = [&](int i) { return i < n_live && !live(i); };
     const uint64_t movers = each_of(w0, w1, moves, [](int, int) {}), holes = each_of(w0, w1, filled, [](int, int) {});
     uint64_t before = block_scan(lane == 0 ? movers | holes << 32 : 0, &sum, part);
-    before = __shfl_sync(~0u, before, 0);
-    if (threadIdx.x == 0) said[1] = sum;
-    cluster_sync();
-    x = lane < kCtas ? cluster_read(&said[1], lane) : 0;
-    uint64_t all = x, mine_at = lane < rank ? x : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        all += __shfl_xor_sync(~0u, all, o);
-        mine_at += __shfl_xor_sync(~0u, mine_at, o);
-    }
-    before += mine_at;
+    const uint64_t all = tell(1, sum, &less);
+    before = __shfl_sync(~0u, before, 0) + less;
     const int at_moves = (int)(uint32_t)before, at_holes = (int)(before >> 32);
     int4* rows = reinterpret_cast<int4*>(p.copies) + 1;
     if (rank == 0 && threadIdx.x == 0) rows[-1] = make_int4((int)(uint32_t)all, 0, p.n_pages - n_live, 0);
-    each_of(w0, w1, filled, [&](int i, int k) { rows[at_holes + k].y = i; });
-    for (int i = w0 + lane; i < w1; i += 32) {
-        const int c = __ldcg(p.ref + i);
-        if (c <= 0) {
-            p.new_id[i] = -1;
-            if (i >= n_live) p.ref_out[i] = 0;
-        } else if (i < n_live) {
-            p.new_id[i] = i;
-            p.ref_out[i] = c;
+    each_of(w0, w1, moves, [&](int i, int k) { rows[at_moves + k].x = i; });
+    // (loads before stores: ref_out may be ref, so the compiler keeps them in order)
+    for (int i0 = w0 + lane; i0 < w1; i0 += 8 * 32) {
+        int count[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) count[e] = i0 + 32 * e < w1 ? __ldcg(p.ref + i0 + 32 * e) : 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int i = i0 + 32 * e;
+            if (i >= w1) break;
+            if (count[e] <= 0) {
+                p.new_id[i] = -1;
+                if (i >= n_live) p.ref_out[i] = 0;
+            } else if (i < n_live) {
+                p.new_id[i] = i;
+                p.ref_out[i] = count[e];
+            }
         }
     }
-    cluster_sync();
-    // (from here on counts of pages that move are read, each by the warp that writes them: ref_out may be ref)
-    each_of(w0, w1, moves, [&](int i, int k) {
-        const int to = __ldcg(&rows[at_moves + k].y);
-        rows[at_moves + k].x = i;
-        rows[at_moves + k].z = 1 << p.page_log2;
-        rows[at_moves + k].w = 0;
-        p.new_id[i] = to;
-        p.ref_out[to] = __ldcg(p.ref + i);
-        p.ref_out[i] = 0;
-    });
+    sync();
+    // (from here on counts of pages that move are read, each by the one that then clears it)
+    int done = 0;
+    for (int i0 = w0; i0 < min(w1, n_live); i0 += 4 * 32) {
+        int k[4], from[4], count[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = i0 + 32 * e + lane;
+            const bool x = i < w1 && filled(i);
+            const uint32_t m = __ballot_sync(~0u, x);
+            k[e] = x ? at_holes + done + __popc(m & ((1u << lane) - 1)) : -1;
+            done += __popc(m);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) from[e] = k[e] >= 0 ? __ldcg(&rows[k[e]].x) : 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) count[e] = k[e] >= 0 ? __ldcg(p.ref + from[e]) : 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (k[e] < 0) continue;
+            const int i = i0 + 32 * e + lane;
+            rows[k[e]] = make_int4(from[e], i, 1 << p.page_log2, 0);
+            p.new_id[from[e]] = i;
+            p.ref_out[i] = count[e];
+            p.ref_out[from[e]] = 0;
+        }
+    }
 }
 
 // Entries of the page table by their pages' new ids (those that name no live page stay).
@@ -338,54 +519,86 @@ __global__ void __launch_bounds__(256) pages_rename_kernel(const PagesCompactPar
     }
 }
 
-// The pages' data.  A page of K, or of V, in pieces of kCopyThreads * kCopyAhead vectors of 16 bytes; those of tokens that the
-// copy leaves out are passed over.  Bound by HBM.
+// The pages' data.  A page of K, or of V, in pieces of kCopyThreads * AHEAD vectors of 16 bytes; those of tokens that the copy
+// leaves out are passed over.  Bound by HBM: 2322 pages of 256 KB (K and V) 180 us, 6.8 TB/s, 1.00 of a copy.  An SM has 64 KB
+// under way, in the fewer CTAs the larger a page is: with eight vectors to a thread, one CTA 216 us, two 182, three 199, four 192;
+// four vectors 191 to 207, streaming loads and stores 187.
 constexpr int kCopyThreads = 256;
-constexpr int kCopyAhead = 8;
+__host__ __device__ constexpr int copy_ctas(int ahead) { return ahead > 1 ? 16 / ahead : 8; }  // on an SM
 
-__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const PagesCopyParams p, int head_log2, int pieces) {
+template <int AHEAD>
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ PagesCopyParams p, int head_log2,
+                                                                                    int pieces) {
     begin_kernel(false);
     const int n = min(max(__ldcg(p.copies), 0), p.max_copies);
     const int64_t items = (int64_t)n * p.n_layers * 2 * pieces;
-    const int head = 1 << head_log2;                              // vectors of a page's head
+    const int head = 1 << head_log2;               // vectors of a page's head
     const int64_t page = (int64_t)p.Hkv << head_log2;
-    const int row_log2 = head_log2 - p.page_log2;                 // vectors of a token
+    const int row_log2 = head_log2 - p.page_log2;  // vectors of a token
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int piece = (int)(item % pieces);
-        const int64_t rest = item / pieces;
-        const int layer = (int)((rest >> 1) % p.n_layers);
-        const int4 c = __ldcg(reinterpret_cast<const int4*>(p.copies) + 1 + (rest >> 1) / p.n_layers);
+        const int64_t whole = item / pieces, copy = (whole >> 1) / p.n_layers;
+        const int layer = (int)((whole >> 1) - copy * p.n_layers);
+        const int4 c = __ldcg(reinterpret_cast<const int4*>(p.copies) + 1 + copy);
         if (c.x < 0 || c.x >= p.n_pages || c.y < 0 || c.y >= p.n_pages || c.x == c.y) continue;
-        uint4* pool = reinterpret_cast<uint4*>(static_cast<char*>(rest & 1 ? p.v_pages : p.k_pages) + layer * p.layer_bytes);
+        uint4* pool = reinterpret_cast<uint4*>(static_cast<char*>(whole & 1 ? p.v_pages : p.k_pages) + layer * p.layer_bytes);
         const uint4* from = pool + c.x * page;
         uint4* to = pool + c.y * page;
-        const int64_t v0 = (int64_t)piece * (kCopyThreads * kCopyAhead) + threadIdx.x;
+        const int64_t v0 = (item - whole * pieces) * (kCopyThreads * AHEAD) + threadIdx.x;
         auto wanted = [&](int64_t v) { return v < page && (int)(v & (head - 1)) >> row_log2 < c.z; };
-        uint4 w[kCopyAhead];
+        uint4 w[AHEAD];
 #pragma unroll
-        for (int e = 0; e < kCopyAhead; ++e)
-            if (wanted(v0 + e * kCopyThreads)) w[e] = __ldcs(from + v0 + e * kCopyThreads);
+        for (int e = 0; e < AHEAD; ++e)
+            if (wanted(v0 + e * kCopyThreads)) w[e] = __ldcg(from + v0 + e * kCopyThreads);
 #pragma unroll
-        for (int e = 0; e < kCopyAhead; ++e)
-            if (wanted(v0 + e * kCopyThreads)) __stcs(to + v0 + e * kCopyThreads, w[e]);
+        for (int e = 0; e < AHEAD; ++e)
+            if (wanted(v0 + e * kCopyThreads)) to[v0 + e * kCopyThreads] = w[e];
     }
+}
+
+template <int AHEAD>
+cudaError_t launch_copy(const PagesCopyParams& p, int head_log2, cudaStream_t stream) {
+    const int64_t per = kCopyThreads * AHEAD, pieces = (((int64_t)p.Hkv << head_log2) + per - 1) / per;
+    const int64_t items = (int64_t)p.max_copies * p.n_layers * 2 * pieces;
+    return launch_dependent(pages_copy_kernel<AHEAD>, dim3((unsigned)std::min<int64_t>(items, copy_ctas(AHEAD) * 152)), kCopyThreads, 0,
+                            stream, p, head_log2, (int)pieces);
 }
 
 }  // namespace
 
 size_t pages_update_workspace(int n_seqs, int max_pages, int n_pages) {
-    UpdateSpace u;
+    Books u;
     return layout(n_seqs, max_pages, n_pages, nullptr, &u);
 }
 
 cudaError_t launch_pages_update(const PagesUpdateParams& p, cudaStream_t stream) {
-    UpdateSpace u;
+    Books u;
     layout(p.n_seqs, p.max_pages, p.n_pages, static_cast<char*>(p.ws), &u);
-    return launch_clusters(pages_update_kernel, 1, kCtas, kThreads, 0, stream, p, u);
+    if (one_cta(p)) {
+        cudaError_t e = allow_smem<pages_update_kernel>((int)books_bytes(kOneSeqs, kOnePages));
+        if (e != cudaSuccess) return e;
+        return launch_dependent(pages_update_kernel, dim3(1), kThreads, books_bytes(p.n_seqs, p.n_pages), stream, p, u.stage);
+    }
+    const auto ctas = [](int64_t threads) { return dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>((threads + 255) / 256, 8 * 152))); };
+    cudaError_t e = launch_dependent(pages_init_kernel, ctas(p.n_pages), kStepThreads, 0, stream, p, u);
+    if (e == cudaSuccess) e = launch_dependent(pages_count_kernel, ctas((int64_t)kStepLanes * p.n_seqs), kStepThreads, 0, stream, p, u);
+    if (e == cudaSuccess) e = launch_clusters(pages_number_kernel, 1, kCtas, kThreads, 0, stream, p, u);
+    const int64_t threads = std::max<int64_t>((int64_t)kStepLanes * p.n_seqs, p.n_pages);
+    if (e == cudaSuccess) e = launch_dependent(pages_write_kernel, ctas(threads), kStepThreads, 0, stream, p, u);
+    return e;
 }
 
 cudaError_t launch_pages_compact(const PagesCompactParams& p, cudaStream_t stream) {
-    cudaError_t e = launch_clusters(pages_compact_kernel, 1, kCtas, kThreads, 0, stream, p);
+    // (one CTA up to so many pages: 5.0 us for 125 pages, 12.3 for 9104; a cluster of eight 7.2 and 8.8)
+    constexpr int kOne = 4096;
+    cudaError_t e;
+    if (p.n_pages <= kOne) {
+        e = launch_dependent(pages_compact_kernel<1>, dim3(1), kThreads, ((size_t)p.n_pages + 31) / 32 * 4, stream, p);
+    } else {
+        e = allow_smem<pages_compact_kernel<kCtas>>((1 << 23) / 8 / kCtas + 4);
+        const int words = (p.n_pages + 31) / 32;
+        if (e == cudaSuccess)
+            e = launch_clusters(pages_compact_kernel<kCtas>, 1, kCtas, kThreads, 4 * (size_t)((words + kCtas - 1) / kCtas), stream, p);
+    }
     const int64_t n = (int64_t)p.n_seqs * p.max_pages;
     if (e != cudaSuccess || n == 0) return e;
     return launch_dependent(pages_rename_kernel, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 8 * 152)), 256, 0, stream, p);
@@ -395,10 +608,11 @@ cudaError_t launch_pages_copy(const PagesCopyParams& p, cudaStream_t stream) {
     int row_log2 = 0;
     while (16 << row_log2 < p.row_bytes) ++row_log2;
     const int head_log2 = row_log2 + p.page_log2;
-    const int64_t per = kCopyThreads * kCopyAhead, pieces = (((int64_t)p.Hkv << head_log2) + per - 1) / per;
-    const int64_t items = (int64_t)p.max_copies * p.n_layers * 2 * pieces;
-    return launch_dependent(pages_copy_kernel, dim3((unsigned)std::min<int64_t>(items, 6 * 152)), kCopyThreads, 0, stream, p,
-                            head_log2, (int)pieces);
+    const int64_t page = (int64_t)p.Hkv << head_log2;
+    return page <= kCopyThreads       ? launch_copy<1>(p, head_log2, stream)
+           : page <= 2 * kCopyThreads ? launch_copy<2>(p, head_log2, stream)
+           : page <= 4 * kCopyThreads ? launch_copy<4>(p, head_log2, stream)
+                                      : launch_copy<8>(p, head_log2, stream);
 }
 
 }  // namespace usp

@@ -583,7 +583,7 @@ usp_status usp_kv_append_axes(const usp_cache* c, int n_tokens, const void* q, i
  * read on the device (a captured graph replays with new values), results do
  * not depend on the run. */
 
-/* Bytes of workspace usp_pages_update needs (20 per page, 24 per slot and 4 per
+/* Bytes of workspace usp_pages_update needs (12 per page, 32 per slot and 4 per
  * entry of the table); 0 for an invalid cache. */
 size_t usp_pages_update_workspace_size(const usp_cache* c);
 
@@ -610,7 +610,7 @@ size_t usp_pages_update_workspace_size(const usp_cache* c);
  * were refused are dropped by keep, say by usp_verify_drafts' keep_lens.)
  * ws: at least usp_pages_update_workspace_size(c) bytes, 256-byte aligned,
  * contents on entry irrelevant; calls that can overlap on the GPU need one
- * each.  n_pages <= 2^30. */
+ * each.  n_pages <= 2^23. */
 usp_status usp_pages_update(const usp_cache* c, const int32_t* parent, const int32_t* keep, const int32_t* grow,
                             int32_t* seq_lens, int32_t* page_table, int32_t* ref, int32_t* copies, void* ws, size_t ws_bytes,
                             usp_stream stream);
@@ -622,7 +622,7 @@ usp_status usp_pages_update(const usp_cache* c, const int32_t* parent, const int
  * counts afterwards; page_table_out the table with new numbers (entries that
  * name no page in use stay as they are).  page_table_out may be page_table
  * and ref_out may be ref.  copies has n_pages/2 rows after row 0.
- * n_pages <= 2^30. */
+ * n_pages <= 2^23. */
 usp_status usp_pages_compact(const usp_cache* c, const int32_t* page_table, const int32_t* ref, int32_t* page_table_out,
                              int32_t* ref_out, int32_t* new_id, int32_t* copies, usp_stream stream);
 

@@ -283,7 +283,7 @@ def test_pages_refusals(lib):
         assert _status(f, _c(n_pages=-1)) == 1 and _status(f, _c(page_size=24)) == 2 and _status(f, _c(d=96)) == 2
         assert _status(f, copies=FAKE + 8) == 3 and _status(f, copies=0) == 3
     for f in (update, compact):
-        assert _status(f, _c(n_pages=(1 << 30) + 1, Hq=1, Hkv=1)) == 2
+        assert _status(f, _c(n_pages=(1 << 23) + 1, Hq=1, Hkv=1)) == 2
     for name in ("lens", "table", "ref"):
         assert _status(update, **{name: 0}) == 3
     for name in ("lens", "table", "ref", "parent", "keep", "grow"):
@@ -542,7 +542,8 @@ def _any_step(rng, B, cap, most):
 @pytest.mark.gpu
 @pytest.mark.parametrize("B,mp,page,n", [(1, 1, 16, 1), (1, 4, 16, 3), (5, 6, 16, 21), (9, 3, 256, 40), (33, 40, 32, 700),
                                          (70, 100, 64, 4097), (1100, 5, 16, 3000), (3, 2000, 16, 20001), (6, 7, 16, 0),
-                                         (4, 0, 16, 5)])
+                                         (4, 0, 16, 5), (300, 1000, 16, 9000), (1024, 9, 16, 16384), (2500, 3, 16, 100),
+                                         (2500, 4, 16, 6000)])
 def test_pages_update(usp, B, mp, page, n):
     guard = Guarded()
     pool = Pool(usp, guard, B, mp, page, n, seed=B)
@@ -565,7 +566,7 @@ def test_pages_update(usp, B, mp, page, n):
                 pool.lens[empty[0]] = -9
             pool.put()
     if n and mp:
-        assert lacking < 25 and (copies > 0 or B == 1)
+        assert lacking < 25 and (copies > 0 or B == 1 or n < B)
 
 
 @pytest.mark.gpu
@@ -639,7 +640,8 @@ def test_sequences_keep_their_tokens(usp, dtype, Hkv, d, page):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("n,B,mp,live", [(1, 1, 1, 1.0), (2, 1, 2, 0.5), (300, 12, 31, 0.6), (4097, 50, 70, 0.3), (40000, 3, 7, 0.9),
-                                         (1000, 4, 4, 0.0), (1000, 300, 3, 1.0), (0, 2, 2, 0.0)])
+                                         (1000, 4, 4, 0.0), (1000, 300, 3, 1.0), (0, 2, 2, 0.0),
+                                         (70001, 9, 50, 0.5), (300000, 2, 9, 0.2)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_pages_compact(usp, n, B, mp, live, in_place):
     import torch
