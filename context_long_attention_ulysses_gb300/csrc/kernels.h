@@ -215,6 +215,7 @@ struct PagesCompactParams {
     const int32_t *page_table, *ref;
     int32_t *page_table_out, *ref_out, *new_id, *copies;
     int n_seqs, max_pages, n_pages, page_log2;
+    bool rename;  // (set by the launcher: the table's entries in the first kernel)
 };
 cudaError_t launch_pages_compact(const PagesCompactParams& p, cudaStream_t stream);
 struct PagesCopyParams {

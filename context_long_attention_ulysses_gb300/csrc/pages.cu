@@ -112,7 +112,6 @@ __host__ __device__ inline size_t layout(int n_seqs, int max_pages, int n_pages,
 // The steps, for PagesUpdateParams p and Books u that more than one CTA uses (ONE: one CTA, the books in its shared memory).
 template <bool ONE>
 struct Update {
-    static constexpr int kRowLanes = ONE ? 8 : 32;  // lanes to a row (one CTA has few warps, and rows that are short or few)
     const PagesUpdateParams& p;
     const Books u;
 
@@ -150,21 +149,22 @@ struct Update {
         if (inside(id)) atomicAdd(u.count + id, n);
     }
 
-    // f(j, x[j], y[j]) for the places [from, max(nx, ny)) of two rows, -1 behind the first nx and ny, by kRowLanes lanes.
+    // f(j, x[j], y[j]) for the places [from, max(nx, ny)) of two rows, -1 behind the first nx and ny, by `lanes` threads.
     template <typename F>
-    __device__ __forceinline__ static void entries(const int32_t* x, int nx, const int32_t* y, int ny, int from, int lane, F&& f) {
+    __device__ __forceinline__ static void entries(const int32_t* x, int nx, const int32_t* y, int ny, int from, int lane, int lanes,
+                                                   F&& f) {
         const int end = max(nx, ny);
-        for (int j = from + lane; j < end; j += 8 * kRowLanes) {
+        for (int j = from + lane; j < end; j += 8 * lanes) {
             int a[8], b[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int i = j + e * kRowLanes;
+                const int i = j + e * lanes;
                 a[e] = i < nx ? __ldcg(x + i) : -1;
                 b[e] = i < ny ? __ldcg(y + i) : -1;
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (j + e * kRowLanes < end) f(j + e * kRowLanes, a[e], b[e]);
+                if (j + e * lanes < end) f(j + e * lanes, a[e], b[e]);
         }
     }
 
@@ -192,17 +192,22 @@ struct Update {
                 if (kept_n + j < old_n) add(__ldcg(row(b) + kept_n + j), -1);
         }
     }
-    // The rest of what slot b gives up, and what it takes over, by kRowLanes lanes.  (Pages that it holds in the same place
+    // Entries of the table that move() and write() read for slot b.
+    __device__ __forceinline__ int reads(int b) const {
+        const int4 s = get(u.slot + b);
+        return get(u.place + b).z & kSlotOther ? max(s.z, pages(s.x)) : s.z - pages(s.x);
+    }
+    // The rest of what slot b gives up, and what it takes over, by `lanes` threads.  (Pages that it holds in the same place
     // before and after, as when the same prompt is forked again, are left alone.)
-    __device__ __forceinline__ void move(int b, int lane) const {
+    __device__ __forceinline__ void move(int b, int lane, int lanes) const {
         const int4 s = get(u.slot + b), at = get(u.place + b);
         const int kept_n = pages(s.x);
         if (!(at.z & kSlotOther)) {
-            entries(row(b), s.z, nullptr, 0, kept_n + 2, lane, [&](int, int id, int) { add(id, -1); });
+            entries(row(b), s.z, nullptr, 0, kept_n + 2, lane, lanes, [&](int, int id, int) { add(id, -1); });
             return;
         }
         int32_t* const to = at.z & kSlotStaged ? stage(b) : nullptr;
-        entries(row(b), s.z, kept_n > 0 ? row(at.w) : nullptr, kept_n, 0, lane, [&](int j, int old, int id) {
+        entries(row(b), s.z, kept_n > 0 ? row(at.w) : nullptr, kept_n, 0, lane, lanes, [&](int j, int old, int id) {
             if (old != id) {
                 add(old, -1);
                 add(id, 1);
@@ -218,8 +223,8 @@ struct Update {
         return (uint64_t)(pages(s.y) - pages(s.x) + copies) | (uint64_t)copies << 40;
     }
 
-    // Slot b, by kRowLanes lanes.
-    __device__ __forceinline__ void write(int b, int lane) const {
+    // Slot b, by `lanes` threads.
+    __device__ __forceinline__ void write(int b, int lane, int lanes) const {
         const int4 s = get(u.slot + b), at = get(u.place + b);
         const int kept_n = pages(s.x), new_n = pages(s.y);
         int32_t* to = row(b);
@@ -233,11 +238,11 @@ struct Update {
         const bool ends_inside = s.x & ((1 << p.page_log2) - 1);
         if (at.z & kSlotOther) {
             const int32_t* from = at.z & kSlotStaged ? stage(b) : slot_exists(at.w) ? row(at.w) : to;
-            entries(from, kept_n - ends_inside, nullptr, 0, 0, lane, [&](int j, int id, int) { to[j] = id; });
+            entries(from, kept_n - ends_inside, nullptr, 0, 0, lane, lanes, [&](int j, int id, int) { to[j] = id; });
         }
         if (lane == 0 && ends_inside && (at.y >= 0 || (at.z & kSlotOther))) to[kept_n - 1] = last;
-        for (int j = kept_n + lane; j < new_n; j += kRowLanes) to[j] = get(u.free_ids + k + (j - kept_n));
-        for (int j = new_n + lane; j < s.z; j += kRowLanes) to[j] = -1;
+        for (int j = kept_n + lane; j < new_n; j += lanes) to[j] = get(u.free_ids + k + (j - kept_n));
+        for (int j = new_n + lane; j < s.z; j += lanes) to[j] = -1;
         if (lane == 0) p.seq_lens[b] = s.y;
     }
 
@@ -257,6 +262,8 @@ struct Update {
 __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_constant__ PagesUpdateParams p, int32_t* stage) {
     extern __shared__ int4 smem[];
     __shared__ uint64_t part[kWarps];
+    __shared__ uint16_t long_rows[kOneSeqs];  // (in any order: counts are added up, rows written by themselves)
+    __shared__ int n_long;
     Books u;
     u.slot = smem;
     u.place = u.slot + p.n_seqs;
@@ -268,14 +275,24 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     begin_kernel(false);
     const int held = x.init(threadIdx.x, kThreads);
+    if (threadIdx.x == 0) n_long = 0;
     __syncthreads();
     // (one slot to a thread: kOneSeqs of them at most)
     const int b = threadIdx.x;
     if (b < p.n_seqs) x.enter(b);
     __syncthreads();
-    constexpr int kLanes = Update<true>::kRowLanes;
-    const int group = threadIdx.x / kLanes, row_lane = threadIdx.x % kLanes;
-    for (int s = group; s < p.n_seqs; s += kThreads / kLanes) x.move(s, row_lane);
+    // rows are short, or many, or both: each has its share of the threads, but 8; a long one all of them, after the others
+    const int lanes = max(8, kThreads >> (32 - __clz(max(p.n_seqs, 1) - 1)));
+    const int group = threadIdx.x / lanes, row_lane = threadIdx.x % lanes;
+    auto is_long = [&](int s) { return x.reads(s) > 64 * lanes; };
+    for (int s = group; s < p.n_seqs; s += kThreads / lanes) {
+        if (!is_long(s))
+            x.move(s, row_lane, lanes);
+        else if (row_lane == 0)
+            long_rows[atomicAdd(&n_long, 1)] = (uint16_t)s;
+    }
+    __syncthreads();
+    for (int k = 0; k < n_long; ++k) x.move(long_rows[k], threadIdx.x, kThreads);
     __syncthreads();
     const uint64_t mine = b < p.n_seqs ? x.needs(b) : 0;
     const int w0 = share(0, p.n_pages, warp, kWarps), w1 = share(0, p.n_pages, warp + 1, kWarps);
@@ -294,14 +311,16 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
     const int first = (int)(uint32_t)__shfl_sync(~0u, before, 0);
     if (first < need) each_of(w0, w1, is_free, [&](int i, int k) { u.free_ids[first + k] = i; });
     __syncthreads();
-    for (int s = group; s < p.n_seqs; s += kThreads / kLanes) x.write(s, row_lane);
+    for (int s = group; s < p.n_seqs; s += kThreads / lanes)
+        if (!is_long(s)) x.write(s, row_lane, lanes);
+    for (int k = 0; k < n_long; ++k) x.write(long_rows[k], threadIdx.x, kThreads);
     const int taken = need > 0 ? u.free_ids[need - 1] : -1;
     for (int i = threadIdx.x; i < p.n_pages; i += kThreads) x.commit(i, taken);
 }
 
 // The same, a launch for each step, with the books in the workspace.
 constexpr int kStepThreads = 256;
-constexpr int kStepLanes = Update<false>::kRowLanes;
+constexpr int kStepLanes = 32;  // to a row
 
 __global__ void __launch_bounds__(kStepThreads) pages_init_kernel(const __grid_constant__ PagesUpdateParams p, const Books u) {
     const Update<false> x{p, u};
@@ -318,7 +337,7 @@ __global__ void __launch_bounds__(kStepThreads) pages_count_kernel(const __grid_
     for (int64_t b = group; b < p.n_seqs; b += groups) {
         if (lane == 0) x.enter((int)b);
         __syncwarp();
-        x.move((int)b, lane);
+        x.move((int)b, lane, kStepLanes);
     }
 }
 
@@ -396,13 +415,28 @@ __global__ void __launch_bounds__(kStepThreads, 4) pages_write_kernel(const __gr
     const int64_t need = __ldcg(u.totals);
     if (need > __ldcg(u.totals + 1)) return;
     const int groups = gridDim.x * (kStepThreads / kStepLanes), group = blockIdx.x * (kStepThreads / kStepLanes) + threadIdx.x / kStepLanes;
-    for (int64_t b = group; b < p.n_seqs; b += groups) x.write((int)b, threadIdx.x % kStepLanes);
+    for (int64_t b = group; b < p.n_seqs; b += groups) x.write((int)b, threadIdx.x % kStepLanes, kStepLanes);
     const int taken = need > 0 ? __ldcg(u.free_ids + need - 1) : -1;
     for (int i = blockIdx.x * kStepThreads + threadIdx.x; i < p.n_pages; i += gridDim.x * kStepThreads) x.commit(i, taken);
 }
 
+// Entries of the page table by their pages' new ids (those that name no live page stay): thread `at` of n.
+__device__ __forceinline__ void rename(const PagesCompactParams& p, int64_t at, int64_t n) {
+    const int64_t entries = (int64_t)p.n_seqs * p.max_pages;
+    for (; at < entries; at += 8 * n) {
+        int id[8], to[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) id[e] = at + e * n < entries ? __ldcg(p.page_table + at + e * n) : -1;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) to[e] = id[e] >= 0 && id[e] < p.n_pages ? __ldcg(p.new_id + id[e]) : -1;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (at + e * n < entries) p.page_table_out[at + e * n] = to[e] >= 0 ? to[e] : id[e];
+    }
+}
+
 // Live pages with ids from their number on go, lowest first, to the free ids below it, lowest first.  C CTAs each take a share of
-// the pages; who is live stays in shared memory, a bit for each page.
+// the pages; who is live stays in shared memory, a bit for each page.  One CTA also renames the entries of a small table.
 template <int C>
 __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_constant__ PagesCompactParams p) {
     extern __shared__ uint32_t bits[];
@@ -506,17 +540,16 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
             p.ref_out[from[e]] = 0;
         }
     }
+    if constexpr (C == 1) {
+        if (!p.rename) return;
+        __syncthreads();
+        rename(p, threadIdx.x, kThreads);
+    }
 }
 
-// Entries of the page table by their pages' new ids (those that name no live page stay).
-__global__ void __launch_bounds__(256) pages_rename_kernel(const PagesCompactParams p) {
+__global__ void __launch_bounds__(256) pages_rename_kernel(const __grid_constant__ PagesCompactParams p) {
     begin_kernel(false);
-    const int64_t n = (int64_t)p.n_seqs * p.max_pages;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
-        const int id = __ldcg(p.page_table + i);
-        const int to = id >= 0 && id < p.n_pages ? __ldcg(p.new_id + id) : -1;
-        p.page_table_out[i] = to >= 0 ? to : id;
-    }
+    rename(p, blockIdx.x * 256ll + threadIdx.x, gridDim.x * 256ll);
 }
 
 // The pages' data.  A page of K, or of V, in pieces of kCopyThreads * AHEAD vectors of 16 bytes; those of tokens that the copy
@@ -587,21 +620,23 @@ cudaError_t launch_pages_update(const PagesUpdateParams& p, cudaStream_t stream)
     return e;
 }
 
-cudaError_t launch_pages_compact(const PagesCompactParams& p, cudaStream_t stream) {
+cudaError_t launch_pages_compact(const PagesCompactParams& params, cudaStream_t stream) {
     // (one CTA up to so many pages: 5.0 us for 125 pages, 12.3 for 9104; a cluster of eight 7.2 and 8.8)
     constexpr int kOne = 4096;
+    PagesCompactParams p = params;
+    const int64_t entries = (int64_t)p.n_seqs * p.max_pages;
+    p.rename = p.n_pages <= kOne && entries <= 8 * kThreads;  // (one round of that CTA; a launch for it 2 us more)
+    const int words = (p.n_pages + 31) / 32;
     cudaError_t e;
     if (p.n_pages <= kOne) {
-        e = launch_dependent(pages_compact_kernel<1>, dim3(1), kThreads, ((size_t)p.n_pages + 31) / 32 * 4, stream, p);
+        e = launch_dependent(pages_compact_kernel<1>, dim3(1), kThreads, 4 * (size_t)words, stream, p);
     } else {
         e = allow_smem<pages_compact_kernel<kCtas>>((1 << 23) / 8 / kCtas + 4);
-        const int words = (p.n_pages + 31) / 32;
         if (e == cudaSuccess)
             e = launch_clusters(pages_compact_kernel<kCtas>, 1, kCtas, kThreads, 4 * (size_t)((words + kCtas - 1) / kCtas), stream, p);
     }
-    const int64_t n = (int64_t)p.n_seqs * p.max_pages;
-    if (e != cudaSuccess || n == 0) return e;
-    return launch_dependent(pages_rename_kernel, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 8 * 152)), 256, 0, stream, p);
+    if (e != cudaSuccess || entries == 0 || p.rename) return e;
+    return launch_dependent(pages_rename_kernel, dim3((unsigned)std::min<int64_t>((entries + 255) / 256, 8 * 152)), 256, 0, stream, p);
 }
 
 cudaError_t launch_pages_copy(const PagesCopyParams& p, cudaStream_t stream) {

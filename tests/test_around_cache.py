@@ -585,6 +585,28 @@ def test_pages_update_when_pages_lack(usp):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B", [4, 70, 1000])
+def test_pages_update_long_rows_among_short(usp, B):
+    """Conversations of thousands of pages among short ones: grown, forked, reordered (rows put aside), truncated, freed."""
+    guard = Guarded()
+    mp = 8000 if B < 70 else 900
+    pool = Pool(usp, guard, B, mp, 16, 16000, seed=B)
+    most, own = mp * 16, np.arange(B)
+    grow = np.full(B, 20)
+    grow[1], grow[3] = most - 5, most // 2 + 3
+    assert pool.step(None, None, grow)[0][1] == 0
+    parent = own.copy()
+    parent[0], parent[2] = 1, 3
+    assert pool.step(parent, None, np.ones(B, int))[0][0] == 1 + 1   # (20, most - 5 and most / 2 + 3 tokens all end inside)
+    parent[[0, 1, 2, 3]] = [3, 0, 1, 2]                    # all change places
+    pool.step(parent, np.full(B, most - 100), np.zeros(B, int))
+    pool.step(parent, None, np.full(B, 3))
+    pool.step(None, np.where(own % 2, 7, most), np.zeros(B, int))
+    pool.step(None, np.zeros(B, int), None)
+    assert (pool.ref == 0).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,Hkv,d,page", [("bf16", 2, 64, 16), ("f32", 3, 128, 32), ("bf16", 8, 128, 64)])
 def test_sequences_keep_their_tokens(usp, dtype, Hkv, d, page):
     """Forks, reorderings, refused tokens and compactions at random, with their copies, and new tokens written: what each slot
@@ -1019,3 +1041,35 @@ def test_speculative_decoding_never_waits_for_the_host(usp, dtype):
     o, _ = usp.paged_attention(c, q[last].contiguous(), kp2, vp2, table2, lens2, q_start, n)
     torch.cuda.synchronize()
     assert torch.equal(o, o_last) and torch.isfinite(o.float()).all() and o.float().abs().max() > 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inter", [False, True])
+def test_a_training_step_with_rotation(usp, orc, inter):
+    """Rotation, all-to-all, attention, back, its backward and the rotation's: outputs and gradients of the unrotated q and k
+    against the float64 oracle, on the rotated values as rounded, to the attention's own tolerances."""
+    import torch
+    from tests.helpers import f64, from_seq, gen, rel_fro, to_dev, to_host, to_seq
+    B, Hq, Hkv, N, d, P = 1, 4, 2, 256, 64, 2
+    p = usp.Problem(B=B, Hq=Hq, Hkv=Hkv, N=N, d=d, P=P)
+    r = usp.Rotary.sections((12, 10, 10), cycled=True, interleaved=inter)
+    q, k, v, dO = gen((B, Hq, N, d), 0), gen((B, Hkv, N, d), 1), gen((B, Hkv, N, d), 2), gen((B, Hq, N, d), 3)
+    t = np.arange(N)
+    pos = np.stack([t // 64, t // 8 % 8, t % 8]).astype(np.int32)
+    dpos = _dev(pos.reshape(3, P, 1, N // P))                # (token n of the sequence: rank n / (N/P), place n % (N/P))
+    f = _freq(32)
+    qr, kr = usp.rotary_embed(p, r, to_dev(to_seq(q, P)), to_dev(to_seq(k, P)), dpos, _dev(f))
+    o, saved = usp.ulysses_attention_fwd(p, qr, kr, to_dev(to_seq(v, P)))
+    dqr, dkr, dv = usp.ulysses_attention_bwd(p, saved, to_dev(to_seq(dO, P)))
+    dq, dk = usp.rotary_embed(p, r, dqr, dkr, dpos, _dev(f), inverse=True)
+    torch.cuda.synchronize()
+    assert usp.usp_device_status() == 0
+    logical = lambda x: f64(from_seq(to_host(x)))  # noqa: E731
+    rows = lambda x, inverse=False: ref_rotate(x[0].transpose(1, 0, 2), pos, r.axis, f, inter, inverse)[0].transpose(1, 0, 2)[None]  # noqa: E731
+    assert rel_fro(logical(qr), rows(f64(q))) < 2.0 ** -8 and rel_fro(logical(kr), rows(f64(k))) < 2.0 ** -8
+    qh, kh = from_seq(to_host(qr)), from_seq(to_host(kr))
+    want_o, _ = orc.attn_rows(qh, kh, v, causal=True)
+    wq, wk, wv, _, _ = orc.attn_bwd_full(qh, kh, v, dO, causal=True)
+    assert rel_fro(logical(o), want_o) < 1e-2
+    for got, want in ((dq, rows(wq, True)), (dk, rows(wk, True)), (dv, wv)):
+        assert rel_fro(logical(got), want) < 2e-2
