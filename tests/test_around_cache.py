@@ -1073,3 +1073,36 @@ def test_a_training_step_with_rotation(usp, orc, inter):
     assert rel_fro(logical(o), want_o) < 1e-2
     for got, want in ((dq, rows(wq, True)), (dk, rows(wk, True)), (dv, wv)):
         assert rel_fro(logical(got), want) < 2e-2
+
+
+@pytest.mark.gpu
+def test_rows_beyond_32_bit_offsets(usp):
+    """Probabilities and queries whose elements lie beyond 2^31 of their tensors."""
+    import torch
+    V, rng = 131072, np.random.default_rng(1)
+    far = (1 << 31) // V + 3
+    x = _drafts(rng, [4], 600, "bf16")
+    tg, dr = (torch.empty((far + 4, V), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for big, small in ((tg, x["tg"]), (dr, x["dr"])):
+        big[far:] = 0
+        big[far:, V - 600:] = small
+    tokens, u = torch.zeros(far + 4, dtype=torch.int32, device="cuda"), torch.zeros(far + 4, device="cuda")
+    tokens[far:], u[far:] = _dev(x["tokens"]) + (V - 600), _dev(x["u"])
+    got = usp.verify_drafts(tg, dr, tokens, u, torch.tensor([far, far + 4], dtype=torch.int32, device="cuda"), _dev(x["lens"]))
+    torch.cuda.synchronize()
+    want = ref_verify(x["target"], x["draft"], x["tokens"], x["u"], x["q_start"], x["lens"])
+    want[1] += V - 600
+    assert np.array_equal(np.stack([g.cpu().numpy() for g in got]), want)
+    del tg, dr
+    T, gap = 40, 1 << 26
+    big = torch.empty(T * gap, dtype=torch.bfloat16, device="cuda")
+    q = big.as_strided((1, 1, T, 2, 64), (0, 0, gap, 64, 1))
+    q.copy_(torch.randn((1, 1, T, 2, 64), generator=torch.Generator().manual_seed(0)))
+    r, p = usp.Rotary.sections((16, 16)), usp.Problem(1, 2, 1, T, 64, 1)
+    pos = torch.arange(2 * T, dtype=torch.int32, device="cuda").view(2, 1, 1, T)
+    want, _ = usp.rotary_embed(p, r, q.contiguous(), None, pos, _dev(_freq(32)))
+    usp.usp_rotary_embed(p, r, q, None, pos, _dev(_freq(32)), q, None)
+    torch.cuda.synchronize()
+    assert torch.equal(q.contiguous(), want)
+    del big, q
+    torch.cuda.empty_cache()
