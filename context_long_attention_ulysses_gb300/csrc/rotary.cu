@@ -137,10 +137,11 @@ cudaError_t launch_t(const RotaryParams& p, int items, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_sized(const RotaryParams& p, cudaStream_t s) {
-    // What the SMs hold at once goes in one round, everything under way together; more of it streams best through small CTAs of
-    // several rounds, many to an SM (131072 tokens: 391 us against 453 in one round; 4097 tokens of 8 heads: 5.2 against 4.4).
+    // Little work goes in one round, everything that the SMs hold under way together; more of it streams best through small CTAs of
+    // several rounds, many to an SM, and the largest with two rounds' more work to each (tokens of 32 query and 8 KV heads of 128
+    // bf16 values, the three ways: 3000 of them 11.8, 12.7 and 18.2 us, 8000 31.8, 29.1 and 30.9, 131072 453, 400 and 391).
     const int64_t items = (int64_t)p.n_tokens * ((p.q ? p.Hq : 0) + (p.k ? p.Hkv : 0)) * p.d / (2 * Vec<T>::N);
-    return items <= 10 * 152 * 384 ? launch_t<T, 96, 4>(p, 384, s) : launch_t<T, 64, 3>(p, 640, s);
+    return items <= 3 << 19 ? launch_t<T, 96, 4>(p, 384, s) : launch_t<T, 64, 3>(p, items <= 8 << 20 ? 384 : 640, s);
 }
 
 }  // namespace
