@@ -10,7 +10,10 @@ The helpers ``ulysses_attention_fwd``/``ulysses_attention_bwd`` and
 ``ring_attention_fwd`` chain those calls the way one sequence-parallel
 attention layer does (all-to-all, attention, all-to-all back) and allocate
 their outputs with torch.  ``kv_append``, ``paged_attention`` and
-``prefix_attention`` serve from a paged key/value cache (:class:`Cache`).
+``prefix_attention`` serve from a paged key/value cache (:class:`Cache`);
+``rotary_embed`` and ``kv_append_axes`` rotate by positions on several axes
+(:class:`Rotary`), ``pages_update``, ``pages_copy`` and ``pages_compact`` move
+a cache's pages, ``verify_drafts`` judges drafted tokens.
 """
 from __future__ import annotations
 
