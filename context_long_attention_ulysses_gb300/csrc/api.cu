@@ -1417,7 +1417,7 @@ usp_status usp_rotary_embed(const usp_problem* p, const usp_rotary* r, int inver
     a.q = q; a.k = k; a.q_out = q_out; a.k_out = k_out;
     a.q_stride = q_stride; a.k_stride = k_stride; a.q_out_stride = q_out_stride; a.k_out_stride = k_out_stride;
     a.pos = pos; a.inv_freq = inv_freq;
-    a.n_tokens = (int)T; a.Hq = p->Hq; a.Hkv = p->Hkv; a.d = p->d; a.rot = r->rot;
+    a.n_tokens = (int)T; a.n_axes = r->n_axes; a.Hq = p->Hq; a.Hkv = p->Hkv; a.d = p->d; a.rot = r->rot;
     a.interleaved = r->interleaved != 0; a.inverse = inverse != 0; a.elem = elem;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return cuda_status(traced("rotary_embed", s, [&] { return launch_rotary(a, s); }));

@@ -151,7 +151,7 @@ struct RotaryParams {
     const int32_t* pos;  // [axes][n_tokens]
     const float* inv_freq;
     PairAxes axes;
-    int n_tokens, Hq, Hkv, d, rot, interleaved, inverse, elem;
+    int n_tokens, n_axes, Hq, Hkv, d, rot, interleaved, inverse, elem;
 };
 cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t stream);
 

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
     for (int x = threadIdx.x; x < angles; x += kThreads) {
         if (x != threadIdx.x) angle_of(x, r0, f0);
         const int tok = x / half, i = x - tok * half;
-        cs[tok][i] = turn(r0, f0);
+        cs[tok][i] = turn(r0, frequency(f0));
     }
     __syncthreads();
     for (int x0 = threadIdx.x; x0 < total; x0 += kItems) {

@@ -8,7 +8,7 @@
 // Bound by HBM: every value is read once and written once.  Work is cut as in kv_append.cu, into items of two 16-byte vectors; a
 // CTA takes a few whole tokens and its threads ask for their angles' positions and frequencies first, then for the data, and form the
 // cosines and sines (one per pair and token, shared by all heads) while that is under way.  131072 tokens of 32 query and 8 KV
-// heads of 128 bf16 values: 391 us, 6.9 TB/s (1.01 of a copy); 4097 tokens of 8 heads of 64 float32 values 4.4 us.
+// heads of 128 bf16 values: 394 us, 6.8 TB/s (1.00 of a copy); 4097 tokens of 8 heads of 64 float32 values 4.3 us.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -24,6 +24,9 @@ template <typename T, bool INTERLEAVED, int kThreads, int kAhead>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p, int tokens_per_cta, int item_log2) {
     constexpr int V = Vec<T>::N, kItems = kThreads * kAhead;  // items of a CTA per round
     __shared__ float2 cs[kMaxTokens][64];
+    __shared__ int positions[USP_MAX_AXES * kMaxTokens];
+    __shared__ Frequency frequencies[64];
+    static_assert(USP_MAX_AXES * kMaxTokens <= kThreads, "a position to a thread");
     const int64_t t0 = (int64_t)blockIdx.x * tokens_per_cta;
     const int n_tok = (int)min((int64_t)tokens_per_cta, p.n_tokens - t0);
     const int d = p.d, half = p.rot / 2;
@@ -66,41 +69,46 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
         }
     };
     begin_kernel(false);
-    constexpr int kEarly = 2;  // angles of a thread whose positions are asked for before the data
+    // Positions and frequencies are asked for first, then the data.  A few angles of a thread keep theirs in registers; with few
+    // heads a CTA has up to 1024 angles of 16 tokens, whose positions go through shared memory (85360 tokens of 6 heads of 64
+    // values 31.0 -> 27.3 us; 131072 of 40 heads of 128 would take 402 us so instead of 391).
+    constexpr int kEarly = 2;
     const int angles = n_tok * half;
-    int at[kEarly];
-    float freq[kEarly];
-    auto place = [&](int x, int& tok, int& i) {
-        tok = x / half;
-        i = x - tok * half;
-    };
-    auto position = [&](int tok, int i) { return p.pos[pair_axis(p.axes, i) * (int64_t)p.n_tokens + t0 + tok]; };
+    if (angles <= kEarly * kThreads) {
+        int at[kEarly];
+        float freq[kEarly];
 #pragma unroll
-    for (int e = 0; e < kEarly; ++e) {
-        const int x = threadIdx.x + e * kThreads;
-        int tok, i;
-        if (x < angles) {
-            place(x, tok, i);
-            at[e] = position(tok, i);
-            freq[e] = p.inv_freq[i];
+        for (int e = 0; e < kEarly; ++e) {
+            const int x = threadIdx.x + e * kThreads, tok = x / max(half, 1), i = x - tok * half;
+            if (x < angles) {
+                at[e] = p.pos[pair_axis(p.axes, i) * (int64_t)p.n_tokens + t0 + tok];
+                freq[e] = p.inv_freq[i];
+            }
         }
-    }
-    asm volatile("" ::: "memory");
-    fetch(threadIdx.x);
-    asm volatile("" ::: "memory");
+        asm volatile("" ::: "memory");
+        fetch(threadIdx.x);
+        asm volatile("" ::: "memory");
 #pragma unroll
-    for (int e = 0; e < kEarly; ++e) {
-        const int x = threadIdx.x + e * kThreads;
-        int tok, i;
-        if (x < angles) {
-            place(x, tok, i);
-            cs[tok][i] = turn(at[e], freq[e]);
+        for (int e = 0; e < kEarly; ++e) {
+            const int x = threadIdx.x + e * kThreads, tok = x / max(half, 1), i = x - tok * half;
+            if (x < angles) cs[tok][i] = turn(at[e], frequency(freq[e]));
         }
-    }
-    for (int x = threadIdx.x + kEarly * kThreads; x < angles; x += kThreads) {
-        int tok, i;
-        place(x, tok, i);
-        cs[tok][i] = turn(position(tok, i), p.inv_freq[i]);
+    } else {
+        const int places = p.n_axes * n_tok;
+        int at = 0;
+        float f = 0.f;
+        if (threadIdx.x < places) at = p.pos[threadIdx.x / n_tok * (int64_t)p.n_tokens + t0 + threadIdx.x % n_tok];
+        if (threadIdx.x < half) f = p.inv_freq[threadIdx.x];
+        asm volatile("" ::: "memory");
+        fetch(threadIdx.x);
+        asm volatile("" ::: "memory");
+        if (threadIdx.x < places) positions[threadIdx.x] = at;
+        if (threadIdx.x < half) frequencies[threadIdx.x] = frequency(f);
+        __syncthreads();
+        for (int x = threadIdx.x; x < angles; x += kThreads) {
+            const int tok = x / half, i = x - tok * half;
+            cs[tok][i] = turn(positions[pair_axis(p.axes, i) * n_tok + tok], frequencies[i]);
+        }
     }
     __syncthreads();
     const float sign = p.inverse ? -1.f : 1.f;

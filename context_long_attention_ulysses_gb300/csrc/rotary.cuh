@@ -18,20 +18,27 @@ __device__ __forceinline__ int pair_axis(const PairAxes& x, int i) { return x.w[
 // to 64 bits: off by f / 2 units of the last bit, as the constant is by a half, and by one of the shift.  Times r, up to 2^31, that
 // is less than 2^-30 turns for f up to 8.  (The scarce float64 units took 3.5 of 144 us for a prompt of 32768 tokens; they
 // remain for f of 2^24 and more, where r f and its turns are three roundings, 3 2^-53 of themselves; infinities and NaN give NaN.)
-__device__ __forceinline__ float2 turn(int r, float f) {
+struct Frequency {
+    uint64_t turns;  // fraction of the turns of one position, times 2^64
+    float f;
+    bool far;        // 2^24 and more: by f
+};
+__device__ __forceinline__ Frequency frequency(float f) {
     const uint32_t bits = __float_as_uint(f) & 0x7fffffffu;
     const int exponent = (int)(bits >> 23), shift = 150 - exponent;
+    const uint32_t m = exponent > 0 ? (bits & 0x7fffffu) | 0x800000u : 0u;  // (a subnormal f turns by nothing: 2^-95 turns)
+    constexpr uint64_t kPerTurn = 0x28be60db9391054aull;                    // 2^64 / 2 pi
+    const uint64_t lo = m * kPerTurn, hi = __umul64hi((uint64_t)m, kPerTurn);
+    const uint64_t frac = shift <= 0 ? lo : shift < 64 ? (lo >> shift) | (hi << (64 - shift)) : shift < 128 ? hi >> (shift - 64) : 0;
+    return {f < 0.f ? (uint64_t)0 - frac : frac, f, shift < 0};
+}
+__device__ __forceinline__ float2 turn(int r, const Frequency& q) {
     float s, c;
-    if (shift >= 0) {
-        const uint32_t m = exponent > 0 ? (bits & 0x7fffffu) | 0x800000u : 0u;  // (a subnormal f turns by nothing: 2^-95 turns)
-        constexpr uint64_t kPerTurn = 0x28be60db9391054aull;                    // 2^64 / 2 pi
-        const uint64_t lo = m * kPerTurn, hi = __umul64hi((uint64_t)m, kPerTurn);
-        const uint64_t frac = shift == 0 ? lo : shift < 64 ? (lo >> shift) | (hi << (64 - shift)) : shift < 128 ? hi >> (shift - 64) : 0;
-        int64_t turns = (int64_t)((uint64_t)(int64_t)r * frac);
-        if (f < 0.f) turns = -turns;
+    if (!q.far) {
+        const int64_t turns = (int64_t)((uint64_t)(int64_t)r * q.turns);
         sincospif((float)(int)(turns >> 32) * 0x1p-31f, &s, &c);
     } else {
-        const double turns = (double)r * (double)f * 0.15915494309189535;  // / 2 pi
+        const double turns = (double)r * (double)q.f * 0.15915494309189535;  // / 2 pi
         sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
     }
     return make_float2(c, s);
