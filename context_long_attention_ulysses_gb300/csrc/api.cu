@@ -1249,7 +1249,7 @@ static bool stride_ok(int64_t stride, int64_t n, int elem) { return stride >= n 
 static usp_status kv_append(const usp_cache* c, int n_tokens, const void* q, int64_t q_stride, const void* k,
                             int64_t k_stride, const void* v, int64_t v_stride, const int32_t* seq, const int32_t* pos,
                             const int32_t* rot_pos, const float* inv_freq, int rot, int interleaved, const PairAxes& axes,
-                            void* q_out, void* k_out, void* k_pages, void* v_pages, const int32_t* page_table,
+                            int n_axes, void* q_out, void* k_out, void* k_pages, void* v_pages, const int32_t* page_table,
                             usp_stream stream) {
     usp_status st = check_cache(c);
     if (st != USP_OK) return st;
@@ -1282,6 +1282,7 @@ static usp_status kv_append(const usp_cache* c, int n_tokens, const void* q, int
     p.page_log2 = page_log2(c);
     p.Hq = c->Hq; p.Hkv = c->Hkv; p.d = c->d; p.rot = rot; p.interleaved = interleaved != 0; p.elem = elem;
     p.axes = axes;
+    p.n_axes = n_axes;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return cuda_status(traced("kv_append", s, [&] { return launch_kv_append(p, s); }));
 }
@@ -1291,7 +1292,7 @@ usp_status usp_kv_append(const usp_cache* c, int n_tokens, const void* q, int64_
                          const int32_t* rot_pos, const float* inv_freq, int rot, int interleaved, void* q_out,
                          void* k_out, void* k_pages, void* v_pages, const int32_t* page_table, usp_stream stream) {
     return kv_append(c, n_tokens, q, q_stride, k, k_stride, v, v_stride, seq, pos, rot_pos, inv_freq, rot, interleaved,
-                     PairAxes{}, q_out, k_out, k_pages, v_pages, page_table, stream);
+                     PairAxes{}, 1, q_out, k_out, k_pages, v_pages, page_table, stream);
 }
 
 // Shapes of a paged attention call; the pointers are filled in by the caller.
@@ -1433,7 +1434,7 @@ usp_status usp_kv_append_axes(const usp_cache* c, int n_tokens, const void* q, i
     if (!pack_axes(r, c->d, &axes)) return USP_ERR_INVALID_ARG;
     if (r->rot > 0 && !rot_pos && n_tokens > 0) return USP_ERR_MISALIGNED;
     return kv_append(c, n_tokens, q, q_stride, k, k_stride, v, v_stride, seq, pos, rot_pos, inv_freq, r->rot, r->interleaved,
-                     axes, q_out, k_out, k_pages, v_pages, page_table, stream);
+                     axes, r->n_axes, q_out, k_out, k_pages, v_pages, page_table, stream);
 }
 
 // ---------------------------------------------------------------- pages of the cache

@@ -167,6 +167,7 @@ struct AppendParams {
     int n_tokens, n_seqs, max_pages, n_pages, page_log2;
     int Hq, Hkv, d, rot, interleaved, elem;
     PairAxes axes;  // all 0: one axis
+    int n_axes;
 };
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
 

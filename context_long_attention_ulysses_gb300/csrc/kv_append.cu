@@ -36,7 +36,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
     constexpr int V = Vec<T>::N;
     __shared__ float2 cs[kMaxTokens][64];
     __shared__ int64_t s_row[kMaxTokens];  // row of head 0 in the pool, -1: padding
-    __shared__ int s_rot[kMaxTokens];
+    __shared__ int s_pos[USP_MAX_AXES * kMaxTokens];
+    __shared__ Frequency s_freq[64];
+    static_assert(USP_MAX_AXES * kMaxTokens <= kThreads, "a position to a thread");
     const int t0 = blockIdx.x * tokens_per_cta, n_tok = min(tokens_per_cta, p.n_tokens - t0);
     const int d = p.d, half = p.rot / 2, psize = 1 << p.page_log2;
     const int hq = p.q ? p.Hq : 0, heads = hq + 2 * p.Hkv, per_token = heads << item_log2;
@@ -83,16 +85,23 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
         }
     };
     begin_kernel(false);
+    // Positions and frequencies are asked for before the data: of one angle to a thread in registers, of more (up to 1024 of 16
+    // tokens, with few heads) through shared memory.
     const int angles = n_tok * half;
+    const bool few = angles <= kThreads;
+    const int32_t* positions = p.rot_pos ? p.rot_pos : p.pos;
     int r0 = 0;
     float f0 = 0.f;
-    auto angle_of = [&](int x, int& r, float& f) {
-        const int tok = x / half, i = x - tok * half;
-        const int64_t t = t0 + tok;
-        r = p.rot_pos ? p.rot_pos[pair_axis(p.axes, i) * (int64_t)p.n_tokens + t] : p.pos[t];
-        f = p.inv_freq[i];
-    };
-    if (threadIdx.x < angles) angle_of(threadIdx.x, r0, f0);
+    if (few) {
+        if (threadIdx.x < angles) {
+            const int tok = threadIdx.x / half, i = threadIdx.x - tok * half;
+            r0 = positions[pair_axis(p.axes, i) * (int64_t)p.n_tokens + t0 + tok];
+            f0 = p.inv_freq[i];
+        }
+    } else {
+        if (threadIdx.x < p.n_axes * n_tok) r0 = positions[threadIdx.x / n_tok * (int64_t)p.n_tokens + t0 + threadIdx.x % n_tok];
+        if (threadIdx.x < half) f0 = p.inv_freq[threadIdx.x];
+    }
     fetch(threadIdx.x);
     if (threadIdx.x < n_tok) {
         const int t = t0 + threadIdx.x, s = p.seq[t], pos = p.pos[t];
@@ -103,11 +112,20 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
         }
         s_row[threadIdx.x] = row;
     }
-    // (not through shared memory: the angles need not wait for the slots)
-    for (int x = threadIdx.x; x < angles; x += kThreads) {
-        if (x != threadIdx.x) angle_of(x, r0, f0);
-        const int tok = x / half, i = x - tok * half;
-        cs[tok][i] = turn(r0, frequency(f0));
+    // (the angles need not wait for the slots)
+    if (few) {
+        if (threadIdx.x < angles) {
+            const int tok = threadIdx.x / half, i = threadIdx.x - tok * half;
+            cs[tok][i] = turn(r0, frequency(f0));
+        }
+    } else {
+        if (threadIdx.x < p.n_axes * n_tok) s_pos[threadIdx.x] = r0;
+        if (threadIdx.x < half) s_freq[threadIdx.x] = frequency(f0);
+        __syncthreads();
+        for (int x = threadIdx.x; x < angles; x += kThreads) {
+            const int tok = x / half, i = x - tok * half;
+            cs[tok][i] = turn(s_pos[pair_axis(p.axes, i) * n_tok + tok], s_freq[i]);
+        }
     }
     __syncthreads();
     for (int x0 = threadIdx.x; x0 < total; x0 += kItems) {

@@ -605,7 +605,10 @@ size_t usp_pages_update_workspace_size(const usp_cache* c);
  * seq_lens [n_seqs], page_table [n_seqs][max_pages] and ref are updated in
  * place; entries of a slot that are no longer used become -1.  If there are not
  * enough free pages, nothing is changed, no copy is listed, and row 0 of
- * copies tells how many are lacking.  copies has n_seqs rows after row 0.
+ * copies tells how many are lacking.  (Pages may then still be shared that an
+ * append would write: a caller who does not look, in a captured step say,
+ * makes the step's tokens padding where copies[0][1] > 0, seq = -1.)  copies
+ * has n_seqs rows after row 0.
  * (Tokens that are appended next have the slots kept .. now - 1; drafts that
  * were refused are dropped by keep, say by usp_verify_drafts' keep_lens.)
  * ws: at least usp_pages_update_workspace_size(c) bytes, 256-byte aligned,
