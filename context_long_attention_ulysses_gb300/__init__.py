@@ -26,6 +26,7 @@ import torch
 
 from ._lib import (NOALLOC_SCRATCH_BYTES, SYMBOLS, USP_BF16, USP_F32, USP_MAX_AXES, USP_OK, UspCache,  # noqa: F401
                    UspError, UspProblem, UspRotary, UspTraceEntry, check, load)
+from ._lib import binding as _load_binding
 
 __all__ = [
     "Problem", "UspError", "SYMBOLS",
@@ -258,31 +259,22 @@ def _rows(x, heads: int, d: int):
     return x.data_ptr(), stride[0] if shape[0] > 1 else heads * d
 
 
-def _token_rows(x, heads: int, d: int):
-    """`_rows` of a sequence-sharded tensor [P][B][N/P][heads][d], or of one that is [tokens][heads][d] already."""
-    if not isinstance(x, _Tensor) or x.dim() != 5:
-        return _rows(x, heads, d)
-    P, B, n, H, w = x.shape
-    sP, sB, sn, sh, sd = x.stride()
-    if H != heads or w != d:
-        raise ValueError(f"expected [P][B][N/P][{heads}][{d}], got {list(x.shape)}")
-    if not P * B * n:
-        return x.data_ptr(), heads * d
-    if not x.is_cuda:
-        raise ValueError("libusp takes device tensors")
-    if sd != 1 or (heads > 1 and sh != d):
-        raise ValueError("the heads of a token must be contiguous")
-    # the one distance between tokens: of the innermost dimension that has more than one of them
-    step = sn if n > 1 else sB if B > 1 else sP if P > 1 else heads * d
-    if (B > 1 and sB != n * step) or (P > 1 and sP != B * n * step):
-        raise ValueError("tokens must be evenly apart")
-    return x.data_ptr(), step
+_bound = None
 
 
-def _rotary(r) -> ctypes.POINTER(UspRotary):
-    if r is None:
-        return None
-    return ctypes.byref(r._kept() if isinstance(r, Rotary) else r)
+def _binding():
+    """The calls around the cache (csrc/binding.cpp)."""
+    global _bound
+    if _bound is None:
+        _bound = _load_binding(_stream, _raw_stream)
+    return _bound
+
+
+def _struct(x) -> int:
+    """Address of the struct of a Problem, Cache or Rotary, or of a struct of the C ABI."""
+    if x is None:
+        return 0
+    return ctypes.addressof(x._kept() if isinstance(x, (Cache, Rotary, Problem)) else x)
 
 
 def _cache(c) -> ctypes.POINTER(UspCache):
@@ -519,20 +511,14 @@ def usp_prefix_attn(c, n_tokens: int, max_q: int, q, k_pages, v_pages, page_tabl
 def usp_rotary_embed(p, r, q, k, pos, inv_freq, q_out, k_out, inverse: bool = False, stream=None) -> None:
     """q, q_out, k, k_out: sequence-sharded [P][B][N/P][H][d], or [tokens][H][d], with any token stride (q, q_out or k,
     k_out may be None)."""
-    (qp, qs), (kp, ks) = _token_rows(q, p.Hq, p.d), _token_rows(k, p.Hkv, p.d)
-    (qo, qos), (ko, kos) = _token_rows(q_out, p.Hq, p.d), _token_rows(k_out, p.Hkv, p.d)
-    check("usp_rotary_embed", load().usp_rotary_embed(_prob(p), _rotary(r), int(bool(inverse)), qp, qs, kp, ks, _ptr(pos),
-                                                      _ptr(inv_freq), qo, qos, ko, kos, _stream(stream)))
+    _binding().rotary_embed(_struct(p), _struct(r), q, k, pos, inv_freq, q_out, k_out, 1 if inverse else 0, stream)
 
 
 def usp_kv_append_axes(c, n_tokens: int, q, k, v, seq, pos, rot_pos, inv_freq, r, q_out, k_out, k_pages, v_pages,
                        page_table, stream=None) -> None:
     """q, k, v: [n_tokens][H][d] with any token stride (q, q_out and k_out may be None); the rest contiguous."""
-    (qp, qs), (kp, ks), (vp, vs) = _rows(q, c.Hq, c.d), _rows(k, c.Hkv, c.d), _rows(v, c.Hkv, c.d)
-    check("usp_kv_append_axes", load().usp_kv_append_axes(_cache(c), int(n_tokens), qp, qs, kp, ks, vp, vs, _ptr(seq),
-                                                          _ptr(pos), _ptr(rot_pos), _ptr(inv_freq), _rotary(r),
-                                                          _ptr(q_out), _ptr(k_out), _ptr(k_pages), _ptr(v_pages),
-                                                          _ptr(page_table), _stream(stream)))
+    _binding().kv_append_axes(_struct(c), n_tokens, q, k, v, seq, pos, rot_pos, inv_freq, _struct(r), q_out, k_out, k_pages,
+                              v_pages, page_table, stream)
 
 
 def usp_pages_update_workspace_size(c) -> int:
@@ -540,42 +526,18 @@ def usp_pages_update_workspace_size(c) -> int:
 
 
 def usp_pages_update(c, parent, keep, grow, seq_lens, page_table, ref, copies, ws, ws_bytes=None, stream=None) -> None:
-    """seq_lens, page_table and ref are updated in place; copies int32 [1 + n_seqs][4]."""
-    if ws_bytes is None:
-        ws_bytes = ws.numel() * ws.element_size() if isinstance(ws, torch.Tensor) else 0
-    check("usp_pages_update", load().usp_pages_update(_cache(c), _ptr(parent), _ptr(keep), _ptr(grow), _ptr(seq_lens),
-                                                      _ptr(page_table), _ptr(ref), _ptr(copies), _ptr(ws),
-                                                      int(ws_bytes), _stream(stream)))
+    """seq_lens, page_table and ref are updated in place; copies int32 [1 + n_seqs][4]; ws_bytes None: those of the tensor."""
+    _binding().pages_update(_struct(c), parent, keep, grow, seq_lens, page_table, ref, copies, ws, ws_bytes, stream)
 
 
 def usp_pages_compact(c, page_table, ref, page_table_out, ref_out, new_id, copies, stream=None) -> None:
     """copies int32 [1 + n_pages // 2][4]; page_table_out and ref_out may be page_table and ref."""
-    check("usp_pages_compact", load().usp_pages_compact(_cache(c), _ptr(page_table), _ptr(ref), _ptr(page_table_out),
-                                                        _ptr(ref_out), _ptr(new_id), _ptr(copies), _stream(stream)))
+    _binding().pages_compact(_struct(c), page_table, ref, page_table_out, ref_out, new_id, copies, stream)
 
 
 def usp_pages_copy(c, max_copies: int, copies, k_pages, v_pages, n_layers: int = 1, layer_stride: int = 0,
                    stream=None) -> None:
-    check("usp_pages_copy", load().usp_pages_copy(_cache(c), int(max_copies), _ptr(copies), int(n_layers),
-                                                  int(layer_stride), _ptr(k_pages), _ptr(v_pages), _stream(stream)))
-
-
-def _prob_rows(x, vocab: int, dtype):
-    """Pointer and row stride (elements) of probabilities [rows][vocab], or of a device pointer to contiguous rows."""
-    if not isinstance(x, _Tensor):
-        return _ptr(x), vocab
-    shape = x.shape
-    if len(shape) != 2 or shape[1] != vocab:
-        raise ValueError(f"expected rows of {vocab} elements, got {list(shape)}")
-    if x.dtype != dtype:
-        raise ValueError(f"expected {dtype}, got {x.dtype}")
-    rows = shape[0]
-    if not x.is_cuda and rows:
-        raise ValueError("libusp takes device tensors")
-    step, one = x.stride()
-    if rows and vocab > 1 and one != 1:
-        raise ValueError("the probabilities of a row must be contiguous")
-    return x.data_ptr(), step if rows > 1 else vocab
+    _binding().pages_copy(_struct(c), max_copies, copies, k_pages, v_pages, n_layers, layer_stride, stream)
 
 
 def usp_verify_drafts(n_seqs: int, n_tokens: int, vocab: int, target, draft, tokens, u, q_start, seq_lens, n_accepted,
@@ -584,12 +546,8 @@ def usp_verify_drafts(n_seqs: int, n_tokens: int, vocab: int, target, draft, tok
     pointers)."""
     if dtype is None:
         dtype = "bf16" if isinstance(target, _Tensor) and target.dtype == torch.bfloat16 else "f32"
-    kind = _TORCH_DTYPE[dtype]
-    (tp, ts), (dp, ds) = _prob_rows(target, vocab, kind), _prob_rows(draft, vocab, kind)
-    check("usp_verify_drafts", load().usp_verify_drafts(n_seqs, n_tokens, vocab, USP_F32 if dtype == "f32" else USP_BF16,
-                                                        tp, ts, dp, ds, _ptr(tokens), _ptr(u), _ptr(q_start),
-                                                        _ptr(seq_lens), _ptr(n_accepted), _ptr(next_tokens),
-                                                        _ptr(keep_lens), _stream(stream)))
+    _binding().verify_drafts(n_seqs, n_tokens, vocab, USP_F32 if dtype == "f32" else USP_BF16, _TORCH_DTYPE[dtype], target,
+                             draft, tokens, u, q_start, seq_lens, n_accepted, next_tokens, keep_lens, stream)
 
 
 def usp_diag_wait_timeout(stream=None) -> None:

@@ -6,10 +6,12 @@ PyTorch fallback for any entry point.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
-from .build import LIB
+from .build import BINDING, LIB
 
 USP_OK = 0
 USP_ERR_INVALID_ARG = 1
@@ -158,6 +160,29 @@ def load() -> ctypes.CDLL:
             f.argtypes = args
         _lib = lib
         return lib
+
+
+_binding = None
+
+
+def binding(stream_of=None, raw_stream=None):
+    """The module that makes the calls around the cache (built by ``build.build()``); raises if it is missing.  The first
+    call says how a ``stream`` argument becomes a handle, and torch's current stream of a device."""
+    global _binding
+    if _binding is not None:
+        return _binding
+    load()
+    with _lock:
+        if _binding is None:
+            if not os.path.exists(BINDING):
+                raise ImportError(f"uspbinding.so not found at {BINDING}; build it first "
+                                  "(python -m context_long_attention_ulysses_gb300.build)")
+            loader = importlib.machinery.ExtensionFileLoader("uspbinding", BINDING)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_loader("uspbinding", loader))
+            loader.exec_module(module)
+            module.configure(stream_of, check, raw_stream)
+            _binding = module
+        return _binding
 
 
 def check(fn: str, status: int) -> None:

@@ -1,7 +1,8 @@
 """Build libusp.so (the C-ABI library) in-tree for sm_103a with nvcc.
 
 Each CUDA translation unit compiles in parallel; the objects link into
-``_build/libusp.so`` against the shared CUDA runtime.  Run as
+``_build/libusp.so`` against the shared CUDA runtime, and ``binding.cpp``, the
+Python side of a decoding step's calls, into ``_build/uspbinding.so``.  Run as
 ``python -m context_long_attention_ulysses_gb300.build``.
 """
 from __future__ import annotations
@@ -10,11 +11,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libusp.so")
+BINDING = os.path.join(BUILD, "uspbinding.so")
 SOURCES = ["api.cu", "remap.cu", "attn_f32.cu", "attn_fwd.cu", "attn_bwd.cu", "ring.cu", "noalloc.cu", "diag.cu",
            "kv_append.cu", "rotary.cu", "pages.cu", "verify.cu", "paged_attn.cu", "paged_mma.cu", "paged_tc.cu", "paged_f32.cu"]
 HEADERS = ["kernels.h", "ptx.cuh", "paged.cuh", "rotary.cuh", "cluster.cuh"]
@@ -45,12 +48,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
         os.path.join(os.path.dirname(HERE), "include", "usp.h")]
     procs = []
     objs = []
-    for src in SOURCES:
+    header = os.path.join(os.path.dirname(HERE), "include", "usp.h")
+    for src in SOURCES + ["binding.cpp"]:
         s = os.path.join(CSRC, src)
-        o = os.path.join(BUILD, src.replace(".cu", ".o"))
+        o = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
         objs.append(o)
-        if force or _stale(o, [s] + header_deps):
+        if force or _stale(o, [s] + (header_deps if src.endswith(".cu") else [header])):
             cmd = [nvcc, *ARCH, *FLAGS, "-c", s, "-o", o + ".tmp"]
+            if not src.endswith(".cu"):
+                cmd[1:1] = ["-I", sysconfig.get_paths()["include"]]
             if verbose:
                 print(" ".join(cmd), flush=True)
             procs.append((subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), o, cmd))
@@ -66,13 +72,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if failed:
         msg = "\n".join(" ".join(c) + "\n" + o for c, o in failed)
         raise RuntimeError(f"nvcc failed:\n{msg}")
-    if force or _stale(LIB, objs):
-        tmp = LIB + f".tmp{os.getpid()}"
-        cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        subprocess.check_call(cmd)
-        os.replace(tmp, LIB)
+    *objs, binding = objs
+    for target, parts in ((LIB, objs), (BINDING, [binding, "-L", BUILD, "-lusp", "-Xlinker", "-rpath=$ORIGIN"])):
+        if force or _stale(target, objs if target == LIB else [binding]):
+            tmp = target + f".tmp{os.getpid()}"
+            cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *parts]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            subprocess.check_call(cmd)
+            os.replace(tmp, target)
     return LIB
 
 

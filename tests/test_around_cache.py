@@ -328,6 +328,35 @@ def test_helpers_refuse_host_tensors():
             call()
 
 
+def test_arguments_that_are_no_buffers_are_refused(lib):
+    import torch
+    x, i = torch.zeros(4, 100), torch.zeros(4, dtype=torch.int32)
+    calls = [lambda y: usp_mod.usp_pages_copy(_c(), 1, y, FAKE, FAKE),
+             lambda y: usp_mod.usp_pages_compact(_c(), y, FAKE, FAKE, FAKE, FAKE, FAKE),
+             lambda y: usp_mod.usp_pages_update(_c(), y, None, None, FAKE, FAKE, FAKE, FAKE, FAKE),
+             lambda y: usp_mod.usp_verify_drafts(1, 4, 100, FAKE, None, y, FAKE, FAKE, None, FAKE, FAKE, None, "f32"),
+             lambda y: usp_mod.usp_verify_drafts(1, 4, 100, y, None, FAKE, FAKE, FAKE, None, FAKE, FAKE, None),
+             lambda y: usp_mod.usp_rotary_embed(_p(), R3, y, None, FAKE, FAKE, FAKE, None)]
+    for call in calls:
+        for y, kind in (("a text", TypeError), ([1], TypeError), (1.5, TypeError)):
+            with pytest.raises(kind):
+                call(y)
+        for y in (x, i, torch.zeros(4, 4, 64)):               # host tensors, or of another shape
+            with pytest.raises(ValueError):
+                call(y)
+    with pytest.raises(ValueError):                           # a row of another type
+        usp_mod.usp_verify_drafts(1, 4, 100, x.bfloat16(), None, FAKE, FAKE, FAKE, None, FAKE, FAKE, None, "f32")
+    for y in (torch.zeros(2, 1, 4, 4, 32), torch.zeros(2, 1, 4, 3, 64), torch.zeros(8, 4, 64)[:, ::2].expand(8, 2, 64),
+              torch.zeros(2, 2, 4, 4, 64).transpose(0, 1)[:, :, 1:]):
+        with pytest.raises(ValueError):
+            usp_mod.usp_rotary_embed(_p(), R3, y, None, FAKE, FAKE, FAKE, None)
+    with pytest.raises((OverflowError, TypeError)):
+        usp_mod.usp_pages_copy(_c(), 1 << 40, FAKE, FAKE, FAKE)
+    with pytest.raises(TypeError):
+        usp_mod._binding().pages_copy(0, 1)
+    assert _status(lambda: usp_mod.usp_pages_copy(_c(page_size=24), 1, FAKE, FAKE, FAKE)) == 2
+
+
 # ------------------------------------------------------------------ GPU
 @pytest.fixture(scope="module")
 def usp():
@@ -1106,3 +1135,27 @@ def test_rows_beyond_32_bit_offsets(usp):
     assert torch.equal(q.contiguous(), want)
     del big, q
     torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+def test_tensors_that_the_calls_cannot_take(usp):
+    """Device tensors without the layout that a call needs, and an argument's own stream, handle or object."""
+    import torch
+    c, p = _c(), _p(N=16)
+    i = torch.zeros((9, 4), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        usp.usp_pages_copy(c, 8, i[:, ::2], i, i)
+    with pytest.raises(ValueError):
+        usp.usp_verify_drafts(1, 4, 50, torch.zeros(4, 100, device="cuda")[:, ::2], None, i, i, i, None, i, i, None)
+    q = torch.zeros((2, 1, 8, 4, 64), dtype=torch.bfloat16, device="cuda")
+    f, pos = torch.zeros(32, device="cuda"), torch.zeros((3, 16), dtype=torch.int32, device="cuda")
+    for bad in (q.transpose(3, 4), q[..., :3, :], torch.zeros((2, 1, 9, 4, 64), dtype=torch.bfloat16, device="cuda")[:, :, 1:]):
+        with pytest.raises(ValueError):
+            usp.usp_rotary_embed(p, R3, bad, None, pos, f, q, None)
+    side = torch.cuda.Stream()
+    for stream in (None, side, side.cuda_stream, 0):
+        usp.usp_rotary_embed(p, R3, q, None, pos, f, q, None, stream=stream)
+    torch.cuda.synchronize()
+    with pytest.raises((TypeError, ValueError)):
+        usp.usp_rotary_embed(p, R3, q, None, pos, f, q, None, stream="a text")
+    assert usp.usp_device_status() == 0
