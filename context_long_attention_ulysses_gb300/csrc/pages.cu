@@ -132,17 +132,14 @@ struct Update {
     __device__ __forceinline__ static uint32_t order(int a, int b) { return a == b ? (uint32_t)b : (uint32_t)b | 0x80000000u; }
     __device__ __forceinline__ bool is_free(int i) const { return get(u.count + i) <= 0 && get(u.first + i) == kNobody; }
 
-    // Pages [i0, i1), in steps of n from i0 + k on.  Returns how many of this thread's are free as they are.
-    __device__ __forceinline__ int init(int k, int n) const {
-        int held = 0;
+    // The pages' counts, every n-th from k on.
+    __device__ __forceinline__ void init(int k, int n) const {
 #pragma unroll 4
         for (int i = k; i < p.n_pages; i += n) {
             const int c = __ldcg(p.ref + i);
             u.count[i] = c;
             u.first[i] = kNobody;
-            held += c <= 0;
         }
-        return held;
     }
 
     __device__ __forceinline__ void add(int id, int n) const {
@@ -168,29 +165,45 @@ struct Update {
         }
     }
 
-    // What slot b is to do, by a thread; a slot that goes on by itself also gives up the first two pages that it drops.
-    __device__ __forceinline__ void enter(int b) const {
-        const int a = parent(b), cap = p.max_pages << p.page_log2;
+    // What a slot is to do, in the order in which it becomes known: what the caller says, then pages that its rows name.
+    struct Entry {
+        int parent, length, keep, grow;
+        int last, drops[2];  // the page that ends inside the kept tokens, -1; the first two that a slot which goes on by itself drops
+        int4 slot;
+        int flags;
+    };
+    __device__ __forceinline__ Entry ask(int b) const {
+        Entry e;
+        e.parent = parent(b);
+        e.length = __ldcg(p.seq_lens + b);
+        e.keep = p.keep ? __ldcg(p.keep + b) : INT32_MAX;
+        e.grow = p.grow ? __ldcg(p.grow + b) : 0;
+        return e;
+    }
+    __device__ __forceinline__ void look_up(int b, Entry& e) const {
+        const int a = e.parent, cap = p.max_pages << p.page_log2;
         const bool known = slot_exists(a), other = a != b;
-        const int old = length(b), most = known ? other ? length(a) : old : 0;
-        const int keeps = kept(b, most), grow = p.grow ? max(__ldcg(p.grow + b), 0) : 0;
-        const int now = keeps + min(grow, cap - keeps), old_n = pages(old), kept_n = pages(keeps);
+        const int old = min(max(e.length, 0), cap), most = known ? other ? length(a) : old : 0;
+        const int keeps = min(max(e.keep, 0), most), now = keeps + min(max(e.grow, 0), cap - keeps);
+        const int old_n = pages(old), kept_n = pages(keeps);
         // (what a slot that goes on by itself keeps is not written in this call, and can be read from its row at the end)
         const bool staged = other && keeps > 0 && (parent(a) != a || kept(a, most) < keeps);
         const bool ends_inside = keeps & ((1 << p.page_log2) - 1);
-        const int last = ends_inside ? __ldcg(row(a) + kept_n - 1) : -1;
-        const bool writes = ends_inside && now > keeps && inside(last);
-        u.slot[b] = make_int4(keeps, now, old_n, last);
-        u.place[b] = make_int4(0, -1, (other ? kSlotOther : 0) | (staged ? kSlotStaged : 0) | (writes ? kSlotWrites : 0), a);
-        if (writes) {
-            atomicMin(u.first + last, order(a, b));
-            atomicAdd(u.count + last, -1);  // (counted on by move(), or already)
-        }
-        if (!other) {
+        e.last = ends_inside ? __ldcg(row(a) + kept_n - 1) : -1;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (kept_n + j < old_n) add(__ldcg(row(b) + kept_n + j), -1);
+        for (int j = 0; j < 2; ++j) e.drops[j] = !other && kept_n + j < old_n ? __ldcg(row(b) + kept_n + j) : -1;
+        e.slot = make_int4(keeps, now, old_n, e.last);
+        e.flags = (other ? kSlotOther : 0) | (staged ? kSlotStaged : 0) | (ends_inside && now > keeps && inside(e.last) ? kSlotWrites : 0);
+    }
+    __device__ __forceinline__ void enter(int b, const Entry& e) const {
+        u.slot[b] = e.slot;
+        u.place[b] = make_int4(0, -1, e.flags, e.parent);
+        if (e.flags & kSlotWrites) {
+            atomicMin(u.first + e.last, order(e.parent, b));
+            atomicAdd(u.count + e.last, -1);  // (counted on by move(), or already)
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) add(e.drops[j], -1);
     }
     // Entries of the table that move() and write() read for slot b.
     __device__ __forceinline__ int reads(int b) const {
@@ -262,8 +275,10 @@ struct Update {
 __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_constant__ PagesUpdateParams p, int32_t* stage) {
     extern __shared__ int4 smem[];
     __shared__ uint64_t part[kWarps];
+    __shared__ uint32_t sums[3][kWarps];
     __shared__ uint16_t long_rows[kOneSeqs];  // (in any order: counts are added up, rows written by themselves)
     __shared__ int n_long;
+    constexpr int kRounds = kOnePages / kThreads;
     Books u;
     u.slot = smem;
     u.place = u.slot + p.n_seqs;
@@ -272,14 +287,28 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
     u.free_ids = reinterpret_cast<int32_t*>(u.first + p.n_pages);
     u.stage = stage;
     const Update<true> x{p, u};
+    using Entry = Update<true>::Entry;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int b = threadIdx.x;  // (one slot to a thread: kOneSeqs of them at most)
     begin_kernel(false);
-    const int held = x.init(threadIdx.x, kThreads);
+    Entry e;
+    if (b < p.n_seqs) e = x.ask(b);
     if (threadIdx.x == 0) n_long = 0;
+    {
+        int c[kRounds];
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) c[r] = b + r * kThreads < p.n_pages ? __ldcg(p.ref + b + r * kThreads) : 0;
+        if (b < p.n_seqs) x.look_up(b, e);  // (its loads are under way with the counts')
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const int i = b + r * kThreads;
+            if (i >= p.n_pages) break;
+            u.count[i] = c[r];
+            u.first[i] = kNobody;
+        }
+    }
     __syncthreads();
-    // (one slot to a thread: kOneSeqs of them at most)
-    const int b = threadIdx.x;
-    if (b < p.n_seqs) x.enter(b);
+    if (b < p.n_seqs) x.enter(b, e);
     __syncthreads();
     // rows are short, or many, or both: each has its share of the threads, but 8; a long one all of them, after the others
     const int lanes = max(8, kThreads >> (32 - __clz(max(p.n_seqs, 1) - 1)));
@@ -292,30 +321,69 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
             long_rows[atomicAdd(&n_long, 1)] = (uint16_t)s;
     }
     __syncthreads();
-    for (int k = 0; k < n_long; ++k) x.move(long_rows[k], threadIdx.x, kThreads);
-    __syncthreads();
-    const uint64_t mine = b < p.n_seqs ? x.needs(b) : 0;
-    const int w0 = share(0, p.n_pages, warp, kWarps), w1 = share(0, p.n_pages, warp + 1, kWarps);
-    auto is_free = [&](int i) { return x.is_free(i); };
-    const int free_here = each_of(w0, w1, is_free, [](int, int) {});
-    uint64_t sum, all;
-    const uint64_t at = block_scan(mine, &sum, part);
-    uint64_t before = block_scan((lane == 0 ? free_here : 0) | (uint64_t)held << 32, &all, part);
-    const int64_t need = sum & ((1ull << 40) - 1), copies = sum >> 40, free_n = (uint32_t)all;
-    if (threadIdx.x == 0) x.head(need, free_n, copies, all >> 32);
-    if (need > free_n) return;
-    if (b < p.n_seqs) {
-        u.place[b].x = (int)(at & ((1ull << 40) - 1));
-        if (mine >> 40) u.place[b].y = (int)(at >> 40);
+    if (n_long > 0) {
+        for (int k = 0; k < n_long; ++k) x.move(long_rows[k], threadIdx.x, kThreads);
+        __syncthreads();
     }
-    const int first = (int)(uint32_t)__shfl_sync(~0u, before, 0);
-    if (first < need) each_of(w0, w1, is_free, [&](int i, int k) { u.free_ids[first + k] = i; });
+
+    // Running sums of what the slots need (a slot's at most 2^15, more than there are pages), of copies, and of free pages: a warp
+    // has up to kRounds times 32 pages, a lane's as bits.
+    const uint64_t mine = b < p.n_seqs ? x.needs(b) : 0;
+    const int w0 = warp * ((p.n_pages + kThreads - 1) / kThreads * 32);
+    const int w1 = min(w0 + (p.n_pages + kThreads - 1) / kThreads * 32, p.n_pages);
+    uint32_t free_bits = 0;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+        if (w0 + 32 * r + lane < w1 && x.is_free(w0 + 32 * r + lane)) free_bits |= 1u << r;
+    uint32_t need_to = (uint32_t)min(mine & ((1ull << 40) - 1), 1ull << 15), copies_to = (uint32_t)(mine >> 40);
+    const uint32_t need_own = need_to, copies_own = copies_to, free_own = __reduce_add_sync(~0u, __popc(free_bits));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t n = __shfl_up_sync(~0u, need_to, o), c = __shfl_up_sync(~0u, copies_to, o);
+        if (lane >= o) {
+            need_to += n;
+            copies_to += c;
+        }
+    }
+    if (lane == 31) {
+        sums[0][warp] = need_to;
+        sums[1][warp] = copies_to;
+        sums[2][warp] = free_own;
+    }
     __syncthreads();
+    const uint32_t v0 = sums[0][lane], v1 = sums[1][lane], v2 = sums[2][lane];
+    const uint32_t need = __reduce_add_sync(~0u, v0), copies = __reduce_add_sync(~0u, v1), free_n = __reduce_add_sync(~0u, v2);
+    const uint32_t need_at = __reduce_add_sync(~0u, lane < warp ? v0 : 0) + need_to - need_own;
+    const uint32_t copies_at = __reduce_add_sync(~0u, lane < warp ? v1 : 0) + copies_to - copies_own;
+    uint32_t free_at = __reduce_add_sync(~0u, lane < warp ? v2 : 0);
+    if (need > free_n) {
+        int held = 0;
+        for (int i = threadIdx.x; i < p.n_pages; i += kThreads) held += __ldcg(p.ref + i) <= 0;
+        uint64_t all_need, all_held;
+        block_scan(mine & ((1ull << 40) - 1), &all_need, part);
+        block_scan(held, &all_held, part);
+        if (threadIdx.x == 0) x.head(all_need, free_n, copies, all_held);
+        return;
+    }
+    if (threadIdx.x == 0) x.head(need, free_n, copies, 0);
+    if (b < p.n_seqs) {
+        u.place[b].x = (int)need_at;
+        if (copies_own) u.place[b].y = (int)copies_at;
+    }
+    if (free_at < need) {
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const uint32_t m = __ballot_sync(~0u, free_bits >> r & 1);
+            if (free_bits >> r & 1) u.free_ids[free_at + __popc(m & ((1u << lane) - 1))] = w0 + 32 * r + lane;
+            free_at += __popc(m);
+        }
+    }
+    __syncthreads();
+    const int taken = need > 0 ? u.free_ids[need - 1] : -1;
+    for (int i = threadIdx.x; i < p.n_pages; i += kThreads) x.commit(i, taken);
     for (int s = group; s < p.n_seqs; s += kThreads / lanes)
         if (!is_long(s)) x.write(s, row_lane, lanes);
     for (int k = 0; k < n_long; ++k) x.write(long_rows[k], threadIdx.x, kThreads);
-    const int taken = need > 0 ? u.free_ids[need - 1] : -1;
-    for (int i = threadIdx.x; i < p.n_pages; i += kThreads) x.commit(i, taken);
 }
 
 // The same, a launch for each step, with the books in the workspace.
@@ -335,7 +403,11 @@ __global__ void __launch_bounds__(kStepThreads) pages_count_kernel(const __grid_
     const int groups = gridDim.x * (kStepThreads / kStepLanes), group = blockIdx.x * (kStepThreads / kStepLanes) + threadIdx.x / kStepLanes;
     const int lane = threadIdx.x % kStepLanes;
     for (int64_t b = group; b < p.n_seqs; b += groups) {
-        if (lane == 0) x.enter((int)b);
+        if (lane == 0) {
+            auto e = x.ask((int)b);
+            x.look_up((int)b, e);
+            x.enter((int)b, e);
+        }
         __syncwarp();
         x.move((int)b, lane, kStepLanes);
     }

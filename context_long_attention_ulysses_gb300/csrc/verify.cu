@@ -116,25 +116,26 @@ __device__ __forceinline__ uint64_t fixed64(float u) {
     return shift >= 0 ? m << shift : m >> min(-shift, 63);
 }
 
-// Sums of tiles stop at the largest number, so that rows which are no probabilities (thousands of ones) still lead to a token.
-__device__ __forceinline__ uint64_t add(uint64_t x, uint64_t y) { return x + y < x ? ~0ull : x + y; }
-__device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = add(x, __shfl_xor_sync(~0u, x, o));
-    return x;
-}
+// A tile's sum is below 2^56 and a warp's below 2^64.  Warps' and CTAs' sums stop at 2^60, so that the cluster's does not overflow
+// for rows which are no probabilities (thousands of ones), and these still lead to a token.
+constexpr uint64_t kMost = 1ull << 60;
+
 __device__ __forceinline__ uint64_t warp_scan(uint64_t x, int lane) {  // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint64_t y = __shfl_up_sync(~0u, x, o);
-        if (lane >= o) x = add(x, y);
+        if (lane >= o) x += y;
     }
     return x;
 }
-// The sum over the lanes of numbers below 2^50, to all.
+// The sum over the lanes, to all: in pieces that the warp's own addition takes; SMALL: of numbers below 2^50.
+template <bool SMALL>
 __device__ __forceinline__ uint64_t lanes_total(uint64_t x) {
-    const uint32_t a = __reduce_add_sync(~0u, (uint32_t)x & 0x3ffffffu), b = __reduce_add_sync(~0u, (uint32_t)(x >> 26));
-    return a + ((uint64_t)b << 26);
+    constexpr uint32_t kPiece = (1u << 26) - 1;
+    const uint32_t a = __reduce_add_sync(~0u, (uint32_t)x & kPiece);
+    if constexpr (SMALL) return a + ((uint64_t)__reduce_add_sync(~0u, (uint32_t)(x >> 26)) << 26);
+    const uint32_t b = __reduce_add_sync(~0u, (uint32_t)(x >> 26) & kPiece), c = __reduce_add_sync(~0u, (uint32_t)(x >> 52));
+    return a + ((uint64_t)b << 26) + ((uint64_t)c << 52);
 }
 
 template <int N>
@@ -149,15 +150,9 @@ struct Weights {
     int from, to;
     int except;      // its place, -1: none
 
-    __device__ __forceinline__ uint64_t at(int i) const {
-        if (i < from || i >= to || i == except) return 0;
-        const uint64_t a = fixed46(value(p + i)), b = q ? fixed46(value(q + i)) : 0;
-        return a > b ? a - b : 0;
-    }
-    // The sum of a lane's places in a row, from i on.
-    __device__ __forceinline__ uint64_t few(int i) const {
+    // A lane's places in a row, from i on: their values and the sum of their weights.
+    __device__ __forceinline__ uint64_t few(int i, float (&x)[E], float (&y)[E]) const {
         Digits d;
-        float x[E], y[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const bool some = i + e >= from && i + e < to && i + e != except;
@@ -166,8 +161,9 @@ struct Weights {
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const float z = __saturatef(y[e]);
-            d.add(fmaxf(__saturatef(x[e]), z), z);
+            y[e] = __saturatef(y[e]);
+            x[e] = fmaxf(__saturatef(x[e]), y[e]);
+            d.add(x[e], y[e]);
         }
         return d.whole();
     }
@@ -194,7 +190,7 @@ struct Weights {
                     d.add(x);
                 }
             }
-            sum[k] = lanes_total(d.whole());
+            sum[k] = lanes_total<true>(d.whole());
             const int j = except - (i + k * step);
             if (!Q && j >= 0 && j < kLength) sum[k] -= fixed46(value(p + except));
         }
@@ -211,7 +207,7 @@ struct Weights {
             tiles<Q, edge.value>(t * kLength, kWarps * kLength, lane, s);
 #pragma unroll
             for (int k = 0; k < count.value; ++k) {
-                sum = add(sum, s[k]);
+                sum += s[k];
                 if (lane == 0) out[t - first + k * kWarps] = s[k];
             }
             t += count.value * kWarps;
@@ -287,14 +283,14 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
     for (int go = 0; go < 2; ++go) {
         const uint64_t sum = w.q ? w.template slice<true>(first, end, warp, lane, tile_sum)
                                  : w.template slice<false>(first, end, warp, lane, tile_sum);
-        if (lane == 0) warp_total[warp] = sum;
+        if (lane == 0) warp_total[warp] = min(sum, kMost);
         __syncthreads();
-        mine = warp_sum(lane < kWarps ? warp_total[lane] : 0);
+        mine = min(lanes_total<false>(lane < kWarps ? warp_total[lane] : 0), kMost);
         if (threadIdx.x == 0) cta_total[go] = mine;
         cluster_sync();
         const uint64_t x = lane < size ? cluster_read(&cta_total[go], lane) : 0;
-        total = warp_sum(x);
-        before = warp_sum(lane < rank ? x : 0);
+        total = lanes_total<false>(x);
+        before = lanes_total<false>(lane < rank ? x : 0);
         if (total > 0 || (!w.q && w.except < 0)) break;
         // nothing is left of the row (q >= p throughout, as rounded): drawn from p itself
         w.q = nullptr;
@@ -317,18 +313,23 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
                 continue;
             }
             const int k = __ffs(over) - 1;
-            const uint64_t less = __shfl_sync(~0u, to, max(k - 1, 0));  // (not to - sum: `to` may have stopped)
+            const uint64_t less = __shfl_sync(~0u, to, max(k - 1, 0));
             if (k > 0) rest -= less;
-            // the tile again: the lane that holds it, then each of its values to a lane
+            // the tile again: the lane that holds it, whose values then go to all
             const int i0 = (t + k) * kLength;
-            const uint64_t upto = warp_scan(w.few(i0 + lane * E), lane);
-            const int l = __ffs(__ballot_sync(~0u, upto > rest)) - 1;
+            float x[E], y[E];
+            const uint64_t upto = warp_scan(w.few(i0 + lane * E, x, y), lane);
+            const int l = max(__ffs(__ballot_sync(~0u, upto > rest)) - 1, 0);
             const uint64_t less_l = __shfl_sync(~0u, upto, max(l - 1, 0));
             if (l > 0) rest -= less_l;
-            const int i1 = i0 + l * E;
-            const uint64_t run = warp_scan(lane < E ? w.at(i1 + lane) : 0, lane);
-            const int e = __ffs(__ballot_sync(~0u, run > rest)) - 1;
-            if (lane == 0) p.next[b] = i1 + e - skip;
+            Digits run;
+            int e = 0;
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                run.add(__shfl_sync(~0u, x[j], l), __shfl_sync(~0u, y[j], l));
+                e += run.whole() <= rest;
+            }
+            if (lane == 0) p.next[b] = i0 + l * E + min(e, E - 1) - skip;
             break;
         }
     }
