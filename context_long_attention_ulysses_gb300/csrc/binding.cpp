@@ -1,7 +1,7 @@
 // The Python side of the calls around the cache: arguments as torch tensors, device addresses or None, turned into pointers
 // and strides and passed on to the C ABI.  (Small calls are over on the GPU before ctypes and checks in Python are done
-// with them: with those the host took 6.6 us for the bookkeeping of 64 conversations, 7.4 to verify one sequence's drafts and
-// 9.6 to append a token each of eight, so 4.5, 4.7 and 5.4; a launch is 2.3 of that.)
+// with them: with those the host took 6.6 us for the bookkeeping of 64 conversations, 7.6 to verify one sequence's drafts and
+// 9.7 to append a token each of eight, so 4.5, 4.8 and 5.9; a launch is 2.3 of that.)
 // What cannot be a buffer of the library raises, as in the package's Python; a status that is not USP_OK goes to the package's
 // check().
 #define PY_SSIZE_T_CLEAN

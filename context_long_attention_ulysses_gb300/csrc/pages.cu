@@ -12,8 +12,8 @@
 //           then, the writers alone hold it, and the first keeps it;
 //   number  new pages and copies slot by slot, free pages page by page;
 //   write   rows, lengths, the list of copies, counts, if there are pages enough.
-// Small caches take one CTA with all counts in its shared memory (64 conversations 11.4 us as one cluster of eight CTAs with the
-// counts in L2, where a step's few dependent accesses and a barrier cost 1 to 4 us), others a launch for each step, which
+// Small caches take one CTA with all counts in its shared memory (64 conversations 4.9 us; 11.4 as one cluster of eight CTAs with
+// the counts in L2, where a step's few dependent accesses and a barrier cost 1 to 4 us), others a launch for each step, which
 // follow each other by dependent launch.
 #include <algorithm>
 
