@@ -247,6 +247,20 @@ def test_rotary_refusals(lib):
             bad.c()
 
 
+def test_structs_of_a_rotation_and_a_problem_are_the_callers_own(lib):
+    """A changed struct is another's: it does not reach the calls of the one it was made from, nor do copies share it."""
+    import copy
+    import pickle
+    r, p = usp_mod.Rotary.sections((8, 12, 12)), _p()
+    call = lambda p_, r_: usp_mod.usp_rotary_embed(p_, r_, FAKE, FAKE, FAKE + 2, FAKE, FAKE, FAKE)  # noqa: E731  (3: pos misaligned)
+    assert _status(call, p, r) == 3
+    s, q = r.c(), p.c()
+    s.n_axes, q.d = 9, 96
+    assert _status(call, p, s) == 1 and _status(call, q, r) == 2 and _status(call, p, r) == 3
+    for same in (copy.copy, copy.deepcopy, lambda x: pickle.loads(pickle.dumps(x))):
+        assert same(r) == r and same(p) == p and _status(call, same(p), same(r)) == 3
+
+
 def test_append_axes_refusals(lib):
     def call(c=None, T=2, rot_pos=FAKE, r=R3, **kw):
         a = dict(q=FAKE, k=FAKE, v=FAKE, seq=FAKE, pos=FAKE, f=FAKE, qo=FAKE, ko=FAKE, kp=FAKE, vp=FAKE, table=FAKE)
@@ -611,6 +625,47 @@ def test_pages_update_when_pages_lack(usp):
     assert pool.step([-1, -1, -1], None, None)[0] == (0, 0, 10, 0)
     assert pool.step(None, None, [64, 64, 33])[0] == (0, 1, 10, 0)   # eleven pages of ten
     assert pool.step(None, None, [64, 64, 32])[0] == (0, 0, 0, 0)
+
+
+@pytest.mark.gpu
+def test_nothing_to_keep_books_of(usp):
+    """Caches without slots, pages or entries: the list's head is written all the same."""
+    import torch
+    guard = Guarded()
+    for B, mp, n in ((0, 3, 50), (0, 0, 0), (3, 0, 7), (2, 2, 0), (1500, 0, 0), (1500, 2, 0)):
+        c = usp.Cache(n, 16, B, mp, 1, 1, 64)
+        lens, table, ref = usp.pages_empty(c)
+        copies = guard.empty((1 + B, 4), torch.int32, "cuda").fill_(-7)
+        ws = guard.bytes(max(usp.usp_pages_update_workspace_size(c), 256), "cuda")
+        usp.usp_pages_update(c, None, None, torch.full((B,), 5, dtype=torch.int32, device="cuda"), lens, table, ref, copies, ws)
+        _done(usp, guard)
+        need = B if mp else 0
+        assert copies[0].tolist() == [0, max(0, need - n), n, 0] and (copies[1:] == -7).all() and (lens == 0).all()
+        many, new_id = usp.pages_compact(c, table, ref)
+        assert many[0].tolist() == [0, 0, n, 0] and (new_id == -1).all()
+
+
+@pytest.mark.gpu
+def test_the_largest_pool(usp):
+    """2^23 pages: grown from nothing pages go out from 0 on; half of them given up, the others move to the front."""
+    import torch
+    n, mp = 1 << 23, 1 << 22
+    c = usp.Cache(n, 16, 3, mp, 1, 1, 64)
+    lens, table, ref = usp.pages_empty(c)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    grow = torch.tensor([16 * mp - 1, 16 * 1000, 16 * (mp - 1000)], **i32)
+    assert usp.pages_update(c, lens, table, ref, grow=grow)[0].tolist() == [0, 0, 0, 0]
+    assert torch.equal(table.view(-1)[:mp], torch.arange(mp, **i32)) and (ref == 1).all()
+    assert torch.equal(table[2, :mp - 1000], torch.arange(mp + 1000, 2 * mp, **i32)) and (table[2, mp - 1000:] == -1).all()
+    head = usp.pages_update(c, lens, table, ref, parent=torch.tensor([1, -1, 2], **i32))[0].tolist()
+    assert head == [0, 0, n - 1000 - (mp - 1000), 0] and lens.tolist() == [16000, 0, 16 * (mp - 1000)]
+    before = table.clone()
+    copies, new_id = usp.pages_compact(c, table, ref)
+    # live: mp .. mp + 999 (slot 0's) and mp + 1000 .. 2 mp - 1 (slot 2's), mp pages, which go to 0 .. mp - 1
+    assert copies[0].tolist() == [mp, 0, n - mp, 0] and (ref[:mp] == 1).all() and (ref[mp:] == 0).all()
+    assert torch.equal(copies[1:, 0], torch.arange(mp, 2 * mp, **i32)) and torch.equal(copies[1:, 1], torch.arange(mp, **i32))
+    assert torch.equal(table, torch.where(before >= 0, before - mp, before))
+    assert (new_id[:mp] == -1).all() and torch.equal(new_id[mp:], torch.arange(mp, **i32))
 
 
 @pytest.mark.gpu
