@@ -213,14 +213,17 @@ struct Update {
     // The rest of what slot b gives up, and what it takes over, by `lanes` threads.  (Pages that it holds in the same place
     // before and after, as when the same prompt is forked again, are left alone.)
     __device__ __forceinline__ void move(int b, int lane, int lanes) const {
-        const int4 s = get(u.slot + b), at = get(u.place + b);
+        const int4 at = get(u.place + b);
+        move(b, get(u.slot + b), at.z, at.w, lane, lanes);
+    }
+    __device__ __forceinline__ void move(int b, const int4& s, int flags, int from, int lane, int lanes) const {
         const int kept_n = pages(s.x);
-        if (!(at.z & kSlotOther)) {
+        if (!(flags & kSlotOther)) {
             entries(row(b), s.z, nullptr, 0, kept_n + 2, lane, lanes, [&](int, int id, int) { add(id, -1); });
             return;
         }
-        int32_t* const to = at.z & kSlotStaged ? stage(b) : nullptr;
-        entries(row(b), s.z, kept_n > 0 ? row(at.w) : nullptr, kept_n, 0, lane, lanes, [&](int j, int old, int id) {
+        int32_t* const to = flags & kSlotStaged ? stage(b) : nullptr;
+        entries(row(b), s.z, kept_n > 0 ? row(from) : nullptr, kept_n, 0, lane, lanes, [&](int j, int old, int id) {
             if (old != id) {
                 add(old, -1);
                 add(id, 1);
@@ -403,13 +406,18 @@ __global__ void __launch_bounds__(kStepThreads) pages_count_kernel(const __grid_
     const int groups = gridDim.x * (kStepThreads / kStepLanes), group = blockIdx.x * (kStepThreads / kStepLanes) + threadIdx.x / kStepLanes;
     const int lane = threadIdx.x % kStepLanes;
     for (int64_t b = group; b < p.n_seqs; b += groups) {
+        Update<false>::Entry e = {};
         if (lane == 0) {
-            auto e = x.ask((int)b);
+            e = x.ask((int)b);
             x.look_up((int)b, e);
             x.enter((int)b, e);
         }
-        __syncwarp();
-        x.move((int)b, lane, kStepLanes);
+        int4 slot;
+        slot.x = __shfl_sync(~0u, e.slot.x, 0);
+        slot.y = __shfl_sync(~0u, e.slot.y, 0);
+        slot.z = __shfl_sync(~0u, e.slot.z, 0);
+        slot.w = __shfl_sync(~0u, e.slot.w, 0);
+        x.move((int)b, slot, __shfl_sync(~0u, e.flags, 0), __shfl_sync(~0u, e.parent, 0), lane, kStepLanes);
     }
 }
 
@@ -443,19 +451,27 @@ __global__ void __launch_bounds__(kThreads, 1) pages_number_kernel(const __grid_
         said[2] = sum;
     }
     cluster_sync();
-    int64_t need = 0, copies = 0, free_n = 0, left = 0, need_at = 0, copies_at = 0, free_at = 0;
-    for (int c = 0; c < kCtas; ++c) {
-        const uint64_t a = cluster_read(&said[0], c), b = cluster_read(&said[1], c), f = cluster_read(&said[2], c);
-        if (c < rank) {
-            need_at += a;
-            copies_at += b;
-            free_at += (uint32_t)f;
-        }
-        need += a;
-        copies += b;
-        free_n += (uint32_t)f;
-        left += f >> 32;
+    // all CTAs' numbers, and those of the ones before this
+    uint64_t told[3], earlier[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        told[k] = lane < kCtas ? cluster_read(&said[k], lane) : 0;
+        earlier[k] = lane < rank ? told[k] : 0;
     }
+#pragma unroll
+    for (int o = kCtas / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            told[k] += __shfl_xor_sync(~0u, told[k], o);
+            earlier[k] += __shfl_xor_sync(~0u, earlier[k], o);
+        }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        told[k] = __shfl_sync(~0u, told[k], 0);
+        earlier[k] = __shfl_sync(~0u, earlier[k], 0);
+    }
+    const int64_t need = told[0], copies = told[1], free_n = (uint32_t)told[2], left = told[2] >> 32, free_at = (uint32_t)earlier[2];
+    int64_t need_at = earlier[0], copies_at = earlier[1];
     cluster_arrive();  // (waited for at the end: others may still read what this CTA says)
     if (rank == 0 && threadIdx.x == 0) {
         x.head(need, free_n, copies, left);
