@@ -76,9 +76,9 @@ struct Books {
     uint32_t* first;    // [n_pages]: the first of those, kNobody
     int32_t* free_ids;  // [n_pages]: free pages, lowest first
     int4* slot;         // [n_seqs]: tokens kept, tokens afterwards, pages held before, the page that ends inside (-1: none)
-    int4* place;        // [n_seqs]: what it needs begins here; place of its copy in the list, -1; kSlot...; parent
+    int4* place;        // [n_seqs]: where the pages it gets begin, its copy's place in the list (-1: none), kSlot flags, parent
     int32_t* stage;     // [n_seqs][max_pages]: rows of slots that change places (workspace in any case)
-    int64_t* totals;    // pages needed, free pages, copies, pages free before
+    int64_t* totals;    // pages needed, free pages (as many at least, or fewer)
 };
 enum : int { kSlotOther = 1, kSlotStaged = 2, kSlotWrites = 4 };
 
@@ -99,7 +99,7 @@ __host__ __device__ inline size_t layout(int n_seqs, int max_pages, int n_pages,
         at += (bytes + 255) / 256 * 256;
         return p;
     };
-    u->totals = reinterpret_cast<int64_t*>(take(4 * sizeof(int64_t)));
+    u->totals = reinterpret_cast<int64_t*>(take(2 * sizeof(int64_t)));
     u->count = reinterpret_cast<int32_t*>(take(4 * (size_t)n_pages));
     u->first = reinterpret_cast<uint32_t*>(take(4 * (size_t)n_pages));
     u->free_ids = reinterpret_cast<int32_t*>(take(4 * (size_t)n_pages));
@@ -275,60 +275,14 @@ struct Update {
     }
 };
 
-__global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_constant__ PagesUpdateParams p, int32_t* stage) {
-    extern __shared__ int4 smem[];
-    __shared__ uint64_t part[kWarps];
-    __shared__ uint32_t sums[3][kWarps];
-    __shared__ uint16_t long_rows[kOneSeqs];  // (in any order: counts are added up, rows written by themselves)
-    __shared__ int n_long;
-    constexpr int kRounds = kOnePages / kThreads;
-    Books u;
-    u.slot = smem;
-    u.place = u.slot + p.n_seqs;
-    u.count = reinterpret_cast<int32_t*>(u.place + p.n_seqs);
-    u.first = reinterpret_cast<uint32_t*>(u.count + p.n_pages);
-    u.free_ids = reinterpret_cast<int32_t*>(u.first + p.n_pages);
-    u.stage = stage;
-    const Update<true> x{p, u};
-    using Entry = Update<true>::Entry;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int b = threadIdx.x;  // (one slot to a thread: kOneSeqs of them at most)
-    begin_kernel(false);
-    Entry e;
-    if (b < p.n_seqs) e = x.ask(b);
-    if (threadIdx.x == 0) n_long = 0;
-    {
-        int c[kRounds];
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r) c[r] = b + r * kThreads < p.n_pages ? __ldcg(p.ref + b + r * kThreads) : 0;
-        if (b < p.n_seqs) x.look_up(b, e);  // (its loads are under way with the counts')
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            const int i = b + r * kThreads;
-            if (i >= p.n_pages) break;
-            u.count[i] = c[r];
-            u.first[i] = kNobody;
-        }
-    }
-    __syncthreads();
-    if (b < p.n_seqs) x.enter(b, e);
-    __syncthreads();
-    // rows are short, or many, or both: each has its share of the threads, but 8; a long one all of them, after the others
-    const int lanes = max(8, kThreads >> (32 - __clz(max(p.n_seqs, 1) - 1)));
-    const int group = threadIdx.x / lanes, row_lane = threadIdx.x % lanes;
-    auto is_long = [&](int s) { return x.reads(s) > 64 * lanes; };
-    for (int s = group; s < p.n_seqs; s += kThreads / lanes) {
-        if (!is_long(s))
-            x.move(s, row_lane, lanes);
-        else if (row_lane == 0)
-            long_rows[atomicAdd(&n_long, 1)] = (uint16_t)s;
-    }
-    __syncthreads();
-    if (n_long > 0) {
-        for (int k = 0; k < n_long; ++k) x.move(long_rows[k], threadIdx.x, kThreads);
-        __syncthreads();
-    }
+// Numbers of a cache of up to kOnePages pages and kOneSeqs slots, by one CTA (a slot to a thread): where the pages that each slot
+// gets begin, copies' places in the list, free pages in order, and the list's head.  Returns the pages needed, -1 if they lack.
+constexpr int kRounds = kOnePages / kThreads;
 
+template <bool ONE>
+__device__ __forceinline__ int64_t number(const Update<ONE>& x, uint32_t (&sums)[3][kWarps], uint64_t (&part)[kWarps]) {
+    const PagesUpdateParams& p = x.p;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, b = threadIdx.x;
     // Running sums of what the slots need (a slot's at most 2^15, more than there are pages), of copies, and of free pages: a warp
     // has up to kRounds times 32 pages, a lane's as bits.
     const uint64_t mine = b < p.n_seqs ? x.needs(b) : 0;
@@ -366,21 +320,79 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
         block_scan(mine & ((1ull << 40) - 1), &all_need, part);
         block_scan(held, &all_held, part);
         if (threadIdx.x == 0) x.head(all_need, free_n, copies, all_held);
-        return;
+        return -1;
     }
     if (threadIdx.x == 0) x.head(need, free_n, copies, 0);
     if (b < p.n_seqs) {
-        u.place[b].x = (int)need_at;
-        if (copies_own) u.place[b].y = (int)copies_at;
+        x.u.place[b].x = (int)need_at;
+        if (copies_own) x.u.place[b].y = (int)copies_at;
     }
     if (free_at < need) {
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
             const uint32_t m = __ballot_sync(~0u, free_bits >> r & 1);
-            if (free_bits >> r & 1) u.free_ids[free_at + __popc(m & ((1u << lane) - 1))] = w0 + 32 * r + lane;
+            if (free_bits >> r & 1) x.u.free_ids[free_at + __popc(m & ((1u << lane) - 1))] = w0 + 32 * r + lane;
             free_at += __popc(m);
         }
     }
+    return need;
+}
+
+__global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_constant__ PagesUpdateParams p, int32_t* stage) {
+    extern __shared__ int4 smem[];
+    __shared__ uint64_t part[kWarps];
+    __shared__ uint32_t sums[3][kWarps];
+    __shared__ uint16_t long_rows[kOneSeqs];  // (in any order: counts are added up, rows written by themselves)
+    __shared__ int n_long;
+    Books u;
+    u.slot = smem;
+    u.place = u.slot + p.n_seqs;
+    u.count = reinterpret_cast<int32_t*>(u.place + p.n_seqs);
+    u.first = reinterpret_cast<uint32_t*>(u.count + p.n_pages);
+    u.free_ids = reinterpret_cast<int32_t*>(u.first + p.n_pages);
+    u.stage = stage;
+    const Update<true> x{p, u};
+    using Entry = Update<true>::Entry;
+    const int b = threadIdx.x;  // (one slot to a thread: kOneSeqs of them at most)
+    begin_kernel(false);
+    Entry e;
+    if (b < p.n_seqs) e = x.ask(b);
+    if (threadIdx.x == 0) n_long = 0;
+    {
+        int c[kRounds];
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) c[r] = b + r * kThreads < p.n_pages ? __ldcg(p.ref + b + r * kThreads) : 0;
+        if (b < p.n_seqs) x.look_up(b, e);  // (its loads are under way with the counts')
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const int i = b + r * kThreads;
+            if (i >= p.n_pages) break;
+            u.count[i] = c[r];
+            u.first[i] = kNobody;
+        }
+    }
+    __syncthreads();
+    if (b < p.n_seqs) x.enter(b, e);
+    __syncthreads();
+    // rows are short, or many, or both: each has its share of the threads, but 8; a long one all of them, after the others
+    const int lanes = max(8, kThreads >> (32 - __clz(max(p.n_seqs, 1) - 1)));
+    const int group = threadIdx.x / lanes, row_lane = threadIdx.x % lanes;
+    auto is_long = [&](int s) { return x.reads(s) > 64 * lanes; };
+    for (int s = group; s < p.n_seqs; s += kThreads / lanes) {
+        if (!is_long(s))
+            x.move(s, row_lane, lanes);
+        else if (row_lane == 0)
+            long_rows[atomicAdd(&n_long, 1)] = (uint16_t)s;
+    }
+    __syncthreads();
+    if (n_long > 0) {
+        for (int k = 0; k < n_long; ++k) x.move(long_rows[k], threadIdx.x, kThreads);
+        __syncthreads();
+    }
+
+    // what lacks changes nothing
+    const int64_t need = number<true>(x, sums, part);
+    if (need < 0) return;
     __syncthreads();
     const int taken = need > 0 ? u.free_ids[need - 1] : -1;
     for (int i = threadIdx.x; i < p.n_pages; i += kThreads) x.commit(i, taken);
@@ -396,7 +408,6 @@ constexpr int kStepLanes = 32;  // to a row
 __global__ void __launch_bounds__(kStepThreads) pages_init_kernel(const __grid_constant__ PagesUpdateParams p, const Books u) {
     const Update<false> x{p, u};
     begin_kernel(false);
-    if (blockIdx.x == 0 && threadIdx.x < 4) u.totals[threadIdx.x] = 0;
     x.init(blockIdx.x * kStepThreads + threadIdx.x, gridDim.x * kStepThreads);
 }
 
@@ -418,6 +429,18 @@ __global__ void __launch_bounds__(kStepThreads) pages_count_kernel(const __grid_
         slot.z = __shfl_sync(~0u, e.slot.z, 0);
         slot.w = __shfl_sync(~0u, e.slot.w, 0);
         x.move((int)b, slot, __shfl_sync(~0u, e.flags, 0), __shfl_sync(~0u, e.parent, 0), lane, kStepLanes);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) pages_number_one_kernel(const __grid_constant__ PagesUpdateParams p, const Books u) {
+    __shared__ uint64_t part[kWarps];
+    __shared__ uint32_t sums[3][kWarps];
+    const Update<false> x{p, u};
+    begin_kernel(false);
+    const int64_t need = number<false>(x, sums, part);
+    if (threadIdx.x == 0) {
+        u.totals[0] = max(need, (int64_t)0);
+        u.totals[1] = need < 0 ? -1 : need;
     }
 }
 
@@ -702,7 +725,10 @@ cudaError_t launch_pages_update(const PagesUpdateParams& p, cudaStream_t stream)
     const auto ctas = [](int64_t threads) { return dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>((threads + 255) / 256, 8 * 152))); };
     cudaError_t e = launch_dependent(pages_init_kernel, ctas(p.n_pages), kStepThreads, 0, stream, p, u);
     if (e == cudaSuccess) e = launch_dependent(pages_count_kernel, ctas((int64_t)kStepLanes * p.n_seqs), kStepThreads, 0, stream, p, u);
-    if (e == cudaSuccess) e = launch_clusters(pages_number_kernel, 1, kCtas, kThreads, 0, stream, p, u);
+    if (e == cudaSuccess)
+        e = p.n_pages <= kOnePages && p.n_seqs <= kOneSeqs
+                ? launch_dependent(pages_number_one_kernel, dim3(1), kThreads, 0, stream, p, u)
+                : launch_clusters(pages_number_kernel, 1, kCtas, kThreads, 0, stream, p, u);
     const int64_t threads = std::max<int64_t>((int64_t)kStepLanes * p.n_seqs, p.n_pages);
     if (e == cudaSuccess) e = launch_dependent(pages_write_kernel, ctas(threads), kStepThreads, 0, stream, p, u);
     return e;
