@@ -284,14 +284,13 @@ __device__ __forceinline__ int64_t number(const Update<ONE>& x, uint32_t (&sums)
     const PagesUpdateParams& p = x.p;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, b = threadIdx.x;
     // Running sums of what the slots need (a slot's at most 2^15, more than there are pages), of copies, and of free pages: a warp
-    // has up to kRounds times 32 pages, a lane's as bits.
+    // has 32 pages a round, a lane's as bits.
     const uint64_t mine = b < p.n_seqs ? x.needs(b) : 0;
-    const int w0 = warp * ((p.n_pages + kThreads - 1) / kThreads * 32);
-    const int w1 = min(w0 + (p.n_pages + kThreads - 1) / kThreads * 32, p.n_pages);
+    const int rounds = (p.n_pages + kThreads - 1) / kThreads, w0 = warp * 32 * rounds;
     uint32_t free_bits = 0;
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r)
-        if (w0 + 32 * r + lane < w1 && x.is_free(w0 + 32 * r + lane)) free_bits |= 1u << r;
+#pragma unroll 4
+    for (int r = 0; r < rounds; ++r)
+        if (w0 + 32 * r + lane < p.n_pages && x.is_free(w0 + 32 * r + lane)) free_bits |= 1u << r;
     uint32_t need_to = (uint32_t)min(mine & ((1ull << 40) - 1), 1ull << 15), copies_to = (uint32_t)(mine >> 40);
     const uint32_t need_own = need_to, copies_own = copies_to, free_own = __reduce_add_sync(~0u, __popc(free_bits));
 #pragma unroll
@@ -328,8 +327,7 @@ __device__ __forceinline__ int64_t number(const Update<ONE>& x, uint32_t (&sums)
         if (copies_own) x.u.place[b].y = (int)copies_at;
     }
     if (free_at < need) {
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
+        for (int r = 0; r < rounds; ++r) {
             const uint32_t m = __ballot_sync(~0u, free_bits >> r & 1);
             if (free_bits >> r & 1) x.u.free_ids[free_at + __popc(m & ((1u << lane) - 1))] = w0 + 32 * r + lane;
             free_at += __popc(m);
@@ -546,41 +544,99 @@ __device__ __forceinline__ void rename(const PagesCompactParams& p, int64_t at, 
     }
 }
 
-// Live pages with ids from their number on go, lowest first, to the free ids below it, lowest first.  C CTAs each take a share of
-// the pages; who is live stays in shared memory, a bit for each page.  One CTA also renames the entries of a small table.
-template <int C>
-__global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_constant__ PagesCompactParams p) {
+// Live pages with ids from their number on go, lowest first, to the free ids below it, lowest first.
+//
+// Up to kOneCompact pages by one CTA, their counts in its shared memory; who moves where is exchanged there, too.  It also renames
+// the entries of a small table.  (Loops of as many rounds as there are pages for: written out for all kRounds, the code, run
+// through once, came to 9.4 us for 125 pages instead of 2.6.  9104 pages take it 8.9, the cluster below 8.8.)
+constexpr int kOneCompact = 8192;
+
+__global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const __grid_constant__ PagesCompactParams p) {
+    extern __shared__ int32_t counts[];  // [n_pages], then the ids that move and those that they go to, [n_pages / 2]
+    uint16_t* const movers = reinterpret_cast<uint16_t*>(counts + p.n_pages);
+    uint16_t* const holes = movers + p.n_pages / 2;
+    __shared__ uint32_t sums[2][kWarps];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rounds = (p.n_pages + kThreads - 1) / kThreads, w0 = warp * 32 * rounds;  // (a warp has 32 pages a round)
+    auto page = [&](int r) { return w0 + 32 * r + lane; };
+    begin_kernel(false);
+    uint32_t live = 0;
+#pragma unroll 4
+    for (int r = 0; r < rounds; ++r) {
+        if (page(r) >= p.n_pages) break;
+        const int c = __ldcg(p.ref + page(r));
+        counts[page(r)] = c;
+        live |= (uint32_t)(c > 0) << r;
+    }
+    const uint32_t live_here = __reduce_add_sync(~0u, __popc(live));
+    if (lane == 0) sums[0][warp] = live_here;
+    __syncthreads();
+    const int n_live = (int)__reduce_add_sync(~0u, sums[0][lane]);
+    uint32_t moves = 0, filled = 0;  // this lane's pages that move, and free ones that are filled
+    for (int r = 0; r < rounds; ++r) {
+        const int i = page(r);
+        const bool alive = live >> r & 1;
+        moves |= (uint32_t)(i >= n_live && alive) << r;
+        filled |= (uint32_t)(i < n_live && !alive) << r;
+    }
+    // (as many of the one as of the other, n_pages / 2 at most: both in a word)
+    const uint32_t here = __reduce_add_sync(~0u, (uint32_t)__popc(moves) | (uint32_t)__popc(filled) << 16);
+    if (lane == 0) sums[1][warp] = here;
+    __syncthreads();
+    const uint32_t v = sums[1][lane], all = __reduce_add_sync(~0u, v), before = __reduce_add_sync(~0u, lane < warp ? v : 0);
+    // f(move's and filling's place in the order, page, whether it moves, whether it is filled) for this lane's pages
+    auto each = [&](auto&& f) {
+        int at_moves = before & 0xffff, at_holes = before >> 16;
+        for (int r = 0; r < rounds; ++r) {
+            const bool x = moves >> r & 1, y = filled >> r & 1;
+            const uint32_t m = __ballot_sync(~0u, x), h = __ballot_sync(~0u, y), less = (1u << lane) - 1;
+            f(at_moves + __popc(m & less), at_holes + __popc(h & less), page(r), x, y);
+            at_moves += __popc(m);
+            at_holes += __popc(h);
+        }
+    };
+    each([&](int k, int l, int i, bool x, bool y) {
+        if (x) movers[k] = (uint16_t)i;
+        if (y) holes[l] = (uint16_t)i;
+    });
+    __syncthreads();
+    // (every count has been read: ref_out may be ref)
+    int4* rows = reinterpret_cast<int4*>(p.copies) + 1;
+    if (threadIdx.x == 0) rows[-1] = make_int4((int)(all & 0xffff), 0, p.n_pages - n_live, 0);
+    each([&](int k, int l, int i, bool x, bool y) {
+        if (i >= p.n_pages) return;
+        const int from = y ? movers[l] : i, c = counts[from];
+        if (y) rows[l] = make_int4(from, i, 1 << p.page_log2, 0);
+        p.ref_out[i] = x ? 0 : max(c, 0);
+        p.new_id[i] = x ? holes[k] : c > 0 && !y ? i : -1;
+    });
+    if (!p.rename) return;
+    __syncthreads();
+    rename(p, threadIdx.x, kThreads);
+}
+
+// More pages by a cluster, whose CTAs each take a share of them; who is live stays in shared memory, a bit for each page.
+__global__ void __launch_bounds__(kThreads) pages_compact_cluster_kernel(const __grid_constant__ PagesCompactParams p) {
     extern __shared__ uint32_t bits[];
     __shared__ uint64_t part[kWarps];
     __shared__ uint64_t said[2];  // to the cluster: its live pages; those that move | free ids that are filled << 32
-    const int rank = C > 1 ? (int)cluster_rank() : 0, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = (int)cluster_rank(), warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     // (shares in whole words of bits)
     const int words = (p.n_pages + 31) / 32;
-    const int c0 = share(0, words, rank, C), c1 = share(0, words, rank + 1, C);
+    const int c0 = share(0, words, rank, kCtas), c1 = share(0, words, rank + 1, kCtas);
     const int v0 = share(c0, c1, warp, kWarps), v1 = share(c0, c1, warp + 1, kWarps);
     const int w0 = 32 * v0, w1 = min(32 * v1, p.n_pages);
-    auto sync = [] {
-        if constexpr (C > 1)
-            cluster_sync();
-        else
-            __syncthreads();
-    };
     auto tell = [&](int k, uint64_t mine, uint64_t* before) {  // the sum over the CTAs, and over those before this one
-        if constexpr (C == 1) {
-            *before = 0;
-            return mine;
-        } else {
-            if (threadIdx.x == 0) said[k] = mine;
-            cluster_sync();
-            uint64_t all = lane < C ? cluster_read(&said[k], lane) : 0, less = lane < rank ? all : 0;
+        if (threadIdx.x == 0) said[k] = mine;
+        cluster_sync();
+        uint64_t all = lane < kCtas ? cluster_read(&said[k], lane) : 0, less = lane < rank ? all : 0;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                all += __shfl_xor_sync(~0u, all, o);
-                less += __shfl_xor_sync(~0u, less, o);
-            }
-            *before = less;
-            return all;
+        for (int o = 16; o > 0; o >>= 1) {
+            all += __shfl_xor_sync(~0u, all, o);
+            less += __shfl_xor_sync(~0u, less, o);
         }
+        *before = less;
+        return all;
     };
     begin_kernel(false);
     int mine = 0;
@@ -624,7 +680,7 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
             }
         }
     }
-    sync();
+    cluster_sync();
     // (from here on counts of pages that move are read, each by the one that then clears it)
     int done = 0;
     for (int i0 = w0; i0 < min(w1, n_live); i0 += 4 * 32) {
@@ -650,11 +706,6 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
             p.ref_out[i] = count[e];
             p.ref_out[from[e]] = 0;
         }
-    }
-    if constexpr (C == 1) {
-        if (!p.rename) return;
-        __syncthreads();
-        rename(p, threadIdx.x, kThreads);
     }
 }
 
@@ -735,19 +786,19 @@ cudaError_t launch_pages_update(const PagesUpdateParams& p, cudaStream_t stream)
 }
 
 cudaError_t launch_pages_compact(const PagesCompactParams& params, cudaStream_t stream) {
-    // (one CTA up to so many pages: 5.0 us for 125 pages, 12.3 for 9104; a cluster of eight 7.2 and 8.8)
-    constexpr int kOne = 4096;
     PagesCompactParams p = params;
+    const bool one = p.n_pages <= kOneCompact;
     const int64_t entries = (int64_t)p.n_seqs * p.max_pages;
-    p.rename = p.n_pages <= kOne && entries <= 8 * kThreads;  // (one round of that CTA; a launch for it 2 us more)
-    const int words = (p.n_pages + 31) / 32;
+    p.rename = one && entries <= 8 * kThreads;  // (one round of that CTA; a launch for it 2 us more)
     cudaError_t e;
-    if (p.n_pages <= kOne) {
-        e = launch_dependent(pages_compact_kernel<1>, dim3(1), kThreads, 4 * (size_t)words, stream, p);
+    if (one) {
+        e = allow_smem<pages_compact_kernel>(6 * kOneCompact);
+        if (e == cudaSuccess) e = launch_dependent(pages_compact_kernel, dim3(1), kThreads, 6 * (size_t)p.n_pages, stream, p);
     } else {
-        e = allow_smem<pages_compact_kernel<kCtas>>((1 << 23) / 8 / kCtas + 4);
+        const int words = (p.n_pages + 31) / 32;
+        e = allow_smem<pages_compact_cluster_kernel>((1 << 23) / 8 / kCtas + 4);
         if (e == cudaSuccess)
-            e = launch_clusters(pages_compact_kernel<kCtas>, 1, kCtas, kThreads, 4 * (size_t)((words + kCtas - 1) / kCtas), stream, p);
+            e = launch_clusters(pages_compact_cluster_kernel, 1, kCtas, kThreads, 4 * (size_t)((words + kCtas - 1) / kCtas), stream, p);
     }
     if (e != cudaSuccess || entries == 0 || p.rename) return e;
     return launch_dependent(pages_rename_kernel, dim3((unsigned)std::min<int64_t>((entries + 255) / 256, 8 * 152)), 256, 0, stream, p);

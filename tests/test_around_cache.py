@@ -746,7 +746,7 @@ def test_sequences_keep_their_tokens(usp, dtype, Hkv, d, page):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("n,B,mp,live", [(1, 1, 1, 1.0), (2, 1, 2, 0.5), (300, 12, 31, 0.6), (4097, 50, 70, 0.3), (40000, 3, 7, 0.9),
-                                         (1000, 4, 4, 0.0), (1000, 300, 3, 1.0), (0, 2, 2, 0.0),
+                                         (1000, 4, 4, 0.0), (1000, 300, 3, 1.0), (0, 2, 2, 0.0), (8192, 5, 9, 0.5), (8193, 5, 9, 0.5), (9104, 127, 297, 0.5),
                                          (70001, 9, 50, 0.5), (300000, 2, 9, 0.2)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_pages_compact(usp, n, B, mp, live, in_place):
