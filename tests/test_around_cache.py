@@ -1214,3 +1214,78 @@ def test_tensors_that_the_calls_cannot_take(usp):
     with pytest.raises((TypeError, ValueError)):
         usp.usp_rotary_embed(p, R3, q, None, pos, f, q, None, stream="a text")
     assert usp.usp_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_verify_long_runs_and_rows_apart(usp, dtype):
+    """Drafts that are all accepted, more than a warp looks at together, and rows of the two distributions at distances of
+    their own."""
+    import torch
+    rng = np.random.default_rng(2)
+    x = _drafts(rng, [70, 33, 34, 2], 900, dtype, gap=4)
+    x["dr"] = torch.full((139, 916), float("nan"), dtype=x["tg"].dtype, device="cuda")[:, :900]
+    x["dr"].copy_(x["tg"].roll(1, 0))                     # row t is what row t - 1 of the target says: nothing is refused
+    x["target"], x["draft"] = _np(x["tg"]), _np(x["dr"])
+    x["tokens"] = np.array([int(rng.choice(np.flatnonzero(r > 0))) for r in x["draft"]], np.int32)
+    got = _verify(usp, x)
+    assert got[0].tolist() == [69, 32, 33, 1]
+    x["tokens"][1 + 40] = 900                             # the first: its 41st draft is no token
+    assert _verify(usp, x)[0].tolist() == [40, 32, 33, 1]
+
+
+@pytest.mark.gpu
+def test_copies_in_layers_apart_and_an_append_without_queries(usp):
+    import torch
+    c = usp.Cache(6, 16, 2, 3, 4, 2, 64)
+    kp, vp = (torch.randn((3, 9, 2, 16, 64), device="cuda").bfloat16() for _ in range(2))   # three pages between the layers' pools
+    want = [x.clone() for x in (kp, vp)]
+    copies = torch.tensor([[2, 0, 0, 0], [5, 0, 16, 0], [1, 4, 3, 0]], dtype=torch.int32, device="cuda")
+    usp.usp_pages_copy(c, 2, copies, kp.data_ptr(), vp.data_ptr(), 3, 9 * 2 * 16 * 64)
+    torch.cuda.synchronize()
+    for x, y in zip((kp, vp), want):
+        y[:, 0], y[:, 4, :, :3] = y[:, 5].clone(), y[:, 1, :, :3].clone()
+        assert torch.equal(x, y)
+    # keys and values alone, and q and k of one tensor rotated in place together
+    r = usp.Rotary.sections((12, 10, 10))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    T, f = 20, _dev(_freq(32))
+    table, seq, pos = torch.arange(6, **i32).view(2, 3), torch.arange(T, **i32) % 2, torch.arange(T, **i32) // 2
+    rot = torch.randint(0, 99, (3, T), device="cuda").int()
+    qkv = torch.randn((T, 8, 64), device="cuda").bfloat16()
+    q, k, v = qkv[:, :4], qkv[:, 4:6], qkv[:, 6:]
+    pools = [[torch.zeros(c.pool_shape(), dtype=torch.bfloat16, device="cuda") for _ in range(2)] for _ in range(2)]
+    none, k_out = usp.kv_append_axes(c, r, None, k, v, seq, pos, rot, f, *pools[0], table)
+    q_out, k_out2 = usp.kv_append_axes(c, r, q, k, v, seq, pos, rot, f, *pools[1], table)
+    assert none is None and torch.equal(k_out, k_out2) and all(torch.equal(a, b) for a, b in zip(*pools))
+    p = usp.Problem(1, 4, 2, T, 64, 1)
+    v0 = v.clone()
+    usp.usp_rotary_embed(p, r, q, k, rot, f, q, k)
+    torch.cuda.synchronize()
+    assert torch.equal(q, q_out) and torch.equal(k, k_out) and torch.equal(v, v0)
+
+
+@pytest.mark.gpu
+def test_traced_calls_are_on_record(usp):
+    import torch
+    c = usp.Cache(40, 16, 3, 20, 1, 1, 64)
+    kp, vp = (torch.zeros(c.pool_shape(), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x = _drafts(np.random.default_rng(1), [3, 2], 300, "f32")
+    grow = torch.full((3,), 30, dtype=torch.int32, device="cuda")
+    results = []
+    for on in (False, True):
+        usp.usp_trace_enable(on)
+        usp.usp_trace_reset()
+        lens, table, ref = usp.pages_empty(c)
+        for _ in range(2):
+            copies = usp.pages_update(c, lens, table, ref, grow=grow)
+            usp.pages_copy(c, copies, kp, vp)
+        usp.pages_compact(c, table, ref)
+        out = usp.verify_drafts(x["tg"], x["dr"], _dev(x["tokens"]), _dev(x["u"]), _dev(x["q_start"]), _dev(x["lens"]))
+        torch.cuda.synchronize()
+        results.append([t.tolist() for t in (lens, table, ref, *out)])
+    report = usp.usp_trace_report()
+    usp.usp_trace_enable(False)
+    usp.usp_trace_reset()
+    assert results[0] == results[1]
+    assert {k: n for k, (n, _) in report.items()} == {"pages_update": 2, "pages_copy": 2, "pages_compact": 1, "verify_drafts": 1}
