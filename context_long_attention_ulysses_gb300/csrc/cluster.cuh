@@ -27,6 +27,13 @@ __device__ __forceinline__ uint64_t cluster_read(const uint64_t* p, uint32_t ran
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
     return v;
 }
+__device__ __forceinline__ ulonglong2 cluster_read(const ulonglong2* p, uint32_t rank) {
+    uint32_t a;
+    ulonglong2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(a) : "memory");
+    return v;
+}
 
 // A dependent launch (paged.cuh) of clusters of `size` CTAs each.
 template <typename... P, typename... A>

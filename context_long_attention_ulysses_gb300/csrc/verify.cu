@@ -116,9 +116,9 @@ __device__ __forceinline__ uint64_t fixed64(float u) {
     return shift >= 0 ? m << shift : m >> min(-shift, 63);
 }
 
-// A tile's sum is below 2^56 and a warp's below 2^64.  Warps' and CTAs' sums stop at 2^60, so that the cluster's does not overflow
-// for rows which are no probabilities (thousands of ones), and these still lead to a token.
-constexpr uint64_t kMost = 1ull << 60;
+// A tile's sum is 2^55 at most, a warp's 2^63, a row's 2^65 (of 2^19 ones; rows need not add up to 1): 128 bits from the CTA's
+// on, so that a token does not depend on how many CTAs its sequence has.
+using Wide = unsigned __int128;
 
 __device__ __forceinline__ uint64_t warp_scan(uint64_t x, int lane) {  // inclusive
 #pragma unroll
@@ -128,14 +128,17 @@ __device__ __forceinline__ uint64_t warp_scan(uint64_t x, int lane) {  // inclus
     }
     return x;
 }
-// The sum over the lanes, to all: in pieces that the warp's own addition takes; SMALL: of numbers below 2^50.
-template <bool SMALL>
+// The sum over the lanes, to all, in pieces that the warp's own addition takes: of numbers of 2^50 at most, or 2^65.
 __device__ __forceinline__ uint64_t lanes_total(uint64_t x) {
+    const uint32_t a = __reduce_add_sync(~0u, (uint32_t)x & ((1u << 26) - 1));
+    return a + ((uint64_t)__reduce_add_sync(~0u, (uint32_t)(x >> 26)) << 26);
+}
+__device__ __forceinline__ Wide lanes_total_wide(Wide x) {
     constexpr uint32_t kPiece = (1u << 26) - 1;
-    const uint32_t a = __reduce_add_sync(~0u, (uint32_t)x & kPiece);
-    if constexpr (SMALL) return a + ((uint64_t)__reduce_add_sync(~0u, (uint32_t)(x >> 26)) << 26);
-    const uint32_t b = __reduce_add_sync(~0u, (uint32_t)(x >> 26) & kPiece), c = __reduce_add_sync(~0u, (uint32_t)(x >> 52));
-    return a + ((uint64_t)b << 26) + ((uint64_t)c << 52);
+    const uint64_t low = (uint64_t)x;
+    const uint32_t a = __reduce_add_sync(~0u, (uint32_t)low & kPiece), b = __reduce_add_sync(~0u, (uint32_t)(low >> 26) & kPiece);
+    const uint32_t c = __reduce_add_sync(~0u, (uint32_t)(x >> 52));
+    return a + ((Wide)b << 26) + ((Wide)c << 52);
 }
 
 template <int N>
@@ -190,7 +193,7 @@ struct Weights {
                     d.add(x);
                 }
             }
-            sum[k] = lanes_total<true>(d.whole());
+            sum[k] = lanes_total(d.whole());
             const int j = except - (i + k * step);
             if (!Q && j >= 0 && j < kLength) sum[k] -= fixed46(value(p + except));
         }
@@ -227,7 +230,7 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams p, int size) {
     __shared__ uint64_t tile_sum[kMaxVocab / kTile<T, VEC> + 1];  // (rows begin inside a vector)
     __shared__ uint64_t warp_total[kWarps];
-    __shared__ uint64_t cta_total[2];   // (a place for each of two goes)
+    __shared__ ulonglong2 cta_total[2];   // low and high word (a place for each of two goes)
     constexpr int E = kEach<T, VEC>, kLength = kTile<T, VEC>;
     const int rank = (int)cluster_rank(), b = blockIdx.x / size;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -279,18 +282,19 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
     const int all = (w.to + kLength - 1) / kLength;
     const int first = all * rank / size, end = all * (rank + 1) / size;  // this CTA's tiles
 
-    uint64_t total = 0, mine = 0, before = 0;
+    Wide total = 0, mine = 0, before = 0;
     for (int go = 0; go < 2; ++go) {
         const uint64_t sum = w.q ? w.template slice<true>(first, end, warp, lane, tile_sum)
                                  : w.template slice<false>(first, end, warp, lane, tile_sum);
-        if (lane == 0) warp_total[warp] = min(sum, kMost);
+        if (lane == 0) warp_total[warp] = sum;
         __syncthreads();
-        mine = min(lanes_total<false>(lane < kWarps ? warp_total[lane] : 0), kMost);
-        if (threadIdx.x == 0) cta_total[go] = mine;
+        mine = lanes_total_wide(lane < kWarps ? warp_total[lane] : 0);
+        if (threadIdx.x == 0) cta_total[go] = make_ulonglong2((uint64_t)mine, (uint64_t)(mine >> 64));
         cluster_sync();
-        const uint64_t x = lane < size ? cluster_read(&cta_total[go], lane) : 0;
-        total = lanes_total<false>(x);
-        before = lanes_total<false>(lane < rank ? x : 0);
+        const ulonglong2 said = lane < size ? cluster_read(&cta_total[go], lane) : make_ulonglong2(0, 0);
+        const Wide x = (Wide)said.y << 64 | said.x;
+        total = lanes_total_wide(x);
+        before = lanes_total_wide(lane < rank ? x : 0);
         if (total > 0 || (!w.q && w.except < 0)) break;
         // nothing is left of the row (q >= p throughout, as rounded): drawn from p itself
         w.q = nullptr;
@@ -302,11 +306,13 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
         if (p.keep_lens) p.keep_lens[b] = len - (n - 1 - a);
         if (total == 0) p.next[b] = -1;
     }
-    uint64_t rest = __umul64hi(total, fixed64(u0));                     // the first token whose running sum exceeds this
+    // the first token whose running sum exceeds u0 times the total, rounded down
+    const uint64_t at = fixed64(u0);
+    Wide rest = (Wide)__umul64hi((uint64_t)total, at) + (uint64_t)(total >> 64) * (Wide)at;
     if (warp == 0 && rest >= before && rest - before < mine) {          // (in one CTA of the cluster)
         rest -= before;
         for (int t = first; t < end; t += 32) {
-            const uint64_t to = warp_scan(t + lane < end ? tile_sum[t + lane - first] : 0, lane);
+            const uint64_t to = warp_scan(t + lane < end ? tile_sum[t + lane - first] : 0, lane);  // (32 tiles: 2^60 at most)
             const uint32_t over = __ballot_sync(~0u, to > rest);
             if (!over) {
                 rest -= __shfl_sync(~0u, to, 31);
@@ -314,20 +320,20 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
             }
             const int k = __ffs(over) - 1;
             const uint64_t less = __shfl_sync(~0u, to, max(k - 1, 0));
-            if (k > 0) rest -= less;
+            uint64_t left = (uint64_t)rest - (k > 0 ? less : 0);  // (of this tile)
             // the tile again: the lane that holds it, whose values then go to all
             const int i0 = (t + k) * kLength;
             float x[E], y[E];
             const uint64_t upto = warp_scan(w.few(i0 + lane * E, x, y), lane);
-            const int l = max(__ffs(__ballot_sync(~0u, upto > rest)) - 1, 0);
+            const int l = max(__ffs(__ballot_sync(~0u, upto > left)) - 1, 0);
             const uint64_t less_l = __shfl_sync(~0u, upto, max(l - 1, 0));
-            if (l > 0) rest -= less_l;
+            if (l > 0) left -= less_l;
             Digits run;
             int e = 0;
 #pragma unroll
             for (int j = 0; j < E; ++j) {
                 run.add(__shfl_sync(~0u, x[j], l), __shfl_sync(~0u, y[j], l));
-                e += run.whole() <= rest;
+                e += run.whole() <= left;
             }
             if (lane == 0) p.next[b] = i0 + l * E + min(e, E - 1) - skip;
             break;

@@ -957,6 +957,33 @@ def test_verify_odd_rows(usp, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [131072, 1 << 19])
+def test_verify_rows_of_ones_whatever_the_cut(usp, V, dtype):
+    """Rows need not add up to 1: from the largest sums, 2^65 in whole numbers, a sequence draws the same token alone (eight
+    CTAs), among 70 (seven) and among 400 (one).  With V equal weights that is the token floor(u V), exactly."""
+    import torch
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    ends = np.array([0.9, 0.0, 1 - 2.0 ** -24, 0.125, np.nextafter(np.float32(0.125), np.float32(0)), 0.5, 2.0 ** -19, 0.99], np.float32)
+    for seqs in (1, 70, 400):
+        rng = np.random.default_rng(seqs)
+        u = np.concatenate([ends[:seqs], (rng.integers(0, 1 << 24, max(seqs - 8, 0)) * 2.0 ** -24).astype(np.float32)])
+        for rows in (1, 2):                               # the last row's p; p - q, each 1/2, behind a draft that is refused
+            guard = Guarded()
+            target = torch.ones((seqs * rows, V), dtype=dt, device="cuda")
+            draft = None if rows == 1 else torch.full((seqs * rows, V), 0.5, dtype=dt, device="cuda")
+            numbers = np.repeat(u, rows)
+            out = [guard.empty((seqs,), torch.int32, "cuda").fill_(-77) for _ in range(2)]
+            usp.usp_verify_drafts(seqs, seqs * rows, V, target, draft, _put(guard, np.full(seqs * rows, -1, np.int32)),
+                                  _put(guard, numbers), _put(guard, np.arange(0, seqs * rows + 1, rows, dtype=np.int32)), None, *out, None)
+            _done(usp, guard)
+            assert (out[0] == 0).all()
+            assert np.array_equal(out[1].cpu().numpy(), np.floor(u.astype(np.float64) * V).astype(np.int64)), (seqs, rows)
+        del target, draft
+        torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
 def test_captured_calls_replay_with_new_values(usp):
     """A fork with its copies and a verification, captured on a side stream: later steps replay with new numbers; two
     captures with workspaces of their own do not disturb each other."""
