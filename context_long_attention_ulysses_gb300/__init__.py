@@ -270,11 +270,18 @@ def _binding():
     return _bound
 
 
-def _struct(x) -> int:
-    """Address of the struct of a Problem, Cache or Rotary, or of a struct of the C ABI."""
+_C_STRUCT = {Problem: UspProblem, Cache: UspCache, Rotary: UspRotary}
+
+
+def _struct(x, kind) -> int:
+    """Address of the struct of a Problem, Cache or Rotary (`kind`), or of the struct of the C ABI that it stands for."""
+    if isinstance(x, kind):
+        return ctypes.addressof(x._kept())
     if x is None:
         return 0
-    return ctypes.addressof(x._kept() if isinstance(x, (Cache, Rotary, Problem)) else x)
+    if not isinstance(x, _C_STRUCT[kind]):
+        raise TypeError(f"expected a {kind.__name__} or its struct, got {type(x).__name__}")
+    return ctypes.addressof(x)
 
 
 def _cache(c) -> ctypes.POINTER(UspCache):
@@ -511,13 +518,13 @@ def usp_prefix_attn(c, n_tokens: int, max_q: int, q, k_pages, v_pages, page_tabl
 def usp_rotary_embed(p, r, q, k, pos, inv_freq, q_out, k_out, inverse: bool = False, stream=None) -> None:
     """q, q_out, k, k_out: sequence-sharded [P][B][N/P][H][d], or [tokens][H][d], with any token stride (q, q_out or k,
     k_out may be None)."""
-    _binding().rotary_embed(_struct(p), _struct(r), q, k, pos, inv_freq, q_out, k_out, 1 if inverse else 0, stream)
+    _binding().rotary_embed(_struct(p, Problem), _struct(r, Rotary), q, k, pos, inv_freq, q_out, k_out, 1 if inverse else 0, stream)
 
 
 def usp_kv_append_axes(c, n_tokens: int, q, k, v, seq, pos, rot_pos, inv_freq, r, q_out, k_out, k_pages, v_pages,
                        page_table, stream=None) -> None:
     """q, k, v: [n_tokens][H][d] with any token stride (q, q_out and k_out may be None); the rest contiguous."""
-    _binding().kv_append_axes(_struct(c), n_tokens, q, k, v, seq, pos, rot_pos, inv_freq, _struct(r), q_out, k_out, k_pages,
+    _binding().kv_append_axes(_struct(c, Cache), n_tokens, q, k, v, seq, pos, rot_pos, inv_freq, _struct(r, Rotary), q_out, k_out, k_pages,
                               v_pages, page_table, stream)
 
 
@@ -527,17 +534,17 @@ def usp_pages_update_workspace_size(c) -> int:
 
 def usp_pages_update(c, parent, keep, grow, seq_lens, page_table, ref, copies, ws, ws_bytes=None, stream=None) -> None:
     """seq_lens, page_table and ref are updated in place; copies int32 [1 + n_seqs][4]; ws_bytes None: those of the tensor."""
-    _binding().pages_update(_struct(c), parent, keep, grow, seq_lens, page_table, ref, copies, ws, ws_bytes, stream)
+    _binding().pages_update(_struct(c, Cache), parent, keep, grow, seq_lens, page_table, ref, copies, ws, ws_bytes, stream)
 
 
 def usp_pages_compact(c, page_table, ref, page_table_out, ref_out, new_id, copies, stream=None) -> None:
     """copies int32 [1 + n_pages // 2][4]; page_table_out and ref_out may be page_table and ref."""
-    _binding().pages_compact(_struct(c), page_table, ref, page_table_out, ref_out, new_id, copies, stream)
+    _binding().pages_compact(_struct(c, Cache), page_table, ref, page_table_out, ref_out, new_id, copies, stream)
 
 
 def usp_pages_copy(c, max_copies: int, copies, k_pages, v_pages, n_layers: int = 1, layer_stride: int = 0,
                    stream=None) -> None:
-    _binding().pages_copy(_struct(c), max_copies, copies, k_pages, v_pages, n_layers, layer_stride, stream)
+    _binding().pages_copy(_struct(c, Cache), max_copies, copies, k_pages, v_pages, n_layers, layer_stride, stream)
 
 
 def usp_verify_drafts(n_seqs: int, n_tokens: int, vocab: int, target, draft, tokens, u, q_start, seq_lens, n_accepted,

@@ -261,6 +261,27 @@ def test_structs_of_a_rotation_and_a_problem_are_the_callers_own(lib):
         assert same(r) == r and same(p) == p and _status(call, same(p), same(r)) == 3
 
 
+def test_structs_of_another_kind_are_refused(lib):
+    """A problem is no cache: its struct is shorter, and a call would read behind its end."""
+    c, p = _c(), _p()
+    calls = {"problem": lambda x: usp_mod.usp_rotary_embed(x, R3, FAKE, None, FAKE, FAKE, FAKE, None),
+             "rotary": lambda x: usp_mod.usp_rotary_embed(p, x, FAKE, None, FAKE, FAKE, FAKE, None),
+             "append": lambda x: usp_mod.usp_kv_append_axes(x, 0, *([FAKE] * 7), R3, *([FAKE] * 5)),
+             "append's rotary": lambda x: usp_mod.usp_kv_append_axes(c, 0, *([FAKE] * 7), x, *([FAKE] * 5)),
+             "update": lambda x: usp_mod.usp_pages_update(x, *([FAKE] * 8), 0),
+             "compact": lambda x: usp_mod.usp_pages_compact(x, *([FAKE] * 6)),
+             "copy": lambda x: usp_mod.usp_pages_copy(x, 0, FAKE, FAKE, FAKE)}
+    mine = {"problem": p, "rotary": R3, "append's rotary": R3}
+    for name, call in calls.items():
+        for x in (c, p, R3, c.c(), p.c(), R3.c()):
+            if type(x) not in (type(mine.get(name, c)), type(mine.get(name, c).c())):
+                with pytest.raises(TypeError):
+                    call(x)
+        for x in ((1, 2), "a text", 5, _lib.UspTraceEntry()):
+            with pytest.raises(TypeError):
+                call(x)
+
+
 def test_append_axes_refusals(lib):
     def call(c=None, T=2, rot_pos=FAKE, r=R3, **kw):
         a = dict(q=FAKE, k=FAKE, v=FAKE, seq=FAKE, pos=FAKE, f=FAKE, qo=FAKE, ko=FAKE, kp=FAKE, vp=FAKE, table=FAKE)
