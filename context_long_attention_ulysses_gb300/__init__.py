@@ -57,8 +57,18 @@ _Tensor = torch.Tensor
 _TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
+class _Kept:
+    """A struct of the C ABI that is made once for all calls (a decoding step is short enough for its making to show)."""
+
+    def _kept(self):
+        """The struct that calls pass on.  (The one that is there first stays: two threads may come here at once, and a call of
+        either holds its address.)"""
+        made = self.__dict__.get("_c")
+        return self.__dict__.setdefault("_c", self.c()) if made is None else made
+
+
 @dataclass(frozen=True)
-class Problem:
+class Problem(_Kept):
     """Q: B x Hq x N x d, K/V: B x Hkv x N x d, sequence-parallel degree P."""
     B: int
     Hq: int
@@ -75,14 +85,6 @@ class Problem:
             raise ValueError(f"dtype must be 'f32' or 'bf16', got {self.dtype!r}")
         return UspProblem(self.B, self.Hq, self.Hkv, self.N, self.d, self.P, int(bool(self.causal)),
                           float(self.scale), USP_F32 if self.dtype == "f32" else USP_BF16)
-
-    def _kept(self) -> UspProblem:
-        """The struct that calls pass on."""
-        made = self.__dict__.get("_c")
-        if made is None:
-            made = self.c()
-            object.__setattr__(self, "_c", made)
-        return made
 
     @property
     def torch_dtype(self) -> torch.dtype:
@@ -115,7 +117,7 @@ class Problem:
 
 
 @dataclass(frozen=True)
-class Cache:
+class Cache(_Kept):
     """A paged key/value cache: pool [n_pages][Hkv][page_size][d] for K and for V, page table [n_seqs][max_pages]."""
     n_pages: int
     page_size: int
@@ -134,14 +136,6 @@ class Cache:
             raise ValueError(f"dtype must be 'f32' or 'bf16', got {self.dtype!r}")
         return UspCache(self.n_pages, self.page_size, self.n_seqs, self.max_pages, self.Hq, self.Hkv, self.d,
                         int(bool(self.causal)), float(self.scale), USP_F32 if self.dtype == "f32" else USP_BF16)
-
-    def _kept(self) -> UspCache:
-        """The struct that calls pass on (kept: a decoding step is short enough for its making to show)."""
-        made = self.__dict__.get("_c")
-        if made is None:
-            made = self.c()
-            object.__setattr__(self, "_c", made)
-        return made
 
     @property
     def torch_dtype(self) -> torch.dtype:
@@ -164,7 +158,7 @@ class Cache:
 
 
 @dataclass(frozen=True)
-class Rotary:
+class Rotary(_Kept):
     """Rotary positions with several axes: axis[i] is the axis of pair i of a head's elements."""
     axis: tuple
     interleaved: bool = False  # pairs are elements (2i, 2i+1), otherwise (i, i + rot/2)
@@ -199,14 +193,6 @@ class Rotary:
         if any(not 0 <= int(a) < self.axes for a in self.axis) or self.axes > USP_MAX_AXES:
             raise ValueError(f"axes are 0 .. {min(self.axes, USP_MAX_AXES) - 1}")
         return UspRotary(self.axes, self.rot, int(bool(self.interleaved)), (ctypes.c_uint8 * 64)(*self.axis))
-
-    def _kept(self) -> UspRotary:
-        """The struct that calls pass on."""
-        made = self.__dict__.get("_c")
-        if made is None:
-            made = self.c()
-            object.__setattr__(self, "_c", made)
-        return made
 
 
 def library_path() -> str:

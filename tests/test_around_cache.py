@@ -282,6 +282,27 @@ def test_structs_of_another_kind_are_refused(lib):
                 call(x)
 
 
+@pytest.mark.parametrize("make", [_c, _p, lambda: usp_mod.Rotary.sections((8, 12, 12))])
+def test_two_threads_first_calls_share_a_struct(lib, make, monkeypatch):
+    """A struct whose address a call of one thread holds is not replaced by another thread's that makes one meanwhile."""
+    import ctypes
+    x = make()
+    cls, c = type(x), type(x).c
+    other = []
+
+    def interrupted(self):
+        if not other:
+            other.append(None)
+            other[0] = usp_mod._struct(self, cls)            # another thread comes in between
+        return c(self)
+
+    monkeypatch.setattr(cls, "c", interrupted)
+    mine = usp_mod._struct(x, cls)
+    assert mine == other[0] == usp_mod._struct(x, cls)
+    kept = type(c(x)).from_address(mine)
+    assert bytes(kept) == bytes(c(x)) and ctypes.sizeof(kept) == ctypes.sizeof(c(x))
+
+
 def test_append_axes_refusals(lib):
     def call(c=None, T=2, rot_pos=FAKE, r=R3, **kw):
         a = dict(q=FAKE, k=FAKE, v=FAKE, seq=FAKE, pos=FAKE, f=FAKE, qo=FAKE, ko=FAKE, kp=FAKE, vp=FAKE, table=FAKE)
