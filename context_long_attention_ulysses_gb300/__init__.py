@@ -20,6 +20,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
+import threading
 from dataclasses import dataclass
 
 import torch
@@ -57,14 +58,28 @@ _Tensor = torch.Tensor
 _TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
+_making = threading.Lock()
+
+
 class _Kept:
-    """A struct of the C ABI that is made once for all calls (a decoding step is short enough for its making to show)."""
+    """A struct of the C ABI that is made once for all calls (a decoding step is short enough for its making to show).  It stands
+    outside an object's own attributes: vars() are the fields, and a copy makes its own."""
+    __slots__ = ("_made",)
 
     def _kept(self):
-        """The struct that calls pass on.  (The one that is there first stays: two threads may come here at once, and a call of
-        either holds its address.)"""
-        made = self.__dict__.get("_c")
-        return self.__dict__.setdefault("_c", self.c()) if made is None else made
+        """The struct that calls pass on, and its address.  (The one that is there first stays: two threads may come here at
+        once, and a call of either holds the address.)"""
+        try:
+            return self._made
+        except AttributeError:
+            struct = self.c()
+        with _making:
+            if not hasattr(self, "_made"):
+                object.__setattr__(self, "_made", (struct, ctypes.addressof(struct)))
+        return self._made
+
+    def __getstate__(self):
+        return self.__dict__
 
 
 @dataclass(frozen=True)
@@ -262,7 +277,7 @@ _C_STRUCT = {Problem: UspProblem, Cache: UspCache, Rotary: UspRotary}
 def _struct(x, kind) -> int:
     """Address of the struct of a Problem, Cache or Rotary (`kind`), or of the struct of the C ABI that it stands for."""
     if isinstance(x, kind):
-        return ctypes.addressof(x._kept())
+        return x._kept()[1]
     if x is None:
         return 0
     if not isinstance(x, _C_STRUCT[kind]):
@@ -273,13 +288,13 @@ def _struct(x, kind) -> int:
 def _cache(c) -> ctypes.POINTER(UspCache):
     if c is None:
         return None
-    return ctypes.byref(c._kept() if isinstance(c, Cache) else c)
+    return ctypes.byref(c._kept()[0] if isinstance(c, Cache) else c)
 
 
 def _prob(p) -> ctypes.POINTER(UspProblem):
     if p is None:
         return None
-    return ctypes.byref(p._kept() if isinstance(p, Problem) else p)
+    return ctypes.byref(p._kept()[0] if isinstance(p, Problem) else p)
 
 
 # --------------------------------------------------------------- C ABI mirror

@@ -303,6 +303,22 @@ def test_two_threads_first_calls_share_a_struct(lib, make, monkeypatch):
     assert bytes(kept) == bytes(c(x)) and ctypes.sizeof(kept) == ctypes.sizeof(c(x))
 
 
+@pytest.mark.parametrize("make", [_c, _p, lambda: usp_mod.Rotary.sections((8, 12, 12))])
+def test_attributes_are_the_fields_before_and_after_a_call(lib, make):
+    """What a call keeps is not among an object's attributes, and a copy has its own."""
+    import copy
+    import dataclasses
+    import pickle
+    x = make()
+    fields = {f.name: getattr(x, f.name) for f in dataclasses.fields(x)}
+    at = usp_mod._struct(x, type(x))
+    assert vars(x) == fields and type(x)(**vars(x)) == x
+    for same in (copy.copy, copy.deepcopy, lambda y: pickle.loads(pickle.dumps(y)), dataclasses.replace):
+        y = same(x)
+        assert y == x and vars(y) == fields and usp_mod._struct(y, type(y)) != at
+        assert bytes(y._kept()[0]) == bytes(x._kept()[0])
+
+
 def test_append_axes_refusals(lib):
     def call(c=None, T=2, rot_pos=FAKE, r=R3, **kw):
         a = dict(q=FAKE, k=FAKE, v=FAKE, seq=FAKE, pos=FAKE, f=FAKE, qo=FAKE, ko=FAKE, kp=FAKE, vp=FAKE, table=FAKE)
