@@ -179,6 +179,10 @@ class Rotary(_Kept):
     interleaved: bool = False  # pairs are elements (2i, 2i+1), otherwise (i, i + rot/2)
     n_axes: int = 0            # 0: as many as axis names
 
+    def __post_init__(self):
+        # (numbers of its own: a list that the caller changes later is another's)
+        object.__setattr__(self, "axis", tuple(int(a) for a in self.axis))
+
     @staticmethod
     def sections(sizes, cycled=False, interleaved=False) -> "Rotary":
         """sizes[a] pairs of axis a: one axis after the other, or (cycled) the axes in turn, with the pairs for which the
@@ -205,7 +209,7 @@ class Rotary(_Kept):
         """A struct of the C ABI, the caller's own."""
         if len(self.axis) > 64:
             raise ValueError(f"at most 64 pairs, got {len(self.axis)}")
-        if any(not 0 <= int(a) < self.axes for a in self.axis) or self.axes > USP_MAX_AXES:
+        if any(not 0 <= a < self.axes for a in self.axis) or self.axes > USP_MAX_AXES:
             raise ValueError(f"axes are 0 .. {min(self.axes, USP_MAX_AXES) - 1}")
         return UspRotary(self.axes, self.rot, int(bool(self.interleaved)), (ctypes.c_uint8 * 64)(*self.axis))
 

@@ -319,6 +319,15 @@ def test_attributes_are_the_fields_before_and_after_a_call(lib, make):
         assert bytes(y._kept()[0]) == bytes(x._kept()[0])
 
 
+def test_a_rotation_keeps_its_axes_when_a_list_changes(lib):
+    axes = [0, 1, 2, 0, 1, 2, 0, 0]
+    r, a = usp_mod.Rotary(axes), usp_mod.Rotary(np.array(axes))
+    assert r == a == usp_mod.Rotary(tuple(axes)) and hash(r) == hash(a)
+    before = bytes(r._kept()[0])
+    axes[0] = 3
+    assert r.axes == 3 and bytes(r.c()) == bytes(r._kept()[0]) == before
+
+
 def test_append_axes_refusals(lib):
     def call(c=None, T=2, rot_pos=FAKE, r=R3, **kw):
         a = dict(q=FAKE, k=FAKE, v=FAKE, seq=FAKE, pos=FAKE, f=FAKE, qo=FAKE, ko=FAKE, kp=FAKE, vp=FAKE, table=FAKE)
