@@ -20,6 +20,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
+import operator
 import threading
 from dataclasses import dataclass
 
@@ -181,7 +182,7 @@ class Rotary(_Kept):
 
     def __post_init__(self):
         # (numbers of its own: a list that the caller changes later is another's)
-        object.__setattr__(self, "axis", tuple(int(a) for a in self.axis))
+        object.__setattr__(self, "axis", tuple(operator.index(a) for a in self.axis))
 
     @staticmethod
     def sections(sizes, cycled=False, interleaved=False) -> "Rotary":

@@ -328,6 +328,12 @@ def test_a_rotation_keeps_its_axes_when_a_list_changes(lib):
     assert r.axes == 3 and bytes(r.c()) == bytes(r._kept()[0]) == before
 
 
+def test_axes_are_whole_numbers():
+    for axes in ((0, 1.7), (0, 1.0), ("0",), (None,)):
+        with pytest.raises(TypeError):
+            usp_mod.Rotary(axes)
+
+
 def test_append_axes_refusals(lib):
     def call(c=None, T=2, rot_pos=FAKE, r=R3, **kw):
         a = dict(q=FAKE, k=FAKE, v=FAKE, seq=FAKE, pos=FAKE, f=FAKE, qo=FAKE, ko=FAKE, kp=FAKE, vp=FAKE, table=FAKE)
