@@ -57,6 +57,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _Tensor = torch.Tensor
 _TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
+_USP_DTYPE = {"f32": USP_F32, "bf16": USP_BF16}
 
 
 _making = threading.Lock()
@@ -530,8 +531,8 @@ def usp_rotary_embed(p, r, q, k, pos, inv_freq, q_out, k_out, inverse: bool = Fa
 def usp_kv_append_axes(c, n_tokens: int, q, k, v, seq, pos, rot_pos, inv_freq, r, q_out, k_out, k_pages, v_pages,
                        page_table, stream=None) -> None:
     """q, k, v: [n_tokens][H][d] with any token stride (q, q_out and k_out may be None); the rest contiguous."""
-    _binding().kv_append_axes(_struct(c, Cache), n_tokens, q, k, v, seq, pos, rot_pos, inv_freq, _struct(r, Rotary), q_out, k_out, k_pages,
-                              v_pages, page_table, stream)
+    _binding().kv_append_axes(_struct(c, Cache), _struct(r, Rotary), n_tokens, q, k, v, seq, pos, rot_pos, inv_freq, q_out, k_out,
+                              k_pages, v_pages, page_table, stream)
 
 
 def usp_pages_update_workspace_size(c) -> int:
@@ -550,7 +551,7 @@ def usp_pages_compact(c, page_table, ref, page_table_out, ref_out, new_id, copie
 
 def usp_pages_copy(c, max_copies: int, copies, k_pages, v_pages, n_layers: int = 1, layer_stride: int = 0,
                    stream=None) -> None:
-    _binding().pages_copy(_struct(c, Cache), max_copies, copies, k_pages, v_pages, n_layers, layer_stride, stream)
+    _binding().pages_copy(_struct(c, Cache), n_layers, layer_stride, max_copies, copies, k_pages, v_pages, stream)
 
 
 def usp_verify_drafts(n_seqs: int, n_tokens: int, vocab: int, target, draft, tokens, u, q_start, seq_lens, n_accepted,
@@ -559,8 +560,8 @@ def usp_verify_drafts(n_seqs: int, n_tokens: int, vocab: int, target, draft, tok
     pointers)."""
     if dtype is None:
         dtype = "bf16" if isinstance(target, _Tensor) and target.dtype == torch.bfloat16 else "f32"
-    _binding().verify_drafts(n_seqs, n_tokens, vocab, USP_F32 if dtype == "f32" else USP_BF16, _TORCH_DTYPE[dtype], target,
-                             draft, tokens, u, q_start, seq_lens, n_accepted, next_tokens, keep_lens, stream)
+    _binding().verify_drafts(n_seqs, n_tokens, vocab, _USP_DTYPE[dtype], target, draft, tokens, u, q_start, seq_lens, n_accepted,
+                             next_tokens, keep_lens, stream)
 
 
 def usp_diag_wait_timeout(stream=None) -> None:

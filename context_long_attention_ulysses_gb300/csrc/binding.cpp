@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <cstdint>
+#include <initializer_list>
 
 #include <cuda_runtime_api.h>
 
@@ -17,7 +18,29 @@ namespace {
 
 // From the package: the stream's handle of a `stream` argument, what raises a status, torch's current stream of a device (or None).
 PyObject *stream_of, *check, *raw_stream;
+PyObject *t_int32, *t_float32, *t_bfloat16;  // torch's
 PyObject *tensor_type, *s_is_cuda, *s_is_contiguous, *s_data_ptr, *s_numel, *s_nbytes, *s_shape, *s_stride, *s_dtype;
+
+// How many elements of a type (of torch's, or null: none that is known) a tensor has to have.
+struct Want {
+    PyObject* type;
+    int64_t n;
+};
+// The product of sizes, as far as it goes; 0 where one is not positive (the C side says what is wrong with it).
+template <typename... N>
+int64_t times(N... sizes) {
+    int64_t n = 1;
+    for (const int64_t x : {(int64_t)sizes...}) {
+        if (x <= 0) return 0;
+        if (__builtin_mul_overflow(n, x, &n)) n = INT64_MAX;
+    }
+    return n;
+}
+Want ints(int64_t n) { return {t_int32, n}; }
+Want floats(int64_t n) { return {t_float32, n}; }
+PyObject* type_of(int dtype) { return dtype == USP_F32 ? t_float32 : dtype == USP_BF16 ? t_bfloat16 : nullptr; }
+int64_t pool(const usp_cache* c) { return c ? times(c->n_pages, c->Hkv, c->page_size, c->d) : 0; }
+int64_t table(const usp_cache* c) { return c ? times(c->n_seqs, c->max_pages) : 0; }
 
 // The arguments of a call, taken from the left.  After the first that is wrong the Python error is set and the rest is 0.
 struct Args {
@@ -134,9 +157,16 @@ struct Args {
             PyErr_Format(PyExc_TypeError, "expected a torch tensor, a device pointer or None, got %s", Py_TYPE(x)->tp_name);
         bad = true;
     }
-    // A contiguous device tensor.
+    void typed(PyObject* x, PyObject* type) {
+        if (bad || !type) return;
+        PyObject* is = PyObject_GetAttr(x, s_dtype);
+        if (is && is != type) PyErr_Format(PyExc_ValueError, "expected %R, got %R", type, is);
+        bad |= is != type;
+        Py_XDECREF(is);
+    }
+    // A contiguous device tensor.  (One without elements is no more than a null pointer.)
     template <typename T>
-    T* device() {
+    T* device(const Want& want) {
         PyObject* x = next();
         uint64_t v = 0;
         if (!x || plain(x, &v)) return (T*)(uintptr_t)v;
@@ -144,23 +174,33 @@ struct Args {
             not_a_buffer(x);
             return nullptr;
         }
-        if (!on_device(x) && !bad && asked(x, s_numel, true) > 0) fail(PyExc_ValueError, "libusp takes device tensors");
+        const long long bytes = asked(x, s_nbytes, false);
+        if (bytes > 0) {
+            typed(x, want.type);
+            if (want.type && !bad && bytes / (want.type == t_bfloat16 ? 2 : 4) < want.n) {
+                PyErr_Format(PyExc_ValueError, "expected %lld elements at least, got %lld", (long long)want.n, asked(x, s_numel, true));
+                bad = true;
+            }
+        }
+        if (!bad && !on_device(x) && bytes > 0) fail(PyExc_ValueError, "libusp takes device tensors");
         if (!bad && !truth(x, s_is_contiguous, true) && !bad) fail(PyExc_ValueError, "libusp takes contiguous tensors");
         return bad ? nullptr : (T*)(uintptr_t)address(x);
     }
     // A workspace and its size, which the argument after it gives, None: the tensor's.
     void* workspace(size_t* bytes) {
         PyObject *x = bad || left < 2 ? nullptr : at[0], *n = x ? at[1] : nullptr;
-        void* p = device<void>();
-        if (!next() || bad) return nullptr;
         *bytes = 0;
-        if (n != Py_None) {
+        if (x && n != Py_None) {
             *bytes = PyLong_AsSize_t(n);
             if (PyErr_Occurred()) bad = true;
-        } else if (x != Py_None && !PyLong_Check(x)) {
-            *bytes = (size_t)asked(x, s_nbytes, false);
         }
-        return p;
+        if (x && !bad && x != Py_None && !PyLong_Check(x) && is_tensor(x)) {
+            const size_t whole = (size_t)asked(x, s_nbytes, false);
+            if (n == Py_None) *bytes = whole;
+            if (!bad && *bytes > whole) fail(PyExc_ValueError, "a workspace of more bytes than the tensor has");
+        }
+        void* p = device<void>({nullptr, 0});
+        return next() && !bad ? p : nullptr;
     }
     // Shape and strides of x; the number of its dimensions, 0 if there are more than five.
     Py_ssize_t layout(PyObject* x, long long (&shape)[5], long long (&stride)[5]) {
@@ -178,9 +218,9 @@ struct Args {
         if (PyErr_Occurred()) bad = true;
         return bad ? 0 : dims;
     }
-    // Rows of `heads` times d contiguous elements, one to a token: [tokens][heads][d], or (five) [P][B][N/P][heads][d] with the
-    // tokens evenly apart.
-    void* rows(int64_t* step, int heads, int d, bool five) {
+    // Rows of `heads` times d contiguous elements, one to each of want.n tokens at least: [tokens][heads][d], or (five)
+    // [P][B][N/P][heads][d] with the tokens evenly apart.
+    void* rows(int64_t* step, int heads, int d, bool five, const Want& want) {
         PyObject* x = next();
         uint64_t v = 0;
         *step = (int64_t)heads * d;
@@ -213,13 +253,18 @@ struct Args {
             PyErr_Format(PyExc_ValueError, "expected rows of [%d][%d], got [%lld][%lld]", heads, d, shape[1], shape[2]);
             bad = true;
         }
+        if (!bad && tokens < want.n) {
+            PyErr_Format(PyExc_ValueError, "expected rows of %lld tokens at least, got %lld", (long long)want.n, tokens);
+            bad = true;
+        }
+        if (tokens > 0) typed(x, want.type);
         if (!bad && tokens > 0 && !on_device(x)) fail(PyExc_ValueError, "libusp takes device tensors");
         if (!bad && tokens > 0 && (stride[2] != 1 || (heads > 1 && stride[1] != d)))
             fail(PyExc_ValueError, "the heads of a token must be contiguous");
         return bad ? nullptr : (void*)(uintptr_t)address(x);
     }
-    // Rows of `vocab` contiguous probabilities of type `dtype` (a torch.dtype).
-    void* probabilities(int64_t* step, int vocab, PyObject* dtype) {
+    // want.n rows, at least, of `vocab` contiguous probabilities.
+    void* probabilities(int64_t* step, int vocab, const Want& want) {
         PyObject* x = next();
         uint64_t v = 0;
         *step = vocab;
@@ -234,13 +279,11 @@ struct Args {
             bad = true;
             return nullptr;
         }
-        PyObject* type = PyObject_GetAttr(x, s_dtype);
-        if (!type) bad = true;
-        if (type && type != dtype) {
-            PyErr_Format(PyExc_ValueError, "expected %R, got %R", dtype, type);
+        typed(x, want.type);
+        if (!bad && shape[0] < want.n) {
+            PyErr_Format(PyExc_ValueError, "expected %lld rows at least, got %lld", (long long)want.n, shape[0]);
             bad = true;
         }
-        Py_XDECREF(type);
         if (shape[0] > 1) *step = stride[0];
         if (!bad && shape[0] > 0 && !on_device(x)) fail(PyExc_ValueError, "libusp takes device tensors");
         if (!bad && shape[0] > 0 && vocab > 1 && stride[1] != 1) fail(PyExc_ValueError, "the probabilities of a row must be contiguous");
@@ -265,11 +308,12 @@ PyObject* rotary_embed(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const auto* p = (const usp_problem*)a.raw();
     const auto* r = (const usp_rotary*)a.raw();
     const int Hq = p ? p->Hq : 0, Hkv = p ? p->Hkv : 0, d = p ? p->d : 0;
+    const Want tokens{p ? type_of(p->dtype) : nullptr, p ? times(p->B, p->N) : 0};
     int64_t qs, ks, qos, kos;
-    const void *q = a.rows(&qs, Hq, d, true), *k = a.rows(&ks, Hkv, d, true);
-    const auto* pos = a.device<const int32_t>();
-    const auto* f = a.device<const float>();
-    void *qo = a.rows(&qos, Hq, d, true), *ko = a.rows(&kos, Hkv, d, true);
+    const void *q = a.rows(&qs, Hq, d, true, tokens), *k = a.rows(&ks, Hkv, d, true, tokens);
+    const auto* pos = a.device<const int32_t>(ints(r && r->rot > 0 ? times(r->n_axes, tokens.n) : 0));
+    const auto* f = a.device<const float>(floats(r && tokens.n > 0 ? r->rot / 2 : 0));
+    void *qo = a.rows(&qos, Hq, d, true, tokens), *ko = a.rows(&kos, Hkv, d, true, tokens);
     const int inverse = a.integer();
     void* s = a.stream();
     return made("usp_rotary_embed", a, [&] { return usp_rotary_embed(p, r, inverse, q, qs, k, ks, pos, f, qo, qos, ko, kos, s); });
@@ -278,62 +322,74 @@ PyObject* rotary_embed(PyObject*, PyObject* const* args, Py_ssize_t n) {
 PyObject* kv_append_axes(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Args a(args, n, 16);
     const auto* c = (const usp_cache*)a.raw();
-    const int Hq = c ? c->Hq : 0, Hkv = c ? c->Hkv : 0, d = c ? c->d : 0, tokens = a.integer();
-    int64_t qs, ks, vs;
-    const void *q = a.rows(&qs, Hq, d, false), *k = a.rows(&ks, Hkv, d, false), *v = a.rows(&vs, Hkv, d, false);
-    const int32_t *seq = a.device<const int32_t>(), *pos = a.device<const int32_t>(), *rot_pos = a.device<const int32_t>();
-    const auto* f = a.device<const float>();
     const auto* r = (const usp_rotary*)a.raw();
-    void *qo = a.device<void>(), *ko = a.device<void>(), *kp = a.device<void>(), *vp = a.device<void>();
-    const auto* table = a.device<const int32_t>();
+    const int Hq = c ? c->Hq : 0, Hkv = c ? c->Hkv : 0, d = c ? c->d : 0, tokens = a.integer();
+    PyObject* type = c ? type_of(c->dtype) : nullptr;
+    const Want each{type, tokens}, all{type, pool(c)};
+    int64_t qs, ks, vs;
+    const void *q = a.rows(&qs, Hq, d, false, each), *k = a.rows(&ks, Hkv, d, false, each), *v = a.rows(&vs, Hkv, d, false, each);
+    const int32_t *seq = a.device<const int32_t>(ints(tokens)), *pos = a.device<const int32_t>(ints(tokens));
+    const auto* rot_pos = a.device<const int32_t>(ints(r && r->rot > 0 ? times(r->n_axes, tokens) : 0));
+    const auto* f = a.device<const float>(floats(r && tokens > 0 ? r->rot / 2 : 0));
+    void *qo = a.device<void>({type, times(tokens, Hq, d)}), *ko = a.device<void>({type, times(tokens, Hkv, d)});
+    void *kp = a.device<void>(all), *vp = a.device<void>(all);
+    const auto* ids = a.device<const int32_t>(ints(table(c)));
     void* s = a.stream();
     return made("usp_kv_append_axes", a, [&] {
-        return usp_kv_append_axes(c, tokens, q, qs, k, ks, v, vs, seq, pos, rot_pos, f, r, qo, ko, kp, vp, table, s);
+        return usp_kv_append_axes(c, tokens, q, qs, k, ks, v, vs, seq, pos, rot_pos, f, r, qo, ko, kp, vp, ids, s);
     });
 }
 
 PyObject* pages_update(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Args a(args, n, 11);
     const auto* c = (const usp_cache*)a.raw();
-    const int32_t *parent = a.device<const int32_t>(), *keep = a.device<const int32_t>(), *grow = a.device<const int32_t>();
-    int32_t *lens = a.device<int32_t>(), *table = a.device<int32_t>(), *ref = a.device<int32_t>(), *copies = a.device<int32_t>();
+    const Want slots = ints(c ? c->n_seqs : 0);
+    const int32_t *parent = a.device<const int32_t>(slots), *keep = a.device<const int32_t>(slots), *grow = a.device<const int32_t>(slots);
+    int32_t *lens = a.device<int32_t>(slots), *ids = a.device<int32_t>(ints(table(c))), *ref = a.device<int32_t>(ints(c ? c->n_pages : 0));
+    int32_t* copies = a.device<int32_t>(ints(times(4, 1 + slots.n)));
     size_t bytes = 0;
     void* ws = a.workspace(&bytes);
     void* s = a.stream();
-    return made("usp_pages_update", a, [&] { return usp_pages_update(c, parent, keep, grow, lens, table, ref, copies, ws, bytes, s); });
+    return made("usp_pages_update", a, [&] { return usp_pages_update(c, parent, keep, grow, lens, ids, ref, copies, ws, bytes, s); });
 }
 
 PyObject* pages_compact(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Args a(args, n, 8);
     const auto* c = (const usp_cache*)a.raw();
-    const int32_t *table = a.device<const int32_t>(), *ref = a.device<const int32_t>();
-    int32_t *table_out = a.device<int32_t>(), *ref_out = a.device<int32_t>(), *new_id = a.device<int32_t>(), *copies = a.device<int32_t>();
+    const Want entries = ints(table(c)), pages = ints(c ? c->n_pages : 0);
+    const int32_t *ids = a.device<const int32_t>(entries), *ref = a.device<const int32_t>(pages);
+    int32_t *ids_out = a.device<int32_t>(entries), *ref_out = a.device<int32_t>(pages), *new_id = a.device<int32_t>(pages);
+    int32_t* copies = a.device<int32_t>(ints(times(4, 1 + pages.n / 2)));
     void* s = a.stream();
-    return made("usp_pages_compact", a, [&] { return usp_pages_compact(c, table, ref, table_out, ref_out, new_id, copies, s); });
+    return made("usp_pages_compact", a, [&] { return usp_pages_compact(c, ids, ref, ids_out, ref_out, new_id, copies, s); });
 }
 
 PyObject* pages_copy(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Args a(args, n, 8);
     const auto* c = (const usp_cache*)a.raw();
-    const int most = a.integer();
-    const auto* copies = a.device<const int32_t>();
-    void *kp = a.device<void>(), *vp = a.device<void>();
     const int layers = a.integer();
     const int64_t stride = a.number();
+    const int most = a.integer();
+    const auto* copies = a.device<const int32_t>(ints(most > 0 ? 4 : 0));  // (row 0 says how many rows are read)
+    const int64_t one = pool(c), before = layers > 1 ? times(layers - 1, stride) : 0;
+    const Want all{c ? type_of(c->dtype) : nullptr, layers < 1 || most < 1 ? 0 : before > INT64_MAX - one ? INT64_MAX : before + one};
+    void *kp = a.device<void>(all), *vp = a.device<void>(all);
     void* s = a.stream();
     return made("usp_pages_copy", a, [&] { return usp_pages_copy(c, most, copies, layers, stride, kp, vp, s); });
 }
 
 PyObject* verify_drafts(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    Args a(args, n, 15);
+    Args a(args, n, 14);
     const int seqs = a.integer(), tokens = a.integer(), vocab = a.integer(), type = a.integer();
-    PyObject* dtype = a.next();
+    const Want each{type_of(type), tokens};
     int64_t ts, ds;
-    const void *target = a.probabilities(&ts, vocab, dtype), *draft = a.probabilities(&ds, vocab, dtype);
-    const auto* ids = a.device<const int32_t>();
-    const auto* u = a.device<const float>();
-    const int32_t *start = a.device<const int32_t>(), *lens = a.device<const int32_t>();
-    int32_t *accepted = a.device<int32_t>(), *next = a.device<int32_t>(), *keep = a.device<int32_t>();
+    const void *target = a.probabilities(&ts, vocab, each), *draft = a.probabilities(&ds, vocab, each);
+    const auto* ids = a.device<const int32_t>(ints(tokens));
+    const auto* u = a.device<const float>(floats(tokens));
+    const Want slots = ints(seqs);
+    const auto* start = a.device<const int32_t>(ints(seqs > 0 ? (int64_t)seqs + 1 : 0));
+    const auto* lens = a.device<const int32_t>(slots);
+    int32_t *accepted = a.device<int32_t>(slots), *next = a.device<int32_t>(slots), *keep = a.device<int32_t>(slots);
     void* s = a.stream();
     return made("usp_verify_drafts", a, [&] {
         return usp_verify_drafts(seqs, tokens, vocab, type, target, ts, draft, ds, ids, u, start, lens, accepted, next, keep, s);
@@ -370,6 +426,9 @@ PyMODINIT_FUNC PyInit_uspbinding(void) {
     PyObject* torch = PyImport_ImportModule("torch");
     if (!torch) return nullptr;
     tensor_type = PyObject_GetAttrString(torch, "Tensor");
+    t_int32 = PyObject_GetAttrString(torch, "int32");
+    t_float32 = PyObject_GetAttrString(torch, "float32");
+    t_bfloat16 = PyObject_GetAttrString(torch, "bfloat16");
     Py_DECREF(torch);
     s_is_cuda = PyUnicode_InternFromString("is_cuda");
     s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
@@ -379,6 +438,6 @@ PyMODINIT_FUNC PyInit_uspbinding(void) {
     s_shape = PyUnicode_InternFromString("shape");
     s_stride = PyUnicode_InternFromString("stride");
     s_dtype = PyUnicode_InternFromString("dtype");
-    if (!tensor_type || !s_dtype) return nullptr;
+    if (!tensor_type || !t_int32 || !t_float32 || !t_bfloat16 || !s_dtype) return nullptr;
     return PyModule_Create(&definition);
 }

@@ -444,6 +444,62 @@ def test_arguments_that_are_no_buffers_are_refused(lib):
     assert _status(lambda: usp_mod.usp_pages_copy(_c(page_size=24), 1, FAKE, FAKE, FAKE)) == 2
 
 
+def test_tensors_of_another_type_or_too_short_are_refused(lib):
+    """Before anything is launched: elements of another type would be misread, and a kernel would go on behind the end of what is
+    shorter than the call says.  (Host tensors: what they hold is refused for its type and length before its place.)"""
+    import torch
+    bf, f32, i32, i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+    c, p, T = _c(), _p(N=16), 16
+    pool = 10 * 2 * 16 * 64
+    size = usp_mod.usp_pages_update_workspace_size(c)
+    # per call: its tensors' types, shapes and least lengths, and the numbers of elements that may be more
+    q, k = ((T, 4, 64), bf), ((T, 2, 64), bf)
+    calls = {
+        "rotary": (lambda x: usp_mod.usp_rotary_embed(p, R3, x["q"], x["k"], x["pos"], x["f"], x["qo"], x["ko"]),
+                   dict(q=q, k=k, pos=((3 * T,), i32), f=((32,), f32), qo=q, ko=k)),
+        "append": (lambda x: usp_mod.usp_kv_append_axes(c, T, x["q"], x["k"], x["v"], x["seq"], x["pos"], x["rot"], x["f"], R3, x["qo"],
+                                                        x["ko"], x["kp"], x["vp"], x["table"]),
+                   dict(q=q, k=k, v=k, seq=((T,), i32), pos=((T,), i32), rot=((3 * T,), i32), f=((32,), f32), qo=q, ko=k,
+                        kp=((pool,), bf), vp=((pool,), bf), table=((2, 4), i32))),
+        "update": (lambda x: usp_mod.usp_pages_update(c, x["parent"], x["keep"], x["grow"], x["lens"], x["table"], x["ref"], x["copies"],
+                                                      x["ws"], size),
+                   dict(parent=((2,), i32), keep=((2,), i32), grow=((2,), i32), lens=((2,), i32), table=((2, 4), i32),
+                        ref=((10,), i32), copies=((3, 4), i32), ws=((size,), torch.uint8))),
+        "compact": (lambda x: usp_mod.usp_pages_compact(c, x["table"], x["ref"], x["table_out"], x["ref_out"], x["new_id"], x["copies"]),
+                    dict(table=((2, 4), i32), ref=((10,), i32), table_out=((2, 4), i32), ref_out=((10,), i32), new_id=((10,), i32),
+                         copies=((6, 4), i32))),
+        "copy": (lambda x: usp_mod.usp_pages_copy(c, 5, x["copies"], x["kp"], x["vp"], 3, pool + 8),
+                 dict(copies=((4,), i32), kp=((3 * pool + 16,), bf), vp=((3 * pool + 16,), bf))),
+        "verify": (lambda x: usp_mod.usp_verify_drafts(3, T, 50, x["target"], x["draft"], x["tokens"], x["u"], x["start"], x["lens"],
+                                                       x["acc"], x["next"], x["keep"], "f32"),
+                   dict(target=((T, 50), f32), draft=((T, 50), f32), tokens=((T,), i32), u=((T,), f32), start=((4,), i32),
+                        lens=((3,), i32), acc=((3,), i32), next=((3,), i32), keep=((3,), i32))),
+    }
+    for name, (call, tensors) in calls.items():
+        for arg, (shape, dtype) in tensors.items():
+            x = {a: FAKE for a in tensors}
+            least = torch.empty(shape, dtype=dtype)
+            x[arg] = least
+            with pytest.raises(ValueError, match="device tensors"):       # what would do, but for its place
+                call(x)
+            x[arg] = torch.empty((shape[0] + 1, *shape[1:]), dtype=dtype)
+            with pytest.raises(ValueError, match="device tensors"):
+                call(x)
+            x[arg] = least[:-1]
+            with pytest.raises(ValueError, match="at least|more bytes"):
+                call(x)
+            if dtype == torch.uint8:
+                continue
+            for other in {i64, i32, bf, f32, torch.float64} - {dtype}:
+                x[arg] = torch.empty(shape, dtype=other)
+                with pytest.raises(ValueError, match="expected torch"):
+                    call(x)
+    # nothing is asked of what a call does not read
+    none = torch.empty(0, 4, 64)
+    usp_mod.usp_rotary_embed(_p(B=0), R3, none, None, torch.empty(0), torch.empty(0), none, None)
+    usp_mod.usp_pages_copy(c, 0, torch.empty(0), torch.empty(0), torch.empty(0))
+
+
 # ------------------------------------------------------------------ GPU
 @pytest.fixture(scope="module")
 def usp():
