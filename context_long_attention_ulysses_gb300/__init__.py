@@ -273,7 +273,7 @@ def _binding():
     """The calls around the cache (csrc/binding.cpp)."""
     global _bound
     if _bound is None:
-        _bound = _load_binding(_stream, _raw_stream)
+        _bound = _load_binding(_stream, _raw_stream, _struct, Problem, Cache, Rotary)
     return _bound
 
 
@@ -525,13 +525,13 @@ def usp_prefix_attn(c, n_tokens: int, max_q: int, q, k_pages, v_pages, page_tabl
 def usp_rotary_embed(p, r, q, k, pos, inv_freq, q_out, k_out, inverse: bool = False, stream=None) -> None:
     """q, q_out, k, k_out: sequence-sharded [P][B][N/P][H][d], or [tokens][H][d], with any token stride (q, q_out or k,
     k_out may be None)."""
-    _binding().rotary_embed(_struct(p, Problem), _struct(r, Rotary), q, k, pos, inv_freq, q_out, k_out, 1 if inverse else 0, stream)
+    (_bound or _binding()).rotary_embed(p, r, q, k, pos, inv_freq, q_out, k_out, 1 if inverse else 0, stream)
 
 
 def usp_kv_append_axes(c, n_tokens: int, q, k, v, seq, pos, rot_pos, inv_freq, r, q_out, k_out, k_pages, v_pages,
                        page_table, stream=None) -> None:
     """q, k, v: [n_tokens][H][d] with any token stride (q, q_out and k_out may be None); the rest contiguous."""
-    _binding().kv_append_axes(_struct(c, Cache), _struct(r, Rotary), n_tokens, q, k, v, seq, pos, rot_pos, inv_freq, q_out, k_out,
+    (_bound or _binding()).kv_append_axes(c, r, n_tokens, q, k, v, seq, pos, rot_pos, inv_freq, q_out, k_out,
                               k_pages, v_pages, page_table, stream)
 
 
@@ -541,17 +541,17 @@ def usp_pages_update_workspace_size(c) -> int:
 
 def usp_pages_update(c, parent, keep, grow, seq_lens, page_table, ref, copies, ws, ws_bytes=None, stream=None) -> None:
     """seq_lens, page_table and ref are updated in place; copies int32 [1 + n_seqs][4]; ws_bytes None: those of the tensor."""
-    _binding().pages_update(_struct(c, Cache), parent, keep, grow, seq_lens, page_table, ref, copies, ws, ws_bytes, stream)
+    (_bound or _binding()).pages_update(c, parent, keep, grow, seq_lens, page_table, ref, copies, ws, ws_bytes, stream)
 
 
 def usp_pages_compact(c, page_table, ref, page_table_out, ref_out, new_id, copies, stream=None) -> None:
     """copies int32 [1 + n_pages // 2][4]; page_table_out and ref_out may be page_table and ref."""
-    _binding().pages_compact(_struct(c, Cache), page_table, ref, page_table_out, ref_out, new_id, copies, stream)
+    (_bound or _binding()).pages_compact(c, page_table, ref, page_table_out, ref_out, new_id, copies, stream)
 
 
 def usp_pages_copy(c, max_copies: int, copies, k_pages, v_pages, n_layers: int = 1, layer_stride: int = 0,
                    stream=None) -> None:
-    _binding().pages_copy(_struct(c, Cache), n_layers, layer_stride, max_copies, copies, k_pages, v_pages, stream)
+    (_bound or _binding()).pages_copy(c, n_layers, layer_stride, max_copies, copies, k_pages, v_pages, stream)
 
 
 def usp_verify_drafts(n_seqs: int, n_tokens: int, vocab: int, target, draft, tokens, u, q_start, seq_lens, n_accepted,
@@ -560,7 +560,7 @@ def usp_verify_drafts(n_seqs: int, n_tokens: int, vocab: int, target, draft, tok
     pointers)."""
     if dtype is None:
         dtype = "bf16" if isinstance(target, _Tensor) and target.dtype == torch.bfloat16 else "f32"
-    _binding().verify_drafts(n_seqs, n_tokens, vocab, _USP_DTYPE[dtype], target, draft, tokens, u, q_start, seq_lens, n_accepted,
+    (_bound or _binding()).verify_drafts(n_seqs, n_tokens, vocab, _USP_DTYPE[dtype], target, draft, tokens, u, q_start, seq_lens, n_accepted,
                              next_tokens, keep_lens, stream)
 
 

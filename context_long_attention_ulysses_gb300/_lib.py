@@ -165,9 +165,10 @@ def load() -> ctypes.CDLL:
 _binding = None
 
 
-def binding(stream_of=None, raw_stream=None):
+def binding(stream_of=None, raw_stream=None, struct_of=None, *kinds):
     """The module that makes the calls around the cache (built by ``build.build()``); raises if it is missing.  The first
-    call says how a ``stream`` argument becomes a handle, and torch's current stream of a device."""
+    call says how a ``stream`` argument becomes a handle, torch's current stream of a device, and how an object of one of
+    ``kinds`` (a problem, a cache, a rotation) becomes the address of its struct."""
     global _binding
     if _binding is not None:
         return _binding
@@ -180,7 +181,7 @@ def binding(stream_of=None, raw_stream=None):
             loader = importlib.machinery.ExtensionFileLoader("uspbinding", BINDING)
             module = importlib.util.module_from_spec(importlib.util.spec_from_loader("uspbinding", loader))
             loader.exec_module(module)
-            module.configure(stream_of, check, raw_stream)
+            module.configure(stream_of, check, raw_stream, struct_of, *kinds)
             _binding = module
         return _binding
 

@@ -16,10 +16,11 @@
 
 namespace {
 
-// From the package: the stream's handle of a `stream` argument, what raises a status, torch's current stream of a device (or None).
-PyObject *stream_of, *check, *raw_stream;
+// From the package: the stream's handle of a `stream` argument, what raises a status, torch's current stream of a device (or None),
+// the address of an object's struct, and the classes of objects that have one.
+PyObject *stream_of, *check, *raw_stream, *struct_of, *problem_type, *cache_type, *rotary_type;
 PyObject *t_int32, *t_float32, *t_bfloat16;  // torch's
-PyObject *tensor_type, *s_is_cuda, *s_is_contiguous, *s_data_ptr, *s_numel, *s_nbytes, *s_shape, *s_stride, *s_dtype;
+PyObject *tensor_type, *s_is_cuda, *s_is_contiguous, *s_data_ptr, *s_numel, *s_nbytes, *s_shape, *s_stride, *s_dtype, *s_made;
 
 // How many elements of a type (of torch's, or null: none that is known) a tensor has to have.
 struct Want {
@@ -134,12 +135,24 @@ struct Args {
         if (PyErr_Occurred()) bad = true;
         return (void*)(uintptr_t)v;
     }
-    void* raw() {  // a host address
+    // The struct of an object of class `kind`, which keeps it with its address as `_made`, or of what the package takes for one.
+    template <typename T>
+    const T* made_of(PyObject* kind) {
         PyObject* x = next();
         if (!x) return nullptr;
-        const uint64_t v = PyLong_AsUnsignedLongLongMask(x);
+        PyObject *kept = (PyObject*)Py_TYPE(x) == kind ? PyObject_GetAttr(x, s_made) : nullptr, *y = nullptr;
+        if (kept && PyTuple_Check(kept) && PyTuple_GET_SIZE(kept) == 2) {
+            y = Py_NewRef(PyTuple_GET_ITEM(kept, 1));
+        } else {
+            if (PyErr_ExceptionMatches(PyExc_AttributeError)) PyErr_Clear();  // (not made yet)
+            PyObject* const both[] = {x, kind};
+            if (!PyErr_Occurred()) y = PyObject_Vectorcall(struct_of, both, 2, nullptr);
+        }
+        Py_XDECREF(kept);
+        const uint64_t v = y ? PyLong_AsUnsignedLongLongMask(y) : 0;
+        Py_XDECREF(y);
         if (PyErr_Occurred()) bad = true;
-        return (void*)(uintptr_t)v;
+        return bad ? nullptr : (const T*)(uintptr_t)v;
     }
     // A device address, or None, in x: true.
     bool plain(PyObject* x, uint64_t* v) {
@@ -305,8 +318,8 @@ PyObject* made(const char* name, Args& a, F&& call) {
 
 PyObject* rotary_embed(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Args a(args, n, 10);
-    const auto* p = (const usp_problem*)a.raw();
-    const auto* r = (const usp_rotary*)a.raw();
+    const auto* p = a.made_of<usp_problem>(problem_type);
+    const auto* r = a.made_of<usp_rotary>(rotary_type);
     const int Hq = p ? p->Hq : 0, Hkv = p ? p->Hkv : 0, d = p ? p->d : 0;
     const Want tokens{p ? type_of(p->dtype) : nullptr, p ? times(p->B, p->N) : 0};
     int64_t qs, ks, qos, kos;
@@ -321,8 +334,8 @@ PyObject* rotary_embed(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 PyObject* kv_append_axes(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Args a(args, n, 16);
-    const auto* c = (const usp_cache*)a.raw();
-    const auto* r = (const usp_rotary*)a.raw();
+    const auto* c = a.made_of<usp_cache>(cache_type);
+    const auto* r = a.made_of<usp_rotary>(rotary_type);
     const int Hq = c ? c->Hq : 0, Hkv = c ? c->Hkv : 0, d = c ? c->d : 0, tokens = a.integer();
     PyObject* type = c ? type_of(c->dtype) : nullptr;
     const Want each{type, tokens}, all{type, pool(c)};
@@ -342,7 +355,7 @@ PyObject* kv_append_axes(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 PyObject* pages_update(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Args a(args, n, 11);
-    const auto* c = (const usp_cache*)a.raw();
+    const auto* c = a.made_of<usp_cache>(cache_type);
     const Want slots = ints(c ? c->n_seqs : 0);
     const int32_t *parent = a.device<const int32_t>(slots), *keep = a.device<const int32_t>(slots), *grow = a.device<const int32_t>(slots);
     int32_t *lens = a.device<int32_t>(slots), *ids = a.device<int32_t>(ints(table(c))), *ref = a.device<int32_t>(ints(c ? c->n_pages : 0));
@@ -355,7 +368,7 @@ PyObject* pages_update(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 PyObject* pages_compact(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Args a(args, n, 8);
-    const auto* c = (const usp_cache*)a.raw();
+    const auto* c = a.made_of<usp_cache>(cache_type);
     const Want entries = ints(table(c)), pages = ints(c ? c->n_pages : 0);
     const int32_t *ids = a.device<const int32_t>(entries), *ref = a.device<const int32_t>(pages);
     int32_t *ids_out = a.device<int32_t>(entries), *ref_out = a.device<int32_t>(pages), *new_id = a.device<int32_t>(pages);
@@ -366,7 +379,7 @@ PyObject* pages_compact(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 PyObject* pages_copy(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Args a(args, n, 8);
-    const auto* c = (const usp_cache*)a.raw();
+    const auto* c = a.made_of<usp_cache>(cache_type);
     const int layers = a.integer();
     const int64_t stride = a.number();
     const int most = a.integer();
@@ -396,10 +409,10 @@ PyObject* verify_drafts(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
-// configure(stream_of, check, raw_stream), by the package before any call.
+// configure(stream_of, check, raw_stream, struct_of, problem_type, cache_type, rotary_type), by the package before any call.
 PyObject* configure(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    Args a(args, n, 3);
-    PyObject** const to[] = {&stream_of, &check, &raw_stream};
+    Args a(args, n, 7);
+    PyObject** const to[] = {&stream_of, &check, &raw_stream, &struct_of, &problem_type, &cache_type, &rotary_type};
     for (PyObject** x : to) {
         PyObject* y = a.next();
         if (!y) return nullptr;
@@ -438,6 +451,7 @@ PyMODINIT_FUNC PyInit_uspbinding(void) {
     s_shape = PyUnicode_InternFromString("shape");
     s_stride = PyUnicode_InternFromString("stride");
     s_dtype = PyUnicode_InternFromString("dtype");
-    if (!tensor_type || !t_int32 || !t_float32 || !t_bfloat16 || !s_dtype) return nullptr;
+    s_made = PyUnicode_InternFromString("_made");
+    if (!tensor_type || !t_int32 || !t_float32 || !t_bfloat16 || !s_dtype || !s_made) return nullptr;
     return PyModule_Create(&definition);
 }
