@@ -57,7 +57,6 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _Tensor = torch.Tensor
 _TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
-_USP_DTYPE = {"f32": USP_F32, "bf16": USP_BF16}
 
 
 _making = threading.Lock()
@@ -531,8 +530,8 @@ def usp_rotary_embed(p, r, q, k, pos, inv_freq, q_out, k_out, inverse: bool = Fa
 def usp_kv_append_axes(c, n_tokens: int, q, k, v, seq, pos, rot_pos, inv_freq, r, q_out, k_out, k_pages, v_pages,
                        page_table, stream=None) -> None:
     """q, k, v: [n_tokens][H][d] with any token stride (q, q_out and k_out may be None); the rest contiguous."""
-    (_bound or _binding()).kv_append_axes(c, r, n_tokens, q, k, v, seq, pos, rot_pos, inv_freq, q_out, k_out,
-                              k_pages, v_pages, page_table, stream)
+    (_bound or _binding()).kv_append_axes(c, r, n_tokens, q, k, v, seq, pos, rot_pos, inv_freq, q_out, k_out, k_pages, v_pages,
+                                          page_table, stream)
 
 
 def usp_pages_update_workspace_size(c) -> int:
@@ -556,12 +555,10 @@ def usp_pages_copy(c, max_copies: int, copies, k_pages, v_pages, n_layers: int =
 
 def usp_verify_drafts(n_seqs: int, n_tokens: int, vocab: int, target, draft, tokens, u, q_start, seq_lens, n_accepted,
                       next_tokens, keep_lens, dtype=None, stream=None) -> None:
-    """target, draft (or None): [n_tokens][vocab] with any row stride; dtype: theirs, "f32" or "bf16" (needed for device
-    pointers)."""
-    if dtype is None:
-        dtype = "bf16" if isinstance(target, _Tensor) and target.dtype == torch.bfloat16 else "f32"
-    (_bound or _binding()).verify_drafts(n_seqs, n_tokens, vocab, _USP_DTYPE[dtype], target, draft, tokens, u, q_start, seq_lens, n_accepted,
-                             next_tokens, keep_lens, stream)
+    """target, draft (or None): [n_tokens][vocab] with any row stride; dtype: theirs, "f32" or "bf16" (None: the
+    tensor's; a device pointer needs it)."""
+    (_bound or _binding()).verify_drafts(n_seqs, n_tokens, vocab, dtype, target, draft, tokens, u, q_start, seq_lens, n_accepted,
+                                         next_tokens, keep_lens, stream)
 
 
 def usp_diag_wait_timeout(stream=None) -> None:

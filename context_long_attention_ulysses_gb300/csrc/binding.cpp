@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <cstdint>
+#include <cstring>
 #include <initializer_list>
 
 #include <cuda_runtime_api.h>
@@ -276,6 +277,29 @@ struct Args {
             fail(PyExc_ValueError, "the heads of a token must be contiguous");
         return bad ? nullptr : (void*)(uintptr_t)address(x);
     }
+    // The type of probabilities, "f32", "bf16" or None: that of the tensor `of`.
+    int probability_type(PyObject* of) {
+        PyObject* x = next();
+        if (!x) return USP_F32;
+        if (x == Py_None && of != Py_None && is_tensor(of)) {
+            PyObject* type = PyObject_GetAttr(of, s_dtype);
+            if (type && type != t_float32 && type != t_bfloat16) PyErr_Format(PyExc_ValueError, "expected float32 or bfloat16, got %R", type);
+            bad |= PyErr_Occurred() != nullptr;
+            Py_XDECREF(type);
+            return type == t_bfloat16 ? USP_BF16 : USP_F32;
+        }
+        if (x == Py_None) {  // (nothing, or what is no buffer and refused as such)
+            if (of != Py_None && PyLong_Check(of)) fail(PyExc_ValueError, "dtype: 'f32' or 'bf16' is needed with a device pointer");
+            return USP_F32;
+        }
+        const char* name = PyUnicode_Check(x) ? PyUnicode_AsUTF8(x) : nullptr;
+        const bool f32 = name && !strcmp(name, "f32"), bf16 = name && !strcmp(name, "bf16");
+        if (!f32 && !bf16) {
+            if (!PyErr_Occurred()) PyErr_Format(PyExc_KeyError, "%R", x);
+            bad = true;
+        }
+        return bf16 ? USP_BF16 : USP_F32;
+    }
     // want.n rows, at least, of `vocab` contiguous probabilities.
     void* probabilities(int64_t* step, int vocab, const Want& want) {
         PyObject* x = next();
@@ -393,7 +417,7 @@ PyObject* pages_copy(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 PyObject* verify_drafts(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Args a(args, n, 14);
-    const int seqs = a.integer(), tokens = a.integer(), vocab = a.integer(), type = a.integer();
+    const int seqs = a.integer(), tokens = a.integer(), vocab = a.integer(), type = a.probability_type(n == 14 ? args[4] : Py_None);
     const Want each{type_of(type), tokens};
     int64_t ts, ds;
     const void *target = a.probabilities(&ts, vocab, each), *draft = a.probabilities(&ds, vocab, each);

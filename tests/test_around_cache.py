@@ -500,6 +500,25 @@ def test_tensors_of_another_type_or_too_short_are_refused(lib):
     usp_mod.usp_pages_copy(c, 0, torch.empty(0), torch.empty(0), torch.empty(0))
 
 
+def test_device_pointers_to_probabilities_need_their_type(lib):
+    import torch
+    call = lambda target, dtype=None, draft=None: usp_mod.usp_verify_drafts(  # noqa: E731
+        1, 4, 100, target, draft, FAKE + 2, FAKE, FAKE, None, FAKE, FAKE, None, dtype)
+    for target in (FAKE, 0):
+        with pytest.raises(ValueError, match="dtype"):
+            call(target)
+    for dtype in ("f32", "bf16"):                             # (3: tokens misaligned)
+        assert _status(call, FAKE, dtype) == 3
+    with pytest.raises(KeyError):
+        call(FAKE, "f16")
+    assert _status(call, None) == 3
+    for wrong in (torch.float16, torch.float64, torch.int32):
+        with pytest.raises(ValueError, match="expected float32 or bfloat16"):
+            call(torch.zeros(4, 100, dtype=wrong))
+    with pytest.raises(ValueError, match="expected torch.bfloat16"):     # one type for both
+        call(FAKE, "bf16", torch.zeros(4, 100))
+
+
 # ------------------------------------------------------------------ GPU
 @pytest.fixture(scope="module")
 def usp():
