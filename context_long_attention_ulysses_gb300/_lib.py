@@ -176,7 +176,7 @@ def binding(stream_of=None, raw_stream=None, struct_of=None, *kinds):
     with _lock:
         if _binding is None:
             if not os.path.exists(BINDING):
-                raise ImportError(f"uspbinding.so not found at {BINDING}; build it first "
+                raise ImportError(f"uspbinding.so not found at {BINDING}; build it first, with Python's C headers "
                                   "(python -m context_long_attention_ulysses_gb300.build)")
             loader = importlib.machinery.ExtensionFileLoader("uspbinding", BINDING)
             module = importlib.util.module_from_spec(importlib.util.spec_from_loader("uspbinding", loader))

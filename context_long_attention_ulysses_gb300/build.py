@@ -2,7 +2,9 @@
 
 Each CUDA translation unit compiles in parallel; the objects link into
 ``_build/libusp.so`` against the shared CUDA runtime, and ``binding.cpp``, the
-Python side of a decoding step's calls, into ``_build/uspbinding.so``.  Run as
+Python side of a decoding step's calls, into ``_build/uspbinding.so``.  The
+library needs nothing of Python: it is linked whatever becomes of the binding,
+which is left out, with a note, where Python's C headers are missing.  Run as
 ``python -m context_long_attention_ulysses_gb300.build``.
 """
 from __future__ import annotations
@@ -33,6 +35,12 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libusp")
 
 
+def _python_headers():
+    """The directory of Python.h; None without it."""
+    path = sysconfig.get_paths()["include"]
+    return path if os.path.exists(os.path.join(path, "Python.h")) else None
+
+
 def _stale(target: str, deps) -> bool:
     if not os.path.exists(target):
         return True
@@ -44,43 +52,47 @@ def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every translation unit for sm_103a and link libusp.so; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
-    header_deps = [os.path.join(CSRC, h) for h in HEADERS] + [
-        os.path.join(os.path.dirname(HERE), "include", "usp.h")]
-    procs = []
-    objs = []
     header = os.path.join(os.path.dirname(HERE), "include", "usp.h")
-    for src in SOURCES + ["binding.cpp"]:
+    header_deps = [os.path.join(CSRC, h) for h in HEADERS] + [header]
+    python = _python_headers()
+    if python is None:
+        print("Python.h not found: libusp.so is built without uspbinding.so, and the package's calls around the cache "
+              "(usp_rotary_embed, usp_kv_append_axes, usp_pages_*, usp_verify_drafts) will raise", file=sys.stderr)
+    binding = os.path.join(BUILD, os.path.splitext(os.path.basename(BINDING))[0] + ".o")
+    objs = [os.path.join(BUILD, os.path.splitext(src)[0] + ".o") for src in SOURCES]
+    units = [(src, o, header_deps, []) for src, o in zip(SOURCES, objs)]
+    if python is not None:
+        units.append(("binding.cpp", binding, [header], ["-I", python]))
+    procs = []
+    for src, o, deps, flags in units:
         s = os.path.join(CSRC, src)
-        o = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-        objs.append(o)
-        if force or _stale(o, [s] + (header_deps if src.endswith(".cu") else [header])):
-            cmd = [nvcc, *ARCH, *FLAGS, "-c", s, "-o", o + ".tmp"]
-            if not src.endswith(".cu"):
-                cmd[1:1] = ["-I", sysconfig.get_paths()["include"]]
+        if force or _stale(o, [s, *deps]):
+            cmd = [nvcc, *flags, *ARCH, *FLAGS, "-c", s, "-o", o + ".tmp"]
             if verbose:
                 print(" ".join(cmd), flush=True)
             procs.append((subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), o, cmd))
-    failed = []
+    failed = {}
     for p, o, cmd in procs:
         out, _ = p.communicate()
         if p.returncode != 0:
-            failed.append((cmd, out.decode(errors="replace")))
+            failed[o] = " ".join(cmd) + "\n" + out.decode(errors="replace")
         else:
             os.replace(o + ".tmp", o)
             if verbose and out:
                 print(out.decode(errors="replace"))
-    if failed:
-        msg = "\n".join(" ".join(c) + "\n" + o for c, o in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
-    *objs, binding = objs
-    for target, parts in ((LIB, objs), (BINDING, [binding, "-L", BUILD, "-lusp", "-Xlinker", "-rpath=$ORIGIN"])):
-        if force or _stale(target, objs if target == LIB else [binding]):
+    links = [(LIB, objs, [])]
+    if python is not None:
+        links.append((BINDING, [binding], ["-L", os.path.dirname(LIB), "-lusp", "-Xlinker", "-rpath=$ORIGIN"]))
+    for target, parts, libs in links:
+        if not failed.keys() & set(parts) and (force or _stale(target, parts)):
             tmp = target + f".tmp{os.getpid()}"
-            cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *parts]
+            cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *parts, *libs]
             if verbose:
                 print(" ".join(cmd), flush=True)
             subprocess.check_call(cmd)
             os.replace(tmp, target)
+        if failed.keys() & set(parts):
+            raise RuntimeError("nvcc failed:\n" + "\n".join(failed.values()))
     return LIB
 
 
