@@ -2,7 +2,7 @@
 
 Each CUDA translation unit compiles in parallel; the objects link into
 ``_build/libusp.so`` against the shared CUDA runtime, and ``binding.cpp``, the
-Python side of a decoding step's calls, into ``_build/uspbinding.so``.  The
+Python side of a decoding step's calls, into ``_build/uspbinding.<Python's ABI>.so``.  The
 library needs nothing of Python: it is linked whatever becomes of the binding,
 which is left out, with a note, where Python's C headers are missing.  Run as
 ``python -m context_long_attention_ulysses_gb300.build``.
@@ -19,7 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libusp.so")
-BINDING = os.path.join(BUILD, "uspbinding.so")
+BINDING = os.path.join(BUILD, "uspbinding" + sysconfig.get_config_var("EXT_SUFFIX"))  # (of this Python alone)
 SOURCES = ["api.cu", "remap.cu", "attn_f32.cu", "attn_fwd.cu", "attn_bwd.cu", "ring.cu", "noalloc.cu", "diag.cu",
            "kv_append.cu", "rotary.cu", "pages.cu", "verify.cu", "paged_attn.cu", "paged_mma.cu", "paged_tc.cu", "paged_f32.cu"]
 HEADERS = ["kernels.h", "ptx.cuh", "paged.cuh", "rotary.cuh", "cluster.cuh"]

@@ -38,3 +38,9 @@ def test_a_unit_that_fails_leaves_no_library(small, monkeypatch):
     with pytest.raises(RuntimeError, match="diag.cu"):
         build.build()
     assert not os.path.exists(build.LIB)
+
+
+def test_a_module_is_for_the_python_that_it_was_built_for():
+    """Another version builds its own, and does not load this one's."""
+    assert os.path.basename(build.BINDING) == "uspbinding" + sysconfig.get_config_var("EXT_SUFFIX")
+    assert sysconfig.get_config_var("EXT_SUFFIX") != ".so"
