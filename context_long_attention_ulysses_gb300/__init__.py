@@ -999,8 +999,8 @@ def verify_drafts(target, draft, tokens, u, q_start, seq_lens=None, stream=None)
 
     target [T][vocab] probabilities (float32 or bf16, any row stride): row t is for the token after tokens[t]; draft likewise:
     row t is what tokens[t] was drawn from, or None; tokens int32 [T], u float32 [T] in [0, 1); q_start int32 [n_seqs + 1].
-    Returns (n_accepted, next token, keep_lens), int32 [n_seqs] each; keep_lens: the cached tokens that stay, None without
-    seq_lens."""
+    Returns (n_accepted, next token, keep_lens), int32 [n_seqs] each; keep_lens: the cached tokens that stay (`keep` of the next
+    pages_update, whose lengths nothing else shortens), None without seq_lens."""
     dev = _serving_device(target)
     if target.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"target: expected float32 or bfloat16, got {target.dtype}")

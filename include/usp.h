@@ -611,6 +611,9 @@ size_t usp_pages_update_workspace_size(const usp_cache* c);
  * has n_seqs rows after row 0.
  * (Tokens that are appended next have the slots kept .. now - 1; drafts that
  * were refused are dropped by keep, say by usp_verify_drafts' keep_lens.)
+ * Between calls seq_lens, page_table and ref are this call's and
+ * usp_pages_compact's to change, and ref by the caller's own holds: the pages
+ * that a slot gives up are those of its length as the call finds it.
  * ws: at least usp_pages_update_workspace_size(c) bytes, 256-byte aligned,
  * contents on entry irrelevant; calls that can overlap on the GPU need one
  * each.  n_pages <= 2^23. */
@@ -654,13 +657,22 @@ usp_status usp_pages_copy(const usp_cache* c, int max_copies, const int32_t* cop
  * as the lowest token whose running sum w_0 + .. + w_x exceeds u[t0] sum w.
  * If all w are 0, target's row itself is drawn from; if that is 0 too, next is -1.
  * n_accepted[s]: drafts accepted; keep_lens[s] = seq_lens[s] - (drafts not
- * accepted), the cached tokens that stay (both NULL: not asked for; keep_lens
- * may be seq_lens).  A sequence without rows has n_accepted 0, next -1 and
- * keep_lens seq_lens.
- * For the draw probabilities are rounded to whole numbers of 2^-46 (half a step
- * of u is 2^-25) and summed exactly, in whatever order.  They are to be in
- * [0, 1] (what lies outside is taken as the nearer end, NaN as 0; NaN refuses a
- * draft), u in [0, 1); rows need not add up to 1.
+ * accepted), the cached tokens that stay (both NULL: not asked for).  A sequence
+ * without rows has n_accepted 0, next -1 and keep_lens seq_lens.  keep_lens may
+ * be seq_lens where the caller keeps the pages' books; with usp_pages_update it
+ * is an array of its own and passed on as keep: that call counts off the pages
+ * of the lengths it finds, and those behind a length which something else made
+ * shorter would stay counted for ever.
+ * For the draw, target and draft are rounded to whole numbers of 2^-46 and summed
+ * exactly, in whatever order.  So next can differ from exact arithmetic where
+ * u[t0] is within vocab * 2^-47 / sum w of a border between two tokens' shares
+ * of sum w (2^-46 where draft is subtracted), half a step of u being 2^-25.
+ * "All w are 0" means as rounded: a row below 2^-47 throughout has no token; and
+ * where no target[x] is over draft[x] by a step, any token of target's row may
+ * come, the refused one among them (rows that add up to 1 and drafts drawn from
+ * theirs are refused there with probability vocab * 2^-46 at most).
+ * Probabilities are to be in [0, 1] (what lies outside is taken as the nearer
+ * end, NaN as 0; NaN refuses a draft), u in [0, 1); rows need not add up to 1.
  * target, draft: [n_tokens] rows of vocab contiguous elements of dtype F32 or
  * BF16, strides in elements, at least vocab.  q_start is clamped to [0,
  * n_tokens].  1 <= vocab <= 2^19; n_seqs <= 2^28 - 1. */

@@ -1132,6 +1132,36 @@ def test_verify_rows_of_ones_whatever_the_cut(usp, V, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("V,close", [(1 << 17, 2.0 ** -19), (1 << 17, 2.0 ** -8), (50001, 2.0 ** -21), (1000, 0.25)])
+def test_verify_draws_from_what_little_is_left(usp, V, close):
+    """Target and draft that nearly agree, against running sums in 64 bits.  Two roundings of half a step, 2^-47, to a weight: the
+    running sum S_x less u times the total W is off by V 2^-46 at most, so u lies within V 2^-46 / W of the token's share
+    [S_x-1 / W, S_x / W]; the comparison's own sums are off by V 2^-53 of W."""
+    import torch
+    rng = np.random.default_rng(V)
+    n = 64
+    p = rng.random(V) + 0.5
+    p = (p / p.sum()).astype(np.float32)
+    q = (p * (1 + close * rng.choice([-1.0, 1.0], V))).astype(np.float32)
+    x = int(np.argmax(q / p))                             # refused by the largest number
+    w = np.maximum(p.astype(np.float64) - q.astype(np.float64), 0)
+    S, W = np.cumsum(w), w.sum()
+    assert 0 < W < 2 * close and q[x] * (1 - 2.0 ** -24) >= p[x]
+    u = np.empty((n, 2), np.float32)
+    u[:, 0], u[:, 1] = (rng.integers(0, 1 << 24, n) * 2.0 ** -24), 1 - 2.0 ** -24
+    guard = Guarded()
+    tg, dr = (torch.from_numpy(y).cuda().repeat(2 * n, 1) for y in (p, q))
+    out = [guard.empty((n,), torch.int32, "cuda").fill_(-77) for _ in range(2)]
+    usp.usp_verify_drafts(n, 2 * n, V, tg, dr, _put(guard, np.full(2 * n, x, np.int32)), _put(guard, u.reshape(-1)),
+                          _put(guard, np.arange(0, 2 * n + 1, 2, dtype=np.int32)), None, *out, None)
+    _done(usp, guard)
+    got, at = out[1].cpu().numpy(), u[:, 0].astype(np.float64)
+    assert (out[0] == 0).all() and (w[got] > 0).all()
+    off = V * 2.0 ** -46 / W + V * 2.0 ** -52
+    assert (at >= (S[got] - w[got]) / W - off).all() and (at <= S[got] / W + off).all()
+
+
+@pytest.mark.gpu
 def test_captured_calls_replay_with_new_values(usp):
     """A fork with its copies and a verification, captured on a side stream: later steps replay with new numbers; two
     captures with workspaces of their own do not disturb each other."""
