@@ -1,9 +1,9 @@
 // The Python side of the calls around the cache: arguments as torch tensors, device addresses or None, turned into pointers
 // and strides and passed on to the C ABI.  (Small calls are over on the GPU before ctypes and checks in Python are done
 // with them: with those the host took 6.6 us for the bookkeeping of 64 conversations, 7.6 to verify one sequence's drafts and
-// 9.7 to append a token each of eight, so 4.5, 4.8 and 5.9; a launch is 2.3 of that.)
-// What cannot be a buffer of the library raises, as in the package's Python; a status that is not USP_OK goes to the package's
-// check().
+// 9.7 to append a token each of eight, so 4.4, 4.7 and 5.4; a launch is 2.3 of that.)
+// What cannot be the buffer of the library that the call says (its place, its type, how much it holds, how it lies) raises, as in
+// the package's Python; a status that is not USP_OK goes to the package's check().
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -21,7 +21,41 @@ namespace {
 // the address of an object's struct, and the classes of objects that have one.
 PyObject *stream_of, *check, *raw_stream, *struct_of, *problem_type, *cache_type, *rotary_type;
 PyObject *t_int32, *t_float32, *t_bfloat16;  // torch's
-PyObject *tensor_type, *s_is_cuda, *s_is_contiguous, *s_data_ptr, *s_numel, *s_nbytes, *s_shape, *s_stride, *s_dtype, *s_made;
+PyObject *tensor_type, *s_made;
+
+// An attribute of tensors, or a method that is called without arguments.  Of a torch.Tensor itself what its class has under the
+// name is called as it is (looked up anew it takes 15 ns more, and a call asks up to fifty times); of a subclass's objects, or
+// where the class has something else there, it is looked up.
+struct Asked {
+    const char* text;
+    PyObject *name = nullptr, *none = nullptr;
+    PyGetSetDef* attribute = nullptr;
+    PyMethodDef* method = nullptr;
+    bool is_method = false;
+
+    bool find() {
+        name = PyUnicode_InternFromString(text);
+        none = PyTuple_New(0);
+        PyObject* x = name && none ? PyObject_GetAttr(tensor_type, name) : nullptr;
+        if (!x) return false;
+        if (Py_TYPE(x) == &PyGetSetDescr_Type) attribute = ((PyGetSetDescrObject*)x)->d_getset;
+        if (Py_TYPE(x) == &PyMethodDescr_Type) method = ((PyMethodDescrObject*)x)->d_method;
+        is_method = PyCallable_Check(x);
+        return true;  // (x, and what it names, stay)
+    }
+    PyObject* of(PyObject* x) const {
+        if ((PyObject*)Py_TYPE(x) == tensor_type) {
+            if (attribute) return attribute->get(x, attribute->closure);
+            if (method && method->ml_flags == METH_NOARGS) return method->ml_meth(x, nullptr);
+            if (method && method->ml_flags == METH_VARARGS) return method->ml_meth(x, none);
+            if (method && method->ml_flags == (METH_VARARGS | METH_KEYWORDS))
+                return ((PyCFunctionWithKeywords)(void (*)(void))method->ml_meth)(x, none, nullptr);
+        }
+        return is_method ? PyObject_CallMethodNoArgs(x, name) : PyObject_GetAttr(x, name);
+    }
+};
+Asked is_cuda{"is_cuda"}, is_contiguous{"is_contiguous"}, data_ptr{"data_ptr"}, numel{"numel"}, nbytes{"nbytes"}, shape_of{"shape"},
+    stride_of{"stride"}, dtype_of{"dtype"};
 
 // How many elements of a type (of torch's, or null: none that is known) a tensor has to have.
 struct Want {
@@ -72,9 +106,9 @@ struct Args {
         if (is < 0) bad = true;
         return is > 0;
     }
-    // A number that an attribute or a method without arguments of x gives.
-    long long asked(PyObject* x, PyObject* name, bool method) {
-        PyObject* y = method ? PyObject_CallMethodNoArgs(x, name) : PyObject_GetAttr(x, name);
+    // A number that x says.
+    long long asked(PyObject* x, const Asked& what) {
+        PyObject* y = what.of(x);
         long long v = 0;
         if (y) {
             v = PyLong_AsLongLong(y);
@@ -84,7 +118,7 @@ struct Args {
         return v;
     }
     uint64_t address(PyObject* x) {
-        PyObject* y = PyObject_CallMethodNoArgs(x, s_data_ptr);
+        PyObject* y = data_ptr.of(x);
         uint64_t v = 0;
         if (y) {
             v = PyLong_AsUnsignedLongLongMask(y);
@@ -94,12 +128,12 @@ struct Args {
         return v;
     }
     bool on_device(PyObject* x) {
-        const bool is = truth(x, s_is_cuda, false);
+        const bool is = truth(x, is_cuda);
         device_seen |= is;
         return is;
     }
-    bool truth(PyObject* x, PyObject* name, bool method) {
-        PyObject* y = method ? PyObject_CallMethodNoArgs(x, name) : PyObject_GetAttr(x, name);
+    bool truth(PyObject* x, const Asked& what) {
+        PyObject* y = what.of(x);
         const int v = y ? PyObject_IsTrue(y) : -1;
         Py_XDECREF(y);
         if (v < 0) bad = true;
@@ -173,7 +207,7 @@ struct Args {
     }
     void typed(PyObject* x, PyObject* type) {
         if (bad || !type) return;
-        PyObject* is = PyObject_GetAttr(x, s_dtype);
+        PyObject* is = dtype_of.of(x);
         if (is && is != type) PyErr_Format(PyExc_ValueError, "expected %R, got %R", type, is);
         bad |= is != type;
         Py_XDECREF(is);
@@ -188,16 +222,16 @@ struct Args {
             not_a_buffer(x);
             return nullptr;
         }
-        const long long bytes = asked(x, s_nbytes, false);
+        const long long bytes = asked(x, nbytes);
         if (bytes > 0) {
             typed(x, want.type);
             if (want.type && !bad && bytes / (want.type == t_bfloat16 ? 2 : 4) < want.n) {
-                PyErr_Format(PyExc_ValueError, "expected %lld elements at least, got %lld", (long long)want.n, asked(x, s_numel, true));
+                PyErr_Format(PyExc_ValueError, "expected %lld elements at least, got %lld", (long long)want.n, asked(x, numel));
                 bad = true;
             }
         }
         if (!bad && !on_device(x) && bytes > 0) fail(PyExc_ValueError, "libusp takes device tensors");
-        if (!bad && !truth(x, s_is_contiguous, true) && !bad) fail(PyExc_ValueError, "libusp takes contiguous tensors");
+        if (!bad && !truth(x, is_contiguous) && !bad) fail(PyExc_ValueError, "libusp takes contiguous tensors");
         return bad ? nullptr : (T*)(uintptr_t)address(x);
     }
     // A workspace and its size, which the argument after it gives, None: the tensor's.
@@ -209,7 +243,7 @@ struct Args {
             if (PyErr_Occurred()) bad = true;
         }
         if (x && !bad && x != Py_None && !PyLong_Check(x) && is_tensor(x)) {
-            const size_t whole = (size_t)asked(x, s_nbytes, false);
+            const size_t whole = (size_t)asked(x, nbytes);
             if (n == Py_None) *bytes = whole;
             if (!bad && *bytes > whole) fail(PyExc_ValueError, "a workspace of more bytes than the tensor has");
         }
@@ -218,7 +252,7 @@ struct Args {
     }
     // Shape and strides of x; the number of its dimensions, 0 if there are more than five.
     Py_ssize_t layout(PyObject* x, long long (&shape)[5], long long (&stride)[5]) {
-        PyObject *a = PyObject_GetAttr(x, s_shape), *b = a ? PyObject_CallMethodNoArgs(x, s_stride) : nullptr;
+        PyObject *a = shape_of.of(x), *b = a ? stride_of.of(x) : nullptr;
         Py_ssize_t dims = 0;
         if (a && b && PyTuple_Check(a) && PyTuple_Check(b) && PyTuple_GET_SIZE(a) == PyTuple_GET_SIZE(b) && PyTuple_GET_SIZE(a) <= 5) {
             dims = PyTuple_GET_SIZE(a);
@@ -282,7 +316,7 @@ struct Args {
         PyObject* x = next();
         if (!x) return USP_F32;
         if (x == Py_None && of != Py_None && is_tensor(of)) {
-            PyObject* type = PyObject_GetAttr(of, s_dtype);
+            PyObject* type = dtype_of.of(of);
             if (type && type != t_float32 && type != t_bfloat16) PyErr_Format(PyExc_ValueError, "expected float32 or bfloat16, got %R", type);
             bad |= PyErr_Occurred() != nullptr;
             Py_XDECREF(type);
@@ -467,15 +501,9 @@ PyMODINIT_FUNC PyInit_uspbinding(void) {
     t_float32 = PyObject_GetAttrString(torch, "float32");
     t_bfloat16 = PyObject_GetAttrString(torch, "bfloat16");
     Py_DECREF(torch);
-    s_is_cuda = PyUnicode_InternFromString("is_cuda");
-    s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
-    s_data_ptr = PyUnicode_InternFromString("data_ptr");
-    s_numel = PyUnicode_InternFromString("numel");
-    s_nbytes = PyUnicode_InternFromString("nbytes");
-    s_shape = PyUnicode_InternFromString("shape");
-    s_stride = PyUnicode_InternFromString("stride");
-    s_dtype = PyUnicode_InternFromString("dtype");
     s_made = PyUnicode_InternFromString("_made");
-    if (!tensor_type || !t_int32 || !t_float32 || !t_bfloat16 || !s_dtype || !s_made) return nullptr;
+    if (!tensor_type || !t_int32 || !t_float32 || !t_bfloat16 || !s_made) return nullptr;
+    for (Asked* x : {&is_cuda, &is_contiguous, &data_ptr, &numel, &nbytes, &shape_of, &stride_of, &dtype_of})
+        if (!x->find()) return nullptr;
     return PyModule_Create(&definition);
 }

@@ -1471,6 +1471,31 @@ def test_copies_in_layers_apart_and_an_append_without_queries(usp):
 
 
 @pytest.mark.gpu
+def test_tensors_of_a_subclass(usp):
+    """Parameters, and a class that has its own of what a call asks, are tensors like others."""
+    import torch
+
+    class Counted(torch.Tensor):
+        asked = 0
+
+        def data_ptr(self):
+            Counted.asked += 1
+            return super().data_ptr()
+
+    x = _drafts(np.random.default_rng(5), [3, 1, 2], 400, "f32")
+    ins = [_dev(x[k]) for k in ("tokens", "u", "q_start", "lens")]
+    results = []
+    for cls in (lambda y: y, lambda y: torch.nn.Parameter(y, requires_grad=False), lambda y: y.as_subclass(Counted)):
+        out = [torch.zeros(3, dtype=torch.int32, device="cuda") for _ in range(3)]
+        usp.usp_verify_drafts(3, 6, 400, cls(x["tg"]), cls(x["dr"]), *[cls(y) for y in ins], *out)
+        results.append(torch.stack(out).tolist())
+    assert results[0] == results[1] == results[2] == ref_verify(x["target"], x["draft"], x["tokens"], x["u"], x["q_start"], x["lens"]).tolist()
+    assert Counted.asked == 6
+    with pytest.raises(ValueError, match="expected torch.float32"):
+        usp.usp_verify_drafts(3, 6, 400, x["tg"], x["dr"], ins[0], torch.nn.Parameter(ins[1].double()), *ins[2:], *out)
+
+
+@pytest.mark.gpu
 def test_traced_calls_are_on_record(usp):
     import torch
     c = usp.Cache(40, 16, 3, 20, 1, 1, 64)
