@@ -54,13 +54,14 @@ struct Asked {
         return is_method ? PyObject_CallMethodNoArgs(x, name) : PyObject_GetAttr(x, name);
     }
 };
-Asked is_cuda{"is_cuda"}, is_contiguous{"is_contiguous"}, data_ptr{"data_ptr"}, numel{"numel"}, nbytes{"nbytes"}, shape_of{"shape"},
+Asked is_cuda{"is_cuda"}, is_contiguous{"is_contiguous"}, data_ptr{"data_ptr"}, nbytes{"nbytes"}, shape_of{"shape"},
     stride_of{"stride"}, dtype_of{"dtype"};
 
-// How many elements of a type (of torch's, or null: none that is known) a tensor has to have.
+// How many elements of a type (of torch's, or null: any) and of how many bytes a tensor has to have.
 struct Want {
     PyObject* type;
     int64_t n;
+    int size = 4;
 };
 // The product of sizes, as far as it goes; 0 where one is not positive (the C side says what is wrong with it).
 template <typename... N>
@@ -74,6 +75,7 @@ int64_t times(N... sizes) {
 }
 Want ints(int64_t n) { return {t_int32, n}; }
 Want floats(int64_t n) { return {t_float32, n}; }
+int size_of(int dtype) { return dtype == USP_BF16 ? 2 : 4; }
 PyObject* type_of(int dtype) { return dtype == USP_F32 ? t_float32 : dtype == USP_BF16 ? t_bfloat16 : nullptr; }
 int64_t pool(const usp_cache* c) { return c ? times(c->n_pages, c->Hkv, c->page_size, c->d) : 0; }
 int64_t table(const usp_cache* c) { return c ? times(c->n_seqs, c->max_pages) : 0; }
@@ -225,8 +227,8 @@ struct Args {
         const long long bytes = asked(x, nbytes);
         if (bytes > 0) {
             typed(x, want.type);
-            if (want.type && !bad && bytes / (want.type == t_bfloat16 ? 2 : 4) < want.n) {
-                PyErr_Format(PyExc_ValueError, "expected %lld elements at least, got %lld", (long long)want.n, asked(x, numel));
+            if (!bad && bytes / want.size < want.n) {
+                PyErr_Format(PyExc_ValueError, "expected %lld elements of %d bytes at least, got %lld bytes", (long long)want.n, want.size, bytes);
                 bad = true;
             }
         }
@@ -396,13 +398,14 @@ PyObject* kv_append_axes(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const auto* r = a.made_of<usp_rotary>(rotary_type);
     const int Hq = c ? c->Hq : 0, Hkv = c ? c->Hkv : 0, d = c ? c->d : 0, tokens = a.integer();
     PyObject* type = c ? type_of(c->dtype) : nullptr;
-    const Want each{type, tokens}, all{type, pool(c)};
+    const int size = c ? size_of(c->dtype) : 4;
+    const Want each{type, tokens, size}, all{type, pool(c), size};
     int64_t qs, ks, vs;
     const void *q = a.rows(&qs, Hq, d, false, each), *k = a.rows(&ks, Hkv, d, false, each), *v = a.rows(&vs, Hkv, d, false, each);
     const int32_t *seq = a.device<const int32_t>(ints(tokens)), *pos = a.device<const int32_t>(ints(tokens));
     const auto* rot_pos = a.device<const int32_t>(ints(r && r->rot > 0 ? times(r->n_axes, tokens) : 0));
     const auto* f = a.device<const float>(floats(r && tokens > 0 ? r->rot / 2 : 0));
-    void *qo = a.device<void>({type, times(tokens, Hq, d)}), *ko = a.device<void>({type, times(tokens, Hkv, d)});
+    void *qo = a.device<void>({type, times(tokens, Hq, d), size}), *ko = a.device<void>({type, times(tokens, Hkv, d), size});
     void *kp = a.device<void>(all), *vp = a.device<void>(all);
     const auto* ids = a.device<const int32_t>(ints(table(c)));
     void* s = a.stream();
@@ -443,7 +446,8 @@ PyObject* pages_copy(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int most = a.integer();
     const auto* copies = a.device<const int32_t>(ints(most > 0 ? 4 : 0));  // (row 0 says how many rows are read)
     const int64_t one = pool(c), before = layers > 1 ? times(layers - 1, stride) : 0;
-    const Want all{c ? type_of(c->dtype) : nullptr, layers < 1 || most < 1 ? 0 : before > INT64_MAX - one ? INT64_MAX : before + one};
+    // (pages are moved as bytes, whatever type the tensor says)
+    const Want all{nullptr, layers < 1 || most < 1 ? 0 : before > INT64_MAX - one ? INT64_MAX : before + one, c ? size_of(c->dtype) : 4};
     void *kp = a.device<void>(all), *vp = a.device<void>(all);
     void* s = a.stream();
     return made("usp_pages_copy", a, [&] { return usp_pages_copy(c, most, copies, layers, stride, kp, vp, s); });
@@ -503,7 +507,7 @@ PyMODINIT_FUNC PyInit_uspbinding(void) {
     Py_DECREF(torch);
     s_made = PyUnicode_InternFromString("_made");
     if (!tensor_type || !t_int32 || !t_float32 || !t_bfloat16 || !s_made) return nullptr;
-    for (Asked* x : {&is_cuda, &is_contiguous, &data_ptr, &numel, &nbytes, &shape_of, &stride_of, &dtype_of})
+    for (Asked* x : {&is_cuda, &is_contiguous, &data_ptr, &nbytes, &shape_of, &stride_of, &dtype_of})
         if (!x->find()) return nullptr;
     return PyModule_Create(&definition);
 }
