@@ -12,9 +12,9 @@
 //           then, the writers alone hold it, and the first keeps it;
 //   number  new pages and copies slot by slot, free pages page by page;
 //   write   rows, lengths, the list of copies, counts, if there are pages enough.
-// Small caches take one CTA with all counts in its shared memory (64 conversations 4.9 us; 11.4 as one cluster of eight CTAs with
-// the counts in L2, where a step's few dependent accesses and a barrier cost 1 to 4 us), others a launch for each step, which
-// follow each other by dependent launch.
+// Small caches take one CTA with all counts in its shared memory (64 conversations 4.7 us in a captured graph; 11.4 as one cluster
+// of eight CTAs with the counts in L2, where a step's few dependent accesses and a barrier cost 1 to 4 us), others a launch for each
+// step, which follow each other by dependent launch.
 #include <algorithm>
 
 #include "cluster.cuh"
@@ -84,8 +84,11 @@ enum : int { kSlotOther = 1, kSlotStaged = 2, kSlotWrites = 4 };
 
 __host__ __device__ inline size_t books_bytes(int n_seqs, int n_pages) { return 12 * (size_t)n_pages + 32 * (size_t)n_seqs; }
 
-// (n_pages and n_seqs of the caches that one CTA takes; of one with forks, also the entries that it may have to copy: 3400 of them
-// took one CTA 13 us and the launches 16, 132000 38 and 16)
+// n_pages and n_seqs of the caches that one CTA takes and, where `parent` is given, the table's entries, which it may then have to
+// copy.  In a captured graph, one CTA and the launches: eight samples of 360 entries in all 4.6 and 7.3 us, 64 of 16000 8.7 and
+// 8.3, 120 of 61600 23.5 and 10.8, 256 of 131000 43 and 11.8; with a parent that is every slot itself 4.7 and 7.4, whatever the
+// table.  (Entries that are dropped without `parent` play no part in the rule: a table of 131000 released at once takes the CTA 36 us,
+// the launches would take 10.3; a step that drops little 4.8 and 7.2.)
 constexpr int kOnePages = 16384, kOneSeqs = 1024;
 constexpr int64_t kOneEntries = 1 << 16;
 __host__ __device__ inline bool one_cta(const PagesUpdateParams& p) {
@@ -715,7 +718,7 @@ __global__ void __launch_bounds__(256) pages_rename_kernel(const __grid_constant
 }
 
 // The pages' data.  A page of K, or of V, in pieces of kCopyThreads * AHEAD vectors of 16 bytes; those of tokens that the copy
-// leaves out are passed over.  Bound by HBM: 2322 pages of 256 KB (K and V) 180 us, 6.8 TB/s, 1.00 of a copy.  An SM has 64 KB
+// leaves out are passed over.  Bound by HBM: 2322 pages of 256 KB (K and V) 181 us, 6.7 TB/s, 0.99 of a copy.  An SM has 64 KB
 // under way, in the fewer CTAs the larger a page is: with eight vectors to a thread, one CTA 216 us, two 182, three 199, four 192;
 // four vectors 191 to 207, streaming loads and stores 187.
 constexpr int kCopyThreads = 256;

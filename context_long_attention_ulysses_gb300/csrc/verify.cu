@@ -10,7 +10,8 @@
 // probabilities are rounded (float64 would do as well, but its units are scarce); they do not depend on the order either.
 //
 // Bound by HBM for many sequences (one row of p, and of q where a draft is refused, are read once; 64 of 131072 float32 tokens
-// 13.2 us, 5.1 TB/s with the 4 us that a launch, the drafts' dependent loads and the search take) and by latency for few: a
+// 13.3 us in a captured graph, 5.0 TB/s with the 4 us that a launch, the drafts' dependent loads and the search take, and 15.2
+// called from Python, 4.4 TB/s) and by latency for few: a
 // cluster of CTAs takes a sequence, each CTA a slice of the vocabulary in tiles, whose sums stay in shared
 // memory; the CTA that holds the threshold finds the tile by them and goes over that tile alone again.
 #include <algorithm>
@@ -76,8 +77,9 @@ struct Loaded<T, true, E> {
 
 // Sums of x in [0, 1], each rounded to whole numbers of 2^-46, kept as two digits: added to a power of two a number's last bits
 // are the digit, what that leaves is exact and, added to a smaller one, gives the next.  (The powers' own bits, which come with
-// every digit, cancel where numbers are subtracted.)  A weight takes 13 instructions; with a third digit, to 2^-53, it took 20,
-// and 64 sequences of 131072 tokens 27 issued instructions a weight, loads and sums of tiles included.
+// every digit, cancel where numbers are subtracted.)  All that is issued, loads and sums of tiles included, is 23 instructions of a
+// lane for a pair of p and q in float32 (64 sequences of 131072 tokens) and 15 for p alone in bf16 (200 of 50001); with a third
+// digit, to 2^-53, the pair took 27.
 struct Digits {
     static constexpr float kOne = 1.f, kTwo = 0x1.8p-23f;  // steps of 2^-23 and 2^-46 (x = 1 is the next power: a step on)
     uint32_t d0 = 0, d1 = 0;
